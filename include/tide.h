@@ -373,6 +373,92 @@ tide_status tide_allgather_copyin(tide_plan* plan, const void* const* shards, in
 tide_status tide_stock_chunk_cat(tide_plan* plan, const uint16_t* const* grads, float* packed, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits: what a rank keeps of a layer's input
+ * between its forward and its backward pass (the sharded parameters and
+ * gradients above leave activations whole), and the weight gradient that is
+ * computed from it and handed to the reduce-scatter.  None of these touches a
+ * plan.
+ *
+ * A matrix of rows x cols values is kept as codes, one byte per value, and
+ * scales, one byte per block of 32 neighbouring values of a row.  Rows are
+ * filled up to whole blocks with zeros: codes is rows x 32*B bytes and scales
+ * rows x B bytes, both row-major without gaps, B = ceil(cols / 32)
+ * (tide_checkpoint_layout).  With b a block's scale byte its values are
+ *   code * 2^(b - 127)
+ * where a code is an e4m3 number (1 sign, 4 exponent, 3 fraction bits, bias 7,
+ * largest 448, no infinities) or a two's complement integer.  Packing chooses
+ * the smallest power of two for which the block's largest magnitude is at most
+ * 448 (e4m3) or 127.5 (int8) units, b held in [10, 246] or [10, 248], and
+ * rounds value / unit to the nearest code, ties to even, saturating at 448 or
+ * 127.  So a value comes back to within 2^-4 of itself or 2^-10 units (e4m3),
+ * or half a unit (int8); saturation passes those bounds only for magnitudes
+ * above 1.75 * 2^127 (e4m3) or 127.5 * 2^121 (int8).  A block that holds a NaN
+ * or an infinity gets b = 255 and comes back as NaN throughout.  Every other
+ * restored value is 0 or a normal bf16 number, so restoring rounds nothing.
+ *
+ * Sizes: rows below 2^31, cols and row strides up to 2^22, a matrix up to
+ * 2^34 elements (else TIDE_ERR_RANGE).  Row strides are in elements and at
+ * least the row's length.  Any size may be 0.
+ * ------------------------------------------------------------------------ */
+
+/* Code types of a checkpoint (its format). */
+#define TIDE_CODE_E4M3 0
+#define TIDE_CODE_INT8 1
+
+/*
+ * Row lengths of a checkpoint of rows of `cols` values: 32*B codes, B scales.
+ * Either output may be NULL.
+ * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE.
+ */
+tide_status tide_checkpoint_layout(int64_t cols, int64_t* code_cols, int64_t* scale_cols);
+
+/*
+ * Pack a matrix.
+ *   x       rows x cols values of `dtype` (TIDE_DTYPE_*), rows `row_stride`
+ *           elements apart, aligned to the element; 16-byte aligned rows are
+ *           read 16 bytes at a time
+ *   codes   16-byte aligned, written in full;  scales written in full
+ * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
+ */
+tide_status tide_checkpoint_pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                                 int32_t format, void* codes, void* scales, void* stream);
+
+/*
+ * Restore a matrix: the first cols values of every row, exactly, into rows
+ * `row_stride` elements apart (what lies between two rows is left alone).
+ * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
+ */
+tide_status tide_checkpoint_unpack(const void* codes, const void* scales, int32_t format, int64_t rows, int64_t cols,
+                                   void* out, int32_t dtype, int64_t row_stride, void* stream);
+
+/*
+ * Weight gradient of a linear layer y = x W^T from the checkpoint of its
+ * input: with X the restored matrix (rows = tokens),
+ *   s[o][i] = sum over tokens t of dy[t][o] * X[t][i]
+ *   dw[o][i] = alpha * s                  (accumulate = 0)
+ *   dw[o][i] = old + alpha * s            (accumulate = 1)
+ * The products are exact, the sum is kept in fp32 (in an order that depends
+ * on the sizes only), and the result is rounded once to dw's type.
+ *   dy      rows x out_features bf16, rows dy_stride elements apart, 2-byte
+ *           aligned
+ *   codes, scales  the checkpoint, rows x in_features, 16-byte aligned codes
+ *   dw      out_features x in_features of dw_dtype, without gaps, aligned to
+ *           the element
+ *   workspace  device memory of at least the bytes that the _workspace call
+ *           gives for the same arguments, 256-byte aligned (may be NULL when
+ *           that is 0).  Its contents need not be kept; calls that may overlap
+ *           must not share it.
+ * rows = 0 gives sums of 0.
+ * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
+ */
+tide_status tide_checkpoint_weight_grad_workspace(const uint16_t* dy, int64_t rows, int64_t out_features,
+                                                  int64_t dy_stride, int64_t in_features, int64_t* bytes);
+tide_status tide_checkpoint_weight_grad(const uint16_t* dy, int64_t rows, int64_t out_features, int64_t dy_stride,
+                                        const void* codes, const void* scales, int32_t format, int64_t in_features,
+                                        void* dw, int32_t dw_dtype, float alpha, int32_t accumulate, void* workspace,
+                                        int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Interference instruments (Section 2.2 "SM Wave Quantization", Equation 4,
  * Figure 3, Table 4 and Table 5): what one GPU can show of the cost a
  * collective's kernels impose on the compute they overlap.  None of these

@@ -8,6 +8,10 @@
                          (tables in a fixed device scratch array)
   allgather_copyout      rank-major bf16 buffer -> per-parameter tensors
   allgather_copyin       every rank's fp32/bf16 shards -> rank-major bf16 buffer
+  checkpoint_pack, checkpoint_unpack
+                         activations kept in 8 bits between the passes
+  checkpoint_weight_grad a linear layer's weight gradient from such a
+                         checkpoint of its input
   stock_chunk_cat        stock FSDP2's gradient pack of one rank (the baseline)
   probe, victim_axpb, Stream
                          interference instruments: hardware-ID probe,
@@ -32,6 +36,14 @@ from .tide import (  # noqa: F401
     allgather_copyin_call,
     allgather_copyout,
     allgather_copyout_call,
+    checkpoint_layout,
+    checkpoint_pack,
+    checkpoint_pack_call,
+    checkpoint_unpack,
+    checkpoint_unpack_call,
+    checkpoint_weight_grad,
+    checkpoint_weight_grad_call,
+    checkpoint_weight_grad_workspace,
     reduce_scatter_call,
     reduce_scatter_local,
     reduce_scatter_local_noalloc,

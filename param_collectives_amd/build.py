@@ -8,13 +8,17 @@ Flags that matter for results:
 """
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libtide.so")
-SOURCES = [os.path.join(CSRC, n) for n in ("plan.cpp", "capi.cpp", "kernels.hip", "instruments.hip", "scratch.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in (
+    "plan.cpp", "capi.cpp", "kernels.hip", "instruments.hip", "scratch.hip",
+    "training.cpp", "checkpoint.hip", "weight_grad.hip")]
 ARCH = "gfx950"
 
 
@@ -25,18 +29,24 @@ def hipcc():
 
 
 def build_library(verbose: bool = False, extra=()) -> str:
-    cmd = [
-        hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    flags = [
+        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
         "-ffp-contract=off", "-fno-fast-math",
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wall", "-Wno-unused-command-line-argument",
-        "-I", INCLUDE, "-I", CSRC,
-        *SOURCES, "-o", LIBRARY + ".tmp",
-        *extra,
+        "-I", INCLUDE, "-I", CSRC, *extra,
     ]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            list(pool.map(lambda so: run([hipcc(), *flags, "-c", so[0], "-o", so[1]]), zip(SOURCES, objects)))
+        run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objects, "-o", LIBRARY + ".tmp"])
     os.replace(LIBRARY + ".tmp", LIBRARY)
     return LIBRARY
 

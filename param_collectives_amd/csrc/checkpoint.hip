@@ -1,0 +1,264 @@
+// Activation checkpoints in 8 bits on MI355X (gfx950): a row-major bf16 or
+// fp32 matrix is kept as one byte of code per value and one exponent byte per
+// block of 32 values of a row, and restored from them.
+//
+// A block's exponent byte b stands for 2^(b - 127), the smallest power of two
+// u with max |x| <= 448 u (e4m3 codes) or <= 127.5 u (int8 codes), b held in
+// [10, 246] or [10, 248]; a value's code is x / u rounded to nearest even and
+// saturated at 448 or 127.  The division is exact, so each value has this one
+// rounding: at most 2^-4 of the value (or u 2^-10) for e4m3, half of u for
+// int8.  A block that holds a NaN or an infinity gets b = 255 and comes back
+// as NaN.  b >= 10 keeps every non-zero u q a normal bf16 number, so restoring
+// rounds nothing, in bf16 either.
+//
+// Both kernels are bound by HBM.  A lane takes 8 values (16 bytes of bf16, 8
+// of codes), four lanes a block, and the block's maximum goes through two
+// cross-lane steps.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm.h"
+#include "training.h"
+
+namespace {
+
+using namespace tide;
+
+constexpr int kUnit = 8;    // values of a lane
+constexpr int kSweeps = 4;  // units of a thread
+constexpr uint32_t kLowest = 10, kNotFinite = 255;
+
+struct PackArgs {
+  void* x;
+  int64_t ld;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t units;       // of the matrix
+  uint32_t row_units;  // of a row, whole blocks
+  uint64_t magic;      // ceil(2^40 / row_units)
+  int32_t cols;
+};
+
+// Row and unit of the row of this thread's unit `i` of the workgroup that
+// starts at unit `first`.
+__device__ __forceinline__ void locate(const PackArgs& a, int64_t first_row, uint32_t first_unit, uint32_t i,
+                                       int64_t* row, uint32_t* unit) {
+  const uint32_t n = first_unit + i;  // below 2^20: the product below 2^60, the quotient exact
+  const uint32_t q = uint32_t((uint64_t(n) * a.magic) >> 40);
+  *row = first_row + q;
+  *unit = n - q * a.row_units;
+}
+
+template <bool F32, bool ALIGNED>
+__device__ __forceinline__ void load8(const void* x, int64_t at, int left, float* v) {
+  if constexpr (F32) {
+    const float* p = static_cast<const float*>(x) + at;
+    if (ALIGNED && left >= kUnit) {
+      const f32x4v lo = *reinterpret_cast<const f32x4v*>(p), hi = *reinterpret_cast<const f32x4v*>(p + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = lo[j];
+        v[4 + j] = hi[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) v[j] = j < left ? p[j] : 0.0f;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+    if (ALIGNED && left >= kUnit) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) v[j] = j < left ? __uint_as_float(uint32_t(p[j]) << 16) : 0.0f;
+    }
+  }
+}
+
+// The larger of this lane's value and its neighbours' in the group of four.
+__device__ __forceinline__ uint32_t max_of_four(uint32_t v) {
+  uint32_t o = uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
+  v = v > o ? v : o;
+  o = uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
+  return v > o ? v : o;
+}
+
+template <Code CODE>
+__device__ __forceinline__ uint32_t exponent_byte(uint32_t top) {
+  // top: the bits of the block's largest magnitude, 1.f 2^(e - 127)
+  constexpr uint32_t kShift = CODE == Code::kE4m3 ? 8 : 6;                      // 448 = 1.75 2^8, 127.5 = 1.992.. 2^6
+  constexpr uint32_t kLimit = CODE == Code::kE4m3 ? 0x600000u : 0x7F0000u;      // their fractions
+  constexpr uint32_t kHighest = CODE == Code::kE4m3 ? 246u : 248u;
+  if (top >= 0x7F800000u) return kNotFinite;
+  int32_t b = int32_t(top >> 23) - int32_t(kShift) + ((top & 0x7FFFFFu) > kLimit ? 1 : 0);
+  b = b > int32_t(kLowest) ? b : int32_t(kLowest);
+  return uint32_t(b) < kHighest ? uint32_t(b) : kHighest;
+}
+
+template <bool F32, Code CODE, bool ALIGNED>
+__global__ __launch_bounds__(256) void checkpoint_pack_kernel(PackArgs a) {
+  const int64_t base = int64_t(blockIdx.x) * (256 * kSweeps);
+  const int64_t row0 = base / a.row_units;
+  const uint32_t unit0 = uint32_t(base - row0 * a.row_units);
+  float v[kSweeps][kUnit];
+  int64_t row[kSweeps];
+  uint32_t unit[kSweeps];
+#pragma unroll
+  for (int s = 0; s < kSweeps; ++s) {
+    const uint32_t i = s * 256 + threadIdx.x;
+    locate(a, row0, unit0, i, &row[s], &unit[s]);
+    const int c = int(unit[s]) * kUnit;
+    // lanes past the end (whole blocks of four) read nothing
+    load8<F32, ALIGNED>(a.x, row[s] * a.ld + c, base + i < a.units ? a.cols - c : 0, v[s]);
+  }
+#pragma unroll
+  for (int s = 0; s < kSweeps; ++s) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) {
+      const uint32_t m = __float_as_uint(v[s][j]) & 0x7FFFFFFFu;
+      top = top > m ? top : m;
+    }
+    const uint32_t b = exponent_byte<CODE>(max_of_four(top));
+    const float r = __uint_as_float((254u - (b == kNotFinite ? kLowest : b)) << 23);  // 2^(127 - b)
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float y[4];
+      constexpr float kTop = CODE == Code::kE4m3 ? 448.0f : 127.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = __builtin_amdgcn_fmed3f(v[s][4 * h + j] * r, -kTop, kTop);
+      if constexpr (CODE == Code::kE4m3) {
+        int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+        w[h] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], p, true));
+        if (b == kNotFinite) w[h] = 0x7F7F7F7Fu;
+      } else {
+        // 1.5 2^23 + y rounds y to an integer (to nearest even) in the low byte
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(y[j] + 12582912.0f);
+        const uint32_t lo = __builtin_amdgcn_perm(q[1], q[0], 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(q[3], q[2], 0x04000C0Cu);
+        w[h] = b == kNotFinite ? 0u : lo | hi;
+      }
+    }
+    if (base + s * 256 + threadIdx.x < a.units) {
+      *reinterpret_cast<u32x2*>(a.codes + (row[s] * a.row_units + unit[s]) * kUnit) = u32x2{w[0], w[1]};
+      if ((unit[s] & 3) == 0) a.scales[row[s] * (a.row_units >> 2) + (unit[s] >> 2)] = uint8_t(b);
+    }
+  }
+}
+
+template <bool F32, Code CODE, bool ALIGNED>
+__global__ __launch_bounds__(256) void checkpoint_unpack_kernel(PackArgs a) {
+  const int64_t base = int64_t(blockIdx.x) * (256 * kSweeps);
+  const int64_t row0 = base / a.row_units;
+  const uint32_t unit0 = uint32_t(base - row0 * a.row_units);
+  u32x2 w[kSweeps];
+  uint32_t b[kSweeps];
+  int64_t row[kSweeps];
+  uint32_t unit[kSweeps];
+#pragma unroll
+  for (int s = 0; s < kSweeps; ++s) {
+    const uint32_t i = s * 256 + threadIdx.x;
+    locate(a, row0, unit0, i, &row[s], &unit[s]);
+    if (base + i < a.units) {
+      w[s] = *reinterpret_cast<const u32x2*>(a.codes + (row[s] * a.row_units + unit[s]) * kUnit);
+      b[s] = a.scales[row[s] * (a.row_units >> 2) + (unit[s] >> 2)];
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kSweeps; ++s) {
+    const int c = int(unit[s]) * kUnit;
+    if (base + s * 256 + threadIdx.x >= a.units || c >= a.cols) continue;
+    const u32x2 lo = widen4<CODE>(w[s][0], b[s]), hi = widen4<CODE>(w[s][1], b[s]);
+    const uint32_t h[4] = {lo.x, lo.y, hi.x, hi.y};
+    const int left = a.cols - c;
+    const int64_t at = row[s] * a.ld + c;
+    if constexpr (F32) {
+      float* p = static_cast<float*>(a.x) + at;
+      float f[kUnit];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(h[j] << 16);
+        f[2 * j + 1] = __uint_as_float(h[j] & 0xFFFF0000u);
+      }
+      if (ALIGNED && left >= kUnit) {
+        *reinterpret_cast<f32x4v*>(p) = f32x4v{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<f32x4v*>(p + 4) = f32x4v{f[4], f[5], f[6], f[7]};
+      } else {
+#pragma unroll
+        for (int j = 0; j < kUnit; ++j)
+          if (j < left) p[j] = f[j];
+      }
+    } else {
+      uint16_t* p = static_cast<uint16_t*>(a.x) + at;
+      if (ALIGNED && left >= kUnit) {
+        *reinterpret_cast<u32x4*>(p) = u32x4{h[0], h[1], h[2], h[3]};
+      } else {
+#pragma unroll
+        for (int j = 0; j < kUnit; ++j)
+          if (j < left) p[j] = uint16_t(h[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  }
+}
+
+template <bool PACK, bool F32, Code CODE>
+void launch_as(const PackArgs& a, bool aligned, unsigned grid, hipStream_t st) {
+  if constexpr (PACK) {
+    if (aligned)
+      hipLaunchKernelGGL((checkpoint_pack_kernel<F32, CODE, true>), dim3(grid), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((checkpoint_pack_kernel<F32, CODE, false>), dim3(grid), dim3(256), 0, st, a);
+  } else {
+    if (aligned)
+      hipLaunchKernelGGL((checkpoint_unpack_kernel<F32, CODE, true>), dim3(grid), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((checkpoint_unpack_kernel<F32, CODE, false>), dim3(grid), dim3(256), 0, st, a);
+  }
+}
+
+template <bool PACK>
+int launch(const PackCall& c, void* stream) {
+  PackArgs a;
+  const int64_t blocks = (c.cols + kPackBlock - 1) / kPackBlock;
+  a.x = const_cast<void*>(c.x);
+  a.ld = c.ld;
+  a.codes = static_cast<uint8_t*>(c.codes);
+  a.scales = static_cast<uint8_t*>(c.scales);
+  a.row_units = uint32_t(blocks * (kPackBlock / kUnit));
+  a.units = c.rows * int64_t(a.row_units);
+  a.magic = ((uint64_t(1) << 40) + a.row_units - 1) / a.row_units;
+  a.cols = int32_t(c.cols);
+  const bool aligned = (reinterpret_cast<uintptr_t>(c.x) & 15) == 0 && c.ld % (c.f32 ? 4 : 8) == 0;
+  const unsigned grid = unsigned((a.units + 256 * kSweeps - 1) / (256 * kSweeps));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (c.f32) {
+    if (c.int8)
+      launch_as<PACK, true, Code::kInt8>(a, aligned, grid, st);
+    else
+      launch_as<PACK, true, Code::kE4m3>(a, aligned, grid, st);
+  } else {
+    if (c.int8)
+      launch_as<PACK, false, Code::kInt8>(a, aligned, grid, st);
+    else
+      launch_as<PACK, false, Code::kE4m3>(a, aligned, grid, st);
+  }
+  return int(hipGetLastError());
+}
+
+}  // namespace
+
+namespace tide {
+
+int launch_pack(const PackCall& c, void* stream) { return launch<true>(c, stream); }
+int launch_unpack(const PackCall& c, void* stream) { return launch<false>(c, stream); }
+
+}  // namespace tide

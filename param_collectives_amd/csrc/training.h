@@ -1,0 +1,56 @@
+// Private types of the training-step operators: the 8-bit activation
+// checkpoints (checkpoint.hip), the weight gradient that reads them
+// (weight_grad.hip), the vocabulary loss (vocab_loss.hip) and their C ABI
+// (training.cpp).
+#pragma once
+
+#include <cstdint>
+
+namespace tide {
+
+constexpr int64_t kPackBlock = 32;                      // values that share an exponent byte
+constexpr int64_t kMaxFeatures = int64_t(1) << 22;      // features, hidden size, vocabulary, row pitch: 32-bit tile offsets
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;  // tokens (rows)
+// Elements of one matrix: a launch counts its threads in 32 bits, and the
+// element-wise kernels give a thread at least 4.
+constexpr int64_t kMaxElems = int64_t(1) << 34;
+
+struct PackCall {
+  const void* x;  // pack: source; unpack: destination
+  int32_t f32;
+  int64_t rows, cols, ld;
+  int32_t int8;
+  void* codes;
+  void* scales;
+};
+
+struct WeightGradCall {
+  const void* dy;
+  int64_t dy_ld;
+  const void* codes;
+  const uint8_t* scales;
+  int64_t tokens, outs, ins;
+  int32_t int8, f32, accumulate;
+  float alpha;
+  void* dw;
+};
+
+// How a weight gradient is cut into tiles and splits, and its workspace:
+// dy_bytes of aligned rows (when dY's are not), then partial_bytes.
+struct WeightGradPlan {
+  bool big;  // 256 x 256 tiles
+  int64_t tiles_m, tiles_n, splits, split_k, dy_ld, dy_bytes, partial_bytes;
+};
+
+// Whether rows of pitch `ld` bf16 elements from p all start on 16 bytes.
+bool rows_aligned(const void* p, int64_t ld);
+WeightGradPlan plan_weight_grad(int64_t tokens, int64_t outs, int64_t ins, bool aligned);
+
+// Launches; each returns the hipError_t as int.
+int launch_pack(const PackCall& c, void* stream);
+int launch_unpack(const PackCall& c, void* stream);
+int launch_weight_grad(const WeightGradCall& c, void* workspace, void* stream);
+int launch_align_rows(const void* src, int64_t src_ld, int64_t rows, int64_t cols, void* dst, int64_t ld,
+                      void* stream);
+
+}  // namespace tide

@@ -1,0 +1,222 @@
+// Weight gradient of a linear layer from its activation checkpoint:
+//   dW[o][i] = alpha sum_t dY[t][o] X[t][i]  (+ the old dW)
+// with dY bf16 and X in the packed 8-bit form (checkpoint.hip).
+#include "gemm.h"
+#include "tide_internal.h"
+#include "training.h"
+
+namespace {
+
+using namespace tide;
+
+struct WeightGradArgs {
+  Operand dy, x;
+  int64_t outs, ins, tokens;
+  int64_t split_k;   // tokens of one split, a multiple of 64
+  float* partial;    // [splits][outs][ins], or null: the result is written
+  void* dw;
+  float alpha;
+  int32_t f32, accumulate;
+  uint32_t tiles_m, tiles_n;
+};
+
+__device__ __forceinline__ uint32_t bf16_bits_of(float v) {
+  const __bf16 b = __bf16(v);  // round to nearest even
+  uint16_t r;
+  __builtin_memcpy(&r, &b, 2);
+  return r;
+}
+
+// alpha s (+ old) for the `n` values v of one row from element `at`, rounded
+// once to the gradient's type.
+__device__ __forceinline__ void store_grad(void* dw, int32_t f32, int32_t accumulate, float alpha, int64_t at, int n,
+                                           f32x4v v) {
+  if (f32) {
+    float* d = static_cast<float*>(dw) + at;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(d) & 15) == 0) {
+      f32x4v r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = alpha * v[i];
+      if (accumulate) {
+        const f32x4v old = *reinterpret_cast<const f32x4v*>(d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = old[i] + r[i];
+      }
+      *reinterpret_cast<f32x4v*>(d) = r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) d[i] = accumulate ? d[i] + alpha * v[i] : alpha * v[i];
+    }
+  } else {
+    uint16_t* d = static_cast<uint16_t*>(dw) + at;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(d) & 7) == 0) {
+      float r[4];
+      u32x2 old = u32x2{0, 0};
+      if (accumulate) old = *reinterpret_cast<const u32x2*>(d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float o = __uint_as_float(i & 1 ? old[i >> 1] & 0xFFFF0000u : old[i >> 1] << 16);
+        r[i] = accumulate ? o + alpha * v[i] : alpha * v[i];
+      }
+      *reinterpret_cast<u32x2*>(d) =
+          u32x2{bf16_bits_of(r[0]) | bf16_bits_of(r[1]) << 16, bf16_bits_of(r[2]) | bf16_bits_of(r[3]) << 16};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) {
+          const float r = alpha * v[i];
+          d[i] = uint16_t(bf16_bits_of(accumulate ? __uint_as_float(uint32_t(d[i]) << 16) + r : r));
+        }
+    }
+  }
+}
+
+template <Code CODE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void weight_grad_kernel(WeightGradArgs a) {
+  using G = Gemm<Form::kCols, Form::kPacked, CODE, BM, BN, WM, WN>;
+  __shared__ __align__(16) char lds0[G::kStage];
+  __shared__ __align__(16) char lds1[G::kStage];
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
+  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
+  const int64_t k0 = int64_t(blockIdx.y) * a.split_k;
+  const int64_t k1 = k0 + a.split_k < a.tokens ? k0 + a.split_k : a.tokens;
+  G g;
+  g.run(a.dy, a.x, m0, n0, k0, k1, lds0, lds1);
+  if (a.partial) {
+    float* p = a.partial + int64_t(blockIdx.y) * a.outs * a.ins;
+    g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
+      if (m < a.outs && n < a.ins) store_grad(p, 1, 0, 1.0f, m * a.ins + n, int(a.ins - n < 4 ? a.ins - n : 4), v);
+    });
+  } else {
+    g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
+      if (m < a.outs && n < a.ins)
+        store_grad(a.dw, a.f32, a.accumulate, a.alpha, m * a.ins + n, int(a.ins - n < 4 ? a.ins - n : 4), v);
+    });
+  }
+}
+
+// Sums the splits in order.
+__global__ __launch_bounds__(256) void join_splits_kernel(const float* partial, int32_t splits, int64_t elems,
+                                                          void* dw, int32_t f32, int32_t accumulate, float alpha) {
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= elems) return;
+  const int n = elems - i < 4 ? int(elems - i) : 4;
+  f32x4v s = f32x4v{0.f, 0.f, 0.f, 0.f};
+  for (int32_t k = 0; k < splits; ++k) {
+    const float* p = partial + int64_t(k) * elems + i;
+    if (n == 4 && (elems & 3) == 0) {
+      const f32x4v v = *reinterpret_cast<const f32x4v*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) s[j] += p[j];
+    }
+  }
+  store_grad(dw, f32, accumulate, alpha, i, n, s);
+}
+
+// Rows of any pitch and alignment -> rows of pitch `ld` (a multiple of 8)
+// that start on 16 bytes, filled up with zeros.
+__global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t* src, int64_t src_ld, int64_t rows,
+                                                         int64_t cols, uint16_t* dst, int64_t ld) {
+  const int64_t groups = ld / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= rows * groups) return;
+  const int64_t r = i / groups, c = (i - r * groups) * 8;
+  const uint16_t* s = src + r * src_ld + c;
+  uint32_t v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = (c + 2 * j < cols ? uint32_t(s[2 * j]) : 0u) | (c + 2 * j + 1 < cols ? uint32_t(s[2 * j + 1]) : 0u) << 16;
+  *reinterpret_cast<u32x4*>(dst + r * ld + c) = u32x4{v[0], v[1], v[2], v[3]};
+}
+
+}  // namespace
+
+namespace tide {
+
+bool rows_aligned(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
+
+int launch_align_rows(const void* src, int64_t src_ld, int64_t rows, int64_t cols, void* dst, int64_t ld,
+                      void* stream) {
+  const int64_t n = rows * (ld / 8);
+  if (n == 0) return 0;
+  hipLaunchKernelGGL(align_rows_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), static_cast<const uint16_t*>(src), src_ld, rows, cols,
+                     static_cast<uint16_t*>(dst), ld);
+  return int(hipGetLastError());
+}
+
+WeightGradPlan plan_weight_grad(int64_t tokens, int64_t outs, int64_t ins, bool aligned) {
+  WeightGradPlan p;
+  const int64_t steps = (tokens + kBK - 1) / kBK;
+  p.big = ((outs + 255) / 256) * ((ins + 255) / 256) >= 192;
+  const int64_t side = p.big ? 256 : 128;
+  p.tiles_m = (outs + side - 1) / side;
+  p.tiles_n = (ins + side - 1) / side;
+  const int64_t tiles = p.tiles_m * p.tiles_n;
+  int64_t splits = 1;
+  if (!p.big && tiles > 0) {
+    splits = 512 / tiles;
+    if (splits > steps / 4) splits = steps / 4;
+    if (splits < 1) splits = 1;
+  }
+  const int64_t per = splits > 1 ? (steps + splits - 1) / splits : (steps > 0 ? steps : 1);
+  p.splits = steps > 0 ? (steps + per - 1) / per : 1;
+  p.split_k = per * kBK;
+  p.dy_ld = (outs + 63) / 64 * 64;
+  p.dy_bytes = aligned ? 0 : (tokens * p.dy_ld * 2 + 255) / 256 * 256;
+  p.partial_bytes = p.splits > 1 ? p.splits * outs * ins * 4 : 0;
+  return p;
+}
+
+int launch_weight_grad(const WeightGradCall& c, void* workspace, void* stream) {
+  const bool aligned = rows_aligned(c.dy, c.dy_ld);
+  const WeightGradPlan p = plan_weight_grad(c.tokens, c.outs, c.ins, aligned);
+  char* ws = static_cast<char*>(workspace);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  WeightGradArgs a;
+  a.dy = Operand{c.dy, nullptr, c.dy_ld, 0, c.outs};
+  if (!aligned) {
+    const int rc = launch_align_rows(c.dy, c.dy_ld, c.tokens, c.outs, ws, p.dy_ld, stream);
+    if (rc != 0) return rc;
+    a.dy.base = ws;
+    a.dy.ld = p.dy_ld;
+  }
+  const int64_t blocks = (c.ins + 31) / 32;
+  a.x = Operand{c.codes, c.scales, blocks * 32, blocks, c.ins};
+  a.outs = c.outs;
+  a.ins = c.ins;
+  a.tokens = c.tokens;
+  a.split_k = p.split_k;
+  a.partial = p.splits > 1 ? reinterpret_cast<float*>(ws + p.dy_bytes) : nullptr;
+  a.dw = c.dw;
+  a.alpha = c.alpha;
+  a.f32 = c.f32;
+  a.accumulate = c.accumulate;
+  a.tiles_m = uint32_t(p.tiles_m);
+  a.tiles_n = uint32_t(p.tiles_n);
+  const dim3 grid(unsigned(p.tiles_m * p.tiles_n), unsigned(p.splits));
+  if (p.big) {
+    if (c.int8)
+      hipLaunchKernelGGL((weight_grad_kernel<Code::kInt8, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
+    else
+      hipLaunchKernelGGL((weight_grad_kernel<Code::kE4m3, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
+  } else {
+    if (c.int8)
+      hipLaunchKernelGGL((weight_grad_kernel<Code::kInt8, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((weight_grad_kernel<Code::kE4m3, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  }
+  int rc = int(hipGetLastError());
+  if (rc != 0 || p.splits == 1) return rc;
+  const int64_t elems = c.outs * c.ins;
+  hipLaunchKernelGGL(join_splits_kernel, dim3(unsigned((elems / 4 + 256) / 256)), dim3(256), 0, st, a.partial,
+                     int32_t(p.splits), elems, c.dw, c.f32, c.accumulate, c.alpha);
+  return int(hipGetLastError());
+}
+
+}  // namespace tide

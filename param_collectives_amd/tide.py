@@ -36,6 +36,8 @@ FLAG_CACHED_STORES = 0x2
 FLAG_NO_LDS = 0x4
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
+CODE_E4M3 = 0
+CODE_INT8 = 1
 MAX_WORLD = 256
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -55,6 +57,11 @@ EXPORTS = (
     "tide_allgather_copyin",
     "tide_reduce_scatter_local_f32",
     "tide_stock_chunk_cat",
+    "tide_checkpoint_layout",
+    "tide_checkpoint_pack",
+    "tide_checkpoint_unpack",
+    "tide_checkpoint_weight_grad_workspace",
+    "tide_checkpoint_weight_grad",
     "tide_device_info",
     "tide_probe_launch",
     "tide_victim_axpb",
@@ -97,6 +104,12 @@ def _load():
     lib.tide_reduce_scatter_local_f32.argtypes = lib.tide_reduce_scatter_local.argtypes
     lib.tide_reduce_scatter_local_noalloc.argtypes = lib.tide_reduce_scatter_local.argtypes
     lib.tide_stock_chunk_cat.argtypes = [vp, ctypes.POINTER(vp), vp, vp]
+    f32 = ctypes.c_float
+    lib.tide_checkpoint_layout.argtypes = [i64, i64p, i64p]
+    lib.tide_checkpoint_pack.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp]
+    lib.tide_checkpoint_unpack.argtypes = [vp, vp, i32, i64, i64, vp, i32, i64, vp]
+    lib.tide_checkpoint_weight_grad_workspace.argtypes = [vp, i64, i64, i64, i64, i64p]
+    lib.tide_checkpoint_weight_grad.argtypes = [vp, i64, i64, i64, vp, vp, i32, i64, vp, i32, f32, i32, vp, i64, vp]
     i32p = ctypes.POINTER(i32)
     lib.tide_device_info.argtypes = [i32p, i32p, i32p, i32p]
     lib.tide_probe_launch.argtypes = [vp, i32, i32, i64, vp]
@@ -434,6 +447,165 @@ def allgather_copyin(plan, shards, rank_major, stream=None):
     W*S elements; fp32 shards are cast by round to nearest even)."""
     ptrs, dt, rm = _ci_checked(plan, shards, rank_major)
     plan.allgather_copyin_raw(ptrs, dt, rm, _stream_handle(stream))
+
+
+# ------------------------------------------------------------ activation checkpoints
+
+
+def _on_device(t, what):
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what}: expected a GPU tensor, got {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: lives on {t.device}, but the kernels run on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _matrix(t, dtypes, what, strided=True):
+    """(address, TIDE_DTYPE_*, rows, columns, row stride) of a matrix of one of
+    `dtypes` whose rows are contiguous; without `strided` they have no gaps."""
+    import torch
+
+    _on_device(t, what)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a matrix, got {t.dim()} dimensions")
+    rows, cols = t.shape
+    # the strides of a dimension of one element (or none) say nothing
+    stride = t.stride(0) if rows > 1 and t.numel() else cols
+    if t.numel() and ((cols > 1 and t.stride(1) != 1) or stride < cols):
+        raise ValueError(f"{what}: expected contiguous, non-overlapping rows, got strides {t.stride()}")
+    if not strided and stride != cols:
+        raise ValueError(f"{what}: expected rows without gaps, got strides {t.stride()}")
+    return ctypes.c_void_p(t.data_ptr() or None), DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16, rows, cols, stride
+
+
+def _floats():
+    import torch
+
+    return (torch.bfloat16, torch.float32)
+
+
+def checkpoint_layout(cols):
+    """(code columns, scale columns) of a checkpoint of rows of `cols` values
+    (tide_checkpoint_layout)."""
+    codes, scales = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib.tide_checkpoint_layout(int(cols), ctypes.byref(codes), ctypes.byref(scales)))
+    return codes.value, scales.value
+
+
+def _packed(codes, scales, rows, cols):
+    """(codes address, scales address, TIDE_CODE_*) of a checkpoint of a rows x cols matrix."""
+    import torch
+
+    kinds = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_INT8}
+    for t, what in ((codes, "codes"), (scales, "scales")):
+        _on_device(t, what)
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous tensor")
+    if codes.dtype not in kinds:
+        raise TypeError(f"codes: expected torch.float8_e4m3fn or torch.int8, got {codes.dtype}")
+    if scales.dtype != torch.uint8:
+        raise TypeError(f"scales: expected torch.uint8, got {scales.dtype}")
+    c, s = checkpoint_layout(cols)
+    if tuple(codes.shape) != (rows, c) or tuple(scales.shape) != (rows, s):
+        raise ValueError(f"codes and scales of a {rows} x {cols} matrix are {(rows, c)} and {(rows, s)}, got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    return ctypes.c_void_p(codes.data_ptr() or None), ctypes.c_void_p(scales.data_ptr() or None), kinds[codes.dtype]
+
+
+def checkpoint_pack_call(x, codes, scales):
+    """A registered checkpoint pack (see checkpoint_pack)."""
+    p, dt, rows, cols, stride = _matrix(x, _floats(), "x")
+    c, s, fmt = _packed(codes, scales, rows, cols)
+    return Call(lib.tide_checkpoint_pack, (p, dt, rows, cols, stride, fmt, c, s), (x, codes, scales))
+
+
+def checkpoint_pack(x, codes, scales, stream=None):
+    """Pack a matrix into its 8-bit form: x (bf16 or fp32, contiguous rows) ->
+    codes (float8_e4m3fn or int8, which chooses the code type) and scales
+    (uint8), sized by checkpoint_layout (tide_checkpoint_pack)."""
+    checkpoint_pack_call(x, codes, scales)(stream)
+
+
+def checkpoint_unpack_call(codes, scales, out):
+    """A registered checkpoint restore (see checkpoint_unpack)."""
+    p, dt, rows, cols, stride = _matrix(out, _floats(), "out")
+    c, s, fmt = _packed(codes, scales, rows, cols)
+    return Call(lib.tide_checkpoint_unpack, (c, s, fmt, rows, cols, p, dt, stride), (codes, scales, out))
+
+
+def checkpoint_unpack(codes, scales, out, stream=None):
+    """Restore a packed matrix, exactly, into out (bf16 or fp32, contiguous
+    rows; tide_checkpoint_unpack)."""
+    checkpoint_unpack_call(codes, scales, out)(stream)
+
+
+def _workspace(nbytes, given, stream):
+    """A workspace of nbytes: the caller's, or one that belongs to the stream
+    the call runs on (freed memory goes back to that stream's work only)."""
+    import torch
+
+    if given is None:
+        if nbytes == 0:
+            return None
+        with torch.cuda.stream(stream):  # None: the current stream
+            return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    _on_device(given, "workspace")
+    if given.dtype != torch.uint8 or not given.is_contiguous():
+        raise TypeError("workspace: expected a contiguous torch.uint8 tensor")
+    return given
+
+
+def _workspace_args(w):
+    return ctypes.c_void_p(w.data_ptr() or None) if w is not None else None, w.numel() if w is not None else 0
+
+
+def _weight_grad(dy, codes, scales, dw, alpha, accumulate, workspace, stream):
+    import torch
+
+    y, _, rows, outs, stride = _matrix(dy, (torch.bfloat16,), "dy")
+    w, dt, w_outs, ins, _ = _matrix(dw, _floats(), "dw", strided=False)
+    if w_outs != outs:
+        raise ValueError(f"dw has {w_outs} rows, dy {outs} columns")
+    c, s, fmt = _packed(codes, scales, rows, ins)
+    need = ctypes.c_int64()
+    _check(lib.tide_checkpoint_weight_grad_workspace(y, rows, outs, stride, ins, ctypes.byref(need)))
+    ws = _workspace(need.value, workspace, stream)
+    return Call(lib.tide_checkpoint_weight_grad,
+                (y, rows, outs, stride, c, s, fmt, ins, w, dt, ctypes.c_float(alpha), int(bool(accumulate)),
+                 *_workspace_args(ws)), (dy, codes, scales, dw, ws))
+
+
+def checkpoint_weight_grad_workspace(dy, in_features):
+    """Bytes of workspace the weight gradient from dy takes
+    (tide_checkpoint_weight_grad_workspace)."""
+    import torch
+
+    y, _, rows, outs, stride = _matrix(dy, (torch.bfloat16,), "dy")
+    need = ctypes.c_int64()
+    _check(lib.tide_checkpoint_weight_grad_workspace(y, rows, outs, stride, int(in_features), ctypes.byref(need)))
+    return need.value
+
+
+def checkpoint_weight_grad_call(dy, codes, scales, dw, alpha=1.0, accumulate=False, workspace=None):
+    """A registered weight gradient (see checkpoint_weight_grad); it keeps one
+    workspace, so its calls must not overlap."""
+    return _weight_grad(dy, codes, scales, dw, alpha, accumulate, workspace, None)
+
+
+def checkpoint_weight_grad(dy, codes, scales, dw, alpha=1.0, accumulate=False, workspace=None, stream=None):
+    """Weight gradient of a linear layer from the checkpoint of its input:
+    dw[o][i] = alpha * sum_t dy[t][o] X[t][i], added to the old dw when
+    accumulate is true; dy bf16 (tokens x out_features, contiguous rows), dw
+    bf16 or fp32 (out_features x in_features).  `workspace` is a uint8 tensor of
+    at least checkpoint_weight_grad_workspace bytes; without one the call takes
+    its own (tide_checkpoint_weight_grad)."""
+    _weight_grad(dy, codes, scales, dw, alpha, accumulate, workspace, stream)(stream)
 
 
 # ------------------------------------------------------------ instruments

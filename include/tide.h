@@ -459,6 +459,58 @@ tide_status tide_checkpoint_weight_grad(const uint16_t* dy, int64_t rows, int64_
                                         int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Vocabulary loss: the cross entropy of the output projection, whose logits
+ * (tokens x vocab) are never kept, and the gradients it sends back: dhidden to
+ * the last layer, dweight to the reduce-scatter.  Neither touches a plan.
+ *
+ * With H the hidden states (tokens x hidden_size bf16) and W the projection's
+ * weights (vocab x hidden_size bf16), for every token t
+ *   z[t][v] = sum over d of H[t][d] * W[v][d]
+ *   lse[t]  = log(sum over v of exp(z[t][v]))
+ *   loss[t] = lse[t] - z[t][targets[t]]
+ *   dz[t][v] = grad_loss[t] * (exp(z[t][v] - lse[t]) - (v == targets[t]))
+ *   dhidden[t][d] = sum over v of dz[t][v] * W[v][d]
+ *   dweight[v][d] = sum over t of dz[t][v] * H[t][d]     (+ old, accumulate = 1)
+ * A token whose target lies outside [0, vocab) is left out: its loss, lse and
+ * row of dhidden are 0, it adds nothing to dweight, and neither its hidden
+ * state nor its grad_loss has any effect, NaN or not.
+ * Products are exact, sums and the softmax fp32.  dz, over the largest
+ * |grad_loss|, is rounded once to bf16 (by at most 2^-8 of it), the operand of
+ * the two gradient products; their sums take that factor back in fp32, and
+ * dhidden and dweight are rounded once more, to their own types.  The order of every sum
+ * depends on the sizes (and, in the gradients, on how many tokens count) only.
+ *
+ *   hidden, weight  rows hidden_stride and weight_stride elements apart, 2-byte
+ *           aligned.  Where weight's rows do not all start and end on 16 bytes
+ *           (a pointer, stride or length that is not a multiple of 8 elements)
+ *           the workspace holds a copy of it.
+ *   targets tokens int64, 8-byte aligned
+ *   loss    tokens fp32;  lse  tokens fp32, or NULL
+ *   grad_loss  tokens fp32: the gradient of each token's loss (1 / tokens for a
+ *           mean)
+ *   dhidden tokens x hidden_size bf16, dweight vocab x hidden_size of
+ *           dweight_dtype, both without gaps
+ *   workspace  as for the weight gradient above.  With gradients it holds the
+ *           exponentials of at most 2 GiB worth of tokens at a time (at least
+ *           256 tokens), 2 bytes each.
+ * Sizes: tokens up to 2^24 (0 allowed: dweight becomes 0, or stays), vocab and
+ * hidden_size in [1, 2^22], matrices up to 2^34 elements.
+ * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+tide_status tide_vocab_loss_workspace(const uint16_t* hidden, int64_t hidden_stride, const uint16_t* weight,
+                                      int64_t weight_stride, int64_t tokens, int64_t hidden_size, int64_t vocab,
+                                      int32_t gradients, int32_t dweight_dtype, int64_t* bytes);
+tide_status tide_vocab_loss(const uint16_t* hidden, int64_t hidden_stride, const uint16_t* weight,
+                            int64_t weight_stride, const int64_t* targets, int64_t tokens, int64_t hidden_size,
+                            int64_t vocab, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+tide_status tide_vocab_loss_grad(const uint16_t* hidden, int64_t hidden_stride, const uint16_t* weight,
+                                 int64_t weight_stride, const int64_t* targets, const float* grad_loss,
+                                 int64_t tokens, int64_t hidden_size, int64_t vocab, float* loss, float* lse,
+                                 uint16_t* dhidden, void* dweight, int32_t dweight_dtype, int32_t accumulate,
+                                 void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Interference instruments (Section 2.2 "SM Wave Quantization", Equation 4,
  * Figure 3, Table 4 and Table 5): what one GPU can show of the cost a
  * collective's kernels impose on the compute they overlap.  None of these

@@ -12,6 +12,9 @@
                          activations kept in 8 bits between the passes
   checkpoint_weight_grad a linear layer's weight gradient from such a
                          checkpoint of its input
+  vocab_loss, vocab_loss_grad
+                         cross entropy of the output projection without its
+                         logits; with its gradients
   stock_chunk_cat        stock FSDP2's gradient pack of one rank (the baseline)
   probe, victim_axpb, Stream
                          interference instruments: hardware-ID probe,
@@ -54,4 +57,9 @@ from .tide import (  # noqa: F401
     device_info,
     probe,
     victim_axpb,
+    vocab_loss,
+    vocab_loss_call,
+    vocab_loss_grad,
+    vocab_loss_grad_call,
+    vocab_loss_workspace,
 )

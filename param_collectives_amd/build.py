@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libtide.so")
 SOURCES = [os.path.join(CSRC, n) for n in (
     "plan.cpp", "capi.cpp", "kernels.hip", "instruments.hip", "scratch.hip",
-    "training.cpp", "checkpoint.hip", "weight_grad.hip")]
+    "training.cpp", "checkpoint.hip", "weight_grad.hip", "vocab_loss.hip")]
 ARCH = "gfx950"
 
 

@@ -375,6 +375,76 @@ struct Gemm {
   }
 };
 
+__device__ __forceinline__ uint32_t bf16_bits_of(float v) {
+  const __bf16 b = __bf16(v);  // round to nearest even
+  uint16_t r;
+  __builtin_memcpy(&r, &b, 2);
+  return r;
+}
+
+// alpha s (+ old) for the `n` values v of one row from element `at`, rounded
+// once to the output's type (fp32 or bf16).
+__device__ __forceinline__ void store_values(void* out, int32_t f32, int32_t accumulate, float alpha, int64_t at, int n,
+                                           f32x4v v) {
+  if (f32) {
+    float* d = static_cast<float*>(out) + at;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(d) & 15) == 0) {
+      f32x4v r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = alpha * v[i];
+      if (accumulate) {
+        const f32x4v old = *reinterpret_cast<const f32x4v*>(d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = old[i] + r[i];
+      }
+      *reinterpret_cast<f32x4v*>(d) = r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) d[i] = accumulate ? d[i] + alpha * v[i] : alpha * v[i];
+    }
+  } else {
+    uint16_t* d = static_cast<uint16_t*>(out) + at;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(d) & 7) == 0) {
+      float r[4];
+      u32x2 old = u32x2{0, 0};
+      if (accumulate) old = *reinterpret_cast<const u32x2*>(d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float o = __uint_as_float(i & 1 ? old[i >> 1] & 0xFFFF0000u : old[i >> 1] << 16);
+        r[i] = accumulate ? o + alpha * v[i] : alpha * v[i];
+      }
+      *reinterpret_cast<u32x2*>(d) =
+          u32x2{bf16_bits_of(r[0]) | bf16_bits_of(r[1]) << 16, bf16_bits_of(r[2]) | bf16_bits_of(r[3]) << 16};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) {
+          const float r = alpha * v[i];
+          d[i] = uint16_t(bf16_bits_of(accumulate ? __uint_as_float(uint32_t(d[i]) << 16) + r : r));
+        }
+    }
+  }
+}
+
+// The splits' values of `n` elements from element `at`, added in order.
+__device__ __forceinline__ f32x4v sum_splits(const float* partial, int32_t splits, int64_t elems, int64_t at, int n) {
+  f32x4v s = f32x4v{0.f, 0.f, 0.f, 0.f};
+  for (int32_t k = 0; k < splits; ++k) {
+    const float* p = partial + int64_t(k) * elems + at;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+      const f32x4v v = *reinterpret_cast<const f32x4v*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) s[j] += p[j];
+    }
+  }
+  return s;
+}
+
 // Workgroups go round-robin over the 8 XCDs, each with an L2 of its own: XCD x
 // takes a contiguous share of the tiles, in an order that walks `group` tile
 // rows before it moves to the next tile column, so that what an XCD works on

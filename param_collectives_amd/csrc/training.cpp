@@ -1,7 +1,7 @@
 // C ABI of the training-step operators (include/tide.h): argument checks and
-// workspace sizes of the 8-bit activation checkpoints and of the weight
-// gradient that reads them.  Host code only; the kernels are in
-// checkpoint.hip and weight_grad.hip.
+// workspace sizes of the 8-bit activation checkpoints, of the weight gradient
+// that reads them and of the vocabulary loss.  Host code only; the kernels are
+// in checkpoint.hip, weight_grad.hip and vocab_loss.hip.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -103,8 +103,35 @@ tide_status check_weight_grad(const void* dy, int64_t rows, int64_t outs, int64_
 
 int64_t weight_grad_bytes(const void* dy, int64_t rows, int64_t outs, int64_t dy_stride, int64_t ins) {
   if (outs == 0 || ins == 0) return 0;
-  const tide::WeightGradPlan p = tide::plan_weight_grad(rows, outs, ins, tide::rows_aligned(dy, dy_stride));
+  const tide::WeightGradPlan p = tide::plan_weight_grad(rows, outs, ins, tide::rows_aligned(dy, dy_stride, outs));
   return p.dy_bytes + p.partial_bytes;
+}
+
+tide_status check_vocab_loss(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride,
+                             int64_t tokens, int64_t hidden_size, int64_t vocab) {
+  TIDE_TRY(check_matrix("hidden", tokens, hidden_size, hidden_stride));
+  TIDE_TRY(check_matrix("weight", vocab, hidden_size, weight_stride));
+  if (vocab > kMaxFeatures || tokens > tide::kMaxLossTokens)
+    return tide::set_error(TIDE_ERR_RANGE, "more than 2^24 tokens, or a vocabulary above 2^22");
+  if (vocab < 1 || hidden_size < 1) return invalid("the vocabulary and the hidden size must be at least 1");
+  if (tokens > 0) {
+    TIDE_TRY(check_pointer("hidden", hidden, 2));
+    TIDE_TRY(check_pointer("weight", weight, 2));
+  }
+  return TIDE_OK;
+}
+
+tide::VocabLossCall vocab_loss_call(const void* hidden, int64_t hidden_stride, const void* weight,
+                                    int64_t weight_stride, int64_t tokens, int64_t hidden_size, int64_t vocab) {
+  tide::VocabLossCall c{};
+  c.h = hidden;
+  c.h_ld = hidden_stride;
+  c.w = weight;
+  c.w_ld = weight_stride;
+  c.tokens = tokens;
+  c.hidden = hidden_size;
+  c.vocab = vocab;
+  return c;
 }
 
 }  // namespace
@@ -187,6 +214,76 @@ tide_status tide_checkpoint_weight_grad(const uint16_t* dy, int64_t rows, int64_
     c.alpha = alpha;
     c.dw = dw;
     return hip_status(tide::launch_weight_grad(c, workspace, stream), "weight_grad_kernel launch");
+  });
+}
+
+tide_status tide_vocab_loss_workspace(const uint16_t* hidden, int64_t hidden_stride, const uint16_t* weight,
+                                      int64_t weight_stride, int64_t tokens, int64_t hidden_size, int64_t vocab,
+                                      int32_t gradients, int32_t dweight_dtype, int64_t* bytes) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    if (bytes == nullptr) return invalid("bytes must not be NULL");
+    if (gradients != 0 && gradients != 1) return invalid("gradients must be 0 or 1");
+    TIDE_TRY(check_dtype("dweight_dtype", dweight_dtype));
+    TIDE_TRY(check_vocab_loss(hidden, hidden_stride, weight, weight_stride, tokens, hidden_size, vocab));
+    tide::VocabLossCall c = vocab_loss_call(hidden, hidden_stride, weight, weight_stride, tokens, hidden_size, vocab);
+    c.dhidden_wanted = gradients == 1;
+    c.dw_f32 = dweight_dtype == TIDE_DTYPE_F32;
+    *bytes = tide::vocab_loss_bytes(c);
+    return TIDE_OK;
+  });
+}
+
+tide_status tide_vocab_loss(const uint16_t* hidden, int64_t hidden_stride, const uint16_t* weight,
+                            int64_t weight_stride, const int64_t* targets, int64_t tokens, int64_t hidden_size,
+                            int64_t vocab, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    TIDE_TRY(check_vocab_loss(hidden, hidden_stride, weight, weight_stride, tokens, hidden_size, vocab));
+    tide::VocabLossCall c = vocab_loss_call(hidden, hidden_stride, weight, weight_stride, tokens, hidden_size, vocab);
+    if (tokens == 0) return TIDE_OK;
+    TIDE_TRY(check_pointer("targets", targets, 8));
+    TIDE_TRY(check_pointer("loss", loss, 4));
+    if (lse) TIDE_TRY(check_pointer("lse", lse, 4));
+    TIDE_TRY(check_workspace(workspace, workspace_bytes, tide::vocab_loss_bytes(c)));
+    c.targets = targets;
+    c.loss = loss;
+    c.lse = lse;
+    return hip_status(tide::launch_vocab_loss(c, workspace, stream), "vocabulary loss launch");
+  });
+}
+
+tide_status tide_vocab_loss_grad(const uint16_t* hidden, int64_t hidden_stride, const uint16_t* weight,
+                                 int64_t weight_stride, const int64_t* targets, const float* grad_loss,
+                                 int64_t tokens, int64_t hidden_size, int64_t vocab, float* loss, float* lse,
+                                 uint16_t* dhidden, void* dweight, int32_t dweight_dtype, int32_t accumulate,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    TIDE_TRY(check_dtype("dweight_dtype", dweight_dtype));
+    if (accumulate != 0 && accumulate != 1) return invalid("accumulate must be 0 or 1");
+    TIDE_TRY(check_vocab_loss(hidden, hidden_stride, weight, weight_stride, tokens, hidden_size, vocab));
+    TIDE_TRY(check_pointer("dweight", dweight, size_of(dweight_dtype)));
+    tide::VocabLossCall c = vocab_loss_call(hidden, hidden_stride, weight, weight_stride, tokens, hidden_size, vocab);
+    c.dhidden_wanted = true;
+    c.dw = dweight;
+    c.dw_f32 = dweight_dtype == TIDE_DTYPE_F32;
+    c.accumulate = accumulate;
+    if (tokens > 0) {
+      TIDE_TRY(check_pointer("targets", targets, 8));
+      TIDE_TRY(check_pointer("grad_loss", grad_loss, 4));
+      TIDE_TRY(check_pointer("loss", loss, 4));
+      if (lse) TIDE_TRY(check_pointer("lse", lse, 4));
+      TIDE_TRY(check_pointer("dhidden", dhidden, 2));
+      TIDE_TRY(check_workspace(workspace, workspace_bytes, tide::vocab_loss_bytes(c)));
+    }
+    c.targets = targets;
+    c.grad_loss = grad_loss;
+    c.loss = loss;
+    c.lse = lse;
+    c.dhidden = dhidden;
+    return hip_status(tide::launch_vocab_loss(c, workspace, stream), "vocabulary loss launch");
   });
 }
 

@@ -1,0 +1,646 @@
+// Cross entropy of an output projection over a large vocabulary on MI355X
+// (gfx950), with its gradients: for tokens t with hidden states H, projection
+// rows W and targets,
+//   z[t][v] = sum_d H[t][d] W[v][d]
+//   lse[t]  = log sum_v exp z[t][v],   loss[t] = lse[t] - z[t][target]
+//   dz[t][v] = g[t] (exp(z[t][v] - lse[t]) - [v = target])
+//   dH = dz W,   dW = dz^T H.
+// The logits are formed tile by tile in the matrix cores' fp32 accumulators
+// and never written.  The loss keeps of each tile row its maximum and its sum
+// of exponentials, and joins them over the vocabulary's tiles.  The gradients
+// need every logit twice more; recomputing them would add a third to the three
+// products' work, so the tile also leaves exp(z - tile maximum), which lies in
+// [0, 1], as an fp16 number times 2^15 (rounded by at most 2^-11, eight times finer
+// than the bf16 it becomes), for a bounded piece of the tokens at a time.  A
+// pass over that piece turns it into dz in bf16, the operand of the two
+// products; the target's entry is expm1(z - lse) from the fp32 logit, since
+// exp(z - lse) - 1 would lose a confident token's gradient to rounding.  What
+// is rounded to bf16 is dz over the largest |g|, which comes back as a factor of
+// the products' fp32 sums: g of a mean over n tokens is 1/n for all of them,
+// and its own rounding (up to 2^-8, the same in every entry) would not average
+// out (measured: the gradients' error of 0.0032 in the 2-norm falls to 0.0019,
+// 0.0017 of it from the results' own rounding).
+//
+// Tokens whose target lies outside the vocabulary are left out: their rows are
+// never read, so nothing in them (a padded batch's NaN) reaches the others.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm.h"
+#include "training.h"
+
+namespace {
+
+using namespace tide;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kExpScale = 32768.0f;  // exponentials are kept as fp16 times this
+
+__device__ __forceinline__ uint32_t half_bits(float v) {
+  const _Float16 h = _Float16(v);  // round to nearest even
+  uint16_t r;
+  __builtin_memcpy(&r, &h, 2);
+  return r;
+}
+
+__device__ __forceinline__ float half_value(uint32_t bits) {
+  const uint16_t b = uint16_t(bits);
+  _Float16 h;
+  __builtin_memcpy(&h, &b, 2);
+  return float(h);
+}
+
+// Rows of this piece that hold a token: the piece covers the listed tokens
+// [first, first + piece).
+__device__ __forceinline__ int64_t rows_of(const int32_t* count, int64_t first, int64_t piece) {
+  int64_t n = int64_t(__builtin_amdgcn_readfirstlane(*count)) - first;
+  n = n < piece ? n : piece;
+  return n > 0 ? n : 0;
+}
+
+// ------------------------------------------------------------ the token list
+
+// Lists the tokens that count, in order, and clears the loss and lse of the
+// others; the largest |grad_loss| of those that count goes to *scale (1 where
+// that is 0 or not finite).  One workgroup: a pass per 1024 tokens.
+__global__ __launch_bounds__(1024) void list_tokens_kernel(const int64_t* targets, int64_t tokens, int64_t vocab,
+                                                           const float* grad_loss, int32_t* list, int32_t* count,
+                                                           float* scale, float* loss, float* lse) {
+  __shared__ int32_t wave_sum[16];
+  __shared__ uint32_t wave_top[16];
+  uint32_t top = 0;  // magnitudes compare as their bits, NaN above all
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int32_t before = 0;
+  for (int64_t t0 = 0; t0 < tokens; t0 += 1024) {
+    const int64_t t = t0 + threadIdx.x;
+    const int64_t v = t < tokens ? targets[t] : -1;
+    const bool keep = v >= 0 && v < vocab;
+    const uint64_t mask = __ballot(keep);
+    if (lane == 0) wave_sum[wave] = int32_t(__popcll(mask));
+    __syncthreads();
+    int32_t at = before, total = 0;
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) at += wave_sum[w];
+      total += wave_sum[w];
+    }
+    if (keep) {
+      list[at + int32_t(__popcll(mask & ((uint64_t(1) << lane) - 1)))] = int32_t(t);
+      if (grad_loss) {
+        const uint32_t g = __float_as_uint(grad_loss[t]) & 0x7FFFFFFFu;
+        top = top > g ? top : g;
+      }
+    } else if (t < tokens) {
+      loss[t] = 0.0f;
+      if (lse) lse[t] = 0.0f;
+    }
+    before += total;
+    __syncthreads();
+  }
+  if (grad_loss) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = uint32_t(__shfl_xor(int(top), d));
+      top = top > o ? top : o;
+    }
+    if (lane == 0) wave_top[wave] = top;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    *count = before;
+    if (grad_loss) {
+      for (int w = 0; w < 16; ++w) top = top > wave_top[w] ? top : wave_top[w];
+      *scale = top == 0 || top >= 0x7F800000u ? 1.0f : __uint_as_float(top);
+    }
+  }
+}
+
+// The listed tokens' hidden states, row after row, each filled up with zeros
+// to a pitch that is a multiple of 64.
+__global__ __launch_bounds__(256) void gather_rows_kernel(const uint16_t* hidden, int64_t ld, int64_t cols,
+                                                          const int32_t* list, const int32_t* count, uint16_t* out,
+                                                          int64_t out_ld, int32_t vec) {
+  const int64_t groups = out_ld / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t r = i / groups, c = (i - r * groups) * 8;
+  if (r >= *count) return;
+  const uint16_t* s = hidden + int64_t(list[r]) * ld + c;
+  u32x4 v;
+  if (vec && c + 8 <= cols) {
+    v = *reinterpret_cast<const u32x4*>(s);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = (c + 2 * j < cols ? uint32_t(s[2 * j]) : 0u) | (c + 2 * j + 1 < cols ? uint32_t(s[2 * j + 1]) : 0u) << 16;
+  }
+  *reinterpret_cast<u32x4*>(out + r * out_ld + c) = v;
+}
+
+// ------------------------------------------------------------ logits
+
+struct LogitsArgs {
+  Operand h, w;            // h.extent is not used: the rows of the piece are
+  const int32_t* count;    // null: every one of `tokens` rows is a token, in order
+  const int32_t* list;
+  const int64_t* targets;
+  int64_t tokens, vocab, depth;
+  int64_t first, piece;
+  float2* stats;           // [row of the piece][vocabulary tile]: maximum, sum
+  float* target_z;         // [row of the piece]
+  uint16_t* e;             // [row of the piece][e_ld], or null
+  int64_t e_ld;
+  uint32_t tiles_m, tiles_n;
+};
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
+  using G = Gemm<Form::kRows, Form::kRows, Code::kE4m3, BM, BN, WM, WN>;
+  __shared__ __align__(16) char lds0[G::kStage];
+  __shared__ __align__(16) char lds1[G::kStage];
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
+  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
+  const int64_t rows = a.count ? rows_of(a.count, a.first, a.piece) : a.tokens;
+  if (m0 >= rows) return;
+  a.h.base = static_cast<const uint16_t*>(a.h.base) + a.first * a.h.ld;
+  a.h.extent = rows;
+  G g;
+  g.run(a.h, a.w, m0, n0, 0, a.depth, lds0, lds1);
+
+  // A lane holds of row 16 i + lane % 16 the columns 16 j + 4 (lane / 16) + r.
+  // The tile row's maximum and sum go over its lanes, then over the WN waves.
+  constexpr int kFM = G::kFM, kFN = G::kFN, kRowsWave = BM / WM, kColsWave = BN / WN;
+  __syncthreads();
+  float* peak = reinterpret_cast<float*>(lds1);  // [WN][BM]
+  float* sums = peak + WN * BM;                  // [WN][BM]
+  const int lane = g.lane, col0 = g.wn * kColsWave + 4 * (lane >> 4);
+  const int row0 = g.wm * kRowsWave + (lane & 15);
+  const int64_t left = a.vocab - n0;
+#pragma unroll
+  for (int i = 0; i < kFM; ++i) {
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < kFN; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (col0 + 16 * j + r >= left) g.acc[i][j][r] = -__builtin_inff();
+        m = fmaxf(m, g.acc[i][j][r]);
+      }
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    if (lane < 16) peak[g.wn * BM + row0 + 16 * i] = m;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kFM; ++i) {
+    const int row = row0 + 16 * i;
+    float m = peak[row];
+#pragma unroll
+    for (int w = 1; w < WN; ++w) m = fmaxf(m, peak[w * BM + row]);
+    if (m == -__builtin_inff()) m = 0.0f;  // nothing but -inf: exponentials of 0
+    float s = 0.0f;
+    // the target's logit, before it becomes an exponential
+    if (m0 + row < rows) {
+      const int64_t token = a.count ? a.list[a.first + m0 + row] : m0 + row;
+      const int64_t target = a.targets[token] - n0;
+#pragma unroll
+      for (int j = 0; j < kFN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (target == col0 + 16 * j + r) a.target_z[m0 + row] = g.acc[i][j][r];
+    }
+#pragma unroll
+    for (int j = 0; j < kFN; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float x = __builtin_amdgcn_exp2f((g.acc[i][j][r] - m) * kLog2e);
+        g.acc[i][j][r] = x;
+        s += x;
+      }
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) sums[g.wn * BM + row] = s;
+  }
+  __syncthreads();
+  for (int row = g.tid; row < BM; row += G::kThreads) {
+    if (m0 + row >= rows) continue;
+    float m = peak[row], s = sums[row];
+#pragma unroll
+    for (int w = 1; w < WN; ++w) {
+      m = fmaxf(m, peak[w * BM + row]);
+      s += sums[w * BM + row];
+    }
+    a.stats[(m0 + row) * a.tiles_n + tn] = make_float2(m, s);
+  }
+  if (a.e) {
+    g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
+      if (m < rows && n < a.e_ld)
+        *reinterpret_cast<u32x2*>(a.e + m * a.e_ld + n) =
+            u32x2{half_bits(v[0] * kExpScale) | half_bits(v[1] * kExpScale) << 16,
+                  half_bits(v[2] * kExpScale) | half_bits(v[3] * kExpScale) << 16};
+    });
+  }
+}
+
+// Joins a row's tiles: one wave per row.  (m, s) stands for s exp(m).
+__global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uint32_t tiles, const int32_t* count,
+                                                        const int32_t* list, const int64_t* targets, int64_t vocab,
+                                                        int64_t tokens, int64_t first, int64_t piece,
+                                                        const float* target_z, float* row_lse, float* loss,
+                                                        float* lse) {
+  const int64_t row = int64_t(blockIdx.x) * 4 + wave_index();
+  const int64_t rows = count ? rows_of(count, first, piece) : tokens;
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 63;
+  const float2* p = stats + row * tiles;
+  float m = -__builtin_inff();
+  for (uint32_t t = lane; t < tiles; t += 64) m = fmaxf(m, p[t].x);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float base = m == -__builtin_inff() ? 0.0f : m;
+  float s = 0.0f;
+  for (uint32_t t = lane; t < tiles; t += 64) {
+    const float2 v = p[t];
+    // a tile of nothing but -inf has the sum 0 at maximum 0
+    s += v.y * (v.x == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((v.x - base) * kLog2e));
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+  if (lane == 0) {
+    const int64_t token = count ? list[first + row] : row;
+    const int64_t target = targets[token];
+    const bool keep = target >= 0 && target < vocab;
+    const float l = base + logf(s);
+    if (row_lse) row_lse[row] = l;
+    loss[token] = keep ? l - target_z[row] : 0.0f;
+    if (lse) lse[token] = keep ? l : 0.0f;
+  }
+}
+
+// ------------------------------------------------------------ gradients
+
+// The piece's exponentials (fp16) -> dz / *scale (bf16), in place; the columns from the
+// vocabulary's end to the row's pitch become 0.  A workgroup takes 2048
+// columns of a row.
+__global__ __launch_bounds__(256) void logit_grad_kernel(uint16_t* e, int64_t e_ld, int64_t vocab, const float2* stats,
+                                                         uint32_t tiles, uint32_t tile_cols, const int32_t* count,
+                                                         const int32_t* list, const int64_t* targets, int64_t first,
+                                                         int64_t piece, const float* target_z, const float* row_lse,
+                                                         const float* grad_loss, const float* scale) {
+  const int64_t row = blockIdx.y + int64_t(blockIdx.z) * 32768;
+  const int64_t rows = rows_of(count, first, piece);
+  if (row >= rows) return;
+  const int64_t c = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (c >= e_ld) return;
+  const int32_t token = list[first + row];
+  const float l = row_lse[row], g = grad_loss[token] / *scale;
+  const int64_t target = targets[token];
+  u32x4* p = reinterpret_cast<u32x4*>(e + row * e_ld + c);
+  uint32_t out[4] = {0, 0, 0, 0};
+  if (c < vocab) {
+    const u32x4 w = *p;
+    const float m = stats[row * tiles + uint32_t(c) / tile_cols].x;
+    const float f = __builtin_amdgcn_exp2f((m - l) * kLog2e) * (g * (1.0f / kExpScale));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float v = half_value(w[j >> 1] >> (16 * (j & 1))) * f;
+      if (c + j == target) v = g * expm1f(target_z[row] - l);
+      if (c + j >= vocab) v = 0.0f;
+      out[j >> 1] |= bf16_bits_of(v) << (16 * (j & 1));
+    }
+  }
+  *p = u32x4{out[0], out[1], out[2], out[3]};
+}
+
+struct HiddenGradArgs {
+  Operand dz, w;
+  const int32_t* count;
+  const float* scale;
+  const int32_t* list;
+  int64_t first, piece, hidden, vocab;
+  int64_t split_k;
+  float* partial;  // [splits][piece][hidden], or null
+  uint16_t* dhidden;
+  uint32_t tiles_m, tiles_n;
+};
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradArgs a) {
+  using G = Gemm<Form::kRows, Form::kCols, Code::kE4m3, BM, BN, WM, WN>;
+  __shared__ __align__(16) char lds0[G::kStage];
+  __shared__ __align__(16) char lds1[G::kStage];
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
+  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
+  const int64_t rows = rows_of(a.count, a.first, a.piece);
+  if (m0 >= rows) return;
+  a.dz.extent = rows;
+  const int64_t k0 = int64_t(blockIdx.y) * a.split_k;
+  const int64_t k1 = k0 + a.split_k < a.vocab ? k0 + a.split_k : a.vocab;
+  G g;
+  g.run(a.dz, a.w, m0, n0, k0, k1, lds0, lds1);
+  const float scale = *a.scale;
+  g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
+    if (m >= rows || n >= a.hidden) return;
+    const int left = int(a.hidden - n < 4 ? a.hidden - n : 4);
+    if (a.partial)
+      store_values(a.partial + int64_t(blockIdx.y) * a.piece * a.hidden, 1, 0, 1.0f, m * a.hidden + n, left, v);
+    else
+      store_values(a.dhidden, 0, 0, scale, int64_t(a.list[a.first + m]) * a.hidden + n, left, v);
+  });
+}
+
+__global__ __launch_bounds__(256) void join_hidden_kernel(const float* partial, int32_t splits, int64_t piece,
+                                                          int64_t hidden, const int32_t* count, const float* scale,
+                                                          const int32_t* list, int64_t first, uint16_t* dhidden) {
+  const int64_t groups = (hidden + 3) / 4, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t r = i / groups, c = (i - r * groups) * 4;
+  if (r >= rows_of(count, first, piece)) return;
+  const int n = hidden - c < 4 ? int(hidden - c) : 4;
+  store_values(dhidden, 0, 0, *scale, int64_t(list[first + r]) * hidden + c, n,
+               sum_splits(partial, splits, piece * hidden, r * hidden + c, n));
+}
+
+// The rows of dH whose tokens do not count.
+__global__ __launch_bounds__(256) void clear_rows_kernel(const int64_t* targets, int64_t vocab, int64_t hidden,
+                                                         int64_t tokens, uint16_t* dhidden) {
+  const int64_t t = int64_t(blockIdx.x) * 4 + wave_index();
+  if (t >= tokens) return;
+  const int64_t v = targets[t];
+  if (v >= 0 && v < vocab) return;
+  for (int64_t c = threadIdx.x & 63; c < hidden; c += 64) dhidden[t * hidden + c] = 0;
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(uint16_t* p, int64_t n) {
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 2;
+  if (i < n) p[i] = 0;
+  if (i + 1 < n) p[i + 1] = 0;
+}
+
+struct VocabGradArgs {
+  Operand dz, h;
+  const int32_t* count;
+  const float* scale;
+  int64_t first, piece, hidden, vocab;
+  const float* sum_in;  // the earlier pieces' sums, or null
+  float* sum_out;       // not the last piece: where the sums go on, or null
+  void* dw;
+  int32_t f32, accumulate;
+  uint32_t tiles_m, tiles_n;
+};
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void vocab_grad_kernel(VocabGradArgs a) {
+  using G = Gemm<Form::kCols, Form::kCols, Code::kE4m3, BM, BN, WM, WN>;
+  __shared__ __align__(16) char lds0[G::kStage];
+  __shared__ __align__(16) char lds1[G::kStage];
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
+  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
+  const int64_t rows = rows_of(a.count, a.first, a.piece);
+  a.h.base = static_cast<const uint16_t*>(a.h.base) + a.first * a.h.ld;
+  G g;
+  g.run(a.dz, a.h, m0, n0, 0, rows, lds0, lds1);
+  const float scale = *a.scale;
+  g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
+    if (m >= a.vocab || n >= a.hidden) return;
+    const int left = int(a.hidden - n < 4 ? a.hidden - n : 4);
+    const int64_t at = m * a.hidden + n;
+    if (a.sum_in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) v[i] = a.sum_in[at + i] + v[i];
+    }
+    if (a.sum_out)
+      store_values(a.sum_out, 1, 0, 1.0f, at, left, v);
+    else
+      store_values(a.dw, a.f32, a.accumulate, scale, at, left, v);
+  });
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Where one call's workspace keeps what.
+struct Layout {
+  int64_t piece = 0, pieces = 0;
+  int64_t h_ld = 0, w_ld = 0, e_ld = 0;
+  bool listed = false;  // tokens are listed and their states gathered
+  int side = 256;       // tile of the logits
+  int64_t tiles_n = 0;
+  bool big_h = false;   // dH
+  int64_t h_splits = 1, h_split_k = 0;
+  bool big_w = false;   // dW
+  bool sums = false;    // dW's sums go over the pieces in the workspace
+  // byte offsets
+  int64_t list = 0, count = 0, h = 0, w = 0, stats = 0, target_z = 0, row_lse = 0, e = 0, partial = 0, dw_sums = 0,
+          bytes = 0;
+};
+
+Layout layout_of(const VocabLossCall& c) {
+  Layout L;
+  const bool grad = c.dhidden_wanted;
+  L.h_ld = up(c.hidden, 64);
+  L.e_ld = up(c.vocab, 64);
+  // A piece's exponentials take at most 2 GiB (and at least one tile of rows);
+  // without them a piece is 32768 tokens.
+  int64_t most = grad ? (int64_t(1) << 31) / (L.e_ld * 2) / 256 * 256 : 32768;
+  if (most < 256) most = 256;
+  L.piece = c.tokens < most ? c.tokens : most;
+  L.pieces = L.piece > 0 ? (c.tokens + L.piece - 1) / L.piece : 1;
+  // One tile of rows gains nothing from leaving tokens out of a loss.
+  L.listed = grad || c.tokens > 256 || !rows_aligned(c.h, c.h_ld, c.hidden);
+  const int64_t t256 = (L.piece + 255) / 256 * ((c.vocab + 255) / 256);
+  L.side = L.piece <= 64 ? 64 : t256 >= 192 ? 256 : 128;
+  L.tiles_n = (c.vocab + L.side - 1) / L.side;
+  int64_t at = 0;
+  auto take = [&](int64_t n) {
+    const int64_t here = at;
+    at += up(n, 256);
+    return here;
+  };
+  if (L.listed) {
+    L.count = take(8);  // and the scale
+    L.list = take(c.tokens * 4);
+    L.h = take(c.tokens * L.h_ld * 2);
+  }
+  if (!rows_aligned(c.w, c.w_ld, c.hidden)) {
+    L.w_ld = L.h_ld;
+    L.w = take(c.vocab * L.w_ld * 2);
+  }
+  L.stats = take(L.piece * L.tiles_n * 8);
+  L.target_z = take(L.piece * 4);
+  if (grad) {
+    L.row_lse = take(L.piece * 4);
+    L.e = take(L.piece * L.e_ld * 2);
+    const int64_t tiles = (L.piece + 255) / 256 * ((c.hidden + 255) / 256);
+    L.big_h = tiles >= 192;
+    const int64_t side = L.big_h ? 256 : 128;
+    const int64_t mine = (L.piece + side - 1) / side * ((c.hidden + side - 1) / side);
+    const int64_t steps = (c.vocab + kBK - 1) / kBK;
+    int64_t splits = L.big_h || mine == 0 ? 1 : 512 / mine;
+    if (splits > steps / 4) splits = steps / 4;
+    if (splits < 1) splits = 1;
+    const int64_t per = (steps + splits - 1) / splits;
+    L.h_splits = (steps + per - 1) / per;
+    L.h_split_k = per * kBK;
+    if (L.h_splits > 1) L.partial = take(L.h_splits * L.piece * c.hidden * 4);
+    L.big_w = (c.vocab + 255) / 256 * ((c.hidden + 255) / 256) >= 192;
+    L.sums = L.pieces > 1 && !c.dw_f32;
+    if (L.sums) L.dw_sums = take(c.vocab * c.hidden * 4);
+  }
+  L.bytes = at;
+  return L;
+}
+
+#define TIDE_LAUNCHED()                       \
+  do {                                        \
+    const int rc_ = int(hipGetLastError());   \
+    if (rc_ != 0) return rc_;                 \
+  } while (0)
+
+}  // namespace
+
+namespace tide {
+
+int64_t vocab_loss_bytes(const VocabLossCall& c) { return c.tokens > 0 ? layout_of(c).bytes : 0; }
+
+int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
+  if (c.tokens == 0) {
+    if (!c.dhidden_wanted || c.accumulate) return 0;
+    const int64_t bytes = c.vocab * c.hidden * (c.dw_f32 ? 4 : 2);
+    hipLaunchKernelGGL(clear_kernel, dim3(unsigned((bytes / 4 + 256) / 256)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), static_cast<uint16_t*>(c.dw), bytes / 2);
+    return int(hipGetLastError());
+  }
+  const Layout L = layout_of(c);
+  char* ws = static_cast<char*>(workspace);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool grad = c.dhidden_wanted;
+  const int64_t* targets = c.targets;
+  int32_t* count = L.listed ? reinterpret_cast<int32_t*>(ws + L.count) : nullptr;
+  float* scale = L.listed ? reinterpret_cast<float*>(count + 1) : nullptr;
+  int32_t* list = L.listed ? reinterpret_cast<int32_t*>(ws + L.list) : nullptr;
+  Operand h{c.h, nullptr, c.h_ld, 0, c.tokens}, w{c.w, nullptr, c.w_ld, 0, c.vocab};
+  if (L.listed) {
+    hipLaunchKernelGGL(list_tokens_kernel, dim3(1), dim3(1024), 0, st, targets, c.tokens, c.vocab,
+                       c.grad_loss, list, count, scale, c.loss, c.lse);
+    TIDE_LAUNCHED();
+    uint16_t* rows = reinterpret_cast<uint16_t*>(ws + L.h);
+    const int64_t n = c.tokens * (L.h_ld / 8);
+    hipLaunchKernelGGL(gather_rows_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st,
+                       static_cast<const uint16_t*>(c.h), c.h_ld, c.hidden, list, count, rows, L.h_ld,
+                       int32_t(rows_aligned(c.h, c.h_ld, c.hidden)));
+    TIDE_LAUNCHED();
+    h.base = rows;
+    h.ld = L.h_ld;
+  }
+  if (!rows_aligned(c.w, c.w_ld, c.hidden)) {
+    const int rc = launch_align_rows(c.w, c.w_ld, c.vocab, c.hidden, ws + L.w, L.w_ld, stream);
+    if (rc != 0) return rc;
+    w.base = ws + L.w;
+    w.ld = L.w_ld;
+  }
+  if (grad) {
+    hipLaunchKernelGGL(clear_rows_kernel, dim3(unsigned((c.tokens + 3) / 4)), dim3(256), 0, st, targets, c.vocab,
+                       c.hidden, c.tokens, static_cast<uint16_t*>(c.dhidden));
+    TIDE_LAUNCHED();
+  }
+  float2* stats = reinterpret_cast<float2*>(ws + L.stats);
+  float* target_z = reinterpret_cast<float*>(ws + L.target_z);
+  float* row_lse = grad ? reinterpret_cast<float*>(ws + L.row_lse) : nullptr;
+  uint16_t* e = grad ? reinterpret_cast<uint16_t*>(ws + L.e) : nullptr;
+  for (int64_t p = 0; p < L.pieces; ++p) {
+    const int64_t first = p * L.piece;
+    LogitsArgs a;
+    a.h = h;
+    a.w = w;
+    a.count = count;
+    a.list = list;
+    a.targets = targets;
+    a.tokens = c.tokens;
+    a.vocab = c.vocab;
+    a.depth = c.hidden;
+    a.first = first;
+    a.piece = L.piece;
+    a.stats = stats;
+    a.target_z = target_z;
+    a.e = e;
+    a.e_ld = L.e_ld;
+    a.tiles_m = uint32_t((L.piece + L.side - 1) / L.side);
+    a.tiles_n = uint32_t(L.tiles_n);
+    const dim3 grid(a.tiles_m * a.tiles_n);
+    if (L.side == 256)
+      hipLaunchKernelGGL((logits_kernel<256, 256, 2, 4>), grid, dim3(512), 0, st, a);
+    else if (L.side == 128)
+      hipLaunchKernelGGL((logits_kernel<128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((logits_kernel<64, 64, 1, 4>), grid, dim3(256), 0, st, a);
+    TIDE_LAUNCHED();
+    hipLaunchKernelGGL(join_rows_kernel, dim3(unsigned((L.piece + 3) / 4)), dim3(256), 0, st, stats, a.tiles_n, count,
+                       list, targets, c.vocab, c.tokens, first, L.piece, target_z, row_lse, c.loss, c.lse);
+    TIDE_LAUNCHED();
+    if (!grad) continue;
+    const int64_t rows_z = L.piece < 32768 ? L.piece : 32768;
+    hipLaunchKernelGGL(logit_grad_kernel,
+                       dim3(unsigned((L.e_ld + 2047) / 2048), unsigned(rows_z), unsigned((L.piece + 32767) / 32768)),
+                       dim3(256), 0, st, e, L.e_ld, c.vocab, stats, a.tiles_n, uint32_t(L.side), count, list, targets,
+                       first, L.piece, target_z, row_lse, c.grad_loss, scale);
+    TIDE_LAUNCHED();
+    HiddenGradArgs d;
+    d.dz = Operand{e, nullptr, L.e_ld, 0, L.piece};
+    d.w = w;
+    d.w.extent = c.hidden;
+    d.count = count;
+    d.scale = scale;
+    d.list = list;
+    d.first = first;
+    d.piece = L.piece;
+    d.hidden = c.hidden;
+    d.vocab = c.vocab;
+    d.split_k = L.h_split_k;
+    d.partial = L.h_splits > 1 ? reinterpret_cast<float*>(ws + L.partial) : nullptr;
+    d.dhidden = static_cast<uint16_t*>(c.dhidden);
+    const int64_t side_h = L.big_h ? 256 : 128;
+    d.tiles_m = uint32_t((L.piece + side_h - 1) / side_h);
+    d.tiles_n = uint32_t((c.hidden + side_h - 1) / side_h);
+    const dim3 grid_h(d.tiles_m * d.tiles_n, unsigned(L.h_splits));
+    if (L.big_h)
+      hipLaunchKernelGGL((hidden_grad_kernel<256, 256, 2, 4>), grid_h, dim3(512), 0, st, d);
+    else
+      hipLaunchKernelGGL((hidden_grad_kernel<128, 128, 2, 2>), grid_h, dim3(256), 0, st, d);
+    TIDE_LAUNCHED();
+    if (L.h_splits > 1) {
+      const int64_t n = L.piece * ((c.hidden + 3) / 4);
+      hipLaunchKernelGGL(join_hidden_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st, d.partial,
+                         int32_t(L.h_splits), L.piece, c.hidden, count, scale, list, first, d.dhidden);
+      TIDE_LAUNCHED();
+    }
+    VocabGradArgs v;
+    v.dz = Operand{e, nullptr, L.e_ld, 0, c.vocab};
+    v.h = h;
+    v.h.extent = c.hidden;
+    v.count = count;
+    v.scale = scale;
+    v.first = first;
+    v.piece = L.piece;
+    v.hidden = c.hidden;
+    v.vocab = c.vocab;
+    float* sums = L.sums ? reinterpret_cast<float*>(ws + L.dw_sums) : nullptr;
+    v.sum_in = p > 0 ? sums : nullptr;
+    v.sum_out = p + 1 < L.pieces ? sums : nullptr;
+    v.dw = c.dw;
+    v.f32 = c.dw_f32;
+    v.accumulate = c.accumulate || (p > 0 && !L.sums);
+    const int64_t side_w = L.big_w ? 256 : 128;
+    v.tiles_m = uint32_t((c.vocab + side_w - 1) / side_w);
+    v.tiles_n = uint32_t((c.hidden + side_w - 1) / side_w);
+    const dim3 grid_w(v.tiles_m * v.tiles_n);
+    if (L.big_w)
+      hipLaunchKernelGGL((vocab_grad_kernel<256, 256, 2, 4>), grid_w, dim3(512), 0, st, v);
+    else
+      hipLaunchKernelGGL((vocab_grad_kernel<128, 128, 2, 2>), grid_w, dim3(256), 0, st, v);
+    TIDE_LAUNCHED();
+  }
+  return 0;
+}
+
+}  // namespace tide

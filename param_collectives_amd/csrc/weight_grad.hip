@@ -20,58 +20,6 @@ struct WeightGradArgs {
   uint32_t tiles_m, tiles_n;
 };
 
-__device__ __forceinline__ uint32_t bf16_bits_of(float v) {
-  const __bf16 b = __bf16(v);  // round to nearest even
-  uint16_t r;
-  __builtin_memcpy(&r, &b, 2);
-  return r;
-}
-
-// alpha s (+ old) for the `n` values v of one row from element `at`, rounded
-// once to the gradient's type.
-__device__ __forceinline__ void store_grad(void* dw, int32_t f32, int32_t accumulate, float alpha, int64_t at, int n,
-                                           f32x4v v) {
-  if (f32) {
-    float* d = static_cast<float*>(dw) + at;
-    if (n == 4 && (reinterpret_cast<uintptr_t>(d) & 15) == 0) {
-      f32x4v r;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = alpha * v[i];
-      if (accumulate) {
-        const f32x4v old = *reinterpret_cast<const f32x4v*>(d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = old[i] + r[i];
-      }
-      *reinterpret_cast<f32x4v*>(d) = r;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) d[i] = accumulate ? d[i] + alpha * v[i] : alpha * v[i];
-    }
-  } else {
-    uint16_t* d = static_cast<uint16_t*>(dw) + at;
-    if (n == 4 && (reinterpret_cast<uintptr_t>(d) & 7) == 0) {
-      float r[4];
-      u32x2 old = u32x2{0, 0};
-      if (accumulate) old = *reinterpret_cast<const u32x2*>(d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float o = __uint_as_float(i & 1 ? old[i >> 1] & 0xFFFF0000u : old[i >> 1] << 16);
-        r[i] = accumulate ? o + alpha * v[i] : alpha * v[i];
-      }
-      *reinterpret_cast<u32x2*>(d) =
-          u32x2{bf16_bits_of(r[0]) | bf16_bits_of(r[1]) << 16, bf16_bits_of(r[2]) | bf16_bits_of(r[3]) << 16};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) {
-          const float r = alpha * v[i];
-          d[i] = uint16_t(bf16_bits_of(accumulate ? __uint_as_float(uint32_t(d[i]) << 16) + r : r));
-        }
-    }
-  }
-}
-
 template <Code CODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void weight_grad_kernel(WeightGradArgs a) {
   using G = Gemm<Form::kCols, Form::kPacked, CODE, BM, BN, WM, WN>;
@@ -87,12 +35,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void weight_grad_kernel(WeightGradA
   if (a.partial) {
     float* p = a.partial + int64_t(blockIdx.y) * a.outs * a.ins;
     g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
-      if (m < a.outs && n < a.ins) store_grad(p, 1, 0, 1.0f, m * a.ins + n, int(a.ins - n < 4 ? a.ins - n : 4), v);
+      if (m < a.outs && n < a.ins) store_values(p, 1, 0, 1.0f, m * a.ins + n, int(a.ins - n < 4 ? a.ins - n : 4), v);
     });
   } else {
     g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
       if (m < a.outs && n < a.ins)
-        store_grad(a.dw, a.f32, a.accumulate, a.alpha, m * a.ins + n, int(a.ins - n < 4 ? a.ins - n : 4), v);
+        store_values(a.dw, a.f32, a.accumulate, a.alpha, m * a.ins + n, int(a.ins - n < 4 ? a.ins - n : 4), v);
     });
   }
 }
@@ -103,20 +51,7 @@ __global__ __launch_bounds__(256) void join_splits_kernel(const float* partial, 
   const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (i >= elems) return;
   const int n = elems - i < 4 ? int(elems - i) : 4;
-  f32x4v s = f32x4v{0.f, 0.f, 0.f, 0.f};
-  for (int32_t k = 0; k < splits; ++k) {
-    const float* p = partial + int64_t(k) * elems + i;
-    if (n == 4 && (elems & 3) == 0) {
-      const f32x4v v = *reinterpret_cast<const f32x4v*>(p);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] += v[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < n) s[j] += p[j];
-    }
-  }
-  store_grad(dw, f32, accumulate, alpha, i, n, s);
+  store_values(dw, f32, accumulate, alpha, i, n, sum_splits(partial, splits, elems, i, n));
 }
 
 // Rows of any pitch and alignment -> rows of pitch `ld` (a multiple of 8)
@@ -138,7 +73,9 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t* src, in
 
 namespace tide {
 
-bool rows_aligned(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
+bool rows_aligned(const void* p, int64_t ld, int64_t cols) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && cols % 8 == 0;
+}
 
 int launch_align_rows(const void* src, int64_t src_ld, int64_t rows, int64_t cols, void* dst, int64_t ld,
                       void* stream) {
@@ -174,7 +111,7 @@ WeightGradPlan plan_weight_grad(int64_t tokens, int64_t outs, int64_t ins, bool 
 }
 
 int launch_weight_grad(const WeightGradCall& c, void* workspace, void* stream) {
-  const bool aligned = rows_aligned(c.dy, c.dy_ld);
+  const bool aligned = rows_aligned(c.dy, c.dy_ld, c.outs);
   const WeightGradPlan p = plan_weight_grad(c.tokens, c.outs, c.ins, aligned);
   char* ws = static_cast<char*>(workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);

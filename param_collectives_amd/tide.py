@@ -62,6 +62,9 @@ EXPORTS = (
     "tide_checkpoint_unpack",
     "tide_checkpoint_weight_grad_workspace",
     "tide_checkpoint_weight_grad",
+    "tide_vocab_loss_workspace",
+    "tide_vocab_loss",
+    "tide_vocab_loss_grad",
     "tide_device_info",
     "tide_probe_launch",
     "tide_victim_axpb",
@@ -110,6 +113,9 @@ def _load():
     lib.tide_checkpoint_unpack.argtypes = [vp, vp, i32, i64, i64, vp, i32, i64, vp]
     lib.tide_checkpoint_weight_grad_workspace.argtypes = [vp, i64, i64, i64, i64, i64p]
     lib.tide_checkpoint_weight_grad.argtypes = [vp, i64, i64, i64, vp, vp, i32, i64, vp, i32, f32, i32, vp, i64, vp]
+    lib.tide_vocab_loss_workspace.argtypes = [vp, i64, vp, i64, i64, i64, i64, i32, i32, i64p]
+    lib.tide_vocab_loss.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp, i64, vp]
+    lib.tide_vocab_loss_grad.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, i64, vp]
     i32p = ctypes.POINTER(i32)
     lib.tide_device_info.argtypes = [i32p, i32p, i32p, i32p]
     lib.tide_probe_launch.argtypes = [vp, i32, i32, i64, vp]
@@ -606,6 +612,99 @@ def checkpoint_weight_grad(dy, codes, scales, dw, alpha=1.0, accumulate=False, w
     at least checkpoint_weight_grad_workspace bytes; without one the call takes
     its own (tide_checkpoint_weight_grad)."""
     _weight_grad(dy, codes, scales, dw, alpha, accumulate, workspace, stream)(stream)
+
+
+# ------------------------------------------------------------ vocabulary loss
+
+
+def _vector(t, dtype, n, what):
+    _require(t, dtype, n, what)
+    return ctypes.c_void_p(t.data_ptr() or None)
+
+
+def _projection(hidden, weight):
+    """(the operands' arguments, tokens, hidden size, vocabulary)."""
+    import torch
+
+    h, _, tokens, size, h_stride = _matrix(hidden, (torch.bfloat16,), "hidden")
+    w, _, vocab, w_size, w_stride = _matrix(weight, (torch.bfloat16,), "weight")
+    if w_size != size:
+        raise ValueError(f"weight has {w_size} columns, hidden {size}")
+    return (h, h_stride, w, w_stride), tokens, size, vocab
+
+
+def _vocab_loss_bytes(operands, tokens, size, vocab, gradients, dtype):
+    need = ctypes.c_int64()
+    _check(lib.tide_vocab_loss_workspace(*operands, tokens, size, vocab, gradients, dtype, ctypes.byref(need)))
+    return need.value
+
+
+def vocab_loss_workspace(hidden, weight, dweight=None):
+    """Bytes of workspace of vocab_loss, or of vocab_loss_grad where its
+    dweight is given (tide_vocab_loss_workspace)."""
+    operands, tokens, size, vocab = _projection(hidden, weight)
+    dtype = DTYPE_F32 if dweight is None else _matrix(dweight, _floats(), "dweight", strided=False)[1]
+    return _vocab_loss_bytes(operands, tokens, size, vocab, int(dweight is not None), dtype)
+
+
+def _vocab_loss(hidden, weight, targets, loss, lse, workspace, stream):
+    import torch
+
+    operands, tokens, size, vocab = _projection(hidden, weight)
+    t = _vector(targets, torch.int64, tokens, "targets")
+    out = _vector(loss, torch.float32, tokens, "loss"), None if lse is None else _vector(lse, torch.float32, tokens, "lse")
+    ws = _workspace(_vocab_loss_bytes(operands, tokens, size, vocab, 0, DTYPE_F32), workspace, stream)
+    return Call(lib.tide_vocab_loss, (*operands, t, tokens, size, vocab, *out, *_workspace_args(ws)),
+                (hidden, weight, targets, loss, lse, ws))
+
+
+def vocab_loss_call(hidden, weight, targets, loss, lse=None, workspace=None):
+    """A registered vocabulary loss (see vocab_loss); it keeps one workspace,
+    so its calls must not overlap."""
+    return _vocab_loss(hidden, weight, targets, loss, lse, workspace, None)
+
+
+def vocab_loss(hidden, weight, targets, loss, lse=None, workspace=None, stream=None):
+    """Cross entropy of the projection hidden @ weight.T (both bf16, contiguous
+    rows) against targets (int64): loss[t] and, if given, the log-sum-exp
+    lse[t], fp32 per token.  A target outside the vocabulary leaves its token
+    out, with 0s.  `workspace` as for checkpoint_weight_grad (tide_vocab_loss)."""
+    _vocab_loss(hidden, weight, targets, loss, lse, workspace, stream)(stream)
+
+
+def _vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate, workspace, stream):
+    import torch
+
+    operands, tokens, size, vocab = _projection(hidden, weight)
+    t = _vector(targets, torch.int64, tokens, "targets")
+    g = _vector(grad_loss, torch.float32, tokens, "grad_loss")
+    out = _vector(loss, torch.float32, tokens, "loss"), None if lse is None else _vector(lse, torch.float32, tokens, "lse")
+    dh, _, *dh_shape, _ = _matrix(dhidden, (torch.bfloat16,), "dhidden", strided=False)
+    dw, dt, *dw_shape, _ = _matrix(dweight, _floats(), "dweight", strided=False)
+    if dh_shape != [tokens, size] or dw_shape != [vocab, size]:
+        raise ValueError(f"dhidden and dweight must be {tokens} x {size} and {vocab} x {size}, got {dh_shape} and "
+                         f"{dw_shape}")
+    ws = _workspace(_vocab_loss_bytes(operands, tokens, size, vocab, 1, dt), workspace, stream)
+    return Call(lib.tide_vocab_loss_grad,
+                (*operands, t, g, tokens, size, vocab, *out, dh, dw, dt, int(bool(accumulate)), *_workspace_args(ws)),
+                (hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, ws))
+
+
+def vocab_loss_grad_call(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate=False,
+                         workspace=None):
+    """A registered vocabulary loss with gradients (see vocab_loss_grad); it
+    keeps one workspace, so its calls must not overlap."""
+    return _vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate, workspace,
+                            None)
+
+
+def vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate=False, workspace=None,
+                    stream=None):
+    """vocab_loss with the gradients of sum_t grad_loss[t] * loss[t]: dhidden
+    (bf16) and dweight (bf16 or fp32; added to the old one when accumulate is
+    true).  lse may be None (tide_vocab_loss_grad)."""
+    _vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate, workspace,
+                     stream)(stream)
 
 
 # ------------------------------------------------------------ instruments

@@ -67,3 +67,61 @@ def weight_grad(dy, x, alpha=1.0, old=None):
     r = alpha * s + (0.0 if old is None else old)
     err = abs(alpha) * (dy.shape[0] + 64) * 2.0**-23 * mag + 2.0**-23 * (np.abs(alpha * s) + np.abs(r))
     return r, err
+
+
+def vocab_loss(h, w, targets, grad_loss=None):
+    """The loss of float64 h and w and, with grad_loss, its gradients, each
+    with a bound of the kernels' error before the result is rounded to its own
+    type, as a dict of (value, bound) pairs.
+
+    A logit is a sum of d exact products, each addition off by at most 2^-23 of
+    the magnitudes (a truncating adder).  An exponential's argument z - m is
+    rounded three times (the difference, the constant log2(e), the product) and
+    the exponential itself by 2^-23; a tile's exponentials meet at most 128
+    additions of 2^-24 on their way to the row's sum, and a second exponential
+    joins the tile.  r is the row's range of logits.  dz's entries are
+    additionally rounded to fp16 times 2^15 (2^-11 relative, or 2^-40 of the
+    tile's largest) and once to bf16 (2^-8); the target's from expm1 instead."""
+    tokens, vocab = h.shape[0], w.shape[0]
+    keep = (targets >= 0) & (targets < vocab)
+    at = np.where(keep, targets, 0)
+    rows = np.arange(tokens)
+    h = np.where(keep[:, None], h, 0.0)
+    z = h @ w.T
+    ez = (h.shape[1] + 8) * 2.0**-23 * (np.abs(h) @ np.abs(w).T)
+    m = z.max(-1)
+    r = m - z.min(-1)
+    lse = m + np.log(np.exp(z - m[:, None]).sum(-1))
+    e_exp = 8 * 2.0**-24 * r + 2 * 2.0**-23
+    e_lse = ez.max(-1) + e_exp + 128 * 2.0**-24 + 4 * 2.0**-24 * (np.abs(lse) + np.abs(m))
+    zt = z[rows, at]
+    loss = lse - zt
+    e_loss = e_lse + ez[rows, at] + 2.0**-24 * np.abs(loss)
+    out = {"loss": (np.where(keep, loss, 0.0), np.where(keep, e_loss, 0.0)),
+           "lse": (np.where(keep, lse, 0.0), np.where(keep, e_lse, 0.0))}
+    if grad_loss is None:
+        return out
+    g = np.where(keep, grad_loss, 0.0)[:, None]
+    p = np.exp(z - lse[:, None])
+    dz = p.copy()
+    dz[rows, at] = np.expm1(zt - lse)
+    # relative error of p from its exponent, and what the roundings add
+    rel = ez + (e_lse + 2 * e_exp)[:, None] + 8 * 2.0**-24
+    edz = p * (rel + 2.0**-11) + 2.0**-39
+    edz[rows, at] = p[rows, at] * rel[rows, at] + 8 * 2.0**-24 * np.abs(dz[rows, at])
+    arith, edz = edz * np.abs(g), edz + 2.0**-8 * (np.abs(dz) + edz)
+    dz, edz = dz * g, edz * np.abs(g) + 2.0**-130
+    adz, half = np.abs(dz) + edz, 2.0**-8
+    for name, a, e, s, b, f in (("dhidden", dz, edz, adz, w, arith), ("dweight", dz.T, edz.T, adz.T, h, arith.T)):
+        value = a @ b
+        sums = (a.shape[1] + 64) * 2.0**-23 * (s @ np.abs(b))
+        bound = e @ np.abs(b) + sums
+        # Root mean square of the error with the roundings of dz and of the
+        # bf16 result taken as independent and uniform in their half steps, 1.5
+        # times, and to it the bound of everything else.  (That part is not
+        # small everywhere: a token whose loss is 7e-6, the difference of an
+        # lse and a logit near 13, has a gradient of relative error 2^-24 * 13 /
+        # 7e-6 = 11% from the rounding of either to fp32.)
+        rms = 1.5 * np.sqrt(((half**2 / 3) * ((a**2) @ (b**2) + value**2)).sum())
+        out[name] = (value, bound, rms + np.sqrt(((f @ np.abs(b) + sums) ** 2).sum()))
+    return out

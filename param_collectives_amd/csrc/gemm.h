@@ -12,10 +12,10 @@
 // Tiles go to LDS, kRows and kCols ones by loads that write LDS directly (16
 // bytes a lane).  Those loads fill LDS in lane order, so the bank swizzle is
 // made by choosing which 16 bytes a lane fetches:
-//   kRows tile [rows][64 k], 8 chunks of 16 bytes a row: chunk c of row r is
-//     kept at slot c ^ (r & 7), and the 16-byte fragment reads of 8
+//   kRows tile [rows][32 k], 4 chunks of 16 bytes a row: chunk c of row r is
+//     kept at c ^ (r / 4 & 3), and the 16-byte fragment reads of 16
 //     consecutive rows touch all 64 banks once;
-//   kCols, kPacked tile [64 k][rows]: chunk c of row k is kept at
+//   kCols, kPacked tile [32 k][rows]: chunk c of row k is kept at
 //     c ^ 2 f(k), f(k) made of bits 0, 1 and 3 of k; a fragment is read by the
 //     transposing LDS read, whose 32 lanes touch 8 rows k of 32 bytes each.
 // The products take the n side first, so a lane holds 4 consecutive n of one m.
@@ -41,7 +41,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 enum class Form { kRows, kCols, kPacked };
 enum class Code { kE4m3, kInt8 };
 
-constexpr int kBK = 64;  // k per staged step
+constexpr int kBK = 32;     // k per staged step
+constexpr int kStages = 4;  // LDS stages a tile's steps go round
 
 struct Operand {
   const void* base;       // bf16 values, or codes (kPacked); 16-byte aligned
@@ -54,13 +55,34 @@ struct Operand {
 // 8 zero values for the lanes whose k lies past the end.
 static __device__ __align__(16) const uint32_t g_zero16[4] = {0, 0, 0, 0};
 
+// 16 bytes a lane from its own address to LDS, in lane order.
 __device__ __forceinline__ void load_to_lds(const void* g, void* lds) {
   __builtin_amdgcn_global_load_lds((const TIDE_GLOBAL void*)g, (TIDE_LDS void*)lds, 16, 0, 0);
 }
 
-// Every load to LDS or registers of this wave has arrived (vmcnt(0) on gfx9;
-// expcnt and lgkmcnt are left at their maxima).
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// The same from a shared base and the lane's offset.  (A buffer load: the
+// compiler takes the global load above for an access to LDS as well, and then
+// waits for all of a wave's LDS reads where it could wait for the oldest.)
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, void* lds) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (TIDE_LDS void*)lds, 16, int(offset), 0, 0, 0);
+}
+
+// Waits until at most N of this wave's loads (to LDS or registers) are still
+// on their way and, with LGKM, until its LDS accesses are done.
+template <int N, bool LGKM>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 16, "the counter's low bits");
+  __builtin_amdgcn_s_waitcnt((LGKM ? 0x0070 : 0x0F70) | N);
+}
+
+// A barrier that waits for nothing but the other waves: what must have arrived
+// before it is waited for by wait_loads.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // The same for every lane: keeps a base address in scalar registers, apart
 // from the lanes' offsets (the loads take both).
@@ -120,21 +142,31 @@ __device__ __forceinline__ u32x2 widen4(uint32_t w, uint32_t scale_byte) {
 // wave's, THREADS threads.
 template <Form FORM, Code CODE, int ROWS, int FRAGS, int THREADS>
 struct Side {
+  static constexpr bool kPacked = FORM == Form::kPacked;
   static constexpr int kBytes = ROWS * kBK * 2;
-  static constexpr int kLoads = kBytes / 16 / THREADS;  // 16-byte loads of a thread per step
-  static constexpr int kRowChunks = FORM == Form::kRows ? 8 : ROWS / 8;
-  static constexpr int kUnits = ROWS / 16;                // kPacked: 16-code units of a row
-  static constexpr int kPasses = kBK * kUnits / THREADS;  // kPacked: units of a thread per step
+  static constexpr int kRowChunks = FORM == Form::kRows ? kBK / 8 : ROWS / 8;
+  // What a thread moves per step: 16-byte loads to LDS, or units of 16 codes.
+  static constexpr int kParts = kPacked ? kBK * (ROWS / 16) / THREADS : kBytes / 16 / THREADS;
+  static constexpr int kLoads = kPacked ? 2 * kParts : kParts;  // a unit's codes and its exponent byte
+  static_assert(kParts >= 1, "tile too small for its threads");
 
   const char* base;        // of the tile's first row (kRows) or column, k = 0
   const uint8_t* scales;
-  int64_t step;            // bytes from one step of 64 k to the next
+  int64_t step;            // bytes from one step of k to the next
   int64_t scale_step;
-  uint32_t off[FORM == Form::kPacked ? kPasses : kLoads];  // byte offset of each load at its step's base
-  uint32_t scale_off[FORM == Form::kPacked ? kPasses : 1];
-  u32x4 held[FORM == Form::kPacked ? kPasses : 1];  // kPacked: codes on their way to LDS
-  uint32_t held_scale[FORM == Form::kPacked ? kPasses : 1];
-  uint32_t put[FORM == Form::kPacked ? kPasses : 1];  // where each unit goes in the tile
+  uint32_t off[kParts];    // byte offset of each part at its step's base
+  uint32_t scale_off[kPacked ? kParts : 1];
+  uint32_t put[kPacked ? kParts : 1];  // where each unit goes in the tile
+
+  // kPacked: codes on their way to LDS
+  struct Held {
+    u32x4 codes[kPacked ? kParts : 1];
+    uint32_t scale[kPacked ? kParts : 1];
+  };
+
+  static __device__ __forceinline__ int part_k(int lin) {
+    return FORM == Form::kRows ? ((lin & 3) ^ ((lin >> 4) & 3)) * 8 : lin / (kPacked ? ROWS / 16 : kRowChunks);
+  }
 
   __device__ __forceinline__ void init(const Operand& o, int64_t first, int tid) {
     // rows (columns) past the end read the last one: their results are dropped
@@ -143,17 +175,17 @@ struct Side {
       base = static_cast<const char*>(o.base) + first * o.ld * 2;
       step = kBK * 2;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int lin = i * THREADS + tid, r = lin >> 3, c = (lin & 7) ^ (r & 7);
+      for (int i = 0; i < kParts; ++i) {
+        const int lin = i * THREADS + tid, r = lin >> 2;
         const int rr = r <= last ? r : int(last);
-        off[i] = uint32_t(rr) * uint32_t(o.ld * 2) + uint32_t(c * 16);
+        off[i] = uint32_t(rr) * uint32_t(o.ld * 2) + uint32_t(part_k(lin) * 2);
       }
     } else if constexpr (FORM == Form::kCols) {
       base = static_cast<const char*>(o.base) + first * 2;
       step = o.ld * (kBK * 2);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int lin = i * THREADS + tid, k = lin / kRowChunks, c = (lin % kRowChunks) ^ col_swizzle(k);
+      for (int i = 0; i < kParts; ++i) {
+        const int lin = i * THREADS + tid, k = part_k(lin), c = (lin % kRowChunks) ^ col_swizzle(k);
         off[i] = uint32_t(k) * uint32_t(o.ld * 2) + (c * 8 <= last ? uint32_t(c * 16) : 0u);
       }
     } else {
@@ -162,8 +194,8 @@ struct Side {
       step = o.ld * kBK;
       scale_step = o.scale_ld * kBK;
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int lin = i * THREADS + tid, k = lin / kUnits, u = lin % kUnits;
+      for (int i = 0; i < kParts; ++i) {
+        const int lin = i * THREADS + tid, k = part_k(lin), u = lin % (ROWS / 16);
         const bool in = u * 16 <= last;
         off[i] = uint32_t(k) * uint32_t(o.ld) + (in ? uint32_t(u * 16) : 0u);
         scale_off[i] = uint32_t(k) * uint32_t(o.scale_ld) + (in ? uint32_t(u >> 1) : 0u);
@@ -172,51 +204,48 @@ struct Side {
     }
   }
 
-  // Start the loads of step s into `lds` (kPacked: into registers).  TAIL:
-  // only `left` < 64 values of k remain, the rest is staged as zeros (k
-  // counts in eights on a kRows side, whose rows are zero from there to the
-  // next multiple of 8).
+  // Start the loads of step s into `lds` (kPacked: into `held`).  TAIL: only
+  // `left` < 32 values of k remain (none, for an empty step), the rest is
+  // staged as zeros (k counts in eights on a kRows side, whose rows are zero
+  // from there to the next multiple of 8).
   template <bool TAIL>
-  __device__ __forceinline__ void fetch(char* lds, int64_t s, int left, int tid) {
+  __device__ __forceinline__ void fetch(char* lds, Held& held, int64_t s, int left, int tid) {
     const char* at = uniform(base + s * step);
-    if constexpr (FORM == Form::kPacked) {
+    if constexpr (kPacked) {
       const uint8_t* sc = uniform(scales + s * scale_step);
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int k = (i * THREADS + tid) / kUnits;
-        if (!TAIL || k < left) {
-          held[i] = *(const TIDE_GLOBAL u32x4*)(at + renew(off[i]));
-          held_scale[i] = *(const TIDE_GLOBAL uint8_t*)(sc + renew(scale_off[i]));
+      for (int i = 0; i < kParts; ++i) {
+        if (!TAIL || part_k(i * THREADS + tid) < left) {
+          held.codes[i] = *(const TIDE_GLOBAL u32x4*)(at + renew(off[i]));
+          held.scale[i] = *(const TIDE_GLOBAL uint8_t*)(sc + renew(scale_off[i]));
         } else {
-          held[i] = u32x4{0, 0, 0, 0};
-          held_scale[i] = 127;
+          held.codes[i] = u32x4{0, 0, 0, 0};
+          held.scale[i] = 127;
         }
       }
     } else {
       const int wave_base = wave_index() * 64;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const char* src = at + renew(off[i]);
-        if constexpr (TAIL) {
-          const int lin = i * THREADS + tid;
-          const int k = FORM == Form::kRows ? ((lin & 7) ^ ((lin >> 3) & 7)) * 8 : lin / kRowChunks;
-          if (k >= left) src = reinterpret_cast<const char*>(g_zero16);
-        }
-        load_to_lds(src, lds + (i * THREADS + wave_base) * 16);
+      for (int i = 0; i < kParts; ++i) {
+        char* to = lds + (i * THREADS + wave_base) * 16;
+        if constexpr (TAIL)
+          load_to_lds(part_k(i * THREADS + tid) < left ? at + off[i] : reinterpret_cast<const char*>(g_zero16), to);
+        else
+          load_to_lds(at, off[i], to);
       }
     }
   }
 
   // kPacked: widen what fetch() loaded and write it to LDS.
-  __device__ __forceinline__ void settle(char* lds, int tid) {
-    if constexpr (FORM == Form::kPacked) {
+  __device__ __forceinline__ void settle(char* lds, const Held& held) {
+    if constexpr (kPacked) {
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
+      for (int i = 0; i < kParts; ++i) {
         char* to = lds + renew(put[i]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32x2 lo = widen4<CODE>(held[i][2 * h], held_scale[i]);
-          const u32x2 hi = widen4<CODE>(held[i][2 * h + 1], held_scale[i]);
+          const u32x2 lo = widen4<CODE>(held.codes[i][2 * h], held.scale[i]);
+          const u32x2 hi = widen4<CODE>(held.codes[i][2 * h + 1], held.scale[i]);
           *reinterpret_cast<u32x4*>(to + 16 * h) = u32x4{lo.x, lo.y, hi.x, hi.y};
         }
       }
@@ -225,12 +254,11 @@ struct Side {
 
   // Where this lane's fragments of a wave's FRAGS x 16 rows (columns) from r0
   // (a multiple of 16 FRAGS) start in the tile.
-  static constexpr int kSpots = FORM == Form::kRows ? 2 : FRAGS;
+  static constexpr int kSpots = FORM == Form::kRows ? 1 : FRAGS;
   static __device__ __forceinline__ void spots(uint32_t* at, int r0, int lane) {
     if constexpr (FORM == Form::kRows) {
       const int r = r0 + (lane & 15);
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) at[kk] = uint32_t((r * 8 + ((4 * kk + (lane >> 4)) ^ (r & 7))) * 16);
+      at[0] = uint32_t((r * kRowChunks + ((lane >> 4) ^ ((r >> 2) & 3))) * 16);
     } else {
       // a transposing read gives lane l of 16 the values of column l in the
       // four rows k of which lanes 4j .. 4j+3 point at 4 columns each
@@ -243,13 +271,12 @@ struct Side {
     }
   }
 
-  // Fragment i: rows (columns) 16 i + 0..15, k = 32 kk + 8 (lane / 16) + 0..7.
-  static __device__ __forceinline__ bf16x8 fragment(const char* lds, uint32_t* at, int i, int kk) {
+  // Fragment i: rows (columns) 16 i + 0..15, k = 8 (lane / 16) + 0..7.
+  static __device__ __forceinline__ bf16x8 fragment(const char* lds, uint32_t* at, int i) {
     if constexpr (FORM == Form::kRows) {
-      return *reinterpret_cast<const bf16x8*>(lds + renew(at[kk]) + i * 2048);
+      return *reinterpret_cast<const bf16x8*>(lds + renew(at[0]) + i * 16 * kRowChunks * 16);
     } else {
-      // rows k, k + 4 and k + 32 share their swizzle
-      const char* p = lds + renew(at[i]) + kk * 32 * kRowChunks * 16;
+      const char* p = lds + renew(at[i]);  // rows k and k + 4 share their swizzle
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * kRowChunks * 16));
       bf16x8 r;
@@ -267,32 +294,25 @@ struct Gemm {
   static constexpr int kFM = BM / WM / 16, kFN = BN / WN / 16;  // fragments of a wave
   using SA = Side<FA, CODE, BM, kFM, kThreads>;
   using SB = Side<FB, CODE, BN, kFN, kThreads>;
+  static constexpr bool kPacked = SA::kPacked || SB::kPacked;
   static constexpr int kStage = SA::kBytes + SB::kBytes;
-  static constexpr int kLds = 2 * kStage;
 
   f32x4v acc[kFM][kFN];
   int tid, lane, wm, wn;
-  uint32_t at_a[SA::kSpots], at_b[SB::kSpots];
 
-  __device__ __forceinline__ void multiply(const char* la, const char* lb) {
-#pragma unroll
-    for (int kk = 0; kk < kBK / 32; ++kk) {
-      bf16x8 b[kFN];
-#pragma unroll
-      for (int j = 0; j < kFN; ++j) b[j] = SB::fragment(lb, at_b, j, kk);
-#pragma unroll
-      for (int i = 0; i < kFM; ++i) {
-        const bf16x8 a = SA::fragment(la, at_a, i, kk);
-#pragma unroll
-        for (int j = 0; j < kFN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a, acc[i][j], 0, 0, 0);
-      }
-    }
-  }
-
-  // Sums k over [k_first, k_end) (k_first a multiple of 64) into acc.  `lds0`
-  // and `lds1` hold kStage bytes each.
+  // Sums k over [k_first, k_end) (k_first a multiple of 32) into acc; the
+  // stages hold kStage bytes each.
+  //
+  // Step i's tiles lie in stage i mod 4.  While a wave multiplies step i it
+  // starts the loads of step i + 3 and reads the first fragments of step i + 1,
+  // so that one barrier a step is enough and no product waits behind it: past
+  // it, step i + 1 has arrived for all waves, and all are done with the stage
+  // that step i + 3 goes to.  (Packed codes are loaded 4 steps ahead into
+  // registers and written to LDS 2 steps ahead.)  The whole steps are filled up
+  // to a multiple of 4 with empty ones, which go first; a short last step goes
+  // before them all, from the last stage.
   __device__ __forceinline__ void run(const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k_first,
-                                      int64_t k_end, char* lds0, char* lds1) {
+                                      int64_t k_end, char* l0, char* l1, char* l2, char* l3) {
     tid = threadIdx.x;
     lane = tid & 63;
     wm = wave_index() / WN;
@@ -302,74 +322,159 @@ struct Gemm {
 #pragma unroll
       for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
     if (k_end <= k_first) return;
+    uint32_t at_a[SA::kSpots], at_b[SB::kSpots];
     SA::spots(at_a, wm * (BM / WM), lane);
     SB::spots(at_b, wn * (BN / WN), lane);
     SA sa;
     SB sb;
     sa.init(a, m0, tid);
     sb.init(b, n0, tid);
-    const int64_t s_first = k_first / kBK, whole = k_end / kBK;
+    typename SA::Held ha[2];
+    typename SB::Held hb[2];
+    const int64_t first = k_first / kBK, whole = k_end / kBK;
     const int left = int(k_end - whole * kBK);
-    auto settle = [&](char* lds) {
-      sa.settle(lds, tid);
-      sb.settle(lds + SA::kBytes, tid);
+    const int64_t rounds = (whole - first + 3) / 4;
+    int64_t s = whole - rounds * 4;  // the running step; below `first`: an empty one
+
+    // Loads of step s + ahead < s + 4, on the sides that are (not) packed.
+    auto fetch_early = [&](char* lds, int ahead, bool packed) {
+      if (s + ahead < first) {
+        if (SA::kPacked == packed) sa.template fetch<true>(lds, ha[ahead & 1], first, 0, tid);
+        if (SB::kPacked == packed) sb.template fetch<true>(lds + SA::kBytes, hb[ahead & 1], first, 0, tid);
+      } else {
+        if (SA::kPacked == packed) sa.template fetch<false>(lds, ha[ahead & 1], s + ahead, 0, tid);
+        if (SB::kPacked == packed) sb.template fetch<false>(lds + SA::kBytes, hb[ahead & 1], s + ahead, 0, tid);
+      }
     };
-    // A short last step goes first, so that the loop's steps are all whole;
-    // the stage it takes makes the last step's the second.
-    const int64_t steps = whole - s_first + (left ? 1 : 0);
-    const bool even = (steps & 1) == 0;
-    char* first_stage = even ? lds0 : lds1;
-    int64_t s = s_first;
+    auto settle = [&](char* lds, int set) {
+      sa.settle(lds, ha[set]);
+      sb.settle(lds + SA::kBytes, hb[set]);
+    };
+    bf16x8 fb[kFN], fa[2];
+
+    auto begin = [&](const char* lds) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fa[i] = SA::fragment(lds, at_a, i);
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) fb[j] = SB::fragment(lds + SA::kBytes, at_b, j);
+    };
+    // Multiplies the step in `now`, whose first fragments have been read;
+    // MORE: reads the first ones of the step in `next`; halfway() comes between.
+    // A fragment is read two rows of products before its own.
+    auto multiply = [&](const char* now, const char* next, bool more, auto halfway) {
+      bf16x8 nb[kFN], a[kFM + 2];
+      a[0] = fa[0];
+      a[1] = fa[1];
+#pragma unroll
+      for (int i = 0; i < kFM; ++i) {
+        if (i + 2 < kFM)
+          a[i + 2] = SA::fragment(now, at_a, i + 2);
+        else if (more)
+          a[i + 2] = SA::fragment(next, at_a, i + 2 - kFM);
+        if (more) {
+#pragma unroll
+          for (int j = 0; j < kFN; ++j)
+            if (i == (j * kFM) / kFN) nb[j] = SB::fragment(next + SA::kBytes, at_b, j);
+        }
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], a[i], acc[i][j], 0, 0, 0);
+        if (i == kFM / 2 - 1) halfway();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) {
+        fa[0] = a[kFM];
+        fa[1] = a[kFM + 1];
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) fb[j] = nb[j];
+      }
+    };
+    // Loads a wave starts after those to LDS of step i + 1, by the beginning of
+    // step i: step i + 2's, and the codes of steps i + 2 and i + 3.
+    constexpr int kCodeLoads = (SA::kPacked ? SA::kLoads : 0) + (SB::kPacked ? SB::kLoads : 0);
+    constexpr int kAfter = SA::kLoads + SB::kLoads + kCodeLoads;
+    auto load = [&](char* to3) {
+      if (!SA::kPacked) sa.template fetch<false>(to3, ha[0], s + 3, 0, tid);
+      if (!SB::kPacked) sb.template fetch<false>(to3 + SA::kBytes, hb[0], s + 3, 0, tid);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto step = [&](char* now, char* next, char* to2, char* to3, int set) {
+      wait_loads<kAfter, kPacked>();
+      bare_barrier();
+      load(to3);
+      multiply(now, next, true, [&] {
+        settle(to2, set);
+        if (SA::kPacked) sa.template fetch<false>(nullptr, ha[set], s + 4, 0, tid);
+        if (SB::kPacked) sb.template fetch<false>(nullptr, hb[set], s + 4, 0, tid);
+      });
+      ++s;
+    };
+
+    char* const stage[4] = {l0, l1, l2, l3};
     if (left) {
-      sa.template fetch<true>(first_stage, whole, left, tid);
-      sb.template fetch<true>(first_stage + SA::kBytes, whole, left, tid);
-    } else {
-      sa.template fetch<false>(first_stage, s, 0, tid);
-      sb.template fetch<false>(first_stage + SA::kBytes, s, 0, tid);
-      ++s;
+      sa.template fetch<true>(l3, ha[0], whole, left, tid);
+      sb.template fetch<true>(l3 + SA::kBytes, hb[0], whole, left, tid);
+      settle(l3, 0);
     }
-    settle(first_stage);
-    // One barrier a step: once past it, this step's tiles are in LDS and every
-    // wave has read the other stage's tiles of the step before.
-    auto one = [&](char* now, char* next) {
-      wait_loads();
-      __syncthreads();
-      sa.template fetch<false>(next, s, 0, tid);
-      sb.template fetch<false>(next + SA::kBytes, s, 0, tid);
-      ++s;
-      __builtin_amdgcn_sched_barrier(0);  // the loads start before the products
-      multiply(now, now + SA::kBytes);
-      settle(next);
-    };
-    if (even) one(lds0, lds1);
-    while (s < whole) {
-      one(lds1, lds0);
-      one(lds0, lds1);
+    if (rounds > 0) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) fetch_early(stage[i], i, false);
+      if constexpr (kPacked) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fetch_early(nullptr, i, true);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) settle(stage[i], i);
+#pragma unroll
+        for (int i = 2; i < 4; ++i) fetch_early(nullptr, i, true);
+      }
     }
-    wait_loads();
-    __syncthreads();
-    multiply(lds1, lds1 + SA::kBytes);
+    wait_loads<0, true>();
+    bare_barrier();
+    if (left) {
+      begin(l3);
+      multiply(l3, l3, false, [] {});
+    }
+    if (rounds == 0) return;
+    begin(l0);
+    for (int64_t r = 1; r < rounds; ++r) {
+      step(l0, l1, l2, l3, 0);
+      step(l1, l2, l3, l0, 1);
+      step(l2, l3, l0, l1, 0);
+      step(l3, l0, l1, l2, 1);
+    }
+    wait_loads<kAfter, kPacked>();
+    bare_barrier();
+    load(l3);
+    multiply(l0, l1, true, [&] { settle(l2, 0); });
+    wait_loads<SA::kLoads + SB::kLoads, kPacked>();  // what was started after step i + 1's: codes and the last step's
+    bare_barrier();
+    multiply(l1, l2, true, [&] { settle(l3, 1); });
+    wait_loads<0, kPacked>();
+    bare_barrier();
+    multiply(l2, l3, true, [] {});
+    multiply(l3, l3, false, [] {});
   }
 
   // f(m, n, values of columns n .. n+3) for every group of four this wave
   // holds.  The groups pass through this wave's 16 rows of LDS (the stages are
-  // free by then), so that 16 lanes hand over 64 neighbouring columns of a row.
+  // free by then), so that 16 lanes hand over 64 neighbouring columns of a row;
+  // group g of row r is kept at g ^ r, which spreads the rows over the banks.
   template <typename F>
-  __device__ __forceinline__ void each(int64_t m0, int64_t n0, char* lds0, F f) {
-    constexpr int kCols = BN / WN, kPitch = kCols + 4, kGroups = kCols / 4;
-    static_assert(WM * WN * 16 * kPitch * 4 <= kStage, "epilogue rows");
-    float* rows = reinterpret_cast<float*>(lds0) + wave_index() * 16 * kPitch;
+  __device__ __forceinline__ void each(int64_t m0, int64_t n0, char* lds, F f) {
+    constexpr int kCols = BN / WN, kGroups = kCols / 4, kMask = kGroups - 1;
+    static_assert(WM * WN * 16 * kCols * 4 <= kStage && (kGroups & kMask) == 0, "epilogue rows");
+    float* rows = reinterpret_cast<float*>(lds) + wave_index() * 16 * kCols;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kFM; ++i) {
+      const int w = lane & 15;
 #pragma unroll
       for (int j = 0; j < kFN; ++j)
-        *reinterpret_cast<f32x4v*>(rows + (lane & 15) * kPitch + j * 16 + 4 * (lane >> 4)) = acc[i][j];
+        *reinterpret_cast<f32x4v*>(rows + w * kCols + ((4 * j + (lane >> 4)) ^ (w & kMask)) * 4) = acc[i][j];
 #pragma unroll 1
       for (int q = lane; q < 16 * kGroups; q += 64) {
-        const int r = q / kGroups, c = (q % kGroups) * 4;
-        f(m0 + wm * (BM / WM) + i * 16 + r, n0 + wn * kCols + c,
-          *reinterpret_cast<const f32x4v*>(rows + r * kPitch + c));
+        const int r = q / kGroups, c = q % kGroups;
+        f(m0 + wm * (BM / WM) + i * 16 + r, n0 + wn * kCols + c * 4,
+          *reinterpret_cast<const f32x4v*>(rows + r * kCols + (c ^ (r & kMask)) * 4));
       }
     }
   }

@@ -156,6 +156,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
   using G = Gemm<Form::kRows, Form::kRows, Code::kE4m3, BM, BN, WM, WN>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
+  __shared__ __align__(16) char lds2[G::kStage];
+  __shared__ __align__(16) char lds3[G::kStage];
   uint32_t tm, tn;
   tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
   const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
@@ -164,7 +166,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
   a.h.base = static_cast<const uint16_t*>(a.h.base) + a.first * a.h.ld;
   a.h.extent = rows;
   G g;
-  g.run(a.h, a.w, m0, n0, 0, a.depth, lds0, lds1);
+  g.run(a.h, a.w, m0, n0, 0, a.depth, lds0, lds1, lds2, lds3);
 
   // A lane holds of row 16 i + lane % 16 the columns 16 j + 4 (lane / 16) + r.
   // The tile row's maximum and sum go over its lanes, then over the WN waves.
@@ -328,6 +330,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
   using G = Gemm<Form::kRows, Form::kCols, Code::kE4m3, BM, BN, WM, WN>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
+  __shared__ __align__(16) char lds2[G::kStage];
+  __shared__ __align__(16) char lds3[G::kStage];
   uint32_t tm, tn;
   tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
   const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
@@ -337,7 +341,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
   const int64_t k0 = int64_t(blockIdx.y) * a.split_k;
   const int64_t k1 = k0 + a.split_k < a.vocab ? k0 + a.split_k : a.vocab;
   G g;
-  g.run(a.dz, a.w, m0, n0, k0, k1, lds0, lds1);
+  g.run(a.dz, a.w, m0, n0, k0, k1, lds0, lds1, lds2, lds3);
   const float scale = *a.scale;
   g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
     if (m >= rows || n >= a.hidden) return;
@@ -393,13 +397,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void vocab_grad_kernel(VocabGradArg
   using G = Gemm<Form::kCols, Form::kCols, Code::kE4m3, BM, BN, WM, WN>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
+  __shared__ __align__(16) char lds2[G::kStage];
+  __shared__ __align__(16) char lds3[G::kStage];
   uint32_t tm, tn;
   tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
   const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
   const int64_t rows = rows_of(a.count, a.first, a.piece);
   a.h.base = static_cast<const uint16_t*>(a.h.base) + a.first * a.h.ld;
   G g;
-  g.run(a.dz, a.h, m0, n0, 0, rows, lds0, lds1);
+  g.run(a.dz, a.h, m0, n0, 0, rows, lds0, lds1, lds2, lds3);
   const float scale = *a.scale;
   g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
     if (m >= a.vocab || n >= a.hidden) return;
@@ -477,7 +483,7 @@ Layout layout_of(const VocabLossCall& c) {
     const int64_t mine = (L.piece + side - 1) / side * ((c.hidden + side - 1) / side);
     const int64_t steps = (c.vocab + kBK - 1) / kBK;
     int64_t splits = L.big_h || mine == 0 ? 1 : 512 / mine;
-    if (splits > steps / 4) splits = steps / 4;
+    if (splits > steps / 8) splits = steps / 8;
     if (splits < 1) splits = 1;
     const int64_t per = (steps + splits - 1) / splits;
     L.h_splits = (steps + per - 1) / per;

@@ -25,13 +25,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void weight_grad_kernel(WeightGradA
   using G = Gemm<Form::kCols, Form::kPacked, CODE, BM, BN, WM, WN>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
+  __shared__ __align__(16) char lds2[G::kStage];
+  __shared__ __align__(16) char lds3[G::kStage];
   uint32_t tm, tn;
   tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
   const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
   const int64_t k0 = int64_t(blockIdx.y) * a.split_k;
   const int64_t k1 = k0 + a.split_k < a.tokens ? k0 + a.split_k : a.tokens;
   G g;
-  g.run(a.dy, a.x, m0, n0, k0, k1, lds0, lds1);
+  g.run(a.dy, a.x, m0, n0, k0, k1, lds0, lds1, lds2, lds3);
   if (a.partial) {
     float* p = a.partial + int64_t(blockIdx.y) * a.outs * a.ins;
     g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
@@ -98,7 +100,7 @@ WeightGradPlan plan_weight_grad(int64_t tokens, int64_t outs, int64_t ins, bool 
   int64_t splits = 1;
   if (!p.big && tiles > 0) {
     splits = 512 / tiles;
-    if (splits > steps / 4) splits = steps / 4;
+    if (splits > steps / 8) splits = steps / 8;
     if (splits < 1) splits = 1;
   }
   const int64_t per = splits > 1 ? (steps + splits - 1) / splits : (steps > 0 ? steps : 1);

@@ -13,8 +13,11 @@
 // bytes a lane).  Those loads fill LDS in lane order, so the bank swizzle is
 // made by choosing which 16 bytes a lane fetches:
 //   kRows tile [rows][32 k], 4 chunks of 16 bytes a row: chunk c of row r is
-//     kept at c ^ (r / 4 & 3), and the 16-byte fragment reads of 16
-//     consecutive rows touch all 64 banks once;
+//     kept at c ^ f(r), f(r) = -(r / 4) mod 4.  A 16-byte fragment read goes
+//     through the 64 banks 16 lanes at a time, not neighbours but lanes 0-3,
+//     12-15 and 20-27, then the rest of 0-31, and so on: f gives each such
+//     group 16 different places (r / 4 mod 4 does not: measured, bank conflicts
+//     in 21% of a kernel's cycles);
 //   kCols, kPacked tile [32 k][rows]: chunk c of row k is kept at
 //     c ^ 2 f(k), f(k) made of bits 0, 1 and 3 of k; a fragment is read by the
 //     transposing LDS read, whose 32 lanes touch 8 rows k of 32 bytes each.
@@ -103,6 +106,7 @@ __device__ __forceinline__ uint32_t renew(uint32_t& v) {
 
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6); }
 
+__device__ __forceinline__ int row_swizzle(int r) { return -(r >> 2) & 3; }
 __device__ __forceinline__ int col_swizzle(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
 
 __device__ __forceinline__ bf16x2 bits_as_bf16x2(uint32_t v) {
@@ -165,7 +169,7 @@ struct Side {
   };
 
   static __device__ __forceinline__ int part_k(int lin) {
-    return FORM == Form::kRows ? ((lin & 3) ^ ((lin >> 4) & 3)) * 8 : lin / (kPacked ? ROWS / 16 : kRowChunks);
+    return FORM == Form::kRows ? ((lin & 3) ^ row_swizzle(lin >> 2)) * 8 : lin / (kPacked ? ROWS / 16 : kRowChunks);
   }
 
   __device__ __forceinline__ void init(const Operand& o, int64_t first, int tid) {
@@ -236,6 +240,11 @@ struct Side {
     }
   }
 
+  // Part i of a whole step's loads to LDS.
+  __device__ __forceinline__ void fetch_part(char* lds, int64_t s, int i) {
+    load_to_lds(uniform(base + s * step), off[i], lds + (i * THREADS + wave_index() * 64) * 16);
+  }
+
   // kPacked: widen what fetch() loaded and write it to LDS.
   __device__ __forceinline__ void settle(char* lds, const Held& held) {
     if constexpr (kPacked) {
@@ -258,7 +267,7 @@ struct Side {
   static __device__ __forceinline__ void spots(uint32_t* at, int r0, int lane) {
     if constexpr (FORM == Form::kRows) {
       const int r = r0 + (lane & 15);
-      at[0] = uint32_t((r * kRowChunks + ((lane >> 4) ^ ((r >> 2) & 3))) * 16);
+      at[0] = uint32_t((r * kRowChunks + ((lane >> 4) ^ row_swizzle(r))) * 16);
     } else {
       // a transposing read gives lane l of 16 the values of column l in the
       // four rows k of which lanes 4j .. 4j+3 point at 4 columns each
@@ -359,9 +368,10 @@ struct Gemm {
       for (int j = 0; j < kFN; ++j) fb[j] = SB::fragment(lds + SA::kBytes, at_b, j);
     };
     // Multiplies the step in `now`, whose first fragments have been read;
-    // MORE: reads the first ones of the step in `next`; halfway() comes between.
-    // A fragment is read two rows of products before its own.
-    auto multiply = [&](const char* now, const char* next, bool more, auto halfway) {
+    // MORE: reads the first ones of the step in `next`.  A fragment is read two
+    // rows of products before its own; part(i) follows row i, halfway() the
+    // middle one.
+    auto multiply = [&](const char* now, const char* next, bool more, auto part, auto halfway) {
       bf16x8 nb[kFN], a[kFM + 2];
       a[0] = fa[0];
       a[1] = fa[1];
@@ -378,6 +388,7 @@ struct Gemm {
         }
 #pragma unroll
         for (int j = 0; j < kFN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], a[i], acc[i][j], 0, 0, 0);
+        part(i);
         if (i == kFM / 2 - 1) halfway();
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -392,16 +403,18 @@ struct Gemm {
     // step i: step i + 2's, and the codes of steps i + 2 and i + 3.
     constexpr int kCodeLoads = (SA::kPacked ? SA::kLoads : 0) + (SB::kPacked ? SB::kLoads : 0);
     constexpr int kAfter = SA::kLoads + SB::kLoads + kCodeLoads;
-    auto load = [&](char* to3) {
-      if (!SA::kPacked) sa.template fetch<false>(to3, ha[0], s + 3, 0, tid);
-      if (!SB::kPacked) sb.template fetch<false>(to3 + SA::kBytes, hb[0], s + 3, 0, tid);
-      __builtin_amdgcn_sched_barrier(0);
+    // Part i of the loads of step s + 3.  (One after each row of products:
+    // started together at the step's head they hold its products up, 4% of a
+    // large product's time.)
+    auto load = [&](char* to3, int i) {
+      if (!SA::kPacked && i < SA::kParts) sa.fetch_part(to3, s + 3, i);
+      const int j = i - (SA::kPacked ? 0 : SA::kParts);
+      if (!SB::kPacked && j >= 0 && j < SB::kParts) sb.fetch_part(to3 + SA::kBytes, s + 3, j);
     };
     auto step = [&](char* now, char* next, char* to2, char* to3, int set) {
       wait_loads<kAfter, kPacked>();
       bare_barrier();
-      load(to3);
-      multiply(now, next, true, [&] {
+      multiply(now, next, true, [&](int i) { load(to3, i); }, [&] {
         settle(to2, set);
         if (SA::kPacked) sa.template fetch<false>(nullptr, ha[set], s + 4, 0, tid);
         if (SB::kPacked) sb.template fetch<false>(nullptr, hb[set], s + 4, 0, tid);
@@ -431,7 +444,7 @@ struct Gemm {
     bare_barrier();
     if (left) {
       begin(l3);
-      multiply(l3, l3, false, [] {});
+      multiply(l3, l3, false, [](int) {}, [] {});
     }
     if (rounds == 0) return;
     begin(l0);
@@ -443,15 +456,14 @@ struct Gemm {
     }
     wait_loads<kAfter, kPacked>();
     bare_barrier();
-    load(l3);
-    multiply(l0, l1, true, [&] { settle(l2, 0); });
+    multiply(l0, l1, true, [&](int i) { load(l3, i); }, [&] { settle(l2, 0); });
     wait_loads<SA::kLoads + SB::kLoads, kPacked>();  // what was started after step i + 1's: codes and the last step's
     bare_barrier();
-    multiply(l1, l2, true, [&] { settle(l3, 1); });
+    multiply(l1, l2, true, [](int) {}, [&] { settle(l3, 1); });
     wait_loads<0, kPacked>();
     bare_barrier();
-    multiply(l2, l3, true, [] {});
-    multiply(l3, l3, false, [] {});
+    multiply(l2, l3, true, [](int) {}, [] {});
+    multiply(l3, l3, false, [](int) {}, [] {});
   }
 
   // f(m, n, values of columns n .. n+3) for every group of four this wave

@@ -8,6 +8,7 @@ smaller than the plan assumes), and raises on a non-zero status.  There is no
 fallback: without the compiled library, importing this module fails.
 """
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -274,10 +275,10 @@ class Plan:
 
 
 def _stream_handle(stream):
-    import torch
-
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:
+        # the handle alone: building torch.cuda.current_stream()'s object takes longer than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return int(stream.cuda_stream)
 
 
 def _require(t, dtype, numel, what):
@@ -457,45 +458,52 @@ def allgather_copyin(plan, shards, rank_major, stream=None):
 
 # ------------------------------------------------------------ activation checkpoints
 
+_BF16 = (torch.bfloat16,)
+_FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+_CODES = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_INT8}
+
 
 def _on_device(t, what):
-    import torch
-
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what}: expected a GPU tensor, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{what}: lives on {t.device}, but the kernels run on the current device "
                          f"cuda:{torch.cuda.current_device()}")
 
 
 def _matrix(t, dtypes, what, strided=True):
-    """(address, TIDE_DTYPE_*, rows, columns, row stride) of a matrix of one of
-    `dtypes` whose rows are contiguous; without `strided` they have no gaps."""
-    import torch
-
+    """(address, rows, columns, row stride) of a matrix of one of `dtypes`
+    whose rows are contiguous; without `strided` they have no gaps."""
     _on_device(t, what)
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{what}: expected a matrix, got {t.dim()} dimensions")
     rows, cols = t.shape
-    # the strides of a dimension of one element (or none) say nothing
-    stride = t.stride(0) if rows > 1 and t.numel() else cols
-    if t.numel() and ((cols > 1 and t.stride(1) != 1) or stride < cols):
+    if t.is_contiguous():
+        return t.data_ptr(), rows, cols, cols
+    # the stride of a dimension of one element says nothing
+    stride = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or stride < cols:
         raise ValueError(f"{what}: expected contiguous, non-overlapping rows, got strides {t.stride()}")
-    if not strided and stride != cols:
+    if not strided:
         raise ValueError(f"{what}: expected rows without gaps, got strides {t.stride()}")
-    return ctypes.c_void_p(t.data_ptr() or None), DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16, rows, cols, stride
+    return t.data_ptr(), rows, cols, stride
 
 
-def _floats():
-    import torch
+def _vector(t, dtype, n, what):
+    _on_device(t, what)
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what}: expected a contiguous tensor of {n} elements, got shape {tuple(t.shape)}, strides "
+                         f"{t.stride()}")
+    return t.data_ptr()
 
-    return (torch.bfloat16, torch.float32)
 
-
+@functools.lru_cache(maxsize=None)
 def checkpoint_layout(cols):
     """(code columns, scale columns) of a checkpoint of rows of `cols` values
     (tide_checkpoint_layout)."""
@@ -506,93 +514,92 @@ def checkpoint_layout(cols):
 
 def _packed(codes, scales, rows, cols):
     """(codes address, scales address, TIDE_CODE_*) of a checkpoint of a rows x cols matrix."""
-    import torch
-
-    kinds = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_INT8}
-    for t, what in ((codes, "codes"), (scales, "scales")):
-        _on_device(t, what)
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: expected a contiguous tensor")
-    if codes.dtype not in kinds:
+    _on_device(codes, "codes")
+    _on_device(scales, "scales")
+    if codes.dtype not in _CODES:
         raise TypeError(f"codes: expected torch.float8_e4m3fn or torch.int8, got {codes.dtype}")
     if scales.dtype != torch.uint8:
         raise TypeError(f"scales: expected torch.uint8, got {scales.dtype}")
     c, s = checkpoint_layout(cols)
-    if tuple(codes.shape) != (rows, c) or tuple(scales.shape) != (rows, s):
+    if codes.shape != (rows, c) or scales.shape != (rows, s):
         raise ValueError(f"codes and scales of a {rows} x {cols} matrix are {(rows, c)} and {(rows, s)}, got "
                          f"{tuple(codes.shape)} and {tuple(scales.shape)}")
-    return ctypes.c_void_p(codes.data_ptr() or None), ctypes.c_void_p(scales.data_ptr() or None), kinds[codes.dtype]
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("codes and scales: expected contiguous tensors")
+    return codes.data_ptr(), scales.data_ptr(), _CODES[codes.dtype]
+
+
+def _pack_args(x, codes, scales):
+    p, rows, cols, stride = _matrix(x, _FLOATS, "x")
+    c, s, fmt = _packed(codes, scales, rows, cols)
+    return p, _FLOATS[x.dtype], rows, cols, stride, fmt, c, s
 
 
 def checkpoint_pack_call(x, codes, scales):
     """A registered checkpoint pack (see checkpoint_pack)."""
-    p, dt, rows, cols, stride = _matrix(x, _floats(), "x")
-    c, s, fmt = _packed(codes, scales, rows, cols)
-    return Call(lib.tide_checkpoint_pack, (p, dt, rows, cols, stride, fmt, c, s), (x, codes, scales))
+    return Call(lib.tide_checkpoint_pack, _pack_args(x, codes, scales), (x, codes, scales))
 
 
 def checkpoint_pack(x, codes, scales, stream=None):
     """Pack a matrix into its 8-bit form: x (bf16 or fp32, contiguous rows) ->
     codes (float8_e4m3fn or int8, which chooses the code type) and scales
     (uint8), sized by checkpoint_layout (tide_checkpoint_pack)."""
-    checkpoint_pack_call(x, codes, scales)(stream)
+    _check(lib.tide_checkpoint_pack(*_pack_args(x, codes, scales), _stream_handle(stream)))
+
+
+def _unpack_args(codes, scales, out):
+    p, rows, cols, stride = _matrix(out, _FLOATS, "out")
+    c, s, fmt = _packed(codes, scales, rows, cols)
+    return c, s, fmt, rows, cols, p, _FLOATS[out.dtype], stride
 
 
 def checkpoint_unpack_call(codes, scales, out):
     """A registered checkpoint restore (see checkpoint_unpack)."""
-    p, dt, rows, cols, stride = _matrix(out, _floats(), "out")
-    c, s, fmt = _packed(codes, scales, rows, cols)
-    return Call(lib.tide_checkpoint_unpack, (c, s, fmt, rows, cols, p, dt, stride), (codes, scales, out))
+    return Call(lib.tide_checkpoint_unpack, _unpack_args(codes, scales, out), (codes, scales, out))
 
 
 def checkpoint_unpack(codes, scales, out, stream=None):
     """Restore a packed matrix, exactly, into out (bf16 or fp32, contiguous
     rows; tide_checkpoint_unpack)."""
-    checkpoint_unpack_call(codes, scales, out)(stream)
+    _check(lib.tide_checkpoint_unpack(*_unpack_args(codes, scales, out), _stream_handle(stream)))
 
 
 def _workspace(nbytes, given, stream):
-    """A workspace of nbytes: the caller's, or one that belongs to the stream
-    the call runs on (freed memory goes back to that stream's work only)."""
-    import torch
-
+    """(address, bytes, tensor) of a workspace of nbytes: the caller's, or one
+    that belongs to the stream the call runs on (once freed it goes back to
+    that stream's work only)."""
     if given is None:
         if nbytes == 0:
-            return None
-        with torch.cuda.stream(stream):  # None: the current stream
-            return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    _on_device(given, "workspace")
-    if given.dtype != torch.uint8 or not given.is_contiguous():
-        raise TypeError("workspace: expected a contiguous torch.uint8 tensor")
-    return given
+            return 0, 0, None
+        if stream is None:
+            given = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        else:
+            with torch.cuda.stream(stream):
+                given = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    else:
+        _on_device(given, "workspace")
+        if given.dtype != torch.uint8 or not given.is_contiguous():
+            raise TypeError("workspace: expected a contiguous torch.uint8 tensor")
+    return given.data_ptr(), given.numel(), given
 
 
-def _workspace_args(w):
-    return ctypes.c_void_p(w.data_ptr() or None) if w is not None else None, w.numel() if w is not None else 0
-
-
-def _weight_grad(dy, codes, scales, dw, alpha, accumulate, workspace, stream):
-    import torch
-
-    y, _, rows, outs, stride = _matrix(dy, (torch.bfloat16,), "dy")
-    w, dt, w_outs, ins, _ = _matrix(dw, _floats(), "dw", strided=False)
+def _weight_grad_args(dy, codes, scales, dw, alpha, accumulate, workspace, stream):
+    """(arguments, workspace tensor)."""
+    y, rows, outs, stride = _matrix(dy, _BF16, "dy")
+    w, w_outs, ins, _ = _matrix(dw, _FLOATS, "dw", strided=False)
     if w_outs != outs:
         raise ValueError(f"dw has {w_outs} rows, dy {outs} columns")
     c, s, fmt = _packed(codes, scales, rows, ins)
     need = ctypes.c_int64()
     _check(lib.tide_checkpoint_weight_grad_workspace(y, rows, outs, stride, ins, ctypes.byref(need)))
-    ws = _workspace(need.value, workspace, stream)
-    return Call(lib.tide_checkpoint_weight_grad,
-                (y, rows, outs, stride, c, s, fmt, ins, w, dt, ctypes.c_float(alpha), int(bool(accumulate)),
-                 *_workspace_args(ws)), (dy, codes, scales, dw, ws))
+    ws, nbytes, keep = _workspace(need.value, workspace, stream)
+    return (y, rows, outs, stride, c, s, fmt, ins, w, _FLOATS[dw.dtype], alpha, int(bool(accumulate)), ws, nbytes), keep
 
 
 def checkpoint_weight_grad_workspace(dy, in_features):
     """Bytes of workspace the weight gradient from dy takes
     (tide_checkpoint_weight_grad_workspace)."""
-    import torch
-
-    y, _, rows, outs, stride = _matrix(dy, (torch.bfloat16,), "dy")
+    y, rows, outs, stride = _matrix(dy, _BF16, "dy")
     need = ctypes.c_int64()
     _check(lib.tide_checkpoint_weight_grad_workspace(y, rows, outs, stride, int(in_features), ctypes.byref(need)))
     return need.value
@@ -601,7 +608,8 @@ def checkpoint_weight_grad_workspace(dy, in_features):
 def checkpoint_weight_grad_call(dy, codes, scales, dw, alpha=1.0, accumulate=False, workspace=None):
     """A registered weight gradient (see checkpoint_weight_grad); it keeps one
     workspace, so its calls must not overlap."""
-    return _weight_grad(dy, codes, scales, dw, alpha, accumulate, workspace, None)
+    args, keep = _weight_grad_args(dy, codes, scales, dw, alpha, accumulate, workspace, None)
+    return Call(lib.tide_checkpoint_weight_grad, args, (dy, codes, scales, dw, keep))
 
 
 def checkpoint_weight_grad(dy, codes, scales, dw, alpha=1.0, accumulate=False, workspace=None, stream=None):
@@ -611,57 +619,53 @@ def checkpoint_weight_grad(dy, codes, scales, dw, alpha=1.0, accumulate=False, w
     bf16 or fp32 (out_features x in_features).  `workspace` is a uint8 tensor of
     at least checkpoint_weight_grad_workspace bytes; without one the call takes
     its own (tide_checkpoint_weight_grad)."""
-    _weight_grad(dy, codes, scales, dw, alpha, accumulate, workspace, stream)(stream)
+    args, keep = _weight_grad_args(dy, codes, scales, dw, alpha, accumulate, workspace, stream)
+    _check(lib.tide_checkpoint_weight_grad(*args, _stream_handle(stream)))
 
 
 # ------------------------------------------------------------ vocabulary loss
 
 
-def _vector(t, dtype, n, what):
-    _require(t, dtype, n, what)
-    return ctypes.c_void_p(t.data_ptr() or None)
-
-
 def _projection(hidden, weight):
-    """(the operands' arguments, tokens, hidden size, vocabulary)."""
-    import torch
-
-    h, _, tokens, size, h_stride = _matrix(hidden, (torch.bfloat16,), "hidden")
-    w, _, vocab, w_size, w_stride = _matrix(weight, (torch.bfloat16,), "weight")
+    """The operands' arguments, (tokens, hidden size, vocabulary)."""
+    h, tokens, size, h_stride = _matrix(hidden, _BF16, "hidden")
+    w, vocab, w_size, w_stride = _matrix(weight, _BF16, "weight")
     if w_size != size:
         raise ValueError(f"weight has {w_size} columns, hidden {size}")
-    return (h, h_stride, w, w_stride), tokens, size, vocab
+    return (h, h_stride, w, w_stride), (tokens, size, vocab)
 
 
-def _vocab_loss_bytes(operands, tokens, size, vocab, gradients, dtype):
+def _vocab_loss_bytes(operands, sizes, gradients, dtype):
     need = ctypes.c_int64()
-    _check(lib.tide_vocab_loss_workspace(*operands, tokens, size, vocab, gradients, dtype, ctypes.byref(need)))
+    _check(lib.tide_vocab_loss_workspace(*operands, *sizes, gradients, dtype, ctypes.byref(need)))
     return need.value
 
 
 def vocab_loss_workspace(hidden, weight, dweight=None):
     """Bytes of workspace of vocab_loss, or of vocab_loss_grad where its
     dweight is given (tide_vocab_loss_workspace)."""
-    operands, tokens, size, vocab = _projection(hidden, weight)
-    dtype = DTYPE_F32 if dweight is None else _matrix(dweight, _floats(), "dweight", strided=False)[1]
-    return _vocab_loss_bytes(operands, tokens, size, vocab, int(dweight is not None), dtype)
+    operands, sizes = _projection(hidden, weight)
+    if dweight is None:
+        return _vocab_loss_bytes(operands, sizes, 0, DTYPE_F32)
+    _matrix(dweight, _FLOATS, "dweight", strided=False)
+    return _vocab_loss_bytes(operands, sizes, 1, _FLOATS[dweight.dtype])
 
 
-def _vocab_loss(hidden, weight, targets, loss, lse, workspace, stream):
-    import torch
-
-    operands, tokens, size, vocab = _projection(hidden, weight)
+def _vocab_loss_args(hidden, weight, targets, loss, lse, workspace, stream):
+    """(arguments, workspace tensor)."""
+    operands, sizes = _projection(hidden, weight)
+    tokens = sizes[0]
     t = _vector(targets, torch.int64, tokens, "targets")
     out = _vector(loss, torch.float32, tokens, "loss"), None if lse is None else _vector(lse, torch.float32, tokens, "lse")
-    ws = _workspace(_vocab_loss_bytes(operands, tokens, size, vocab, 0, DTYPE_F32), workspace, stream)
-    return Call(lib.tide_vocab_loss, (*operands, t, tokens, size, vocab, *out, *_workspace_args(ws)),
-                (hidden, weight, targets, loss, lse, ws))
+    ws, nbytes, keep = _workspace(_vocab_loss_bytes(operands, sizes, 0, DTYPE_F32), workspace, stream)
+    return (*operands, t, *sizes, *out, ws, nbytes), keep
 
 
 def vocab_loss_call(hidden, weight, targets, loss, lse=None, workspace=None):
     """A registered vocabulary loss (see vocab_loss); it keeps one workspace,
     so its calls must not overlap."""
-    return _vocab_loss(hidden, weight, targets, loss, lse, workspace, None)
+    args, keep = _vocab_loss_args(hidden, weight, targets, loss, lse, workspace, None)
+    return Call(lib.tide_vocab_loss, args, (hidden, weight, targets, loss, lse, keep))
 
 
 def vocab_loss(hidden, weight, targets, loss, lse=None, workspace=None, stream=None):
@@ -669,33 +673,36 @@ def vocab_loss(hidden, weight, targets, loss, lse=None, workspace=None, stream=N
     rows) against targets (int64): loss[t] and, if given, the log-sum-exp
     lse[t], fp32 per token.  A target outside the vocabulary leaves its token
     out, with 0s.  `workspace` as for checkpoint_weight_grad (tide_vocab_loss)."""
-    _vocab_loss(hidden, weight, targets, loss, lse, workspace, stream)(stream)
+    args, keep = _vocab_loss_args(hidden, weight, targets, loss, lse, workspace, stream)
+    _check(lib.tide_vocab_loss(*args, _stream_handle(stream)))
 
 
-def _vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate, workspace, stream):
-    import torch
-
-    operands, tokens, size, vocab = _projection(hidden, weight)
+def _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate, workspace,
+                          stream):
+    """(arguments, workspace tensor)."""
+    operands, sizes = _projection(hidden, weight)
+    tokens, size, vocab = sizes
     t = _vector(targets, torch.int64, tokens, "targets")
     g = _vector(grad_loss, torch.float32, tokens, "grad_loss")
     out = _vector(loss, torch.float32, tokens, "loss"), None if lse is None else _vector(lse, torch.float32, tokens, "lse")
-    dh, _, *dh_shape, _ = _matrix(dhidden, (torch.bfloat16,), "dhidden", strided=False)
-    dw, dt, *dw_shape, _ = _matrix(dweight, _floats(), "dweight", strided=False)
+    dh, *dh_shape, _ = _matrix(dhidden, _BF16, "dhidden", strided=False)
+    dw, *dw_shape, _ = _matrix(dweight, _FLOATS, "dweight", strided=False)
     if dh_shape != [tokens, size] or dw_shape != [vocab, size]:
         raise ValueError(f"dhidden and dweight must be {tokens} x {size} and {vocab} x {size}, got {dh_shape} and "
                          f"{dw_shape}")
-    ws = _workspace(_vocab_loss_bytes(operands, tokens, size, vocab, 1, dt), workspace, stream)
-    return Call(lib.tide_vocab_loss_grad,
-                (*operands, t, g, tokens, size, vocab, *out, dh, dw, dt, int(bool(accumulate)), *_workspace_args(ws)),
-                (hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, ws))
+    dtype = _FLOATS[dweight.dtype]
+    ws, nbytes, keep = _workspace(_vocab_loss_bytes(operands, sizes, 1, dtype), workspace, stream)
+    return (*operands, t, g, *sizes, *out, dh, dw, dtype, int(bool(accumulate)), ws, nbytes), keep
 
 
 def vocab_loss_grad_call(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate=False,
                          workspace=None):
     """A registered vocabulary loss with gradients (see vocab_loss_grad); it
     keeps one workspace, so its calls must not overlap."""
-    return _vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate, workspace,
-                            None)
+    args, keep = _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate,
+                                       workspace, None)
+    return Call(lib.tide_vocab_loss_grad, args,
+                (hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, keep))
 
 
 def vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate=False, workspace=None,
@@ -703,8 +710,9 @@ def vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dwei
     """vocab_loss with the gradients of sum_t grad_loss[t] * loss[t]: dhidden
     (bf16) and dweight (bf16 or fp32; added to the old one when accumulate is
     true).  lse may be None (tide_vocab_loss_grad)."""
-    _vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate, workspace,
-                     stream)(stream)
+    args, keep = _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate,
+                                       workspace, stream)
+    _check(lib.tide_vocab_loss_grad(*args, _stream_handle(stream)))
 
 
 # ------------------------------------------------------------ instruments

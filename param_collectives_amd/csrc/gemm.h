@@ -296,7 +296,59 @@ struct Side {
   }
 };
 
-// The tile loop.  WM x WN waves, each holding an (BM / WM) x (BN / WN) part.
+__device__ __forceinline__ uint32_t bf16_bits_of(float v) {
+  const __bf16 b = __bf16(v);  // round to nearest even
+  uint16_t r;
+  __builtin_memcpy(&r, &b, 2);
+  return r;
+}
+__device__ __forceinline__ uint32_t two_bf16(float a, float b) { return bf16_bits_of(a) | bf16_bits_of(b) << 16; }
+__device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+__device__ __forceinline__ f32x4v add4(f32x4v a, f32x4v b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = a[j] + b[j];
+  return b;
+}
+
+// Where a product goes: alpha (add + s) (+ old), rounded once to fp32 or bf16.
+struct Target {
+  void* base;
+  int64_t ld, rows, cols;
+  const int32_t* row_map;  // the row of `base` (and `add`) that each row goes to, or null
+  const float* add;        // as `base`, or null
+  float alpha;
+  int32_t f32, accumulate;
+};
+
+// Orders this wave's LDS accesses for all its lanes: what a lane wrote before is
+// read by the others after, and the other way round.  (The LDS serves a wave in
+// order; it is the compiler that must not swap accesses of different lanes.)
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Waits for this wave's LDS accesses, then for the other waves (not for loads).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  bare_barrier();
+}
+
+// The tile loop.  WM x WN waves, each holding an (BM / WM) x (BN / WN) part.  A
+// workgroup takes one tile after another: open() starts a tile's first loads,
+// loop() sums it into acc, and between that and the use of acc comes the next
+// tile's open(), so that its loads (but codes) pass under the epilogue.
+//
+// Step i's tiles lie in stage i mod 4.  While a wave multiplies step i it
+// starts the loads of step i + 3 and reads the first fragments of step i + 1,
+// so that one barrier a step is enough and no product waits behind it: past
+// it, step i + 1 has arrived for all waves, and all are done with the stage
+// that step i + 3 goes to.  (Packed codes are loaded 4 steps ahead into
+// registers and written to LDS 2 steps ahead.)  The whole steps are filled up
+// to a multiple of 4 with empty ones, which go first; a short last step goes
+// before them all, from the last stage.
 template <Form FA, Form FB, Code CODE, int BM, int BN, int WM, int WN>
 struct Gemm {
   static constexpr int kThreads = WM * WN * 64;
@@ -304,62 +356,80 @@ struct Gemm {
   using SA = Side<FA, CODE, BM, kFM, kThreads>;
   using SB = Side<FB, CODE, BN, kFN, kThreads>;
   static constexpr bool kPacked = SA::kPacked || SB::kPacked;
-  static constexpr int kStage = SA::kBytes + SB::kBytes;
+  static constexpr int kStage = SA::kBytes + SB::kBytes;  // bytes of each of the four stages
 
   f32x4v acc[kFM][kFN];
   int tid, lane, wm, wn;
 
-  // Sums k over [k_first, k_end) (k_first a multiple of 32) into acc; the
-  // stages hold kStage bytes each.
-  //
-  // Step i's tiles lie in stage i mod 4.  While a wave multiplies step i it
-  // starts the loads of step i + 3 and reads the first fragments of step i + 1,
-  // so that one barrier a step is enough and no product waits behind it: past
-  // it, step i + 1 has arrived for all waves, and all are done with the stage
-  // that step i + 3 goes to.  (Packed codes are loaded 4 steps ahead into
-  // registers and written to LDS 2 steps ahead.)  The whole steps are filled up
-  // to a multiple of 4 with empty ones, which go first; a short last step goes
-  // before them all, from the last stage.
-  __device__ __forceinline__ void run(const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k_first,
-                                      int64_t k_end, char* l0, char* l1, char* l2, char* l3) {
+  SA sa;
+  SB sb;
+  uint32_t at_a[SA::kSpots], at_b[SB::kSpots];
+  int64_t s;       // the running step, in 32 k; below `first`: an empty one
+  int64_t first, whole, rounds;
+  int left;
+
+  __device__ __forceinline__ void setup() {
     tid = threadIdx.x;
     lane = tid & 63;
     wm = wave_index() / WN;
     wn = wave_index() % WN;
+    SA::spots(at_a, wm * (BM / WM), lane);
+    SB::spots(at_b, wn * (BN / WN), lane);
+  }
+
+  // Loads to LDS of step s + ahead < s + 3.
+  __device__ __forceinline__ void fetch_early(char* lds, int ahead) {
+    typename SA::Held na;
+    typename SB::Held nb;
+    if (s + ahead < first) {
+      if (!SA::kPacked) sa.template fetch<true>(lds, na, first, 0, tid);
+      if (!SB::kPacked) sb.template fetch<true>(lds + SA::kBytes, nb, first, 0, tid);
+    } else {
+      if (!SA::kPacked) sa.template fetch<false>(lds, na, s + ahead, 0, tid);
+      if (!SB::kPacked) sb.template fetch<false>(lds + SA::kBytes, nb, s + ahead, 0, tid);
+    }
+  }
+
+  // Starts the tile at (m0, n0), k in [k_first, k_end) (k_first a multiple of
+  // 32), in the first three stages, which no wave uses any more.
+  __device__ __forceinline__ void open(const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k_first,
+                                       int64_t k_end, char* l0, char* l1, char* l2) {
+    sa.init(a, m0, tid);
+    sb.init(b, n0, tid);
+    first = k_first / kBK;
+    whole = k_end > k_first ? k_end / kBK : first;
+    left = k_end > k_first ? int(k_end - whole * kBK) : 0;
+    rounds = (whole - first + 3) / 4;
+    s = whole - rounds * 4;
+    if (rounds == 0) return;
+    fetch_early(l0, 0);
+    fetch_early(l1, 1);
+    fetch_early(l2, 2);
+  }
+
+  // Sums the opened tile into acc.  All waves are done with the stages then.
+  __device__ __forceinline__ void loop(char* l0, char* l1, char* l2, char* l3) {
 #pragma unroll
     for (int i = 0; i < kFM; ++i)
 #pragma unroll
       for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
-    if (k_end <= k_first) return;
-    uint32_t at_a[SA::kSpots], at_b[SB::kSpots];
-    SA::spots(at_a, wm * (BM / WM), lane);
-    SB::spots(at_b, wn * (BN / WN), lane);
-    SA sa;
-    SB sb;
-    sa.init(a, m0, tid);
-    sb.init(b, n0, tid);
-    typename SA::Held ha[2];
+    bf16x8 fb[kFN], fa[2];
+    typename SA::Held ha[2];  // packed sides: codes of an even and an odd step
     typename SB::Held hb[2];
-    const int64_t first = k_first / kBK, whole = k_end / kBK;
-    const int left = int(k_end - whole * kBK);
-    const int64_t rounds = (whole - first + 3) / 4;
-    int64_t s = whole - rounds * 4;  // the running step; below `first`: an empty one
-
-    // Loads of step s + ahead < s + 4, on the sides that are (not) packed.
-    auto fetch_early = [&](char* lds, int ahead, bool packed) {
+    // Codes of step s + ahead < s + 4.
+    auto codes_early = [&](int ahead) {
       if (s + ahead < first) {
-        if (SA::kPacked == packed) sa.template fetch<true>(lds, ha[ahead & 1], first, 0, tid);
-        if (SB::kPacked == packed) sb.template fetch<true>(lds + SA::kBytes, hb[ahead & 1], first, 0, tid);
+        if (SA::kPacked) sa.template fetch<true>(nullptr, ha[ahead & 1], first, 0, tid);
+        if (SB::kPacked) sb.template fetch<true>(nullptr, hb[ahead & 1], first, 0, tid);
       } else {
-        if (SA::kPacked == packed) sa.template fetch<false>(lds, ha[ahead & 1], s + ahead, 0, tid);
-        if (SB::kPacked == packed) sb.template fetch<false>(lds + SA::kBytes, hb[ahead & 1], s + ahead, 0, tid);
+        if (SA::kPacked) sa.template fetch<false>(nullptr, ha[ahead & 1], s + ahead, 0, tid);
+        if (SB::kPacked) sb.template fetch<false>(nullptr, hb[ahead & 1], s + ahead, 0, tid);
       }
     };
     auto settle = [&](char* lds, int set) {
       sa.settle(lds, ha[set]);
       sb.settle(lds + SA::kBytes, hb[set]);
     };
-    bf16x8 fb[kFN], fa[2];
 
     auto begin = [&](const char* lds) {
 #pragma unroll
@@ -422,22 +492,23 @@ struct Gemm {
       ++s;
     };
 
-    char* const stage[4] = {l0, l1, l2, l3};
     if (left) {
-      sa.template fetch<true>(l3, ha[0], whole, left, tid);
-      sb.template fetch<true>(l3 + SA::kBytes, hb[0], whole, left, tid);
-      settle(l3, 0);
+      lds_barrier();  // the last stage may have served an epilogue
+      typename SA::Held ta;
+      typename SB::Held tb;
+      sa.template fetch<true>(l3, ta, whole, left, tid);
+      sb.template fetch<true>(l3 + SA::kBytes, tb, whole, left, tid);
+      sa.settle(l3, ta);
+      sb.settle(l3 + SA::kBytes, tb);
     }
-    if (rounds > 0) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) fetch_early(stage[i], i, false);
-      if constexpr (kPacked) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) fetch_early(nullptr, i, true);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) settle(stage[i], i);
-#pragma unroll
-        for (int i = 2; i < 4; ++i) fetch_early(nullptr, i, true);
+    if constexpr (kPacked) {
+      if (rounds > 0) {
+        codes_early(0);
+        codes_early(1);
+        settle(l0, 0);
+        settle(l1, 1);
+        codes_early(2);
+        codes_early(3);
       }
     }
     wait_loads<0, true>();
@@ -446,58 +517,119 @@ struct Gemm {
       begin(l3);
       multiply(l3, l3, false, [](int) {}, [] {});
     }
-    if (rounds == 0) return;
-    begin(l0);
-    for (int64_t r = 1; r < rounds; ++r) {
-      step(l0, l1, l2, l3, 0);
-      step(l1, l2, l3, l0, 1);
-      step(l2, l3, l0, l1, 0);
-      step(l3, l0, l1, l2, 1);
+    if (rounds > 0) {
+      begin(l0);
+      for (int64_t r = 1; r < rounds; ++r) {
+        step(l0, l1, l2, l3, 0);
+        step(l1, l2, l3, l0, 1);
+        step(l2, l3, l0, l1, 0);
+        step(l3, l0, l1, l2, 1);
+      }
+      wait_loads<kAfter, kPacked>();
+      bare_barrier();
+      multiply(l0, l1, true, [&](int i) { load(l3, i); }, [&] { settle(l2, 0); });
+      wait_loads<SA::kLoads + SB::kLoads, kPacked>();  // what was started after step i + 1's: codes and the last step's
+      bare_barrier();
+      multiply(l1, l2, true, [](int) {}, [&] { settle(l3, 1); });
+      wait_loads<0, kPacked>();
+      bare_barrier();
+      multiply(l2, l3, true, [](int) {}, [] {});
+      multiply(l3, l3, false, [](int) {}, [] {});
     }
-    wait_loads<kAfter, kPacked>();
-    bare_barrier();
-    multiply(l0, l1, true, [&](int i) { load(l3, i); }, [&] { settle(l2, 0); });
-    wait_loads<SA::kLoads + SB::kLoads, kPacked>();  // what was started after step i + 1's: codes and the last step's
-    bare_barrier();
-    multiply(l1, l2, true, [](int) {}, [&] { settle(l3, 1); });
-    wait_loads<0, kPacked>();
-    bare_barrier();
-    multiply(l2, l3, true, [](int) {}, [] {});
-    multiply(l3, l3, false, [](int) {}, [] {});
+    lds_barrier();
   }
 
-  // f(m, n, values of columns n .. n+3) for every group of four this wave
-  // holds.  The groups pass through this wave's 16 rows of LDS (the stages are
-  // free by then), so that 16 lanes hand over 64 neighbouring columns of a row;
-  // group g of row r is kept at g ^ r, which spreads the rows over the banks.
-  template <typename F>
-  __device__ __forceinline__ void each(int64_t m0, int64_t n0, char* lds, F f) {
-    constexpr int kCols = BN / WN, kGroups = kCols / 4, kMask = kGroups - 1;
-    static_assert(WM * WN * 16 * kCols * 4 <= kStage && (kGroups & kMask) == 0, "epilogue rows");
+  // f(row, column, values of 8 columns from that one) for every group of eight
+  // this wave holds, rows and columns counted in the tile.  The groups pass
+  // through this wave's 16 rows of the last stage, so that the lanes hand over
+  // neighbouring columns of a row; the 16 bytes g of row r are kept at g ^ r,
+  // which spreads the rows over the banks.
+  template <bool UNROLL, typename F>
+  __device__ __forceinline__ void each(char* lds, F f) {
+    constexpr int kCols = BN / WN, kQuads = kCols / 4, kMask = kQuads - 1, kGroups = kCols / 8;
+    static_assert(WM * WN * 16 * kCols * 4 <= kStage && (kQuads & kMask) == 0, "epilogue rows");
     float* rows = reinterpret_cast<float*>(lds) + wave_index() * 16 * kCols;
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kFM; ++i) {
       const int w = lane & 15;
 #pragma unroll
       for (int j = 0; j < kFN; ++j)
         *reinterpret_cast<f32x4v*>(rows + w * kCols + ((4 * j + (lane >> 4)) ^ (w & kMask)) * 4) = acc[i][j];
-#pragma unroll 1
-      for (int q = lane; q < 16 * kGroups; q += 64) {
+      wave_order();
+      auto group = [&](int q) {
         const int r = q / kGroups, c = q % kGroups;
-        f(m0 + wm * (BM / WM) + i * 16 + r, n0 + wn * kCols + c * 4,
-          *reinterpret_cast<const f32x4v*>(rows + r * kCols + (c ^ (r & kMask)) * 4));
+        f(wm * (BM / WM) + i * 16 + r, wn * kCols + c * 8,
+          *reinterpret_cast<const f32x4v*>(rows + r * kCols + ((2 * c) ^ (r & kMask)) * 4),
+          *reinterpret_cast<const f32x4v*>(rows + r * kCols + ((2 * c + 1) ^ (r & kMask)) * 4));
+      };
+      if constexpr (UNROLL && 16 * kGroups % 64 == 0) {
+#pragma unroll
+        for (int q = 0; q < 16 * kGroups / 64; ++q) group(lane + 64 * q);
+      } else {
+#pragma unroll 1
+        for (int q = lane; q < 16 * kGroups; q += 64) group(q);
       }
+      wave_order();
+    }
+  }
+
+  // Writes the tile at (m0, n0) to `t`.
+  __device__ __forceinline__ void write(const Target& t, int64_t m0, int64_t n0, char* lds) {
+    const bool vec = (reinterpret_cast<uintptr_t>(t.base) & 15) == 0 && t.ld % (t.f32 ? 4 : 8) == 0 &&
+                     (t.add == nullptr || ((reinterpret_cast<uintptr_t>(t.add) & 15) == 0 && t.ld % 4 == 0));
+    if (vec && m0 + BM <= t.rows && n0 + BN <= t.cols) {
+      each<true>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) {
+        const int64_t row = t.row_map ? t.row_map[m0 + r] : m0 + r, at = row * t.ld + n0 + c;
+        if (t.add) {
+          lo = add4(*reinterpret_cast<const f32x4v*>(t.add + at), lo);
+          hi = add4(*reinterpret_cast<const f32x4v*>(t.add + at + 4), hi);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          lo[j] = t.alpha * lo[j];
+          hi[j] = t.alpha * hi[j];
+        }
+        if (t.f32) {
+          float* d = static_cast<float*>(t.base) + at;
+          if (t.accumulate) {
+            lo = add4(*reinterpret_cast<const f32x4v*>(d), lo);
+            hi = add4(*reinterpret_cast<const f32x4v*>(d + 4), hi);
+          }
+          *reinterpret_cast<f32x4v*>(d) = lo;
+          *reinterpret_cast<f32x4v*>(d + 4) = hi;
+        } else {
+          u32x4* d = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(t.base) + at);
+          if (t.accumulate) {
+            const u32x4 o = *d;
+            lo = add4(f32x4v{low_bf16(o[0]), high_bf16(o[0]), low_bf16(o[1]), high_bf16(o[1])}, lo);
+            hi = add4(f32x4v{low_bf16(o[2]), high_bf16(o[2]), low_bf16(o[3]), high_bf16(o[3])}, hi);
+          }
+          *d = u32x4{two_bf16(lo[0], lo[1]), two_bf16(lo[2], lo[3]), two_bf16(hi[0], hi[1]), two_bf16(hi[2], hi[3])};
+        }
+      });
+    } else {
+      each<false>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) {
+        const int64_t m = m0 + r, n = n0 + c;
+        if (m >= t.rows) return;
+        const int64_t row = t.row_map ? t.row_map[m] : m, at = row * t.ld + n;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (n + j >= t.cols) continue;
+          float v = j < 4 ? lo[j & 3] : hi[j & 3];
+          if (t.add) v = t.add[at + j] + v;
+          v = t.alpha * v;
+          if (t.f32) {
+            float* d = static_cast<float*>(t.base) + at + j;
+            *d = t.accumulate ? *d + v : v;
+          } else {
+            uint16_t* d = static_cast<uint16_t*>(t.base) + at + j;
+            *d = uint16_t(bf16_bits_of(t.accumulate ? low_bf16(*d) + v : v));
+          }
+        }
+      });
     }
   }
 };
-
-__device__ __forceinline__ uint32_t bf16_bits_of(float v) {
-  const __bf16 b = __bf16(v);  // round to nearest even
-  uint16_t r;
-  __builtin_memcpy(&r, &b, 2);
-  return r;
-}
 
 // alpha s (+ old) for the `n` values v of one row from element `at`, rounded
 // once to the output's type (fp32 or bf16).
@@ -562,10 +694,12 @@ __device__ __forceinline__ f32x4v sum_splits(const float* partial, int32_t split
   return s;
 }
 
-// Workgroups go round-robin over the 8 XCDs, each with an L2 of its own: XCD x
-// takes a contiguous share of the tiles, in an order that walks `group` tile
-// rows before it moves to the next tile column, so that what an XCD works on
-// at one time shares operand tiles.
+// Workgroups go round-robin over the 8 XCDs, each with an L2 of its own, and
+// take every gridDim-th item (gridDim is a multiple of 8 or no smaller than the
+// items): XCD x takes a contiguous share of the tiles, in an order that walks
+// `group` tile rows before it moves to the next tile column, so that what an XCD
+// works on at one time shares operand tiles.  (A group of 4 measured against 2,
+// 8 and 16 on 4096 x 128000 x 4096: 1.5%, 1.5% and 6% faster.)
 __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n, uint32_t group, uint32_t* tm,
                                         uint32_t* tn) {
   const uint32_t total = tiles_m * tiles_n, x = bid & 7, each = total >> 3, more = total & 7;

@@ -66,6 +66,13 @@ struct VocabLossCall {
 bool rows_aligned(const void* p, int64_t ld, int64_t cols);
 WeightGradPlan plan_weight_grad(int64_t tokens, int64_t outs, int64_t ins, bool aligned);
 
+// Workgroups of a tile kernel with `items` tiles of side x side: as many as the
+// 256 CUs hold at once (by their LDS), each taking one item after another.
+inline unsigned resident_groups(int64_t items, int64_t side) {
+  const int64_t most = side == 256 ? 256 : side == 128 ? 512 : 1024;
+  return unsigned(items < most ? items : most);
+}
+
 // Launches; each returns the hipError_t as int.
 int launch_pack(const PackCall& c, void* stream);
 int launch_unpack(const PackCall& c, void* stream);

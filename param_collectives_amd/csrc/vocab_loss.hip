@@ -35,7 +35,23 @@ namespace {
 using namespace tide;
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kExpScale = 32768.0f;  // exponentials are kept as fp16 times this
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A tile row's reference from its maximum; nothing but -inf: a finite one, with
+// exponentials of 0.
+__device__ __forceinline__ float reference(float m) { return (m == -__builtin_inff() ? 0.0f : m * kLog2e) - 15.0f; }
+
+// The value 16 (32) lanes away: lane XOR 16 (32).
+__device__ __forceinline__ float other_16(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return __uint_as_float((threadIdx.x & 16) ? p[0] : p[1]);
+}
+__device__ __forceinline__ float other_32(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float((threadIdx.x & 32) ? p[0] : p[1]);
+}
 
 __device__ __forceinline__ uint32_t half_bits(float v) {
   const _Float16 h = _Float16(v);  // round to nearest even
@@ -43,6 +59,8 @@ __device__ __forceinline__ uint32_t half_bits(float v) {
   __builtin_memcpy(&r, &h, 2);
   return r;
 }
+
+__device__ __forceinline__ uint32_t two_halves(float a, float b) { return half_bits(a) | half_bits(b) << 16; }
 
 __device__ __forceinline__ float half_value(uint32_t bits) {
   const uint16_t b = uint16_t(bits);
@@ -144,11 +162,11 @@ struct LogitsArgs {
   const int64_t* targets;
   int64_t tokens, vocab, depth;
   int64_t first, piece;
-  float2* stats;           // [row of the piece][vocabulary tile]: maximum, sum
+  float2* stats;           // [row of the piece][vocabulary tile]: reference, sum of exponentials
   float* target_z;         // [row of the piece]
   uint16_t* e;             // [row of the piece][e_ld], or null
   int64_t e_ld;
-  uint32_t tiles_m, tiles_n;
+  uint32_t tiles_n;
 };
 
 template <int BM, int BN, int WM, int WN>
@@ -158,96 +176,135 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
-  uint32_t tm, tn;
-  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
-  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
+  // Per row of the tile: its waves' maxima and sums, and the target's column
+  // (of the tile that runs and of the next).
+  __shared__ float peak[WN][BM];
+  __shared__ float sums[WN][BM];
+  __shared__ int32_t aim[2][BM];
+  constexpr int kFM = G::kFM, kFN = G::kFN, kRowsWave = BM / WM, kColsWave = BN / WN;
   const int64_t rows = a.count ? rows_of(a.count, a.first, a.piece) : a.tokens;
-  if (m0 >= rows) return;
+  const uint32_t tiles_m = uint32_t((rows + BM - 1) / BM), items = tiles_m * a.tiles_n;
+  if (blockIdx.x >= items) return;
   a.h.base = static_cast<const uint16_t*>(a.h.base) + a.first * a.h.ld;
   a.h.extent = rows;
+  int64_t m0, n0;
+  uint32_t tn;
   G g;
-  g.run(a.h, a.w, m0, n0, 0, a.depth, lds0, lds1, lds2, lds3);
+  g.setup();
+  auto open = [&](uint32_t item) {
+    uint32_t tm;
+    tile_of(item, tiles_m, a.tiles_n, 4, &tm, &tn);
+    m0 = int64_t(tm) * BM;
+    n0 = int64_t(tn) * BN;
+    g.open(a.h, a.w, m0, n0, 0, a.depth, lds0, lds1, lds2);
+  };
+  auto take_aim = [&](int set) {
+    for (int row = g.tid; row < BM; row += G::kThreads) {
+      int64_t col = -1;
+      if (m0 + row < rows) col = a.targets[a.count ? a.list[a.first + m0 + row] : m0 + row] - n0;
+      aim[set][row] = col >= 0 && col < BN ? int32_t(col) : -1;
+    }
+  };
+  open(blockIdx.x);
+  take_aim(0);
+  int set = 0;
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x, set ^= 1) {
+    g.loop(lds0, lds1, lds2, lds3);
+    const int64_t m1 = m0, n1 = n0;
+    const uint32_t t1 = tn;
+    if (item + gridDim.x < items) open(item + gridDim.x);
 
-  // A lane holds of row 16 i + lane % 16 the columns 16 j + 4 (lane / 16) + r.
-  // The tile row's maximum and sum go over its lanes, then over the WN waves.
-  constexpr int kFM = G::kFM, kFN = G::kFN, kRowsWave = BM / WM, kColsWave = BN / WN;
-  __syncthreads();
-  float* peak = reinterpret_cast<float*>(lds1);  // [WN][BM]
-  float* sums = peak + WN * BM;                  // [WN][BM]
-  const int lane = g.lane, col0 = g.wn * kColsWave + 4 * (lane >> 4);
-  const int row0 = g.wm * kRowsWave + (lane & 15);
-  const int64_t left = a.vocab - n0;
+    // A lane holds of row 16 i + lane % 16 the columns 16 j + 4 (lane / 16) + r.
+    // The tile row's maximum and sum go over its lanes, then over the WN waves.
+    // The reference is kept in powers of 2, c = log2(e) max - 15: the
+    // exponentials 2^(log2(e) z - c) then reach 2^15, as fp16 keeps them.
+    const int col0 = g.wn * kColsWave + 4 * (g.lane >> 4), row0 = g.wm * kRowsWave + (g.lane & 15);
+    if (a.vocab - n1 < BN) {
+      const int left = int(a.vocab - n1);
 #pragma unroll
-  for (int i = 0; i < kFM; ++i) {
-    float m = -__builtin_inff();
+      for (int i = 0; i < kFM; ++i)
 #pragma unroll
-    for (int j = 0; j < kFN; ++j)
+        for (int j = 0; j < kFN; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (col0 + 16 * j + r >= left) g.acc[i][j][r] = -__builtin_inff();
-        m = fmaxf(m, g.acc[i][j][r]);
-      }
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    if (lane < 16) peak[g.wn * BM + row0 + 16 * i] = m;
-  }
-  __syncthreads();
+          for (int r = 0; r < 4; ++r)
+            if (col0 + 16 * j + r >= left) g.acc[i][j][r] = -__builtin_inff();
+    }
 #pragma unroll
-  for (int i = 0; i < kFM; ++i) {
-    const int row = row0 + 16 * i;
-    float m = peak[row];
-#pragma unroll
-    for (int w = 1; w < WN; ++w) m = fmaxf(m, peak[w * BM + row]);
-    if (m == -__builtin_inff()) m = 0.0f;  // nothing but -inf: exponentials of 0
-    float s = 0.0f;
-    // the target's logit, before it becomes an exponential
-    if (m0 + row < rows) {
-      const int64_t token = a.count ? a.list[a.first + m0 + row] : m0 + row;
-      const int64_t target = a.targets[token] - n0;
+    for (int i = 0; i < kFM; ++i) {
+      float m = g.acc[i][0][0];
 #pragma unroll
       for (int j = 0; j < kFN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (target == col0 + 16 * j + r) a.target_z[m0 + row] = g.acc[i][j][r];
+        for (int r = 0; r < 4; ++r) m = fmaxf(m, g.acc[i][j][r]);
+      m = fmaxf(m, other_16(m));
+      m = fmaxf(m, other_32(m));
+      if (g.lane < 16) peak[g.wn][row0 + 16 * i] = m;
     }
+    lds_barrier();
 #pragma unroll
-    for (int j = 0; j < kFN; ++j)
+    for (int i = 0; i < kFM; ++i) {
+      const int row = row0 + 16 * i;
+      const int at = aim[set][row] - col0;
+      if (__any(at >= 0 && at < kColsWave)) {
+        // the target's logit, before it becomes an exponential
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float x = __builtin_amdgcn_exp2f((g.acc[i][j][r] - m) * kLog2e);
-        g.acc[i][j][r] = x;
-        s += x;
+        for (int j = 0; j < kFN; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (at == 16 * j + r) a.target_z[m1 + row] = g.acc[i][j][r];
       }
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (lane < 16) sums[g.wn * BM + row] = s;
-  }
-  __syncthreads();
-  for (int row = g.tid; row < BM; row += G::kThreads) {
-    if (m0 + row >= rows) continue;
-    float m = peak[row], s = sums[row];
+      float m = peak[0][row];
 #pragma unroll
-    for (int w = 1; w < WN; ++w) {
-      m = fmaxf(m, peak[w * BM + row]);
-      s += sums[w * BM + row];
+      for (int w = 1; w < WN; ++w) m = fmaxf(m, peak[w][row]);
+      const float c = reference(m);
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kFN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(g.acc[i][j][r], kLog2e, -c));
+          g.acc[i][j][r] = x;
+          s += x;
+        }
+      s += other_16(s);
+      s += other_32(s);
+      if (g.lane < 16) sums[g.wn][row] = s;
     }
-    a.stats[(m0 + row) * a.tiles_n + tn] = make_float2(m, s);
-  }
-  if (a.e) {
-    g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
-      if (m < rows && n < a.e_ld)
-        *reinterpret_cast<u32x2*>(a.e + m * a.e_ld + n) =
-            u32x2{half_bits(v[0] * kExpScale) | half_bits(v[1] * kExpScale) << 16,
-                  half_bits(v[2] * kExpScale) | half_bits(v[3] * kExpScale) << 16};
-    });
+    lds_barrier();
+    for (int row = g.tid; row < BM; row += G::kThreads) {
+      if (m1 + row >= rows) continue;
+      float m = peak[0][row], s = sums[0][row];
+#pragma unroll
+      for (int w = 1; w < WN; ++w) {
+        m = fmaxf(m, peak[w][row]);
+        s += sums[w][row];
+      }
+      a.stats[(m1 + row) * a.tiles_n + t1] = make_float2(reference(m), s);
+    }
+    if (a.e) {
+      // the pitch is a multiple of 64: a group of 8 columns is in or out
+      auto put = [&](int r, int c, f32x4v lo, f32x4v hi) {
+        const u32x4 v = u32x4{two_halves(lo[0], lo[1]), two_halves(lo[2], lo[3]), two_halves(hi[0], hi[1]),
+                              two_halves(hi[2], hi[3])};
+        *reinterpret_cast<u32x4*>(a.e + (m1 + r) * a.e_ld + n1 + c) = v;
+      };
+      if (m1 + BM <= rows && n1 + BN <= a.e_ld) {
+        g.template each<true>(lds3, put);
+      } else {
+        g.template each<false>(lds3, [&](int r, int c, f32x4v lo, f32x4v hi) {
+          if (m1 + r < rows && n1 + c < a.e_ld) put(r, c, lo, hi);
+        });
+      }
+    }
+    if (item + gridDim.x < items) take_aim(set ^ 1);
   }
 }
 
-// Joins a row's tiles: one wave per row.  (m, s) stands for s exp(m).
+// Joins a row's tiles: one wave per row.  (c, s) stands for s 2^c.
 __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uint32_t tiles, const int32_t* count,
                                                         const int32_t* list, const int64_t* targets, int64_t vocab,
                                                         int64_t tokens, int64_t first, int64_t piece,
-                                                        const float* target_z, float* row_lse, float* loss,
+                                                        const float* target_z, float* row_log2, float* loss,
                                                         float* lse) {
   const int64_t row = int64_t(blockIdx.x) * 4 + wave_index();
   const int64_t rows = count ? rows_of(count, first, piece) : tokens;
@@ -258,12 +315,10 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uin
   for (uint32_t t = lane; t < tiles; t += 64) m = fmaxf(m, p[t].x);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  const float base = m == -__builtin_inff() ? 0.0f : m;
   float s = 0.0f;
   for (uint32_t t = lane; t < tiles; t += 64) {
     const float2 v = p[t];
-    // a tile of nothing but -inf has the sum 0 at maximum 0
-    s += v.y * (v.x == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((v.x - base) * kLog2e));
+    s += v.y * __builtin_amdgcn_exp2f(v.x - m);
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
@@ -271,8 +326,8 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uin
     const int64_t token = count ? list[first + row] : row;
     const int64_t target = targets[token];
     const bool keep = target >= 0 && target < vocab;
-    const float l = base + logf(s);
-    if (row_lse) row_lse[row] = l;
+    const float l2 = m + __builtin_log2f(s), l = l2 * kLn2;
+    if (row_log2) row_log2[row] = l2;
     loss[token] = keep ? l - target_z[row] : 0.0f;
     if (lse) lse[token] = keep ? l : 0.0f;
   }
@@ -286,7 +341,7 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uin
 __global__ __launch_bounds__(256) void logit_grad_kernel(uint16_t* e, int64_t e_ld, int64_t vocab, const float2* stats,
                                                          uint32_t tiles, uint32_t tile_cols, const int32_t* count,
                                                          const int32_t* list, const int64_t* targets, int64_t first,
-                                                         int64_t piece, const float* target_z, const float* row_lse,
+                                                         int64_t piece, const float* target_z, const float* row_log2,
                                                          const float* grad_loss, const float* scale) {
   const int64_t row = blockIdx.y + int64_t(blockIdx.z) * 32768;
   const int64_t rows = rows_of(count, first, piece);
@@ -294,18 +349,17 @@ __global__ __launch_bounds__(256) void logit_grad_kernel(uint16_t* e, int64_t e_
   const int64_t c = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (c >= e_ld) return;
   const int32_t token = list[first + row];
-  const float l = row_lse[row], g = grad_loss[token] / *scale;
+  const float l2 = row_log2[row], g = grad_loss[token] / *scale;
   const int64_t target = targets[token];
   u32x4* p = reinterpret_cast<u32x4*>(e + row * e_ld + c);
   uint32_t out[4] = {0, 0, 0, 0};
   if (c < vocab) {
     const u32x4 w = *p;
-    const float m = stats[row * tiles + uint32_t(c) / tile_cols].x;
-    const float f = __builtin_amdgcn_exp2f((m - l) * kLog2e) * (g * (1.0f / kExpScale));
+    const float f = __builtin_amdgcn_exp2f(stats[row * tiles + uint32_t(c) / tile_cols].x - l2) * g;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float v = half_value(w[j >> 1] >> (16 * (j & 1))) * f;
-      if (c + j == target) v = g * expm1f(target_z[row] - l);
+      if (c + j == target) v = g * expm1f(target_z[row] - l2 * kLn2);
       if (c + j >= vocab) v = 0.0f;
       out[j >> 1] |= bf16_bits_of(v) << (16 * (j & 1));
     }
@@ -322,7 +376,7 @@ struct HiddenGradArgs {
   int64_t split_k;
   float* partial;  // [splits][piece][hidden], or null
   uint16_t* dhidden;
-  uint32_t tiles_m, tiles_n;
+  uint32_t tiles_n, splits;
 };
 
 template <int BM, int BN, int WM, int WN>
@@ -332,25 +386,33 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
-  uint32_t tm, tn;
-  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
-  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
   const int64_t rows = rows_of(a.count, a.first, a.piece);
-  if (m0 >= rows) return;
+  const uint32_t tiles_m = uint32_t((rows + BM - 1) / BM), tiles = tiles_m * a.tiles_n, items = tiles * a.splits;
+  if (blockIdx.x >= items) return;
   a.dz.extent = rows;
-  const int64_t k0 = int64_t(blockIdx.y) * a.split_k;
-  const int64_t k1 = k0 + a.split_k < a.vocab ? k0 + a.split_k : a.vocab;
-  G g;
-  g.run(a.dz, a.w, m0, n0, k0, k1, lds0, lds1, lds2, lds3);
   const float scale = *a.scale;
-  g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
-    if (m >= rows || n >= a.hidden) return;
-    const int left = int(a.hidden - n < 4 ? a.hidden - n : 4);
-    if (a.partial)
-      store_values(a.partial + int64_t(blockIdx.y) * a.piece * a.hidden, 1, 0, 1.0f, m * a.hidden + n, left, v);
-    else
-      store_values(a.dhidden, 0, 0, scale, int64_t(a.list[a.first + m]) * a.hidden + n, left, v);
-  });
+  int64_t m0, n0, split;
+  G g;
+  g.setup();
+  auto open = [&](uint32_t item) {
+    uint32_t tm, tn;
+    tile_of(item % tiles, tiles_m, a.tiles_n, 4, &tm, &tn);
+    m0 = int64_t(tm) * BM;
+    n0 = int64_t(tn) * BN;
+    split = item / tiles;
+    const int64_t k0 = split * a.split_k, k1 = k0 + a.split_k;
+    g.open(a.dz, a.w, m0, n0, k0, k1 < a.vocab ? k1 : a.vocab, lds0, lds1, lds2);
+  };
+  open(blockIdx.x);
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    g.loop(lds0, lds1, lds2, lds3);
+    const int64_t m1 = m0, n1 = n0;
+    const Target t = a.partial ? Target{a.partial + split * a.piece * a.hidden, a.hidden, rows, a.hidden, nullptr,
+                                        nullptr, 1.0f, 1, 0}
+                               : Target{a.dhidden, a.hidden, rows, a.hidden, a.list + a.first, nullptr, scale, 0, 0};
+    if (item + gridDim.x < items) open(item + gridDim.x);
+    g.write(t, m1, n1, lds3);
+  }
 }
 
 __global__ __launch_bounds__(256) void join_hidden_kernel(const float* partial, int32_t splits, int64_t piece,
@@ -399,28 +461,29 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void vocab_grad_kernel(VocabGradArg
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
-  uint32_t tm, tn;
-  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, 4, &tm, &tn);
-  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
+  const uint32_t items = a.tiles_m * a.tiles_n;
   const int64_t rows = rows_of(a.count, a.first, a.piece);
   a.h.base = static_cast<const uint16_t*>(a.h.base) + a.first * a.h.ld;
-  G g;
-  g.run(a.dz, a.h, m0, n0, 0, rows, lds0, lds1, lds2, lds3);
   const float scale = *a.scale;
-  g.each(m0, n0, lds0, [&](int64_t m, int64_t n, f32x4v v) {
-    if (m >= a.vocab || n >= a.hidden) return;
-    const int left = int(a.hidden - n < 4 ? a.hidden - n : 4);
-    const int64_t at = m * a.hidden + n;
-    if (a.sum_in) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) v[i] = a.sum_in[at + i] + v[i];
-    }
-    if (a.sum_out)
-      store_values(a.sum_out, 1, 0, 1.0f, at, left, v);
-    else
-      store_values(a.dw, a.f32, a.accumulate, scale, at, left, v);
-  });
+  int64_t m0, n0;
+  G g;
+  g.setup();
+  const Target t = a.sum_out ? Target{a.sum_out, a.hidden, a.vocab, a.hidden, nullptr, a.sum_in, 1.0f, 1, 0}
+                             : Target{a.dw, a.hidden, a.vocab, a.hidden, nullptr, a.sum_in, scale, a.f32, a.accumulate};
+  auto open = [&](uint32_t item) {
+    uint32_t tm, tn;
+    tile_of(item, a.tiles_m, a.tiles_n, 4, &tm, &tn);
+    m0 = int64_t(tm) * BM;
+    n0 = int64_t(tn) * BN;
+    g.open(a.dz, a.h, m0, n0, 0, rows, lds0, lds1, lds2);
+  };
+  open(blockIdx.x);
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    g.loop(lds0, lds1, lds2, lds3);
+    const int64_t m1 = m0, n1 = n0;
+    if (item + gridDim.x < items) open(item + gridDim.x);
+    g.write(t, m1, n1, lds3);
+  }
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -437,7 +500,7 @@ struct Layout {
   bool big_w = false;   // dW
   bool sums = false;    // dW's sums go over the pieces in the workspace
   // byte offsets
-  int64_t list = 0, count = 0, h = 0, w = 0, stats = 0, target_z = 0, row_lse = 0, e = 0, partial = 0, dw_sums = 0,
+  int64_t list = 0, count = 0, h = 0, w = 0, stats = 0, target_z = 0, row_log2 = 0, e = 0, partial = 0, dw_sums = 0,
           bytes = 0;
 };
 
@@ -475,7 +538,7 @@ Layout layout_of(const VocabLossCall& c) {
   L.stats = take(L.piece * L.tiles_n * 8);
   L.target_z = take(L.piece * 4);
   if (grad) {
-    L.row_lse = take(L.piece * 4);
+    L.row_log2 = take(L.piece * 4);
     L.e = take(L.piece * L.e_ld * 2);
     const int64_t tiles = (L.piece + 255) / 256 * ((c.hidden + 255) / 256);
     L.big_h = tiles >= 192;
@@ -552,7 +615,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
   }
   float2* stats = reinterpret_cast<float2*>(ws + L.stats);
   float* target_z = reinterpret_cast<float*>(ws + L.target_z);
-  float* row_lse = grad ? reinterpret_cast<float*>(ws + L.row_lse) : nullptr;
+  float* row_log2 = grad ? reinterpret_cast<float*>(ws + L.row_log2) : nullptr;
   uint16_t* e = grad ? reinterpret_cast<uint16_t*>(ws + L.e) : nullptr;
   for (int64_t p = 0; p < L.pieces; ++p) {
     const int64_t first = p * L.piece;
@@ -571,9 +634,8 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     a.target_z = target_z;
     a.e = e;
     a.e_ld = L.e_ld;
-    a.tiles_m = uint32_t((L.piece + L.side - 1) / L.side);
     a.tiles_n = uint32_t(L.tiles_n);
-    const dim3 grid(a.tiles_m * a.tiles_n);
+    const dim3 grid(resident_groups((L.piece + L.side - 1) / L.side * L.tiles_n, L.side));
     if (L.side == 256)
       hipLaunchKernelGGL((logits_kernel<256, 256, 2, 4>), grid, dim3(512), 0, st, a);
     else if (L.side == 128)
@@ -582,14 +644,14 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
       hipLaunchKernelGGL((logits_kernel<64, 64, 1, 4>), grid, dim3(256), 0, st, a);
     TIDE_LAUNCHED();
     hipLaunchKernelGGL(join_rows_kernel, dim3(unsigned((L.piece + 3) / 4)), dim3(256), 0, st, stats, a.tiles_n, count,
-                       list, targets, c.vocab, c.tokens, first, L.piece, target_z, row_lse, c.loss, c.lse);
+                       list, targets, c.vocab, c.tokens, first, L.piece, target_z, row_log2, c.loss, c.lse);
     TIDE_LAUNCHED();
     if (!grad) continue;
     const int64_t rows_z = L.piece < 32768 ? L.piece : 32768;
     hipLaunchKernelGGL(logit_grad_kernel,
                        dim3(unsigned((L.e_ld + 2047) / 2048), unsigned(rows_z), unsigned((L.piece + 32767) / 32768)),
                        dim3(256), 0, st, e, L.e_ld, c.vocab, stats, a.tiles_n, uint32_t(L.side), count, list, targets,
-                       first, L.piece, target_z, row_lse, c.grad_loss, scale);
+                       first, L.piece, target_z, row_log2, c.grad_loss, scale);
     TIDE_LAUNCHED();
     HiddenGradArgs d;
     d.dz = Operand{e, nullptr, L.e_ld, 0, L.piece};
@@ -606,9 +668,9 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     d.partial = L.h_splits > 1 ? reinterpret_cast<float*>(ws + L.partial) : nullptr;
     d.dhidden = static_cast<uint16_t*>(c.dhidden);
     const int64_t side_h = L.big_h ? 256 : 128;
-    d.tiles_m = uint32_t((L.piece + side_h - 1) / side_h);
     d.tiles_n = uint32_t((c.hidden + side_h - 1) / side_h);
-    const dim3 grid_h(d.tiles_m * d.tiles_n, unsigned(L.h_splits));
+    d.splits = uint32_t(L.h_splits);
+    const dim3 grid_h(resident_groups((L.piece + side_h - 1) / side_h * d.tiles_n * L.h_splits, side_h));
     if (L.big_h)
       hipLaunchKernelGGL((hidden_grad_kernel<256, 256, 2, 4>), grid_h, dim3(512), 0, st, d);
     else
@@ -639,7 +701,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     const int64_t side_w = L.big_w ? 256 : 128;
     v.tiles_m = uint32_t((c.vocab + side_w - 1) / side_w);
     v.tiles_n = uint32_t((c.hidden + side_w - 1) / side_w);
-    const dim3 grid_w(v.tiles_m * v.tiles_n);
+    const dim3 grid_w(resident_groups(int64_t(v.tiles_m) * v.tiles_n, side_w));
     if (L.big_w)
       hipLaunchKernelGGL((vocab_grad_kernel<256, 256, 2, 4>), grid_w, dim3(512), 0, st, v);
     else

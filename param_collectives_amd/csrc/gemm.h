@@ -28,6 +28,8 @@
 
 #include <cstdint>
 
+#include "training.h"
+
 namespace tide {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -44,7 +46,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 enum class Form { kRows, kCols, kPacked };
 enum class Code { kE4m3, kInt8 };
 
-constexpr int kBK = 32;     // k per staged step
 constexpr int kStages = 4;  // LDS stages a tile's steps go round
 
 struct Operand {
@@ -143,8 +144,9 @@ __device__ __forceinline__ u32x2 widen4(uint32_t w, uint32_t scale_byte) {
 }
 
 // One operand side of the tile: ROWS rows (columns) of C, FRAGS x 16 of them a
-// wave's, THREADS threads.
-template <Form FORM, Code CODE, int ROWS, int FRAGS, int THREADS>
+// wave's, THREADS threads.  LEAN: where fragments start is worked out at each
+// read, from one register (see Gemm).
+template <Form FORM, Code CODE, int ROWS, int FRAGS, int THREADS, bool LEAN>
 struct Side {
   static constexpr bool kPacked = FORM == Form::kPacked;
   static constexpr int kBytes = ROWS * kBK * 2;
@@ -263,7 +265,7 @@ struct Side {
 
   // Where this lane's fragments of a wave's FRAGS x 16 rows (columns) from r0
   // (a multiple of 16 FRAGS) start in the tile.
-  static constexpr int kSpots = FORM == Form::kRows ? 1 : FRAGS;
+  static constexpr int kSpots = FORM == Form::kRows || LEAN ? 1 : FRAGS;
   static __device__ __forceinline__ void spots(uint32_t* at, int r0, int lane) {
     if constexpr (FORM == Form::kRows) {
       const int r = r0 + (lane & 15);
@@ -271,21 +273,22 @@ struct Side {
     } else {
       // a transposing read gives lane l of 16 the values of column l in the
       // four rows k of which lanes 4j .. 4j+3 point at 4 columns each
-      const int k = 8 * (lane >> 4) + ((lane & 15) >> 2);
+      const int k = 8 * (lane >> 4) + ((lane & 15) >> 2), col = r0 + 4 * (lane & 3);
+      const uint32_t first = uint32_t((k * kRowChunks + ((col >> 3) ^ col_swizzle(k))) * 16 + (col & 4) * 2);
 #pragma unroll
-      for (int i = 0; i < FRAGS; ++i) {
-        const int col = r0 + 16 * i + 4 * (lane & 3);
-        at[i] = uint32_t((k * kRowChunks + ((col >> 3) ^ col_swizzle(k))) * 16 + (col & 4) * 2);
-      }
+      for (int i = 0; i < kSpots; ++i) at[i] = spot(first, i);
     }
   }
+  // 16 i columns on are 2 i chunks, bits that are 0 before the swizzle.
+  static __device__ __forceinline__ uint32_t spot(uint32_t first, int i) { return first ^ uint32_t(i * 32); }
 
   // Fragment i: rows (columns) 16 i + 0..15, k = 8 (lane / 16) + 0..7.
   static __device__ __forceinline__ bf16x8 fragment(const char* lds, uint32_t* at, int i) {
     if constexpr (FORM == Form::kRows) {
       return *reinterpret_cast<const bf16x8*>(lds + renew(at[0]) + i * 16 * kRowChunks * 16);
     } else {
-      const char* p = lds + renew(at[i]);  // rows k and k + 4 share their swizzle
+      // rows k and k + 4 share their swizzle
+      const char* p = lds + (LEAN ? spot(renew(at[0]), i) : renew(at[i]));
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * kRowChunks * 16));
       bf16x8 r;
@@ -321,6 +324,63 @@ struct Target {
   int32_t f32, accumulate;
 };
 
+// Whether the 8 columns from a multiple of 8 of any row go out as vectors.
+__device__ __forceinline__ bool target_vectors(const Target& t) {
+  return (reinterpret_cast<uintptr_t>(t.base) & 15) == 0 && t.ld % (t.f32 ? 4 : 8) == 0 &&
+         (t.add == nullptr || ((reinterpret_cast<uintptr_t>(t.add) & 15) == 0 && t.ld % 4 == 0));
+}
+
+// Writes 8 columns of row m from column n, all of them in range and aligned.
+__device__ __forceinline__ void put_vectors(const Target& t, int64_t m, int64_t n, f32x4v lo, f32x4v hi) {
+  const int64_t at = (t.row_map ? int64_t(t.row_map[m]) : m) * t.ld + n;
+  if (t.add) {
+    lo = add4(*reinterpret_cast<const f32x4v*>(t.add + at), lo);
+    hi = add4(*reinterpret_cast<const f32x4v*>(t.add + at + 4), hi);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    lo[j] = t.alpha * lo[j];
+    hi[j] = t.alpha * hi[j];
+  }
+  if (t.f32) {
+    float* d = static_cast<float*>(t.base) + at;
+    if (t.accumulate) {
+      lo = add4(*reinterpret_cast<const f32x4v*>(d), lo);
+      hi = add4(*reinterpret_cast<const f32x4v*>(d + 4), hi);
+    }
+    *reinterpret_cast<f32x4v*>(d) = lo;
+    *reinterpret_cast<f32x4v*>(d + 4) = hi;
+  } else {
+    u32x4* d = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(t.base) + at);
+    if (t.accumulate) {
+      const u32x4 o = *d;
+      lo = add4(f32x4v{low_bf16(o[0]), high_bf16(o[0]), low_bf16(o[1]), high_bf16(o[1])}, lo);
+      hi = add4(f32x4v{low_bf16(o[2]), high_bf16(o[2]), low_bf16(o[3]), high_bf16(o[3])}, hi);
+    }
+    *d = u32x4{two_bf16(lo[0], lo[1]), two_bf16(lo[2], lo[3]), two_bf16(hi[0], hi[1]), two_bf16(hi[2], hi[3])};
+  }
+}
+
+// The same one by one, of those in range.
+__device__ __forceinline__ void put_some(const Target& t, int64_t m, int64_t n, f32x4v lo, f32x4v hi) {
+  if (m >= t.rows) return;
+  const int64_t at = (t.row_map ? int64_t(t.row_map[m]) : m) * t.ld + n;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (n + j >= t.cols) continue;
+    float v = j < 4 ? lo[j & 3] : hi[j & 3];
+    if (t.add) v = t.add[at + j] + v;
+    v = t.alpha * v;
+    if (t.f32) {
+      float* d = static_cast<float*>(t.base) + at + j;
+      *d = t.accumulate ? *d + v : v;
+    } else {
+      uint16_t* d = static_cast<uint16_t*>(t.base) + at + j;
+      *d = uint16_t(bf16_bits_of(t.accumulate ? low_bf16(*d) + v : v));
+    }
+  }
+}
+
 // Orders this wave's LDS accesses for all its lanes: what a lane wrote before is
 // read by the others after, and the other way round.  (The LDS serves a wave in
 // order; it is the compiler that must not swap accesses of different lanes.)
@@ -353,9 +413,13 @@ template <Form FA, Form FB, Code CODE, int BM, int BN, int WM, int WN>
 struct Gemm {
   static constexpr int kThreads = WM * WN * 64;
   static constexpr int kFM = BM / WM / 16, kFN = BN / WN / 16;  // fragments of a wave
-  using SA = Side<FA, CODE, BM, kFM, kThreads>;
-  using SB = Side<FB, CODE, BN, kFN, kThreads>;
-  static constexpr bool kPacked = SA::kPacked || SB::kPacked;
+  static constexpr bool kPacked = FA == Form::kPacked || FB == Form::kPacked;
+  // With e4m3 codes the fragments' addresses no longer fit the registers beside
+  // the products' sums (spilled in the step loop: 12% slower); with int8 codes
+  // there is no time to work them out (3% slower), nor need without codes.
+  static constexpr bool kLean = kPacked && CODE == Code::kE4m3;
+  using SA = Side<FA, CODE, BM, kFM, kThreads, kLean>;
+  using SB = Side<FB, CODE, BN, kFN, kThreads, kLean>;
   static constexpr int kStage = SA::kBytes + SB::kBytes;  // bytes of each of the four stages
 
   f32x4v acc[kFM][kFN];
@@ -409,21 +473,17 @@ struct Gemm {
 
   // Sums the opened tile into acc.  All waves are done with the stages then.
   __device__ __forceinline__ void loop(char* l0, char* l1, char* l2, char* l3) {
-#pragma unroll
-    for (int i = 0; i < kFM; ++i)
-#pragma unroll
-      for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
     bf16x8 fb[kFN], fa[2];
     typename SA::Held ha[2];  // packed sides: codes of an even and an odd step
     typename SB::Held hb[2];
     // Codes of step s + ahead < s + 4.
-    auto codes_early = [&](int ahead) {
+    auto codes_early = [&](int ahead, typename SA::Held& na, typename SB::Held& nb) {
       if (s + ahead < first) {
-        if (SA::kPacked) sa.template fetch<true>(nullptr, ha[ahead & 1], first, 0, tid);
-        if (SB::kPacked) sb.template fetch<true>(nullptr, hb[ahead & 1], first, 0, tid);
+        if (SA::kPacked) sa.template fetch<true>(nullptr, na, first, 0, tid);
+        if (SB::kPacked) sb.template fetch<true>(nullptr, nb, first, 0, tid);
       } else {
-        if (SA::kPacked) sa.template fetch<false>(nullptr, ha[ahead & 1], s + ahead, 0, tid);
-        if (SB::kPacked) sb.template fetch<false>(nullptr, hb[ahead & 1], s + ahead, 0, tid);
+        if (SA::kPacked) sa.template fetch<false>(nullptr, na, s + ahead, 0, tid);
+        if (SB::kPacked) sb.template fetch<false>(nullptr, nb, s + ahead, 0, tid);
       }
     };
     auto settle = [&](char* lds, int set) {
@@ -492,25 +552,34 @@ struct Gemm {
       ++s;
     };
 
+    // every first load on its way before the first is waited for
+    typename SA::Held ta, ea[2];
+    typename SB::Held tb, eb[2];
     if (left) {
       lds_barrier();  // the last stage may have served an epilogue
-      typename SA::Held ta;
-      typename SB::Held tb;
       sa.template fetch<true>(l3, ta, whole, left, tid);
       sb.template fetch<true>(l3 + SA::kBytes, tb, whole, left, tid);
+    }
+    if (kPacked && rounds > 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) codes_early(i, ea[i], eb[i]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) codes_early(2 + i, ha[i], hb[i]);
+    }
+    if (left) {
       sa.settle(l3, ta);
       sb.settle(l3 + SA::kBytes, tb);
     }
-    if constexpr (kPacked) {
-      if (rounds > 0) {
-        codes_early(0);
-        codes_early(1);
-        settle(l0, 0);
-        settle(l1, 1);
-        codes_early(2);
-        codes_early(3);
-      }
+    if (kPacked && rounds > 0) {
+      sa.settle(l0, ea[0]);
+      sb.settle(l0 + SA::kBytes, eb[0]);
+      sa.settle(l1, ea[1]);
+      sb.settle(l1 + SA::kBytes, eb[1]);
     }
+#pragma unroll
+    for (int i = 0; i < kFM; ++i)
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
     wait_loads<0, true>();
     bare_barrier();
     if (left) {
@@ -575,124 +644,12 @@ struct Gemm {
 
   // Writes the tile at (m0, n0) to `t`.
   __device__ __forceinline__ void write(const Target& t, int64_t m0, int64_t n0, char* lds) {
-    const bool vec = (reinterpret_cast<uintptr_t>(t.base) & 15) == 0 && t.ld % (t.f32 ? 4 : 8) == 0 &&
-                     (t.add == nullptr || ((reinterpret_cast<uintptr_t>(t.add) & 15) == 0 && t.ld % 4 == 0));
-    if (vec && m0 + BM <= t.rows && n0 + BN <= t.cols) {
-      each<true>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) {
-        const int64_t row = t.row_map ? t.row_map[m0 + r] : m0 + r, at = row * t.ld + n0 + c;
-        if (t.add) {
-          lo = add4(*reinterpret_cast<const f32x4v*>(t.add + at), lo);
-          hi = add4(*reinterpret_cast<const f32x4v*>(t.add + at + 4), hi);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          lo[j] = t.alpha * lo[j];
-          hi[j] = t.alpha * hi[j];
-        }
-        if (t.f32) {
-          float* d = static_cast<float*>(t.base) + at;
-          if (t.accumulate) {
-            lo = add4(*reinterpret_cast<const f32x4v*>(d), lo);
-            hi = add4(*reinterpret_cast<const f32x4v*>(d + 4), hi);
-          }
-          *reinterpret_cast<f32x4v*>(d) = lo;
-          *reinterpret_cast<f32x4v*>(d + 4) = hi;
-        } else {
-          u32x4* d = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(t.base) + at);
-          if (t.accumulate) {
-            const u32x4 o = *d;
-            lo = add4(f32x4v{low_bf16(o[0]), high_bf16(o[0]), low_bf16(o[1]), high_bf16(o[1])}, lo);
-            hi = add4(f32x4v{low_bf16(o[2]), high_bf16(o[2]), low_bf16(o[3]), high_bf16(o[3])}, hi);
-          }
-          *d = u32x4{two_bf16(lo[0], lo[1]), two_bf16(lo[2], lo[3]), two_bf16(hi[0], hi[1]), two_bf16(hi[2], hi[3])};
-        }
-      });
-    } else {
-      each<false>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) {
-        const int64_t m = m0 + r, n = n0 + c;
-        if (m >= t.rows) return;
-        const int64_t row = t.row_map ? t.row_map[m] : m, at = row * t.ld + n;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (n + j >= t.cols) continue;
-          float v = j < 4 ? lo[j & 3] : hi[j & 3];
-          if (t.add) v = t.add[at + j] + v;
-          v = t.alpha * v;
-          if (t.f32) {
-            float* d = static_cast<float*>(t.base) + at + j;
-            *d = t.accumulate ? *d + v : v;
-          } else {
-            uint16_t* d = static_cast<uint16_t*>(t.base) + at + j;
-            *d = uint16_t(bf16_bits_of(t.accumulate ? low_bf16(*d) + v : v));
-          }
-        }
-      });
-    }
+    if (m0 + BM <= t.rows && n0 + BN <= t.cols && target_vectors(t))
+      each<true>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) { put_vectors(t, m0 + r, n0 + c, lo, hi); });
+    else
+      each<false>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) { put_some(t, m0 + r, n0 + c, lo, hi); });
   }
 };
-
-// alpha s (+ old) for the `n` values v of one row from element `at`, rounded
-// once to the output's type (fp32 or bf16).
-__device__ __forceinline__ void store_values(void* out, int32_t f32, int32_t accumulate, float alpha, int64_t at, int n,
-                                           f32x4v v) {
-  if (f32) {
-    float* d = static_cast<float*>(out) + at;
-    if (n == 4 && (reinterpret_cast<uintptr_t>(d) & 15) == 0) {
-      f32x4v r;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = alpha * v[i];
-      if (accumulate) {
-        const f32x4v old = *reinterpret_cast<const f32x4v*>(d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = old[i] + r[i];
-      }
-      *reinterpret_cast<f32x4v*>(d) = r;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) d[i] = accumulate ? d[i] + alpha * v[i] : alpha * v[i];
-    }
-  } else {
-    uint16_t* d = static_cast<uint16_t*>(out) + at;
-    if (n == 4 && (reinterpret_cast<uintptr_t>(d) & 7) == 0) {
-      float r[4];
-      u32x2 old = u32x2{0, 0};
-      if (accumulate) old = *reinterpret_cast<const u32x2*>(d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float o = __uint_as_float(i & 1 ? old[i >> 1] & 0xFFFF0000u : old[i >> 1] << 16);
-        r[i] = accumulate ? o + alpha * v[i] : alpha * v[i];
-      }
-      *reinterpret_cast<u32x2*>(d) =
-          u32x2{bf16_bits_of(r[0]) | bf16_bits_of(r[1]) << 16, bf16_bits_of(r[2]) | bf16_bits_of(r[3]) << 16};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) {
-          const float r = alpha * v[i];
-          d[i] = uint16_t(bf16_bits_of(accumulate ? __uint_as_float(uint32_t(d[i]) << 16) + r : r));
-        }
-    }
-  }
-}
-
-// The splits' values of `n` elements from element `at`, added in order.
-__device__ __forceinline__ f32x4v sum_splits(const float* partial, int32_t splits, int64_t elems, int64_t at, int n) {
-  f32x4v s = f32x4v{0.f, 0.f, 0.f, 0.f};
-  for (int32_t k = 0; k < splits; ++k) {
-    const float* p = partial + int64_t(k) * elems + at;
-    if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-      const f32x4v v = *reinterpret_cast<const f32x4v*>(p);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] += v[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < n) s[j] += p[j];
-    }
-  }
-  return s;
-}
 
 // Workgroups go round-robin over the 8 XCDs, each with an L2 of its own, and
 // take every gridDim-th item (gridDim is a multiple of 8 or no smaller than the
@@ -708,6 +665,47 @@ __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t tiles_m, uint32_t
   const uint32_t rows = band * group + group <= tiles_m ? group : tiles_m - band * group;
   *tm = __builtin_amdgcn_readfirstlane(band * group + in % rows);
   *tn = __builtin_amdgcn_readfirstlane(in / rows);
+}
+
+// The tile, and the range of steps, of an item of a cut (training.h).
+struct Piece {
+  uint32_t tile;
+  int64_t k_first, k_end;  // of a depth of k
+  int64_t slot;            // of its partial sums; -1: it is a whole tile
+};
+__device__ __forceinline__ Piece piece_of(const Cut& c, uint32_t item, int64_t depth) {
+  if (item < c.full) return Piece{item, 0, depth, -1};
+  const uint32_t q = item - c.full, rest = c.tiles - c.full, split = q / rest;
+  const int64_t k0 = int64_t(split) * c.per * kBK, k1 = k0 + int64_t(c.per) * kBK;
+  return Piece{c.full + q - split * rest, k0, k1 < depth ? k1 : depth, c.splits > 1 ? int64_t(q) : -1};
+}
+
+// Where the partial sums of a slot go.
+template <int SIDE>
+__device__ __forceinline__ Target slot_target(float* partial, int64_t slot) {
+  return Target{partial + slot * SIDE * SIDE, SIDE, SIDE, SIDE, nullptr, nullptr, 1.0f, 1, 0};
+}
+
+// Joins the partial sums of tile full + r (of a cut with splits), in order of
+// the splits, into `t`: `part` of the SIDE * SIDE / 2048 parts of a tile.
+template <int SIDE>
+__device__ __forceinline__ void join_tile(const float* partial, const Cut& c, uint32_t tiles_m, uint32_t tiles_n,
+                                          uint32_t r, uint32_t part, const Target& t) {
+  const uint32_t rest = c.tiles - c.full, g = part * 256 + threadIdx.x, row = g / (SIDE / 8), col = g % (SIDE / 8) * 8;
+  uint32_t tm, tn;
+  tile_of(c.full + r, tiles_m, tiles_n, 4, &tm, &tn);
+  const int64_t m = int64_t(tm) * SIDE + row, n = int64_t(tn) * SIDE + col;
+  if (m >= t.rows || n >= t.cols) return;
+  const float* p = partial + int64_t(r) * SIDE * SIDE + row * SIDE + col;
+  f32x4v lo = f32x4v{0.f, 0.f, 0.f, 0.f}, hi = lo;
+  for (uint32_t k = 0; k < c.splits; ++k, p += int64_t(rest) * SIDE * SIDE) {
+    lo = add4(lo, *reinterpret_cast<const f32x4v*>(p));
+    hi = add4(hi, *reinterpret_cast<const f32x4v*>(p + 4));
+  }
+  if (n + 8 <= t.cols && target_vectors(t))
+    put_vectors(t, m, n, lo, hi);
+  else
+    put_some(t, m, n, lo, hi);
 }
 
 }  // namespace tide

@@ -36,11 +36,63 @@ struct WeightGradCall {
   void* dw;
 };
 
-// How a weight gradient is cut into tiles and splits, and its workspace:
-// dy_bytes of aligned rows (when dY's are not), then partial_bytes.
+constexpr int kBK = 32;  // k per step of the matrix products
+
+// How a product's tiles go to the resident workgroups (slots): whole rounds of
+// tiles as they are, and the rest of them in splits of `per` steps of k each,
+// whose fp32 partial sums are joined afterwards.  Items [0, full) are tiles,
+// the others (tiles - full) * splits pieces.
+struct Cut {
+  uint32_t tiles, full, splits, per, items;
+};
+
+#ifdef __HIPCC__
+#define TIDE_BOTH __host__ __device__
+#else
+#define TIDE_BOTH
+#endif
+
+TIDE_BOTH inline int64_t tile_slots(int64_t side) { return side == 256 ? 256 : side == 128 ? 512 : 1024; }
+
+// Splitting pays where it saves more steps (about 0.7 us each for a 256 x 256
+// tile a CU, 0.3 us for two of 128 x 128) than the partial sums and the join
+// cost, about 30 and 8 us.
+TIDE_BOTH inline Cut cut_tiles(int64_t tiles, int64_t steps, int64_t side) {
+  Cut c{uint32_t(tiles), uint32_t(tiles), 1, uint32_t(steps), uint32_t(tiles)};
+  const int64_t slots = tile_slots(side), rest = tiles % slots;
+  const int64_t shortest = side == 256 ? 32 : 16, worth = side == 256 ? 64 : 32;
+  if (rest == 0) return c;
+  int64_t splits = slots / rest;
+  if (splits > steps / shortest) splits = steps / shortest;
+  if (splits < 2) return c;
+  const int64_t per = (steps + splits - 1) / splits;
+  if (steps - per < worth) return c;
+  splits = (steps + per - 1) / per;
+  c.full = uint32_t(tiles - rest);
+  c.splits = uint32_t(splits);
+  c.per = uint32_t(per);
+  c.items = uint32_t(tiles - rest + rest * splits);
+  return c;
+}
+
+inline int64_t partial_bytes(const Cut& c, int64_t side) {
+  return c.splits > 1 ? int64_t(c.items - c.full) * side * side * 4 : 0;
+}
+
+// About what a product of that cut takes, in us, for the choice of the tile.
+inline double cut_cost(const Cut& c, int64_t steps, int64_t side) {
+  const double step = side == 256 ? 0.72 : 0.45, tile = side == 256 ? 8.0 : 5.0;
+  const int64_t slots = tile_slots(side), rounds = c.full / slots, rest = c.splits > 1 ? c.per : c.full % slots ? steps : 0;
+  return double(rounds) * (double(steps) * step + tile) + double(rest) * step + (rest ? tile : 0.0) +
+         (c.splits > 1 ? 5.0 + 0.4e-6 * double(partial_bytes(c, side)) : 0.0);
+}
+
+// How a weight gradient is laid out, and its workspace: dy_bytes of aligned
+// rows (when dY's are not), then partial_bytes.
 struct WeightGradPlan {
-  bool big;  // 256 x 256 tiles
-  int64_t tiles_m, tiles_n, splits, split_k, dy_ld, dy_bytes, partial_bytes;
+  int64_t side;  // of its tiles
+  Cut cut;
+  int64_t tiles_m, tiles_n, dy_ld, dy_bytes, partial_bytes;
 };
 
 struct VocabLossCall {
@@ -69,8 +121,7 @@ WeightGradPlan plan_weight_grad(int64_t tokens, int64_t outs, int64_t ins, bool 
 // Workgroups of a tile kernel with `items` tiles of side x side: as many as the
 // 256 CUs hold at once (by their LDS), each taking one item after another.
 inline unsigned resident_groups(int64_t items, int64_t side) {
-  const int64_t most = side == 256 ? 256 : side == 128 ? 512 : 1024;
-  return unsigned(items < most ? items : most);
+  return unsigned(items < tile_slots(side) ? items : tile_slots(side));
 }
 
 // Launches; each returns the hipError_t as int.

@@ -373,10 +373,9 @@ struct HiddenGradArgs {
   const float* scale;
   const int32_t* list;
   int64_t first, piece, hidden, vocab;
-  int64_t split_k;
-  float* partial;  // [splits][piece][hidden], or null
+  float* partial;  // a slot of a tile for each piece of the cut, which the tokens that count decide
   uint16_t* dhidden;
-  uint32_t tiles_n, splits;
+  uint32_t tiles_n;
 };
 
 template <int BM, int BN, int WM, int WN>
@@ -387,43 +386,43 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
   const int64_t rows = rows_of(a.count, a.first, a.piece);
-  const uint32_t tiles_m = uint32_t((rows + BM - 1) / BM), tiles = tiles_m * a.tiles_n, items = tiles * a.splits;
-  if (blockIdx.x >= items) return;
+  const uint32_t tiles_m = uint32_t((rows + BM - 1) / BM);
+  const Cut cut = cut_tiles(tiles_m * a.tiles_n, (a.vocab + kBK - 1) / kBK, BM);
+  if (blockIdx.x >= cut.items) return;
   a.dz.extent = rows;
-  const float scale = *a.scale;
-  int64_t m0, n0, split;
+  const Target out{a.dhidden, a.hidden, rows, a.hidden, a.list + a.first, nullptr, *a.scale, 0, 0};
+  int64_t m0, n0, slot;
   G g;
   g.setup();
   auto open = [&](uint32_t item) {
+    const Piece p = piece_of(cut, item, a.vocab);
     uint32_t tm, tn;
-    tile_of(item % tiles, tiles_m, a.tiles_n, 4, &tm, &tn);
+    tile_of(p.tile, tiles_m, a.tiles_n, 4, &tm, &tn);
     m0 = int64_t(tm) * BM;
     n0 = int64_t(tn) * BN;
-    split = item / tiles;
-    const int64_t k0 = split * a.split_k, k1 = k0 + a.split_k;
-    g.open(a.dz, a.w, m0, n0, k0, k1 < a.vocab ? k1 : a.vocab, lds0, lds1, lds2);
+    slot = p.slot;
+    g.open(a.dz, a.w, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
   };
   open(blockIdx.x);
-  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+  for (uint32_t item = blockIdx.x; item < cut.items; item += gridDim.x) {
     g.loop(lds0, lds1, lds2, lds3);
-    const int64_t m1 = m0, n1 = n0;
-    const Target t = a.partial ? Target{a.partial + split * a.piece * a.hidden, a.hidden, rows, a.hidden, nullptr,
-                                        nullptr, 1.0f, 1, 0}
-                               : Target{a.dhidden, a.hidden, rows, a.hidden, a.list + a.first, nullptr, scale, 0, 0};
-    if (item + gridDim.x < items) open(item + gridDim.x);
+    const int64_t m1 = slot >= 0 ? 0 : m0, n1 = slot >= 0 ? 0 : n0;
+    const Target t = slot >= 0 ? slot_target<BM>(a.partial, slot) : out;
+    if (item + gridDim.x < cut.items) open(item + gridDim.x);
     g.write(t, m1, n1, lds3);
   }
 }
 
-__global__ __launch_bounds__(256) void join_hidden_kernel(const float* partial, int32_t splits, int64_t piece,
-                                                          int64_t hidden, const int32_t* count, const float* scale,
-                                                          const int32_t* list, int64_t first, uint16_t* dhidden) {
-  const int64_t groups = (hidden + 3) / 4, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t r = i / groups, c = (i - r * groups) * 4;
-  if (r >= rows_of(count, first, piece)) return;
-  const int n = hidden - c < 4 ? int(hidden - c) : 4;
-  store_values(dhidden, 0, 0, *scale, int64_t(list[first + r]) * hidden + c, n,
-               sum_splits(partial, splits, piece * hidden, r * hidden + c, n));
+template <int SIDE>
+__global__ __launch_bounds__(256) void join_hidden_kernel(HiddenGradArgs a) {
+  constexpr uint32_t kParts = SIDE * SIDE / 2048;
+  const int64_t rows = rows_of(a.count, a.first, a.piece);
+  const uint32_t tiles_m = uint32_t((rows + SIDE - 1) / SIDE);
+  const Cut cut = cut_tiles(tiles_m * a.tiles_n, (a.vocab + kBK - 1) / kBK, SIDE);
+  if (cut.splits == 1) return;
+  for (uint32_t i = blockIdx.x; i < (cut.tiles - cut.full) * kParts; i += gridDim.x)
+    join_tile<SIDE>(a.partial, cut, tiles_m, a.tiles_n, i / kParts, i % kParts,
+                    Target{a.dhidden, a.hidden, rows, a.hidden, a.list + a.first, nullptr, *a.scale, 0, 0});
 }
 
 // The rows of dH whose tokens do not count.
@@ -495,9 +494,9 @@ struct Layout {
   bool listed = false;  // tokens are listed and their states gathered
   int side = 256;       // tile of the logits
   int64_t tiles_n = 0;
-  bool big_h = false;   // dH
-  int64_t h_splits = 1, h_split_k = 0;
-  bool big_w = false;   // dW
+  int side_h = 256;     // of dH's tiles
+  bool h_splits = false;  // whether they may be split
+  int side_w = 256;     // of dW's tiles
   bool sums = false;    // dW's sums go over the pieces in the workspace
   // byte offsets
   int64_t list = 0, count = 0, h = 0, w = 0, stats = 0, target_z = 0, row_log2 = 0, e = 0, partial = 0, dw_sums = 0,
@@ -540,19 +539,24 @@ Layout layout_of(const VocabLossCall& c) {
   if (grad) {
     L.row_log2 = take(L.piece * 4);
     L.e = take(L.piece * L.e_ld * 2);
-    const int64_t tiles = (L.piece + 255) / 256 * ((c.hidden + 255) / 256);
-    L.big_h = tiles >= 192;
-    const int64_t side = L.big_h ? 256 : 128;
-    const int64_t mine = (L.piece + side - 1) / side * ((c.hidden + side - 1) / side);
+    // The cut itself waits for the number of tokens that count.  Its partial
+    // sums take no more slots than there are workgroups, nor than every tile
+    // split as far as may be.
     const int64_t steps = (c.vocab + kBK - 1) / kBK;
-    int64_t splits = L.big_h || mine == 0 ? 1 : 512 / mine;
-    if (splits > steps / 8) splits = steps / 8;
-    if (splits < 1) splits = 1;
-    const int64_t per = (steps + splits - 1) / splits;
-    L.h_splits = (steps + per - 1) / per;
-    L.h_split_k = per * kBK;
-    if (L.h_splits > 1) L.partial = take(L.h_splits * L.piece * c.hidden * 4);
-    L.big_w = (c.vocab + 255) / 256 * ((c.hidden + 255) / 256) >= 192;
+    const int64_t big = (L.piece + 255) / 256 * ((c.hidden + 255) / 256);
+    const int64_t small = (L.piece + 127) / 128 * ((c.hidden + 127) / 128);
+    L.side_h = cut_cost(cut_tiles(big, steps, 256), steps, 256) <= cut_cost(cut_tiles(small, steps, 128), steps, 128)
+                   ? 256
+                   : 128;
+#ifdef FORCE_SIDE
+    L.side_h = FORCE_SIDE;
+#endif
+    const int64_t most = L.side_h == 256 ? big * (steps / 32) : small * (steps / 16);
+    const int64_t slots = most < tile_slots(L.side_h) ? most : tile_slots(L.side_h);
+    L.h_splits = steps >= (L.side_h == 256 ? 64 : 32) && slots > 1;
+    if (L.h_splits) L.partial = take(slots * L.side_h * L.side_h * 4);
+    const int64_t w_big = (c.vocab + 255) / 256 * ((c.hidden + 255) / 256);
+    L.side_w = w_big >= 192 ? 256 : 128;
     L.sums = L.pieces > 1 && !c.dw_f32;
     if (L.sums) L.dw_sums = take(c.vocab * c.hidden * 4);
   }
@@ -664,22 +668,22 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     d.piece = L.piece;
     d.hidden = c.hidden;
     d.vocab = c.vocab;
-    d.split_k = L.h_split_k;
-    d.partial = L.h_splits > 1 ? reinterpret_cast<float*>(ws + L.partial) : nullptr;
+    d.partial = reinterpret_cast<float*>(ws + L.partial);
     d.dhidden = static_cast<uint16_t*>(c.dhidden);
-    const int64_t side_h = L.big_h ? 256 : 128;
-    d.tiles_n = uint32_t((c.hidden + side_h - 1) / side_h);
-    d.splits = uint32_t(L.h_splits);
-    const dim3 grid_h(resident_groups((L.piece + side_h - 1) / side_h * d.tiles_n * L.h_splits, side_h));
-    if (L.big_h)
+    d.tiles_n = uint32_t((c.hidden + L.side_h - 1) / L.side_h);
+    // as many workgroups as any cut has items for (a cut with pieces fills the slots at most)
+    const int64_t tiles_h = (L.piece + L.side_h - 1) / L.side_h * d.tiles_n;
+    const dim3 grid_h(L.h_splits ? unsigned(tile_slots(L.side_h)) : resident_groups(tiles_h, L.side_h));
+    if (L.side_h == 256)
       hipLaunchKernelGGL((hidden_grad_kernel<256, 256, 2, 4>), grid_h, dim3(512), 0, st, d);
     else
       hipLaunchKernelGGL((hidden_grad_kernel<128, 128, 2, 2>), grid_h, dim3(256), 0, st, d);
     TIDE_LAUNCHED();
-    if (L.h_splits > 1) {
-      const int64_t n = L.piece * ((c.hidden + 3) / 4);
-      hipLaunchKernelGGL(join_hidden_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st, d.partial,
-                         int32_t(L.h_splits), L.piece, c.hidden, count, scale, list, first, d.dhidden);
+    if (L.h_splits) {
+      if (L.side_h == 256)
+        hipLaunchKernelGGL(join_hidden_kernel<256>, dim3(1024), dim3(256), 0, st, d);
+      else
+        hipLaunchKernelGGL(join_hidden_kernel<128>, dim3(1024), dim3(256), 0, st, d);
       TIDE_LAUNCHED();
     }
     VocabGradArgs v;
@@ -698,11 +702,11 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     v.dw = c.dw;
     v.f32 = c.dw_f32;
     v.accumulate = c.accumulate || (p > 0 && !L.sums);
-    const int64_t side_w = L.big_w ? 256 : 128;
+    const int64_t side_w = L.side_w;
     v.tiles_m = uint32_t((c.vocab + side_w - 1) / side_w);
     v.tiles_n = uint32_t((c.hidden + side_w - 1) / side_w);
     const dim3 grid_w(resident_groups(int64_t(v.tiles_m) * v.tiles_n, side_w));
-    if (L.big_w)
+    if (L.side_w == 256)
       hipLaunchKernelGGL((vocab_grad_kernel<256, 256, 2, 4>), grid_w, dim3(512), 0, st, v);
     else
       hipLaunchKernelGGL((vocab_grad_kernel<128, 128, 2, 2>), grid_w, dim3(256), 0, st, v);

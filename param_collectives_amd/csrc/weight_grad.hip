@@ -12,8 +12,8 @@ using namespace tide;
 struct WeightGradArgs {
   Operand dy, x;
   int64_t outs, ins, tokens;
-  int64_t split_k;   // tokens of one split, a multiple of 64
-  float* partial;    // [splits][outs][ins], or null: the result is written
+  Cut cut;
+  float* partial;    // a slot of a tile for each piece of the cut
   void* dw;
   float alpha;
   int32_t f32, accumulate;
@@ -29,28 +29,25 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void weight_grad_kernel(WeightGradA
   __shared__ __align__(16) char lds3[G::kStage];
   // One tile a workgroup: with the next tile's loads under the epilogue, as in
   // the vocabulary loss, the codes' registers spill (measured 2-18% slower).
-  const uint32_t tiles = a.tiles_m * a.tiles_n;
+  const Piece p = piece_of(a.cut, blockIdx.x, a.tokens);
   uint32_t tm, tn;
-  tile_of(blockIdx.x % tiles, a.tiles_m, a.tiles_n, 4, &tm, &tn);
-  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN, split = blockIdx.x / tiles;
-  const int64_t k0 = split * a.split_k, k1 = k0 + a.split_k;
+  tile_of(p.tile, a.tiles_m, a.tiles_n, 4, &tm, &tn);
+  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
   G g;
   g.setup();
-  g.open(a.dy, a.x, m0, n0, k0, k1 < a.tokens ? k1 : a.tokens, lds0, lds1, lds2);
+  g.open(a.dy, a.x, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
   g.loop(lds0, lds1, lds2, lds3);
-  const Target t = a.partial ? Target{a.partial + split * a.outs * a.ins, a.ins, a.outs, a.ins, nullptr, nullptr, 1.0f,
-                                      1, 0}
-                             : Target{a.dw, a.ins, a.outs, a.ins, nullptr, nullptr, a.alpha, a.f32, a.accumulate};
-  g.write(t, m0, n0, lds3);
+  if (p.slot >= 0)
+    g.write(slot_target<BM>(a.partial, p.slot), 0, 0, lds3);
+  else
+    g.write(Target{a.dw, a.ins, a.outs, a.ins, nullptr, nullptr, a.alpha, a.f32, a.accumulate}, m0, n0, lds3);
 }
 
-// Sums the splits in order.
-__global__ __launch_bounds__(256) void join_splits_kernel(const float* partial, int32_t splits, int64_t elems,
-                                                          void* dw, int32_t f32, int32_t accumulate, float alpha) {
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= elems) return;
-  const int n = elems - i < 4 ? int(elems - i) : 4;
-  store_values(dw, f32, accumulate, alpha, i, n, sum_splits(partial, splits, elems, i, n));
+template <int SIDE>
+__global__ __launch_bounds__(256) void join_weight_grad_kernel(WeightGradArgs a) {
+  constexpr uint32_t kParts = SIDE * SIDE / 2048;
+  join_tile<SIDE>(a.partial, a.cut, a.tiles_m, a.tiles_n, blockIdx.x / kParts, blockIdx.x % kParts,
+                  Target{a.dw, a.ins, a.outs, a.ins, nullptr, nullptr, a.alpha, a.f32, a.accumulate});
 }
 
 // Rows of any pitch and alignment -> rows of pitch `ld` (a multiple of 8)
@@ -87,25 +84,20 @@ int launch_align_rows(const void* src, int64_t src_ld, int64_t rows, int64_t col
 }
 
 WeightGradPlan plan_weight_grad(int64_t tokens, int64_t outs, int64_t ins, bool aligned) {
-  WeightGradPlan p;
   const int64_t steps = (tokens + kBK - 1) / kBK;
-  p.big = ((outs + 255) / 256) * ((ins + 255) / 256) >= 192;
-  const int64_t side = p.big ? 256 : 128;
-  p.tiles_m = (outs + side - 1) / side;
-  p.tiles_n = (ins + side - 1) / side;
-  const int64_t tiles = p.tiles_m * p.tiles_n;
-  int64_t splits = 1;
-  if (!p.big && tiles > 0) {
-    splits = 512 / tiles;
-    if (splits > steps / 8) splits = steps / 8;
-    if (splits < 1) splits = 1;
-  }
-  const int64_t per = splits > 1 ? (steps + splits - 1) / splits : (steps > 0 ? steps : 1);
-  p.splits = steps > 0 ? (steps + per - 1) / per : 1;
-  p.split_k = per * kBK;
+  const int64_t big = (outs + 255) / 256 * ((ins + 255) / 256), small = (outs + 127) / 128 * ((ins + 127) / 128);
+  const Cut cb = cut_tiles(big, steps, 256), cs = cut_tiles(small, steps, 128);
+  WeightGradPlan p;
+  p.side = cut_cost(cb, steps, 256) <= cut_cost(cs, steps, 128) ? 256 : 128;
+#ifdef FORCE_SIDE
+  p.side = FORCE_SIDE;
+#endif
+  p.cut = p.side == 256 ? cb : cs;
+  p.tiles_m = (outs + p.side - 1) / p.side;
+  p.tiles_n = (ins + p.side - 1) / p.side;
   p.dy_ld = (outs + 63) / 64 * 64;
   p.dy_bytes = aligned ? 0 : (tokens * p.dy_ld * 2 + 255) / 256 * 256;
-  p.partial_bytes = p.splits > 1 ? p.splits * outs * ins * 4 : 0;
+  p.partial_bytes = partial_bytes(p.cut, p.side);
   return p;
 }
 
@@ -127,16 +119,16 @@ int launch_weight_grad(const WeightGradCall& c, void* workspace, void* stream) {
   a.outs = c.outs;
   a.ins = c.ins;
   a.tokens = c.tokens;
-  a.split_k = p.split_k;
-  a.partial = p.splits > 1 ? reinterpret_cast<float*>(ws + p.dy_bytes) : nullptr;
+  a.cut = p.cut;
+  a.partial = reinterpret_cast<float*>(ws + p.dy_bytes);
   a.dw = c.dw;
   a.alpha = c.alpha;
   a.f32 = c.f32;
   a.accumulate = c.accumulate;
   a.tiles_m = uint32_t(p.tiles_m);
   a.tiles_n = uint32_t(p.tiles_n);
-  const dim3 grid(unsigned(p.tiles_m * p.tiles_n * p.splits));
-  if (p.big) {
+  const dim3 grid(p.cut.items);
+  if (p.side == 256) {
     if (c.int8)
       hipLaunchKernelGGL((weight_grad_kernel<Code::kInt8, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
     else
@@ -147,11 +139,13 @@ int launch_weight_grad(const WeightGradCall& c, void* workspace, void* stream) {
     else
       hipLaunchKernelGGL((weight_grad_kernel<Code::kE4m3, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
   }
-  int rc = int(hipGetLastError());
-  if (rc != 0 || p.splits == 1) return rc;
-  const int64_t elems = c.outs * c.ins;
-  hipLaunchKernelGGL(join_splits_kernel, dim3(unsigned((elems / 4 + 256) / 256)), dim3(256), 0, st, a.partial,
-                     int32_t(p.splits), elems, c.dw, c.f32, c.accumulate, c.alpha);
+  const int rc = int(hipGetLastError());
+  if (rc != 0 || p.cut.splits == 1) return rc;
+  const unsigned rest = p.cut.tiles - p.cut.full;
+  if (p.side == 256)
+    hipLaunchKernelGGL(join_weight_grad_kernel<256>, dim3(rest * 32), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(join_weight_grad_kernel<128>, dim3(rest * 8), dim3(256), 0, st, a);
   return int(hipGetLastError());
 }
 

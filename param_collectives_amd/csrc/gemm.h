@@ -533,13 +533,19 @@ struct Gemm {
     // step i: step i + 2's, and the codes of steps i + 2 and i + 3.
     constexpr int kCodeLoads = (SA::kPacked ? SA::kLoads : 0) + (SB::kPacked ? SB::kLoads : 0);
     constexpr int kAfter = SA::kLoads + SB::kLoads + kCodeLoads;
-    // Part i of the loads of step s + 3.  (One after each row of products:
+    // Loads of step s + 3 that follow row i.  (One after each row of products:
     // started together at the step's head they hold its products up, 4% of a
     // large product's time.)
+    constexpr int kPartsA = SA::kPacked ? 0 : SA::kParts, kParts = kPartsA + (SB::kPacked ? 0 : SB::kParts);
+    constexpr int kPerRow = (kParts + kFM - 1) / kFM;
     auto load = [&](char* to3, int i) {
-      if (!SA::kPacked && i < SA::kParts) sa.fetch_part(to3, s + 3, i);
-      const int j = i - (SA::kPacked ? 0 : SA::kParts);
-      if (!SB::kPacked && j >= 0 && j < SB::kParts) sb.fetch_part(to3 + SA::kBytes, s + 3, j);
+#pragma unroll
+      for (int n = i * kPerRow; n < (i + 1) * kPerRow; ++n) {
+        if (n < kPartsA)
+          sa.fetch_part(to3, s + 3, n);
+        else if (n < kParts)
+          sb.fetch_part(to3 + SA::kBytes, s + 3, n - kPartsA);
+      }
     };
     auto step = [&](char* now, char* next, char* to2, char* to3, int set) {
       wait_loads<kAfter, kPacked>();

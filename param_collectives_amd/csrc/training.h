@@ -52,7 +52,7 @@ struct Cut {
 #define TIDE_BOTH
 #endif
 
-TIDE_BOTH inline int64_t tile_slots(int64_t side) { return side == 256 ? 256 : side == 128 ? 512 : 1024; }
+TIDE_BOTH inline int64_t tile_slots(int64_t side) { return side == 256 ? 256 : 512; }
 
 // Splitting pays where it saves more steps (about 0.7 us each for a 256 x 256
 // tile a CU, 0.3 us for two of 128 x 128) than the partial sums and the join

@@ -300,33 +300,197 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
   }
 }
 
-// Joins a row's tiles: one wave per row.  (c, s) stands for s 2^c.
+// The same for up to 16 NT tokens, where the weights' traffic is all that
+// counts: a wave reads the fragments of 16 vocabulary rows straight into
+// registers, a block of 256 k ahead (8 KiB a wave, 16 MiB over the GPU).  The
+// states' blocks come through LDS, two in turn, for the four waves of a workgroup
+// (each wave reading them for itself, which the L1 does not hold, took 44 us
+// instead of 31 for 17 x 2048 x 32000 from cold caches).  Row r's 16 bytes c are
+// kept at c ^ (r & 15): the fragment reads touch all banks once.
+template <int NT>
+__global__ __launch_bounds__(256) void few_logits_kernel(LogitsArgs a) {
+  constexpr int kDeep = 256, kSteps = kDeep / 32, kLoads = 2 * NT;
+  __shared__ __align__(16) char h0[16 * NT * kDeep * 2];
+  __shared__ __align__(16) char h1[16 * NT * kDeep * 2];
+  __shared__ float peak[4][16 * NT];
+  __shared__ float sums[4][16 * NT];
+  const int64_t rows = a.count ? rows_of(a.count, a.first, a.piece) : a.tokens;
+  if (rows == 0) return;
+  const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
+  const int64_t n0 = int64_t(blockIdx.x) * 64 + wave * 16;
+  // rows past the end read the last one: their results are dropped
+  const int64_t v = n0 + r < a.vocab ? n0 + r : a.vocab - 1;
+  const char* w = static_cast<const char*>(a.w.base) + v * a.w.ld * 2 + g * 16;
+  const char* h = static_cast<const char*>(a.h.base) + a.first * a.h.ld * 2;
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int lin = i * 256 + int(threadIdx.x), row = lin >> 5, c = (lin & 31) ^ (row & 15);
+    off[i] = uint32_t(row < rows ? row : int(rows) - 1) * uint32_t(a.h.ld * 2) + uint32_t(c * 16);
+  }
+  auto load = [](const char* p) { return *(const TIDE_GLOBAL bf16x8*)p; };
+  auto states = [&](char* to, int64_t block) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load_to_lds(uniform(h + block * kDeep * 2), off[i], to + (i * 256 + wave * 64) * 16);
+  };
+  f32x4v acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  const int64_t blocks = a.depth / kDeep;
+  bf16x8 w0[kSteps], w1[kSteps];
+  auto weights = [&](bf16x8* to, int64_t block) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) to[i] = load(w + block * kDeep * 2 + i * 64);
+  };
+  auto multiply = [&](const char* now, const bf16x8* wf) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const bf16x8 hf = *reinterpret_cast<const bf16x8*>(now + ((16 * t + r) * 32 + ((4 * i + g) ^ r)) * 16);
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i], hf, acc[t], 0, 0, 0);
+      }
+  };
+  auto block = [&](const char* now, char* next, const bf16x8* wf, bf16x8* wn, int64_t b) {
+    wait_loads<kSteps, true>();  // this block's states are older than its weights
+    bare_barrier();
+    states(next, b + 1);
+    weights(wn, b + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(now, wf);
+  };
+  auto last = [&](const char* now, const bf16x8* wf) {
+    wait_loads<kSteps, true>();
+    bare_barrier();
+    multiply(now, wf);
+  };
+  if (blocks > 0) {
+    states(h0, 0);
+    weights(w0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    int64_t b = 0;
+    for (; b + 2 < blocks; b += 2) {
+      block(h0, h1, w0, w1, b);
+      block(h1, h0, w1, w0, b + 1);
+    }
+    if (b + 1 < blocks) {
+      block(h0, h1, w0, w1, b);
+      last(h1, w1);
+    } else {
+      last(h0, w0);
+    }
+  }
+  for (int64_t k = blocks * kDeep; k < a.depth; k += 32) {
+    const bool in = k + 8 * g < a.depth;  // k counts in eights
+    const bf16x8 zero = {};
+    const bf16x8 wv = in ? load(w + k * 2) : zero;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int64_t row = 16 * t + r < rows ? 16 * t + r : rows - 1;
+      const bf16x8 hv = in ? load(h + row * a.h.ld * 2 + (k + 8 * g) * 2) : zero;
+      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, hv, acc[t], 0, 0, 0);
+    }
+  }
+
+  // A lane holds of token 16 t + r the vocabulary rows n0 + 4 g + 0..3.
+  const int64_t left = a.vocab - n0 - 4 * g;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= left) acc[t][j] = -__builtin_inff();
+      m = fmaxf(m, acc[t][j]);
+    }
+    m = fmaxf(m, other_16(m));
+    m = fmaxf(m, other_32(m));
+    if (lane < 16) peak[wave][16 * t + r] = m;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = 16 * t + r;
+    if (row < rows) {
+      const int64_t at = a.targets[a.count ? a.list[a.first + row] : row] - n0 - 4 * g;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (at == j && j < left) a.target_z[row] = acc[t][j];
+    }
+    float m = peak[0][row];
+#pragma unroll
+    for (int w4 = 1; w4 < 4; ++w4) m = fmaxf(m, peak[w4][row]);
+    const float c = reference(m);
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc[t][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[t][j], kLog2e, -c));
+      s += acc[t][j];
+    }
+    s += other_16(s);
+    s += other_32(s);
+    if (lane < 16) sums[wave][row] = s;
+    if (a.e && row < rows && n0 + 4 * g < a.e_ld)
+      *reinterpret_cast<u32x2*>(a.e + row * a.e_ld + n0 + 4 * g) =
+          u32x2{two_halves(acc[t][0], acc[t][1]), two_halves(acc[t][2], acc[t][3])};
+  }
+  __syncthreads();
+  for (int row = threadIdx.x; row < rows; row += 256) {
+    float m = peak[0][row], s = sums[0][row];
+#pragma unroll
+    for (int w4 = 1; w4 < 4; ++w4) {
+      m = fmaxf(m, peak[w4][row]);
+      s += sums[w4][row];
+    }
+    a.stats[row * a.tiles_n + blockIdx.x] = make_float2(reference(m), s);
+  }
+}
+
+// Joins a row's tiles: one workgroup per row.  (c, s) stands for s 2^c.  Each
+// thread takes four tiles at a time, so that their loads overlap (a wave per row
+// that read the tiles twice took 4.8 us for 17 rows of 500).
 __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uint32_t tiles, const int32_t* count,
                                                         const int32_t* list, const int64_t* targets, int64_t vocab,
                                                         int64_t tokens, int64_t first, int64_t piece,
                                                         const float* target_z, float* row_log2, float* loss,
                                                         float* lse) {
-  const int64_t row = int64_t(blockIdx.x) * 4 + wave_index();
+  constexpr float kLowest = -3.0e38f;  // finite: the difference of two of them is 0
+  __shared__ float2 wave_part[4];
+  const int64_t row = blockIdx.x;
   const int64_t rows = count ? rows_of(count, first, piece) : tokens;
   if (row >= rows) return;
   const int lane = threadIdx.x & 63;
   const float2* p = stats + row * tiles;
-  float m = -__builtin_inff();
-  for (uint32_t t = lane; t < tiles; t += 64) m = fmaxf(m, p[t].x);
+  float m = kLowest, s = 0.0f;
+  for (uint32_t t = threadIdx.x; t < tiles; t += 1024) {
+    float2 v[4];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  float s = 0.0f;
-  for (uint32_t t = lane; t < tiles; t += 64) {
-    const float2 v = p[t];
-    s += v.y * __builtin_amdgcn_exp2f(v.x - m);
+    for (int j = 0; j < 4; ++j) v[j] = t + 256 * j < tiles ? p[t + 256 * j] : make_float2(kLowest, 0.0f);
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = fmaxf(top, v[j].x);
+    s *= __builtin_amdgcn_exp2f(m - top);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += v[j].y * __builtin_amdgcn_exp2f(v[j].x - top);
+    m = top;
   }
+  float top = m;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  s *= __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-  if (lane == 0) {
+  if (lane == 0) wave_part[threadIdx.x >> 6] = make_float2(top, s);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, wave_part[w].x);
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s += wave_part[w].y * __builtin_amdgcn_exp2f(wave_part[w].x - top);
     const int64_t token = count ? list[first + row] : row;
     const int64_t target = targets[token];
     const bool keep = target >= 0 && target < vocab;
-    const float l2 = m + __builtin_log2f(s), l = l2 * kLn2;
+    const float l2 = top + __builtin_log2f(s), l = l2 * kLn2;
     if (row_log2) row_log2[row] = l2;
     loss[token] = keep ? l - target_z[row] : 0.0f;
     if (lse) lse[token] = keep ? l : 0.0f;
@@ -492,7 +656,7 @@ struct Layout {
   int64_t piece = 0, pieces = 0;
   int64_t h_ld = 0, w_ld = 0, e_ld = 0;
   bool listed = false;  // tokens are listed and their states gathered
-  int side = 256;       // tile of the logits
+  int rows = 256, cols = 256;  // tile of the logits; up to 64 tokens (rows 16 to 64) without LDS
   int64_t tiles_n = 0;
   int side_h = 256;     // of dH's tiles
   bool h_splits = false;  // whether they may be split
@@ -517,8 +681,9 @@ Layout layout_of(const VocabLossCall& c) {
   // One tile of rows gains nothing from leaving tokens out of a loss.
   L.listed = grad || c.tokens > 256 || !rows_aligned(c.h, c.h_ld, c.hidden);
   const int64_t t256 = (L.piece + 255) / 256 * ((c.vocab + 255) / 256);
-  L.side = L.piece <= 64 ? 64 : t256 >= 192 ? 256 : 128;
-  L.tiles_n = (c.vocab + L.side - 1) / L.side;
+  L.rows = L.piece <= 64 ? int(up(L.piece, 16)) : t256 >= 192 ? 256 : 128;
+  L.cols = L.piece <= 64 ? 64 : L.rows;
+  L.tiles_n = (c.vocab + L.cols - 1) / L.cols;
   int64_t at = 0;
   auto take = [&](int64_t n) {
     const int64_t here = at;
@@ -639,22 +804,28 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     a.e = e;
     a.e_ld = L.e_ld;
     a.tiles_n = uint32_t(L.tiles_n);
-    const dim3 grid(resident_groups((L.piece + L.side - 1) / L.side * L.tiles_n, L.side));
-    if (L.side == 256)
+    const dim3 grid(resident_groups((L.piece + L.rows - 1) / L.rows * L.tiles_n, L.rows));
+    if (L.rows == 256)
       hipLaunchKernelGGL((logits_kernel<256, 256, 2, 4>), grid, dim3(512), 0, st, a);
-    else if (L.side == 128)
+    else if (L.rows == 128)
       hipLaunchKernelGGL((logits_kernel<128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+    else if (L.rows == 64)
+      hipLaunchKernelGGL(few_logits_kernel<4>, dim3(a.tiles_n), dim3(256), 0, st, a);
+    else if (L.rows == 48)
+      hipLaunchKernelGGL(few_logits_kernel<3>, dim3(a.tiles_n), dim3(256), 0, st, a);
+    else if (L.rows == 32)
+      hipLaunchKernelGGL(few_logits_kernel<2>, dim3(a.tiles_n), dim3(256), 0, st, a);
     else
-      hipLaunchKernelGGL((logits_kernel<64, 64, 1, 4>), grid, dim3(256), 0, st, a);
+      hipLaunchKernelGGL(few_logits_kernel<1>, dim3(a.tiles_n), dim3(256), 0, st, a);
     TIDE_LAUNCHED();
-    hipLaunchKernelGGL(join_rows_kernel, dim3(unsigned((L.piece + 3) / 4)), dim3(256), 0, st, stats, a.tiles_n, count,
+    hipLaunchKernelGGL(join_rows_kernel, dim3(unsigned(L.piece)), dim3(256), 0, st, stats, a.tiles_n, count,
                        list, targets, c.vocab, c.tokens, first, L.piece, target_z, row_log2, c.loss, c.lse);
     TIDE_LAUNCHED();
     if (!grad) continue;
     const int64_t rows_z = L.piece < 32768 ? L.piece : 32768;
     hipLaunchKernelGGL(logit_grad_kernel,
                        dim3(unsigned((L.e_ld + 2047) / 2048), unsigned(rows_z), unsigned((L.piece + 32767) / 32768)),
-                       dim3(256), 0, st, e, L.e_ld, c.vocab, stats, a.tiles_n, uint32_t(L.side), count, list, targets,
+                       dim3(256), 0, st, e, L.e_ld, c.vocab, stats, a.tiles_n, uint32_t(L.cols), count, list, targets,
                        first, L.piece, target_z, row_log2, c.grad_loss, scale);
     TIDE_LAUNCHED();
     HiddenGradArgs d;

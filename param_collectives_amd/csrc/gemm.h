@@ -650,8 +650,10 @@ struct Gemm {
 
   // Writes the tile at (m0, n0) to `t`.
   __device__ __forceinline__ void write(const Target& t, int64_t m0, int64_t n0, char* lds) {
-    if (m0 + BM <= t.rows && n0 + BN <= t.cols && target_vectors(t))
-      each<true>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) { put_vectors(t, m0 + r, n0 + c, lo, hi); });
+    if (n0 + BN <= t.cols && target_vectors(t))
+      each<true>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) {
+        if (m0 + r < t.rows) put_vectors(t, m0 + r, n0 + c, lo, hi);
+      });
     else
       each<false>(lds, [&](int r, int c, f32x4v lo, f32x4v hi) { put_some(t, m0 + r, n0 + c, lo, hi); });
   }
@@ -686,10 +688,10 @@ __device__ __forceinline__ Piece piece_of(const Cut& c, uint32_t item, int64_t d
   return Piece{c.full + q - split * rest, k0, k1 < depth ? k1 : depth, c.splits > 1 ? int64_t(q) : -1};
 }
 
-// Where the partial sums of a slot go.
+// Where the partial sums of a slot go, of a tile of which `rows` exist.
 template <int SIDE>
-__device__ __forceinline__ Target slot_target(float* partial, int64_t slot) {
-  return Target{partial + slot * SIDE * SIDE, SIDE, SIDE, SIDE, nullptr, nullptr, 1.0f, 1, 0};
+__device__ __forceinline__ Target slot_target(float* partial, int64_t slot, int64_t rows) {
+  return Target{partial + slot * SIDE * SIDE, SIDE, rows < SIDE ? rows : SIDE, SIDE, nullptr, nullptr, 1.0f, 1, 0};
 }
 
 // Joins the partial sums of tile full + r (of a cut with splits), in order of
@@ -704,6 +706,7 @@ __device__ __forceinline__ void join_tile(const float* partial, const Cut& c, ui
   if (m >= t.rows || n >= t.cols) return;
   const float* p = partial + int64_t(r) * SIDE * SIDE + row * SIDE + col;
   f32x4v lo = f32x4v{0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll 4
   for (uint32_t k = 0; k < c.splits; ++k, p += int64_t(rest) * SIDE * SIDE) {
     lo = add4(lo, *reinterpret_cast<const f32x4v*>(p));
     hi = add4(hi, *reinterpret_cast<const f32x4v*>(p + 4));

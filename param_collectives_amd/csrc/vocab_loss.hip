@@ -134,12 +134,21 @@ __global__ __launch_bounds__(1024) void list_tokens_kernel(const int64_t* target
 }
 
 // The listed tokens' hidden states, row after row, each filled up with zeros
-// to a pitch that is a multiple of 64.
+// to a pitch that is a multiple of 64; and zeros in the rows of dH (if any)
+// whose tokens are not listed.
 __global__ __launch_bounds__(256) void gather_rows_kernel(const uint16_t* hidden, int64_t ld, int64_t cols,
                                                           const int32_t* list, const int32_t* count, uint16_t* out,
-                                                          int64_t out_ld, int32_t vec) {
+                                                          int64_t out_ld, int32_t vec, int64_t tokens,
+                                                          const int64_t* targets, int64_t vocab, uint16_t* dhidden) {
   const int64_t groups = out_ld / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t r = i / groups, c = (i - r * groups) * 8;
+  if (r >= tokens) return;
+  if (dhidden) {
+    const int64_t target = targets[r];
+    if (target < 0 || target >= vocab) {
+      for (int64_t j = c; j < c + 8 && j < cols; ++j) dhidden[r * cols + j] = 0;
+    }
+  }
   if (r >= *count) return;
   const uint16_t* s = hidden + int64_t(list[r]) * ld + c;
   u32x4 v;
@@ -571,7 +580,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
   for (uint32_t item = blockIdx.x; item < cut.items; item += gridDim.x) {
     g.loop(lds0, lds1, lds2, lds3);
     const int64_t m1 = slot >= 0 ? 0 : m0, n1 = slot >= 0 ? 0 : n0;
-    const Target t = slot >= 0 ? slot_target<BM>(a.partial, slot) : out;
+    const Target t = slot >= 0 ? slot_target<BM>(a.partial, slot, rows - m0) : out;
     if (item + gridDim.x < cut.items) open(item + gridDim.x);
     g.write(t, m1, n1, lds3);
   }
@@ -587,16 +596,6 @@ __global__ __launch_bounds__(256) void join_hidden_kernel(HiddenGradArgs a) {
   for (uint32_t i = blockIdx.x; i < (cut.tiles - cut.full) * kParts; i += gridDim.x)
     join_tile<SIDE>(a.partial, cut, tiles_m, a.tiles_n, i / kParts, i % kParts,
                     Target{a.dhidden, a.hidden, rows, a.hidden, a.list + a.first, nullptr, *a.scale, 0, 0});
-}
-
-// The rows of dH whose tokens do not count.
-__global__ __launch_bounds__(256) void clear_rows_kernel(const int64_t* targets, int64_t vocab, int64_t hidden,
-                                                         int64_t tokens, uint16_t* dhidden) {
-  const int64_t t = int64_t(blockIdx.x) * 4 + wave_index();
-  if (t >= tokens) return;
-  const int64_t v = targets[t];
-  if (v >= 0 && v < vocab) return;
-  for (int64_t c = threadIdx.x & 63; c < hidden; c += 64) dhidden[t * hidden + c] = 0;
 }
 
 __global__ __launch_bounds__(256) void clear_kernel(uint16_t* p, int64_t n) {
@@ -766,7 +765,8 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     const int64_t n = c.tokens * (L.h_ld / 8);
     hipLaunchKernelGGL(gather_rows_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st,
                        static_cast<const uint16_t*>(c.h), c.h_ld, c.hidden, list, count, rows, L.h_ld,
-                       int32_t(rows_aligned(c.h, c.h_ld, c.hidden)));
+                       int32_t(rows_aligned(c.h, c.h_ld, c.hidden)), c.tokens, targets, c.vocab,
+                       grad ? static_cast<uint16_t*>(c.dhidden) : nullptr);
     TIDE_LAUNCHED();
     h.base = rows;
     h.ld = L.h_ld;
@@ -776,11 +776,6 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     if (rc != 0) return rc;
     w.base = ws + L.w;
     w.ld = L.w_ld;
-  }
-  if (grad) {
-    hipLaunchKernelGGL(clear_rows_kernel, dim3(unsigned((c.tokens + 3) / 4)), dim3(256), 0, st, targets, c.vocab,
-                       c.hidden, c.tokens, static_cast<uint16_t*>(c.dhidden));
-    TIDE_LAUNCHED();
   }
   float2* stats = reinterpret_cast<float2*>(ws + L.stats);
   float* target_z = reinterpret_cast<float*>(ws + L.target_z);

@@ -77,17 +77,38 @@ __device__ __forceinline__ int64_t rows_of(const int32_t* count, int64_t first, 
   return n > 0 ? n : 0;
 }
 
+// A workgroup's first item of a queue.
+__device__ __forceinline__ uint32_t first_item(Queue& q, uint32_t* words, uint32_t items, uint32_t* turn) {
+  q.setup(words, items);
+  if (threadIdx.x == 0) *turn = q.settle(q.ask());
+  __syncthreads();
+  const uint32_t item = __builtin_amdgcn_readfirstlane(*turn);
+  __syncthreads();
+  return item;
+}
+
+// The workgroup's next item, which its first thread asked for as k (at the end of
+// a tile's sums: earlier, a workgroup would take what one that is still to start
+// should have).
+__device__ __forceinline__ uint32_t next_item(Queue& q, uint32_t k, uint32_t* turn) {
+  if (threadIdx.x == 0) *turn = q.settle(k);
+  lds_barrier();
+  return __builtin_amdgcn_readfirstlane(*turn);
+}
+
 // ------------------------------------------------------------ the token list
 
 // Lists the tokens that count, in order, and clears the loss and lse of the
-// others; the largest |grad_loss| of those that count goes to *scale (1 where
+// others; clears the products' queues; the largest |grad_loss| of those that count goes to *scale (1 where
 // that is 0 or not finite).  One workgroup: a pass per 1024 tokens.
 __global__ __launch_bounds__(1024) void list_tokens_kernel(const int64_t* targets, int64_t tokens, int64_t vocab,
                                                            const float* grad_loss, int32_t* list, int32_t* count,
-                                                           float* scale, float* loss, float* lse) {
+                                                           float* scale, float* loss, float* lse, uint32_t* queues,
+                                                           int64_t queue_words) {
   __shared__ int32_t wave_sum[16];
   __shared__ uint32_t wave_top[16];
   uint32_t top = 0;  // magnitudes compare as their bits, NaN above all
+  for (int64_t i = threadIdx.x; i < queue_words; i += 1024) queues[i] = 0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int32_t before = 0;
   for (int64_t t0 = 0; t0 < tokens; t0 += 1024) {
@@ -176,6 +197,7 @@ struct LogitsArgs {
   uint16_t* e;             // [row of the piece][e_ld], or null
   int64_t e_ld;
   uint32_t tiles_n;
+  uint32_t* queue;         // null: every workgroup has its one tile
 };
 
 template <int BM, int BN, int WM, int WN>
@@ -193,7 +215,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
   constexpr int kFM = G::kFM, kFN = G::kFN, kRowsWave = BM / WM, kColsWave = BN / WN;
   const int64_t rows = a.count ? rows_of(a.count, a.first, a.piece) : a.tokens;
   const uint32_t tiles_m = uint32_t((rows + BM - 1) / BM), items = tiles_m * a.tiles_n;
-  if (blockIdx.x >= items) return;
+  __shared__ uint32_t turn;
+  Queue q;
+  uint32_t item = blockIdx.x < items ? blockIdx.x : kNoItem;
+  if (a.queue) item = first_item(q, a.queue, items, &turn);
+  if (item == kNoItem) return;
   a.h.base = static_cast<const uint16_t*>(a.h.base) + a.first * a.h.ld;
   a.h.extent = rows;
   int64_t m0, n0;
@@ -214,14 +240,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
       aim[set][row] = col >= 0 && col < BN ? int32_t(col) : -1;
     }
   };
-  open(blockIdx.x);
+  open(item);
   take_aim(0);
-  int set = 0;
-  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x, set ^= 1) {
+  for (int set = 0; item != kNoItem; set ^= 1) {
     g.loop(lds0, lds1, lds2, lds3);
+    const uint32_t k = a.queue && g.tid == 0 ? q.ask() : 0;
     const int64_t m1 = m0, n1 = n0;
     const uint32_t t1 = tn;
-    if (item + gridDim.x < items) open(item + gridDim.x);
 
     // A lane holds of row 16 i + lane % 16 the columns 16 j + 4 (lane / 16) + r.
     // The tile row's maximum and sum go over its lanes, then over the WN waves.
@@ -279,7 +304,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
       s += other_32(s);
       if (g.lane < 16) sums[g.wn][row] = s;
     }
-    lds_barrier();
+    if (a.queue) {
+      item = next_item(q, k, &turn);
+      if (item != kNoItem) open(item);
+    } else {
+      item = kNoItem;
+      lds_barrier();
+    }
     for (int row = g.tid; row < BM; row += G::kThreads) {
       if (m1 + row >= rows) continue;
       float m = peak[0][row], s = sums[0][row];
@@ -298,14 +329,14 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
         *reinterpret_cast<u32x4*>(a.e + (m1 + r) * a.e_ld + n1 + c) = v;
       };
       if (m1 + BM <= rows && n1 + BN <= a.e_ld) {
-        g.template each<true>(lds3, put);
+        g.template each<true>(lds3, put, [] {});
       } else {
         g.template each<false>(lds3, [&](int r, int c, f32x4v lo, f32x4v hi) {
           if (m1 + r < rows && n1 + c < a.e_ld) put(r, c, lo, hi);
-        });
+        }, [] {});
       }
     }
-    if (item + gridDim.x < items) take_aim(set ^ 1);
+    if (item != kNoItem) take_aim(set ^ 1);
   }
 }
 
@@ -549,6 +580,7 @@ struct HiddenGradArgs {
   float* partial;  // a slot of a tile for each piece of the cut, which the tokens that count decide
   uint16_t* dhidden;
   uint32_t tiles_n;
+  uint32_t* queue;
 };
 
 template <int BM, int BN, int WM, int WN>
@@ -561,7 +593,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
   const int64_t rows = rows_of(a.count, a.first, a.piece);
   const uint32_t tiles_m = uint32_t((rows + BM - 1) / BM);
   const Cut cut = cut_tiles(tiles_m * a.tiles_n, (a.vocab + kBK - 1) / kBK, BM);
-  if (blockIdx.x >= cut.items) return;
+  __shared__ uint32_t turn;
+  Queue q;
+  uint32_t item = first_item(q, a.queue, cut.items, &turn);
+  if (item == kNoItem) return;
   a.dz.extent = rows;
   const Target out{a.dhidden, a.hidden, rows, a.hidden, a.list + a.first, nullptr, *a.scale, 0, 0};
   int64_t m0, n0, slot;
@@ -576,13 +611,16 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
     slot = p.slot;
     g.open(a.dz, a.w, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
   };
-  open(blockIdx.x);
-  for (uint32_t item = blockIdx.x; item < cut.items; item += gridDim.x) {
+  open(item);
+  while (item != kNoItem) {
     g.loop(lds0, lds1, lds2, lds3);
+    const uint32_t k = g.tid == 0 ? q.ask() : 0;
     const int64_t m1 = slot >= 0 ? 0 : m0, n1 = slot >= 0 ? 0 : n0;
     const Target t = slot >= 0 ? slot_target<BM>(a.partial, slot, rows - m0) : out;
-    if (item + gridDim.x < cut.items) open(item + gridDim.x);
-    g.write(t, m1, n1, lds3);
+    g.write(t, m1, n1, lds3, [&] {
+      item = next_item(q, k, &turn);
+      if (item != kNoItem) open(item);
+    });
   }
 }
 
@@ -614,6 +652,7 @@ struct VocabGradArgs {
   void* dw;
   int32_t f32, accumulate;
   uint32_t tiles_m, tiles_n;
+  uint32_t* queue;
 };
 
 template <int BM, int BN, int WM, int WN>
@@ -623,7 +662,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void vocab_grad_kernel(VocabGradArg
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
-  const uint32_t items = a.tiles_m * a.tiles_n;
+  __shared__ uint32_t turn;
+  Queue q;
+  uint32_t item = first_item(q, a.queue, a.tiles_m * a.tiles_n, &turn);
+  if (item == kNoItem) return;
   const int64_t rows = rows_of(a.count, a.first, a.piece);
   a.h.base = static_cast<const uint16_t*>(a.h.base) + a.first * a.h.ld;
   const float scale = *a.scale;
@@ -639,12 +681,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void vocab_grad_kernel(VocabGradArg
     n0 = int64_t(tn) * BN;
     g.open(a.dz, a.h, m0, n0, 0, rows, lds0, lds1, lds2);
   };
-  open(blockIdx.x);
-  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+  open(item);
+  while (item != kNoItem) {
     g.loop(lds0, lds1, lds2, lds3);
+    const uint32_t k = g.tid == 0 ? q.ask() : 0;
     const int64_t m1 = m0, n1 = n0;
-    if (item + gridDim.x < items) open(item + gridDim.x);
-    g.write(t, m1, n1, lds3);
+    g.write(t, m1, n1, lds3, [&] {
+      item = next_item(q, k, &turn);
+      if (item != kNoItem) open(item);
+    });
   }
 }
 
@@ -662,7 +707,7 @@ struct Layout {
   int side_w = 256;     // of dW's tiles
   bool sums = false;    // dW's sums go over the pieces in the workspace
   // byte offsets
-  int64_t list = 0, count = 0, h = 0, w = 0, stats = 0, target_z = 0, row_log2 = 0, e = 0, partial = 0, dw_sums = 0,
+  int64_t list = 0, count = 0, queues = 0, h = 0, w = 0, stats = 0, target_z = 0, row_log2 = 0, e = 0, partial = 0, dw_sums = 0,
           bytes = 0;
 };
 
@@ -691,6 +736,7 @@ Layout layout_of(const VocabLossCall& c) {
   };
   if (L.listed) {
     L.count = take(8);  // and the scale
+    L.queues = take(L.pieces * 24 * 4);
     L.list = take(c.tokens * 4);
     L.h = take(c.tokens * L.h_ld * 2);
   }
@@ -755,11 +801,13 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
   const int64_t* targets = c.targets;
   int32_t* count = L.listed ? reinterpret_cast<int32_t*>(ws + L.count) : nullptr;
   float* scale = L.listed ? reinterpret_cast<float*>(count + 1) : nullptr;
+  // 8 words for each of a piece's three products
+  uint32_t* queues = L.listed ? reinterpret_cast<uint32_t*>(ws + L.queues) : nullptr;
   int32_t* list = L.listed ? reinterpret_cast<int32_t*>(ws + L.list) : nullptr;
   Operand h{c.h, nullptr, c.h_ld, 0, c.tokens}, w{c.w, nullptr, c.w_ld, 0, c.vocab};
   if (L.listed) {
     hipLaunchKernelGGL(list_tokens_kernel, dim3(1), dim3(1024), 0, st, targets, c.tokens, c.vocab,
-                       c.grad_loss, list, count, scale, c.loss, c.lse);
+                       c.grad_loss, list, count, scale, c.loss, c.lse, queues, L.pieces * 24);
     TIDE_LAUNCHED();
     uint16_t* rows = reinterpret_cast<uint16_t*>(ws + L.h);
     const int64_t n = c.tokens * (L.h_ld / 8);
@@ -799,7 +847,9 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     a.e = e;
     a.e_ld = L.e_ld;
     a.tiles_n = uint32_t(L.tiles_n);
-    const dim3 grid(resident_groups((L.piece + L.rows - 1) / L.rows * L.tiles_n, L.rows));
+    const int64_t tiles = (L.piece + L.rows - 1) / L.rows * L.tiles_n;
+    a.queue = L.listed ? queues + p * 24 : nullptr;
+    const dim3 grid(L.listed ? resident_groups(tiles, L.rows) : unsigned(tiles));
     if (L.rows == 256)
       hipLaunchKernelGGL((logits_kernel<256, 256, 2, 4>), grid, dim3(512), 0, st, a);
     else if (L.rows == 128)
@@ -837,6 +887,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     d.partial = reinterpret_cast<float*>(ws + L.partial);
     d.dhidden = static_cast<uint16_t*>(c.dhidden);
     d.tiles_n = uint32_t((c.hidden + L.side_h - 1) / L.side_h);
+    d.queue = queues + p * 24 + 8;
     // as many workgroups as any cut has items for (a cut with pieces fills the slots at most)
     const int64_t tiles_h = (L.piece + L.side_h - 1) / L.side_h * d.tiles_n;
     const dim3 grid_h(L.h_splits ? unsigned(tile_slots(L.side_h)) : resident_groups(tiles_h, L.side_h));
@@ -866,6 +917,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     v.sum_in = p > 0 ? sums : nullptr;
     v.sum_out = p + 1 < L.pieces ? sums : nullptr;
     v.dw = c.dw;
+    v.queue = queues + p * 24 + 16;
     v.f32 = c.dw_f32;
     v.accumulate = c.accumulate || (p > 0 && !L.sums);
     const int64_t side_w = L.side_w;

@@ -38,9 +38,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void weight_grad_kernel(WeightGradA
   g.open(a.dy, a.x, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
   g.loop(lds0, lds1, lds2, lds3);
   if (p.slot >= 0)
-    g.write(slot_target<BM>(a.partial, p.slot, a.outs - m0), 0, 0, lds3);
+    g.write(slot_target<BM>(a.partial, p.slot, a.outs - m0), 0, 0, lds3, [] {});
   else
-    g.write(Target{a.dw, a.ins, a.outs, a.ins, nullptr, nullptr, a.alpha, a.f32, a.accumulate}, m0, n0, lds3);
+    g.write(Target{a.dw, a.ins, a.outs, a.ins, nullptr, nullptr, a.alpha, a.f32, a.accumulate}, m0, n0, lds3,
+            [] {});
 }
 
 template <int SIDE>

@@ -22,7 +22,11 @@ Aggressors (one call each, repeated back to back on their own stream):
                      removes from the all-gather).
 Victims (on a second stream): the 256 MiB elementwise kernel (y = a*x + b),
 a small-M GEMM (256 x 8192 x 8192, bf16) and a large GEMM (8192^3, bf16), both
-torch.matmul (the vendor GEMM library).  Reported per pair: the victim's p50
+torch.matmul (the vendor GEMM library).  On request (--victims), the library's
+own kernels of the backward pass that a reduce-scatter overlaps: a down
+projection's weight gradient from its 8-bit checkpoint (8192 tokens, 4096 x
+14336) and the vocabulary loss with its gradients (2048 tokens, 32000 x 4096).
+Reported per pair: the victim's p50
 latency alone and beside the aggressor (only launches that ran entirely
 inside the aggressor's run count), the slowdown, the aggressor's own time
 alone and beside the victim, and its CU-ms per call (CUs held x time), the
@@ -54,6 +58,9 @@ ROOT = os.path.dirname(HERE)
 
 ELEMENTWISE_ELEMS = 64 * 2**20  # 256 MiB of fp32 in, 256 MiB out
 GEMMS = {"gemm_256x8192x8192": (256, 8192, 8192), "gemm_8192x8192x8192": (8192, 8192, 8192)}
+# tokens, out features, in features; tokens, hidden size, vocabulary
+WEIGHT_GRADS = {"weight_grad_8192x4096x14336": (8192, 4096, 14336)}
+VOCAB_LOSSES = {"vocab_loss_grad_2048x4096x32000": (2048, 4096, 32000)}
 
 
 def _median(v):
@@ -125,6 +132,27 @@ class Study:
             x = torch.randn(ELEMENTWISE_ELEMS, device="cuda")
             y = torch.empty_like(x)
             return lambda s: tide.victim_axpb(x, y, 1.5, 0.25, stream=s)
+        if name in WEIGHT_GRADS:
+            tokens, outs, ins = WEIGHT_GRADS[name]
+            x = torch.randn(tokens, ins, device="cuda").to(torch.bfloat16)
+            dy = torch.randn(tokens, outs, device="cuda").to(torch.bfloat16)
+            c, sc = tide.checkpoint_layout(ins)
+            codes = torch.empty(tokens, c, dtype=torch.int8, device="cuda")
+            scales = torch.empty(tokens, sc, dtype=torch.uint8, device="cuda")
+            tide.checkpoint_pack(x, codes, scales)
+            dw = torch.empty(outs, ins, dtype=torch.bfloat16, device="cuda")
+            torch.cuda.synchronize()
+            return tide.checkpoint_weight_grad_call(dy, codes, scales, dw)
+        if name in VOCAB_LOSSES:
+            tokens, size, vocab = VOCAB_LOSSES[name]
+            h = torch.randn(tokens, size, device="cuda").to(torch.bfloat16)
+            w = (torch.randn(vocab, size, device="cuda") * size**-0.5).to(torch.bfloat16)
+            t = torch.randint(vocab, (tokens,), device="cuda")
+            g = torch.full((tokens,), 1.0 / tokens, device="cuda")
+            loss = torch.empty(tokens, device="cuda")
+            dh, dw = torch.empty_like(h), torch.empty_like(w)
+            torch.cuda.synchronize()
+            return tide.vocab_loss_grad_call(h, w, t, g, loss, None, dh, dw)
         m, k, n = GEMMS[name]
         a = torch.randn(m, k, device="cuda").to(torch.bfloat16)
         b = torch.randn(k, n, device="cuda").to(torch.bfloat16)
@@ -399,7 +427,8 @@ def main(argv=None):
     ap.add_argument("--workload", default="llama3.1-8b-layer")
     ap.add_argument("--out", required=True, help="folder for the JSON result")
     ap.add_argument("--profiles", default=None, help="also write the text summary here")
-    ap.add_argument("--victims", default="elementwise," + ",".join(GEMMS))
+    ap.add_argument("--victims", default="elementwise," + ",".join(GEMMS),
+                    help="also: " + ", ".join([*WEIGHT_GRADS, *VOCAB_LOSSES]))
     ap.add_argument("--per-call", action="store_true", help="one aggressor call inside a victim sequence")
     args = ap.parse_args(argv)
     if ROOT not in sys.path:

@@ -466,9 +466,10 @@ _CODES = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_INT8}
 def _on_device(t, what):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
-    if not t.is_cuda:
+    device = t.get_device()  # -1 on the host
+    if device < 0:
         raise ValueError(f"{what}: expected a GPU tensor, got {t.device}")
-    if t.get_device() != torch.cuda.current_device():
+    if device != torch.cuda.current_device():
         raise ValueError(f"{what}: lives on {t.device}, but the kernels run on the current device "
                          f"cuda:{torch.cuda.current_device()}")
 

@@ -48,6 +48,9 @@ class Run:
         self.loss = torch.full((self.tokens,), 77.0, device="cuda")
         self.lse = None if null_lse else torch.full((self.tokens,), 77.0, device="cuda")
         targets = torch.from_numpy(t).cuda()
+        grads = None if g is None else torch.from_numpy(g).cuda()
+        if kw.get("stream") is not None:
+            kw["stream"].wait_stream(torch.cuda.current_stream())  # the operands and canaries
         if g is None:
             tide.vocab_loss(*dev, targets, self.loss, self.lse, **kw)
             return
@@ -56,7 +59,9 @@ class Run:
                              dtype=torch.float32 if dtype == "f32" else torch.bfloat16)
         if old is not None:
             self.dw.copy_(old)
-        tide.vocab_loss_grad(*dev, targets, torch.from_numpy(g).cuda(), self.loss, self.lse, self.dh, self.dw,
+        if kw.get("stream") is not None:
+            kw["stream"].wait_stream(torch.cuda.current_stream())
+        tide.vocab_loss_grad(*dev, targets, grads, self.loss, self.lse, self.dh, self.dw,
                              accumulate=old is not None, **kw)
 
     def check(self, want, old=None):

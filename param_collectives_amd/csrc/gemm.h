@@ -247,14 +247,15 @@ struct Side {
     load_to_lds(uniform(base + s * step), off[i], lds + (i * THREADS + wave_index() * 64) * 16);
   }
 
-  // kPacked: widen what fetch() loaded and write it to LDS.
-  __device__ __forceinline__ void settle(char* lds, const Held& held) {
+  // kPacked: widen what fetch() loaded, halves [h0, h1) of each unit, and write
+  // it to LDS.
+  __device__ __forceinline__ void settle(char* lds, const Held& held, int h0 = 0, int h1 = 2) {
     if constexpr (kPacked) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
         char* to = lds + renew(put[i]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = h0; h < h1; ++h) {
           const u32x2 lo = widen4<CODE>(held.codes[i][2 * h], held.scale[i]);
           const u32x2 hi = widen4<CODE>(held.codes[i][2 * h + 1], held.scale[i]);
           *reinterpret_cast<u32x4*>(to + 16 * h) = u32x4{lo.x, lo.y, hi.x, hi.y};
@@ -418,6 +419,10 @@ struct Gemm {
   // the products' sums (spilled in the step loop: 12% slower); with int8 codes
   // there is no time to work them out (3% slower), nor need without codes.
   static constexpr bool kLean = kPacked && CODE == Code::kE4m3;
+  // Codes are widened beside the products, e4m3 ones half a unit at a time with a
+  // row of products between the halves (4096^3: 107.4 -> 105.5 us; 8192 x 4096 x
+  // 14336: 773 -> 762 us), int8 ones at once (in halves 846 -> 853 us).
+  static constexpr int kHalves = kPacked && CODE == Code::kE4m3 ? 2 : 1;
   using SA = Side<FA, CODE, BM, kFM, kThreads, kLean>;
   using SB = Side<FB, CODE, BN, kFN, kThreads, kLean>;
   static constexpr int kStage = SA::kBytes + SB::kBytes;  // bytes of each of the four stages
@@ -486,9 +491,9 @@ struct Gemm {
         if (SB::kPacked) sb.template fetch<false>(nullptr, nb, s + ahead, 0, tid);
       }
     };
-    auto settle = [&](char* lds, int set) {
-      sa.settle(lds, ha[set]);
-      sb.settle(lds + SA::kBytes, hb[set]);
+    auto settle = [&](char* lds, int set, int h) {
+      sa.settle(lds, ha[set], h * 2 / kHalves, (h + 1) * 2 / kHalves);
+      sb.settle(lds + SA::kBytes, hb[set], h * 2 / kHalves, (h + 1) * 2 / kHalves);
     };
 
     auto begin = [&](const char* lds) {
@@ -499,8 +504,8 @@ struct Gemm {
     };
     // Multiplies the step in `now`, whose first fragments have been read;
     // MORE: reads the first ones of the step in `next`.  A fragment is read two
-    // rows of products before its own; part(i) follows row i, halfway() the
-    // middle one.
+    // rows of products before its own; part(i) follows row i, halfway(h) the
+    // middle ones.
     auto multiply = [&](const char* now, const char* next, bool more, auto part, auto halfway) {
       bf16x8 nb[kFN], a[kFM + 2];
       a[0] = fa[0];
@@ -519,7 +524,8 @@ struct Gemm {
 #pragma unroll
         for (int j = 0; j < kFN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], a[i], acc[i][j], 0, 0, 0);
         part(i);
-        if (i == kFM / 2 - 1) halfway();
+        if (i == kFM / 2 - kHalves) halfway(0);
+        if (kHalves == 2 && i == kFM / 2) halfway(1);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (more) {
@@ -550,8 +556,9 @@ struct Gemm {
     auto step = [&](char* now, char* next, char* to2, char* to3, int set) {
       wait_loads<kAfter, kPacked>();
       bare_barrier();
-      multiply(now, next, true, [&](int i) { load(to3, i); }, [&] {
-        settle(to2, set);
+      multiply(now, next, true, [&](int i) { load(to3, i); }, [&](int h) {
+        settle(to2, set, h);
+        if (h + 1 < kHalves) return;
         if (SA::kPacked) sa.template fetch<false>(nullptr, ha[set], s + 4, 0, tid);
         if (SB::kPacked) sb.template fetch<false>(nullptr, hb[set], s + 4, 0, tid);
       });
@@ -590,7 +597,7 @@ struct Gemm {
     bare_barrier();
     if (left) {
       begin(l3);
-      multiply(l3, l3, false, [](int) {}, [] {});
+      multiply(l3, l3, false, [](int) {}, [](int) {});
     }
     if (rounds > 0) {
       begin(l0);
@@ -602,14 +609,14 @@ struct Gemm {
       }
       wait_loads<kAfter, kPacked>();
       bare_barrier();
-      multiply(l0, l1, true, [&](int i) { load(l3, i); }, [&] { settle(l2, 0); });
+      multiply(l0, l1, true, [&](int i) { load(l3, i); }, [&](int h) { settle(l2, 0, h); });
       wait_loads<SA::kLoads + SB::kLoads, kPacked>();  // what was started after step i + 1's: codes and the last step's
       bare_barrier();
-      multiply(l1, l2, true, [](int) {}, [&] { settle(l3, 1); });
+      multiply(l1, l2, true, [](int) {}, [&](int h) { settle(l3, 1, h); });
       wait_loads<0, kPacked>();
       bare_barrier();
-      multiply(l2, l3, true, [](int) {}, [] {});
-      multiply(l3, l3, false, [](int) {}, [] {});
+      multiply(l2, l3, true, [](int) {}, [](int) {});
+      multiply(l3, l3, false, [](int) {}, [](int) {});
     }
     lds_barrier();
   }

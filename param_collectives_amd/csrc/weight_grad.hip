@@ -90,9 +90,6 @@ WeightGradPlan plan_weight_grad(int64_t tokens, int64_t outs, int64_t ins, bool 
   const Cut cb = cut_tiles(big, steps, 256), cs = cut_tiles(small, steps, 128);
   WeightGradPlan p;
   p.side = cut_cost(cb, steps, 256) <= cut_cost(cs, steps, 128) ? 256 : 128;
-#ifdef FORCE_SIDE
-  p.side = FORCE_SIDE;
-#endif
   p.cut = p.side == 256 ? cb : cs;
   p.tiles_m = (outs + p.side - 1) / p.side;
   p.tiles_n = (ins + p.side - 1) / p.side;

@@ -397,7 +397,8 @@ tide_status tide_stock_chunk_cat(tide_plan* plan, const uint16_t* const* grads, 
  * restored value is 0 or a normal bf16 number, so restoring rounds nothing.
  *
  * Sizes: rows below 2^31, cols and row strides up to 2^22, a matrix up to
- * 2^34 elements (else TIDE_ERR_RANGE).  Row strides are in elements and at
+ * 2^34 elements with its rows filled up to a multiple of 64 (else
+ * TIDE_ERR_RANGE).  Row strides are in elements and at
  * least the row's length.  Any size may be 0.
  * ------------------------------------------------------------------------ */
 
@@ -494,7 +495,7 @@ tide_status tide_checkpoint_weight_grad(const uint16_t* dy, int64_t rows, int64_
  *           exponentials of at most 2 GiB worth of tokens at a time (at least
  *           256 tokens), 2 bytes each.
  * Sizes: tokens up to 2^24 (0 allowed: dweight becomes 0, or stays), vocab and
- * hidden_size in [1, 2^22], matrices up to 2^34 elements.
+ * hidden_size in [1, 2^22], matrices up to 2^34 elements as above.
  * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
  * ------------------------------------------------------------------------ */
 tide_status tide_vocab_loss_workspace(const uint16_t* hidden, int64_t hidden_stride, const uint16_t* weight,

@@ -30,7 +30,8 @@ tide_status check_matrix(const char* name, int64_t rows, int64_t cols, int64_t s
   if (rows > kMaxTokens || cols > kMaxFeatures || stride > kMaxFeatures)
     return tide::set_error(TIDE_ERR_RANGE, n + ": more than 2^31 - 1 rows, or a row or row stride above 2^22 elements");
   if (stride < cols) return invalid(n + ": the row stride is smaller than the row");
-  if (rows > 0 && cols > kMaxElems / rows) return tide::set_error(TIDE_ERR_RANGE, n + ": more than 2^34 elements");
+  if (rows > 0 && (cols + 63) / 64 * 64 > kMaxElems / rows)
+    return tide::set_error(TIDE_ERR_RANGE, n + ": more than 2^34 elements, with rows filled up to a multiple of 64");
   return TIDE_OK;
 }
 

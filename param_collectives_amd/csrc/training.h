@@ -12,8 +12,9 @@ constexpr int64_t kPackBlock = 32;                      // values that share an 
 constexpr int64_t kMaxFeatures = int64_t(1) << 22;      // features, hidden size, vocabulary, row pitch: 32-bit tile offsets
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;  // tokens (rows)
 constexpr int64_t kMaxLossTokens = int64_t(1) << 24;    // tokens of one vocabulary loss
-// Elements of one matrix: a launch counts its threads in 32 bits, and the
-// element-wise kernels give a thread at least 4.
+// Elements of one matrix with its rows filled up to a multiple of 64, the widest
+// pitch a copy of it may get: a launch counts its threads in 32 bits, and the
+// element-wise kernels give a thread 8.
 constexpr int64_t kMaxElems = int64_t(1) << 34;
 
 struct PackCall {

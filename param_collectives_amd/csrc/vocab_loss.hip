@@ -637,9 +637,7 @@ __global__ __launch_bounds__(256) void join_hidden_kernel(HiddenGradArgs a) {
 }
 
 __global__ __launch_bounds__(256) void clear_kernel(uint16_t* p, int64_t n) {
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 2;
-  if (i < n) p[i] = 0;
-  if (i + 1 < n) p[i + 1] = 0;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) p[i] = 0;
 }
 
 struct VocabGradArgs {
@@ -717,8 +715,10 @@ Layout layout_of(const VocabLossCall& c) {
   L.h_ld = up(c.hidden, 64);
   L.e_ld = up(c.vocab, 64);
   // A piece's exponentials take at most 2 GiB (and at least one tile of rows);
-  // without them a piece is 32768 tokens.
+  // without them a piece is 32768 tokens.  (And at most 2^22 rows, each of which
+  // gets a workgroup: a launch counts its threads in 32 bits.)
   int64_t most = grad ? (int64_t(1) << 31) / (L.e_ld * 2) / 256 * 256 : 32768;
+  if (most > int64_t(1) << 22) most = int64_t(1) << 22;
   if (most < 256) most = 256;
   L.piece = c.tokens < most ? c.tokens : most;
   L.pieces = L.piece > 0 ? (c.tokens + L.piece - 1) / L.piece : 1;
@@ -758,9 +758,6 @@ Layout layout_of(const VocabLossCall& c) {
     L.side_h = cut_cost(cut_tiles(big, steps, 256), steps, 256) <= cut_cost(cut_tiles(small, steps, 128), steps, 128)
                    ? 256
                    : 128;
-#ifdef FORCE_SIDE
-    L.side_h = FORCE_SIDE;
-#endif
     const int64_t most = L.side_h == 256 ? big * (steps / 32) : small * (steps / 16);
     const int64_t slots = most < tile_slots(L.side_h) ? most : tile_slots(L.side_h);
     L.h_splits = steps >= (L.side_h == 256 ? 64 : 32) && slots > 1;
@@ -790,7 +787,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
   if (c.tokens == 0) {
     if (!c.dhidden_wanted || c.accumulate) return 0;
     const int64_t bytes = c.vocab * c.hidden * (c.dw_f32 ? 4 : 2);
-    hipLaunchKernelGGL(clear_kernel, dim3(unsigned((bytes / 4 + 256) / 256)), dim3(256), 0,
+    hipLaunchKernelGGL(clear_kernel, dim3(2048), dim3(256), 0,
                        static_cast<hipStream_t>(stream), static_cast<uint16_t*>(c.dw), bytes / 2);
     return int(hipGetLastError());
   }

@@ -54,6 +54,15 @@ def test_pack_and_unpack_refusals(tide, change, status):
     assert got == status and tide.lib.tide_last_error()
 
 
+def test_short_rows_count_with_their_filling(tide):
+    # 2^31 - 1 rows of one value take 32 codes each, and 64 elements in an aligned copy
+    for rows, status in (((1 << 31) - 1, RANGE), ((1 << 28) + 1, RANGE), (1 << 28, INVALID)):
+        assert tide.lib.tide_checkpoint_pack(None, 1, rows, 1, 1, 0, P, P, None) == status
+        assert tide.lib.tide_checkpoint_unpack(P, P, 0, rows, 1, None, 1, 1, None) == status
+        need = ctypes.c_int64()
+        assert tide.lib.tide_checkpoint_weight_grad_workspace(None, rows, 1, 1, 64, ctypes.byref(need)) == status
+
+
 def test_empty_matrices_need_no_pointers(tide):
     for rows, cols in ((0, 64), (4, 0), (0, 0)):
         assert tide.lib.tide_checkpoint_pack(None, 1, rows, cols, cols, 0, None, None, None) == 0

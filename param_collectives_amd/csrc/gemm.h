@@ -693,15 +693,24 @@ struct Queue {
     asm volatile("s_getreg_b32 %0, hwreg(HW_REG_XCC_ID)" : "=s"(x));
     x &= 7;
   }
-  // One thread's: asks for an item of the own share; settles what ask() gave.
-  __device__ __forceinline__ uint32_t ask() { return atomicAdd(words + x, 1u); }
-  __device__ __forceinline__ uint32_t settle(uint32_t k) {
-    for (int tries = 0; tries < 8; ++tries) {
-      if (k < (items >> 3) + (x < (items & 7) ? 1u : 0u)) return 8 * k + x;
-      x = (x + 1) & 7;
-      if (tries < 7) k = atomicAdd(words + x, 1u);
+  __device__ __forceinline__ uint32_t share(uint32_t of) const { return (items >> 3) + (of < (items & 7) ? 1u : 0u); }
+  // The first wave's: its first lane asks for an item of the own share, and the
+  // wave settles what ask() gave.  Whether the others' shares have items left is
+  // looked up for all of them at once (asked for one after the other, the last
+  // look of each workgroup took 10 us).
+  __device__ __forceinline__ uint32_t ask() { return threadIdx.x == 0 ? atomicAdd(words + x, 1u) : 0u; }
+  __device__ __forceinline__ uint32_t settle(uint32_t asked) {
+    uint32_t k = __builtin_amdgcn_readfirstlane(asked), used = 0;
+    while (k >= share(x)) {
+      used |= 1u << x;
+      const uint32_t lane = threadIdx.x;
+      const bool left = lane < 8 && __hip_atomic_load(words + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < share(lane);
+      const uint32_t open = uint32_t(__ballot(left)) & ~used;
+      if (open == 0) return kNoItem;
+      x = (x + __builtin_ctz((open | open << 8) >> x)) & 7;
+      k = __builtin_amdgcn_readfirstlane(ask());
     }
-    return kNoItem;
+    return 8 * k + x;
   }
 };
 

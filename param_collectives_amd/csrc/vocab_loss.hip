@@ -80,18 +80,24 @@ __device__ __forceinline__ int64_t rows_of(const int32_t* count, int64_t first, 
 // A workgroup's first item of a queue.
 __device__ __forceinline__ uint32_t first_item(Queue& q, uint32_t* words, uint32_t items, uint32_t* turn) {
   q.setup(words, items);
-  if (threadIdx.x == 0) *turn = q.settle(q.ask());
+  if (wave_index() == 0) {
+    const uint32_t got = q.settle(q.ask());
+    if (threadIdx.x == 0) *turn = got;
+  }
   __syncthreads();
   const uint32_t item = __builtin_amdgcn_readfirstlane(*turn);
   __syncthreads();
   return item;
 }
 
-// The workgroup's next item, which its first thread asked for as k (at the end of
-// a tile's sums: earlier, a workgroup would take what one that is still to start
-// should have).
+// The workgroup's next item, which was asked for as k (at the end of a tile's
+// sums: earlier, a workgroup would take what one that is still to start should
+// have).
 __device__ __forceinline__ uint32_t next_item(Queue& q, uint32_t k, uint32_t* turn) {
-  if (threadIdx.x == 0) *turn = q.settle(k);
+  if (wave_index() == 0) {
+    const uint32_t got = q.settle(k);
+    if (threadIdx.x == 0) *turn = got;
+  }
   lds_barrier();
   return __builtin_amdgcn_readfirstlane(*turn);
 }
@@ -244,7 +250,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
   take_aim(0);
   for (int set = 0; item != kNoItem; set ^= 1) {
     g.loop(lds0, lds1, lds2, lds3);
-    const uint32_t k = a.queue && g.tid == 0 ? q.ask() : 0;
+    const uint32_t k = a.queue ? q.ask() : 0;
     const int64_t m1 = m0, n1 = n0;
     const uint32_t t1 = tn;
 
@@ -614,7 +620,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
   open(item);
   while (item != kNoItem) {
     g.loop(lds0, lds1, lds2, lds3);
-    const uint32_t k = g.tid == 0 ? q.ask() : 0;
+    const uint32_t k = q.ask();
     const int64_t m1 = slot >= 0 ? 0 : m0, n1 = slot >= 0 ? 0 : n0;
     const Target t = slot >= 0 ? slot_target<BM>(a.partial, slot, rows - m0) : out;
     g.write(t, m1, n1, lds3, [&] {
@@ -682,7 +688,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void vocab_grad_kernel(VocabGradArg
   open(item);
   while (item != kNoItem) {
     g.loop(lds0, lds1, lds2, lds3);
-    const uint32_t k = g.tid == 0 ? q.ask() : 0;
+    const uint32_t k = q.ask();
     const int64_t m1 = m0, n1 = n0;
     g.write(t, m1, n1, lds3, [&] {
       item = next_item(q, k, &turn);

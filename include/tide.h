@@ -416,8 +416,7 @@ tide_status tide_checkpoint_layout(int64_t cols, int64_t* code_cols, int64_t* sc
 /*
  * Pack a matrix.
  *   x       rows x cols values of `dtype` (TIDE_DTYPE_*), rows `row_stride`
- *           elements apart, aligned to the element; 16-byte aligned rows are
- *           read 16 bytes at a time
+ *           elements apart, aligned to the element
  *   codes   16-byte aligned, written in full;  scales written in full
  * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
  */

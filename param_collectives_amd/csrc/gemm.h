@@ -39,6 +39,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// 16 bytes of a caller's matrix, aligned to its elements only: global memory
+// takes such accesses whole.
+typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+typedef f32x4v any_f32x4 __attribute__((aligned(4)));
 
 #define TIDE_GLOBAL __attribute__((address_space(1)))
 #define TIDE_LDS __attribute__((address_space(3)))
@@ -315,6 +319,16 @@ __device__ __forceinline__ f32x4v add4(f32x4v a, f32x4v b) {
   return b;
 }
 
+// 8 bf16 values from s, of which `left` exist (any number): zeros for the rest.
+__device__ __forceinline__ u32x4 eight_of(const uint16_t* s, int64_t left) {
+  if (left >= 8) return *reinterpret_cast<const any_u32x4*>(s);
+  u32x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = (2 * j < left ? uint32_t(s[2 * j]) : 0u) | (2 * j + 1 < left ? uint32_t(s[2 * j + 1]) : 0u) << 16;
+  return v;
+}
+
 // Where a product goes: alpha (add + s) (+ old), rounded once to fp32 or bf16.
 struct Target {
   void* base;
@@ -325,18 +339,12 @@ struct Target {
   int32_t f32, accumulate;
 };
 
-// Whether the 8 columns from a multiple of 8 of any row go out as vectors.
-__device__ __forceinline__ bool target_vectors(const Target& t) {
-  return (reinterpret_cast<uintptr_t>(t.base) & 15) == 0 && t.ld % (t.f32 ? 4 : 8) == 0 &&
-         (t.add == nullptr || ((reinterpret_cast<uintptr_t>(t.add) & 15) == 0 && t.ld % 4 == 0));
-}
-
-// Writes 8 columns of row m from column n, all of them in range and aligned.
+// Writes 8 columns of row m from column n, all of them in range.
 __device__ __forceinline__ void put_vectors(const Target& t, int64_t m, int64_t n, f32x4v lo, f32x4v hi) {
   const int64_t at = (t.row_map ? int64_t(t.row_map[m]) : m) * t.ld + n;
   if (t.add) {
-    lo = add4(*reinterpret_cast<const f32x4v*>(t.add + at), lo);
-    hi = add4(*reinterpret_cast<const f32x4v*>(t.add + at + 4), hi);
+    lo = add4(*reinterpret_cast<const any_f32x4*>(t.add + at), lo);
+    hi = add4(*reinterpret_cast<const any_f32x4*>(t.add + at + 4), hi);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -346,13 +354,13 @@ __device__ __forceinline__ void put_vectors(const Target& t, int64_t m, int64_t 
   if (t.f32) {
     float* d = static_cast<float*>(t.base) + at;
     if (t.accumulate) {
-      lo = add4(*reinterpret_cast<const f32x4v*>(d), lo);
-      hi = add4(*reinterpret_cast<const f32x4v*>(d + 4), hi);
+      lo = add4(*reinterpret_cast<const any_f32x4*>(d), lo);
+      hi = add4(*reinterpret_cast<const any_f32x4*>(d + 4), hi);
     }
-    *reinterpret_cast<f32x4v*>(d) = lo;
-    *reinterpret_cast<f32x4v*>(d + 4) = hi;
+    *reinterpret_cast<any_f32x4*>(d) = lo;
+    *reinterpret_cast<any_f32x4*>(d + 4) = hi;
   } else {
-    u32x4* d = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(t.base) + at);
+    any_u32x4* d = reinterpret_cast<any_u32x4*>(static_cast<uint16_t*>(t.base) + at);
     if (t.accumulate) {
       const u32x4 o = *d;
       lo = add4(f32x4v{low_bf16(o[0]), high_bf16(o[0]), low_bf16(o[1]), high_bf16(o[1])}, lo);
@@ -362,9 +370,10 @@ __device__ __forceinline__ void put_vectors(const Target& t, int64_t m, int64_t 
   }
 }
 
-// The same one by one, of those in range.
+// The same, of those in range, which at the row's end go one by one.
 __device__ __forceinline__ void put_some(const Target& t, int64_t m, int64_t n, f32x4v lo, f32x4v hi) {
-  if (m >= t.rows) return;
+  if (m >= t.rows || n >= t.cols) return;
+  if (n + 8 <= t.cols) return put_vectors(t, m, n, lo, hi);
   const int64_t at = (t.row_map ? int64_t(t.row_map[m]) : m) * t.ld + n;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -660,7 +669,7 @@ struct Gemm {
   // Writes the tile at (m0, n0) to `t`.
   template <typename H>
   __device__ __forceinline__ void write(const Target& t, int64_t m0, int64_t n0, char* lds, H halfway) {
-    if (n0 + BN <= t.cols && target_vectors(t))
+    if (n0 + BN <= t.cols)
       each<true>(
           lds,
           [&](int r, int c, f32x4v lo, f32x4v hi) {
@@ -764,10 +773,7 @@ __device__ __forceinline__ void join_tile(const float* partial, const Cut& c, ui
     lo = add4(lo, *reinterpret_cast<const f32x4v*>(p));
     hi = add4(hi, *reinterpret_cast<const f32x4v*>(p + 4));
   }
-  if (n + 8 <= t.cols && target_vectors(t))
-    put_vectors(t, m, n, lo, hi);
-  else
-    put_some(t, m, n, lo, hi);
+  put_some(t, m, n, lo, hi);
 }
 
 }  // namespace tide

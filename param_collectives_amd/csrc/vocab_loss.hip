@@ -165,7 +165,7 @@ __global__ __launch_bounds__(1024) void list_tokens_kernel(const int64_t* target
 // whose tokens are not listed.
 __global__ __launch_bounds__(256) void gather_rows_kernel(const uint16_t* hidden, int64_t ld, int64_t cols,
                                                           const int32_t* list, const int32_t* count, uint16_t* out,
-                                                          int64_t out_ld, int32_t vec, int64_t tokens,
+                                                          int64_t out_ld, int64_t tokens,
                                                           const int64_t* targets, int64_t vocab, uint16_t* dhidden) {
   const int64_t groups = out_ld / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t r = i / groups, c = (i - r * groups) * 8;
@@ -177,16 +177,7 @@ __global__ __launch_bounds__(256) void gather_rows_kernel(const uint16_t* hidden
     }
   }
   if (r >= *count) return;
-  const uint16_t* s = hidden + int64_t(list[r]) * ld + c;
-  u32x4 v;
-  if (vec && c + 8 <= cols) {
-    v = *reinterpret_cast<const u32x4*>(s);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = (c + 2 * j < cols ? uint32_t(s[2 * j]) : 0u) | (c + 2 * j + 1 < cols ? uint32_t(s[2 * j + 1]) : 0u) << 16;
-  }
-  *reinterpret_cast<u32x4*>(out + r * out_ld + c) = v;
+  *reinterpret_cast<u32x4*>(out + r * out_ld + c) = eight_of(hidden + int64_t(list[r]) * ld + c, cols - c);
 }
 
 // ------------------------------------------------------------ logits
@@ -816,7 +807,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     const int64_t n = c.tokens * (L.h_ld / 8);
     hipLaunchKernelGGL(gather_rows_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st,
                        static_cast<const uint16_t*>(c.h), c.h_ld, c.hidden, list, count, rows, L.h_ld,
-                       int32_t(rows_aligned(c.h, c.h_ld, c.hidden)), c.tokens, targets, c.vocab,
+                       c.tokens, targets, c.vocab,
                        grad ? static_cast<uint16_t*>(c.dhidden) : nullptr);
     TIDE_LAUNCHED();
     h.base = rows;

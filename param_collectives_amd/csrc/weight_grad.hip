@@ -58,12 +58,7 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t* src, in
   const int64_t groups = ld / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= rows * groups) return;
   const int64_t r = i / groups, c = (i - r * groups) * 8;
-  const uint16_t* s = src + r * src_ld + c;
-  uint32_t v[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    v[j] = (c + 2 * j < cols ? uint32_t(s[2 * j]) : 0u) | (c + 2 * j + 1 < cols ? uint32_t(s[2 * j + 1]) : 0u) << 16;
-  *reinterpret_cast<u32x4*>(dst + r * ld + c) = u32x4{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<u32x4*>(dst + r * ld + c) = eight_of(src + r * src_ld + c, cols - c);
 }
 
 }  // namespace

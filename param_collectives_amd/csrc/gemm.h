@@ -723,31 +723,50 @@ struct Queue {
   }
 };
 
+// Item 8 k + x of `total` -> the k-th of XCD x's share, the shares contiguous.
+__device__ __forceinline__ uint32_t nth_of_share(uint32_t item, uint32_t total) {
+  const uint32_t x = item & 7, each = total >> 3, more = total & 7;
+  return x * each + (x < more ? x : more) + (item >> 3);
+}
+
 // The tile of an item: XCD x's share of the tiles is contiguous, in an order
 // that walks `group` tile rows before it moves to the next tile column, so that
 // what an XCD works on at one time shares operand tiles.  (A group of 4 measured
 // against 2, 8 and 16 on 4096 x 128000 x 4096: 1.5%, 1.5% and 6% faster.)
 __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n, uint32_t group, uint32_t* tm,
                                         uint32_t* tn) {
-  const uint32_t total = tiles_m * tiles_n, x = bid & 7, each = total >> 3, more = total & 7;
-  const uint32_t t = x * each + (x < more ? x : more) + (bid >> 3);
+  const uint32_t t = nth_of_share(bid, tiles_m * tiles_n);
   const uint32_t band = t / (group * tiles_n), in = t - band * group * tiles_n;
   const uint32_t rows = band * group + group <= tiles_m ? group : tiles_m - band * group;
   *tm = __builtin_amdgcn_readfirstlane(band * group + in % rows);
   *tn = __builtin_amdgcn_readfirstlane(in / rows);
 }
 
-// The tile, and the range of steps, of an item of a cut (training.h).
+// The tile, and the range of steps, of an item of a cut (training.h).  RANGES: an
+// XCD's share of the pieces is contiguous with the splits outside, so it reads a
+// range of k of both operands once, instead of some tiles' whole k (for dH, whose
+// operands are large: the loss with gradients of 667 x 2048 x 50001, 240 pieces,
+// 508 -> 485 us).  Otherwise the XCD keeps its tiles (weight gradients: no different
+// at 8192 x 4096 x 14336, and 22.6 instead of 25.0 us at 2048 x 768 x 2048).
 struct Piece {
   uint32_t tile;
   int64_t k_first, k_end;  // of a depth of k
   int64_t slot;            // of its partial sums; -1: it is a whole tile
 };
+template <bool RANGES>
 __device__ __forceinline__ Piece piece_of(const Cut& c, uint32_t item, int64_t depth) {
   if (item < c.full) return Piece{item, 0, depth, -1};
-  const uint32_t q = item - c.full, rest = c.tiles - c.full, split = q / rest;
+  const uint32_t rest = c.tiles - c.full, i = item - c.full, q = RANGES ? nth_of_share(i, c.items - c.full) : i;
+  const uint32_t split = q / rest;
+  uint32_t r = q - split * rest;
+  if constexpr (RANGES) {
+    // neighbours: tile full + 8 j + x is x's j-th (tile_of)
+    const uint32_t u = r, each = rest >> 3, more = rest & 7, large = more * (each + 1);
+    const uint32_t x = u < large ? u / (each + 1) : more + (u - large) / each;
+    r = 8 * (u < large ? u - x * (each + 1) : (u - large) - (x - more) * each) + x;
+  }
   const int64_t k0 = int64_t(split) * c.per * kBK, k1 = k0 + int64_t(c.per) * kBK;
-  return Piece{c.full + q - split * rest, k0, k1 < depth ? k1 : depth, c.splits > 1 ? int64_t(q) : -1};
+  return Piece{c.full + r, k0, k1 < depth ? k1 : depth, c.splits > 1 ? int64_t(split) * rest + r : -1};
 }
 
 // Where the partial sums of a slot go, of a tile of which `rows` exist.

@@ -600,7 +600,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void hidden_grad_kernel(HiddenGradA
   G g;
   g.setup();
   auto open = [&](uint32_t item) {
-    const Piece p = piece_of(cut, item, a.vocab);
+    const Piece p = piece_of<true>(cut, item, a.vocab);
     uint32_t tm, tn;
     tile_of(p.tile, tiles_m, a.tiles_n, 4, &tm, &tn);
     m0 = int64_t(tm) * BM;

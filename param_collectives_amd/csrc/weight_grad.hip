@@ -29,7 +29,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void weight_grad_kernel(WeightGradA
   __shared__ __align__(16) char lds3[G::kStage];
   // One tile a workgroup: with the next tile's loads under the epilogue, as in
   // the vocabulary loss, the codes' registers spill (measured 2-18% slower).
-  const Piece p = piece_of(a.cut, blockIdx.x, a.tokens);
+  const Piece p = piece_of<false>(a.cut, blockIdx.x, a.tokens);
   uint32_t tm, tn;
   tile_of(p.tile, a.tiles_m, a.tiles_n, 4, &tm, &tn);
   const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;

@@ -764,7 +764,8 @@ Layout layout_of(const VocabLossCall& c) {
                    : 128;
     const int64_t most = L.side_h == 256 ? big * (steps / 32) : small * (steps / 16);
     const int64_t slots = most < tile_slots(L.side_h) ? most : tile_slots(L.side_h);
-    L.h_splits = steps >= (L.side_h == 256 ? 64 : 32) && slots > 1;
+    // one tile is split if any number of them is
+    L.h_splits = cut_tiles(1, steps, L.side_h).splits > 1;
     if (L.h_splits) L.partial = take(slots * L.side_h * L.side_h * 4);
     L.side_w = tile_side(c.vocab, c.hidden);
     L.sums = L.pieces > 1 && !c.dw_f32;

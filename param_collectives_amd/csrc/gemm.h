@@ -689,8 +689,10 @@ struct Gemm {
 // used up from the others'.  So the CUs that a kernel beside this one or a
 // stream's CU mask leaves free get all the work: with a fixed share for each of
 // 256 workgroups, those without a CU began when the others ended (measured: 58%
-// slower on a stream of 240 CUs).
+// slower on a stream of 240 CUs).  The words lie apart: on one line, 512 workgroups'
+// requests took 35 us one after the other.
 constexpr uint32_t kNoItem = ~0u;
+constexpr uint32_t kQueueWords = 8, kQueuePitch = 64;  // of a queue; from word to word
 
 struct Queue {
   uint32_t* words;
@@ -707,13 +709,14 @@ struct Queue {
   // wave settles what ask() gave.  Whether the others' shares have items left is
   // looked up for all of them at once (asked for one after the other, the last
   // look of each workgroup took 10 us).
-  __device__ __forceinline__ uint32_t ask() { return threadIdx.x == 0 ? atomicAdd(words + x, 1u) : 0u; }
+  __device__ __forceinline__ uint32_t ask() { return threadIdx.x == 0 ? atomicAdd(words + x * kQueuePitch, 1u) : 0u; }
   __device__ __forceinline__ uint32_t settle(uint32_t asked) {
     uint32_t k = __builtin_amdgcn_readfirstlane(asked), used = 0;
     while (k >= share(x)) {
       used |= 1u << x;
       const uint32_t lane = threadIdx.x;
-      const bool left = lane < 8 && __hip_atomic_load(words + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < share(lane);
+      const bool left = lane < kQueueWords && __hip_atomic_load(words + lane * kQueuePitch, __ATOMIC_RELAXED,
+                                                                __HIP_MEMORY_SCOPE_AGENT) < share(lane);
       const uint32_t open = uint32_t(__ballot(left)) & ~used;
       if (open == 0) return kNoItem;
       x = (x + __builtin_ctz((open | open << 8) >> x)) & 7;

@@ -69,6 +69,8 @@ __device__ __forceinline__ float half_value(uint32_t bits) {
   return float(h);
 }
 
+constexpr uint32_t kQueues = 3;  // of a piece's three products
+
 // Rows of this piece that hold a token: the piece covers the listed tokens
 // [first, first + piece).
 __device__ __forceinline__ int64_t rows_of(const int32_t* count, int64_t first, int64_t piece) {
@@ -105,16 +107,16 @@ __device__ __forceinline__ uint32_t next_item(Queue& q, uint32_t k, uint32_t* tu
 // ------------------------------------------------------------ the token list
 
 // Lists the tokens that count, in order, and clears the loss and lse of the
-// others; clears the products' queues; the largest |grad_loss| of those that count goes to *scale (1 where
-// that is 0 or not finite).  One workgroup: a pass per 1024 tokens.
+// others; clears the queues; the largest |grad_loss| of the tokens that count goes
+// to *scale (1 where that is 0 or not finite).  One workgroup: a pass per 1024
+// tokens.
 __global__ __launch_bounds__(1024) void list_tokens_kernel(const int64_t* targets, int64_t tokens, int64_t vocab,
                                                            const float* grad_loss, int32_t* list, int32_t* count,
-                                                           float* scale, float* loss, float* lse, uint32_t* queues,
-                                                           int64_t queue_words) {
+                                                           float* scale, float* loss, float* lse, uint32_t* queues) {
   __shared__ int32_t wave_sum[16];
   __shared__ uint32_t wave_top[16];
   uint32_t top = 0;  // magnitudes compare as their bits, NaN above all
-  for (int64_t i = threadIdx.x; i < queue_words; i += 1024) queues[i] = 0;
+  if (threadIdx.x < kQueues * kQueueWords) queues[threadIdx.x * kQueuePitch] = 0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int32_t before = 0;
   for (int64_t t0 = 0; t0 < tokens; t0 += 1024) {
@@ -484,14 +486,17 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LogitsArgs a) {
 
 // Joins a row's tiles: one workgroup per row.  (c, s) stands for s 2^c.  Each
 // thread takes four tiles at a time, so that their loads overlap (a wave per row
-// that read the tiles twice took 4.8 us for 17 rows of 500).
+// that read the tiles twice took 4.8 us for 17 rows of 500).  Clears the queues, which
+// no workgroup uses by now.
 __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uint32_t tiles, const int32_t* count,
                                                         const int32_t* list, const int64_t* targets, int64_t vocab,
                                                         int64_t tokens, int64_t first, int64_t piece,
                                                         const float* target_z, float* row_log2, float* loss,
-                                                        float* lse) {
+                                                        float* lse, uint32_t* queues) {
   constexpr float kLowest = -3.0e38f;  // finite: the difference of two of them is 0
   __shared__ float2 wave_part[4];
+  // the logits' queue for the next piece, the others' for this one
+  if (blockIdx.x == 0 && queues && threadIdx.x < kQueues * kQueueWords) queues[threadIdx.x * kQueuePitch] = 0;
   const int64_t row = blockIdx.x;
   const int64_t rows = count ? rows_of(count, first, piece) : tokens;
   if (row >= rows) return;
@@ -740,7 +745,7 @@ Layout layout_of(const VocabLossCall& c) {
   };
   if (L.listed) {
     L.count = take(8);  // and the scale
-    L.queues = take(L.pieces * 24 * 4);
+    L.queues = take(kQueues * kQueueWords * kQueuePitch * 4);
     L.list = take(c.tokens * 4);
     L.h = take(c.tokens * L.h_ld * 2);
   }
@@ -802,13 +807,12 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
   const int64_t* targets = c.targets;
   int32_t* count = L.listed ? reinterpret_cast<int32_t*>(ws + L.count) : nullptr;
   float* scale = L.listed ? reinterpret_cast<float*>(count + 1) : nullptr;
-  // 8 words for each of a piece's three products
   uint32_t* queues = L.listed ? reinterpret_cast<uint32_t*>(ws + L.queues) : nullptr;
   int32_t* list = L.listed ? reinterpret_cast<int32_t*>(ws + L.list) : nullptr;
   Operand h{c.h, nullptr, c.h_ld, 0, c.tokens}, w{c.w, nullptr, c.w_ld, 0, c.vocab};
   if (L.listed) {
     hipLaunchKernelGGL(list_tokens_kernel, dim3(1), dim3(1024), 0, st, targets, c.tokens, c.vocab,
-                       c.grad_loss, list, count, scale, c.loss, c.lse, queues, L.pieces * 24);
+                       c.grad_loss, list, count, scale, c.loss, c.lse, queues);
     TIDE_LAUNCHED();
     uint16_t* rows = reinterpret_cast<uint16_t*>(ws + L.h);
     const int64_t n = c.tokens * (L.h_ld / 8);
@@ -849,7 +853,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     a.e_ld = L.e_ld;
     a.tiles_n = uint32_t(L.tiles_n);
     const int64_t tiles = (L.piece + L.rows - 1) / L.rows * L.tiles_n;
-    a.queue = L.listed ? queues + p * 24 : nullptr;
+    a.queue = queues;
     const dim3 grid(L.listed ? resident_groups(tiles, L.rows) : unsigned(tiles));
     if (L.rows == 256)
       hipLaunchKernelGGL((logits_kernel<256, 256, 2, 4>), grid, dim3(512), 0, st, a);
@@ -865,7 +869,8 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
       hipLaunchKernelGGL(few_logits_kernel<1>, dim3(a.tiles_n), dim3(256), 0, st, a);
     TIDE_LAUNCHED();
     hipLaunchKernelGGL(join_rows_kernel, dim3(unsigned(L.piece)), dim3(256), 0, st, stats, a.tiles_n, count,
-                       list, targets, c.vocab, c.tokens, first, L.piece, target_z, row_log2, c.loss, c.lse);
+                       list, targets, c.vocab, c.tokens, first, L.piece, target_z, row_log2, c.loss, c.lse,
+                       queues);
     TIDE_LAUNCHED();
     if (!grad) continue;
     const int64_t rows_z = L.piece < 32768 ? L.piece : 32768;
@@ -888,7 +893,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     d.partial = reinterpret_cast<float*>(ws + L.partial);
     d.dhidden = static_cast<uint16_t*>(c.dhidden);
     d.tiles_n = uint32_t((c.hidden + L.side_h - 1) / L.side_h);
-    d.queue = queues + p * 24 + 8;
+    d.queue = queues + kQueueWords * kQueuePitch;
     // as many workgroups as any cut has items for (a cut with pieces fills the slots at most)
     const int64_t tiles_h = (L.piece + L.side_h - 1) / L.side_h * d.tiles_n;
     const dim3 grid_h(L.h_splits ? unsigned(tile_slots(L.side_h)) : resident_groups(tiles_h, L.side_h));
@@ -918,7 +923,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     v.sum_in = p > 0 ? sums : nullptr;
     v.sum_out = p + 1 < L.pieces ? sums : nullptr;
     v.dw = c.dw;
-    v.queue = queues + p * 24 + 16;
+    v.queue = queues + 2 * kQueueWords * kQueuePitch;
     v.f32 = c.dw_f32;
     v.accumulate = c.accumulate || (p > 0 && !L.sums);
     const int64_t side_w = L.side_w;

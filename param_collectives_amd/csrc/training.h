@@ -56,7 +56,7 @@ struct Cut {
 TIDE_BOTH inline int64_t tile_slots(int64_t side) { return side == 256 ? 256 : 512; }
 
 // Splitting pays where it saves more steps (about 0.7 us each for a 256 x 256
-// tile a CU, 0.3 us for two of 128 x 128) than the partial sums and the join
+// tile a CU, 0.45 us for two of 128 x 128) than the partial sums and the join
 // cost, about 30 and 8 us.
 TIDE_BOTH inline Cut cut_tiles(int64_t tiles, int64_t steps, int64_t side) {
   Cut c{uint32_t(tiles), uint32_t(tiles), 1, uint32_t(steps), uint32_t(tiles)};

@@ -492,7 +492,8 @@ tide_status tide_checkpoint_weight_grad(const uint16_t* dy, int64_t rows, int64_
  *           dweight_dtype, both without gaps
  *   workspace  as for the weight gradient above.  With gradients it holds the
  *           exponentials of at most 2 GiB worth of tokens at a time (at least
- *           256 tokens), 2 bytes each.
+ *           256 tokens), 2 bytes each; where that is not all of them and
+ *           dweight is bf16, also dweight's sums in fp32.
  * Sizes: tokens up to 2^24 (0 allowed: dweight becomes 0, or stays), vocab and
  * hidden_size in [1, 2^22], matrices up to 2^34 elements as above.
  * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.

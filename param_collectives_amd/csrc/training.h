@@ -55,24 +55,35 @@ struct Cut {
 
 TIDE_BOTH inline int64_t tile_slots(int64_t side) { return side == 256 ? 256 : 512; }
 
-// Splitting pays where it saves more steps (about 0.7 us each for a 256 x 256
-// tile a CU, 0.45 us for two of 128 x 128) than the partial sums and the join
-// cost, about 30 and 8 us.
-TIDE_BOTH inline Cut cut_tiles(int64_t tiles, int64_t steps, int64_t side) {
-  Cut c{uint32_t(tiles), uint32_t(tiles), 1, uint32_t(steps), uint32_t(tiles)};
-  const int64_t slots = tile_slots(side), rest = tiles % slots;
-  const int64_t shortest = side == 256 ? 32 : 16, worth = side == 256 ? 64 : 32;
+// The rest is split so that its pieces fill a round, or not at all, whichever is
+// estimated to end first: a round takes its steps (0.72 us each for a 256 x 256
+// tile a CU, 0.45 us for two of 128 x 128) and about 11 more, the join about 5 us,
+// and each piece 0.1 or 0.03 us for its partial sums.  Large tiles that are more
+// than half a round, too many to be split in one, may fill two or three: the loss
+// with gradients of 4096 x 2560 x 50000, whose dH has 160, takes 2.83 instead of
+// 3.30 ms (and half a round, 96 tiles, 2% more in two rounds than in one).
+TIDE_BOTH inline int64_t most_rounds(int64_t side) { return side == 256 ? 3 : 1; }
+
+TIDE_BOTH inline Cut cut_tiles(int64_t all, int64_t all_steps, int64_t side) {
+  const uint32_t tiles = uint32_t(all), steps = uint32_t(all_steps), slots = uint32_t(tile_slots(side));
+  const uint32_t rest = tiles % slots, longest = steps / (side == 256 ? 32 : 16);  // splits, by the shortest piece
+  Cut c{tiles, tiles, 1, steps, tiles};
   if (rest == 0) return c;
-  int64_t splits = slots / rest;
-  if (splits > steps / shortest) splits = steps / shortest;
-  if (splits < 2) return c;
-  const int64_t per = (steps + splits - 1) / splits;
-  if (steps - per < worth) return c;
-  splits = (steps + per - 1) / per;
-  c.full = uint32_t(tiles - rest);
-  c.splits = uint32_t(splits);
-  c.per = uint32_t(per);
-  c.items = uint32_t(tiles - rest + rest * splits);
+  // in 64ths of a step
+  const uint32_t round = 11 * 64, join = (side == 256 ? 7 : 11) * 64, piece = side == 256 ? 9 : 4;
+  uint32_t best = steps * 64 + round;
+  for (uint32_t r = 1; r <= uint32_t(most_rounds(side)); ++r) {
+    uint32_t splits = r * slots / rest;
+    splits = splits < longest ? splits : longest;
+    if (splits < 2) continue;
+    const uint32_t per = (steps + splits - 1) / splits;
+    splits = (steps + per - 1) / per;
+    const uint32_t n = rest * splits, cost = (n + slots - 1) / slots * (per * 64 + round) + join + n * piece;
+    if (cost >= best) continue;
+    best = cost;
+    c = Cut{tiles, tiles - rest, splits, per, tiles - rest + n};
+    if (r == 1) break;
+  }
   return c;
 }
 
@@ -83,8 +94,8 @@ inline int64_t partial_bytes(const Cut& c, int64_t side) {
 // About what a product of that cut takes, in us, for the choice of the tile.
 inline double cut_cost(const Cut& c, int64_t steps, int64_t side) {
   const double step = side == 256 ? 0.72 : 0.45, tile = side == 256 ? 8.0 : 5.0;
-  const int64_t slots = tile_slots(side), rounds = c.full / slots, rest = c.splits > 1 ? c.per : c.full % slots ? steps : 0;
-  return double(rounds) * (double(steps) * step + tile) + double(rest) * step + (rest ? tile : 0.0) +
+  const int64_t slots = tile_slots(side), rounds = (c.full + slots - 1) / slots, more = (c.items - c.full + slots - 1) / slots;
+  return double(rounds) * (double(steps) * step + tile) + double(more) * (double(c.per) * step + tile) +
          (c.splits > 1 ? 5.0 + 0.4e-6 * double(partial_bytes(c, side)) : 0.0);
 }
 

@@ -768,7 +768,7 @@ Layout layout_of(const VocabLossCall& c) {
     L.row_log2 = take(L.piece * 4);
     L.e = take(L.piece * L.e_ld * 2);
     // The cut itself waits for the number of tokens that count.  Its partial
-    // sums take no more slots than there are workgroups, nor than every tile
+    // sums take no more slots than the rounds of its pieces, nor than every tile
     // split as far as may be.
     const int64_t steps = (c.vocab + kBK - 1) / kBK;
     const int64_t big = (L.piece + 255) / 256 * ((c.hidden + 255) / 256);
@@ -777,7 +777,8 @@ Layout layout_of(const VocabLossCall& c) {
                    ? 256
                    : 128;
     const int64_t most = L.side_h == 256 ? big * (steps / 32) : small * (steps / 16);
-    const int64_t slots = most < tile_slots(L.side_h) ? most : tile_slots(L.side_h);
+    const int64_t room = most_rounds(L.side_h) * tile_slots(L.side_h);
+    const int64_t slots = most < room ? most : room;
     // one tile is split if any number of them is
     L.h_splits = cut_tiles(1, steps, L.side_h).splits > 1;
     if (L.h_splits) L.partial = take(slots * L.side_h * L.side_h * 4);
@@ -903,7 +904,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     d.dhidden = static_cast<uint16_t*>(c.dhidden);
     d.tiles_n = uint32_t((c.hidden + L.side_h - 1) / L.side_h);
     d.queue = queues + kQueueWords * kQueuePitch;
-    // as many workgroups as any cut has items for (a cut with pieces fills the slots at most)
+    // as many workgroups as fit, where there may be pieces: the cut waits for the tokens that count
     const int64_t tiles_h = (L.piece + L.side_h - 1) / L.side_h * d.tiles_n;
     const dim3 grid_h(L.h_splits ? unsigned(tile_slots(L.side_h)) : resident_groups(tiles_h, L.side_h));
     if (L.side_h == 256)

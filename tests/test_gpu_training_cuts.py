@@ -138,3 +138,15 @@ def test_streams_that_hold_some_cus(tide):
         assert torch.equal(getattr(some, name), getattr(whole, name)), name
     assert torch.equal(dw[0], dw[1])
     stream.destroy()
+
+
+def test_weight_grad_pieces_in_rounds(tide):
+    """160 large tiles, split in 3: 480 pieces, two rounds."""
+    for fmt, dtype in (("e4m3", "bf16"), ("int8", "f32")):
+        test_weight_grad_cuts(tide, 21999, 2560, 4090, fmt, dtype)
+
+
+def test_vocab_loss_pieces_in_rounds(tide):
+    """The same for dH; the tokens that count decide it."""
+    test_vocab_loss_rounds(tide, 2560, 4096, 22001, 0.0, "bf16")
+    test_vocab_loss_rounds(tide, 2900, 4096, 22001, 0.12, "f32")

@@ -74,8 +74,9 @@ def test_workspace(tide):
 
     assert size(grad=2) == INVALID and size(dtype=9) == INVALID and size(h_ld=100) == INVALID
     step = size()
-    # the exponentials of 4096 tokens, the tokens' states, little else
-    assert 4096 * 128000 * 2 < step < 4096 * 128000 * 2 + (128 << 20)
+    # the exponentials of 4096 tokens, the tokens' states, and the partial sums of at most three rounds of 256 split
+    # tiles (65536 fp32 sums each: 192 MiB), little else (500 pairs of statistics a token: 15.6 MiB)
+    assert 4096 * 128000 * 2 < step < 4096 * 128000 * 2 + 4096 * 4096 * 2 + (192 << 20) + (16 << 20)
     # more tokens than 2 GiB of exponentials hold: in pieces, with dweight's sums in fp32 unless dweight holds them
     assert size(tokens=65536, dtype=1) < (2 << 30) + (1 << 30)
     assert size(tokens=65536, dtype=0) - size(tokens=65536, dtype=1) == 128000 * 4096 * 4

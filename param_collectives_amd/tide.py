@@ -469,7 +469,7 @@ def _on_device(t, what):
     device = t.get_device()  # -1 on the host
     if device < 0:
         raise ValueError(f"{what}: expected a GPU tensor, got {t.device}")
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():  # torch.cuda.current_device(), but for its check that there is one
         raise ValueError(f"{what}: lives on {t.device}, but the kernels run on the current device "
                          f"cuda:{torch.cuda.current_device()}")
 

@@ -28,14 +28,17 @@ def hipcc():
     return path if os.path.exists(path) else "hipcc"
 
 
+FLAGS = [
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+    "-ffp-contract=off", "-fno-fast-math",
+    "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    "-Wall", "-Wno-unused-command-line-argument",
+    "-I", INCLUDE, "-I", CSRC,
+]
+
+
 def build_library(verbose: bool = False, extra=()) -> str:
-    flags = [
-        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
-        "-ffp-contract=off", "-fno-fast-math",
-        "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-Wall", "-Wno-unused-command-line-argument",
-        "-I", INCLUDE, "-I", CSRC, *extra,
-    ]
+    flags = [*FLAGS, *extra]
 
     def run(cmd):
         if verbose:

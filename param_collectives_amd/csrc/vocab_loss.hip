@@ -355,6 +355,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
 // (each wave reading them for itself, which the L1 does not hold, took 44 us
 // instead of 31 for 17 x 2048 x 32000 from cold caches).  Row r's 16 bytes c are
 // kept at c ^ (r & 15): the fragment reads touch all banks once.
+// A block's states are started before its weights, and the compiler must not mix
+// them: the wait before a barrier lets the kSteps youngest loads go on, which
+// have to be the weights', for the states are read by the other waves too.
 template <int NT>
 __global__ __launch_bounds__(256) void few_logits_kernel(LogitsArgs a) {
   constexpr int kDeep = 256, kSteps = kDeep / 32, kLoads = 2 * NT;
@@ -403,6 +406,7 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LogitsArgs a) {
     wait_loads<kSteps, true>();  // this block's states are older than its weights
     bare_barrier();
     states(next, b + 1);
+    __builtin_amdgcn_sched_barrier(0);
     weights(wn, b + 1);
     __builtin_amdgcn_sched_barrier(0);
     multiply(now, wf);
@@ -414,6 +418,7 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LogitsArgs a) {
   };
   if (blocks > 0) {
     states(h0, 0);
+    __builtin_amdgcn_sched_barrier(0);
     weights(w0, 0);
     __builtin_amdgcn_sched_barrier(0);
     int64_t b = 0;

@@ -511,6 +511,12 @@ struct Gemm {
 #pragma unroll
       for (int j = 0; j < kFN; ++j) fb[j] = SB::fragment(lds + SA::kBytes, at_b, j);
     };
+    // Loads to LDS of step s + 3, kPerRow of them after a row.  (Started together at
+    // the step's head they hold its products up, 4% of a large product's time.)
+    constexpr int kPartsA = SA::kPacked ? 0 : SA::kParts, kParts = kPartsA + (SB::kPacked ? 0 : SB::kParts);
+    constexpr int kPerRow = (kParts + kFM - 1) / kFM;
+    // codes are loaded after row kFM / 2 - 1 or a later one
+    static_assert(!kPacked || (kParts + kPerRow - 1) / kPerRow <= kFM / 2, "loads to LDS before codes");
     // Multiplies the step in `now`, whose first fragments have been read;
     // MORE: reads the first ones of the step in `next`.  A fragment is read two
     // rows of products before its own; part(i) follows row i, halfway(h) the
@@ -533,6 +539,10 @@ struct Gemm {
 #pragma unroll
         for (int j = 0; j < kFN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], a[i], acc[i][j], 0, 0, 0);
         part(i);
+        // A step's loads to LDS come before its codes', as the next waits count
+        // them.  (Not between them everywhere: with 256 x 256 tiles of int8 codes
+        // it costs spilled registers, and there a row of products lies between.)
+        if (kPacked && i == kFM / 2 - 1 && i * kPerRow < kParts) __builtin_amdgcn_sched_barrier(0);
         if (i == kFM / 2 - kHalves) halfway(0);
         if (kHalves == 2 && i == kFM / 2) halfway(1);
         __builtin_amdgcn_sched_barrier(0);
@@ -548,11 +558,7 @@ struct Gemm {
     // step i: step i + 2's, and the codes of steps i + 2 and i + 3.
     constexpr int kCodeLoads = (SA::kPacked ? SA::kLoads : 0) + (SB::kPacked ? SB::kLoads : 0);
     constexpr int kAfter = SA::kLoads + SB::kLoads + kCodeLoads;
-    // Loads of step s + 3 that follow row i.  (One after each row of products:
-    // started together at the step's head they hold its products up, 4% of a
-    // large product's time.)
-    constexpr int kPartsA = SA::kPacked ? 0 : SA::kParts, kParts = kPartsA + (SB::kPacked ? 0 : SB::kParts);
-    constexpr int kPerRow = (kParts + kFM - 1) / kFM;
+    // Those that follow row i.
     auto load = [&](char* to3, int i) {
 #pragma unroll
       for (int n = i * kPerRow; n < (i + 1) * kPerRow; ++n) {

@@ -52,3 +52,13 @@ def test_few_tokens_states_before_weights(segments):
         assert sum("L" in p for p in parts) >= 4, (name, parts)
         for p in parts:
             assert "rL" not in p, (name, parts)
+
+
+def test_weight_gradient_rows_before_codes(segments):
+    kernels = {n: s for n, s in segments("weight_grad.hip").items() if "weight_grad_kernel" in n and "join" not in n}
+    assert len(kernels) == 4
+    for name, parts in kernels.items():
+        # the four steps of the loop: a thread's two loads to LDS, then its codes and their exponent byte
+        assert sum(p == "LLrr" for p in parts) >= 4, (name, parts)
+        for p in parts[:-1]:  # the last is the epilogue
+            assert "rL" not in p, (name, parts)

@@ -21,7 +21,8 @@
                          elementwise victim, CU-masked streams
 
 The *_call variants check and marshal the tensors once and return a callable
-that launches with one library call (for buffers reused every step).
+that launches with one library call (for buffers reused every step); where an
+operation needs a workspace, each launch takes its own unless it is given one.
 
 The work runs in the HIP library libtide.so (include/tide.h); importing this
 package fails if that library has not been built.

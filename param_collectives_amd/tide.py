@@ -314,6 +314,24 @@ class Call:
         _check(self._fn(*self._args, ctypes.c_void_p(_stream_handle(stream) or None)))
 
 
+class WorkspaceCall(Call):
+    """A Call of an operation with a workspace: the caller's, or one that each
+    launch takes for itself on the stream it runs on.  A launch of its own
+    workspace may overlap others on other streams, the object may be dropped
+    while it runs, and one that is captured takes it from the graph's memory."""
+
+    def __init__(self, fn, args, tensors, nbytes, workspace):
+        super().__init__(fn, args, tensors)
+        self._bytes = nbytes
+        self._workspace = workspace
+        if workspace is not None:
+            _workspace(nbytes, workspace, None)  # its checks
+
+    def __call__(self, stream=None):
+        ws, nbytes, keep = _workspace(self._bytes, self._workspace, stream)
+        _check(self._fn(*self._args, ws, nbytes, ctypes.c_void_p(_stream_handle(stream) or None)))
+
+
 def _rs_checked(plan, grads, outs):
     """Checks the tensors of a reduce-scatter; returns (gradient pointers,
     output pointers, whether the gradients are fp32)."""
@@ -584,8 +602,8 @@ def _workspace(nbytes, given, stream):
     return given.data_ptr(), given.numel(), given
 
 
-def _weight_grad_args(dy, codes, scales, dw, alpha, accumulate, workspace, stream):
-    """(arguments, workspace tensor)."""
+def _weight_grad_args(dy, codes, scales, dw, alpha, accumulate):
+    """(arguments up to the workspace's, bytes of workspace)."""
     y, rows, outs, stride = _matrix(dy, _BF16, "dy")
     w, w_outs, ins, _ = _matrix(dw, _FLOATS, "dw", strided=False)
     if w_outs != outs:
@@ -593,8 +611,7 @@ def _weight_grad_args(dy, codes, scales, dw, alpha, accumulate, workspace, strea
     c, s, fmt = _packed(codes, scales, rows, ins)
     need = ctypes.c_int64()
     _check(lib.tide_checkpoint_weight_grad_workspace(y, rows, outs, stride, ins, ctypes.byref(need)))
-    ws, nbytes, keep = _workspace(need.value, workspace, stream)
-    return (y, rows, outs, stride, c, s, fmt, ins, w, _FLOATS[dw.dtype], alpha, int(bool(accumulate)), ws, nbytes), keep
+    return (y, rows, outs, stride, c, s, fmt, ins, w, _FLOATS[dw.dtype], alpha, int(bool(accumulate))), need.value
 
 
 def checkpoint_weight_grad_workspace(dy, in_features):
@@ -607,10 +624,12 @@ def checkpoint_weight_grad_workspace(dy, in_features):
 
 
 def checkpoint_weight_grad_call(dy, codes, scales, dw, alpha=1.0, accumulate=False, workspace=None):
-    """A registered weight gradient (see checkpoint_weight_grad); it keeps one
-    workspace, so its calls must not overlap."""
-    args, keep = _weight_grad_args(dy, codes, scales, dw, alpha, accumulate, workspace, None)
-    return Call(lib.tide_checkpoint_weight_grad, args, (dy, codes, scales, dw, keep))
+    """A registered weight gradient (see checkpoint_weight_grad).  With a
+    `workspace` of the caller's its launches must not overlap, and a graph that
+    records one needs it as long as it is replayed; without one each launch takes
+    its own."""
+    args, need = _weight_grad_args(dy, codes, scales, dw, alpha, accumulate)
+    return WorkspaceCall(lib.tide_checkpoint_weight_grad, args, (dy, codes, scales, dw), need, workspace)
 
 
 def checkpoint_weight_grad(dy, codes, scales, dw, alpha=1.0, accumulate=False, workspace=None, stream=None):
@@ -620,8 +639,9 @@ def checkpoint_weight_grad(dy, codes, scales, dw, alpha=1.0, accumulate=False, w
     bf16 or fp32 (out_features x in_features).  `workspace` is a uint8 tensor of
     at least checkpoint_weight_grad_workspace bytes; without one the call takes
     its own (tide_checkpoint_weight_grad)."""
-    args, keep = _weight_grad_args(dy, codes, scales, dw, alpha, accumulate, workspace, stream)
-    _check(lib.tide_checkpoint_weight_grad(*args, _stream_handle(stream)))
+    args, need = _weight_grad_args(dy, codes, scales, dw, alpha, accumulate)
+    ws, nbytes, keep = _workspace(need, workspace, stream)
+    _check(lib.tide_checkpoint_weight_grad(*args, ws, nbytes, _stream_handle(stream)))
 
 
 # ------------------------------------------------------------ vocabulary loss
@@ -652,21 +672,20 @@ def vocab_loss_workspace(hidden, weight, dweight=None):
     return _vocab_loss_bytes(operands, sizes, 1, _FLOATS[dweight.dtype])
 
 
-def _vocab_loss_args(hidden, weight, targets, loss, lse, workspace, stream):
-    """(arguments, workspace tensor)."""
+def _vocab_loss_args(hidden, weight, targets, loss, lse):
+    """(arguments up to the workspace's, bytes of workspace)."""
     operands, sizes = _projection(hidden, weight)
     tokens = sizes[0]
     t = _vector(targets, torch.int64, tokens, "targets")
     out = _vector(loss, torch.float32, tokens, "loss"), None if lse is None else _vector(lse, torch.float32, tokens, "lse")
-    ws, nbytes, keep = _workspace(_vocab_loss_bytes(operands, sizes, 0, DTYPE_F32), workspace, stream)
-    return (*operands, t, *sizes, *out, ws, nbytes), keep
+    return (*operands, t, *sizes, *out), _vocab_loss_bytes(operands, sizes, 0, DTYPE_F32)
 
 
 def vocab_loss_call(hidden, weight, targets, loss, lse=None, workspace=None):
-    """A registered vocabulary loss (see vocab_loss); it keeps one workspace,
-    so its calls must not overlap."""
-    args, keep = _vocab_loss_args(hidden, weight, targets, loss, lse, workspace, None)
-    return Call(lib.tide_vocab_loss, args, (hidden, weight, targets, loss, lse, keep))
+    """A registered vocabulary loss (see vocab_loss); `workspace` as for
+    checkpoint_weight_grad_call."""
+    args, need = _vocab_loss_args(hidden, weight, targets, loss, lse)
+    return WorkspaceCall(lib.tide_vocab_loss, args, (hidden, weight, targets, loss, lse), need, workspace)
 
 
 def vocab_loss(hidden, weight, targets, loss, lse=None, workspace=None, stream=None):
@@ -674,13 +693,13 @@ def vocab_loss(hidden, weight, targets, loss, lse=None, workspace=None, stream=N
     rows) against targets (int64): loss[t] and, if given, the log-sum-exp
     lse[t], fp32 per token.  A target outside the vocabulary leaves its token
     out, with 0s.  `workspace` as for checkpoint_weight_grad (tide_vocab_loss)."""
-    args, keep = _vocab_loss_args(hidden, weight, targets, loss, lse, workspace, stream)
-    _check(lib.tide_vocab_loss(*args, _stream_handle(stream)))
+    args, need = _vocab_loss_args(hidden, weight, targets, loss, lse)
+    ws, nbytes, keep = _workspace(need, workspace, stream)
+    _check(lib.tide_vocab_loss(*args, ws, nbytes, _stream_handle(stream)))
 
 
-def _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate, workspace,
-                          stream):
-    """(arguments, workspace tensor)."""
+def _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate):
+    """(arguments up to the workspace's, bytes of workspace)."""
     operands, sizes = _projection(hidden, weight)
     tokens, size, vocab = sizes
     t = _vector(targets, torch.int64, tokens, "targets")
@@ -692,18 +711,16 @@ def _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden
         raise ValueError(f"dhidden and dweight must be {tokens} x {size} and {vocab} x {size}, got {dh_shape} and "
                          f"{dw_shape}")
     dtype = _FLOATS[dweight.dtype]
-    ws, nbytes, keep = _workspace(_vocab_loss_bytes(operands, sizes, 1, dtype), workspace, stream)
-    return (*operands, t, g, *sizes, *out, dh, dw, dtype, int(bool(accumulate)), ws, nbytes), keep
+    return (*operands, t, g, *sizes, *out, dh, dw, dtype, int(bool(accumulate))), _vocab_loss_bytes(operands, sizes, 1, dtype)
 
 
 def vocab_loss_grad_call(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate=False,
                          workspace=None):
-    """A registered vocabulary loss with gradients (see vocab_loss_grad); it
-    keeps one workspace, so its calls must not overlap."""
-    args, keep = _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate,
-                                       workspace, None)
-    return Call(lib.tide_vocab_loss_grad, args,
-                (hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, keep))
+    """A registered vocabulary loss with gradients (see vocab_loss_grad);
+    `workspace` as for checkpoint_weight_grad_call."""
+    args, need = _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate)
+    return WorkspaceCall(lib.tide_vocab_loss_grad, args,
+                         (hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight), need, workspace)
 
 
 def vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate=False, workspace=None,
@@ -711,9 +728,9 @@ def vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dwei
     """vocab_loss with the gradients of sum_t grad_loss[t] * loss[t]: dhidden
     (bf16) and dweight (bf16 or fp32; added to the old one when accumulate is
     true).  lse may be None (tide_vocab_loss_grad)."""
-    args, keep = _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate,
-                                       workspace, stream)
-    _check(lib.tide_vocab_loss_grad(*args, _stream_handle(stream)))
+    args, need = _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate)
+    ws, nbytes, keep = _workspace(need, workspace, stream)
+    _check(lib.tide_vocab_loss_grad(*args, ws, nbytes, _stream_handle(stream)))
 
 
 # ------------------------------------------------------------ instruments

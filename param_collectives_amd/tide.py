@@ -314,9 +314,27 @@ class Call:
         _check(self._fn(*self._args, ctypes.c_void_p(_stream_handle(stream) or None)))
 
 
-class WorkspaceCall(Call):
-    """A Call of an operation with a workspace: the caller's, or one that each
-    launch takes for itself on the stream it runs on.  A launch of its own
+class TensorCall(Call):
+    """A Call without a plan, which would be bound to its device: it is launched
+    on the device it was made on only."""
+
+    def __init__(self, fn, args, tensors):
+        super().__init__(fn, args, tensors)
+        self._device = _current_device()
+
+    def __call__(self, stream=None):
+        self._on_its_device()
+        _check(self._fn(*self._args, _device_stream(stream)))
+
+    def _on_its_device(self):
+        if _current_device() != self._device:
+            raise ValueError(f"the call was made on cuda:{self._device}, but the current device is "
+                             f"cuda:{_current_device()}")
+
+
+class WorkspaceCall(TensorCall):
+    """A TensorCall of an operation with a workspace: the caller's, or one that
+    each launch takes for itself on the stream it runs on.  A launch of its own
     workspace may overlap others on other streams, the object may be dropped
     while it runs, and one that is captured takes it from the graph's memory."""
 
@@ -328,8 +346,10 @@ class WorkspaceCall(Call):
             _workspace(nbytes, workspace, None)  # its checks
 
     def __call__(self, stream=None):
+        self._on_its_device()
+        handle = _device_stream(stream)
         ws, nbytes, keep = _workspace(self._bytes, self._workspace, stream)
-        _check(self._fn(*self._args, ws, nbytes, ctypes.c_void_p(_stream_handle(stream) or None)))
+        _check(self._fn(*self._args, ws, nbytes, handle))
 
 
 def _rs_checked(plan, grads, outs):
@@ -481,15 +501,27 @@ _FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 _CODES = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_INT8}
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()  # torch.cuda.current_device(), but for its check that there is one
+
+
+def _device_stream(stream):
+    """The handle of a stream (None: the current one) of the current device."""
+    if stream is not None and getattr(stream, "device_index", None) not in (None, _current_device()):
+        raise ValueError(f"the stream is one of cuda:{stream.device_index}, but the kernels run on the current device "
+                         f"cuda:{_current_device()}")
+    return _stream_handle(stream)
+
+
 def _on_device(t, what):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
     device = t.get_device()  # -1 on the host
     if device < 0:
         raise ValueError(f"{what}: expected a GPU tensor, got {t.device}")
-    if device != torch._C._cuda_getDevice():  # torch.cuda.current_device(), but for its check that there is one
+    if device != _current_device():
         raise ValueError(f"{what}: lives on {t.device}, but the kernels run on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
+                         f"cuda:{_current_device()}")
 
 
 def _matrix(t, dtypes, what, strided=True):
@@ -556,14 +588,14 @@ def _pack_args(x, codes, scales):
 
 def checkpoint_pack_call(x, codes, scales):
     """A registered checkpoint pack (see checkpoint_pack)."""
-    return Call(lib.tide_checkpoint_pack, _pack_args(x, codes, scales), (x, codes, scales))
+    return TensorCall(lib.tide_checkpoint_pack, _pack_args(x, codes, scales), (x, codes, scales))
 
 
 def checkpoint_pack(x, codes, scales, stream=None):
     """Pack a matrix into its 8-bit form: x (bf16 or fp32, contiguous rows) ->
     codes (float8_e4m3fn or int8, which chooses the code type) and scales
     (uint8), sized by checkpoint_layout (tide_checkpoint_pack)."""
-    _check(lib.tide_checkpoint_pack(*_pack_args(x, codes, scales), _stream_handle(stream)))
+    _check(lib.tide_checkpoint_pack(*_pack_args(x, codes, scales), _device_stream(stream)))
 
 
 def _unpack_args(codes, scales, out):
@@ -574,13 +606,13 @@ def _unpack_args(codes, scales, out):
 
 def checkpoint_unpack_call(codes, scales, out):
     """A registered checkpoint restore (see checkpoint_unpack)."""
-    return Call(lib.tide_checkpoint_unpack, _unpack_args(codes, scales, out), (codes, scales, out))
+    return TensorCall(lib.tide_checkpoint_unpack, _unpack_args(codes, scales, out), (codes, scales, out))
 
 
 def checkpoint_unpack(codes, scales, out, stream=None):
     """Restore a packed matrix, exactly, into out (bf16 or fp32, contiguous
     rows; tide_checkpoint_unpack)."""
-    _check(lib.tide_checkpoint_unpack(*_unpack_args(codes, scales, out), _stream_handle(stream)))
+    _check(lib.tide_checkpoint_unpack(*_unpack_args(codes, scales, out), _device_stream(stream)))
 
 
 def _workspace(nbytes, given, stream):
@@ -640,8 +672,9 @@ def checkpoint_weight_grad(dy, codes, scales, dw, alpha=1.0, accumulate=False, w
     at least checkpoint_weight_grad_workspace bytes; without one the call takes
     its own (tide_checkpoint_weight_grad)."""
     args, need = _weight_grad_args(dy, codes, scales, dw, alpha, accumulate)
+    handle = _device_stream(stream)
     ws, nbytes, keep = _workspace(need, workspace, stream)
-    _check(lib.tide_checkpoint_weight_grad(*args, ws, nbytes, _stream_handle(stream)))
+    _check(lib.tide_checkpoint_weight_grad(*args, ws, nbytes, handle))
 
 
 # ------------------------------------------------------------ vocabulary loss
@@ -694,8 +727,9 @@ def vocab_loss(hidden, weight, targets, loss, lse=None, workspace=None, stream=N
     lse[t], fp32 per token.  A target outside the vocabulary leaves its token
     out, with 0s.  `workspace` as for checkpoint_weight_grad (tide_vocab_loss)."""
     args, need = _vocab_loss_args(hidden, weight, targets, loss, lse)
+    handle = _device_stream(stream)
     ws, nbytes, keep = _workspace(need, workspace, stream)
-    _check(lib.tide_vocab_loss(*args, ws, nbytes, _stream_handle(stream)))
+    _check(lib.tide_vocab_loss(*args, ws, nbytes, handle))
 
 
 def _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate):
@@ -729,8 +763,9 @@ def vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dwei
     (bf16) and dweight (bf16 or fp32; added to the old one when accumulate is
     true).  lse may be None (tide_vocab_loss_grad)."""
     args, need = _vocab_loss_grad_args(hidden, weight, targets, grad_loss, loss, lse, dhidden, dweight, accumulate)
+    handle = _device_stream(stream)
     ws, nbytes, keep = _workspace(need, workspace, stream)
-    _check(lib.tide_vocab_loss_grad(*args, ws, nbytes, _stream_handle(stream)))
+    _check(lib.tide_vocab_loss_grad(*args, ws, nbytes, handle))
 
 
 # ------------------------------------------------------------ instruments

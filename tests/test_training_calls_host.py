@@ -10,6 +10,7 @@ def tide(monkeypatch):
     from param_collectives_amd import tide
 
     monkeypatch.setattr(tide, "_on_device", lambda t, what: None)
+    monkeypatch.setattr(tide, "_current_device", lambda: 0, raising=False)
     return tide
 
 
@@ -58,7 +59,7 @@ def test_a_launch_takes_its_workspace_on_its_own_stream(tide, monkeypatch, name)
         call(s)
     assert [s for s, _ in taken] == [*streams, streams[0]]
     for (s, at), (ws, _, handle) in zip(taken, launched):
-        assert ws == at and handle.value == s.cuda_stream
+        assert ws == at and getattr(handle, "value", handle) == s.cuda_stream
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -74,3 +75,39 @@ def test_the_callers_workspace_serves_every_launch(tide, monkeypatch, name):
     assert launched == [(ws.data_ptr(), 1 << 20)] * 2
     with pytest.raises(TypeError):
         registered(tide, name, ws.view(torch.int32))
+
+
+ALL_CALLS = ["tide_checkpoint_pack", "tide_checkpoint_unpack", *CALLS]
+
+
+@pytest.mark.parametrize("name", ALL_CALLS)
+def test_launches_on_another_device_are_refused(tide, monkeypatch, name):
+    """The tensors are checked when the call is made; a launch would take its
+    stream from the device that is current then."""
+    import torch
+
+    launched = []
+    monkeypatch.setattr(tide.lib, name, lambda *a: launched.append(a) or 0)
+    x, codes, scales = torch.zeros(4, 64), torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 2, dtype=torch.uint8)
+    ws = torch.empty(1 << 20, dtype=torch.uint8)
+    here = types.SimpleNamespace(cuda_stream=0x1000, device_index=0)
+    there = types.SimpleNamespace(cuda_stream=0x2000, device_index=1)
+    if name == "tide_checkpoint_pack":
+        call = tide.checkpoint_pack_call(x, codes, scales)
+        once = lambda s: tide.checkpoint_pack(x, codes, scales, stream=s)
+    elif name == "tide_checkpoint_unpack":
+        call = tide.checkpoint_unpack_call(codes, scales, x)
+        once = lambda s: tide.checkpoint_unpack(codes, scales, x, stream=s)
+    else:
+        call = once = registered(tide, name, ws)
+    call(here)
+    once(here)
+    assert len(launched) == 2
+    for launch in (call, once):
+        with pytest.raises(ValueError, match="device"):
+            launch(there)
+    monkeypatch.setattr(tide, "_current_device", lambda: 1)
+    for stream in (here, there):
+        with pytest.raises(ValueError, match="device"):
+            call(stream)
+    assert len(launched) == 2

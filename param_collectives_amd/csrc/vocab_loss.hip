@@ -44,11 +44,15 @@ namespace {
 using namespace tide;
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
-// A tile row's reference from its maximum; nothing but -inf: a finite one, with
-// exponentials of 0.
-__device__ __forceinline__ float reference(float m) { return (m == -__builtin_inff() ? 0.0f : m * kLog2e) - 15.0f; }
+// exp(z - m) 2^15 for the tile row's maximum m, which fp16 keeps; nothing but -inf
+// in the row: 0.  (The difference first: a multiple of m by itself overflows
+// where a mask has left a tile row nothing but the lowest numbers.)
+__device__ __forceinline__ float reference(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+__device__ __forceinline__ float power(float z, float ref) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(z - ref, kLog2e, 15.0f));
+}
+constexpr float kSumUnit = 0x1p-15f;  // of the sums of those
 
 // The value 16 (32) lanes away: lane XOR 16 (32).
 __device__ __forceinline__ float other_16(float v) {
@@ -200,7 +204,7 @@ struct LogitsArgs {
   const int64_t* targets;
   int64_t tokens, vocab, depth;
   int64_t first, piece;
-  float2* stats;           // [row of the piece][vocabulary tile]: reference, sum of exponentials
+  float2* stats;           // [row of the piece][vocabulary tile]: maximum, sum of the powers
   float* target_z;         // [row of the piece]
   uint16_t* e;             // [row of the piece][e_ld], or null
   int64_t e_ld;
@@ -258,8 +262,6 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
 
     // A lane holds of row 16 i + lane % 16 the columns 16 j + 4 (lane / 16) + r.
     // The tile row's maximum and sum go over its lanes, then over the WN waves.
-    // The reference is kept in powers of 2, c = log2(e) max - 15: the
-    // exponentials 2^(log2(e) z - c) then reach 2^15, as fp16 keeps them.
     const int col0 = g.wn * kColsWave + 4 * (g.lane >> 4), row0 = g.wm * kRowsWave + (g.lane & 15);
     if (a.vocab - n1 < BN) {
       const int left = int(a.vocab - n1);
@@ -304,7 +306,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
       for (int j = 0; j < kFN; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(g.acc[i][j][r], kLog2e, -c));
+          const float x = power(g.acc[i][j][r], c);
           g.acc[i][j][r] = x;
           s += x;
         }
@@ -327,7 +329,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
         m = fmaxf(m, peak[w][row]);
         s += sums[w][row];
       }
-      a.stats[(m1 + row) * a.tiles_n + t1] = make_float2(reference(m), s);
+      a.stats[(m1 + row) * a.tiles_n + t1] = make_float2(m, s);
     }
     if (a.e) {
       // the pitch is a multiple of 64: a group of 8 columns is in or out
@@ -476,7 +478,7 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LogitsArgs a) {
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      acc[t][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[t][j], kLog2e, -c));
+      acc[t][j] = power(acc[t][j], c);
       s += acc[t][j];
     }
     s += other_16(s);
@@ -494,20 +496,21 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LogitsArgs a) {
       m = fmaxf(m, peak[w4][row]);
       s += sums[w4][row];
     }
-    a.stats[row * a.tiles_n + blockIdx.x] = make_float2(reference(m), s);
+    a.stats[row * a.tiles_n + blockIdx.x] = make_float2(m, s);
   }
 }
 
-// Joins a row's tiles: one workgroup per row.  (c, s) stands for s 2^c.  Each
+// Joins a row's tiles: one workgroup per row.  (m, s) stands for s exp(m), and a
+// tile of nothing but -inf, (-inf, 0), for nothing.  Each
 // thread takes four tiles at a time, so that their loads overlap (a wave per row
 // that read the tiles twice took 4.8 us for 17 rows of 500).  Clears the queues, which
 // no workgroup uses by now.
 __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uint32_t tiles, const int32_t* count,
                                                         const int32_t* list, const int64_t* targets, int64_t vocab,
                                                         int64_t tokens, int64_t first, int64_t piece,
-                                                        const float* target_z, float* row_log2, float* loss,
+                                                        const float* target_z, float2* row_sum, float* loss,
                                                         float* lse, uint32_t* queues) {
-  constexpr float kLowest = -3.0e38f;  // finite: the difference of two of them is 0
+  constexpr float kLowest = -3.402823466e38f;  // finite: the difference of two of them is 0
   __shared__ float2 wave_part[4];
   // the logits' queue for the next piece, the others' for this one
   if (blockIdx.x == 0 && queues && threadIdx.x < kQueues * kQueueWords) queues[threadIdx.x * kQueuePitch] = 0;
@@ -524,15 +527,15 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uin
     float top = m;
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = fmaxf(top, v[j].x);
-    s *= __builtin_amdgcn_exp2f(m - top);
+    s *= __builtin_amdgcn_exp2f((m - top) * kLog2e);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s += v[j].y * __builtin_amdgcn_exp2f(v[j].x - top);
+    for (int j = 0; j < 4; ++j) s += v[j].y * __builtin_amdgcn_exp2f((v[j].x - top) * kLog2e);
     m = top;
   }
   float top = m;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-  s *= __builtin_amdgcn_exp2f(m - top);
+  s *= __builtin_amdgcn_exp2f((m - top) * kLog2e);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
   if (lane == 0) wave_part[threadIdx.x >> 6] = make_float2(top, s);
@@ -542,12 +545,13 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uin
     for (int w = 1; w < 4; ++w) top = fmaxf(top, wave_part[w].x);
     s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) s += wave_part[w].y * __builtin_amdgcn_exp2f(wave_part[w].x - top);
+    for (int w = 0; w < 4; ++w) s += wave_part[w].y * __builtin_amdgcn_exp2f((wave_part[w].x - top) * kLog2e);
     const int64_t token = count ? list[first + row] : row;
     const int64_t target = targets[token];
     const bool keep = target >= 0 && target < vocab;
-    const float l2 = top + __builtin_log2f(s), l = l2 * kLn2;
-    if (row_log2) row_log2[row] = l2;
+    s *= kSumUnit;
+    const float l = top + logf(s);
+    if (row_sum) row_sum[row] = make_float2(top, s);
     loss[token] = keep ? l - target_z[row] : 0.0f;
     if (lse) lse[token] = keep ? l : 0.0f;
   }
@@ -561,7 +565,7 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uin
 __global__ __launch_bounds__(256) void logit_grad_kernel(uint16_t* e, int64_t e_ld, int64_t vocab, const float2* stats,
                                                          uint32_t tiles, uint32_t tile_cols, const int32_t* count,
                                                          const int32_t* list, const int64_t* targets, int64_t first,
-                                                         int64_t piece, const float* target_z, const float* row_log2,
+                                                         int64_t piece, const float* target_z, const float2* row_sum,
                                                          const float* grad_loss, const float* scale) {
   const int64_t row = blockIdx.y + int64_t(blockIdx.z) * 32768;
   const int64_t rows = rows_of(count, first, piece);
@@ -569,17 +573,19 @@ __global__ __launch_bounds__(256) void logit_grad_kernel(uint16_t* e, int64_t e_
   const int64_t c = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (c >= e_ld) return;
   const int32_t token = list[first + row];
-  const float l2 = row_log2[row], g = grad_loss[token] / *scale;
+  const float2 sum = row_sum[row];
+  const float g = grad_loss[token] / *scale;
   const int64_t target = targets[token];
   u32x4* p = reinterpret_cast<u32x4*>(e + row * e_ld + c);
   uint32_t out[4] = {0, 0, 0, 0};
   if (c < vocab) {
     const u32x4 w = *p;
-    const float f = __builtin_amdgcn_exp2f(stats[row * tiles + uint32_t(c) / tile_cols].x - l2) * g;
+    const float tile_max = stats[row * tiles + uint32_t(c) / tile_cols].x;
+    const float f = __builtin_amdgcn_exp2f((tile_max - sum.x) * kLog2e) * (kSumUnit / sum.y * g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float v = half_value(w[j >> 1] >> (16 * (j & 1))) * f;
-      if (c + j == target) v = g * expm1f(target_z[row] - l2 * kLn2);
+      if (c + j == target) v = g * expm1f(target_z[row] - (sum.x + logf(sum.y)));
       if (c + j >= vocab) v = 0.0f;
       out[j >> 1] |= bf16_bits_of(v) << (16 * (j & 1));
     }
@@ -729,7 +735,7 @@ struct Layout {
   int side_w = 256;     // of dW's tiles
   bool sums = false;    // dW's sums go over the pieces in the workspace
   // byte offsets
-  int64_t list = 0, count = 0, queues = 0, h = 0, w = 0, stats = 0, target_z = 0, row_log2 = 0, e = 0, partial = 0, dw_sums = 0,
+  int64_t list = 0, count = 0, queues = 0, h = 0, w = 0, stats = 0, target_z = 0, row_sum = 0, e = 0, partial = 0, dw_sums = 0,
           bytes = 0;
 };
 
@@ -770,7 +776,7 @@ Layout layout_of(const VocabLossCall& c) {
   L.stats = take(L.piece * L.tiles_n * 8);
   L.target_z = take(L.piece * 4);
   if (grad) {
-    L.row_log2 = take(L.piece * 4);
+    L.row_sum = take(L.piece * 8);
     L.e = take(L.piece * L.e_ld * 2);
     // The cut itself waits for the number of tokens that count.  Its partial
     // sums take no more slots than the rounds of its pieces, nor than every tile
@@ -847,7 +853,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
   }
   float2* stats = reinterpret_cast<float2*>(ws + L.stats);
   float* target_z = reinterpret_cast<float*>(ws + L.target_z);
-  float* row_log2 = grad ? reinterpret_cast<float*>(ws + L.row_log2) : nullptr;
+  float2* row_sum = grad ? reinterpret_cast<float2*>(ws + L.row_sum) : nullptr;
   uint16_t* e = grad ? reinterpret_cast<uint16_t*>(ws + L.e) : nullptr;
   for (int64_t p = 0; p < L.pieces; ++p) {
     const int64_t first = p * L.piece;
@@ -884,7 +890,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
       hipLaunchKernelGGL(few_logits_kernel<1>, dim3(a.tiles_n), dim3(256), 0, st, a);
     TIDE_LAUNCHED();
     hipLaunchKernelGGL(join_rows_kernel, dim3(unsigned(L.piece)), dim3(256), 0, st, stats, a.tiles_n, count,
-                       list, targets, c.vocab, c.tokens, first, L.piece, target_z, row_log2, c.loss, c.lse,
+                       list, targets, c.vocab, c.tokens, first, L.piece, target_z, row_sum, c.loss, c.lse,
                        queues);
     TIDE_LAUNCHED();
     if (!grad) continue;
@@ -892,7 +898,7 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream) {
     hipLaunchKernelGGL(logit_grad_kernel,
                        dim3(unsigned((L.e_ld + 2047) / 2048), unsigned(rows_z), unsigned((L.piece + 32767) / 32768)),
                        dim3(256), 0, st, e, L.e_ld, c.vocab, stats, a.tiles_n, uint32_t(L.cols), count, list, targets,
-                       first, L.piece, target_z, row_log2, c.grad_loss, scale);
+                       first, L.piece, target_z, row_sum, c.grad_loss, scale);
     TIDE_LAUNCHED();
     HiddenGradArgs d;
     d.dz = Operand{e, nullptr, L.e_ld, 0, L.piece};

@@ -474,11 +474,14 @@ tide_status tide_checkpoint_weight_grad(const uint16_t* dy, int64_t rows, int64_
  * A token whose target lies outside [0, vocab) is left out: its loss, lse and
  * row of dhidden are 0, it adds nothing to dweight, and neither its hidden
  * state nor its grad_loss has any effect, NaN or not.
- * Products are exact, sums and the softmax fp32.  dz, over the largest
- * |grad_loss|, is rounded once to bf16 (by at most 2^-8 of it), the operand of
- * the two gradient products; their sums take that factor back in fp32, and
- * dhidden and dweight are rounded once more, to their own types.  The order of every sum
- * depends on the sizes (and, in the gradients, on how many tokens count) only.
+ * Products are exact, sums and the softmax fp32.  The exponentials in dz are kept
+ * with 11 significant bits (rounded by at most 2^-11, or by 2^-73 of 1 where they
+ * are below 2^-62).  dz, over the largest |grad_loss|, is then rounded to bf16 (by
+ * at most 2^-8 of it, or by 2^-134 of that largest), the operand of the two
+ * gradient products, also where dweight is fp32; their sums take that factor back
+ * in fp32, and dhidden and dweight are rounded once more, to their own types.  The
+ * order of every sum depends on the sizes (and, in the gradients, on how many
+ * tokens count) only.
  *
  *   hidden, weight  rows hidden_stride and weight_stride elements apart, 2-byte
  *           aligned.  Where weight's rows do not all start and end on 16 bytes

@@ -9,10 +9,10 @@
 // and never written.  The loss keeps of each tile row its maximum and its sum
 // of exponentials, and joins them over the vocabulary's tiles.  The gradients
 // need every logit twice more; recomputing them would add a third to the three
-// products' work, so the tile also leaves exp(z - tile maximum), which lies in
-// [0, 1], as an fp16 number times 2^15 (rounded by at most 2^-11, eight times finer
-// than the bf16 it becomes), for a bounded piece of the tokens at a time.  A
-// pass over that piece turns it into dz in bf16, the operand of the two
+// products' work, so the tile also leaves exp(z - tile row's maximum), which lies in
+// [0, 1], in 16 bits (rounded by at most 2^-11, eight times finer than the bf16 it
+// becomes; see two_powers), for a bounded piece of the tokens at a time.  A pass
+// over that piece turns it into dz in bf16, the operand of the two
 // products; the target's entry is expm1(z - lse) from the fp32 logit, since
 // exp(z - lse) - 1 would lose a confident token's gradient to rounding.  What
 // is rounded to bf16 is dz over the largest |g|, which comes back as a factor of
@@ -45,14 +45,11 @@ using namespace tide;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// exp(z - m) 2^15 for the tile row's maximum m, which fp16 keeps; nothing but -inf
-// in the row: 0.  (The difference first: a multiple of m by itself overflows
-// where a mask has left a tile row nothing but the lowest numbers.)
+// exp(z - m) for the tile row's maximum m; nothing but -inf in the row: 0.  (The
+// difference first: a multiple of m by itself overflows where a mask has left a
+// tile row nothing but the lowest numbers.)
 __device__ __forceinline__ float reference(float m) { return m == -__builtin_inff() ? 0.0f : m; }
-__device__ __forceinline__ float power(float z, float ref) {
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(z - ref, kLog2e, 15.0f));
-}
-constexpr float kSumUnit = 0x1p-15f;  // of the sums of those
+__device__ __forceinline__ float power(float z, float ref) { return __builtin_amdgcn_exp2f((z - ref) * kLog2e); }
 
 // The value 16 (32) lanes away: lane XOR 16 (32).
 __device__ __forceinline__ float other_16(float v) {
@@ -66,21 +63,20 @@ __device__ __forceinline__ float other_32(float v) {
   return __uint_as_float((threadIdx.x & 32) ? p[0] : p[1]);
 }
 
-__device__ __forceinline__ uint32_t half_bits(float v) {
-  const _Float16 h = _Float16(v);  // round to nearest even
-  uint16_t r;
-  __builtin_memcpy(&r, &h, 2);
-  return r;
+// Two numbers of [0, 1] in 16 bits each: 6 bits of exponent and 10 of fraction, the
+// middle bits of the fp32 number over 2^64, whose sign and two high exponent bits
+// are 0.  Above 2^-62 they are rounded by at most 2^-11 of themselves, below by
+// 2^-73.  (A word that is unlikely for every token gets its whole gradient from
+// such entries: of fp16 numbers, times 2^15, those below 2^-29 lose bits and those
+// below 2^-40 are 0.)
+constexpr float kPowerUnit = 0x1p64f;
+__device__ __forceinline__ uint32_t two_powers(float a, float b) {
+  const uint32_t x = (__float_as_uint(a * (1.0f / kPowerUnit)) << 3) + 0x8000u;
+  const uint32_t y = (__float_as_uint(b * (1.0f / kPowerUnit)) << 3) + 0x8000u;
+  return __builtin_amdgcn_perm(y, x, 0x07060302u);
 }
-
-__device__ __forceinline__ uint32_t two_halves(float a, float b) { return half_bits(a) | half_bits(b) << 16; }
-
-__device__ __forceinline__ float half_value(uint32_t bits) {
-  const uint16_t b = uint16_t(bits);
-  _Float16 h;
-  __builtin_memcpy(&h, &b, 2);
-  return float(h);
-}
+// The number in the low 16 bits, over kPowerUnit.
+__device__ __forceinline__ float power_value(uint32_t bits) { return __uint_as_float((bits & 0xFFFFu) << 13); }
 
 constexpr uint32_t kQueues = 3;  // of a piece's three products
 
@@ -206,7 +202,7 @@ struct LogitsArgs {
   int64_t first, piece;
   float2* stats;           // [row of the piece][vocabulary tile]: maximum, sum of the powers
   float* target_z;         // [row of the piece]
-  uint16_t* e;             // [row of the piece][e_ld], or null
+  uint16_t* e;             // [row of the piece][e_ld]: the powers in 16 bits, or null
   int64_t e_ld;
   uint32_t tiles_n;
   uint32_t* queue;         // null: every workgroup has its one tile
@@ -334,8 +330,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void logits_kernel(LogitsArgs a) {
     if (a.e) {
       // the pitch is a multiple of 64: a group of 8 columns is in or out
       auto put = [&](int r, int c, f32x4v lo, f32x4v hi) {
-        const u32x4 v = u32x4{two_halves(lo[0], lo[1]), two_halves(lo[2], lo[3]), two_halves(hi[0], hi[1]),
-                              two_halves(hi[2], hi[3])};
+        const u32x4 v = u32x4{two_powers(lo[0], lo[1]), two_powers(lo[2], lo[3]), two_powers(hi[0], hi[1]),
+                              two_powers(hi[2], hi[3])};
         *reinterpret_cast<u32x4*>(a.e + (m1 + r) * a.e_ld + n1 + c) = v;
       };
       if (m1 + BM <= rows && n1 + BN <= a.e_ld) {
@@ -486,7 +482,7 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LogitsArgs a) {
     if (lane < 16) sums[wave][row] = s;
     if (a.e && row < rows && n0 + 4 * g < a.e_ld)
       *reinterpret_cast<u32x2*>(a.e + row * a.e_ld + n0 + 4 * g) =
-          u32x2{two_halves(acc[t][0], acc[t][1]), two_halves(acc[t][2], acc[t][3])};
+          u32x2{two_powers(acc[t][0], acc[t][1]), two_powers(acc[t][2], acc[t][3])};
   }
   __syncthreads();
   for (int row = threadIdx.x; row < rows; row += 256) {
@@ -549,7 +545,6 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uin
     const int64_t token = count ? list[first + row] : row;
     const int64_t target = targets[token];
     const bool keep = target >= 0 && target < vocab;
-    s *= kSumUnit;
     const float l = top + logf(s);
     if (row_sum) row_sum[row] = make_float2(top, s);
     loss[token] = keep ? l - target_z[row] : 0.0f;
@@ -559,7 +554,7 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float2* stats, uin
 
 // ------------------------------------------------------------ gradients
 
-// The piece's exponentials (fp16) -> dz / *scale (bf16), in place; the columns from the
+// The piece's exponentials (two_powers) -> dz / *scale (bf16), in place; the columns from the
 // vocabulary's end to the row's pitch become 0.  A workgroup takes 2048
 // columns of a row.
 __global__ __launch_bounds__(256) void logit_grad_kernel(uint16_t* e, int64_t e_ld, int64_t vocab, const float2* stats,
@@ -581,10 +576,10 @@ __global__ __launch_bounds__(256) void logit_grad_kernel(uint16_t* e, int64_t e_
   if (c < vocab) {
     const u32x4 w = *p;
     const float tile_max = stats[row * tiles + uint32_t(c) / tile_cols].x;
-    const float f = __builtin_amdgcn_exp2f((tile_max - sum.x) * kLog2e) * (kSumUnit / sum.y * g);
+    const float f = __builtin_amdgcn_exp2f((tile_max - sum.x) * kLog2e) * (kPowerUnit / sum.y * g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float v = half_value(w[j >> 1] >> (16 * (j & 1))) * f;
+      float v = power_value(w[j >> 1] >> (16 * (j & 1))) * f;
       if (c + j == target) v = g * expm1f(target_z[row] - (sum.x + logf(sum.y)));
       if (c + j >= vocab) v = 0.0f;
       out[j >> 1] |= bf16_bits_of(v) << (16 * (j & 1));

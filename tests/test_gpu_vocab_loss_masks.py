@@ -60,6 +60,31 @@ def test_masked_words(tide, tokens, mask, below):
         r.check({"dhidden": small["dhidden"]})
 
 
+@pytest.mark.parametrize("tokens", [10, 100, 300])
+def test_nothing_left_but_the_lowest_number(tide, tokens):
+    """Every logit the lowest number: all words are as likely."""
+    import torch
+
+    size, vocab = 40, 1500
+    h, w, t, g = make(np.random.default_rng(tokens), tokens, size, vocab)
+    h[:, :] = 0.0
+    h[:, -1] = 1.0
+    w[:, -1] = LOWEST
+    for r in (Run(tide, h, w, t, None), Run(tide, h, w, t, g, "f32")):
+        # sums of 1500 ones, and a logarithm
+        assert float((r.loss.double() - np.log(vocab)).abs().max()) < 2.0**-19
+        assert bool((r.lse == LOWEST).all())
+    want = np.zeros((vocab, size))
+    np.add.at(want[:, -1], t, -g.astype(float))
+    want[:, -1] += g.astype(float).sum() / vocab
+    terms = np.zeros(vocab)
+    np.add.at(terms, t, g.astype(float))
+    terms += g.astype(float).sum() / vocab
+    # dz rounded by 2^-8, its exponentials and sums far less
+    assert (np.abs(r.dw.double().cpu().numpy() - want)[:, -1] <= 1.01 * 2.0**-8 * terms).all()
+    assert not r.dw[:, :-1].any()
+
+
 @pytest.mark.parametrize("tokens", [10, 300])
 def test_nothing_left_but_minus_infinity(tide, tokens):
     """Every logit of one token -infinity: NaN in its loss, the others' are

@@ -274,10 +274,17 @@ class Plan:
                                           _ptr_array(param_ptrs), ctypes.c_void_p(int(stream) or None)))
 
 
+# The current stream's handle alone (building torch.cuda.current_stream()'s object
+# takes longer than a launch) and torch.cuda.current_device() without its check
+# that there is one, or the public calls in a torch that lacks these.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream_handle(stream):
     if stream is None:
-        # the handle alone: building torch.cuda.current_stream()'s object takes longer than a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     return int(stream.cuda_stream)
 
 
@@ -499,10 +506,6 @@ def allgather_copyin(plan, shards, rank_major, stream=None):
 _BF16 = (torch.bfloat16,)
 _FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 _CODES = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_INT8}
-
-
-def _current_device():
-    return torch._C._cuda_getDevice()  # torch.cuda.current_device(), but for its check that there is one
 
 
 def _device_stream(stream):

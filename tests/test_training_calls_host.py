@@ -1,5 +1,8 @@
 """Registered calls of the operators with a workspace (no GPU: the library's
 launches and the device's parts of the binding are replaced)."""
+import os
+import subprocess
+import sys
 import types
 
 import pytest
@@ -111,3 +114,19 @@ def test_launches_on_another_device_are_refused(tide, monkeypatch, name):
         with pytest.raises(ValueError, match="device"):
             call(stream)
     assert len(launched) == 2
+
+
+def test_public_torch_calls_where_the_private_ones_are_missing():
+    code = """
+import types
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    delattr(torch._C, name)
+from param_collectives_amd import tide
+assert tide._current_device is torch.cuda.current_device
+torch.cuda.current_device = lambda: 0
+torch.cuda.current_stream = lambda device: types.SimpleNamespace(cuda_stream=0x5000 + device)
+assert tide._stream_handle(None) == 0x5000
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)

@@ -557,7 +557,7 @@ def _vector(t, dtype, n, what):
     return t.data_ptr()
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=256)
 def checkpoint_layout(cols):
     """(code columns, scale columns) of a checkpoint of rows of `cols` values
     (tide_checkpoint_layout)."""

@@ -130,3 +130,12 @@ assert tide._stream_handle(None) == 0x5000
 """
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
+
+
+def test_the_layouts_kept_are_bounded():
+    from param_collectives_amd import tide
+
+    for cols in range(2000):
+        blocks = -(-cols // 32)
+        assert tide.checkpoint_layout(cols) == (32 * blocks, blocks)
+    assert tide.checkpoint_layout.cache_info().currsize <= 256

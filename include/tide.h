@@ -394,7 +394,8 @@ tide_status tide_stock_chunk_cat(tide_plan* plan, const uint16_t* const* grads, 
  * or half a unit (int8); saturation passes those bounds only for magnitudes
  * above 1.75 * 2^127 (e4m3) or 127.5 * 2^121 (int8).  A block that holds a NaN
  * or an infinity gets b = 255 and comes back as NaN throughout.  Every other
- * restored value is 0 or a normal bf16 number, so restoring rounds nothing.
+ * restored value is 0 or a normal bf16 number, so restoring rounds nothing.  The
+ * readers are defined for the scale bytes that packing writes, these only.
  *
  * Sizes: rows below 2^31, cols and row strides up to 2^22, a matrix up to
  * 2^34 elements with its rows filled up to a multiple of 64 (else

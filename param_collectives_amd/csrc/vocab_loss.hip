@@ -22,16 +22,18 @@
 // 0.0017 of it from the results' own rounding).
 //
 // Bound by the matrix cores and their power: at 4096 x 4096 x 128000 (tokens x
-// hidden x vocabulary) the three products run 69 to 75% of the cycles, with the
-// clock down to 1.7 GHz, and take 3.4, 3.2 and 3.2 of 10.2 ms (9.8 to 10.3 ms over
-// the cards; 1250 to 1310 TFLOP/s); turning the logits into dz takes 0.33 ms at
+// hidden x vocabulary) the three products run 66 to 80% of the cycles, with the
+// clock down to 1.75 GHz, and take 3.4, 2.9 to 3.2 and 3.2 of 9.9 ms (9.8 to 10.3 ms
+// over the cards; 1250 to 1310 TFLOP/s); turning the logits into dz takes 0.33 ms at
 // 6.3 TB/s.  The loss of 4096 x 4096 x 65536 takes 1.65 to 1.75 ms.  At up to 64
 // tokens the weights' traffic is the bound (few_logits_kernel), in between a
 // tile's latency: a step of 32 k takes 0.45 us with 128 x 128 tiles, 0.72 us with
 // 256 x 256 ones.
 //
-// Tokens whose target lies outside the vocabulary are left out: their rows are
-// never read, so nothing in them (a padded batch's NaN) reaches the others.
+// Tokens whose target lies outside the vocabulary are left out: nothing in their
+// rows (a padded batch's NaN) reaches the others.  Where tokens are listed, those
+// rows are never read; the loss of at most 256 tokens reads them with the others,
+// and what a tile's row holds stays in its row.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -391,7 +391,8 @@ def per_call_text(res, command):
              "one aggressor call released in a back-to-back victim sequence: the victims' extra time (penalty, "
              "median of 5), the call's duration beside them, and penalty / call duration (the slowdown of the "
              "victim work the call overlapped); the disjoint split runs the victims on 240 CUs, the call on the "
-             "other 16"]
+             "other 16; a sequence's time varies by some tenths of a millisecond by itself, so that the penalty of "
+             "a call as short as the copy-out's is not resolved"]
     vics = list(res["victims"])
     head = f"{'aggressor':<26} {'CUs':>4} {'alone ms':>9} " + " ".join(
         f"{v[:18] + ' pen ms':>26} {'call ms':>8} {'overlap %':>9}" for v in vics)

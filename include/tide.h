@@ -516,6 +516,47 @@ tide_status tide_vocab_loss_grad(const uint16_t* hidden, int64_t hidden_stride, 
                                  void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Layer norm and its gradients, the start of a sublayer: the weight's and the
+ * bias's go to the reduce-scatter.  None touches a plan.
+ *
+ * For every row of n = cols values
+ *   mean = sum x / n,  rstd = 1 / sqrt(sum (x - mean)^2 / n + eps)
+ *   out  = (x - mean) * rstd * weight + bias
+ * and, from dout and with xh = (x - mean) * rstd, g = dout * weight,
+ *   dx      = rstd * (g - sum g / n - xh * sum (g * xh) / n)
+ *   dweight = sum over rows of dout * xh,  dbias = sum over rows of dout
+ *                                     (+ old, accumulate = 1)
+ * Everything is computed in fp32 and rounded once to the results' types; sums go
+ * in an order that depends on the sizes and types only.  A row that holds a NaN
+ * or an infinity comes out as NaN, the other rows are not touched by it (dweight
+ * and dbias sum over all).
+ *
+ *   x, dx    rows x cols of x_dtype;  out, dout  rows x cols of out_dtype
+ *            (dout_dtype); rows their strides apart, aligned to the element.
+ *            What lies between two rows is left alone.  No output may overlap
+ *            an input.
+ *   weight, bias, dweight, dbias  cols values of affine_dtype without gaps.
+ *            weight NULL stands for 1, bias NULL for 0; dweight or dbias NULL:
+ *            not wanted.
+ *   mean, rstd  rows fp32; forward: either may be NULL
+ *   workspace  as for the weight gradient above (not needed where neither
+ *            dweight nor dbias is wanted)
+ * Sizes: as for the checkpoints, cols at least 1.  rows = 0: dweight and dbias
+ * become 0, or stay.
+ * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+tide_status tide_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t cols,
+                            const void* weight, const void* bias, int32_t affine_dtype, float eps, void* out,
+                            int32_t out_dtype, int64_t out_stride, float* mean, float* rstd, void* stream);
+tide_status tide_layer_norm_grad_workspace(int32_t x_dtype, int32_t dout_dtype, int64_t rows, int64_t cols,
+                                           int64_t* bytes);
+tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t dout_stride, const void* x,
+                                 int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t cols, const void* weight,
+                                 int32_t affine_dtype, const float* mean, const float* rstd, void* dx,
+                                 int64_t dx_stride, void* dweight, void* dbias, int32_t accumulate, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Interference instruments (Section 2.2 "SM Wave Quantization", Equation 4,
  * Figure 3, Table 4 and Table 5): what one GPU can show of the cost a
  * collective's kernels impose on the compute they overlap.  None of these

@@ -111,6 +111,18 @@ __device__ __forceinline__ uint32_t renew(uint32_t& v) {
 
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6); }
 
+// The value 16 (32) lanes away: lane XOR 16 (32).
+__device__ __forceinline__ float other_16(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return __uint_as_float((threadIdx.x & 16) ? p[0] : p[1]);
+}
+__device__ __forceinline__ float other_32(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float((threadIdx.x & 32) ? p[0] : p[1]);
+}
+
 __device__ __forceinline__ int row_swizzle(int r) { return -(r >> 2) & 3; }
 __device__ __forceinline__ int col_swizzle(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
 

@@ -1,7 +1,8 @@
 // C ABI of the training-step operators (include/tide.h): argument checks and
 // workspace sizes of the 8-bit activation checkpoints, of the weight gradient
-// that reads them and of the vocabulary loss.  Host code only; the kernels are
-// in checkpoint.hip, weight_grad.hip and vocab_loss.hip.
+// that reads them, of the vocabulary loss, of layer norm, of the gated block and
+// of the orthogonalised updates.  Host code only; the kernels are in the .hip
+// files of those names.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -133,6 +134,33 @@ tide::VocabLossCall vocab_loss_call(const void* hidden, int64_t hidden_stride, c
   c.hidden = hidden_size;
   c.vocab = vocab;
   return c;
+}
+
+// Checks shared by layer norm and its gradients; *call is filled in.
+tide_status layer_norm_call(const void* x, int32_t x_dtype, int64_t x_stride, const char* y_name, int32_t y_dtype,
+                            int64_t y_stride, int64_t rows, int64_t cols, const void* weight, const void* bias,
+                            int32_t affine_dtype, tide::LayerNormCall* call) {
+  TIDE_TRY(check_dtype("x_dtype", x_dtype));
+  TIDE_TRY(check_dtype((std::string(y_name) + "_dtype").c_str(), y_dtype));
+  TIDE_TRY(check_dtype("affine_dtype", affine_dtype));
+  TIDE_TRY(check_matrix("x", rows, cols, x_stride));
+  TIDE_TRY(check_matrix(y_name, rows, cols, y_stride));
+  if (cols < 1) return invalid("a row must hold at least one value");
+  if (weight) TIDE_TRY(check_pointer("weight", weight, size_of(affine_dtype)));
+  if (bias) TIDE_TRY(check_pointer("bias", bias, size_of(affine_dtype)));
+  if (rows > 0) TIDE_TRY(check_pointer("x", x, size_of(x_dtype)));
+  *call = tide::LayerNormCall{};
+  call->x = x;
+  call->x_ld = x_stride;
+  call->x_f32 = x_dtype == TIDE_DTYPE_F32;
+  call->y_f32 = y_dtype == TIDE_DTYPE_F32;
+  call->y_ld = y_stride;
+  call->weight = weight;
+  call->bias = bias;
+  call->affine_f32 = affine_dtype == TIDE_DTYPE_F32;
+  call->rows = rows;
+  call->cols = cols;
+  return TIDE_OK;
 }
 
 }  // namespace
@@ -285,6 +313,76 @@ tide_status tide_vocab_loss_grad(const uint16_t* hidden, int64_t hidden_stride, 
     c.lse = lse;
     c.dhidden = dhidden;
     return hip_status(tide::launch_vocab_loss(c, workspace, stream), "vocabulary loss launch");
+  });
+}
+
+tide_status tide_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t cols,
+                            const void* weight, const void* bias, int32_t affine_dtype, float eps, void* out,
+                            int32_t out_dtype, int64_t out_stride, float* mean, float* rstd, void* stream) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    tide::LayerNormCall c;
+    TIDE_TRY(layer_norm_call(x, x_dtype, x_stride, "out", out_dtype, out_stride, rows, cols, weight, bias, affine_dtype,
+                             &c));
+    if (!(eps >= 0)) return invalid("eps must not be negative");
+    if (rows == 0) return TIDE_OK;
+    TIDE_TRY(check_pointer("out", out, size_of(out_dtype)));
+    if (mean) TIDE_TRY(check_pointer("mean", mean, 4));
+    if (rstd) TIDE_TRY(check_pointer("rstd", rstd, 4));
+    c.eps = eps;
+    c.out = out;
+    c.mean = mean;
+    c.rstd = rstd;
+    return hip_status(tide::launch_layer_norm(c, nullptr, stream), "layer norm launch");
+  });
+}
+
+tide_status tide_layer_norm_grad_workspace(int32_t x_dtype, int32_t dout_dtype, int64_t rows, int64_t cols,
+                                           int64_t* bytes) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    if (bytes == nullptr) return invalid("bytes must not be NULL");
+    tide::LayerNormCall c;
+    const float here = 0.0f;  // stands for tensors
+    TIDE_TRY(layer_norm_call(&here, x_dtype, cols, "dout", dout_dtype, cols, rows, cols, nullptr, nullptr, TIDE_DTYPE_F32,
+                             &c));
+    c.dweight = const_cast<float*>(&here);
+    *bytes = tide::layer_norm_grad_bytes(c);
+    return TIDE_OK;
+  });
+}
+
+tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t dout_stride, const void* x,
+                                 int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t cols, const void* weight,
+                                 int32_t affine_dtype, const float* mean, const float* rstd, void* dx,
+                                 int64_t dx_stride, void* dweight, void* dbias, int32_t accumulate, void* workspace,
+                                 int64_t workspace_bytes, void* stream) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    tide::LayerNormCall c;
+    TIDE_TRY(layer_norm_call(x, x_dtype, x_stride, "dout", dout_dtype, dout_stride, rows, cols, weight, nullptr,
+                             affine_dtype, &c));
+    if (accumulate != 0 && accumulate != 1) return invalid("accumulate must be 0 or 1");
+    TIDE_TRY(check_matrix("dx", rows, cols, dx_stride));
+    if (dweight) TIDE_TRY(check_pointer("dweight", dweight, size_of(affine_dtype)));
+    if (dbias) TIDE_TRY(check_pointer("dbias", dbias, size_of(affine_dtype)));
+    c.grad = true;
+    c.dweight = dweight;
+    c.dbias = dbias;
+    c.accumulate = accumulate;
+    if (rows > 0) {
+      TIDE_TRY(check_pointer("dout", dout, size_of(dout_dtype)));
+      TIDE_TRY(check_pointer("mean", mean, 4));
+      TIDE_TRY(check_pointer("rstd", rstd, 4));
+      TIDE_TRY(check_pointer("dx", dx, size_of(x_dtype)));
+      TIDE_TRY(check_workspace(workspace, workspace_bytes, tide::layer_norm_grad_bytes(c)));
+    }
+    c.dout = dout;
+    c.mean = const_cast<float*>(mean);
+    c.rstd = const_cast<float*>(rstd);
+    c.dx = dx;
+    c.dx_ld = dx_stride;
+    return hip_status(tide::launch_layer_norm(c, workspace, stream), "layer norm gradient launch");
   });
 }
 

@@ -1,7 +1,8 @@
 // Private types of the training-step operators: the 8-bit activation
 // checkpoints (checkpoint.hip), the weight gradient that reads them
-// (weight_grad.hip), the vocabulary loss (vocab_loss.hip) and their C ABI
-// (training.cpp).
+// (weight_grad.hip), the vocabulary loss (vocab_loss.hip), layer norm
+// (layer_norm.hip), the gated block (gated_block.hip), orthogonalised updates
+// (orthogonalize.hip) and their C ABI (training.cpp).
 #pragma once
 
 #include <cstdint>
@@ -124,6 +125,29 @@ struct VocabLossCall {
   int32_t dw_f32, accumulate;
 };
 
+struct LayerNormCall {
+  const void* x;
+  int64_t x_ld;
+  int32_t x_f32, y_f32;  // of x and dx, of out and dout
+  const void* weight;    // may be null, as bias
+  const void* bias;
+  int32_t affine_f32;
+  int64_t rows, cols;
+  float eps;
+  void* out;
+  int64_t y_ld;  // of out or dout
+  float* mean;   // may be null in the forward pass
+  float* rstd;
+  // the gradients
+  bool grad;
+  const void* dout;
+  void* dx;
+  int64_t dx_ld;
+  void* dweight;  // may be null, as dbias
+  void* dbias;
+  int32_t accumulate;
+};
+
 // Whether rows of `cols` bf16 elements, `ld` apart from p, all start and end on
 // 16 bytes: the tiles then read them in place, 16 bytes at a time and never
 // past a row's end.
@@ -142,6 +166,8 @@ int launch_unpack(const PackCall& c, void* stream);
 int launch_weight_grad(const WeightGradCall& c, void* workspace, void* stream);
 int64_t vocab_loss_bytes(const VocabLossCall& c);  // its workspace
 int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream);
+int64_t layer_norm_grad_bytes(const LayerNormCall& c);
+int launch_layer_norm(const LayerNormCall& c, void* workspace, void* stream);
 int launch_align_rows(const void* src, int64_t src_ld, int64_t rows, int64_t cols, void* dst, int64_t ld,
                       void* stream);
 

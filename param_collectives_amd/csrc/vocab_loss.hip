@@ -53,18 +53,6 @@ constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ float reference(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 __device__ __forceinline__ float power(float z, float ref) { return __builtin_amdgcn_exp2f((z - ref) * kLog2e); }
 
-// The value 16 (32) lanes away: lane XOR 16 (32).
-__device__ __forceinline__ float other_16(float v) {
-  const uint32_t b = __float_as_uint(v);
-  const auto p = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-  return __uint_as_float((threadIdx.x & 16) ? p[0] : p[1]);
-}
-__device__ __forceinline__ float other_32(float v) {
-  const uint32_t b = __float_as_uint(v);
-  const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __uint_as_float((threadIdx.x & 32) ? p[0] : p[1]);
-}
-
 // A token's loss from its row's maximum, the sum of exp(z - maximum) (at least 1,
 // the maximum's own) and the target's logit.  The two logits' difference is taken
 // first: lse - z_t, each rounded by itself, is noise where the target is likely

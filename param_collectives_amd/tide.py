@@ -66,6 +66,9 @@ EXPORTS = (
     "tide_vocab_loss_workspace",
     "tide_vocab_loss",
     "tide_vocab_loss_grad",
+    "tide_layer_norm",
+    "tide_layer_norm_grad_workspace",
+    "tide_layer_norm_grad",
     "tide_device_info",
     "tide_probe_launch",
     "tide_victim_axpb",
@@ -117,6 +120,10 @@ def _load():
     lib.tide_vocab_loss_workspace.argtypes = [vp, i64, vp, i64, i64, i64, i64, i32, i32, i64p]
     lib.tide_vocab_loss.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp, i64, vp]
     lib.tide_vocab_loss_grad.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, i64, vp]
+    lib.tide_layer_norm.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, i32, i64, vp, vp, vp]
+    lib.tide_layer_norm_grad_workspace.argtypes = [i32, i32, i64, i64, i64p]
+    lib.tide_layer_norm_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, i64, vp, vp, i32, vp,
+                                         i64, vp]
     i32p = ctypes.POINTER(i32)
     lib.tide_device_info.argtypes = [i32p, i32p, i32p, i32p]
     lib.tide_probe_launch.argtypes = [vp, i32, i32, i64, vp]
@@ -769,6 +776,93 @@ def vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dwei
     handle = _device_stream(stream)
     ws, nbytes, keep = _workspace(need, workspace, stream)
     _check(lib.tide_vocab_loss_grad(*args, ws, nbytes, handle))
+
+
+# ------------------------------------------------------------ layer norm
+
+
+def _affine(named, cols):
+    """(addresses, TIDE_DTYPE_*) of vectors of `cols` values that may be None,
+    all of one dtype."""
+    given = [t for _, t in named if t is not None]
+    dtype = given[0].dtype if given and isinstance(given[0], torch.Tensor) else torch.float32
+    if dtype not in _FLOATS:
+        raise TypeError(f"{' and '.join(what for what, _ in named)}: expected torch.bfloat16 or torch.float32, got {dtype}")
+    return [None if t is None else _vector(t, dtype, cols, what) for what, t in named], _FLOATS[dtype]
+
+
+def _same_shape(rows, cols, what, got):
+    if got != (rows, cols):
+        raise ValueError(f"{what} must be {rows} x {cols}, got {got[0]} x {got[1]}")
+
+
+def _layer_norm_args(x, weight, bias, out, mean, rstd, eps):
+    p, rows, cols, stride = _matrix(x, _FLOATS, "x")
+    y, *shape, y_stride = _matrix(out, _FLOATS, "out")
+    _same_shape(rows, cols, "out", tuple(shape))
+    (w, b), affine = _affine((("weight", weight), ("bias", bias)), cols)
+    stats = [None if t is None else _vector(t, torch.float32, rows, what) for what, t in (("mean", mean), ("rstd", rstd))]
+    return p, _FLOATS[x.dtype], stride, rows, cols, w, b, affine, eps, y, _FLOATS[out.dtype], y_stride, *stats
+
+
+def layer_norm_call(x, weight, bias, out, mean=None, rstd=None, eps=1e-5):
+    """A registered layer norm (see layer_norm)."""
+    return TensorCall(lib.tide_layer_norm, _layer_norm_args(x, weight, bias, out, mean, rstd, eps),
+                      (x, weight, bias, out, mean, rstd))
+
+
+def layer_norm(x, weight, bias, out, mean=None, rstd=None, eps=1e-5, stream=None):
+    """Layer norm of the rows of x (bf16 or fp32, contiguous rows) into out (bf16
+    or fp32): out = (x - mean) * rstd * weight + bias.  weight and bias hold one
+    value a column, bf16 or fp32, or are None (1 and 0).  mean and rstd, if given,
+    receive each row's (fp32), as layer_norm_grad reads them (tide_layer_norm)."""
+    _check(lib.tide_layer_norm(*_layer_norm_args(x, weight, bias, out, mean, rstd, eps), _device_stream(stream)))
+
+
+def layer_norm_grad_workspace(x, dout):
+    """Bytes of workspace layer_norm_grad takes (tide_layer_norm_grad_workspace)."""
+    _, rows, cols, _ = _matrix(x, _FLOATS, "x")
+    _matrix(dout, _FLOATS, "dout")
+    return _layer_norm_grad_bytes(_FLOATS[x.dtype], _FLOATS[dout.dtype], rows, cols)
+
+
+def _layer_norm_grad_bytes(x_dtype, dout_dtype, rows, cols):
+    need = ctypes.c_int64()
+    _check(lib.tide_layer_norm_grad_workspace(x_dtype, dout_dtype, rows, cols, ctypes.byref(need)))
+    return need.value
+
+
+def _layer_norm_grad_args(dout, x, weight, mean, rstd, dx, dweight, dbias, accumulate):
+    """(arguments up to the workspace's, bytes of workspace)."""
+    p, rows, cols, stride = _matrix(x, _FLOATS, "x")
+    y, *y_shape, y_stride = _matrix(dout, _FLOATS, "dout")
+    _same_shape(rows, cols, "dout", tuple(y_shape))
+    d, *d_shape, d_stride = _matrix(dx, (x.dtype,), "dx")
+    _same_shape(rows, cols, "dx", tuple(d_shape))
+    (w, dw, db), affine = _affine((("weight", weight), ("dweight", dweight), ("dbias", dbias)), cols)
+    m, r = _vector(mean, torch.float32, rows, "mean"), _vector(rstd, torch.float32, rows, "rstd")
+    xt, yt = _FLOATS[x.dtype], _FLOATS[dout.dtype]
+    need = 0 if dw is None and db is None else _layer_norm_grad_bytes(xt, yt, rows, cols)
+    return (y, yt, y_stride, p, xt, stride, rows, cols, w, affine, m, r, d, d_stride, dw, db, int(bool(accumulate))), need
+
+
+def layer_norm_grad_call(dout, x, weight, mean, rstd, dx, dweight=None, dbias=None, accumulate=False, workspace=None):
+    """A registered gradient of layer norm (see layer_norm_grad); `workspace` as
+    for checkpoint_weight_grad_call."""
+    args, need = _layer_norm_grad_args(dout, x, weight, mean, rstd, dx, dweight, dbias, accumulate)
+    return WorkspaceCall(lib.tide_layer_norm_grad, args, (dout, x, weight, mean, rstd, dx, dweight, dbias), need, workspace)
+
+
+def layer_norm_grad(dout, x, weight, mean, rstd, dx, dweight=None, dbias=None, accumulate=False, workspace=None,
+                    stream=None):
+    """Gradients of layer_norm from dout and its x, weight, mean and rstd: dx (of
+    x's dtype) and, if given, dweight and dbias (of weight's dtype; added to the
+    old ones when accumulate is true).  `workspace` as for checkpoint_weight_grad
+    (tide_layer_norm_grad)."""
+    args, need = _layer_norm_grad_args(dout, x, weight, mean, rstd, dx, dweight, dbias, accumulate)
+    handle = _device_stream(stream)
+    ws, nbytes, keep = _workspace(need, workspace, stream)
+    _check(lib.tide_layer_norm_grad(*args, ws, nbytes, handle))
 
 
 # ------------------------------------------------------------ instruments

@@ -1,0 +1,80 @@
+"""64-bit references of the sublayer's operators (layer norm, the gated block,
+orthogonalised updates), for the tests: numpy on the CPU, from the definitions
+in include/tide.h, each with a bound of the kernels' error before the result is
+rounded to its own type."""
+import numpy as np
+
+U32 = 2.0**-24  # half a step of fp32: a rounding's relative error
+HALF = {"bf16": 2.0**-8, "f32": 2.0**-24, "f16": 2.0**-11}
+TINY = {"bf16": 2.0**-134, "f32": 2.0**-150}  # half a step below the normal numbers
+
+
+def rounded(value, err, dtype):
+    """The bound after one rounding to `dtype`."""
+    return err + HALF[dtype] * (np.abs(value) + err) + TINY[dtype]
+
+
+def row_adds(n):
+    """Additions a value of a row of n goes through: a thread's own (at most 16
+    values, or n / 1024 where rows are read by loops of 1024 threads), six steps
+    of a wave and at most 16 waves' sums, and two more for the division."""
+    return max(16, -(-n // 1024) + 4) + 6 + 16 + 2
+
+
+def layer_norm(x, w, b, eps):
+    """{name: (value, bound)} of out, mean and rstd for float64 x (rows x n), w
+    and b.
+
+    A mean is rounded once, whatever its sum lost: what is left of it, off, is
+    taken back.  v = x - mean is rounded by U32 of itself, off is a mean of n of
+    them and differs from theirs by K + 1 roundings of the mean magnitude, and
+    x - mean - off is rounded again.  The squares' mean carries 3 + K of them,
+    rstd half of those and four more (eps, the root, the division, each counted
+    twice for routines that are off by a whole step).  The factor 1.01 stands for
+    products of these errors."""
+    n = x.shape[1]
+    K = row_adds(n)
+    mean = x.mean(-1, keepdims=True)
+    d = x - mean
+    var = (d * d).mean(-1, keepdims=True)
+    # the mean as first rounded is off by at most this, and so are the v
+    first = (K + 1) * U32 * np.abs(x).mean(-1, keepdims=True)
+    v = np.abs(d) + first
+    e_off = (K + 2) * U32 * v.mean(-1, keepdims=True)
+    e_mean = e_off + U32 * (np.abs(mean) + e_off)
+    e_num = 3 * U32 * v + e_off
+    squares = (v * v).mean(-1, keepdims=True)
+    e_var = (K + 4) * U32 * squares + 2 * (K + 4) * U32 * first**2 + 2 * first * e_off
+    rstd = 1 / np.sqrt(var + eps)
+    rel = e_var / (var + eps) / 2 * (1 + 2 * e_var / (var + eps)) + 8 * U32
+    xh = d * rstd
+    out = xh * w + b
+    e = 1.01 * (np.abs(w) * (rstd * e_num * (1 + rel) + np.abs(xh) * (rel + 3 * U32)) + 2 * U32 * (np.abs(xh * w) + np.abs(b)))
+    return {"out": (out, e), "mean": (mean[:, 0], 1.01 * e_mean[:, 0]), "rstd": (rstd[:, 0], 1.01 * (rel * rstd)[:, 0])}
+
+
+def layer_norm_grad(dy, x, w, mean, rstd, old_dw=None, old_db=None):
+    """{name: (value, bound)} of dx, dweight and dbias from the mean and rstd that
+    are given (float64 of fp32 values).
+
+    xh carries 2 roundings, g 1, their row sums K more; dx's four operations one
+    each.  A column's sum goes through at most rows / 256 + 150 additions: a
+    thread's rows (256 workgroups at least where there are that many rows), 4
+    waves', a 16th of at most 2048 workgroups', 16 shares."""
+    rows, n = x.shape
+    K = row_adds(n)
+    mean, rstd = mean[:, None], rstd[:, None]
+    xh = (x - mean) * rstd
+    g = dy * w
+    s, sx = g.mean(-1, keepdims=True), (g * xh).mean(-1, keepdims=True)
+    ma, mx = np.abs(g).mean(-1, keepdims=True), np.abs(g * xh).mean(-1, keepdims=True)
+    dx = rstd * (g - s - xh * sx)
+    mag = np.abs(g) + np.abs(s) + np.abs(xh * sx)
+    e = rstd * (U32 * np.abs(g) + (K + 2) * U32 * ma + np.abs(xh) * (K + 6) * U32 * mx + 3 * U32 * np.abs(xh * sx) + 4 * U32 * mag)
+    L = rows / 256 + 150
+    dw, db = (dy * xh).sum(0), dy.sum(0)
+    e_dw, e_db = (L + 4) * U32 * np.abs(dy * xh).sum(0), (L + 1) * U32 * np.abs(dy).sum(0)
+    if old_dw is not None:
+        dw, db = dw + old_dw, db + old_db
+        e_dw, e_db = e_dw + U32 * np.abs(dw), e_db + U32 * np.abs(db)
+    return {"dx": (dx, 1.01 * e), "dweight": (dw, 1.01 * e_dw), "dbias": (db, 1.01 * e_db)}

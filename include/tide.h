@@ -557,6 +557,62 @@ tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t d
                                  int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The gated feed-forward block and its gradients: both projections, the
+ * activation and the product.  The weights' gradients go to the reduce-scatter.
+ * None touches a plan.
+ *
+ * With x (tokens x hidden_size), w_gate and w_up (ffn_size x hidden_size each,
+ * all bf16)
+ *   g[t][f] = sum over d of x[t][d] * w_gate[f][d]
+ *   u[t][f] = sum over d of x[t][d] * w_up[f][d]
+ *   out = act(g) * u
+ * and, from dout,
+ *   dg = dout * u * act'(g),  du = dout * act(g)
+ *   dx[t][d] = sum over f of dg[t][f] * w_gate[f][d] + du[t][f] * w_up[f][d]
+ *   dw_gate[f][d] = sum over t of dg[t][f] * x[t][d]
+ *   dw_up[f][d]   = sum over t of du[t][f] * x[t][d]      (+ old, accumulate = 1)
+ * act(g) is g / (1 + exp(-g)) (TIDE_ACT_SILU) or GELU in its tanh form,
+ *   g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))) (TIDE_ACT_GELU).
+ * Products are exact, sums and activations fp32.  out is rounded once.  `gates`,
+ * if given, receives g and then u of every token in bf16 (g at column 0, u at
+ * column ffn_size of rows of 2 * ffn_size): with it the gradients need not form
+ * them again, and are those of the rounded g and u; without it they use the fp32
+ * ones.  dg and du are rounded to bf16 (by at most 2^-8 of themselves) as operands
+ * of the last three products, also where dw is fp32, and those round once more to
+ * their own types.  The order of every sum depends on the sizes, strides and
+ * alignments only.
+ *
+ *   x, dx, w_gate, w_up, out, dout, gates  rows their strides apart, 2-byte
+ *           aligned.  What lies between two rows is left alone.  No output may
+ *           overlap an input.  Where rows of x or of the weights do not all start
+ *           and end on 16 bytes, the weights' strides differ, or, for the
+ *           gradients, ffn_size is no multiple of 32, the workspace holds a copy of
+ *           them (the forward pass of up to 16 tokens needs none).
+ *   dw_gate, dw_up  ffn_size x hidden_size of dw_dtype, without gaps
+ *   workspace  as for the weight gradient above; with gradients it also holds dg
+ *           and du.  The _workspace call takes the same gates (NULL or not).
+ * Sizes: matrices as for the checkpoints, hidden_size and ffn_size at least 1,
+ * ffn_size up to 2^21.  tokens = 0: the weights' gradients become 0, or stay.
+ * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+#define TIDE_ACT_SILU 0
+#define TIDE_ACT_GELU 1
+
+tide_status tide_gated_block_workspace(const uint16_t* x, int64_t x_stride, const uint16_t* w_gate, int64_t gate_stride,
+                                       const uint16_t* w_up, int64_t up_stride, int64_t tokens, int64_t hidden_size,
+                                       int64_t ffn_size, int32_t gradients, const uint16_t* gates, int64_t* bytes);
+tide_status tide_gated_block(const uint16_t* x, int64_t x_stride, const uint16_t* w_gate, int64_t gate_stride,
+                             const uint16_t* w_up, int64_t up_stride, int64_t tokens, int64_t hidden_size,
+                             int64_t ffn_size, int32_t activation, uint16_t* out, int64_t out_stride, uint16_t* gates,
+                             int64_t gates_stride, void* workspace, int64_t workspace_bytes, void* stream);
+tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, const uint16_t* x, int64_t x_stride,
+                                  const uint16_t* w_gate, int64_t gate_stride, const uint16_t* w_up, int64_t up_stride,
+                                  int64_t tokens, int64_t hidden_size, int64_t ffn_size, int32_t activation,
+                                  const uint16_t* gates, int64_t gates_stride, uint16_t* dx, int64_t dx_stride,
+                                  void* dw_gate, void* dw_up, int32_t dw_dtype, int32_t accumulate, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Interference instruments (Section 2.2 "SM Wave Quantization", Equation 4,
  * Figure 3, Table 4 and Table 5): what one GPU can show of the cost a
  * collective's kernels impose on the compute they overlap.  None of these

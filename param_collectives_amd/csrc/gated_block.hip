@@ -1,0 +1,605 @@
+// The gated feed-forward block on MI355X (gfx950): for tokens x (T x D) and
+// weights Wg, Wu (F x D each)
+//   g = x Wg^T,  u = x Wu^T,  h = act(g) u
+// and, from dh,
+//   dg = dh u act'(g),  du = dh act(g)
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
+//
+// Forward: a tile holds the products with the same columns of both weights (the
+// B side of a tile is half Wg's rows, half Wu's), and a wave those that belong
+// together, so that h leaves the accumulators in the one launch and g and u are
+// written only where the backward pass is to have them.
+//
+// Backward: dg and du, side by side in rounded bf16, are the operand of the other
+// products.  They come from kept g and u in a pass over them, or, where only x was
+// kept, from the forward pass's product again, whose epilogue then reads dh: the
+// unrounded sums go in, and nothing but dg and du is written.  dx is one product
+// over 2 F values of k, the two weights stacked; dWg and dWu are one launch.
+//
+// Up to 16 tokens, the weights' traffic is all that counts (few_gated_kernel).
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm.h"
+#include "training.h"
+
+namespace {
+
+using namespace tide;
+
+// The activation and its derivative.  Both activations are z sigma(k(z)) (GELU in
+// its tanh form: (1 + tanh y) / 2 = sigma(2 y)), with sigma and 1 - sigma each
+// taken from exp(-|k|): neither cancels nor overflows at either end.
+struct Act {
+  float value, slope;
+};
+__device__ __forceinline__ Act activate(float z, int32_t gelu) {
+  constexpr float kLog2e = 1.44269504088896340736f, kRoot = 1.59576912160573071176f, kCube = 0.044715f;
+  const float z2 = z * z;
+  const float k = gelu ? kRoot * z * (1.0f + kCube * z2) : z;
+  const float dk = gelu ? kRoot * (1.0f + 3.0f * kCube * z2) : 1.0f;
+  const float e = __builtin_amdgcn_exp2f(-fabsf(k) * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+  const float s = k >= 0.0f ? r : (k < 0.0f ? er : k);  // NaN stays
+  const float both = r * er;                            // sigma (1 - sigma)
+  // where that is 0 the slope is sigma, whatever z dk is
+  return Act{z * s, s + (both == 0.0f ? 0.0f : z * both * dk)};
+}
+
+// What becomes of g and u.
+struct Finish {
+  int64_t rows, cols;  // T, F
+  int32_t gelu;
+  // forward
+  uint16_t* out;
+  int64_t out_ld;
+  uint16_t* gates;  // g, then u at column F; or null
+  int64_t gates_ld;
+  // backward
+  const uint16_t* dout;  // null: forward
+  int64_t dout_ld;
+  uint16_t* dgates;  // dg, then du at column `half`; rows 2 * half apart
+  int64_t half;      // F filled up to a multiple of 32
+};
+
+__device__ __forceinline__ u32x4 eight_bf16(const float* v) {
+  return u32x4{two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7])};
+}
+
+// 8 values to p, of which `left` exist.
+__device__ __forceinline__ void put_eight(uint16_t* p, u32x4 v, int64_t left) {
+  if (left >= 8) {
+    *reinterpret_cast<any_u32x4*>(p) = v;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 7; ++j)
+    if (j < left) p[j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
+}
+
+// Columns n .. n + 7 of row m, which exists.
+__device__ __forceinline__ void finish(const Finish& f, int64_t m, int64_t n, f32x4v g0, f32x4v g1, f32x4v u0,
+                                       f32x4v u1) {
+  const int64_t left = f.cols - n;
+  float a[8], b[8];
+  if (f.dout == nullptr) {
+    if (left <= 0) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = activate(j < 4 ? g0[j & 3] : g1[j & 3], f.gelu).value * (j < 4 ? u0[j & 3] : u1[j & 3]);
+    }
+    put_eight(f.out + m * f.out_ld + n, eight_bf16(a), left);
+    if (f.gates == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = j < 4 ? g0[j & 3] : g1[j & 3];
+      b[j] = j < 4 ? u0[j & 3] : u1[j & 3];
+    }
+    put_eight(f.gates + m * f.gates_ld + n, eight_bf16(a), left);
+    put_eight(f.gates + m * f.gates_ld + f.cols + n, eight_bf16(b), left);
+    return;
+  }
+  if (n >= f.half) return;
+  const u32x4 d = eight_of(f.dout + m * f.dout_ld + n, left);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float dh = (j & 1) ? high_bf16(d[j >> 1]) : low_bf16(d[j >> 1]);
+    const Act act = activate(j < 4 ? g0[j & 3] : g1[j & 3], f.gelu);
+    // columns that fill up k are 0
+    a[j] = j < left ? dh * (j < 4 ? u0[j & 3] : u1[j & 3]) * act.slope : 0.0f;
+    b[j] = j < left ? dh * act.value : 0.0f;
+  }
+  uint16_t* p = f.dgates + m * 2 * f.half + n;
+  *reinterpret_cast<u32x4*>(p) = eight_bf16(a);
+  *reinterpret_cast<u32x4*>(p + f.half) = eight_bf16(b);
+}
+
+// ------------------------------------------------------------ g and u
+
+struct GatedArgs {
+  Operand x, w;
+  int64_t depth;
+  Cut cut;
+  float* partial;
+  uint32_t tiles_m, tiles_n;
+  uint32_t* queue;  // null: every workgroup has its one item
+  Finish f;
+};
+
+template <int SIDE, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void gated_kernel(GatedArgs a) {
+  using G = Gemm<Form::kRows, Form::kPair, Code::kE4m3, SIDE, SIDE, WM, WN>;
+  __shared__ __align__(16) char lds0[G::kStage];
+  __shared__ __align__(16) char lds1[G::kStage];
+  __shared__ __align__(16) char lds2[G::kStage];
+  __shared__ __align__(16) char lds3[G::kStage];
+  __shared__ uint32_t turn;
+  Queue q;
+  uint32_t item = blockIdx.x;
+  if (a.queue) item = first_item(q, a.queue, a.cut.items, &turn);
+  if (item == kNoItem) return;
+  int64_t m0, n0, slot;
+  G g;
+  g.setup();
+  auto open = [&](uint32_t item) {
+    const Piece p = piece_of<false>(a.cut, item, a.depth);
+    uint32_t tm, tn;
+    tile_of(p.tile, a.tiles_m, a.tiles_n, 4, &tm, &tn);
+    m0 = int64_t(tm) * SIDE;
+    n0 = int64_t(tn) * (SIDE / 2);
+    slot = p.slot;
+    g.open(a.x, a.w, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
+  };
+  open(item);
+  while (item != kNoItem) {
+    g.loop(lds0, lds1, lds2, lds3);
+    const uint32_t k = a.queue ? q.ask() : 0;
+    const int64_t m1 = m0, n1 = n0, s1 = slot;
+    auto halfway = [&] {
+      item = a.queue ? next_item(q, k, &turn) : kNoItem;
+      if (item != kNoItem) open(item);
+    };
+    if (s1 >= 0) {
+      float* to = a.partial + s1 * SIDE * SIDE;
+      g.each_pair(
+          lds3,
+          [&](int r, int c, f32x4v g0, f32x4v g1, f32x4v u0, f32x4v u1) {
+            if (m1 + r >= a.f.rows) return;
+            float* p = to + r * SIDE + c;
+            *reinterpret_cast<f32x4v*>(p) = g0;
+            *reinterpret_cast<f32x4v*>(p + 4) = g1;
+            *reinterpret_cast<f32x4v*>(p + SIDE / 2) = u0;
+            *reinterpret_cast<f32x4v*>(p + SIDE / 2 + 4) = u1;
+          },
+          halfway);
+    } else {
+      g.each_pair(
+          lds3,
+          [&](int r, int c, f32x4v g0, f32x4v g1, f32x4v u0, f32x4v u1) {
+            if (m1 + r < a.f.rows) finish(a.f, m1 + r, n1 + c, g0, g1, u0, u1);
+          },
+          halfway);
+    }
+  }
+}
+
+// Joins the partial sums of g and u and finishes them, 8 columns a thread.
+template <int SIDE>
+__global__ __launch_bounds__(256) void join_gated_kernel(GatedArgs a) {
+  constexpr uint32_t kParts = SIDE * SIDE / 2 / 2048;
+  const uint32_t r = blockIdx.x / kParts, i = blockIdx.x % kParts * 256 + threadIdx.x;
+  const uint32_t row = i / (SIDE / 16), col = i % (SIDE / 16) * 8;
+  uint32_t tm, tn;
+  tile_of(a.cut.full + r, a.tiles_m, a.tiles_n, 4, &tm, &tn);
+  const int64_t m = int64_t(tm) * SIDE + row, n = int64_t(tn) * (SIDE / 2) + col;
+  if (m >= a.f.rows || n >= a.f.half) return;
+  f32x4v g0, g1, u0, u1;
+  join_eight<SIDE>(a.partial, a.cut, r, row, col, &g0, &g1);
+  join_eight<SIDE>(a.partial, a.cut, r, row, SIDE / 2 + col, &u0, &u1);
+  finish(a.f, m, n, g0, g1, u0, u1);
+}
+
+// dg and du from kept g and u.
+__global__ __launch_bounds__(256) void kept_gates_kernel(const uint16_t* gates, int64_t ld, Finish f) {
+  const int64_t groups = f.half / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t m = i / groups, n = (i - m * groups) * 8;
+  if (m >= f.rows) return;
+  const uint16_t* p = gates + m * ld + n;
+  const u32x4 g = eight_of(p, f.cols - n), u = eight_of(p + f.cols, f.cols - n);
+  finish(f, m, n, f32x4v{low_bf16(g[0]), high_bf16(g[0]), low_bf16(g[1]), high_bf16(g[1])},
+         f32x4v{low_bf16(g[2]), high_bf16(g[2]), low_bf16(g[3]), high_bf16(g[3])},
+         f32x4v{low_bf16(u[0]), high_bf16(u[0]), low_bf16(u[1]), high_bf16(u[1])},
+         f32x4v{low_bf16(u[2]), high_bf16(u[2]), low_bf16(u[3]), high_bf16(u[3])});
+}
+
+// Up to 16 tokens: a workgroup has 16 columns, and its waves split k; each reads
+// its part of the 16 rows of both weights straight into registers, and the
+// tokens' states, which every workgroup reads, from the caches.  Rows may start
+// anywhere: nothing is copied first.
+template <int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void few_gated_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* gate,
+                                                               int64_t gate_ld, const uint16_t* up, int64_t up_ld,
+                                                               int64_t depth, Finish f) {
+  constexpr int kDeep = 8;  // steps whose loads go out together
+  __shared__ f32x4v part[2][WAVES][64];
+  const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
+  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  // rows past the end read the last one: their results are dropped
+  const int64_t v = n0 + r < f.cols ? n0 + r : f.cols - 1, t = r < f.rows ? r : f.rows - 1;
+  const uint16_t* wg = gate + v * gate_ld + 8 * g;
+  const uint16_t* wu = up + v * up_ld + 8 * g;
+  const uint16_t* xt = x + t * x_ld + 8 * g;
+  typedef bf16x8 any_bf16x8 __attribute__((aligned(2)));
+  auto load = [](const uint16_t* p) -> bf16x8 { return *(const TIDE_GLOBAL any_bf16x8*)p; };
+  const int64_t whole = depth / 32, per = (whole + WAVES - 1) / WAVES;
+  int64_t s = wave * per;
+  const int64_t end = s + per < whole ? s + per : whole;
+  f32x4v ag = f32x4v{0.f, 0.f, 0.f, 0.f}, au = ag;
+  for (; s + kDeep <= end; s += kDeep) {
+    bf16x8 bg[kDeep], bu[kDeep], bx[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      bg[i] = load(wg + (s + i) * 32);
+      bu[i] = load(wu + (s + i) * 32);
+      bx[i] = load(xt + (s + i) * 32);
+    }
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bg[i], bx[i], ag, 0, 0, 0);
+      au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bu[i], bx[i], au, 0, 0, 0);
+    }
+  }
+  for (; s < end; ++s) {
+    const bf16x8 bg = load(wg + s * 32), bu = load(wu + s * 32), bx = load(xt + s * 32);
+    ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bg, bx, ag, 0, 0, 0);
+    au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bu, bx, au, 0, 0, 0);
+  }
+  if (wave == WAVES - 1 && whole * 32 < depth) {
+    const int64_t k = whole * 32, left = depth - k - 8 * g;
+    auto some = [&](const uint16_t* p) {
+      const u32x4 b = eight_of(p + k, left);
+      bf16x8 o;
+      __builtin_memcpy(&o, &b, 16);
+      return o;
+    };
+    const bf16x8 bg = some(wg), bu = some(wu), bx = some(xt);
+    ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bg, bx, ag, 0, 0, 0);
+    au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bu, bx, au, 0, 0, 0);
+  }
+  part[0][wave][lane] = ag;
+  part[1][wave][lane] = au;
+  __syncthreads();
+  // a lane holds of token r the columns n0 + 4 g + 0..3; 32 threads take 8 columns each
+  if (threadIdx.x >= 32) return;
+  const int token = threadIdx.x & 15, pair = threadIdx.x >> 4;
+  if (token >= f.rows) return;
+  f32x4v sum[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) sum[i] = add4(sum[i], part[i >> 1][k][token + 16 * (2 * pair + (i & 1))]);
+  }
+  finish(f, token, n0 + 8 * pair, sum[0], sum[1], sum[2], sum[3]);
+}
+
+// ------------------------------------------------------------ dx, dWg and dWu
+
+// One or two products of the same sizes: the second's tiles follow the first's,
+// with its own A, `shift` bytes on, and its own target.
+struct GradArgs {
+  Operand a, b;
+  int64_t depth;
+  int64_t shift;
+  Target to[2];
+  Cut cut;
+  float* partial;
+  uint32_t tiles_m, tiles_n;  // of one product
+  int32_t products;
+  uint32_t* queue;  // null: every workgroup has its one item
+};
+
+__device__ __forceinline__ uint32_t grad_tile(const GradArgs& a, uint32_t tile, uint32_t* tm, uint32_t* tn) {
+  tile_of(tile, a.tiles_m * a.products, a.tiles_n, 4, tm, tn);
+  const uint32_t second = *tm >= a.tiles_m ? 1 : 0;
+  *tm -= second * a.tiles_m;
+  return second;
+}
+
+template <Form FA, Form FB, int SIDE, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void gated_grad_kernel(GradArgs a) {
+  using G = Gemm<FA, FB, Code::kE4m3, SIDE, SIDE, WM, WN>;
+  __shared__ __align__(16) char lds0[G::kStage];
+  __shared__ __align__(16) char lds1[G::kStage];
+  __shared__ __align__(16) char lds2[G::kStage];
+  __shared__ __align__(16) char lds3[G::kStage];
+  __shared__ uint32_t turn;
+  Queue q;
+  uint32_t item = blockIdx.x;
+  if (a.queue) item = first_item(q, a.queue, a.cut.items, &turn);
+  if (item == kNoItem) return;
+  int64_t m0, n0, slot;
+  uint32_t second;
+  G g;
+  g.setup();
+  auto open = [&](uint32_t item) {
+    const Piece p = piece_of<FB == Form::kStack>(a.cut, item, a.depth);
+    uint32_t tm, tn;
+    second = grad_tile(a, p.tile, &tm, &tn);
+    m0 = int64_t(tm) * SIDE;
+    n0 = int64_t(tn) * SIDE;
+    slot = p.slot;
+    Operand left = a.a;
+    left.base = static_cast<const char*>(left.base) + second * a.shift;
+    g.open(left, a.b, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
+  };
+  open(item);
+  while (item != kNoItem) {
+    g.loop(lds0, lds1, lds2, lds3);
+    const uint32_t k = a.queue ? q.ask() : 0;
+    const Target t = slot >= 0 ? slot_target<SIDE>(a.partial, slot, a.to[0].rows - m0) : second ? a.to[1] : a.to[0];
+    const int64_t m1 = slot >= 0 ? 0 : m0, n1 = slot >= 0 ? 0 : n0;
+    g.write(t, m1, n1, lds3, [&] {
+      item = a.queue ? next_item(q, k, &turn) : kNoItem;
+      if (item != kNoItem) open(item);
+    });
+  }
+}
+
+template <int SIDE>
+__global__ __launch_bounds__(256) void join_grad_kernel(GradArgs a) {
+  constexpr uint32_t kParts = SIDE * SIDE / 2048;
+  const uint32_t r = blockIdx.x / kParts, i = blockIdx.x % kParts * 256 + threadIdx.x;
+  const uint32_t row = i / (SIDE / 8), col = i % (SIDE / 8) * 8;
+  uint32_t tm, tn;
+  const uint32_t second = grad_tile(a, a.cut.full + r, &tm, &tn);
+  const int64_t m = int64_t(tm) * SIDE + row, n = int64_t(tn) * SIDE + col;
+  if (m >= a.to[0].rows || n >= a.to[0].cols) return;
+  f32x4v lo, hi;
+  join_eight<SIDE>(a.partial, a.cut, r, row, col, &lo, &hi);
+  put_some(second ? a.to[1] : a.to[0], m, n, lo, hi);
+}
+
+__global__ __launch_bounds__(256) void clear_words_kernel(uint32_t* p, uint32_t n) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0;
+}
+
+// No tokens: the weights' gradients are 0.
+__global__ __launch_bounds__(256) void clear_gradients_kernel(uint16_t* a, uint16_t* b, int64_t n) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) a[i] = b[i] = 0;
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// A product's tiles: the side and the cut that are estimated to end first.
+struct Tiling {
+  int64_t side = 256, tiles_m = 0, tiles_n = 0;
+  Cut cut{};
+};
+Tiling tiling(int64_t m, int64_t n, int64_t products, int64_t depth, int64_t columns_of_256) {
+  const int64_t steps = (depth + kBK - 1) / kBK;
+  Tiling best;
+  double least = 0;
+  for (int64_t side : {256, 128}) {
+    Tiling t;
+    t.side = side;
+    t.tiles_m = (m + side - 1) / side;
+    const int64_t across = columns_of_256 * side / 256;
+    t.tiles_n = (n + across - 1) / across;
+    t.cut = cut_tiles(t.tiles_m * t.tiles_n * products, steps, side);
+    const double cost = cut_cost(t.cut, steps, side);
+    if (side == 256 || cost < least) {
+      best = t;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+constexpr int64_t kFew = 16;       // tokens that few_gated_kernel takes
+constexpr uint32_t kProducts = 3;  // g and u; dx; dWg and dWu
+
+// Where one call's workspace keeps what.
+struct Layout {
+  bool few = false, copy_x = false, copy_w = false, gates = false;  // gates: g and u are formed
+  int64_t ld = 0, half = 0;
+  Tiling fwd, dx, dw;
+  bool queued = false;
+  // byte offsets
+  int64_t queues = 0, x = 0, w = 0, dgates = 0, partial = 0, bytes = 0;
+};
+
+Layout layout_of(const GatedCall& c) {
+  Layout L;
+  L.gates = !c.grad || c.gates == nullptr;
+  L.few = c.tokens <= kFew;
+  L.half = up(c.ffn, 32);
+  L.ld = up(c.hidden, 64);
+  // Tiles read rows that start and end on 16 bytes; dx reads the weights one behind the other.
+  const bool tiles = c.grad || !L.few;
+  const bool w_aligned = rows_aligned(c.w_gate, c.gate_ld, c.hidden) && rows_aligned(c.w_up, c.up_ld, c.hidden) &&
+                         c.gate_ld == c.up_ld;
+  L.copy_x = tiles && !rows_aligned(c.x, c.x_ld, c.hidden);
+  L.copy_w = tiles && (!w_aligned || (c.grad && c.ffn % kBK != 0));
+  int64_t at = 0, partial = 0;
+  auto take = [&](int64_t n) {
+    const int64_t here = at;
+    at += up(n, 256);
+    return here;
+  };
+  auto also = [&](const Tiling& t) {
+    const int64_t n = partial_bytes(t.cut, t.side);
+    partial = n > partial ? n : partial;
+    L.queued |= t.cut.items > tile_slots(t.side);
+  };
+  if (L.gates && !L.few) {
+    L.fwd = tiling(c.tokens, c.ffn, 1, c.hidden, 128);
+    also(L.fwd);
+  }
+  if (c.grad) {
+    L.dx = tiling(c.tokens, c.hidden, 1, 2 * L.half, 256);
+    L.dw = tiling(c.ffn, c.hidden, 2, c.tokens, 256);
+    also(L.dx);
+    also(L.dw);
+  }
+  if (L.queued) L.queues = take(kProducts * kQueueWords * kQueuePitch * 4);
+  if (L.copy_x) L.x = take(c.tokens * L.ld * 2);
+  if (L.copy_w) L.w = take(2 * L.half * L.ld * 2);
+  if (c.grad) L.dgates = take(c.tokens * 2 * L.half * 2);
+  if (partial > 0) L.partial = take(partial);
+  L.bytes = at;
+  return L;
+}
+
+#define TIDE_LAUNCHED()                       \
+  do {                                        \
+    const int rc_ = int(hipGetLastError());   \
+    if (rc_ != 0) return rc_;                 \
+  } while (0)
+
+template <Form FA, Form FB>
+int launch_grad(GradArgs a, const Tiling& t, float* partial, uint32_t* queue, hipStream_t st) {
+  a.cut = t.cut;
+  a.partial = partial;
+  a.tiles_m = uint32_t(t.tiles_m);
+  a.tiles_n = uint32_t(t.tiles_n);
+  a.queue = t.cut.items > tile_slots(t.side) ? queue : nullptr;
+  const dim3 grid(resident_groups(t.cut.items, t.side));
+  if (t.side == 256)
+    hipLaunchKernelGGL((gated_grad_kernel<FA, FB, 256, 2, 4>), grid, dim3(512), 0, st, a);
+  else
+    hipLaunchKernelGGL((gated_grad_kernel<FA, FB, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  TIDE_LAUNCHED();
+  if (t.cut.splits == 1) return 0;
+  const unsigned rest = t.cut.tiles - t.cut.full;
+  if (t.side == 256)
+    hipLaunchKernelGGL(join_grad_kernel<256>, dim3(rest * 32), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(join_grad_kernel<128>, dim3(rest * 8), dim3(256), 0, st, a);
+  return int(hipGetLastError());
+}
+
+}  // namespace
+
+namespace tide {
+
+int64_t gated_block_bytes(const GatedCall& c) { return c.tokens > 0 && c.ffn > 0 ? layout_of(c).bytes : 0; }
+
+int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  if (c.tokens == 0) {
+    if (!c.grad || c.accumulate || c.ffn == 0) return 0;
+    hipLaunchKernelGGL(clear_gradients_kernel, dim3(2048), dim3(256), 0, st, static_cast<uint16_t*>(c.dw_gate),
+                       static_cast<uint16_t*>(c.dw_up), c.ffn * c.hidden * (c.dw_f32 ? 2 : 1));
+    return int(hipGetLastError());
+  }
+  const Layout L = layout_of(c);
+  uint32_t* queues = reinterpret_cast<uint32_t*>(ws + L.queues);
+  float* partial = reinterpret_cast<float*>(ws + L.partial);
+  if (L.queued) {
+    constexpr uint32_t kWords = kProducts * kQueueWords * kQueuePitch;
+    hipLaunchKernelGGL(clear_words_kernel, dim3((kWords + 255) / 256), dim3(256), 0, st, queues, kWords);
+    TIDE_LAUNCHED();
+  }
+  Operand x{c.x, nullptr, c.x_ld, 0, c.tokens}, w{c.w_gate, nullptr, c.gate_ld, 0, c.ffn};
+  w.second = c.w_up;
+  if (L.copy_x) {
+    const int rc = launch_align_rows(c.x, c.x_ld, c.tokens, c.hidden, ws + L.x, L.ld, stream);
+    if (rc != 0) return rc;
+    x.base = ws + L.x;
+    x.ld = L.ld;
+  }
+  if (L.copy_w) {
+    char* to = ws + L.w;
+    char* up_to = to + L.half * L.ld * 2;
+    int rc = launch_align_rows(c.w_gate, c.gate_ld, c.ffn, c.hidden, to, L.ld, stream, L.half);
+    if (rc == 0) rc = launch_align_rows(c.w_up, c.up_ld, c.ffn, c.hidden, up_to, L.ld, stream, L.half);
+    if (rc != 0) return rc;
+    w.base = to;
+    w.second = up_to;
+    w.ld = L.ld;
+  }
+  Finish f{};
+  f.rows = c.tokens;
+  f.cols = c.ffn;
+  f.gelu = c.gelu;
+  f.half = L.half;
+  if (c.grad) {
+    f.dout = static_cast<const uint16_t*>(c.dout);
+    f.dout_ld = c.dout_ld;
+    f.dgates = reinterpret_cast<uint16_t*>(ws + L.dgates);
+  } else {
+    f.out = static_cast<uint16_t*>(c.out);
+    f.out_ld = c.out_ld;
+    f.gates = static_cast<uint16_t*>(c.gates);
+    f.gates_ld = c.gates_ld;
+  }
+  if (!L.gates) {
+    const int64_t n = c.tokens * (L.half / 8);
+    hipLaunchKernelGGL(kept_gates_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st,
+                       static_cast<const uint16_t*>(c.gates), c.gates_ld, f);
+    TIDE_LAUNCHED();
+  } else if (L.few) {
+    // the caller's own rows: they may start anywhere
+    const unsigned grid = unsigned((c.grad ? L.half : c.ffn) + 15) / 16;
+    const uint16_t *xp = static_cast<const uint16_t*>(c.x), *gate = static_cast<const uint16_t*>(c.w_gate),
+                   *up_w = static_cast<const uint16_t*>(c.w_up);
+    if (grid >= 512)
+      hipLaunchKernelGGL(few_gated_kernel<4>, dim3(grid), dim3(256), 0, st, xp, c.x_ld, gate, c.gate_ld, up_w, c.up_ld,
+                         c.hidden, f);
+    else
+      hipLaunchKernelGGL(few_gated_kernel<16>, dim3(grid), dim3(1024), 0, st, xp, c.x_ld, gate, c.gate_ld, up_w, c.up_ld,
+                         c.hidden, f);
+    TIDE_LAUNCHED();
+  } else {
+    GatedArgs a;
+    a.x = x;
+    a.w = w;
+    a.depth = c.hidden;
+    a.cut = L.fwd.cut;
+    a.partial = partial;
+    a.tiles_m = uint32_t(L.fwd.tiles_m);
+    a.tiles_n = uint32_t(L.fwd.tiles_n);
+    a.queue = a.cut.items > tile_slots(L.fwd.side) ? queues : nullptr;
+    a.f = f;
+    const dim3 grid(resident_groups(a.cut.items, L.fwd.side));
+    const unsigned rest = a.cut.tiles - a.cut.full;
+    if (L.fwd.side == 256) {
+      hipLaunchKernelGGL((gated_kernel<256, 2, 4>), grid, dim3(512), 0, st, a);
+      TIDE_LAUNCHED();
+      if (a.cut.splits > 1) hipLaunchKernelGGL(join_gated_kernel<256>, dim3(rest * 16), dim3(256), 0, st, a);
+    } else {
+      hipLaunchKernelGGL((gated_kernel<128, 2, 2>), grid, dim3(256), 0, st, a);
+      TIDE_LAUNCHED();
+      if (a.cut.splits > 1) hipLaunchKernelGGL(join_gated_kernel<128>, dim3(rest * 4), dim3(256), 0, st, a);
+    }
+    TIDE_LAUNCHED();
+  }
+  if (!c.grad) return 0;
+
+  GradArgs d{};
+  d.a = Operand{f.dgates, nullptr, 2 * L.half, 0, c.tokens};
+  d.b = w;
+  d.b.extent = c.hidden;
+  d.b.split = L.half / kBK;
+  d.depth = 2 * L.half;
+  d.products = 1;
+  d.to[0] = d.to[1] = Target{c.dx, c.dx_ld, c.tokens, c.hidden, nullptr, nullptr, 1.0f, 0, 0};
+  int rc = launch_grad<Form::kRows, Form::kStack>(d, L.dx, partial, queues + kQueueWords * kQueuePitch, st);
+  if (rc != 0) return rc;
+  GradArgs v{};
+  v.a = Operand{f.dgates, nullptr, 2 * L.half, 0, c.ffn};
+  v.b = x;
+  v.b.extent = c.hidden;
+  v.depth = c.tokens;
+  v.shift = L.half * 2;
+  v.products = 2;
+  v.to[0] = Target{c.dw_gate, c.hidden, c.ffn, c.hidden, nullptr, nullptr, 1.0f, c.dw_f32, c.accumulate};
+  v.to[1] = v.to[0];
+  v.to[1].base = c.dw_up;
+  return launch_grad<Form::kCols, Form::kCols>(v, L.dw, partial, queues + 2 * kQueueWords * kQueuePitch, st);
+}
+
+}  // namespace tide

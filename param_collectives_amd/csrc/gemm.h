@@ -3,22 +3,27 @@
 //   C[m][n] = sum_k A(m, k) B(k, n)
 // with bf16 operands and fp32 sums on the matrix cores (16x16x32 products).
 //
-// An operand is read in one of three forms:
+// An operand is read in one of five forms:
 //   Form::kRows    its rows are C's rows (columns), k runs along them;
+//   Form::kPair    as kRows, from two matrices: a tile's first half of rows are
+//                  the one's, the second half the same rows of the other, and a
+//                  wave holds the products of both for its share of them;
 //   Form::kCols    its rows are the values of k, C's rows (columns) run along
 //                  them;
+//   Form::kStack   as kCols, from two matrices: the values of k go on in the
+//                  second after `split` steps;
 //   Form::kPacked  as kCols, in the packed 8-bit form (codes and one exponent
 //                  byte per block of 32), widened while it is staged.
-// Tiles go to LDS, kRows and kCols ones by loads that write LDS directly (16
+// Tiles go to LDS, all but kPacked ones by loads that write LDS directly (16
 // bytes a lane).  Those loads fill LDS in lane order, so the bank swizzle is
 // made by choosing which 16 bytes a lane fetches:
-//   kRows tile [rows][32 k], 4 chunks of 16 bytes a row: chunk c of row r is
+//   kRows, kPair tile [rows][32 k], 4 chunks of 16 bytes a row: chunk c of row r is
 //     kept at c ^ f(r), f(r) = -(r / 4) mod 4.  A 16-byte fragment read goes
 //     through the 64 banks 16 lanes at a time, not neighbours but lanes 0-3,
 //     12-15 and 20-27, then the rest of 0-31, and so on: f gives each such
 //     group 16 different places (r / 4 mod 4 does not: measured, bank conflicts
 //     in 21% of a kernel's cycles);
-//   kCols, kPacked tile [32 k][rows]: chunk c of row k is kept at
+//   kCols, kStack, kPacked tile [32 k][rows]: chunk c of row k is kept at
 //     c ^ 2 f(k), f(k) made of bits 0, 1 and 3 of k; a fragment is read by the
 //     transposing LDS read, whose 32 lanes touch 8 rows k of 32 bytes each.
 // The products take the n side first, so a lane holds 4 consecutive n of one m.
@@ -47,7 +52,7 @@ typedef f32x4v any_f32x4 __attribute__((aligned(4)));
 #define TIDE_GLOBAL __attribute__((address_space(1)))
 #define TIDE_LDS __attribute__((address_space(3)))
 
-enum class Form { kRows, kCols, kPacked };
+enum class Form { kRows, kPair, kCols, kStack, kPacked };
 enum class Code { kE4m3, kInt8 };
 
 constexpr int kStages = 4;  // LDS stages a tile's steps go round
@@ -58,6 +63,8 @@ struct Operand {
   int64_t ld;             // elements from row to row, a multiple of 8 (kPacked: of 32)
   int64_t scale_ld;
   int64_t extent;         // rows (columns) of C that exist on this side
+  const void* second = nullptr;  // kPair, kStack: the other matrix, of the same layout
+  int64_t split = 0;             // kStack: steps of k in the first
 };
 
 // 8 zero values for the lanes whose k lies past the end.
@@ -164,13 +171,16 @@ __device__ __forceinline__ u32x2 widen4(uint32_t w, uint32_t scale_byte) {
 // read, from one register (see Gemm).
 template <Form FORM, Code CODE, int ROWS, int FRAGS, int THREADS, bool LEAN>
 struct Side {
-  static constexpr bool kPacked = FORM == Form::kPacked;
+  static constexpr bool kPacked = FORM == Form::kPacked, kPair = FORM == Form::kPair, kStack = FORM == Form::kStack;
+  static constexpr bool kAlong = FORM == Form::kRows || kPair;  // k runs along the rows
   static constexpr int kBytes = ROWS * kBK * 2;
-  static constexpr int kRowChunks = FORM == Form::kRows ? kBK / 8 : ROWS / 8;
+  static constexpr int kRowChunks = kAlong ? kBK / 8 : ROWS / 8;
   // What a thread moves per step: 16-byte loads to LDS, or units of 16 codes.
   static constexpr int kParts = kPacked ? kBK * (ROWS / 16) / THREADS : kBytes / 16 / THREADS;
   static constexpr int kLoads = kPacked ? 2 * kParts : kParts;  // a unit's codes and its exponent byte
   static_assert(kParts >= 1, "tile too small for its threads");
+  // kPair: the parts of the first matrix are half of them
+  static_assert(!kPair || (kParts % 2 == 0 && FRAGS % 2 == 0), "halves of a tile");
 
   const char* base;        // of the tile's first row (kRows) or column, k = 0
   const uint8_t* scales;
@@ -179,6 +189,8 @@ struct Side {
   uint32_t off[kParts];    // byte offset of each part at its step's base
   uint32_t scale_off[kPacked ? kParts : 1];
   uint32_t put[kPacked ? kParts : 1];  // where each unit goes in the tile
+  const char* second;  // kPair, kStack: `base` of the other matrix
+  int64_t split;       // kStack
 
   // kPacked: codes on their way to LDS
   struct Held {
@@ -187,23 +199,28 @@ struct Side {
   };
 
   static __device__ __forceinline__ int part_k(int lin) {
-    return FORM == Form::kRows ? ((lin & 3) ^ row_swizzle(lin >> 2)) * 8 : lin / (kPacked ? ROWS / 16 : kRowChunks);
+    return kAlong ? ((lin & 3) ^ row_swizzle(lin >> 2)) * 8 : lin / (kPacked ? ROWS / 16 : kRowChunks);
   }
 
   __device__ __forceinline__ void init(const Operand& o, int64_t first, int tid) {
     // rows (columns) past the end read the last one: their results are dropped
     const int64_t last = o.extent - 1 - first;
-    if constexpr (FORM == Form::kRows) {
+    if constexpr (kAlong) {
       base = static_cast<const char*>(o.base) + first * o.ld * 2;
+      if constexpr (kPair) second = static_cast<const char*>(o.second) + first * o.ld * 2;
       step = kBK * 2;
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
-        const int lin = i * THREADS + tid, r = lin >> 2;
+        const int lin = i * THREADS + tid, r = (lin >> 2) % (kPair ? ROWS / 2 : ROWS);
         const int rr = r <= last ? r : int(last);
         off[i] = uint32_t(rr) * uint32_t(o.ld * 2) + uint32_t(part_k(lin) * 2);
       }
-    } else if constexpr (FORM == Form::kCols) {
+    } else if constexpr (!kPacked) {
       base = static_cast<const char*>(o.base) + first * 2;
+      if constexpr (kStack) {
+        second = static_cast<const char*>(o.second) + first * 2;
+        split = o.split;
+      }
       step = o.ld * (kBK * 2);
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
@@ -226,14 +243,21 @@ struct Side {
     }
   }
 
+  // Where part i of step s starts.
+  __device__ __forceinline__ const char* at_step(int64_t s, int i) const {
+    if constexpr (kPair) return uniform((i < kParts / 2 ? base : second) + s * step);
+    if constexpr (kStack) return uniform(s < split ? base + s * step : second + (s - split) * step);
+    return uniform(base + s * step);
+  }
+
   // Start the loads of step s into `lds` (kPacked: into `held`).  TAIL: only
   // `left` < 32 values of k remain (none, for an empty step), the rest is
-  // staged as zeros (k counts in eights on a kRows side, whose rows are zero
-  // from there to the next multiple of 8).
+  // staged as zeros (k counts in eights where it runs along the rows, which are
+  // zero from there to the next multiple of 8).
   template <bool TAIL>
   __device__ __forceinline__ void fetch(char* lds, Held& held, int64_t s, int left, int tid) {
-    const char* at = uniform(base + s * step);
     if constexpr (kPacked) {
+      const char* at = at_step(s, 0);
       const uint8_t* sc = uniform(scales + s * scale_step);
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
@@ -249,6 +273,7 @@ struct Side {
       const int wave_base = wave_index() * 64;
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
+        const char* at = at_step(s, i);
         char* to = lds + (i * THREADS + wave_base) * 16;
         if constexpr (TAIL)
           load_to_lds(part_k(i * THREADS + tid) < left ? at + off[i] : reinterpret_cast<const char*>(g_zero16), to);
@@ -260,7 +285,7 @@ struct Side {
 
   // Part i of a whole step's loads to LDS.
   __device__ __forceinline__ void fetch_part(char* lds, int64_t s, int i) {
-    load_to_lds(uniform(base + s * step), off[i], lds + (i * THREADS + wave_index() * 64) * 16);
+    load_to_lds(at_step(s, i), off[i], lds + (i * THREADS + wave_index() * 64) * 16);
   }
 
   // kPacked: widen what fetch() loaded, halves [h0, h1) of each unit, and write
@@ -282,10 +307,10 @@ struct Side {
 
   // Where this lane's fragments of a wave's FRAGS x 16 rows (columns) from r0
   // (a multiple of 16 FRAGS) start in the tile.
-  static constexpr int kSpots = FORM == Form::kRows || LEAN ? 1 : FRAGS;
+  static constexpr int kSpots = kAlong || LEAN ? 1 : FRAGS;
   static __device__ __forceinline__ void spots(uint32_t* at, int r0, int lane) {
-    if constexpr (FORM == Form::kRows) {
-      const int r = r0 + (lane & 15);
+    if constexpr (kAlong) {
+      const int r = (kPair ? r0 / 2 : r0) + (lane & 15);
       at[0] = uint32_t((r * kRowChunks + ((lane >> 4) ^ row_swizzle(r))) * 16);
     } else {
       // a transposing read gives lane l of 16 the values of column l in the
@@ -299,10 +324,12 @@ struct Side {
   // 16 i columns on are 2 i chunks, bits that are 0 before the swizzle.
   static __device__ __forceinline__ uint32_t spot(uint32_t first, int i) { return first ^ uint32_t(i * 32); }
 
-  // Fragment i: rows (columns) 16 i + 0..15, k = 8 (lane / 16) + 0..7.
+  // Fragment i: rows (columns) 16 i + 0..15, k = 8 (lane / 16) + 0..7.  (kPair: the
+  // second half of the fragments are the second matrix's.)
   static __device__ __forceinline__ bf16x8 fragment(const char* lds, uint32_t* at, int i) {
-    if constexpr (FORM == Form::kRows) {
-      return *reinterpret_cast<const bf16x8*>(lds + renew(at[0]) + i * 16 * kRowChunks * 16);
+    if constexpr (kAlong) {
+      const int r = kPair && i >= FRAGS / 2 ? ROWS / 2 + (i - FRAGS / 2) * 16 : i * 16;
+      return *reinterpret_cast<const bf16x8*>(lds + renew(at[0]) + r * kRowChunks * 16);
     } else {
       // rows k and k + 4 share their swizzle
       const char* p = lds + (LEAN ? spot(renew(at[0]), i) : renew(at[i]));
@@ -684,6 +711,32 @@ struct Gemm {
     }
   }
 
+  // The same where B is a pair: f(row, column, 8 values of the first matrix, and
+  // those of the second), columns counted in the half tile.
+  template <typename F, typename H>
+  __device__ __forceinline__ void each_pair(char* lds, F f, H halfway) {
+    constexpr int kCols = BN / WN, kQuads = kCols / 4, kMask = kQuads - 1, kGroups = kCols / 16;
+    static_assert(FB == Form::kPair && 16 * kGroups % 64 == 0 && WM * WN * 16 * kCols * 4 <= kStage, "epilogue rows");
+    float* rows = reinterpret_cast<float*>(lds) + wave_index() * 16 * kCols;
+#pragma unroll
+    for (int i = 0; i < kFM; ++i) {
+      const int w = lane & 15;
+#pragma unroll
+      for (int j = 0; j < kFN; ++j)
+        *reinterpret_cast<f32x4v*>(rows + w * kCols + ((4 * j + (lane >> 4)) ^ (w & kMask)) * 4) = acc[i][j];
+      wave_order();
+#pragma unroll
+      for (int q = lane; q < 16 * kGroups; q += 64) {
+        const int r = q / kGroups, c = q % kGroups;
+        auto quad = [&](int k) { return *reinterpret_cast<const f32x4v*>(rows + r * kCols + (k ^ (r & kMask)) * 4); };
+        f(wm * (BM / WM) + i * 16 + r, wn * (kCols / 2) + c * 8, quad(2 * c), quad(2 * c + 1), quad(kQuads / 2 + 2 * c),
+          quad(kQuads / 2 + 2 * c + 1));
+      }
+      wave_order();
+      if (i == kFM / 2 - 1) halfway();
+    }
+  }
+
   // Writes the tile at (m0, n0) to `t`.
   template <typename H>
   __device__ __forceinline__ void write(const Target& t, int64_t m0, int64_t n0, char* lds, H halfway) {
@@ -744,6 +797,31 @@ struct Queue {
   }
 };
 
+// A workgroup's first item of a queue.
+__device__ __forceinline__ uint32_t first_item(Queue& q, uint32_t* words, uint32_t items, uint32_t* turn) {
+  q.setup(words, items);
+  if (wave_index() == 0) {
+    const uint32_t got = q.settle(q.ask());
+    if (threadIdx.x == 0) *turn = got;
+  }
+  __syncthreads();
+  const uint32_t item = __builtin_amdgcn_readfirstlane(*turn);
+  __syncthreads();
+  return item;
+}
+
+// The workgroup's next item, which was asked for as k (at the end of a tile's
+// sums: earlier, a workgroup would take what one that is still to start should
+// have).
+__device__ __forceinline__ uint32_t next_item(Queue& q, uint32_t k, uint32_t* turn) {
+  if (wave_index() == 0) {
+    const uint32_t got = q.settle(k);
+    if (threadIdx.x == 0) *turn = got;
+  }
+  lds_barrier();
+  return __builtin_amdgcn_readfirstlane(*turn);
+}
+
 // Item 8 k + x of `total` -> the k-th of XCD x's share, the shares contiguous.
 __device__ __forceinline__ uint32_t nth_of_share(uint32_t item, uint32_t total) {
   const uint32_t x = item & 7, each = total >> 3, more = total & 7;
@@ -796,23 +874,34 @@ __device__ __forceinline__ Target slot_target(float* partial, int64_t slot, int6
   return Target{partial + slot * SIDE * SIDE, SIDE, rows < SIDE ? rows : SIDE, SIDE, nullptr, nullptr, 1.0f, 1, 0};
 }
 
+// The partial sums of 8 columns from `col` of row `row` of tile full + r (of a cut
+// with splits), added in order of the splits.
+template <int SIDE>
+__device__ __forceinline__ void join_eight(const float* partial, const Cut& c, uint32_t r, uint32_t row, uint32_t col,
+                                           f32x4v* lo, f32x4v* hi) {
+  const float* p = partial + int64_t(r) * SIDE * SIDE + row * SIDE + col;
+  f32x4v l = f32x4v{0.f, 0.f, 0.f, 0.f}, h = l;
+#pragma unroll 4
+  for (uint32_t k = 0; k < c.splits; ++k, p += int64_t(c.tiles - c.full) * SIDE * SIDE) {
+    l = add4(l, *reinterpret_cast<const f32x4v*>(p));
+    h = add4(h, *reinterpret_cast<const f32x4v*>(p + 4));
+  }
+  *lo = l;
+  *hi = h;
+}
+
 // Joins the partial sums of tile full + r (of a cut with splits), in order of
 // the splits, into `t`: `part` of the SIDE * SIDE / 2048 parts of a tile.
 template <int SIDE>
 __device__ __forceinline__ void join_tile(const float* partial, const Cut& c, uint32_t tiles_m, uint32_t tiles_n,
                                           uint32_t r, uint32_t part, const Target& t) {
-  const uint32_t rest = c.tiles - c.full, g = part * 256 + threadIdx.x, row = g / (SIDE / 8), col = g % (SIDE / 8) * 8;
+  const uint32_t g = part * 256 + threadIdx.x, row = g / (SIDE / 8), col = g % (SIDE / 8) * 8;
   uint32_t tm, tn;
   tile_of(c.full + r, tiles_m, tiles_n, 4, &tm, &tn);
   const int64_t m = int64_t(tm) * SIDE + row, n = int64_t(tn) * SIDE + col;
   if (m >= t.rows || n >= t.cols) return;
-  const float* p = partial + int64_t(r) * SIDE * SIDE + row * SIDE + col;
-  f32x4v lo = f32x4v{0.f, 0.f, 0.f, 0.f}, hi = lo;
-#pragma unroll 4
-  for (uint32_t k = 0; k < c.splits; ++k, p += int64_t(rest) * SIDE * SIDE) {
-    lo = add4(lo, *reinterpret_cast<const f32x4v*>(p));
-    hi = add4(hi, *reinterpret_cast<const f32x4v*>(p + 4));
-  }
+  f32x4v lo, hi;
+  join_eight<SIDE>(partial, c, r, row, col, &lo, &hi);
   put_some(t, m, n, lo, hi);
 }
 

@@ -163,6 +163,41 @@ tide_status layer_norm_call(const void* x, int32_t x_dtype, int64_t x_stride, co
   return TIDE_OK;
 }
 
+// Checks shared by the gated block, its gradients and its workspace; *call is
+// filled in.
+tide_status gated_call(const uint16_t* x, int64_t x_stride, const uint16_t* w_gate, int64_t gate_stride,
+                       const uint16_t* w_up, int64_t up_stride, int64_t tokens, int64_t hidden_size, int64_t ffn_size,
+                       int32_t activation, const uint16_t* gates, int64_t gates_stride, tide::GatedCall* call) {
+  if (activation != TIDE_ACT_SILU && activation != TIDE_ACT_GELU)
+    return invalid("activation must be TIDE_ACT_SILU or TIDE_ACT_GELU");
+  TIDE_TRY(check_matrix("x", tokens, hidden_size, x_stride));
+  TIDE_TRY(check_matrix("w_gate", ffn_size, hidden_size, gate_stride));
+  TIDE_TRY(check_matrix("w_up", ffn_size, hidden_size, up_stride));
+  if (hidden_size < 1 || ffn_size < 1) return invalid("the hidden sizes must be at least 1");
+  if (ffn_size > kMaxFeatures / 2) return tide::set_error(TIDE_ERR_RANGE, "an inner size above 2^21");
+  TIDE_TRY(check_matrix("gates", tokens, 2 * ffn_size, gates ? gates_stride : 2 * ffn_size));
+  if (tokens > 0) {
+    TIDE_TRY(check_pointer("x", x, 2));
+    TIDE_TRY(check_pointer("w_gate", w_gate, 2));
+    TIDE_TRY(check_pointer("w_up", w_up, 2));
+    if (gates) TIDE_TRY(check_pointer("gates", gates, 2));
+  }
+  *call = tide::GatedCall{};
+  call->x = x;
+  call->x_ld = x_stride;
+  call->w_gate = w_gate;
+  call->gate_ld = gate_stride;
+  call->w_up = w_up;
+  call->up_ld = up_stride;
+  call->tokens = tokens;
+  call->hidden = hidden_size;
+  call->ffn = ffn_size;
+  call->gelu = activation == TIDE_ACT_GELU;
+  call->gates = const_cast<uint16_t*>(gates);
+  call->gates_ld = gates_stride;
+  return TIDE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -383,6 +418,76 @@ tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t d
     c.dx = dx;
     c.dx_ld = dx_stride;
     return hip_status(tide::launch_layer_norm(c, workspace, stream), "layer norm gradient launch");
+  });
+}
+
+tide_status tide_gated_block_workspace(const uint16_t* x, int64_t x_stride, const uint16_t* w_gate, int64_t gate_stride,
+                                       const uint16_t* w_up, int64_t up_stride, int64_t tokens, int64_t hidden_size,
+                                       int64_t ffn_size, int32_t gradients, const uint16_t* gates, int64_t* bytes) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    if (bytes == nullptr) return invalid("bytes must not be NULL");
+    if (gradients != 0 && gradients != 1) return invalid("gradients must be 0 or 1");
+    tide::GatedCall c;
+    TIDE_TRY(gated_call(x, x_stride, w_gate, gate_stride, w_up, up_stride, tokens, hidden_size, ffn_size, TIDE_ACT_SILU,
+                        gates, 2 * ffn_size, &c));
+    c.grad = gradients == 1;
+    *bytes = tide::gated_block_bytes(c);
+    return TIDE_OK;
+  });
+}
+
+tide_status tide_gated_block(const uint16_t* x, int64_t x_stride, const uint16_t* w_gate, int64_t gate_stride,
+                             const uint16_t* w_up, int64_t up_stride, int64_t tokens, int64_t hidden_size,
+                             int64_t ffn_size, int32_t activation, uint16_t* out, int64_t out_stride, uint16_t* gates,
+                             int64_t gates_stride, void* workspace, int64_t workspace_bytes, void* stream) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    tide::GatedCall c;
+    TIDE_TRY(gated_call(x, x_stride, w_gate, gate_stride, w_up, up_stride, tokens, hidden_size, ffn_size, activation,
+                        gates, gates_stride, &c));
+    TIDE_TRY(check_matrix("out", tokens, ffn_size, out_stride));
+    if (tokens == 0) return TIDE_OK;
+    TIDE_TRY(check_pointer("out", out, 2));
+    TIDE_TRY(check_workspace(workspace, workspace_bytes, tide::gated_block_bytes(c)));
+    c.out = out;
+    c.out_ld = out_stride;
+    return hip_status(tide::launch_gated_block(c, workspace, stream), "gated block launch");
+  });
+}
+
+tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, const uint16_t* x, int64_t x_stride,
+                                  const uint16_t* w_gate, int64_t gate_stride, const uint16_t* w_up, int64_t up_stride,
+                                  int64_t tokens, int64_t hidden_size, int64_t ffn_size, int32_t activation,
+                                  const uint16_t* gates, int64_t gates_stride, uint16_t* dx, int64_t dx_stride,
+                                  void* dw_gate, void* dw_up, int32_t dw_dtype, int32_t accumulate, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    TIDE_TRY(check_dtype("dw_dtype", dw_dtype));
+    if (accumulate != 0 && accumulate != 1) return invalid("accumulate must be 0 or 1");
+    tide::GatedCall c;
+    TIDE_TRY(gated_call(x, x_stride, w_gate, gate_stride, w_up, up_stride, tokens, hidden_size, ffn_size, activation,
+                        gates, gates_stride, &c));
+    TIDE_TRY(check_matrix("dout", tokens, ffn_size, dout_stride));
+    TIDE_TRY(check_matrix("dx", tokens, hidden_size, dx_stride));
+    TIDE_TRY(check_pointer("dw_gate", dw_gate, size_of(dw_dtype)));
+    TIDE_TRY(check_pointer("dw_up", dw_up, size_of(dw_dtype)));
+    c.grad = true;
+    if (tokens > 0) {
+      TIDE_TRY(check_pointer("dout", dout, 2));
+      TIDE_TRY(check_pointer("dx", dx, 2));
+      TIDE_TRY(check_workspace(workspace, workspace_bytes, tide::gated_block_bytes(c)));
+    }
+    c.dout = dout;
+    c.dout_ld = dout_stride;
+    c.dx = dx;
+    c.dx_ld = dx_stride;
+    c.dw_gate = dw_gate;
+    c.dw_up = dw_up;
+    c.dw_f32 = dw_dtype == TIDE_DTYPE_F32;
+    c.accumulate = accumulate;
+    return hip_status(tide::launch_gated_block(c, workspace, stream), "gated block gradient launch");
   });
 }
 

@@ -148,6 +148,30 @@ struct LayerNormCall {
   int32_t accumulate;
 };
 
+struct GatedCall {
+  const void* x;  // tokens x hidden bf16, rows x_ld apart
+  int64_t x_ld;
+  const void* w_gate;  // ffn x hidden bf16 each
+  int64_t gate_ld;
+  const void* w_up;
+  int64_t up_ld;
+  int64_t tokens, hidden, ffn;
+  int32_t gelu;
+  void* gates;  // tokens x 2 ffn bf16; written by the forward pass, read for the gradients; or null
+  int64_t gates_ld;
+  void* out;
+  int64_t out_ld;
+  // the gradients
+  bool grad;
+  const void* dout;
+  int64_t dout_ld;
+  void* dx;
+  int64_t dx_ld;
+  void* dw_gate;
+  void* dw_up;
+  int32_t dw_f32, accumulate;
+};
+
 // Whether rows of `cols` bf16 elements, `ld` apart from p, all start and end on
 // 16 bytes: the tiles then read them in place, 16 bytes at a time and never
 // past a row's end.
@@ -169,6 +193,8 @@ int launch_vocab_loss(const VocabLossCall& c, void* workspace, void* stream);
 int64_t layer_norm_grad_bytes(const LayerNormCall& c);
 int launch_layer_norm(const LayerNormCall& c, void* workspace, void* stream);
 int launch_align_rows(const void* src, int64_t src_ld, int64_t rows, int64_t cols, void* dst, int64_t ld,
-                      void* stream);
+                      void* stream, int64_t out_rows = 0);
+int64_t gated_block_bytes(const GatedCall& c);  // its workspace
+int launch_gated_block(const GatedCall& c, void* workspace, void* stream);
 
 }  // namespace tide

@@ -86,31 +86,6 @@ __device__ __forceinline__ int64_t rows_of(const int32_t* count, int64_t first, 
   return n > 0 ? n : 0;
 }
 
-// A workgroup's first item of a queue.
-__device__ __forceinline__ uint32_t first_item(Queue& q, uint32_t* words, uint32_t items, uint32_t* turn) {
-  q.setup(words, items);
-  if (wave_index() == 0) {
-    const uint32_t got = q.settle(q.ask());
-    if (threadIdx.x == 0) *turn = got;
-  }
-  __syncthreads();
-  const uint32_t item = __builtin_amdgcn_readfirstlane(*turn);
-  __syncthreads();
-  return item;
-}
-
-// The workgroup's next item, which was asked for as k (at the end of a tile's
-// sums: earlier, a workgroup would take what one that is still to start should
-// have).
-__device__ __forceinline__ uint32_t next_item(Queue& q, uint32_t k, uint32_t* turn) {
-  if (wave_index() == 0) {
-    const uint32_t got = q.settle(k);
-    if (threadIdx.x == 0) *turn = got;
-  }
-  lds_barrier();
-  return __builtin_amdgcn_readfirstlane(*turn);
-}
-
 // ------------------------------------------------------------ the token list
 
 // Lists the tokens that count, in order, and clears the loss and lse of the

@@ -39,6 +39,7 @@ DTYPE_BF16 = 0
 DTYPE_F32 = 1
 CODE_E4M3 = 0
 CODE_INT8 = 1
+ACTIVATIONS = {"silu": 0, "gelu": 1}
 MAX_WORLD = 256
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -69,6 +70,9 @@ EXPORTS = (
     "tide_layer_norm",
     "tide_layer_norm_grad_workspace",
     "tide_layer_norm_grad",
+    "tide_gated_block_workspace",
+    "tide_gated_block",
+    "tide_gated_block_grad",
     "tide_device_info",
     "tide_probe_launch",
     "tide_victim_axpb",
@@ -124,6 +128,10 @@ def _load():
     lib.tide_layer_norm_grad_workspace.argtypes = [i32, i32, i64, i64, i64p]
     lib.tide_layer_norm_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, i64, vp, vp, i32, vp,
                                          i64, vp]
+    lib.tide_gated_block_workspace.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64p]
+    lib.tide_gated_block.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp]
+    lib.tide_gated_block_grad.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, vp, i64, vp, vp,
+                                          i32, i32, vp, i64, vp]
     i32p = ctypes.POINTER(i32)
     lib.tide_device_info.argtypes = [i32p, i32p, i32p, i32p]
     lib.tide_probe_launch.argtypes = [vp, i32, i32, i64, vp]
@@ -863,6 +871,109 @@ def layer_norm_grad(dout, x, weight, mean, rstd, dx, dweight=None, dbias=None, a
     handle = _device_stream(stream)
     ws, nbytes, keep = _workspace(need, workspace, stream)
     _check(lib.tide_layer_norm_grad(*args, ws, nbytes, handle))
+
+
+# ------------------------------------------------------------ gated block
+
+
+def _block(x, w_gate, w_up, gates):
+    """The operands' arguments, (tokens, hidden size, ffn size), gates' arguments."""
+    p, tokens, size, stride = _matrix(x, _BF16, "x")
+    g, ffn, g_size, g_stride = _matrix(w_gate, _BF16, "w_gate")
+    u, *u_shape, u_stride = _matrix(w_up, _BF16, "w_up")
+    if g_size != size:
+        raise ValueError(f"w_gate has {g_size} columns, x {size}")
+    _same_shape(ffn, size, "w_up", tuple(u_shape))
+    kept = None, 0
+    if gates is not None:
+        k, *k_shape, k_stride = _matrix(gates, _BF16, "gates")
+        _same_shape(tokens, 2 * ffn, "gates", tuple(k_shape))
+        kept = k, k_stride
+    return (p, stride, g, g_stride, u, u_stride), (tokens, size, ffn), kept
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _gated_block_bytes(operands, sizes, gradients, gates):
+    need = ctypes.c_int64()
+    _check(lib.tide_gated_block_workspace(*operands, *sizes, gradients, gates, ctypes.byref(need)))
+    return need.value
+
+
+def gated_block_workspace(x, w_gate, w_up, gradients=False, gates=None):
+    """Bytes of workspace of gated_block, or with `gradients` of gated_block_grad,
+    with or without gates (tide_gated_block_workspace)."""
+    operands, sizes, kept = _block(x, w_gate, w_up, gates)
+    return _gated_block_bytes(operands, sizes, int(bool(gradients)), kept[0])
+
+
+def _gated_block_args(x, w_gate, w_up, out, gates, activation):
+    """(arguments up to the workspace's, bytes of workspace)."""
+    operands, sizes, kept = _block(x, w_gate, w_up, gates)
+    o, *shape, stride = _matrix(out, _BF16, "out")
+    _same_shape(sizes[0], sizes[2], "out", tuple(shape))
+    return (*operands, *sizes, _activation(activation), o, stride, *kept), _gated_block_bytes(operands, sizes, 0, kept[0])
+
+
+def gated_block_call(x, w_gate, w_up, out, gates=None, activation="silu", workspace=None):
+    """A registered gated block (see gated_block); `workspace` as for
+    checkpoint_weight_grad_call."""
+    args, need = _gated_block_args(x, w_gate, w_up, out, gates, activation)
+    return WorkspaceCall(lib.tide_gated_block, args, (x, w_gate, w_up, out, gates), need, workspace)
+
+
+def gated_block(x, w_gate, w_up, out, gates=None, activation="silu", workspace=None, stream=None):
+    """The gated feed-forward block: out = act(x @ w_gate.T) * (x @ w_up.T), all
+    bf16 with contiguous rows, act "silu" or "gelu" (its tanh form).  gates
+    (tokens x 2 ffn, bf16), if given, receives the two products for
+    gated_block_grad.  `workspace` as for checkpoint_weight_grad
+    (tide_gated_block)."""
+    args, need = _gated_block_args(x, w_gate, w_up, out, gates, activation)
+    handle = _device_stream(stream)
+    ws, nbytes, keep = _workspace(need, workspace, stream)
+    _check(lib.tide_gated_block(*args, ws, nbytes, handle))
+
+
+def _gated_block_grad_args(dout, x, w_gate, w_up, dx, dw_gate, dw_up, gates, activation, accumulate):
+    """(arguments up to the workspace's, bytes of workspace)."""
+    operands, sizes, kept = _block(x, w_gate, w_up, gates)
+    tokens, size, ffn = sizes
+    d, *d_shape, d_stride = _matrix(dout, _BF16, "dout")
+    _same_shape(tokens, ffn, "dout", tuple(d_shape))
+    o, *o_shape, o_stride = _matrix(dx, _BF16, "dx")
+    _same_shape(tokens, size, "dx", tuple(o_shape))
+    g, *g_shape, _ = _matrix(dw_gate, _FLOATS, "dw_gate", strided=False)
+    u, *u_shape, _ = _matrix(dw_up, (dw_gate.dtype,), "dw_up", strided=False)
+    _same_shape(ffn, size, "dw_gate", tuple(g_shape))
+    _same_shape(ffn, size, "dw_up", tuple(u_shape))
+    args = (d, d_stride, *operands, *sizes, _activation(activation), *kept, o, o_stride, g, u, _FLOATS[dw_gate.dtype],
+            int(bool(accumulate)))
+    return args, _gated_block_bytes(operands, sizes, 1, kept[0])
+
+
+def gated_block_grad_call(dout, x, w_gate, w_up, dx, dw_gate, dw_up, gates=None, activation="silu", accumulate=False,
+                          workspace=None):
+    """A registered gradient of the gated block (see gated_block_grad);
+    `workspace` as for checkpoint_weight_grad_call."""
+    args, need = _gated_block_grad_args(dout, x, w_gate, w_up, dx, dw_gate, dw_up, gates, activation, accumulate)
+    return WorkspaceCall(lib.tide_gated_block_grad, args, (dout, x, w_gate, w_up, dx, dw_gate, dw_up, gates), need,
+                         workspace)
+
+
+def gated_block_grad(dout, x, w_gate, w_up, dx, dw_gate, dw_up, gates=None, activation="silu", accumulate=False,
+                     workspace=None, stream=None):
+    """Gradients of gated_block from dout: dx (bf16) and the weights' (bf16 or
+    fp32; added to the old ones when accumulate is true).  gates are those that
+    gated_block left; without them the two products are formed again.  `workspace`
+    as for checkpoint_weight_grad (tide_gated_block_grad)."""
+    args, need = _gated_block_grad_args(dout, x, w_gate, w_up, dx, dw_gate, dw_up, gates, activation, accumulate)
+    handle = _device_stream(stream)
+    ws, nbytes, keep = _workspace(need, workspace, stream)
+    _check(lib.tide_gated_block_grad(*args, ws, nbytes, handle))
 
 
 # ------------------------------------------------------------ instruments

@@ -78,3 +78,88 @@ def layer_norm_grad(dy, x, w, mean, rstd, old_dw=None, old_db=None):
         dw, db = dw + old_dw, db + old_db
         e_dw, e_db = e_dw + U32 * np.abs(dw), e_db + U32 * np.abs(db)
     return {"dx": (dx, 1.01 * e), "dweight": (dw, 1.01 * e_dw), "dbias": (db, 1.01 * e_db)}
+
+EXACT_SUM = 2.0**-23  # of the magnitudes, per addition of an adder that may truncate
+
+
+def act(z, name):
+    """(value, derivative, the sigmoid's argument) in float64."""
+    if name == "silu":
+        k, dk = z, np.ones_like(z)
+    else:
+        c = 2 * np.sqrt(2 / np.pi)
+        k, dk = c * (z + 0.044715 * z**3), c * (1 + 3 * 0.044715 * z**2)
+    e = np.exp(-np.abs(k))
+    s = np.where(k >= 0, 1, e) / (1 + e)
+    return z * s, s + z * dk * e / (1 + e) ** 2, k
+
+
+def _activated(z, ez, name):
+    """(value, bound, derivative, bound) of the activation of z that is off by ez.
+
+    The slopes of both activations are below 1.13 and their second derivatives
+    below 0.8.  The sigmoid's argument is rounded at most 7 times (GELU's cubic,
+    the constant log2 e), which an exponential multiplies by |k|; the exponential,
+    the reciprocal and the operations around them are off by 2^-23 each, at most
+    8 of them.  Exponentials below 2^-126 may be flushed."""
+    a, d, k = act(z, name)
+    rel = (4 * np.abs(k) + 10) * EXACT_SUM
+    s, flush = np.abs(a / np.where(z == 0, 1, z)) + (z == 0) * 0.5, 2.0**-125 * (1 + np.abs(z))
+    ea = 1.13 * ez + np.abs(a) * rel + flush
+    return a, ea, d, 0.8 * ez + rel * (s + np.abs(d - np.where(z == 0, 0.5, a / np.where(z == 0, 1, z)))) + flush
+
+
+def _gates(x, wg, wu):
+    n = (x.shape[1] + 64) * EXACT_SUM
+    return x @ wg.T, n * (np.abs(x) @ np.abs(wg).T), x @ wu.T, n * (np.abs(x) @ np.abs(wu).T)
+
+
+def gated_block(x, wg, wu, name):
+    """{name: (value, bound)} of out and gates for float64 x, wg and wu: sums of
+    hidden exact products, the activation, and one more rounding of the product."""
+    g, eg, u, eu = _gates(x, wg, wu)
+    a, ea, _, _ = _activated(g, eg, name)
+    eh = ea * np.abs(u) + np.abs(a) * eu + ea * eu + 2 * U32 * np.abs(a * u)
+    return {"out": (a * u, eh), "gates": (np.concatenate([g, u], 1), np.concatenate([eg, eu], 1))}
+
+
+def gated_block_grad(dout, x, wg, wu, name, gates=None, old=None):
+    """{name: (value, bound, rms)} of dx, dw_gate and dw_up: bounds before the
+    result's own rounding, and of the root mean square of the whole error of a bf16
+    result.  gates: the values that were kept, which are then exact.
+
+    dg and du are rounded to bf16 once; the sums add at most K products and 64
+    partial sums.  For the root mean square those roundings and the result's are
+    taken as independent and uniform in their half steps, 1.5 times, and to it the
+    bound of everything else."""
+    f = wg.shape[0]
+    if gates is None:
+        g, eg, u, eu = _gates(x, wg, wu)
+    else:
+        g, u = gates[:, :f], gates[:, f:]
+        eg = eu = np.zeros_like(g)
+    a, ea, d, ed = _activated(g, eg, name)
+    dh = np.abs(dout)
+    dg, du = dout * u * d, dout * a
+    arith = [dh * (np.abs(u) * ed + np.abs(d) * eu + ed * eu) + 3 * U32 * np.abs(dg), dh * ea + 2 * U32 * np.abs(du)]
+    err = [rounded(v, e, "bf16") for v, e in zip((dg, du), arith)]
+    out = {}
+    half = HALF["bf16"]
+
+    def product(name, pairs, old=None):
+        value = sum(p @ b for p, _, _, b in pairs)
+        k = sum(b.shape[0] for _, _, _, b in pairs)
+        sums = (k + 64) * EXACT_SUM * sum((np.abs(p) + e) @ np.abs(b) for p, e, _, b in pairs)
+        var = half**2 / 3 * sum((p**2) @ (b**2) for p, _, _, b in pairs)
+        rest = sum(ar @ np.abs(b) for _, _, ar, b in pairs) + sums
+        bound = sum(e @ np.abs(b) for _, e, _, b in pairs) + sums
+        if old is not None:
+            value = value + old
+            bound, rest = bound + U32 * np.abs(value), rest + U32 * np.abs(value)
+        rms = 1.5 * np.sqrt((var + half**2 / 3 * value**2).sum()) + np.sqrt((rest**2).sum())
+        out[name] = (value, bound, rms)
+
+    product("dx", [(dg, err[0], arith[0], wg), (du, err[1], arith[1], wu)])
+    product("dw_gate", [(dg.T, err[0].T, arith[0].T, x)], None if old is None else old[0])
+    product("dw_up", [(du.T, err[1].T, arith[1].T, x)], None if old is None else old[1])
+    return out

@@ -613,6 +613,43 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
                                   int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Orthogonalized updates: what an optimizer makes of the whole gradient (or
+ * momentum) of a weight matrix, by Newton-Schulz products.  Touches no plan.
+ *
+ * For each of `count` matrices X of rows x cols,
+ *   X0 = X / (sqrt(sum of squares) + eps)
+ * and `steps` times
+ *   G = X X^T,  X <- (a I + b G + c G^2) X
+ * so that every singular value s becomes s (a + b s^2 + c s^4) a step, towards 1
+ * for coefficients such as 3.4445, -4.7750, 2.0315 in 5 steps.  (With more rows
+ * than columns the same from X^T X, on the right.)  The norm is summed in fp64,
+ * every product in fp32; the products' operands X, G and the polynomial are rounded
+ * to fp16 times 2^12 (by at most 2^-11 of themselves, or by 2^-37), but in the first
+ * three steps the term a X comes from X to 22 bits; the result is rounded once to
+ * bf16.  The order of every sum depends on the sizes and the count only.  Entries of
+ * those operands must stay below 16: coefficients and steps with which they may
+ * not are refused (TIDE_ERR_INVALID).
+ * A matrix of zeros stays zero (with eps above 0); one that holds a NaN or an
+ * infinity comes out as NaN throughout.  The others are not touched by it.
+ *
+ *   x       count matrices of x_dtype, aligned to the element, rows x_stride
+ *           elements apart (all the same)
+ *   out     count matrices of bf16, rows out_stride apart.  out[i] may be x[i]
+ *           (bf16, the same strides), otherwise none may overlap another or an input;
+ *           one that is listed twice, or as another's input, is refused.
+ *           Both lists are read during the call only.
+ *   workspace  as for the weight gradient above; matrices are taken so many at a
+ *           time that it stays below about 1 GiB, one at least
+ * Sizes: rows and cols up to 2^22, matrices and the square of the smaller side as
+ * for the checkpoints; steps in [1, 64].
+ * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+tide_status tide_orthogonalize_workspace(int32_t count, int64_t rows, int64_t cols, int32_t steps, int64_t* bytes);
+tide_status tide_orthogonalize(const void* const* x, int32_t x_dtype, int64_t x_stride, uint16_t* const* out,
+                               int64_t out_stride, int32_t count, int64_t rows, int64_t cols, int32_t steps, float a,
+                               float b, float c, float eps, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Interference instruments (Section 2.2 "SM Wave Quantization", Equation 4,
  * Figure 3, Table 4 and Table 5): what one GPU can show of the cost a
  * collective's kernels impose on the compute they overlap.  None of these

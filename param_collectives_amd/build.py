@@ -19,7 +19,7 @@ LIBRARY = os.path.join(HERE, "libtide.so")
 SOURCES = [os.path.join(CSRC, n) for n in (
     "plan.cpp", "capi.cpp", "kernels.hip", "instruments.hip", "scratch.hip",
     "training.cpp", "checkpoint.hip", "weight_grad.hip", "vocab_loss.hip",
-    "layer_norm.hip", "gated_block.hip")]
+    "layer_norm.hip", "gated_block.hip", "orthogonalize.hip")]
 ARCH = "gfx950"
 
 

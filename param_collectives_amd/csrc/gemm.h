@@ -1,7 +1,9 @@
 // The matrix-product core of the training-step operators (weight_grad.hip,
-// vocab_loss.hip) on MI355X (gfx950): one workgroup computes a BM x BN tile of
+// vocab_loss.hip, gated_block.hip, orthogonalize.hip) on MI355X (gfx950): one
+// workgroup computes a BM x BN tile of
 //   C[m][n] = sum_k A(m, k) B(k, n)
-// with bf16 operands and fp32 sums on the matrix cores (16x16x32 products).
+// with bf16 (or, on request, fp16) operands and fp32 sums on the matrix cores
+// (16x16x32 products).
 //
 // An operand is read in one of five forms:
 //   Form::kRows    its rows are C's rows (columns), k runs along them;
@@ -40,6 +42,7 @@ namespace tide {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -58,7 +61,7 @@ enum class Code { kE4m3, kInt8 };
 constexpr int kStages = 4;  // LDS stages a tile's steps go round
 
 struct Operand {
-  const void* base;       // bf16 values, or codes (kPacked); 16-byte aligned
+  const void* base;       // bf16 (fp16) values, or codes (kPacked); 16-byte aligned
   const uint8_t* scales;  // kPacked: [k][scale_ld]
   int64_t ld;             // elements from row to row, a multiple of 8 (kPacked: of 32)
   int64_t scale_ld;
@@ -458,7 +461,7 @@ __device__ __forceinline__ void lds_barrier() {
 // registers and written to LDS 2 steps ahead.)  The whole steps are filled up
 // to a multiple of 4 with empty ones, which go first; a short last step goes
 // before them all, from the last stage.
-template <Form FA, Form FB, Code CODE, int BM, int BN, int WM, int WN>
+template <Form FA, Form FB, Code CODE, int BM, int BN, int WM, int WN, bool F16 = false>
 struct Gemm {
   static constexpr int kThreads = WM * WN * 64;
   static constexpr int kFM = BM / WM / 16, kFN = BN / WN / 16;  // fragments of a wave
@@ -492,6 +495,13 @@ struct Gemm {
     wn = wave_index() % WN;
     SA::spots(at_a, wm * (BM / WM), lane);
     SB::spots(at_b, wn * (BN / WN), lane);
+  }
+
+  static __device__ __forceinline__ f32x4v product(bf16x8 n, bf16x8 m, f32x4v sum) {
+    if constexpr (F16)
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, n), __builtin_bit_cast(f16x8, m), sum, 0, 0,
+                                                    0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(n, m, sum, 0, 0, 0);
   }
 
   // Loads to LDS of step s + ahead < s + 3.
@@ -576,7 +586,7 @@ struct Gemm {
             if (i == (j * kFM) / kFN) nb[j] = SB::fragment(next + SA::kBytes, at_b, j);
         }
 #pragma unroll
-        for (int j = 0; j < kFN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], a[i], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < kFN; ++j) acc[i][j] = product(fb[j], a[i], acc[i][j]);
         part(i);
         // A step's loads to LDS come before its codes', as the next waits count
         // them.  (Not between them everywhere: with 256 x 256 tiles of int8 codes
@@ -737,6 +747,48 @@ struct Gemm {
     }
   }
 
+  // each(), and with `mirror` also t(column, row, values of 8 rows from that one)
+  // for every group of eight in a column.
+  template <typename F, typename T, typename H>
+  __device__ __forceinline__ void each_mirrored(char* lds, bool mirror, F f, T t, H halfway) {
+    constexpr int kCols = BN / WN, kQuads = kCols / 4, kMask = kQuads - 1, kGroups = kCols / 8;
+    static_assert(WM * WN * 16 * kCols * 4 <= kStage && 16 * kGroups % 64 == 0, "epilogue rows");
+    float* rows = reinterpret_cast<float*>(lds) + wave_index() * 16 * kCols;
+#pragma unroll
+    for (int i = 0; i < kFM; ++i) {
+      const int w = lane & 15;
+#pragma unroll
+      for (int j = 0; j < kFN; ++j)
+        *reinterpret_cast<f32x4v*>(rows + w * kCols + ((4 * j + (lane >> 4)) ^ (w & kMask)) * 4) = acc[i][j];
+      wave_order();
+#pragma unroll 1
+      for (int q = lane; q < 16 * kGroups; q += 64) {
+        const int r = q / kGroups, c = q % kGroups;
+        f(wm * (BM / WM) + i * 16 + r, wn * kCols + c * 8,
+          *reinterpret_cast<const f32x4v*>(rows + r * kCols + ((2 * c) ^ (r & kMask)) * 4),
+          *reinterpret_cast<const f32x4v*>(rows + r * kCols + ((2 * c + 1) ^ (r & kMask)) * 4));
+      }
+      if (mirror) {
+#pragma unroll 1
+        for (int q = lane; q < kCols * 2; q += 64) {
+          const int n = q >> 1, r0 = (q & 1) * 8;
+          f32x4v lo, hi;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float v = rows[(r0 + j) * kCols + ((n >> 2) ^ ((r0 + j) & kMask)) * 4 + (n & 3)];
+            if (j < 4)
+              lo[j & 3] = v;
+            else
+              hi[j & 3] = v;
+          }
+          t(wn * kCols + n, wm * (BM / WM) + i * 16 + r0, lo, hi);
+        }
+      }
+      wave_order();
+      if (i == kFM / 2 - 1) halfway();
+    }
+  }
+
   // Writes the tile at (m0, n0) to `t`.
   template <typename H>
   __device__ __forceinline__ void write(const Target& t, int64_t m0, int64_t n0, char* lds, H halfway) {
@@ -872,6 +924,14 @@ __device__ __forceinline__ Piece piece_of(const Cut& c, uint32_t item, int64_t d
 template <int SIDE>
 __device__ __forceinline__ Target slot_target(float* partial, int64_t slot, int64_t rows) {
   return Target{partial + slot * SIDE * SIDE, SIDE, rows < SIDE ? rows : SIDE, SIDE, nullptr, nullptr, 1.0f, 1, 0};
+}
+
+// 8 columns from `col` of row `row` of a slot.
+template <int SIDE>
+__device__ __forceinline__ void put_slot(float* partial, int64_t slot, int row, int col, f32x4v lo, f32x4v hi) {
+  float* p = partial + slot * SIDE * SIDE + row * SIDE + col;
+  *reinterpret_cast<f32x4v*>(p) = lo;
+  *reinterpret_cast<f32x4v*>(p + 4) = hi;
 }
 
 // The partial sums of 8 columns from `col` of row `row` of tile full + r (of a cut

@@ -1,0 +1,666 @@
+// Orthogonalised updates on MI355X (gfx950): a matrix X is taken towards U V^T of
+// its singular value decomposition by a few steps of
+//   X <- X / (|X| + eps)                       (the Frobenius norm)
+//   G = X X^T,  P = a I + b G + c G^2,  X <- P X    (X^T X and X P for tall ones)
+// so that every singular value s goes to s (a + b s^2 + c s^4) a step.  G and P
+// are symmetric: only the tiles on and below the diagonal are formed, and written
+// twice.
+//
+// Bound by the matrix cores: m (m + 1) n + m^2 (m + 1) + 2 m^2 n operations a
+// step, m the smaller side.  The operands of the products are fp16, whose rate is
+// bf16's: all entries of X, G and P are below 16, and kept times 2^12 they are
+// normal numbers down to 2^-26, rounded by at most 2^-11.  bf16's roundings come
+// out as errors of 1 to 3% in the 2-norm where a few directions are strong: what
+// the first roundings of X leave in the weak directions is raised with them.  For
+// the same reason the first kExact steps take the term a X from X with the rest of
+// its rounding, a second fp16, and P without its diagonal: 0.1% instead of 0.4%
+// (a simulation in 64 bits with these roundings).  From then on the weak
+// directions are large enough, and a I stays in P.
+//
+// The norm is summed in fp64, which no entry's square leaves.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm.h"
+#include "training.h"
+
+namespace {
+
+using namespace tide;
+
+constexpr int kExact = 3;               // steps whose a X keeps the rest of X's rounding
+constexpr float kUnit = 4096.0f;        // entries are kept times this
+constexpr float kRest = 2048.0f;        // and the rest of a rounding times this as well
+constexpr int64_t kMost = 64;           // matrices of a piece, whose addresses go with the launch
+constexpr int64_t kSumBlocks = 256;     // workgroups that share a matrix's norm, at most
+
+__device__ __forceinline__ uint32_t f16_bits(float v) {
+  const _Float16 h = _Float16(v);
+  uint16_t r;
+  __builtin_memcpy(&r, &h, 2);
+  return r;
+}
+__device__ __forceinline__ float f16_value(uint32_t bits) {
+  const uint16_t b = uint16_t(bits);
+  _Float16 h;
+  __builtin_memcpy(&h, &b, 2);
+  return float(h);
+}
+__device__ __forceinline__ float f16_at(const u32x4& v, int j) { return f16_value(v[j >> 1] >> (16 * (j & 1))); }
+__device__ __forceinline__ u32x4 eight_f16(const float* v) {
+  u32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = f16_bits(v[2 * j]) | f16_bits(v[2 * j + 1]) << 16;
+  return r;
+}
+// Eight values and the rests of their roundings.
+__device__ __forceinline__ void split_eight(const float* v, u32x4* hi, u32x4* lo) {
+  *hi = eight_f16(v);
+  float rest[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) rest[j] = (v[j] - f16_at(*hi, j)) * kRest;
+  *lo = eight_f16(rest);
+}
+
+struct Pointers {
+  void* p[kMost];
+};
+
+// ------------------------------------------------------------ the norm
+
+struct StartArgs {
+  Pointers x;
+  int32_t f32;
+  int64_t ld, rows, cols;
+  double* sums;  // [matrix][gridDim.x]
+  uint32_t* queues;
+  uint32_t queue_words;
+  float eps;
+  uint16_t* hi;  // [matrix][rows][pitch]
+  uint16_t* lo;
+  int64_t pitch, matrix;
+};
+
+// 8 values of a row from column c, as fp32; zeros past its end.
+__device__ __forceinline__ void eight_values(const StartArgs& a, const void* x, int64_t r, int64_t c, float* v) {
+  const int64_t left = a.cols - c;
+  if (a.f32) {
+    const float* p = static_cast<const float*>(x) + r * a.ld + c;
+    if (left >= 8) {
+      const f32x4v l = *reinterpret_cast<const any_f32x4*>(p), h = *reinterpret_cast<const any_f32x4*>(p + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < 4 ? l[j & 3] : h[j & 3];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : 0.0f;
+    }
+  } else {
+    const u32x4 w = eight_of(static_cast<const uint16_t*>(x) + r * a.ld + c, left);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (j & 1) ? high_bf16(w[j >> 1]) : low_bf16(w[j >> 1]);
+  }
+}
+
+// The sum of squares of a workgroup's share of matrix blockIdx.y.  Clears the
+// queues of the launches that follow.
+__global__ __launch_bounds__(256) void square_sums_kernel(StartArgs a) {
+  __shared__ double part[4];
+  for (uint32_t i = (blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x; i < a.queue_words;
+       i += gridDim.x * gridDim.y * 256)
+    a.queues[i] = 0;
+  const void* x = a.x.p[blockIdx.y];
+  const int64_t groups = (a.cols + 7) / 8, all = a.rows * groups;
+  double s = 0;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / groups;
+    float v[8];
+    eight_values(a, x, r, (i - r * groups) * 8, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += double(v[j]) * double(v[j]);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) a.sums[blockIdx.y * gridDim.x + blockIdx.x] = part[0] + part[1] + part[2] + part[3];
+}
+
+// X over its norm, times kUnit, in two fp16; zeros to the row's pitch.  The
+// product is taken in fp64: the factor may lie outside fp32's range.
+__global__ __launch_bounds__(256) void normalize_kernel(StartArgs a, int32_t blocks) {
+  __shared__ double factor;
+  if (threadIdx.x < 64) {
+    double s = 0;
+    for (int i = threadIdx.x; i < blocks; i += 64) s += a.sums[int64_t(blockIdx.y) * blocks + i];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+    if (threadIdx.x == 0) factor = double(kUnit) / (sqrt(s) + double(a.eps));
+  }
+  __syncthreads();
+  const double f = factor;
+  const void* x = a.x.p[blockIdx.y];
+  const int64_t groups = a.pitch / 8, all = a.rows * groups;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / groups, c = (i - r * groups) * 8;
+    float v[8];
+    eight_values(a, x, r, c, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < a.cols ? float(double(v[j]) * f) : 0.0f;
+    u32x4 hi, lo;
+    split_eight(v, &hi, &lo);
+    const int64_t at = int64_t(blockIdx.y) * a.matrix + r * a.pitch + c;
+    *reinterpret_cast<u32x4*>(a.hi + at) = hi;
+    *reinterpret_cast<u32x4*>(a.lo + at) = lo;
+  }
+}
+
+// ------------------------------------------------------------ G and P
+
+// alpha S + beta G (+ diagonal), S = A A^T of each matrix.
+struct SymmetricArgs {
+  Operand a;
+  int64_t a_matrix;  // elements from matrix to matrix
+  int64_t depth;
+  Cut cut;
+  float* partial;
+  uint32_t tiles, side_tiles;  // of a matrix; on its side
+  uint32_t* queue;
+  const uint16_t* g;  // or null
+  uint16_t* out;      // size x size each, rows `ld` apart, `matrix` elements from one to the next
+  int64_t size, ld, matrix;
+  float alpha, beta, diagonal;
+
+  // 8 values of row m from column n, of a matrix.
+  __device__ __forceinline__ void put(int64_t z, int64_t m, int64_t n, f32x4v lo, f32x4v hi) const {
+    if (m >= size || n >= size) return;  // the pitch is a multiple of 8
+    const int64_t at = z * matrix + m * ld + n;
+    float v[8];
+    u32x4 old = u32x4{0, 0, 0, 0};
+    if (g) old = *reinterpret_cast<const u32x4*>(g + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = alpha * (j < 4 ? lo[j & 3] : hi[j & 3]) + beta * f16_at(old, j);
+      if (m == n + j) v[j] += diagonal;
+      if (n + j >= size) v[j] = 0.0f;
+    }
+    *reinterpret_cast<u32x4*>(out + at) = eight_f16(v);
+  }
+};
+
+// The matrix and the tile (row >= column) of tile t of all matrices.
+__device__ __forceinline__ void symmetric_tile(const SymmetricArgs& a, uint32_t t, int64_t* z, uint32_t* tm,
+                                               uint32_t* tn) {
+  const uint32_t u = nth_of_share(t, a.cut.tiles), k = u / a.tiles, i = u - k * a.tiles;
+  uint32_t row = uint32_t((sqrtf(8.0f * float(i) + 1.0f) - 1.0f) * 0.5f);
+  while (row * (row + 1) / 2 > i) --row;
+  while ((row + 1) * (row + 2) / 2 <= i) ++row;
+  *z = __builtin_amdgcn_readfirstlane(k);
+  *tm = __builtin_amdgcn_readfirstlane(row);
+  *tn = __builtin_amdgcn_readfirstlane(i - row * (row + 1) / 2);
+}
+
+template <Form F, int SIDE, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void symmetric_kernel(SymmetricArgs a) {
+  using G = Gemm<F, F, Code::kE4m3, SIDE, SIDE, WM, WN, true>;
+  __shared__ __align__(16) char lds0[G::kStage];
+  __shared__ __align__(16) char lds1[G::kStage];
+  __shared__ __align__(16) char lds2[G::kStage];
+  __shared__ __align__(16) char lds3[G::kStage];
+  __shared__ uint32_t turn;
+  Queue q;
+  uint32_t item = blockIdx.x;
+  if (a.queue) item = first_item(q, a.queue, a.cut.items, &turn);
+  if (item == kNoItem) return;
+  int64_t m0, n0, slot, z;
+  G g;
+  g.setup();
+  auto open = [&](uint32_t item) {
+    const Piece p = piece_of<false>(a.cut, item, a.depth);
+    uint32_t tm, tn;
+    symmetric_tile(a, p.tile, &z, &tm, &tn);
+    m0 = int64_t(tm) * SIDE;
+    n0 = int64_t(tn) * SIDE;
+    slot = p.slot;
+    Operand x = a.a;
+    x.base = static_cast<const uint16_t*>(x.base) + z * a.a_matrix;
+    g.open(x, x, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
+  };
+  open(item);
+  while (item != kNoItem) {
+    g.loop(lds0, lds1, lds2, lds3);
+    const uint32_t k = a.queue ? q.ask() : 0;
+    const int64_t m1 = m0, n1 = n0, z1 = z, s1 = slot;
+    auto halfway = [&] {
+      item = a.queue ? next_item(q, k, &turn) : kNoItem;
+      if (item != kNoItem) open(item);
+    };
+    g.each_mirrored(
+        lds3, s1 < 0 && m1 != n1,
+        [&](int r, int c, f32x4v lo, f32x4v hi) {
+          if (s1 >= 0)
+            put_slot<SIDE>(a.partial, s1, r, c, lo, hi);
+          else
+            a.put(z1, m1 + r, n1 + c, lo, hi);
+        },
+        [&](int c, int r, f32x4v lo, f32x4v hi) { a.put(z1, n1 + c, m1 + r, lo, hi); }, halfway);
+  }
+}
+
+// A part of a tile is 32 rows of 64 columns.
+template <int SIDE>
+__global__ __launch_bounds__(256) void join_symmetric_kernel(SymmetricArgs a) {
+  constexpr uint32_t kParts = SIDE * SIDE / 2048;
+  __shared__ float values[32][65];
+  const uint32_t r = blockIdx.x / kParts, part = blockIdx.x % kParts;
+  const uint32_t r0 = part / (SIDE / 64) * 32, c0 = part % (SIDE / 64) * 64;
+  int64_t z;
+  uint32_t tm, tn;
+  symmetric_tile(a, a.cut.full + r, &z, &tm, &tn);
+  const int64_t m0 = int64_t(tm) * SIDE, n0 = int64_t(tn) * SIDE;
+  const uint32_t row = threadIdx.x / 8, col = threadIdx.x % 8 * 8;
+  if (m0 + r0 >= a.size || n0 + c0 >= a.size) return;  // the whole part
+  f32x4v lo = f32x4v{0.f, 0.f, 0.f, 0.f}, hi = lo;
+  if (m0 + r0 + row < a.size) join_eight<SIDE>(a.partial, a.cut, r, r0 + row, c0 + col, &lo, &hi);
+  a.put(z, m0 + r0 + row, n0 + c0 + col, lo, hi);
+  if (tm == tn) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) values[row][col + j] = j < 4 ? lo[j & 3] : hi[j & 3];
+  __syncthreads();
+  const uint32_t n = threadIdx.x / 4, m = threadIdx.x % 4 * 8;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j < 4)
+      lo[j & 3] = values[m + j][n];
+    else
+      hi[j & 3] = values[m + j][n];
+  }
+  a.put(z, n0 + c0 + n, m0 + r0 + m, lo, hi);
+}
+
+// ------------------------------------------------------------ P X
+
+struct UpdateArgs {
+  Operand a, b;
+  int64_t a_matrix, b_matrix;  // elements from matrix to matrix
+  int64_t depth;
+  Cut cut;
+  float* partial;
+  uint32_t tiles_m, tiles_n;
+  uint32_t* queue;
+  int64_t rows, cols, ld, matrix;
+  const uint16_t* hi;  // X, where its term is added here (with lo), or null
+  uint16_t* lo;
+  float coefficient;
+  uint16_t* next;  // X's next, or null: the last step's result goes to out
+  int32_t keep;    // the rest of its rounding goes to lo
+  Pointers out;
+  int64_t out_ld;
+
+  __device__ __forceinline__ void put(int64_t z, int64_t m, int64_t n, f32x4v l, f32x4v h) const {
+    if (m >= rows || n >= cols) return;
+    const int64_t at = z * matrix + m * ld + n;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (j < 4 ? l[j & 3] : h[j & 3]) * (1.0f / kUnit);
+    if (hi) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(hi + at), y = *reinterpret_cast<const u32x4*>(lo + at);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = coefficient * (f16_at(x, j) + f16_at(y, j) * (1.0f / kRest)) + v[j];
+    }
+    if (next) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j >= cols) v[j] = 0.0f;
+      u32x4 x, y;
+      split_eight(v, &x, &y);
+      *reinterpret_cast<u32x4*>(next + at) = x;
+      if (keep) *reinterpret_cast<u32x4*>(lo + at) = y;
+      return;
+    }
+    uint16_t* o = static_cast<uint16_t*>(out.p[z]) + m * out_ld + n;
+    u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = two_bf16(v[2 * j] * (1.0f / kUnit), v[2 * j + 1] * (1.0f / kUnit));
+    if (n + 8 <= cols) {
+      *reinterpret_cast<any_u32x4*>(o) = w;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (n + j < cols) o[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
+  }
+};
+
+__device__ __forceinline__ void update_tile(const UpdateArgs& a, uint32_t t, int64_t* z, uint32_t* tm, uint32_t* tn) {
+  const uint32_t tiles = a.tiles_m * a.tiles_n, u = nth_of_share(t, a.cut.tiles), k = u / tiles, i = u - k * tiles;
+  const uint32_t band = i / (4 * a.tiles_n), in = i - band * 4 * a.tiles_n;
+  const uint32_t rows = band * 4 + 4 <= a.tiles_m ? 4 : a.tiles_m - band * 4;
+  *z = __builtin_amdgcn_readfirstlane(k);
+  *tm = __builtin_amdgcn_readfirstlane(band * 4 + in % rows);
+  *tn = __builtin_amdgcn_readfirstlane(in / rows);
+}
+
+template <Form FB, int SIDE, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void update_kernel(UpdateArgs a) {
+  using G = Gemm<Form::kRows, FB, Code::kE4m3, SIDE, SIDE, WM, WN, true>;
+  __shared__ __align__(16) char lds0[G::kStage];
+  __shared__ __align__(16) char lds1[G::kStage];
+  __shared__ __align__(16) char lds2[G::kStage];
+  __shared__ __align__(16) char lds3[G::kStage];
+  __shared__ uint32_t turn;
+  Queue q;
+  uint32_t item = blockIdx.x;
+  if (a.queue) item = first_item(q, a.queue, a.cut.items, &turn);
+  if (item == kNoItem) return;
+  int64_t m0, n0, slot, z;
+  G g;
+  g.setup();
+  auto open = [&](uint32_t item) {
+    const Piece p = piece_of<false>(a.cut, item, a.depth);
+    uint32_t tm, tn;
+    update_tile(a, p.tile, &z, &tm, &tn);
+    m0 = int64_t(tm) * SIDE;
+    n0 = int64_t(tn) * SIDE;
+    slot = p.slot;
+    Operand x = a.a, y = a.b;
+    x.base = static_cast<const uint16_t*>(x.base) + z * a.a_matrix;
+    y.base = static_cast<const uint16_t*>(y.base) + z * a.b_matrix;
+    g.open(x, y, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
+  };
+  open(item);
+  while (item != kNoItem) {
+    g.loop(lds0, lds1, lds2, lds3);
+    const uint32_t k = a.queue ? q.ask() : 0;
+    const int64_t m1 = m0, n1 = n0, z1 = z, s1 = slot;
+    auto halfway = [&] {
+      item = a.queue ? next_item(q, k, &turn) : kNoItem;
+      if (item != kNoItem) open(item);
+    };
+    g.template each<false>(
+        lds3,
+        [&](int r, int c, f32x4v lo, f32x4v hi) {
+          if (s1 >= 0)
+            put_slot<SIDE>(a.partial, s1, r, c, lo, hi);
+          else
+            a.put(z1, m1 + r, n1 + c, lo, hi);
+        },
+        halfway);
+  }
+}
+
+template <int SIDE>
+__global__ __launch_bounds__(256) void join_update_kernel(UpdateArgs a) {
+  constexpr uint32_t kParts = SIDE * SIDE / 2048;
+  const uint32_t r = blockIdx.x / kParts, i = blockIdx.x % kParts * 256 + threadIdx.x;
+  const uint32_t row = i / (SIDE / 8), col = i % (SIDE / 8) * 8;
+  int64_t z;
+  uint32_t tm, tn;
+  update_tile(a, a.cut.full + r, &z, &tm, &tn);
+  const int64_t m = int64_t(tm) * SIDE + row, n = int64_t(tn) * SIDE + col;
+  if (m >= a.rows || n >= a.cols) return;
+  f32x4v lo, hi;
+  join_eight<SIDE>(a.partial, a.cut, r, row, col, &lo, &hi);
+  a.put(z, m, n, lo, hi);
+}
+
+// ------------------------------------------------------------ launches
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+struct Tiling {
+  int64_t side = 256, tiles = 0;  // of all matrices
+  Cut cut{};
+};
+// The side and the cut that are estimated to end first, of tiles(side) tiles.
+template <typename F>
+Tiling tiling(int64_t depth, F tiles) {
+  const int64_t steps = (depth + kBK - 1) / kBK;
+  Tiling best;
+  double least = 0;
+  for (int64_t side : {256, 128}) {
+    Tiling t;
+    t.side = side;
+    t.tiles = tiles(side);
+    t.cut = cut_tiles(t.tiles, steps, side);
+    const double cost = cut_cost(t.cut, steps, side);
+    if (side == 256 || cost < least) {
+      best = t;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+// Where one call's workspace keeps what, of `piece` matrices at a time.
+struct Layout {
+  bool tall = false;
+  int64_t piece = 0, small = 0, pitch = 0, small_pitch = 0, matrix = 0, small_matrix = 0;
+  int64_t sum_blocks = 0;
+  int64_t partial_bytes = 0;
+  // byte offsets
+  int64_t sums = 0, queues = 0, x0 = 0, x1 = 0, lo = 0, g = 0, p = 0, partial = 0, bytes = 0;
+};
+
+struct Tilings {
+  Tiling gram, square, update;
+};
+Tilings tilings_of(const OrthogonalCall& c, const Layout& L, int64_t count) {
+  const int64_t large = c.rows > c.cols ? c.rows : c.cols;
+  auto triangle = [&](int64_t side) {
+    const int64_t t = (L.small + side - 1) / side;
+    return count * t * (t + 1) / 2;
+  };
+  Tilings t;
+  t.gram = tiling(large, triangle);
+  t.square = tiling(L.small, triangle);
+  t.update = tiling(L.small, [&](int64_t side) { return count * ((c.rows + side - 1) / side) * ((c.cols + side - 1) / side); });
+  return t;
+}
+
+Layout layout_of(const OrthogonalCall& c) {
+  Layout L;
+  L.tall = c.rows > c.cols;
+  L.small = L.tall ? c.cols : c.rows;
+  L.pitch = up(c.cols, 64);
+  L.small_pitch = up(L.small, 64);
+  L.matrix = c.rows * L.pitch;
+  L.small_matrix = L.small * L.small_pitch;
+  const int64_t each = 3 * L.matrix * 2 + 2 * L.small_matrix * 2;
+  L.piece = (int64_t(1) << 30) / each;
+  L.piece = L.piece < 1 ? 1 : L.piece > kMost ? kMost : L.piece;
+  if (L.piece > c.count) L.piece = c.count;
+  // pieces of one size, the last one's rest apart
+  const int64_t pieces = (c.count + L.piece - 1) / L.piece;
+  L.piece = (c.count + pieces - 1) / pieces;
+  const int64_t groups = (c.rows * (L.pitch / 8) + 255) / 256;
+  L.sum_blocks = 2048 / L.piece;
+  if (L.sum_blocks > kSumBlocks) L.sum_blocks = kSumBlocks;
+  if (L.sum_blocks > groups) L.sum_blocks = groups;
+  const int64_t last = c.count - (pieces - 1) * L.piece;
+  for (int64_t n : {L.piece, last}) {
+    const Tilings t = tilings_of(c, L, n);
+    for (const Tiling& one : {t.gram, t.square, t.update}) {
+      const int64_t bytes = partial_bytes(one.cut, one.side);
+      L.partial_bytes = bytes > L.partial_bytes ? bytes : L.partial_bytes;
+    }
+  }
+  int64_t at = 0;
+  auto take = [&](int64_t n) {
+    const int64_t here = at;
+    at += up(n, 256);
+    return here;
+  };
+  L.sums = take(L.piece * L.sum_blocks * 8);
+  L.queues = take(3 * c.steps * kQueueWords * kQueuePitch * 4);
+  L.x0 = take(L.piece * L.matrix * 2);
+  L.x1 = take(L.piece * L.matrix * 2);
+  L.lo = take(L.piece * L.matrix * 2);
+  L.g = take(L.piece * L.small_matrix * 2);
+  L.p = take(L.piece * L.small_matrix * 2);
+  if (L.partial_bytes > 0) L.partial = take(L.partial_bytes);
+  L.bytes = at;
+  return L;
+}
+
+#define TIDE_LAUNCHED()                       \
+  do {                                        \
+    const int rc_ = int(hipGetLastError());   \
+    if (rc_ != 0) return rc_;                 \
+  } while (0)
+
+template <Form F>
+int launch_symmetric(SymmetricArgs a, const Tiling& t, int64_t count, uint32_t* queue, hipStream_t st) {
+  a.cut = t.cut;
+  a.tiles = uint32_t(t.tiles / count);
+  a.side_tiles = uint32_t((a.size + t.side - 1) / t.side);
+  a.queue = t.cut.items > tile_slots(t.side) ? queue : nullptr;
+  const dim3 grid(resident_groups(t.cut.items, t.side));
+  if (t.side == 256)
+    hipLaunchKernelGGL((symmetric_kernel<F, 256, 2, 4>), grid, dim3(512), 0, st, a);
+  else
+    hipLaunchKernelGGL((symmetric_kernel<F, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  TIDE_LAUNCHED();
+  if (t.cut.splits == 1) return 0;
+  const unsigned rest = t.cut.tiles - t.cut.full;
+  if (t.side == 256)
+    hipLaunchKernelGGL(join_symmetric_kernel<256>, dim3(rest * 32), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(join_symmetric_kernel<128>, dim3(rest * 8), dim3(256), 0, st, a);
+  return int(hipGetLastError());
+}
+
+template <Form FB>
+int launch_update(UpdateArgs a, const Tiling& t, uint32_t* queue, hipStream_t st) {
+  a.cut = t.cut;
+  a.tiles_m = uint32_t((a.rows + t.side - 1) / t.side);
+  a.tiles_n = uint32_t((a.cols + t.side - 1) / t.side);
+  a.queue = t.cut.items > tile_slots(t.side) ? queue : nullptr;
+  const dim3 grid(resident_groups(t.cut.items, t.side));
+  if (t.side == 256)
+    hipLaunchKernelGGL((update_kernel<FB, 256, 2, 4>), grid, dim3(512), 0, st, a);
+  else
+    hipLaunchKernelGGL((update_kernel<FB, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  TIDE_LAUNCHED();
+  if (t.cut.splits == 1) return 0;
+  const unsigned rest = t.cut.tiles - t.cut.full;
+  if (t.side == 256)
+    hipLaunchKernelGGL(join_update_kernel<256>, dim3(rest * 32), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(join_update_kernel<128>, dim3(rest * 8), dim3(256), 0, st, a);
+  return int(hipGetLastError());
+}
+
+int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t count, char* ws, hipStream_t st) {
+  uint32_t* queues = reinterpret_cast<uint32_t*>(ws + L.queues);
+  uint16_t* now = reinterpret_cast<uint16_t*>(ws + L.x0);
+  uint16_t* next = reinterpret_cast<uint16_t*>(ws + L.x1);
+  uint16_t* lo = reinterpret_cast<uint16_t*>(ws + L.lo);
+  uint16_t* gram = reinterpret_cast<uint16_t*>(ws + L.g);
+  uint16_t* poly = reinterpret_cast<uint16_t*>(ws + L.p);
+  float* partial = reinterpret_cast<float*>(ws + L.partial);
+  StartArgs s{};
+  Pointers out{};
+  for (int64_t i = 0; i < count; ++i) {
+    s.x.p[i] = const_cast<void*>(c.x[first + i]);
+    out.p[i] = c.out[first + i];
+  }
+  s.f32 = c.x_f32;
+  s.ld = c.x_ld;
+  s.rows = c.rows;
+  s.cols = c.cols;
+  s.sums = reinterpret_cast<double*>(ws + L.sums);
+  s.queues = queues;
+  s.queue_words = uint32_t(3 * c.steps * kQueueWords * kQueuePitch);
+  s.eps = c.eps;
+  s.hi = now;
+  s.lo = lo;
+  s.pitch = L.pitch;
+  s.matrix = L.matrix;
+  hipLaunchKernelGGL(square_sums_kernel, dim3(unsigned(L.sum_blocks), unsigned(count)), dim3(256), 0, st, s);
+  TIDE_LAUNCHED();
+  hipLaunchKernelGGL(normalize_kernel, dim3(unsigned(L.sum_blocks), unsigned(count)), dim3(256), 0, st, s,
+                     int32_t(L.sum_blocks));
+  TIDE_LAUNCHED();
+  const Tilings t = tilings_of(c, L, count);
+  for (int32_t k = 0; k < c.steps; ++k) {
+    const bool exact = k < kExact, last = k + 1 == c.steps;
+    uint32_t* q = queues + 3 * k * kQueueWords * kQueuePitch;
+    SymmetricArgs g{};
+    g.a = Operand{now, nullptr, L.pitch, 0, L.small};
+    g.a_matrix = L.matrix;
+    g.depth = L.tall ? c.rows : c.cols;
+    g.partial = partial;
+    g.out = gram;
+    g.size = L.small;
+    g.ld = L.small_pitch;
+    g.matrix = L.small_matrix;
+    g.alpha = 1.0f / kUnit;
+    int rc = L.tall ? launch_symmetric<Form::kCols>(g, t.gram, count, q, st)
+                    : launch_symmetric<Form::kRows>(g, t.gram, count, q, st);
+    if (rc != 0) return rc;
+    g.a = Operand{gram, nullptr, L.small_pitch, 0, L.small};
+    g.a_matrix = L.small_matrix;
+    g.depth = L.small;
+    g.g = gram;
+    g.out = poly;
+    g.alpha = c.c / kUnit;
+    g.beta = c.b;
+    g.diagonal = exact ? 0.0f : c.a * kUnit;
+    rc = launch_symmetric<Form::kRows>(g, t.square, count, q + kQueueWords * kQueuePitch, st);
+    if (rc != 0) return rc;
+    UpdateArgs u{};
+    u.depth = L.small;
+    u.partial = partial;
+    u.rows = c.rows;
+    u.cols = c.cols;
+    u.ld = L.pitch;
+    u.matrix = L.matrix;
+    u.hi = exact ? now : nullptr;
+    u.lo = lo;
+    u.coefficient = c.a;
+    u.next = last ? nullptr : next;
+    u.keep = k + 1 < kExact;
+    u.out = out;
+    u.out_ld = c.out_ld;
+    if (L.tall) {
+      u.a = Operand{now, nullptr, L.pitch, 0, c.rows};
+      u.a_matrix = L.matrix;
+      u.b = Operand{poly, nullptr, L.small_pitch, 0, L.small};
+      u.b_matrix = L.small_matrix;
+      rc = launch_update<Form::kRows>(u, t.update, q + 2 * kQueueWords * kQueuePitch, st);
+    } else {
+      u.a = Operand{poly, nullptr, L.small_pitch, 0, L.small};
+      u.a_matrix = L.small_matrix;
+      u.b = Operand{now, nullptr, L.pitch, 0, c.cols};
+      u.b_matrix = L.matrix;
+      rc = launch_update<Form::kCols>(u, t.update, q + 2 * kQueueWords * kQueuePitch, st);
+    }
+    if (rc != 0) return rc;
+    uint16_t* const old = now;
+    now = next;
+    next = old;
+  }
+  return 0;
+}
+
+}  // namespace
+
+namespace tide {
+
+int64_t orthogonalize_bytes(const OrthogonalCall& c) {
+  return c.count > 0 && c.rows > 0 && c.cols > 0 ? layout_of(c).bytes : 0;
+}
+
+int launch_orthogonalize(const OrthogonalCall& c, void* workspace, void* stream) {
+  if (c.count == 0 || c.rows == 0 || c.cols == 0) return 0;
+  const Layout L = layout_of(c);
+  for (int64_t first = 0; first < c.count; first += L.piece) {
+    const int64_t n = c.count - first < L.piece ? c.count - first : L.piece;
+    const int rc = run_piece(c, L, first, n, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+    if (rc != 0) return rc;
+  }
+  return 0;
+}
+
+}  // namespace tide

@@ -5,8 +5,12 @@
 // files of those names.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "tide_internal.h"
 #include "training.h"
@@ -195,6 +199,73 @@ tide_status gated_call(const uint16_t* x, int64_t x_stride, const uint16_t* w_ga
   call->gelu = activation == TIDE_ACT_GELU;
   call->gates = const_cast<uint16_t*>(gates);
   call->gates_ld = gates_stride;
+  return TIDE_OK;
+}
+
+tide_status check_orthogonalize(int32_t count, int64_t rows, int64_t cols, int64_t x_stride, int64_t out_stride,
+                                int32_t steps) {
+  if (count < 0) return invalid("a negative number of matrices");
+  TIDE_TRY(check_matrix("x", rows, cols, x_stride));
+  TIDE_TRY(check_matrix("out", rows, cols, out_stride));
+  if (rows > kMaxFeatures) return tide::set_error(TIDE_ERR_RANGE, "more than 2^22 rows");
+  const int64_t small = std::min(rows, cols);
+  TIDE_TRY(check_matrix("the smaller side's square", small, small, small));
+  if (steps < 1 || steps > 64) return invalid("steps must be in [1, 64]");
+  return TIDE_OK;
+}
+
+// The largest magnitude of p(t) = a + b t + c t^2 over [0, top].
+double largest_factor(double a, double b, double c, double top) {
+  double most = std::max(std::abs(a), std::abs(a + top * (b + top * c)));
+  const double at = c != 0 ? -b / (2 * c) : -1;
+  if (at > 0 && at < top) most = std::max(most, std::abs(a + at * (b + at * c)));
+  return most;
+}
+
+// Whether the steps keep every entry of their matrices in the range that fp16
+// operands times 2^12 hold (16, with room for roundings): a matrix's entries are
+// at most its largest singular value, which the polynomials bound.
+tide_status check_coefficients(double a, double b, double c, int32_t steps) {
+  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return invalid("the coefficients must be finite");
+  constexpr double kRoom = 14.0;
+  double top = 1.0;  // the largest singular value there may be
+  for (int32_t k = 0; k < steps; ++k) {
+    const double t = top * top;
+    bool fits = t <= kRoom && largest_factor(a, b, c, t) <= kRoom && largest_factor(0, b, c, t) <= kRoom;
+    if (fits) {
+      // s (a + b s^2 + c s^4) over [0, top]: its ends and where a + 3 b t + 5 c t^2 = 0
+      auto value = [&](double u) { return u >= 0 && u <= t ? std::sqrt(u) * std::abs(a + u * (b + u * c)) : 0.0; };
+      double next = value(t);
+      const double d = 9 * b * b - 20 * a * c;
+      if (c != 0 && d >= 0) {
+        next = std::max(next, value((-3 * b + std::sqrt(d)) / (10 * c)));
+        next = std::max(next, value((-3 * b - std::sqrt(d)) / (10 * c)));
+      } else if (c == 0 && b != 0) {
+        next = std::max(next, value(-a / (3 * b)));
+      }
+      top = next;
+      fits = top * top <= kRoom;
+    }
+    if (!fits) return invalid("with these coefficients the steps leave the range that their fp16 operands hold");
+  }
+  return TIDE_OK;
+}
+
+// No output twice, and none that is another matrix's input.
+tide_status check_distinct(const void* const* x, uint16_t* const* out, int32_t count) {
+  std::vector<std::pair<uintptr_t, int32_t>> at(count);
+  for (int32_t i = 0; i < count; ++i) at[i] = {reinterpret_cast<uintptr_t>(out[i]), i};
+  std::sort(at.begin(), at.end());
+  for (int32_t i = 1; i < count; ++i)
+    if (at[i].first == at[i - 1].first)
+      return invalid("out[" + std::to_string(at[i - 1].second) + "] and out[" + std::to_string(at[i].second) +
+                     "] are the same matrix");
+  for (int32_t i = 0; i < count; ++i) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(x[i]);
+    const auto same = std::lower_bound(at.begin(), at.end(), std::make_pair(p, int32_t(0)));
+    if (same != at.end() && same->first == p && same->second != i)
+      return invalid("out[" + std::to_string(same->second) + "] is x[" + std::to_string(i) + "]");
+  }
   return TIDE_OK;
 }
 
@@ -488,6 +559,57 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
     c.dw_f32 = dw_dtype == TIDE_DTYPE_F32;
     c.accumulate = accumulate;
     return hip_status(tide::launch_gated_block(c, workspace, stream), "gated block gradient launch");
+  });
+}
+
+tide_status tide_orthogonalize_workspace(int32_t count, int64_t rows, int64_t cols, int32_t steps, int64_t* bytes) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    if (bytes == nullptr) return invalid("bytes must not be NULL");
+    TIDE_TRY(check_orthogonalize(count, rows, cols, cols, cols, steps));
+    tide::OrthogonalCall c{};
+    c.count = count;
+    c.rows = rows;
+    c.cols = cols;
+    c.steps = steps;
+    *bytes = tide::orthogonalize_bytes(c);
+    return TIDE_OK;
+  });
+}
+
+tide_status tide_orthogonalize(const void* const* x, int32_t x_dtype, int64_t x_stride, uint16_t* const* out,
+                               int64_t out_stride, int32_t count, int64_t rows, int64_t cols, int32_t steps, float a,
+                               float b, float c, float eps, void* workspace, int64_t workspace_bytes, void* stream) {
+  return tide::guarded([&]() -> tide_status {
+    tide::clear_error();
+    TIDE_TRY(check_dtype("x_dtype", x_dtype));
+    TIDE_TRY(check_orthogonalize(count, rows, cols, x_stride, out_stride, steps));
+    TIDE_TRY(check_coefficients(a, b, c, steps));
+    if (!(eps >= 0)) return invalid("eps must not be negative");
+    if (count == 0 || rows == 0 || cols == 0) return TIDE_OK;
+    if (x == nullptr || out == nullptr) return invalid("x and out must not be NULL");
+    for (int32_t i = 0; i < count; ++i) {
+      const std::string n = "[" + std::to_string(i) + "]";
+      TIDE_TRY(check_pointer(("x" + n).c_str(), x[i], size_of(x_dtype)));
+      TIDE_TRY(check_pointer(("out" + n).c_str(), out[i], 2));
+    }
+    TIDE_TRY(check_distinct(x, out, count));
+    tide::OrthogonalCall o{};
+    o.x = x;
+    o.x_f32 = x_dtype == TIDE_DTYPE_F32;
+    o.x_ld = x_stride;
+    o.out = reinterpret_cast<void* const*>(out);
+    o.out_ld = out_stride;
+    o.count = count;
+    o.rows = rows;
+    o.cols = cols;
+    o.steps = steps;
+    o.a = a;
+    o.b = b;
+    o.c = c;
+    o.eps = eps;
+    TIDE_TRY(check_workspace(workspace, workspace_bytes, tide::orthogonalize_bytes(o)));
+    return hip_status(tide::launch_orthogonalize(o, workspace, stream), "orthogonalized update launch");
   });
 }
 

@@ -172,6 +172,18 @@ struct GatedCall {
   int32_t dw_f32, accumulate;
 };
 
+struct OrthogonalCall {
+  const void* const* x;  // `count` matrices of rows x cols, rows x_ld apart
+  int32_t x_f32;
+  int64_t x_ld;
+  void* const* out;  // bf16
+  int64_t out_ld;
+  int32_t count;
+  int64_t rows, cols;
+  int32_t steps;
+  float a, b, c, eps;
+};
+
 // Whether rows of `cols` bf16 elements, `ld` apart from p, all start and end on
 // 16 bytes: the tiles then read them in place, 16 bytes at a time and never
 // past a row's end.
@@ -196,5 +208,7 @@ int launch_align_rows(const void* src, int64_t src_ld, int64_t rows, int64_t col
                       void* stream, int64_t out_rows = 0);
 int64_t gated_block_bytes(const GatedCall& c);  // its workspace
 int launch_gated_block(const GatedCall& c, void* workspace, void* stream);
+int64_t orthogonalize_bytes(const OrthogonalCall& c);  // its workspace
+int launch_orthogonalize(const OrthogonalCall& c, void* workspace, void* stream);
 
 }  // namespace tide

@@ -73,6 +73,8 @@ EXPORTS = (
     "tide_gated_block_workspace",
     "tide_gated_block",
     "tide_gated_block_grad",
+    "tide_orthogonalize_workspace",
+    "tide_orthogonalize",
     "tide_device_info",
     "tide_probe_launch",
     "tide_victim_axpb",
@@ -132,6 +134,9 @@ def _load():
     lib.tide_gated_block.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp]
     lib.tide_gated_block_grad.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, vp, i64, vp, vp,
                                           i32, i32, vp, i64, vp]
+    lib.tide_orthogonalize_workspace.argtypes = [i32, i64, i64, i32, i64p]
+    lib.tide_orthogonalize.argtypes = [ctypes.POINTER(vp), i32, i64, ctypes.POINTER(vp), i64, i32, i64, i64, i32, f32, f32,
+                                       f32, f32, vp, i64, vp]
     i32p = ctypes.POINTER(i32)
     lib.tide_device_info.argtypes = [i32p, i32p, i32p, i32p]
     lib.tide_probe_launch.argtypes = [vp, i32, i32, i64, vp]
@@ -974,6 +979,66 @@ def gated_block_grad(dout, x, w_gate, w_up, dx, dw_gate, dw_up, gates=None, acti
     handle = _device_stream(stream)
     ws, nbytes, keep = _workspace(need, workspace, stream)
     _check(lib.tide_gated_block_grad(*args, ws, nbytes, handle))
+
+
+# ------------------------------------------------------------ orthogonalized updates
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def _matrices(tensors, dtypes, what):
+    """(addresses, rows, columns, row stride) of a list of matrices that are alike."""
+    if isinstance(tensors, torch.Tensor) or len(tensors) == 0:
+        raise TypeError(f"{what}: expected a list of matrices")
+    found = [_matrix(t, dtypes, f"{what}[{i}]") for i, t in enumerate(tensors)]
+    first = found[0][1:]
+    for i, (t, f) in enumerate(zip(tensors, found)):
+        if f[1:] != first or t.dtype != tensors[0].dtype:
+            raise ValueError(f"{what}[{i}] differs from {what}[0] in its shape, row stride or dtype")
+    return [f[0] for f in found], *first
+
+
+def _orthogonalize_bytes(count, rows, cols, steps):
+    need = ctypes.c_int64()
+    _check(lib.tide_orthogonalize_workspace(count, rows, cols, int(steps), ctypes.byref(need)))
+    return need.value
+
+
+def orthogonalize_workspace(updates, steps=5):
+    """Bytes of workspace orthogonalize takes (tide_orthogonalize_workspace)."""
+    addresses, rows, cols, _ = _matrices(updates, _FLOATS, "updates")
+    return _orthogonalize_bytes(len(addresses), rows, cols, steps)
+
+
+def _orthogonalize_args(updates, outs, steps, coefficients, eps):
+    """(arguments up to the workspace's, bytes of workspace)."""
+    x, rows, cols, stride = _matrices(updates, _FLOATS, "updates")
+    o, *shape, o_stride = _matrices(outs, _BF16, "outs")
+    if len(o) != len(x):
+        raise ValueError(f"{len(x)} updates, but {len(o)} outs")
+    _same_shape(rows, cols, "outs", tuple(shape))
+    a, b, c = (float(v) for v in coefficients)
+    return (_ptr_array(x), _FLOATS[updates[0].dtype], stride, _ptr_array(o), o_stride, len(x), rows, cols, int(steps), a, b,
+            c, float(eps)), _orthogonalize_bytes(len(x), rows, cols, steps)
+
+
+def orthogonalize_call(updates, outs, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, workspace=None):
+    """A registered orthogonalization (see orthogonalize); `workspace` as for
+    checkpoint_weight_grad_call."""
+    args, need = _orthogonalize_args(updates, outs, steps, coefficients, eps)
+    return WorkspaceCall(lib.tide_orthogonalize, args, (list(updates), list(outs)), need, workspace)
+
+
+def orthogonalize(updates, outs, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, workspace=None, stream=None):
+    """Orthogonalized updates: each of the matrices `updates` (a list, bf16 or fp32,
+    contiguous rows, all of one shape) is divided by its Frobenius norm (plus eps)
+    and taken through `steps` Newton-Schulz products a X + b (X X^T) X +
+    c (X X^T)^2 X into the matrix of `outs` (bf16), which may be the update itself.
+    `workspace` as for checkpoint_weight_grad (tide_orthogonalize)."""
+    args, need = _orthogonalize_args(updates, outs, steps, coefficients, eps)
+    handle = _device_stream(stream)
+    ws, nbytes, keep = _workspace(need, workspace, stream)
+    _check(lib.tide_orthogonalize(*args, ws, nbytes, handle))
 
 
 # ------------------------------------------------------------ instruments

@@ -163,3 +163,47 @@ def gated_block_grad(dout, x, wg, wu, name, gates=None, old=None):
     product("dw_gate", [(dg.T, err[0].T, arith[0].T, x)], None if old is None else old[0])
     product("dw_up", [(du.T, err[1].T, arith[1].T, x)], None if old is None else old[1])
     return out
+
+
+def _f16(t):
+    """The value that fp16 keeps of t times 2^12."""
+    with np.errstate(over="ignore"):
+        return (t * 4096).astype(np.float16).astype(np.float64) / 4096
+
+
+def newton_schulz(x, steps, a, b, c, eps):
+    """The definition, in float64."""
+    x = x / (np.sqrt((x**2).sum()) + eps)
+    for _ in range(steps):
+        g = x @ x.T if x.shape[0] <= x.shape[1] else x.T @ x
+        p = b * g + c * (g @ g)
+        x = a * x + (p @ x if x.shape[0] <= x.shape[1] else x @ p)
+    return x
+
+
+def orthogonalize(x, steps, a, b, c, eps, exact=3):
+    """(value, tolerance of the error's Frobenius norm after the rounding to bf16) of
+    a float64 matrix.
+
+    A bound that takes every rounding at its worst and in the worst direction is of
+    no use here: a step multiplies by up to 3.5 what lies in the weak directions.
+    The tolerance is the error of the definition with the kernels' roundings put in
+    where they are (X, G and the polynomial to fp16 times 2^12, a X from 22 bits in
+    the first `exact` steps), 1.5 times, since the kernels' own fp32 sums let some
+    values round the other way: as many roundings of the same sizes in other
+    directions, not more or larger ones (the sums' own errors are 2^-13 of them).
+    To it comes 1.5 times the root mean square of the result's rounding."""
+    value = newton_schulz(x, steps, a, b, c, eps)
+    tall = x.shape[0] > x.shape[1]
+    y = x.T if tall else x
+    y = y / (np.sqrt((y**2).sum()) + eps)
+    for k in range(steps):
+        h = _f16(y)
+        g = _f16(h @ h.T)
+        q = b * g + c * (g @ g)
+        if k < exact:
+            y = a * (h + _f16((y - h) * 2048) / 2048) + _f16(q) @ h
+        else:
+            y = _f16(q + a * np.eye(len(g))) @ h
+    err = np.linalg.norm((y.T if tall else y) - value)
+    return value, 1.5 * (err + HALF["bf16"] / np.sqrt(3) * np.linalg.norm(value)) + 2.0**-20 * np.linalg.norm(value)

@@ -28,22 +28,29 @@ namespace {
 
 using namespace tide;
 
-// The activation and its derivative.  Both activations are z sigma(k(z)) (GELU in
-// its tanh form: (1 + tanh y) / 2 = sigma(2 y)), with sigma and 1 - sigma each
-// taken from exp(-|k|): neither cancels nor overflows at either end.
+// Both activations are z sigma(k(z)) (GELU in its tanh form: (1 + tanh y) / 2 =
+// sigma(2 y)), with 1 - sigma(k) = sigma(k) exp(-k): neither cancels at either end.
+// Where exp(-k) leaves fp32, sigma is 0.
+constexpr float kLog2e = 1.44269504088896340736f, kRoot = 1.59576912160573071176f, kCube = 0.044715f;
+
+__device__ __forceinline__ float act_value(float z, int32_t gelu) {
+  const float k = gelu ? kRoot * z * (1.0f + kCube * (z * z)) : z;
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-k * kLog2e));
+}
+
+// The activation and its derivative.
 struct Act {
   float value, slope;
 };
 __device__ __forceinline__ Act activate(float z, int32_t gelu) {
-  constexpr float kLog2e = 1.44269504088896340736f, kRoot = 1.59576912160573071176f, kCube = 0.044715f;
   const float z2 = z * z;
   const float k = gelu ? kRoot * z * (1.0f + kCube * z2) : z;
-  const float dk = gelu ? kRoot * (1.0f + 3.0f * kCube * z2) : 1.0f;
-  const float e = __builtin_amdgcn_exp2f(-fabsf(k) * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
-  const float s = k >= 0.0f ? r : (k < 0.0f ? er : k);  // NaN stays
-  const float both = r * er;                            // sigma (1 - sigma)
-  // where that is 0 the slope is sigma, whatever z dk is
-  return Act{z * s, s + (both == 0.0f ? 0.0f : z * both * dk)};
+  const float e = __builtin_amdgcn_exp2f(-k * kLog2e), s = __builtin_amdgcn_rcpf(1.0f + e);
+  float more = z * (s * (s * e));
+  if (gelu) more *= kRoot * (1.0f + 3.0f * kCube * z2);
+  // both ends, where the factors are 0 and infinite: sigma (1 - sigma) is 0
+  if (s == 0.0f || e == 0.0f) more = 0.0f;
+  return Act{z * s, s + more};
 }
 
 // What becomes of g and u.
@@ -62,10 +69,6 @@ struct Finish {
   int64_t half;      // F filled up to a multiple of 32
 };
 
-__device__ __forceinline__ u32x4 eight_bf16(const float* v) {
-  return u32x4{two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7])};
-}
-
 // 8 values to p, of which `left` exist.
 __device__ __forceinline__ void put_eight(uint16_t* p, u32x4 v, int64_t left) {
   if (left >= 8) {
@@ -77,41 +80,58 @@ __device__ __forceinline__ void put_eight(uint16_t* p, u32x4 v, int64_t left) {
     if (j < left) p[j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
 }
 
+// g, u -> h of 8 columns.
+__device__ __forceinline__ u32x4 eight_out(int32_t gelu, f32x4v g0, f32x4v g1, f32x4v u0, f32x4v u1) {
+  float h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = act_value(j < 4 ? g0[j & 3] : g1[j & 3], gelu) * (j < 4 ? u0[j & 3] : u1[j & 3]);
+  return u32x4{two_bf16(h[0], h[1]), two_bf16(h[2], h[3]), two_bf16(h[4], h[5]), two_bf16(h[6], h[7])};
+}
+__device__ __forceinline__ u32x4 eight_bf16(f32x4v lo, f32x4v hi) {
+  return u32x4{two_bf16(lo[0], lo[1]), two_bf16(lo[2], lo[3]), two_bf16(hi[0], hi[1]), two_bf16(hi[2], hi[3])};
+}
+// g, u, dh (bf16) -> dg and du of 8 columns, of which `left` exist: zeros for the
+// rest, which fill up k.
+__device__ __forceinline__ void eight_dgates(int32_t gelu, f32x4v g0, f32x4v g1, f32x4v u0, f32x4v u1, u32x4 d,
+                                             int64_t left, u32x4* dg, u32x4* du) {
+  float a[8], b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float dh = (j & 1) ? high_bf16(d[j >> 1]) : low_bf16(d[j >> 1]);
+    const Act act = activate(j < 4 ? g0[j & 3] : g1[j & 3], gelu);
+    a[j] = dh * (j < 4 ? u0[j & 3] : u1[j & 3]) * act.slope;
+    b[j] = dh * act.value;
+  }
+  if (left < 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j >= left) a[j] = b[j] = 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    (*dg)[j] = two_bf16(a[2 * j], a[2 * j + 1]);
+    (*du)[j] = two_bf16(b[2 * j], b[2 * j + 1]);
+  }
+}
+
 // Columns n .. n + 7 of row m, which exists.
 __device__ __forceinline__ void finish(const Finish& f, int64_t m, int64_t n, f32x4v g0, f32x4v g1, f32x4v u0,
                                        f32x4v u1) {
   const int64_t left = f.cols - n;
-  float a[8], b[8];
   if (f.dout == nullptr) {
     if (left <= 0) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = activate(j < 4 ? g0[j & 3] : g1[j & 3], f.gelu).value * (j < 4 ? u0[j & 3] : u1[j & 3]);
-    }
-    put_eight(f.out + m * f.out_ld + n, eight_bf16(a), left);
+    put_eight(f.out + m * f.out_ld + n, eight_out(f.gelu, g0, g1, u0, u1), left);
     if (f.gates == nullptr) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = j < 4 ? g0[j & 3] : g1[j & 3];
-      b[j] = j < 4 ? u0[j & 3] : u1[j & 3];
-    }
-    put_eight(f.gates + m * f.gates_ld + n, eight_bf16(a), left);
-    put_eight(f.gates + m * f.gates_ld + f.cols + n, eight_bf16(b), left);
+    put_eight(f.gates + m * f.gates_ld + n, eight_bf16(g0, g1), left);
+    put_eight(f.gates + m * f.gates_ld + f.cols + n, eight_bf16(u0, u1), left);
     return;
   }
   if (n >= f.half) return;
-  const u32x4 d = eight_of(f.dout + m * f.dout_ld + n, left);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float dh = (j & 1) ? high_bf16(d[j >> 1]) : low_bf16(d[j >> 1]);
-    const Act act = activate(j < 4 ? g0[j & 3] : g1[j & 3], f.gelu);
-    // columns that fill up k are 0
-    a[j] = j < left ? dh * (j < 4 ? u0[j & 3] : u1[j & 3]) * act.slope : 0.0f;
-    b[j] = j < left ? dh * act.value : 0.0f;
-  }
+  u32x4 dg, du;
+  eight_dgates(f.gelu, g0, g1, u0, u1, eight_of(f.dout + m * f.dout_ld + n, left), left, &dg, &du);
   uint16_t* p = f.dgates + m * 2 * f.half + n;
-  *reinterpret_cast<u32x4*>(p) = eight_bf16(a);
-  *reinterpret_cast<u32x4*>(p + f.half) = eight_bf16(b);
+  *reinterpret_cast<u32x4*>(p) = dg;
+  *reinterpret_cast<u32x4*>(p + f.half) = du;
 }
 
 // ------------------------------------------------------------ g and u
@@ -126,14 +146,19 @@ struct GatedArgs {
   Finish f;
 };
 
-template <int SIDE, int WM, int WN>
+// A lane's columns of both products lie side by side in its accumulators (Form::kPair):
+// the epilogue takes no LDS, its stores are 16 bytes a lane, 64 a row, from one
+// shared address and the lane's offset, and dh's rows are asked for before the
+// first is used.  GRAD: dg and du instead of h.
+template <bool GRAD, int SIDE, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void gated_kernel(GatedArgs a) {
-  using G = Gemm<Form::kRows, Form::kPair, Code::kE4m3, SIDE, SIDE, WM, WN>;
+  using G = Gemm<Form::kRows, Form::kPair, Code::kE4m3, SIDE, SIDE, WM, WN, false, true>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
   __shared__ uint32_t turn;
+  static_assert(G::kFN == 4 && SIDE / WN == 64, "8 columns a lane");
   Queue q;
   uint32_t item = blockIdx.x;
   if (a.queue) item = first_item(q, a.queue, a.cut.items, &turn);
@@ -150,35 +175,64 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void gated_kernel(GatedArgs a) {
     slot = p.slot;
     g.open(a.x, a.w, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
   };
+  const int32_t gelu = a.f.gelu;
   open(item);
   while (item != kNoItem) {
     g.loop(lds0, lds1, lds2, lds3);
     const uint32_t k = a.queue ? q.ask() : 0;
-    const int64_t m1 = m0, n1 = n0, s1 = slot;
-    auto halfway = [&] {
-      item = a.queue ? next_item(q, k, &turn) : kNoItem;
-      if (item != kNoItem) open(item);
-    };
-    if (s1 >= 0) {
-      float* to = a.partial + s1 * SIDE * SIDE;
-      g.each_pair(
-          lds3,
-          [&](int r, int c, f32x4v g0, f32x4v g1, f32x4v u0, f32x4v u1) {
-            if (m1 + r >= a.f.rows) return;
-            float* p = to + r * SIDE + c;
-            *reinterpret_cast<f32x4v*>(p) = g0;
-            *reinterpret_cast<f32x4v*>(p + 4) = g1;
-            *reinterpret_cast<f32x4v*>(p + SIDE / 2) = u0;
-            *reinterpret_cast<f32x4v*>(p + SIDE / 2 + 4) = u1;
-          },
-          halfway);
-    } else {
-      g.each_pair(
-          lds3,
-          [&](int r, int c, f32x4v g0, f32x4v g1, f32x4v u0, f32x4v u1) {
-            if (m1 + r < a.f.rows) finish(a.f, m1 + r, n1 + c, g0, g1, u0, u1);
-          },
-          halfway);
+    const int64_t s1 = slot;
+    // this wave's part of the tile: rows from m1, 16 at a time, columns from n1; this lane's row and columns of it
+    const int64_t m1 = m0 + g.wm * (SIDE / WM), n1 = n0 + g.wn * 32;
+    g.renew_lane();
+    const uint32_t row = g.lane & 15, col = uint32_t(g.lane >> 4) * 8;
+    const int64_t left = a.f.cols - n1 - col, rows = a.f.rows - m1 - row;
+    u32x4 d[GRAD ? G::kFM : 1];
+    if constexpr (GRAD) {
+      if (s1 < 0) {
+        const uint16_t* from = a.f.dout + m1 * a.f.dout_ld + n1;
+        uint32_t at = row * uint32_t(a.f.dout_ld) + col;
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i) {
+          d[i] = u32x4{0, 0, 0, 0};
+          if (16 * i < rows) d[i] = eight_of(from + at, left);
+          at += 16 * uint32_t(a.f.dout_ld);
+        }
+      }
+    }
+    // the rows come in order, and the places go on with them
+    const uint32_t ld = GRAD ? uint32_t(2 * a.f.half) : uint32_t(a.f.out_ld);
+    uint16_t* const to = GRAD ? a.f.dgates + m1 * 2 * a.f.half + n1 : a.f.out + m1 * a.f.out_ld + n1;
+    uint16_t* const kept = a.f.gates + m1 * a.f.gates_ld + n1;
+    uint32_t at = row * ld + col, kept_at = row * uint32_t(a.f.gates_ld) + col;
+#pragma unroll
+    for (int i = 0; i < G::kFM; ++i) {
+      const f32x4v g0 = g.acc[i][0], g1 = g.acc[i][1], u0 = g.acc[i][2], u1 = g.acc[i][3];
+      if (s1 >= 0) {
+        float* p = a.partial + s1 * SIDE * SIDE + (g.wm * (SIDE / WM) + 16 * i + row) * SIDE + g.wn * 32 + col;
+        *reinterpret_cast<f32x4v*>(p) = g0;
+        *reinterpret_cast<f32x4v*>(p + 4) = g1;
+        *reinterpret_cast<f32x4v*>(p + SIDE / 2) = u0;
+        *reinterpret_cast<f32x4v*>(p + SIDE / 2 + 4) = u1;
+      } else if constexpr (GRAD) {
+        if (16 * i < rows && col + n1 < a.f.half) {
+          u32x4 dg, du;
+          eight_dgates(gelu, g0, g1, u0, u1, d[i], left, &dg, &du);
+          *reinterpret_cast<u32x4*>(to + at) = dg;
+          *reinterpret_cast<u32x4*>(to + a.f.half + at) = du;
+        }
+      } else if (16 * i < rows && left > 0) {
+        put_eight(to + at, eight_out(gelu, g0, g1, u0, u1), left);
+        if (a.f.gates) {
+          put_eight(kept + kept_at, eight_bf16(g0, g1), left);
+          put_eight(kept + a.f.cols + kept_at, eight_bf16(u0, u1), left);
+        }
+      }
+      at += 16 * ld;
+      kept_at += 16 * uint32_t(a.f.gates_ld);
+      if (i == G::kFM / 2 - 1) {
+        item = a.queue ? next_item(q, k, &turn) : kNoItem;
+        if (item != kNoItem) open(item);
+      }
     }
   }
 }
@@ -308,7 +362,7 @@ __device__ __forceinline__ uint32_t grad_tile(const GradArgs& a, uint32_t tile, 
 
 template <Form FA, Form FB, int SIDE, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void gated_grad_kernel(GradArgs a) {
-  using G = Gemm<FA, FB, Code::kE4m3, SIDE, SIDE, WM, WN>;
+  using G = Gemm<FA, FB, Code::kE4m3, SIDE, SIDE, WM, WN, false, FB == Form::kStack>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
@@ -339,7 +393,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void gated_grad_kernel(GradArgs a) 
     const uint32_t k = a.queue ? q.ask() : 0;
     const Target t = slot >= 0 ? slot_target<SIDE>(a.partial, slot, a.to[0].rows - m0) : second ? a.to[1] : a.to[0];
     const int64_t m1 = slot >= 0 ? 0 : m0, n1 = slot >= 0 ? 0 : n0;
-    g.write(t, m1, n1, lds3, [&] {
+    g.write_rows(t, m1, n1, lds3, [&] {
       item = a.queue ? next_item(q, k, &turn) : kNoItem;
       if (item != kNoItem) open(item);
     });
@@ -403,7 +457,7 @@ constexpr uint32_t kProducts = 3;  // g and u; dx; dWg and dWu
 // Where one call's workspace keeps what.
 struct Layout {
   bool few = false, copy_x = false, copy_w = false, gates = false;  // gates: g and u are formed
-  int64_t ld = 0, half = 0;
+  int64_t ld = 0, half = 0, depth = 0;
   Tiling fwd, dx, dw;
   bool queued = false;
   // byte offsets
@@ -416,11 +470,14 @@ Layout layout_of(const GatedCall& c) {
   L.few = c.tokens <= kFew;
   L.half = up(c.ffn, 32);
   L.ld = up(c.hidden, 64);
-  // Tiles read rows that start and end on 16 bytes; dx reads the weights one behind the other.
+  L.depth = up(c.hidden, kBK);
+  // Tiles read rows that start and end on 16 bytes, of whole steps of k (copies are
+  // filled up with zeros); dx reads the weights one behind the other.
   const bool tiles = c.grad || !L.few;
-  const bool w_aligned = rows_aligned(c.w_gate, c.gate_ld, c.hidden) && rows_aligned(c.w_up, c.up_ld, c.hidden) &&
+  const bool steps = !(L.gates && !L.few) || c.hidden % kBK == 0;
+  const bool w_aligned = steps && rows_aligned(c.w_gate, c.gate_ld, c.hidden) && rows_aligned(c.w_up, c.up_ld, c.hidden) &&
                          c.gate_ld == c.up_ld;
-  L.copy_x = tiles && !rows_aligned(c.x, c.x_ld, c.hidden);
+  L.copy_x = tiles && !(steps && rows_aligned(c.x, c.x_ld, c.hidden));
   L.copy_w = tiles && (!w_aligned || (c.grad && c.ffn % kBK != 0));
   int64_t at = 0, partial = 0;
   auto take = [&](int64_t n) {
@@ -557,7 +614,7 @@ int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
     GatedArgs a;
     a.x = x;
     a.w = w;
-    a.depth = c.hidden;
+    a.depth = L.depth;
     a.cut = L.fwd.cut;
     a.partial = partial;
     a.tiles_m = uint32_t(L.fwd.tiles_m);
@@ -567,11 +624,17 @@ int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
     const dim3 grid(resident_groups(a.cut.items, L.fwd.side));
     const unsigned rest = a.cut.tiles - a.cut.full;
     if (L.fwd.side == 256) {
-      hipLaunchKernelGGL((gated_kernel<256, 2, 4>), grid, dim3(512), 0, st, a);
+      if (c.grad)
+        hipLaunchKernelGGL((gated_kernel<true, 256, 2, 4>), grid, dim3(512), 0, st, a);
+      else
+        hipLaunchKernelGGL((gated_kernel<false, 256, 2, 4>), grid, dim3(512), 0, st, a);
       TIDE_LAUNCHED();
       if (a.cut.splits > 1) hipLaunchKernelGGL(join_gated_kernel<256>, dim3(rest * 16), dim3(256), 0, st, a);
     } else {
-      hipLaunchKernelGGL((gated_kernel<128, 2, 2>), grid, dim3(256), 0, st, a);
+      if (c.grad)
+        hipLaunchKernelGGL((gated_kernel<true, 128, 2, 2>), grid, dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((gated_kernel<false, 128, 2, 2>), grid, dim3(256), 0, st, a);
       TIDE_LAUNCHED();
       if (a.cut.splits > 1) hipLaunchKernelGGL(join_gated_kernel<128>, dim3(rest * 4), dim3(256), 0, st, a);
     }

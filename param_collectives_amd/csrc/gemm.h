@@ -44,6 +44,7 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2v __attribute__((ext_vector_type(2)));
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -201,8 +202,12 @@ struct Side {
     uint32_t scale[kPacked ? kParts : 1];
   };
 
+  // (kPair: a fragment's rows 4 b .. 4 b + 3 are the tile's 8 b .. 8 b + 3, or the
+  // four after them, so that a lane holds 8 neighbouring columns of C; the swizzle
+  // goes with the fragment's rows.)
+  static __device__ __forceinline__ int swizzle(int r) { return row_swizzle(kPair ? r >> 1 : r); }
   static __device__ __forceinline__ int part_k(int lin) {
-    return kAlong ? ((lin & 3) ^ row_swizzle(lin >> 2)) * 8 : lin / (kPacked ? ROWS / 16 : kRowChunks);
+    return kAlong ? ((lin & 3) ^ swizzle(lin >> 2)) * 8 : lin / (kPacked ? ROWS / 16 : kRowChunks);
   }
 
   __device__ __forceinline__ void init(const Operand& o, int64_t first, int tid) {
@@ -313,8 +318,8 @@ struct Side {
   static constexpr int kSpots = kAlong || LEAN ? 1 : FRAGS;
   static __device__ __forceinline__ void spots(uint32_t* at, int r0, int lane) {
     if constexpr (kAlong) {
-      const int r = (kPair ? r0 / 2 : r0) + (lane & 15);
-      at[0] = uint32_t((r * kRowChunks + ((lane >> 4) ^ row_swizzle(r))) * 16);
+      const int r = kPair ? r0 / 2 + 2 * (lane & 12) + (lane & 3) : r0 + (lane & 15);
+      at[0] = uint32_t((r * kRowChunks + ((lane >> 4) ^ swizzle(r))) * 16);
     } else {
       // a transposing read gives lane l of 16 the values of column l in the
       // four rows k of which lanes 4j .. 4j+3 point at 4 columns each
@@ -328,10 +333,12 @@ struct Side {
   static __device__ __forceinline__ uint32_t spot(uint32_t first, int i) { return first ^ uint32_t(i * 32); }
 
   // Fragment i: rows (columns) 16 i + 0..15, k = 8 (lane / 16) + 0..7.  (kPair: the
-  // second half of the fragments are the second matrix's.)
+  // second half of the fragments are the second matrix's, and of 32 rows two
+  // fragments have every other four.)
   static __device__ __forceinline__ bf16x8 fragment(const char* lds, uint32_t* at, int i) {
     if constexpr (kAlong) {
-      const int r = kPair && i >= FRAGS / 2 ? ROWS / 2 + (i - FRAGS / 2) * 16 : i * 16;
+      constexpr int kHalf = FRAGS / 2;
+      const int j = kPair ? i % kHalf : i, r = kPair ? i / kHalf * (ROWS / 2) + j / 2 * 32 + j % 2 * 4 : j * 16;
       return *reinterpret_cast<const bf16x8*>(lds + renew(at[0]) + r * kRowChunks * 16);
     } else {
       // rows k and k + 4 share their swizzle
@@ -352,7 +359,10 @@ __device__ __forceinline__ uint32_t bf16_bits_of(float v) {
   __builtin_memcpy(&r, &b, 2);
   return r;
 }
-__device__ __forceinline__ uint32_t two_bf16(float a, float b) { return bf16_bits_of(a) | bf16_bits_of(b) << 16; }
+// (One instruction for both.)
+__device__ __forceinline__ uint32_t two_bf16(float a, float b) {
+  return bf16x2_as_bits(__builtin_convertvector((f32x2v{a, b}), bf16x2));
+}
 __device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 __device__ __forceinline__ f32x4v add4(f32x4v a, f32x4v b) {
@@ -460,8 +470,10 @@ __device__ __forceinline__ void lds_barrier() {
 // that step i + 3 goes to.  (Packed codes are loaded 4 steps ahead into
 // registers and written to LDS 2 steps ahead.)  The whole steps are filled up
 // to a multiple of 4 with empty ones, which go first; a short last step goes
-// before them all, from the last stage.
-template <Form FA, Form FB, Code CODE, int BM, int BN, int WM, int WN, bool F16 = false>
+// before them all, from the last stage.  WHOLE: there is never a short one (the
+// second place where sums are formed costs registers: without it the sums of a
+// 256 x 256 tile of two kRows sides are not spilled).
+template <Form FA, Form FB, Code CODE, int BM, int BN, int WM, int WN, bool F16 = false, bool WHOLE = false>
 struct Gemm {
   static constexpr int kThreads = WM * WN * 64;
   static constexpr int kFM = BM / WM / 16, kFN = BN / WN / 16;  // fragments of a wave
@@ -497,6 +509,10 @@ struct Gemm {
     SB::spots(at_b, wn * (BN / WN), lane);
   }
 
+  // What an epilogue computes from the lane from here on is not worked out before
+  // the sums, whose registers it would take.
+  __device__ __forceinline__ void renew_lane() { asm("" : "+v"(lane)); }
+
   static __device__ __forceinline__ f32x4v product(bf16x8 n, bf16x8 m, f32x4v sum) {
     if constexpr (F16)
       return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, n), __builtin_bit_cast(f16x8, m), sum, 0, 0,
@@ -525,7 +541,7 @@ struct Gemm {
     sb.init(b, n0, tid);
     first = k_first / kBK;
     whole = k_end > k_first ? k_end / kBK : first;
-    left = k_end > k_first ? int(k_end - whole * kBK) : 0;
+    left = !WHOLE && k_end > k_first ? int(k_end - whole * kBK) : 0;
     rounds = (whole - first + 3) / 4;
     s = whole - rounds * 4;
     if (rounds == 0) return;
@@ -632,7 +648,7 @@ struct Gemm {
     // every first load on its way before the first is waited for
     typename SA::Held ta, ea[2];
     typename SB::Held tb, eb[2];
-    if (left) {
+    if (!WHOLE && left) {
       lds_barrier();  // the last stage may have served an epilogue
       sa.template fetch<true>(l3, ta, whole, left, tid);
       sb.template fetch<true>(l3 + SA::kBytes, tb, whole, left, tid);
@@ -643,7 +659,7 @@ struct Gemm {
 #pragma unroll
       for (int i = 0; i < 2; ++i) codes_early(2 + i, ha[i], hb[i]);
     }
-    if (left) {
+    if (!WHOLE && left) {
       sa.settle(l3, ta);
       sb.settle(l3 + SA::kBytes, tb);
     }
@@ -659,7 +675,7 @@ struct Gemm {
       for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
     wait_loads<0, true>();
     bare_barrier();
-    if (left) {
+    if (!WHOLE && left) {
       begin(l3);
       multiply(l3, l3, false, [](int) {}, [](int) {});
     }
@@ -721,57 +737,75 @@ struct Gemm {
     }
   }
 
-  // The same where B is a pair: f(row, column, 8 values of the first matrix, and
-  // those of the second), columns counted in the half tile.
-  template <typename F, typename H>
-  __device__ __forceinline__ void each_pair(char* lds, F f, H halfway) {
-    constexpr int kCols = BN / WN, kQuads = kCols / 4, kMask = kQuads - 1, kGroups = kCols / 16;
-    static_assert(FB == Form::kPair && 16 * kGroups % 64 == 0 && WM * WN * 16 * kCols * 4 <= kStage, "epilogue rows");
+  // f(row, values of 8 columns) for every group of eight this wave holds, 8 rows
+  // at a time: the group is column() of row `row` + lane / 8, `row` the same for
+  // all lanes, so that addresses take one scalar addition.  before(i) comes two
+  // calls of f ahead of the 2 i-th.
+  static constexpr int kRowGroups = BN / WN / 8;
+  static_assert(64 % kRowGroups == 0, "groups of a row");
+  __device__ __forceinline__ int column() const { return wn * (BN / WN) + lane % kRowGroups * 8; }
+  template <typename P, typename F, typename H>
+  __device__ __forceinline__ void each_rows(char* lds, P before, F f, H halfway) {
+    constexpr int kCols = BN / WN, kMask = kCols / 4 - 1, kRows = 64 / kRowGroups;
+    static_assert(WM * WN * 16 * kCols * 4 <= kStage, "epilogue rows");
     float* rows = reinterpret_cast<float*>(lds) + wave_index() * 16 * kCols;
+    const int w = lane & 15, c = lane % kRowGroups;
+    before(0);
 #pragma unroll
     for (int i = 0; i < kFM; ++i) {
-      const int w = lane & 15;
 #pragma unroll
       for (int j = 0; j < kFN; ++j)
         *reinterpret_cast<f32x4v*>(rows + w * kCols + ((4 * j + (lane >> 4)) ^ (w & kMask)) * 4) = acc[i][j];
+      if (i + 1 < kFM) before(i + 1);
       wave_order();
 #pragma unroll
-      for (int q = lane; q < 16 * kGroups; q += 64) {
-        const int r = q / kGroups, c = q % kGroups;
-        auto quad = [&](int k) { return *reinterpret_cast<const f32x4v*>(rows + r * kCols + (k ^ (r & kMask)) * 4); };
-        f(wm * (BM / WM) + i * 16 + r, wn * (kCols / 2) + c * 8, quad(2 * c), quad(2 * c + 1), quad(kQuads / 2 + 2 * c),
-          quad(kQuads / 2 + 2 * c + 1));
+      for (int q = 0; q < 16 / kRows; ++q) {
+        const int r = q * kRows + lane / kRowGroups;
+        f(wm * (BM / WM) + i * 16 + q * kRows, i, q,
+          *reinterpret_cast<const f32x4v*>(rows + r * kCols + ((2 * c) ^ (r & kMask)) * 4),
+          *reinterpret_cast<const f32x4v*>(rows + r * kCols + ((2 * c + 1) ^ (r & kMask)) * 4));
       }
       wave_order();
       if (i == kFM / 2 - 1) halfway();
     }
   }
 
-  // each(), and with `mirror` also t(column, row, values of 8 rows from that one)
-  // for every group of eight in a column.
-  template <typename F, typename T, typename H>
-  __device__ __forceinline__ void each_mirrored(char* lds, bool mirror, F f, T t, H halfway) {
-    constexpr int kCols = BN / WN, kQuads = kCols / 4, kMask = kQuads - 1, kGroups = kCols / 8;
-    static_assert(WM * WN * 16 * kCols * 4 <= kStage && 16 * kGroups % 64 == 0, "epilogue rows");
+  // The same, where f may change the values; with `mirror` also t(row, values of 8
+  // rows of a column) of the changed values: rows `row` + 0..7 or, in the odd lanes,
+  // 8..15, of column mirror_column() (+ 32 in the second call).
+  __device__ __forceinline__ int mirror_column() const { return wn * (BN / WN) + (lane >> 1); }
+  template <typename P, typename F, typename T, typename H>
+  __device__ __forceinline__ void each_mirrored(char* lds, bool mirror, P before, F f, T t, H halfway) {
+    constexpr int kCols = BN / WN, kMask = kCols / 4 - 1, kRows = 64 / kRowGroups;
+    static_assert(kCols == 64 && WM * WN * 16 * kCols * 4 <= kStage, "epilogue rows");
     float* rows = reinterpret_cast<float*>(lds) + wave_index() * 16 * kCols;
+    const int w = lane & 15, c = lane % kRowGroups;
+    before(0);
 #pragma unroll
     for (int i = 0; i < kFM; ++i) {
-      const int w = lane & 15;
 #pragma unroll
       for (int j = 0; j < kFN; ++j)
         *reinterpret_cast<f32x4v*>(rows + w * kCols + ((4 * j + (lane >> 4)) ^ (w & kMask)) * 4) = acc[i][j];
+      if (i + 1 < kFM) before(i + 1);
       wave_order();
-#pragma unroll 1
-      for (int q = lane; q < 16 * kGroups; q += 64) {
-        const int r = q / kGroups, c = q % kGroups;
-        f(wm * (BM / WM) + i * 16 + r, wn * kCols + c * 8,
-          *reinterpret_cast<const f32x4v*>(rows + r * kCols + ((2 * c) ^ (r & kMask)) * 4),
-          *reinterpret_cast<const f32x4v*>(rows + r * kCols + ((2 * c + 1) ^ (r & kMask)) * 4));
+#pragma unroll
+      for (int q = 0; q < 16 / kRows; ++q) {
+        const int r = q * kRows + lane / kRowGroups;
+        f32x4v* p0 = reinterpret_cast<f32x4v*>(rows + r * kCols + ((2 * c) ^ (r & kMask)) * 4);
+        f32x4v* p1 = reinterpret_cast<f32x4v*>(rows + r * kCols + ((2 * c + 1) ^ (r & kMask)) * 4);
+        f32x4v lo = *p0, hi = *p1;
+        f(wm * (BM / WM) + i * 16 + q * kRows, i, q, lo, hi);
+        if (mirror) {
+          *p0 = lo;
+          *p1 = hi;
+        }
       }
+      wave_order();
       if (mirror) {
-#pragma unroll 1
-        for (int q = lane; q < kCols * 2; q += 64) {
-          const int n = q >> 1, r0 = (q & 1) * 8;
+        const int r0 = (lane & 1) * 8;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int n = (lane >> 1) + 32 * q;
           f32x4v lo, hi;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -781,12 +815,51 @@ struct Gemm {
             else
               hi[j & 3] = v;
           }
-          t(wn * kCols + n, wm * (BM / WM) + i * 16 + r0, lo, hi);
+          t(wm * (BM / WM) + i * 16, q, lo, hi);
         }
+        wave_order();
       }
-      wave_order();
       if (i == kFM / 2 - 1) halfway();
     }
+  }
+
+  // Writes the tile at (m0, n0) to `t`, which has no row map, adds nothing and takes
+  // the sums as they are: as write(), with fewer instructions.
+  template <typename H>
+  __device__ __forceinline__ void write_rows(const Target& t, int64_t m0, int64_t n0, char* lds, H halfway) {
+    const int64_t n1 = n0 + column(), left = t.cols - n1;
+    const uint32_t row = lane / kRowGroups, ld = uint32_t(t.ld);
+    // the rows come in order: the place goes on with them (a product for each row's
+    // would be worked out for all of them beforehand, and spilled)
+    uint32_t at = (wm * (BM / WM) + row) * ld + uint32_t(column());
+    const int64_t first = m0 * t.ld + n0;
+    const int64_t rows = t.rows - m0 - row;
+    each_rows(
+        lds, [](int) {},
+        [&](int r, int, int, f32x4v lo, f32x4v hi) {
+          const uint32_t here = at;
+          at += (64 / kRowGroups) * ld;
+          if (r >= rows || left <= 0) return;
+          if (left < 8) return put_some(t, m0 + r + row, n1, lo, hi);
+          if (t.f32) {
+            any_f32x4* d = reinterpret_cast<any_f32x4*>(static_cast<float*>(t.base) + first + here);
+            if (t.accumulate) {
+              lo = add4(d[0], lo);
+              hi = add4(d[1], hi);
+            }
+            d[0] = lo;
+            d[1] = hi;
+          } else {
+            any_u32x4* d = reinterpret_cast<any_u32x4*>(static_cast<uint16_t*>(t.base) + first + here);
+            if (t.accumulate) {
+              const u32x4 o = *d;
+              lo = add4(f32x4v{low_bf16(o[0]), high_bf16(o[0]), low_bf16(o[1]), high_bf16(o[1])}, lo);
+              hi = add4(f32x4v{low_bf16(o[2]), high_bf16(o[2]), low_bf16(o[3]), high_bf16(o[3])}, hi);
+            }
+            *d = u32x4{two_bf16(lo[0], lo[1]), two_bf16(lo[2], lo[3]), two_bf16(hi[0], hi[1]), two_bf16(hi[2], hi[3])};
+          }
+        },
+        halfway);
   }
 
   // Writes the tile at (m0, n0) to `t`.

@@ -35,33 +35,27 @@ constexpr float kRest = 2048.0f;        // and the rest of a rounding times this
 constexpr int64_t kMost = 64;           // matrices of a piece, whose addresses go with the launch
 constexpr int64_t kSumBlocks = 256;     // workgroups that share a matrix's norm, at most
 
-__device__ __forceinline__ uint32_t f16_bits(float v) {
-  const _Float16 h = _Float16(v);
-  uint16_t r;
-  __builtin_memcpy(&r, &h, 2);
-  return r;
+typedef float f32x8v __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ u32x4 eight_f16(f32x8v v) { return __builtin_bit_cast(u32x4, __builtin_convertvector(v, f16x8)); }
+__device__ __forceinline__ f32x8v f16_values(u32x4 v) {
+  return __builtin_convertvector(__builtin_bit_cast(f16x8, v), f32x8v);
 }
-__device__ __forceinline__ float f16_value(uint32_t bits) {
-  const uint16_t b = uint16_t(bits);
-  _Float16 h;
-  __builtin_memcpy(&h, &b, 2);
-  return float(h);
-}
-__device__ __forceinline__ float f16_at(const u32x4& v, int j) { return f16_value(v[j >> 1] >> (16 * (j & 1))); }
-__device__ __forceinline__ u32x4 eight_f16(const float* v) {
-  u32x4 r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = f16_bits(v[2 * j]) | f16_bits(v[2 * j + 1]) << 16;
-  return r;
+__device__ __forceinline__ f32x8v join_quads(f32x4v lo, f32x4v hi) {
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 // Eight values and the rests of their roundings.
-__device__ __forceinline__ void split_eight(const float* v, u32x4* hi, u32x4* lo) {
+__device__ __forceinline__ void split_eight(f32x8v v, u32x4* hi, u32x4* lo) {
   *hi = eight_f16(v);
-  float rest[8];
+  const f32x8v h = f16_values(*hi);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) rest[j] = (v[j] - f16_at(*hi, j)) * kRest;
-  *lo = eight_f16(rest);
+  for (int j = 0; j < 8; ++j) v[j] = (v[j] - h[j]) * kRest;
+  *lo = eight_f16(v);
 }
+
+// Rows and columns of the workspace's matrices are filled up with zeros to a
+// multiple of this, the k of a step.
+__host__ __device__ __forceinline__ int64_t padded(int64_t n) { return (n + kBK - 1) / kBK * kBK; }
 
 struct Pointers {
   void* p[kMost];
@@ -83,7 +77,8 @@ struct StartArgs {
 };
 
 // 8 values of a row from column c, as fp32; zeros past its end.
-__device__ __forceinline__ void eight_values(const StartArgs& a, const void* x, int64_t r, int64_t c, float* v) {
+__device__ __forceinline__ f32x8v eight_values(const StartArgs& a, const void* x, int64_t r, int64_t c) {
+  f32x8v v;
   const int64_t left = a.cols - c;
   if (a.f32) {
     const float* p = static_cast<const float*>(x) + r * a.ld + c;
@@ -100,6 +95,7 @@ __device__ __forceinline__ void eight_values(const StartArgs& a, const void* x, 
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (j & 1) ? high_bf16(w[j >> 1]) : low_bf16(w[j >> 1]);
   }
+  return v;
 }
 
 // The sum of squares of a workgroup's share of matrix blockIdx.y.  Clears the
@@ -114,8 +110,7 @@ __global__ __launch_bounds__(256) void square_sums_kernel(StartArgs a) {
   double s = 0;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
     const int64_t r = i / groups;
-    float v[8];
-    eight_values(a, x, r, (i - r * groups) * 8, v);
+    const f32x8v v = eight_values(a, x, r, (i - r * groups) * 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += double(v[j]) * double(v[j]);
   }
@@ -126,7 +121,7 @@ __global__ __launch_bounds__(256) void square_sums_kernel(StartArgs a) {
   if (threadIdx.x == 0) a.sums[blockIdx.y * gridDim.x + blockIdx.x] = part[0] + part[1] + part[2] + part[3];
 }
 
-// X over its norm, times kUnit, in two fp16; zeros to the row's pitch.  The
+// X over its norm, times kUnit, in two fp16; zeros around it.  The
 // product is taken in fp64: the factor may lie outside fp32's range.
 __global__ __launch_bounds__(256) void normalize_kernel(StartArgs a, int32_t blocks) {
   __shared__ double factor;
@@ -140,13 +135,13 @@ __global__ __launch_bounds__(256) void normalize_kernel(StartArgs a, int32_t blo
   __syncthreads();
   const double f = factor;
   const void* x = a.x.p[blockIdx.y];
-  const int64_t groups = a.pitch / 8, all = a.rows * groups;
+  const int64_t groups = a.pitch / 8, all = padded(a.rows) * groups;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
     const int64_t r = i / groups, c = (i - r * groups) * 8;
-    float v[8];
-    eight_values(a, x, r, c, v);
+    f32x8v v = {};
+    if (r < a.rows) v = eight_values(a, x, r, c);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < a.cols ? float(double(v[j]) * f) : 0.0f;
+    for (int j = 0; j < 8; ++j) v[j] = r < a.rows && c + j < a.cols ? float(double(v[j]) * f) : 0.0f;
     u32x4 hi, lo;
     split_eight(v, &hi, &lo);
     const int64_t at = int64_t(blockIdx.y) * a.matrix + r * a.pitch + c;
@@ -167,24 +162,27 @@ struct SymmetricArgs {
   uint32_t tiles, side_tiles;  // of a matrix; on its side
   uint32_t* queue;
   const uint16_t* g;  // or null
-  uint16_t* out;      // size x size each, rows `ld` apart, `matrix` elements from one to the next
+  uint16_t* out;      // size x size each (columns to padded(size)), rows `ld` apart, `matrix` elements from one to the next
   int64_t size, ld, matrix;
   float alpha, beta, diagonal;
 
-  // 8 values of row m from column n, of a matrix.
-  __device__ __forceinline__ void put(int64_t z, int64_t m, int64_t n, f32x4v lo, f32x4v hi) const {
-    if (m >= size || n >= size) return;  // the pitch is a multiple of 8
-    const int64_t at = z * matrix + m * ld + n;
-    float v[8];
-    u32x4 old = u32x4{0, 0, 0, 0};
-    if (g) old = *reinterpret_cast<const u32x4*>(g + at);
+  // The values of 8 columns of row m from column n, whose G (if any) is `old`.
+  __device__ __forceinline__ f32x8v value(int64_t m, int64_t n, f32x4v lo, f32x4v hi, u32x4 old) const {
+    f32x8v v = join_quads(lo, hi);
+    const f32x8v o = f16_values(old);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = alpha * (j < 4 ? lo[j & 3] : hi[j & 3]) + beta * f16_at(old, j);
-      if (m == n + j) v[j] += diagonal;
-      if (n + j >= size) v[j] = 0.0f;
+    for (int j = 0; j < 8; ++j) v[j] = alpha * v[j] + (g ? beta * o[j] : 0.0f);
+    if (diagonal != 0.0f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (m == n + j) v[j] += diagonal;
     }
-    *reinterpret_cast<u32x4*>(out + at) = eight_f16(v);
+    if (n + 8 > size) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j >= size) v[j] = 0.0f;
+    }
+    return v;
   }
 };
 
@@ -202,7 +200,7 @@ __device__ __forceinline__ void symmetric_tile(const SymmetricArgs& a, uint32_t 
 
 template <Form F, int SIDE, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void symmetric_kernel(SymmetricArgs a) {
-  using G = Gemm<F, F, Code::kE4m3, SIDE, SIDE, WM, WN, true>;
+  using G = Gemm<F, F, Code::kE4m3, SIDE, SIDE, WM, WN, true, true>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
@@ -230,20 +228,54 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void symmetric_kernel(SymmetricArgs
   while (item != kNoItem) {
     g.loop(lds0, lds1, lds2, lds3);
     const uint32_t k = a.queue ? q.ask() : 0;
-    const int64_t m1 = m0, n1 = n0, z1 = z, s1 = slot;
-    auto halfway = [&] {
-      item = a.queue ? next_item(q, k, &turn) : kNoItem;
-      if (item != kNoItem) open(item);
+    const int64_t m1 = m0, n1 = n0, s1 = slot;
+    g.renew_lane();
+    const uint32_t row = g.lane / G::kRowGroups, ld = uint32_t(a.ld);
+    // the rows come in order, and the places go on with them
+    uint32_t at = (g.wm * (SIDE / WM) + row) * ld + uint32_t(g.column()), ahead = at;
+    const int64_t rows = a.size - m1 - row, left = padded(a.size) - n1 - g.column();
+    const int64_t first = z * a.matrix + m1 * a.ld + n1;
+    uint16_t* const mirrored = a.out + z * a.matrix + n1 * a.ld + m1;
+    // G's values of the rows that come next
+    u32x4 old[2][2];
+    auto before = [&](int i) {
+      if (a.g == nullptr || s1 >= 0) return;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int r = g.wm * (SIDE / WM) + i * 16 + q * 8;
+        if (r < rows && left > 0) old[i & 1][q] = *reinterpret_cast<const u32x4*>(a.g + first + ahead);
+        ahead += 8 * ld;
+      }
     };
+    // rows of the mirrored tile are this one's columns
+    const uint32_t m_at = uint32_t(g.mirror_column()) * ld + uint32_t(g.lane & 1) * 8;
+    const int64_t m_rows = a.size - n1 - g.mirror_column(), m_left = a.size - m1 - (g.lane & 1) * 8;
+    const int64_t m_pad = padded(a.size) - a.size;
     g.each_mirrored(
-        lds3, s1 < 0 && m1 != n1,
-        [&](int r, int c, f32x4v lo, f32x4v hi) {
-          if (s1 >= 0)
-            put_slot<SIDE>(a.partial, s1, r, c, lo, hi);
-          else
-            a.put(z1, m1 + r, n1 + c, lo, hi);
+        lds3, s1 < 0 && m1 != n1, before,
+        [&](int r, int i, int q, f32x4v& lo, f32x4v& hi) {
+          if (s1 >= 0) return put_slot<SIDE>(a.partial, s1, r + row, g.column(), lo, hi);
+          const f32x8v v = a.value(m1 + r + row, n1 + g.column(), lo, hi, a.g ? old[i & 1][q] : u32x4{0, 0, 0, 0});
+          if (r < rows && left > 0) *reinterpret_cast<u32x4*>(a.out + first + at) = eight_f16(v);
+          at += 8 * ld;
+          lo = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+          hi = __builtin_shufflevector(v, v, 4, 5, 6, 7);
         },
-        [&](int c, int r, f32x4v lo, f32x4v hi) { a.put(z1, n1 + c, m1 + r, lo, hi); }, halfway);
+        [&](int r, int q, f32x4v lo, f32x4v hi) {
+          f32x8v v = join_quads(lo, hi);
+          const int64_t some = m_left - r;  // the tile below this one's rows may end inside the group
+          if (some < 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j >= some) v[j] = 0.0f;
+          }
+          if (32 * q < m_rows && some > -m_pad)
+            *reinterpret_cast<u32x4*>(mirrored + r + (m_at + 32 * q * ld)) = eight_f16(v);
+        },
+        [&] {
+          item = a.queue ? next_item(q, k, &turn) : kNoItem;
+          if (item != kNoItem) open(item);
+        });
   }
 }
 
@@ -259,23 +291,27 @@ __global__ __launch_bounds__(256) void join_symmetric_kernel(SymmetricArgs a) {
   symmetric_tile(a, a.cut.full + r, &z, &tm, &tn);
   const int64_t m0 = int64_t(tm) * SIDE, n0 = int64_t(tn) * SIDE;
   const uint32_t row = threadIdx.x / 8, col = threadIdx.x % 8 * 8;
-  if (m0 + r0 >= a.size || n0 + c0 >= a.size) return;  // the whole part
-  f32x4v lo = f32x4v{0.f, 0.f, 0.f, 0.f}, hi = lo;
-  if (m0 + r0 + row < a.size) join_eight<SIDE>(a.partial, a.cut, r, r0 + row, c0 + col, &lo, &hi);
-  a.put(z, m0 + r0 + row, n0 + c0 + col, lo, hi);
+  if (m0 + r0 >= padded(a.size) || n0 + c0 >= padded(a.size)) return;  // the whole part
+  const int64_t m1 = m0 + r0 + row, n1 = n0 + c0 + col;
+  f32x8v v = {};
+  if (m1 < a.size && n1 < padded(a.size)) {
+    f32x4v lo, hi;
+    join_eight<SIDE>(a.partial, a.cut, r, r0 + row, c0 + col, &lo, &hi);
+    const int64_t at = z * a.matrix + m1 * a.ld + n1;
+    v = a.value(m1, n1, lo, hi, a.g ? *reinterpret_cast<const u32x4*>(a.g + at) : u32x4{0, 0, 0, 0});
+    *reinterpret_cast<u32x4*>(a.out + at) = eight_f16(v);
+  }
   if (tm == tn) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) values[row][col + j] = j < 4 ? lo[j & 3] : hi[j & 3];
+  for (int j = 0; j < 8; ++j) values[row][col + j] = v[j];
   __syncthreads();
   const uint32_t n = threadIdx.x / 4, m = threadIdx.x % 4 * 8;
+  const int64_t m2 = n0 + c0 + n, n2 = m0 + r0 + m;
+  if (m2 >= a.size || n2 >= padded(a.size)) return;
+  // (zeros where the rows of this part end)
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (j < 4)
-      lo[j & 3] = values[m + j][n];
-    else
-      hi[j & 3] = values[m + j][n];
-  }
-  a.put(z, n0 + c0 + n, m0 + r0 + m, lo, hi);
+  for (int j = 0; j < 8; ++j) v[j] = values[m + j][n];
+  *reinterpret_cast<u32x4*>(a.out + z * a.matrix + m2 * a.ld + n2) = eight_f16(v);
 }
 
 // ------------------------------------------------------------ P X
@@ -297,38 +333,48 @@ struct UpdateArgs {
   Pointers out;
   int64_t out_ld;
 
-  __device__ __forceinline__ void put(int64_t z, int64_t m, int64_t n, f32x4v l, f32x4v h) const {
-    if (m >= rows || n >= cols) return;
-    const int64_t at = z * matrix + m * ld + n;
-    float v[8];
+  // The next X times kUnit, of 8 columns, whose own X (if it is added here) is in
+  // two parts.
+  __device__ __forceinline__ f32x8v value(f32x4v l, f32x4v h, u32x4 x, u32x4 y) const {
+    f32x8v v = join_quads(l, h);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (j < 4 ? l[j & 3] : h[j & 3]) * (1.0f / kUnit);
+    for (int j = 0; j < 8; ++j) v[j] *= 1.0f / kUnit;
     if (hi) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(hi + at), y = *reinterpret_cast<const u32x4*>(lo + at);
+      const f32x8v a = f16_values(x), b = f16_values(y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = coefficient * (f16_at(x, j) + f16_at(y, j) * (1.0f / kRest)) + v[j];
+      for (int j = 0; j < 8; ++j) v[j] = coefficient * (a[j] + b[j] * (1.0f / kRest)) + v[j];
     }
+    return v;
+  }
+  // Its 8 columns, of which `left` exist (0 of a row that fills up), to places in
+  // next, lo or out.
+  __device__ __forceinline__ void put(f32x8v v, int64_t left, uint16_t* to_next, uint16_t* to_lo, uint16_t* to_out) const {
     if (next) {
+      if (left < 8) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (n + j >= cols) v[j] = 0.0f;
+        for (int j = 0; j < 8; ++j)
+          if (j >= left) v[j] = 0.0f;
+      }
+      if (!keep) {
+        *reinterpret_cast<u32x4*>(to_next) = eight_f16(v);
+        return;
+      }
       u32x4 x, y;
       split_eight(v, &x, &y);
-      *reinterpret_cast<u32x4*>(next + at) = x;
-      if (keep) *reinterpret_cast<u32x4*>(lo + at) = y;
+      *reinterpret_cast<u32x4*>(to_next) = x;
+      *reinterpret_cast<u32x4*>(to_lo) = y;
       return;
     }
-    uint16_t* o = static_cast<uint16_t*>(out.p[z]) + m * out_ld + n;
     u32x4 w;
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = two_bf16(v[2 * j] * (1.0f / kUnit), v[2 * j + 1] * (1.0f / kUnit));
-    if (n + 8 <= cols) {
-      *reinterpret_cast<any_u32x4*>(o) = w;
+    if (left >= 8) {
+      *reinterpret_cast<any_u32x4*>(to_out) = w;
       return;
     }
 #pragma unroll
     for (int j = 0; j < 7; ++j)
-      if (n + j < cols) o[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
+      if (j < left) to_out[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
   }
 };
 
@@ -343,7 +389,7 @@ __device__ __forceinline__ void update_tile(const UpdateArgs& a, uint32_t t, int
 
 template <Form FB, int SIDE, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void update_kernel(UpdateArgs a) {
-  using G = Gemm<Form::kRows, FB, Code::kE4m3, SIDE, SIDE, WM, WN, true>;
+  using G = Gemm<Form::kRows, FB, Code::kE4m3, SIDE, SIDE, WM, WN, true, true>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
@@ -372,20 +418,45 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void update_kernel(UpdateArgs a) {
   while (item != kNoItem) {
     g.loop(lds0, lds1, lds2, lds3);
     const uint32_t k = a.queue ? q.ask() : 0;
-    const int64_t m1 = m0, n1 = n0, z1 = z, s1 = slot;
-    auto halfway = [&] {
-      item = a.queue ? next_item(q, k, &turn) : kNoItem;
-      if (item != kNoItem) open(item);
+    const int64_t m1 = m0, n1 = n0, s1 = slot;
+    g.renew_lane();
+    const uint32_t row = g.lane / G::kRowGroups;
+    // the rows come in order, and the places go on with them
+    const uint32_t ld = uint32_t(a.ld), out_ld = uint32_t(a.out_ld), r0 = g.wm * (SIDE / WM) + row;
+    uint32_t at = r0 * ld + uint32_t(g.column()), ahead = at, out_at = r0 * out_ld + uint32_t(g.column());
+    const int64_t rows = a.rows - m1 - row, left = a.cols - n1 - g.column();
+    const int64_t row_pad = padded(a.rows) - a.rows, col_pad = padded(a.cols) - a.cols;
+    const int64_t first = z * a.matrix + m1 * a.ld + n1;
+    uint16_t* out = static_cast<uint16_t*>(a.out.p[z]) + m1 * a.out_ld + n1;
+    // X's values of the rows that come next
+    u32x4 x[2][2], y[2][2];
+    auto before = [&](int i) {
+      if (a.hi == nullptr || s1 >= 0) return;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int r = g.wm * (SIDE / WM) + i * 16 + q * 8;
+        if (r - rows < row_pad && left > -col_pad) {
+          x[i & 1][q] = *reinterpret_cast<const u32x4*>(a.hi + first + ahead);
+          y[i & 1][q] = *reinterpret_cast<const u32x4*>(a.lo + first + ahead);
+        }
+        ahead += 8 * ld;
+      }
     };
-    g.template each<false>(
-        lds3,
-        [&](int r, int c, f32x4v lo, f32x4v hi) {
-          if (s1 >= 0)
-            put_slot<SIDE>(a.partial, s1, r, c, lo, hi);
-          else
-            a.put(z1, m1 + r, n1 + c, lo, hi);
+    g.each_rows(
+        lds3, before,
+        [&](int r, int i, int q, f32x4v lo, f32x4v hi) {
+          if (s1 >= 0) return put_slot<SIDE>(a.partial, s1, r + row, g.column(), lo, hi);
+          const uint32_t here = at, out_here = out_at;
+          at += 8 * ld;
+          out_at += 8 * out_ld;
+          if (r - rows >= row_pad || left <= -col_pad) return;
+          a.put(a.value(lo, hi, x[i & 1][q], y[i & 1][q]), r < rows ? left : 0, a.next + first + here,
+                a.lo + first + here, out + out_here);
         },
-        halfway);
+        [&] {
+          item = a.queue ? next_item(q, k, &turn) : kNoItem;
+          if (item != kNoItem) open(item);
+        });
   }
 }
 
@@ -398,10 +469,16 @@ __global__ __launch_bounds__(256) void join_update_kernel(UpdateArgs a) {
   uint32_t tm, tn;
   update_tile(a, a.cut.full + r, &z, &tm, &tn);
   const int64_t m = int64_t(tm) * SIDE + row, n = int64_t(tn) * SIDE + col;
-  if (m >= a.rows || n >= a.cols) return;
-  f32x4v lo, hi;
-  join_eight<SIDE>(a.partial, a.cut, r, row, col, &lo, &hi);
-  a.put(z, m, n, lo, hi);
+  if (m >= padded(a.rows) || n >= padded(a.cols)) return;
+  f32x4v lo = {}, hi = {};
+  if (m < a.rows) join_eight<SIDE>(a.partial, a.cut, r, row, col, &lo, &hi);
+  const int64_t at = z * a.matrix + m * a.ld + n;
+  u32x4 x = u32x4{0, 0, 0, 0}, y = x;
+  if (a.hi) {
+    x = *reinterpret_cast<const u32x4*>(a.hi + at);
+    y = *reinterpret_cast<const u32x4*>(a.lo + at);
+  }
+  a.put(a.value(lo, hi, x, y), m < a.rows ? a.cols - n : 0, a.next + at, a.lo + at, static_cast<uint16_t*>(a.out.p[z]) + m * a.out_ld + n);
 }
 
 // ------------------------------------------------------------ launches
@@ -464,7 +541,7 @@ Layout layout_of(const OrthogonalCall& c) {
   L.small = L.tall ? c.cols : c.rows;
   L.pitch = up(c.cols, 64);
   L.small_pitch = up(L.small, 64);
-  L.matrix = c.rows * L.pitch;
+  L.matrix = padded(c.rows) * L.pitch;
   L.small_matrix = L.small * L.small_pitch;
   const int64_t each = 3 * L.matrix * 2 + 2 * L.small_matrix * 2;
   L.piece = (int64_t(1) << 30) / each;
@@ -473,7 +550,7 @@ Layout layout_of(const OrthogonalCall& c) {
   // pieces of one size, the last one's rest apart
   const int64_t pieces = (c.count + L.piece - 1) / L.piece;
   L.piece = (c.count + pieces - 1) / pieces;
-  const int64_t groups = (c.rows * (L.pitch / 8) + 255) / 256;
+  const int64_t groups = (padded(c.rows) * (L.pitch / 8) + 255) / 256;
   L.sum_blocks = 2048 / L.piece;
   if (L.sum_blocks > kSumBlocks) L.sum_blocks = kSumBlocks;
   if (L.sum_blocks > groups) L.sum_blocks = groups;
@@ -589,7 +666,7 @@ int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t c
     SymmetricArgs g{};
     g.a = Operand{now, nullptr, L.pitch, 0, L.small};
     g.a_matrix = L.matrix;
-    g.depth = L.tall ? c.rows : c.cols;
+    g.depth = padded(L.tall ? c.rows : c.cols);
     g.partial = partial;
     g.out = gram;
     g.size = L.small;
@@ -601,7 +678,7 @@ int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t c
     if (rc != 0) return rc;
     g.a = Operand{gram, nullptr, L.small_pitch, 0, L.small};
     g.a_matrix = L.small_matrix;
-    g.depth = L.small;
+    g.depth = padded(L.small);
     g.g = gram;
     g.out = poly;
     g.alpha = c.c / kUnit;
@@ -610,7 +687,7 @@ int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t c
     rc = launch_symmetric<Form::kRows>(g, t.square, count, q + kQueueWords * kQueuePitch, st);
     if (rc != 0) return rc;
     UpdateArgs u{};
-    u.depth = L.small;
+    u.depth = padded(L.small);
     u.partial = partial;
     u.rows = c.rows;
     u.cols = c.cols;

@@ -6,17 +6,18 @@
 //   dw = sum over rows of dy xh,  db = sum over rows of dy.
 //
 // Bound by HBM.  A row stays in the registers of the threads that share it (a
-// wave, or a workgroup of 256 to 1024), so that every value is read once: the
-// mean, the squares around it and the result come from there.  A thread takes 16
-// bytes of the wider type at a time, neighbouring threads neighbouring ones, and
-// holds the same columns of each row that its workgroup walks: weight and bias
-// are read once, and the sums of dw and db go on in registers, fp32, until the
-// workgroup's last row.  They are then written for a second launch, which adds
-// them over the workgroups in order.
+// wave, or a workgroup of 256 or 512), so that every value is read once: the mean,
+// the squares around it and the result come from there.  A thread takes 16 bytes
+// of the wider type at a time, neighbouring threads neighbouring ones, and holds
+// the same columns of each row that its workgroup walks: weight and bias are read
+// once, and the sums of dw and db go on in registers, fp32, until the workgroup's
+// last row.  They are then written for a second launch, which adds them over the
+// workgroups in order.  While a row is worked on, the next two are on their way:
+// the barriers of a row's sums wait for LDS only.
 //
-// The squares are taken around the mean as rounded, whose error (the mean of
-// what is left) is taken back from both: a mean far above the deviations costs
-// the rounding of x alone.
+// A row's values are summed in fp64 and the mean is kept in two fp32: a mean far
+// above the deviations costs the rounding of x alone.  The other sums of a row are
+// fp32 in a thread (at most 32 values) and fp64 over the threads.
 //
 // Rows too long for the registers are read two or three times, by loops.
 #include <hip/hip_runtime.h>
@@ -55,24 +56,33 @@ struct Raw {
   static constexpr int kWords = U * (F32 ? 4 : 2) / 4;
   uint32_t w[kWords];
 
-  // Of which `left` exist (any number): zeros for the rest.
-  __device__ __forceinline__ void load(const void* row, int64_t c, int left) {
-    if (left >= U) {
-      if constexpr (kWords == 4) {
-        typedef any_u32x4 __attribute__((may_alias)) vec;
-        const vec* p = reinterpret_cast<const vec*>(static_cast<const char*>(row) + c * (F32 ? 4 : 2));
-        const u32x4 v = __builtin_nontemporal_load(p);
+  __device__ __forceinline__ void load(const void* row, uint32_t c) {
+    const char* p = static_cast<const char*>(row) + c * (F32 ? 4 : 2);
+    if constexpr (kWords == 4) {
+      typedef any_u32x4 __attribute__((may_alias)) vec;
+      const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = v[i];
-      } else {
-        typedef u32x2 __attribute__((aligned(2), may_alias)) vec;
-        const vec* p = reinterpret_cast<const vec*>(static_cast<const char*>(row) + c * (F32 ? 4 : 2));
-        const u32x2 v = __builtin_nontemporal_load(p);
-        w[0] = v[0];
-        w[1] = v[1];
-      }
-      return;
+      for (int i = 0; i < 4; ++i) w[i] = v[i];
+    } else {
+      typedef u32x2 __attribute__((aligned(2), may_alias)) vec;
+      const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
+      w[0] = v[0];
+      w[1] = v[1];
     }
+  }
+  __device__ __forceinline__ void store(void* row, uint32_t c) const {
+    char* p = static_cast<char*>(row) + c * (F32 ? 4 : 2);
+    if constexpr (kWords == 4) {
+      typedef any_u32x4 __attribute__((may_alias)) vec;
+      __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<vec*>(p));
+    } else {
+      typedef u32x2 __attribute__((aligned(2), may_alias)) vec;
+      __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<vec*>(p));
+    }
+  }
+  // The same of the first `left` values; zeros for the rest.
+  __device__ __forceinline__ void load_some(const void* row, int64_t c, int left) {
+    if (left >= U) return load(static_cast<const char*>(row) + c * (F32 ? 4 : 2), 0);
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0;
 #pragma unroll
@@ -84,6 +94,23 @@ struct Raw {
         w[i / 2] |= uint32_t(static_cast<const uint16_t*>(row)[c + i]) << (16 * (i & 1));
     }
   }
+  __device__ __forceinline__ void store_some(void* row, int64_t c, int left) const {
+    if (left >= U) return store(static_cast<char*>(row) + c * (F32 ? 4 : 2), 0);
+#pragma unroll
+    for (int i = 0; i < U - 1; ++i) {
+      if (i >= left) break;
+      if constexpr (F32)
+        static_cast<uint32_t*>(row)[c + i] = w[i];
+      else
+        static_cast<uint16_t*>(row)[c + i] = uint16_t(w[i / 2] >> (16 * (i & 1)));
+    }
+  }
+
+  // New to the compiler: what was worked out from it is not kept.
+  __device__ __forceinline__ void renewed() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) renew(w[i]);
+  }
 
   __device__ __forceinline__ float value(int i) const {
     if constexpr (F32) return __uint_as_float(w[i]);
@@ -94,33 +121,23 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = F32 ? __float_as_uint(v[i]) : two_bf16(v[2 * i], v[2 * i + 1]);
   }
-
-  __device__ __forceinline__ void store(void* row, int64_t c, int left) const {
-    if (left >= U) {
-      if constexpr (kWords == 4) {
-        typedef any_u32x4 __attribute__((may_alias)) vec;
-        __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]},
-                                    reinterpret_cast<vec*>(static_cast<char*>(row) + c * (F32 ? 4 : 2)));
-      } else {
-        typedef u32x2 __attribute__((aligned(2), may_alias)) vec;
-        __builtin_nontemporal_store(u32x2{w[0], w[1]},
-                                    reinterpret_cast<vec*>(static_cast<char*>(row) + c * (F32 ? 4 : 2)));
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < U - 1; ++i) {
-      if (i >= left) break;
-      if constexpr (F32)
-        static_cast<uint32_t*>(row)[c + i] = w[i];
-      else
-        static_cast<uint16_t*>(row)[c + i] = uint16_t(w[i / 2] >> (16 * (i & 1)));
-    }
-  }
 };
 
 template <bool F32>
 constexpr int64_t kSize = F32 ? 4 : 2;
+
+// The U columns of piece j of thread t of SHARE.  A row's last piece may be short:
+// its thread takes the last U columns instead, of which the first `again` are its
+// neighbour's too.  Both write them, the same values; sums leave them out.
+struct Columns {
+  uint32_t first;
+  int again;  // U: there are none
+};
+template <int U, int SHARE>
+__device__ __forceinline__ Columns columns_of(int cols, int j, int t) {
+  const int c = (j * SHARE + t) * U, over = c + U - cols;
+  return Columns{uint32_t(over > 0 ? cols - U : c), over <= 0 ? 0 : over < U ? over : U};
+}
 
 __device__ __forceinline__ float affine(const void* p, int32_t f32, int64_t c, float none) {
   if (p == nullptr) return none;
@@ -129,42 +146,64 @@ __device__ __forceinline__ float affine(const void* p, int32_t f32, int64_t c, f
 
 // The sum over a wave, in every lane.
 template <int CTRL>
-__device__ __forceinline__ float with_lane(float v) {
-  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, 0xF, 0xF, true));
+__device__ __forceinline__ float moved(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, 0xF, 0xF, true));
 }
-__device__ __forceinline__ float wave_sum(float v) {
-  v = with_lane<0xB1>(v);   // lane ^ 1
-  v = with_lane<0x4E>(v);   // lane ^ 2
-  v = with_lane<0x141>(v);  // the other four of eight
-  v = with_lane<0x140>(v);  // the other eight of sixteen
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(b), CTRL, 0xF, 0xF, true));
+  const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(b >> 32), CTRL, 0xF, 0xF, true));
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ double other_16(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, uint64_t(__float_as_uint(tide::other_16(__uint_as_float(uint32_t(b >> 32))))) << 32 |
+                                        __float_as_uint(tide::other_16(__uint_as_float(uint32_t(b)))));
+}
+__device__ __forceinline__ double other_32(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, uint64_t(__float_as_uint(tide::other_32(__uint_as_float(uint32_t(b >> 32))))) << 32 |
+                                        __float_as_uint(tide::other_32(__uint_as_float(uint32_t(b)))));
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+  v += moved<0xB1>(v);   // lane ^ 1
+  v += moved<0x4E>(v);   // lane ^ 2
+  v += moved<0x141>(v);  // the other four of eight
+  v += moved<0x140>(v);  // the other eight of sixteen
   v += other_16(v);
   return v + other_32(v);
 }
 
-// Two sums over the threads that share a row, in every one of them.  `turn`
-// alternates between two sets of words, so that one barrier a sum is enough.
+// Sums over the threads that share a row, in every one of them.  `turn` alternates
+// between two sets of words, so that one barrier a sum is enough; it waits for LDS
+// only, not for the rows on their way.
 template <int SHARE>
 struct RowSum {
   static constexpr int kWaves = SHARE / 64;
-  float2 (*words)[kWaves > 1 ? kWaves : 1];
+  double (*words)[2][kWaves];
   int turn = 0;
 
-  __device__ __forceinline__ float2 operator()(float a, float b) {
-    a = wave_sum(a);
-    b = wave_sum(b);
-    if constexpr (kWaves > 1) {
-      if ((threadIdx.x & 63) == 0) words[turn][wave_index()] = make_float2(a, b);
-      __syncthreads();
-      a = b = 0.0f;
+  // one sum in fp64, or two
+  template <int N>
+  __device__ __forceinline__ void operator()(double* v) {
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float2 v = words[turn][w];
-        a += v.x;
-        b += v.y;
+    for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+    if constexpr (kWaves > 1) {
+      if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) words[turn][k][wave_index()] = v[k];
+      }
+      lds_barrier();
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        v[k] = words[turn][k][0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v[k] += words[turn][k][w];
       }
       turn ^= 1;
     }
-    return make_float2(a, b);
   }
 };
 
@@ -173,149 +212,212 @@ struct RowSum {
 template <int SHARE>
 constexpr int kBlock = SHARE < 256 ? 256 : SHARE;
 
-template <bool XF32, bool YF32, int SHARE, int J>
-__global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_kernel(NormArgs a) {
-  constexpr int U = XF32 || YF32 ? 4 : 8, kRows = kBlock<SHARE> / SHARE;
-  __shared__ float2 words[2][SHARE / 64];
-  RowSum<SHARE> sum{words};
-  const int t = threadIdx.x % SHARE;
-  const float n = float(a.cols);
-  float w[J * U], b[J * U];
-  int left[J];
+// A mean in two parts, and 1 / sqrt(var + eps).
+struct Stats {
+  float mean, rest, rstd;
+};
+__device__ __forceinline__ Stats mean_of(double sum, double per_value) {
+  const double m = sum * per_value;
+  const float mean = float(m);
+  // (infinite or NaN: nothing is left)
+  return Stats{mean, float(m - double(mean)), 0.0f};
+}
+__device__ __forceinline__ float rstd_of(double squares, double per_value, float eps) {
+  return 1.0f / sqrtf(float(squares * per_value) + eps);
+}
+
+// The same for all lanes of a wave.
+template <int SHARE>
+__device__ __forceinline__ int64_t first_row() {
+  static_assert(SHARE == 64 || SHARE == kBlock<SHARE>, "rows of a workgroup");
+  return SHARE == 64 ? int64_t(blockIdx.x) * (kBlock<SHARE> / SHARE) + wave_index() : int64_t(blockIdx.x);
+}
+
+// One row after another through SETS sets of registers: use(k, row) is called
+// for every row of this thread with the set that fetch(k, row) filled, SETS - 1
+// rows ahead.
+template <int SETS, typename F, typename U>
+__device__ __forceinline__ void walk(int64_t r, int64_t step, int64_t rows, F fetch, U use) {
+  constexpr int kAhead = SETS - 1;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int c = (j * SHARE + t) * U;
-    left[j] = a.cols - c;
+  for (int k = 0; k < kAhead; ++k)
+    if (r + k * step < rows) fetch(k, r + k * step);
+  while (r < rows) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      w[j * U + i] = i < left[j] ? affine(a.weight, a.affine_f32, c + i, 1.0f) : 0.0f;
-      b[j * U + i] = i < left[j] ? affine(a.bias, a.affine_f32, c + i, 0.0f) : 0.0f;
-    }
-  }
-  const int64_t step = int64_t(gridDim.x) * kRows;
-  int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / SHARE;
-  Raw<XF32, U> next[J];
-  auto fetch = [&](int64_t row) {
-    const char* p = static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>;
-#pragma unroll
-    for (int j = 0; j < J; ++j) next[j].load(p, (j * SHARE + t) * U, left[j]);
-  };
-  if (r < a.rows) fetch(r);
-  // a row's threads leave together: with more than one wave a row, a workgroup has one
-  for (; r < a.rows; r += step) {
-    float x[J * U];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < U; ++i) x[j * U + i] = next[j].value(i);
-    if (r + step < a.rows) fetch(r + step);
-    float s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < J * U; ++k) s += x[k];
-    const float mean = sum(s, 0.0f).x / n;
-    float off = 0.0f, squares = 0.0f;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        float& v = x[j * U + i];
-        v = i < left[j] ? v - mean : 0.0f;
-        off += v;
-        squares += v * v;
-      }
-    const float2 both = sum(off, squares);
-    off = both.x / n;
-    const float var = fmaxf(both.y / n - off * off, 0.0f);
-    // a NaN of the row must come out: the maximum would drop it
-    const float rstd = 1.0f / sqrtf((both.y != both.y ? both.y : var) + a.eps);
-    char* out = static_cast<char*>(a.out) + r * a.out_ld * kSize<YF32>;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float y[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) y[i] = (x[j * U + i] - off) * rstd * w[j * U + i] + b[j * U + i];
-      Raw<YF32, U> v;
-      v.set(y);
-      v.store(out, (j * SHARE + t) * U, left[j]);
-    }
-    if (t == 0) {
-      if (a.mean) a.mean[r] = mean + off;
-      if (a.rstd) a.rstd[r] = rstd;
+    for (int k = 0; k < SETS; ++k) {
+      if (r + kAhead * step < rows) fetch((k + kAhead) % SETS, r + kAhead * step);
+      if (r < rows) use(k, r);
+      r += step;
     }
   }
 }
+// Two sets of that many registers where three would be more than `most`.
+constexpr int sets_of(int words, int most) { return 3 * words > most ? 2 : 3; }
 
 template <bool XF32, bool YF32, int SHARE, int J>
-__global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_grad_kernel(NormArgs a) {
+__global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_kernel(NormArgs a) {
   constexpr int U = XF32 || YF32 ? 4 : 8, kRows = kBlock<SHARE> / SHARE;
-  __shared__ float2 words[2][SHARE / 64];
+  __shared__ double words[2][2][SHARE / 64];
   RowSum<SHARE> sum{words};
   const int t = threadIdx.x % SHARE;
-  const float n = float(a.cols);
-  float w[J * U], dw[J * U], db[J * U];
-  int left[J];
+  const double per_value = 1.0 / double(a.cols);
+  float w[J * U], b[J * U];
+  Columns at[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int c = (j * SHARE + t) * U;
-    left[j] = a.cols - c;
+    at[j] = columns_of<U, SHARE>(a.cols, j, t);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      w[j * U + i] = i < left[j] ? affine(a.weight, a.affine_f32, c + i, 1.0f) : 0.0f;
+      w[j * U + i] = affine(a.weight, a.affine_f32, at[j].first + i, 1.0f);
+      b[j * U + i] = affine(a.bias, a.affine_f32, at[j].first + i, 0.0f);
+    }
+  }
+  constexpr int kSet = sets_of(J * Raw<XF32, U>::kWords, 96);
+  Raw<XF32, U> x[kSet][J];
+  walk<kSet>(
+      first_row<SHARE>(), int64_t(gridDim.x) * kRows, a.rows,
+      [&](int set, int64_t row) {
+        const char* p = static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (at[j].again < U) x[set][j].load(p, at[j].first);
+      },
+      [&](int set, int64_t row) {
+        // a row's threads leave together: with more than one wave a row, a workgroup has one
+        auto sum_of = [&](auto value) {
+          decltype(value(0.0f)) s = 0;
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            if (at[j].again == 0) {
+#pragma unroll
+              for (int i = 0; i < U; ++i) s += value(x[set][j].value(i));
+            } else if (at[j].again < U) {
+#pragma unroll
+              for (int i = 1; i < U; ++i)
+                if (i >= at[j].again) s += value(x[set][j].value(i));
+            }
+          }
+          return s;
+        };
+        double total[1] = {sum_of([](float v) { return double(v); })};
+        sum.template operator()<1>(total);
+        Stats m = mean_of(total[0], per_value);
+        total[0] = double(sum_of([&](float v) {
+          const float d = v - m.mean - m.rest;
+          return d * d;
+        }));
+        sum.template operator()<1>(total);
+#pragma unroll
+        for (int j = 0; j < J; ++j) x[set][j].renewed();
+        m.rstd = rstd_of(total[0], per_value, a.eps);
+        char* out = static_cast<char*>(a.out) + row * a.out_ld * kSize<YF32>;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (at[j].again == U) continue;
+          float y[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i)
+            y[i] = (x[set][j].value(i) - m.mean - m.rest) * m.rstd * w[j * U + i] + b[j * U + i];
+          Raw<YF32, U> v;
+          v.set(y);
+          v.store(out, at[j].first);
+        }
+        if (t == 0) {
+          if (a.mean) a.mean[row] = m.mean;
+          if (a.rstd) a.rstd[row] = m.rstd;
+        }
+      });
+}
+
+template <bool XF32, bool YF32, int SHARE, int J>
+__global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormArgs a) {
+  constexpr int U = XF32 || YF32 ? 4 : 8, kRows = kBlock<SHARE> / SHARE;
+  __shared__ double words[2][2][SHARE / 64];
+  RowSum<SHARE> sum{words};
+  const int t = threadIdx.x % SHARE;
+  const double per_value = 1.0 / double(a.cols);
+  float w[J * U], dw[J * U], db[J * U];
+  Columns at[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    at[j] = columns_of<U, SHARE>(a.cols, j, t);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      w[j * U + i] = affine(a.weight, a.affine_f32, at[j].first + i, 1.0f);
       dw[j * U + i] = db[j * U + i] = 0.0f;
     }
   }
-  const int64_t step = int64_t(gridDim.x) * kRows;
-  int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / SHARE;
-  Raw<XF32, U> next_x[J];
-  Raw<YF32, U> next_dy[J];
-  float next_mean = 0.0f, next_rstd = 0.0f;
-  auto fetch = [&](int64_t row) {
-    const char* px = static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>;
-    const char* py = static_cast<const char*>(a.dy) + row * a.dy_ld * kSize<YF32>;
+  constexpr int kSet = sets_of(J * (Raw<XF32, U>::kWords + Raw<YF32, U>::kWords), 24);
+  Raw<XF32, U> x[kSet][J];
+  Raw<YF32, U> y[kSet][J];
+  float mean[kSet], rstd[kSet];
+  walk<kSet>(
+      first_row<SHARE>(), int64_t(gridDim.x) * kRows, a.rows,
+      [&](int set, int64_t row) {
+        const char* px = static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>;
+        const char* py = static_cast<const char*>(a.dy) + row * a.dy_ld * kSize<YF32>;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      next_x[j].load(px, (j * SHARE + t) * U, left[j]);
-      next_dy[j].load(py, (j * SHARE + t) * U, left[j]);
-    }
-    next_mean = a.mean[row];
-    next_rstd = a.rstd[row];
-  };
-  if (r < a.rows) fetch(r);
-  for (; r < a.rows; r += step) {
-    float xh[J * U], g[J * U];
-    const float mean = next_mean, rstd = next_rstd;
-    float s = 0.0f, sx = 0.0f;
+        for (int j = 0; j < J; ++j) {
+          if (at[j].again == U) continue;
+          x[set][j].load(px, at[j].first);
+          y[set][j].load(py, at[j].first);
+        }
+        mean[set] = a.mean[row];
+        rstd[set] = a.rstd[row];
+      },
+      [&](int set, int64_t row) {
+        float s = 0.0f, sx = 0.0f;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j) {
+          if (at[j].again == U) continue;
+          float gs = 0.0f, gx = 0.0f;
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int k = j * U + i;
-        const float dy = next_dy[j].value(i);
-        xh[k] = i < left[j] ? (next_x[j].value(i) - mean) * rstd : 0.0f;
-        g[k] = dy * w[k];
-        dw[k] += dy * xh[k];
-        db[k] += dy;
-        s += g[k];
-        sx += g[k] * xh[k];
-      }
-    if (r + step < a.rows) fetch(r + step);
-    const float2 both = sum(s, sx);
-    s = both.x / n;
-    sx = both.y / n;
-    char* out = static_cast<char*>(a.out) + r * a.out_ld * kSize<XF32>;
+          for (int i = 0; i < U; ++i) {
+            const int k = j * U + i;
+            const float dy = y[set][j].value(i), xh = (x[set][j].value(i) - mean[set]) * rstd[set], g = dy * w[k];
+            dw[k] += dy * xh;
+            db[k] += dy;
+            gs += g;
+            gx += g * xh;
+          }
+          if (at[j].again > 0) {
+            gs = gx = 0.0f;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float d[U];
+            for (int i = 1; i < U; ++i) {
+              if (i < at[j].again) continue;
+              const float g = y[set][j].value(i) * w[j * U + i];
+              gs += g;
+              gx += g * ((x[set][j].value(i) - mean[set]) * rstd[set]);
+            }
+          }
+          s += gs;
+          sx += gx;
+        }
+        double both[2] = {double(s), double(sx)};
+        sum.template operator()<2>(both);
+        // (kept from above, the values would take twice the rows' registers)
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int k = j * U + i;
-        d[i] = rstd * (g[k] - s - xh[k] * sx);
-      }
-      Raw<XF32, U> v;
-      v.set(d);
-      v.store(out, (j * SHARE + t) * U, left[j]);
-    }
-  }
+        for (int j = 0; j < J; ++j) {
+          x[set][j].renewed();
+          y[set][j].renewed();
+        }
+        s = float(both[0] * per_value);
+        sx = float(both[1] * per_value);
+        char* out = static_cast<char*>(a.out) + row * a.out_ld * kSize<XF32>;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (at[j].again == U) continue;
+          float d[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const float xh = (x[set][j].value(i) - mean[set]) * rstd[set];
+            d[i] = rstd[set] * (y[set][j].value(i) * w[j * U + i] - s - xh * sx);
+          }
+          Raw<XF32, U> v;
+          v.set(d);
+          v.store(out, at[j].first);
+        }
+      });
   if (a.partial == nullptr) return;
   float* p = a.partial + int64_t(blockIdx.x) * 2 * a.cols;
   if constexpr (kRows > 1) {
@@ -344,8 +446,8 @@ __global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_grad_kernel(NormArgs
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (i < left[j]) {
-        const int c = (j * SHARE + t) * U + i;
+      if (i >= at[j].again) {
+        const uint32_t c = at[j].first + i;
         p[c] = dw[j * U + i];
         p[a.cols + c] = db[j * U + i];
       }
@@ -398,9 +500,9 @@ __device__ __forceinline__ float at(const void* row, int64_t c) {
 
 template <bool XF32, bool YF32>
 __global__ __launch_bounds__(kWideBlock) void wide_norm_kernel(NormArgs a) {
-  __shared__ float2 words[2][kWideBlock / 64];
+  __shared__ double words[2][2][kWideBlock / 64];
   RowSum<kWideBlock> sum{words};
-  const float n = float(a.cols);
+  const double per_value = 1.0 / double(a.cols);
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const char* x = static_cast<const char*>(a.x) + r * a.x_ld * kSize<XF32>;
     char* out = static_cast<char*>(a.out) + r * a.out_ld * kSize<YF32>;
@@ -408,52 +510,53 @@ __global__ __launch_bounds__(kWideBlock) void wide_norm_kernel(NormArgs a) {
       for (int64_t c = int64_t(threadIdx.x) * kWideU; c < a.cols; c += kWideBlock * kWideU) {
         const int left = a.cols - c < kWideU ? int(a.cols - c) : kWideU;
         Raw<XF32, kWideU> v;
-        v.load(x, c, left);
+        v.load_some(x, c, left);
         f(v, c, left);
       }
     };
-    float s = 0.0f;
+    // a row may be long: the threads' own sums are fp64 too
+    double total[1] = {0.0};
     each([&](const Raw<XF32, kWideU>& v, int64_t, int) {
 #pragma unroll
-      for (int i = 0; i < kWideU; ++i) s += v.value(i);
+      for (int i = 0; i < kWideU; ++i) total[0] += double(v.value(i));
     });
-    const float mean = sum(s, 0.0f).x / n;
-    float off = 0.0f, squares = 0.0f;
+    sum.template operator()<1>(total);
+    Stats m = mean_of(total[0], per_value);
+    total[0] = 0.0;
     each([&](const Raw<XF32, kWideU>& v, int64_t, int left) {
+      float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWideU; ++i) {
-        const float d = i < left ? v.value(i) - mean : 0.0f;
-        off += d;
-        squares += d * d;
+        const float d = v.value(i) - m.mean - m.rest;
+        if (i < left) s += d * d;
       }
+      total[0] += double(s);
     });
-    const float2 both = sum(off, squares);
-    off = both.x / n;
-    const float var = fmaxf(both.y / n - off * off, 0.0f);
-    const float rstd = 1.0f / sqrtf((both.y != both.y ? both.y : var) + a.eps);
+    sum.template operator()<1>(total);
+    m.rstd = rstd_of(total[0], per_value, a.eps);
     each([&](const Raw<XF32, kWideU>& v, int64_t c, int left) {
       float y[kWideU];
 #pragma unroll
       for (int i = 0; i < kWideU; ++i)
-        y[i] = i < left ? (v.value(i) - mean - off) * rstd * affine(a.weight, a.affine_f32, c + i, 1.0f) +
+        y[i] = i < left ? (v.value(i) - m.mean - m.rest) * m.rstd * affine(a.weight, a.affine_f32, c + i, 1.0f) +
                               affine(a.bias, a.affine_f32, c + i, 0.0f)
                         : 0.0f;
       Raw<YF32, kWideU> o;
       o.set(y);
-      o.store(out, c, left);
+      o.store_some(out, c, left);
     });
     if (threadIdx.x == 0) {
-      if (a.mean) a.mean[r] = mean + off;
-      if (a.rstd) a.rstd[r] = rstd;
+      if (a.mean) a.mean[r] = m.mean;
+      if (a.rstd) a.rstd[r] = m.rstd;
     }
   }
 }
 
 template <bool XF32, bool YF32>
 __global__ __launch_bounds__(kWideBlock) void wide_norm_grad_kernel(NormArgs a) {
-  __shared__ float2 words[2][kWideBlock / 64];
+  __shared__ double words[2][2][kWideBlock / 64];
   RowSum<kWideBlock> sum{words};
-  const float n = float(a.cols);
+  const double per_value = 1.0 / double(a.cols);
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const char* x = static_cast<const char*>(a.x) + r * a.x_ld * kSize<XF32>;
     const char* dy = static_cast<const char*>(a.dy) + r * a.dy_ld * kSize<YF32>;
@@ -464,8 +567,8 @@ __global__ __launch_bounds__(kWideBlock) void wide_norm_grad_kernel(NormArgs a) 
         const int left = a.cols - c < kWideU ? int(a.cols - c) : kWideU;
         Raw<XF32, kWideU> vx;
         Raw<YF32, kWideU> vy;
-        vx.load(x, c, left);
-        vy.load(dy, c, left);
+        vx.load_some(x, c, left);
+        vy.load_some(dy, c, left);
         float xh[kWideU], g[kWideU];
 #pragma unroll
         for (int i = 0; i < kWideU; ++i) {
@@ -475,24 +578,26 @@ __global__ __launch_bounds__(kWideBlock) void wide_norm_grad_kernel(NormArgs a) 
         f(xh, g, c, left);
       }
     };
-    float s = 0.0f, sx = 0.0f;
+    double both[2] = {0.0, 0.0};
     each([&](const float* xh, const float* g, int64_t, int) {
+      float s = 0.0f, sx = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWideU; ++i) {
         s += g[i];
         sx += g[i] * xh[i];
       }
+      both[0] += double(s);
+      both[1] += double(sx);
     });
-    const float2 both = sum(s, sx);
-    s = both.x / n;
-    sx = both.y / n;
+    sum.template operator()<2>(both);
+    const float s = float(both[0] * per_value), sx = float(both[1] * per_value);
     each([&](const float* xh, const float* g, int64_t c, int left) {
       float d[kWideU];
 #pragma unroll
       for (int i = 0; i < kWideU; ++i) d[i] = rstd * (g[i] - s - xh[i] * sx);
       Raw<XF32, kWideU> o;
       o.set(d);
-      o.store(out, c, left);
+      o.store_some(out, c, left);
     });
   }
 }
@@ -521,13 +626,21 @@ struct Shape {
   int64_t groups;
 };
 
+// As few threads a row as hold it in 32 values each (16 of a wave's, and for the
+// gradients, which hold three more values for each), so that several rows are
+// worked on in a CU and few threads wait for each other.  A workgroup of the
+// gradients leaves two fp32 sums a column, so there are no more of them than a 16th
+// of the rows, but one a CU.
 Shape shape_of(const LayerNormCall& c, bool grad) {
   const int64_t u = c.x_f32 || c.y_f32 ? 4 : 8;
   Shape s{0, 0, 0};
+  if (c.cols >= u)
   for (int share : {64, 256, 512, 1024}) {
-    if (c.cols <= share * u * 2) {
+    const int64_t most = (share == 64 || grad ? 16 : 32) / u;
+    if (!grad && share == 1024) break;
+    if (c.cols <= share * u * most) {
       s.share = share;
-      s.j = c.cols <= share * u ? 1 : 2;
+      s.j = int((c.cols + share * u - 1) / (share * u));
       break;
     }
   }
@@ -536,41 +649,71 @@ Shape shape_of(const LayerNormCall& c, bool grad) {
     return s;
   }
   const int64_t block = s.share < 256 ? 256 : s.share, at_once = block / s.share;
-  const int64_t need = (c.rows + at_once - 1) / at_once, most = 256 * (2048 / block) / (grad ? 2 : 1);
+  const int64_t need = (c.rows + at_once - 1) / at_once;
+  int64_t most = 1024 * 256 / block;
+  if (grad) {
+    if (most > need / 16) most = need / 16;
+    if (most < 256) most = 256;
+  }
   s.groups = need < most ? need : most;
   return s;
 }
 
 template <bool XF32, bool YF32>
+int launch_wide(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(s.groups));
+  if (!grad) {
+    hipLaunchKernelGGL((wide_norm_kernel<XF32, YF32>), grid, dim3(kWideBlock), 0, st, a);
+    return int(hipGetLastError());
+  }
+  hipLaunchKernelGGL((wide_norm_grad_kernel<XF32, YF32>), grid, dim3(kWideBlock), 0, st, a);
+  const int rc = int(hipGetLastError());
+  if (rc != 0 || a.partial == nullptr) return rc;
+  hipLaunchKernelGGL((wide_affine_kernel<XF32, YF32>), dim3(unsigned((c.cols + 255) / 256), unsigned(s.groups)),
+                     dim3(256), 0, st, a);
+  return int(hipGetLastError());
+}
+
+template <bool XF32, bool YF32>
 int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(s.groups));
-#define TIDE_NORM(SHARE, J)                                                                                     \
-  do {                                                                                                          \
-    if (grad)                                                                                                   \
-      hipLaunchKernelGGL((layer_norm_grad_kernel<XF32, YF32, SHARE, J>), grid, dim3(kBlock<SHARE>), 0, st, a); \
-    else                                                                                                        \
-      hipLaunchKernelGGL((layer_norm_kernel<XF32, YF32, SHARE, J>), grid, dim3(kBlock<SHARE>), 0, st, a);      \
-  } while (0)
-  if (s.share == 64 && s.j == 1)
-    TIDE_NORM(64, 1);
-  else if (s.share == 64)
-    TIDE_NORM(64, 2);
-  else if (s.share == 256 && s.j == 1)
-    TIDE_NORM(256, 1);
-  else if (s.share == 256)
-    TIDE_NORM(256, 2);
-  else if (s.share == 512)
-    TIDE_NORM(512, 2);  // one piece would have fitted 256 threads
-  else if (s.share == 1024)
-    TIDE_NORM(1024, 2);
-  else if (!grad)
-    hipLaunchKernelGGL((wide_norm_kernel<XF32, YF32>), grid, dim3(kWideBlock), 0, st, a);
-  else {
-    hipLaunchKernelGGL((wide_norm_grad_kernel<XF32, YF32>), grid, dim3(kWideBlock), 0, st, a);
-    const int rc = int(hipGetLastError());
-    if (rc != 0 || a.partial == nullptr) return rc;
-    hipLaunchKernelGGL((wide_affine_kernel<XF32, YF32>), dim3(unsigned((c.cols + 255) / 256), unsigned(s.groups)),
-                       dim3(256), 0, st, a);
+  if (s.share == 0) return launch_wide<XF32, YF32>(c, s, a, grad, st);
+  constexpr int kPer = XF32 || YF32 ? 2 : 1;  // pieces of 8 values
+#define TIDE_NORM(KERNEL, SHARE, J) hipLaunchKernelGGL((KERNEL<XF32, YF32, SHARE, J>), grid, dim3(kBlock<SHARE>), 0, st, a)
+  if (grad) {
+    if (s.share == 64 && s.j <= kPer)
+      TIDE_NORM(layer_norm_grad_kernel, 64, kPer);
+    else if (s.share == 64)
+      TIDE_NORM(layer_norm_grad_kernel, 64, 2 * kPer);
+    else if (s.share == 256 && s.j <= kPer)
+      TIDE_NORM(layer_norm_grad_kernel, 256, kPer);
+    else if (s.share == 256)
+      TIDE_NORM(layer_norm_grad_kernel, 256, 2 * kPer);
+    else if (s.share == 512 && kPer == 2 && s.j == 3)
+      TIDE_NORM(layer_norm_grad_kernel, 512, 3);
+    else if (s.share == 512)
+      TIDE_NORM(layer_norm_grad_kernel, 512, 2 * kPer);
+    else if (kPer == 2 && s.j == 3)
+      TIDE_NORM(layer_norm_grad_kernel, 1024, 3);
+    else
+      TIDE_NORM(layer_norm_grad_kernel, 1024, 2 * kPer);
+  } else {
+    if (s.share == 64 && s.j <= kPer)
+      TIDE_NORM(layer_norm_kernel, 64, kPer);
+    else if (s.share == 64)
+      TIDE_NORM(layer_norm_kernel, 64, 2 * kPer);
+    else if (s.share == 512)
+      TIDE_NORM(layer_norm_kernel, 512, 4 * kPer);
+    else if (s.j <= kPer)
+      TIDE_NORM(layer_norm_kernel, 256, kPer);
+    else if (s.j <= 2 * kPer)
+      TIDE_NORM(layer_norm_kernel, 256, 2 * kPer);
+    else if (kPer == 2 && s.j == 5)
+      TIDE_NORM(layer_norm_kernel, 256, 5);
+    else if (s.j <= 3 * kPer)
+      TIDE_NORM(layer_norm_kernel, 256, 3 * kPer);
+    else
+      TIDE_NORM(layer_norm_kernel, 256, 4 * kPer);
   }
 #undef TIDE_NORM
   return int(hipGetLastError());

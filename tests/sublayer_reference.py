@@ -25,13 +25,14 @@ def layer_norm(x, w, b, eps):
     """{name: (value, bound)} of out, mean and rstd for float64 x (rows x n), w
     and b.
 
-    A mean is rounded once, whatever its sum lost: what is left of it, off, is
-    taken back.  v = x - mean is rounded by U32 of itself, off is a mean of n of
-    them and differs from theirs by K + 1 roundings of the mean magnitude, and
-    x - mean - off is rounded again.  The squares' mean carries 3 + K of them,
-    rstd half of those and four more (eps, the root, the division, each counted
-    twice for routines that are off by a whole step).  The factor 1.01 stands for
-    products of these errors."""
+    The bounds are those of sums in fp32 throughout whose mean is corrected by the
+    mean of what it leaves; sums in fp64 stay within them.  A mean is rounded once,
+    whatever its sum lost: what is left of it, off, is taken back.  v = x - mean is
+    rounded by U32 of itself, off is a mean of n of them and differs from theirs by
+    K + 1 roundings of the mean magnitude, and x - mean - off is rounded again.  The
+    squares' mean carries 3 + K of them, rstd half of those and four more (eps, the
+    root, the division, each counted twice for routines that are off by a whole
+    step).  The factor 1.01 stands for products of these errors."""
     n = x.shape[1]
     K = row_adds(n)
     mean = x.mean(-1, keepdims=True)

@@ -23,6 +23,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "gemm.h"
 #include "training.h"
@@ -144,39 +145,61 @@ __device__ __forceinline__ float affine(const void* p, int32_t f32, int64_t c, f
   return f32 ? static_cast<const float*>(p)[c] : low_bf16(static_cast<const uint16_t*>(p)[c]);
 }
 
-// The sum over a wave, in every lane.
-template <int CTRL>
-__device__ __forceinline__ float moved(float v) {
-  return __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, 0xF, 0xF, true));
+// U neighbouring ones.
+template <int U>
+__device__ __forceinline__ void affine_values(const void* p, int32_t f32, uint32_t c, float none, float* v) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) v[i] = none;
+  } else if (f32) {
+#pragma unroll
+    for (int i = 0; i < U; i += 4) {
+      Raw<true, 4> r;
+      r.load(p, c + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i + k] = r.value(k);
+    }
+  } else {
+    Raw<false, U> r;
+    r.load(p, c);
+#pragma unroll
+    for (int i = 0; i < U; ++i) v[i] = r.value(i);
+  }
 }
-template <int CTRL>
+
+// The sum over a wave, in every lane: within 16 lanes, then lane 15 of a row of
+// lanes to the next one and lane 31 to the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, ROWS, 0xF, true));
+}
+template <int CTRL, int ROWS>
 __device__ __forceinline__ double moved(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(b), CTRL, 0xF, 0xF, true));
-  const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(b >> 32), CTRL, 0xF, 0xF, true));
+  const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(b), CTRL, ROWS, 0xF, true));
+  const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(b >> 32), CTRL, ROWS, 0xF, true));
   return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
 }
-__device__ __forceinline__ double other_16(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, uint64_t(__float_as_uint(tide::other_16(__uint_as_float(uint32_t(b >> 32))))) << 32 |
-                                        __float_as_uint(tide::other_16(__uint_as_float(uint32_t(b)))));
+__device__ __forceinline__ float last_lane(float v) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
-__device__ __forceinline__ double other_32(double v) {
+__device__ __forceinline__ double last_lane(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, uint64_t(__float_as_uint(tide::other_32(__uint_as_float(uint32_t(b >> 32))))) << 32 |
-                                        __float_as_uint(tide::other_32(__uint_as_float(uint32_t(b)))));
+  return __builtin_bit_cast(double, uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(b >> 32), 63))) << 32 |
+                                        uint32_t(__builtin_amdgcn_readlane(uint32_t(b), 63)));
 }
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {
-  v += moved<0xB1>(v);   // lane ^ 1
-  v += moved<0x4E>(v);   // lane ^ 2
-  v += moved<0x141>(v);  // the other four of eight
-  v += moved<0x140>(v);  // the other eight of sixteen
-  v += other_16(v);
-  return v + other_32(v);
+  v += moved<0xB1, 0xF>(v);   // lane ^ 1
+  v += moved<0x4E, 0xF>(v);   // lane ^ 2
+  v += moved<0x141, 0xF>(v);  // the other four of eight
+  v += moved<0x140, 0xF>(v);  // the other eight of sixteen
+  v += moved<0x142, 0xA>(v);
+  v += moved<0x143, 0xC>(v);
+  return last_lane(v);
 }
 
-// Sums over the threads that share a row, in every one of them.  `turn` alternates
+// N sums over the threads that share a row, in every one of them.  `turn` alternates
 // between two sets of words, so that one barrier a sum is enough; it waits for LDS
 // only, not for the rows on their way.
 template <int SHARE>
@@ -185,22 +208,22 @@ struct RowSum {
   double (*words)[2][kWaves];
   int turn = 0;
 
-  // one sum in fp64, or two
-  template <int N>
-  __device__ __forceinline__ void operator()(double* v) {
+  template <int N, typename T>
+  __device__ __forceinline__ void operator()(T* v) {
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
     if constexpr (kWaves > 1) {
+      T(*w)[kWaves] = reinterpret_cast<T(*)[kWaves]>(words[turn]);
       if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) words[turn][k][wave_index()] = v[k];
+        for (int k = 0; k < N; ++k) w[k][wave_index()] = v[k];
       }
       lds_barrier();
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        v[k] = words[turn][k][0];
+        v[k] = w[k][0];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v[k] += words[turn][k][w];
+        for (int i = 1; i < kWaves; ++i) v[k] += w[k][i];
       }
       turn ^= 1;
     }
@@ -222,8 +245,10 @@ __device__ __forceinline__ Stats mean_of(double sum, double per_value) {
   // (infinite or NaN: nothing is left)
   return Stats{mean, float(m - double(mean)), 0.0f};
 }
-__device__ __forceinline__ float rstd_of(double squares, double per_value, float eps) {
-  return 1.0f / sqrtf(float(squares * per_value) + eps);
+// From the mean square around m.mean, whose own mean is m.rest.
+__device__ __forceinline__ float rstd_of(float square, float rest, float eps) {
+  const float var = square - rest * rest;
+  return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
 }
 
 // The same for all lanes of a wave.
@@ -266,24 +291,22 @@ __global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_kernel(NormArgs a) {
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     at[j] = columns_of<U, SHARE>(a.cols, j, t);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      w[j * U + i] = affine(a.weight, a.affine_f32, at[j].first + i, 1.0f);
-      b[j * U + i] = affine(a.bias, a.affine_f32, at[j].first + i, 0.0f);
-    }
+    affine_values<U>(a.weight, a.affine_f32, at[j].first, 1.0f, w + j * U);
+    affine_values<U>(a.bias, a.affine_f32, at[j].first, 0.0f, b + j * U);
   }
   constexpr int kSet = sets_of(J * Raw<XF32, U>::kWords, 96);
   Raw<XF32, U> x[kSet][J];
   walk<kSet>(
       first_row<SHARE>(), int64_t(gridDim.x) * kRows, a.rows,
       [&](int set, int64_t row) {
-        const char* p = static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>;
+        const char* p = uniform(static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>);
 #pragma unroll
         for (int j = 0; j < J; ++j)
           if (at[j].again < U) x[set][j].load(p, at[j].first);
       },
       [&](int set, int64_t row) {
         // a row's threads leave together: with more than one wave a row, a workgroup has one
+        using Total = std::conditional_t<XF32, double, float>;
         auto sum_of = [&](auto value) {
           decltype(value(0.0f)) s = 0;
 #pragma unroll
@@ -299,25 +322,27 @@ __global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_kernel(NormArgs a) {
           }
           return s;
         };
-        double total[1] = {sum_of([](float v) { return double(v); })};
+        // a few bf16 numbers add up exactly in fp32, or nearly
+        double total[1] = {double(sum_of([](float v) { return Total(v); }))};
         sum.template operator()<1>(total);
         Stats m = mean_of(total[0], per_value);
-        total[0] = double(sum_of([&](float v) {
-          const float d = v - m.mean - m.rest;
+        float square[1] = {sum_of([&](float v) {
+          const float d = v - m.mean;
           return d * d;
-        }));
-        sum.template operator()<1>(total);
+        })};
+        sum.template operator()<1>(square);
 #pragma unroll
         for (int j = 0; j < J; ++j) x[set][j].renewed();
-        m.rstd = rstd_of(total[0], per_value, a.eps);
-        char* out = static_cast<char*>(a.out) + row * a.out_ld * kSize<YF32>;
+        m.rstd = rstd_of(square[0] / float(a.cols), m.rest, a.eps);
+        const float back = -m.rest * m.rstd;
+        char* out = const_cast<char*>(uniform(static_cast<const char*>(a.out) + row * a.out_ld * kSize<YF32>));
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if (at[j].again == U) continue;
           float y[U];
 #pragma unroll
           for (int i = 0; i < U; ++i)
-            y[i] = (x[set][j].value(i) - m.mean - m.rest) * m.rstd * w[j * U + i] + b[j * U + i];
+            y[i] = fmaf(fmaf(x[set][j].value(i) - m.mean, m.rstd, back), w[j * U + i], b[j * U + i]);
           Raw<YF32, U> v;
           v.set(y);
           v.store(out, at[j].first);
@@ -335,17 +360,15 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
   __shared__ double words[2][2][SHARE / 64];
   RowSum<SHARE> sum{words};
   const int t = threadIdx.x % SHARE;
-  const double per_value = 1.0 / double(a.cols);
+  const float per_value = 1.0f / float(a.cols);
   float w[J * U], dw[J * U], db[J * U];
   Columns at[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     at[j] = columns_of<U, SHARE>(a.cols, j, t);
+    affine_values<U>(a.weight, a.affine_f32, at[j].first, 1.0f, w + j * U);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      w[j * U + i] = affine(a.weight, a.affine_f32, at[j].first + i, 1.0f);
-      dw[j * U + i] = db[j * U + i] = 0.0f;
-    }
+    for (int i = 0; i < U; ++i) dw[j * U + i] = db[j * U + i] = 0.0f;
   }
   constexpr int kSet = sets_of(J * (Raw<XF32, U>::kWords + Raw<YF32, U>::kWords), 24);
   Raw<XF32, U> x[kSet][J];
@@ -354,8 +377,8 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
   walk<kSet>(
       first_row<SHARE>(), int64_t(gridDim.x) * kRows, a.rows,
       [&](int set, int64_t row) {
-        const char* px = static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>;
-        const char* py = static_cast<const char*>(a.dy) + row * a.dy_ld * kSize<YF32>;
+        const char* px = uniform(static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>);
+        const char* py = uniform(static_cast<const char*>(a.dy) + row * a.dy_ld * kSize<YF32>);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if (at[j].again == U) continue;
@@ -375,10 +398,10 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
           for (int i = 0; i < U; ++i) {
             const int k = j * U + i;
             const float dy = y[set][j].value(i), xh = (x[set][j].value(i) - mean[set]) * rstd[set], g = dy * w[k];
-            dw[k] += dy * xh;
+            dw[k] = fmaf(dy, xh, dw[k]);
             db[k] += dy;
             gs += g;
-            gx += g * xh;
+            gx = fmaf(g, xh, gx);
           }
           if (at[j].again > 0) {
             gs = gx = 0.0f;
@@ -387,13 +410,14 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
               if (i < at[j].again) continue;
               const float g = y[set][j].value(i) * w[j * U + i];
               gs += g;
-              gx += g * ((x[set][j].value(i) - mean[set]) * rstd[set]);
+              gx = fmaf(g, (x[set][j].value(i) - mean[set]) * rstd[set], gx);
             }
           }
           s += gs;
           sx += gx;
+          __builtin_amdgcn_sched_barrier(0);
         }
-        double both[2] = {double(s), double(sx)};
+        float both[2] = {s, sx};
         sum.template operator()<2>(both);
         // (kept from above, the values would take twice the rows' registers)
 #pragma unroll
@@ -401,9 +425,9 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
           x[set][j].renewed();
           y[set][j].renewed();
         }
-        s = float(both[0] * per_value);
-        sx = float(both[1] * per_value);
-        char* out = static_cast<char*>(a.out) + row * a.out_ld * kSize<XF32>;
+        s = both[0] * per_value;
+        sx = -both[1] * per_value;
+        char* out = const_cast<char*>(uniform(static_cast<const char*>(a.out) + row * a.out_ld * kSize<XF32>));
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if (at[j].again == U) continue;
@@ -411,11 +435,12 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
 #pragma unroll
           for (int i = 0; i < U; ++i) {
             const float xh = (x[set][j].value(i) - mean[set]) * rstd[set];
-            d[i] = rstd[set] * (y[set][j].value(i) * w[j * U + i] - s - xh * sx);
+            d[i] = rstd[set] * fmaf(xh, sx, fmaf(y[set][j].value(i), w[j * U + i], -s));
           }
           Raw<XF32, U> v;
           v.set(d);
           v.store(out, at[j].first);
+          __builtin_amdgcn_sched_barrier(0);
         }
       });
   if (a.partial == nullptr) return;
@@ -527,13 +552,13 @@ __global__ __launch_bounds__(kWideBlock) void wide_norm_kernel(NormArgs a) {
       float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWideU; ++i) {
-        const float d = v.value(i) - m.mean - m.rest;
+        const float d = v.value(i) - m.mean;
         if (i < left) s += d * d;
       }
       total[0] += double(s);
     });
     sum.template operator()<1>(total);
-    m.rstd = rstd_of(total[0], per_value, a.eps);
+    m.rstd = rstd_of(float(total[0] * per_value), m.rest, a.eps);
     each([&](const Raw<XF32, kWideU>& v, int64_t c, int left) {
       float y[kWideU];
 #pragma unroll
@@ -679,6 +704,7 @@ int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad,
   const dim3 grid(static_cast<unsigned>(s.groups));
   if (s.share == 0) return launch_wide<XF32, YF32>(c, s, a, grad, st);
   constexpr int kPer = XF32 || YF32 ? 2 : 1;  // pieces of 8 values
+  constexpr int kMore = kPer == 2 ? 3 : 2, kFive = kPer == 2 ? 5 : 3;
 #define TIDE_NORM(KERNEL, SHARE, J) hipLaunchKernelGGL((KERNEL<XF32, YF32, SHARE, J>), grid, dim3(kBlock<SHARE>), 0, st, a)
   if (grad) {
     if (s.share == 64 && s.j <= kPer)
@@ -689,12 +715,12 @@ int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad,
       TIDE_NORM(layer_norm_grad_kernel, 256, kPer);
     else if (s.share == 256)
       TIDE_NORM(layer_norm_grad_kernel, 256, 2 * kPer);
-    else if (s.share == 512 && kPer == 2 && s.j == 3)
-      TIDE_NORM(layer_norm_grad_kernel, 512, 3);
+    else if (s.share == 512 && s.j <= kMore)
+      TIDE_NORM(layer_norm_grad_kernel, 512, kMore);
     else if (s.share == 512)
       TIDE_NORM(layer_norm_grad_kernel, 512, 2 * kPer);
-    else if (kPer == 2 && s.j == 3)
-      TIDE_NORM(layer_norm_grad_kernel, 1024, 3);
+    else if (s.j <= kMore)
+      TIDE_NORM(layer_norm_grad_kernel, 1024, kMore);
     else
       TIDE_NORM(layer_norm_grad_kernel, 1024, 2 * kPer);
   } else {
@@ -708,8 +734,8 @@ int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad,
       TIDE_NORM(layer_norm_kernel, 256, kPer);
     else if (s.j <= 2 * kPer)
       TIDE_NORM(layer_norm_kernel, 256, 2 * kPer);
-    else if (kPer == 2 && s.j == 5)
-      TIDE_NORM(layer_norm_kernel, 256, 5);
+    else if (s.j <= kFive)
+      TIDE_NORM(layer_norm_kernel, 256, kFive);
     else if (s.j <= 3 * kPer)
       TIDE_NORM(layer_norm_kernel, 256, 3 * kPer);
     else

@@ -20,6 +20,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "gemm.h"
 #include "training.h"
@@ -150,15 +151,16 @@ struct GatedArgs {
 // the epilogue takes no LDS, its stores are 16 bytes a lane, 64 a row, from one
 // shared address and the lane's offset, and dh's rows are asked for before the
 // first is used.  GRAD: dg and du instead of h.
-template <bool GRAD, int SIDE, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64, 2) void gated_kernel(GatedArgs a) {
-  using G = Gemm<Form::kRows, Form::kPair, Code::kE4m3, SIDE, SIDE, WM, WN, false, true>;
+template <bool GRAD, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, BM == 64 ? 1 : 2) void gated_kernel(GatedArgs a) {
+  using G = std::conditional_t<BM == 64, DeepGemm<Form::kRows, Form::kPair, BM, BN, WM, WN, false, 2>,
+                               Gemm<Form::kRows, Form::kPair, Code::kE4m3, BM, BN, WM, WN, false, true>>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
   __shared__ uint32_t turn;
-  static_assert(G::kFN == 4 && SIDE / WN == 64, "8 columns a lane");
+  static_assert(G::kFN == 4 && BN / WN == 64, "8 columns a lane");
   Queue q;
   uint32_t item = blockIdx.x;
   if (a.queue) item = first_item(q, a.queue, a.cut.items, &turn);
@@ -170,8 +172,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void gated_kernel(GatedArgs a) {
     const Piece p = piece_of<false>(a.cut, item, a.depth);
     uint32_t tm, tn;
     tile_of(p.tile, a.tiles_m, a.tiles_n, 4, &tm, &tn);
-    m0 = int64_t(tm) * SIDE;
-    n0 = int64_t(tn) * (SIDE / 2);
+    m0 = int64_t(tm) * BM;
+    n0 = int64_t(tn) * (BN / 2);
     slot = p.slot;
     g.open(a.x, a.w, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
   };
@@ -182,7 +184,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void gated_kernel(GatedArgs a) {
     const uint32_t k = a.queue ? q.ask() : 0;
     const int64_t s1 = slot;
     // this wave's part of the tile: rows from m1, 16 at a time, columns from n1; this lane's row and columns of it
-    const int64_t m1 = m0 + g.wm * (SIDE / WM), n1 = n0 + g.wn * 32;
+    const int64_t m1 = m0 + g.wm * (BM / WM), n1 = n0 + g.wn * 32;
     g.renew_lane();
     const uint32_t row = g.lane & 15, col = uint32_t(g.lane >> 4) * 8;
     const int64_t left = a.f.cols - n1 - col, rows = a.f.rows - m1 - row;
@@ -208,11 +210,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void gated_kernel(GatedArgs a) {
     for (int i = 0; i < G::kFM; ++i) {
       const f32x4v g0 = g.acc[i][0], g1 = g.acc[i][1], u0 = g.acc[i][2], u1 = g.acc[i][3];
       if (s1 >= 0) {
-        float* p = a.partial + s1 * SIDE * SIDE + (g.wm * (SIDE / WM) + 16 * i + row) * SIDE + g.wn * 32 + col;
+        float* p = a.partial + s1 * BM * BN + (g.wm * (BM / WM) + 16 * i + row) * BN + g.wn * 32 + col;
         *reinterpret_cast<f32x4v*>(p) = g0;
         *reinterpret_cast<f32x4v*>(p + 4) = g1;
-        *reinterpret_cast<f32x4v*>(p + SIDE / 2) = u0;
-        *reinterpret_cast<f32x4v*>(p + SIDE / 2 + 4) = u1;
+        *reinterpret_cast<f32x4v*>(p + BN / 2) = u0;
+        *reinterpret_cast<f32x4v*>(p + BN / 2 + 4) = u1;
       } else if constexpr (GRAD) {
         if (16 * i < rows && col + n1 < a.f.half) {
           u32x4 dg, du;
@@ -361,8 +363,9 @@ __device__ __forceinline__ uint32_t grad_tile(const GradArgs& a, uint32_t tile, 
 }
 
 template <Form FA, Form FB, int SIDE, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64, 2) void gated_grad_kernel(GradArgs a) {
-  using G = Gemm<FA, FB, Code::kE4m3, SIDE, SIDE, WM, WN, false, FB == Form::kStack>;
+__global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void gated_grad_kernel(GradArgs a) {
+  using G = std::conditional_t<SIDE == 64, DeepGemm<FA, FB, SIDE, SIDE, WM, WN, false, 4>,
+                               Gemm<FA, FB, Code::kE4m3, SIDE, SIDE, WM, WN, false, FB == Form::kStack>>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
@@ -426,30 +429,9 @@ __global__ __launch_bounds__(256) void clear_gradients_kernel(uint16_t* a, uint1
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// A product's tiles: the side and the cut that are estimated to end first.
-struct Tiling {
-  int64_t side = 256, tiles_m = 0, tiles_n = 0;
-  Cut cut{};
-};
-Tiling tiling(int64_t m, int64_t n, int64_t products, int64_t depth, int64_t columns_of_256) {
-  const int64_t steps = (depth + kBK - 1) / kBK;
-  Tiling best;
-  double least = 0;
-  for (int64_t side : {256, 128}) {
-    Tiling t;
-    t.side = side;
-    t.tiles_m = (m + side - 1) / side;
-    const int64_t across = columns_of_256 * side / 256;
-    t.tiles_n = (n + across - 1) / across;
-    t.cut = cut_tiles(t.tiles_m * t.tiles_n * products, steps, side);
-    const double cost = cut_cost(t.cut, steps, side);
-    if (side == 256 || cost < least) {
-      best = t;
-      least = cost;
-    }
-  }
-  return best;
-}
+int64_t tiles_on(int64_t n, int64_t side) { return (n + side - 1) / side; }
+// Columns of g and u in a tile.
+int64_t pair_columns(int64_t side) { return side == 64 ? 64 : side / 2; }
 
 constexpr int64_t kFew = 16;       // tokens that few_gated_kernel takes
 constexpr uint32_t kProducts = 3;  // g and u; dx; dWg and dWu
@@ -491,12 +473,14 @@ Layout layout_of(const GatedCall& c) {
     L.queued |= t.cut.items > tile_slots(t.side);
   };
   if (L.gates && !L.few) {
-    L.fwd = tiling(c.tokens, c.ffn, 1, c.hidden, 128);
+    L.fwd = tiling_of(L.depth / kBK,
+                      [&](int64_t side) { return tiles_on(c.tokens, side) * tiles_on(c.ffn, pair_columns(side)); });
     also(L.fwd);
   }
   if (c.grad) {
-    L.dx = tiling(c.tokens, c.hidden, 1, 2 * L.half, 256);
-    L.dw = tiling(c.ffn, c.hidden, 2, c.tokens, 256);
+    L.dx = tiling_of(2 * L.half / kBK, [&](int64_t side) { return tiles_on(c.tokens, side) * tiles_on(c.hidden, side); });
+    L.dw = tiling_of((c.tokens + kBK - 1) / kBK,
+                     [&](int64_t side) { return 2 * tiles_on(c.ffn, side) * tiles_on(c.hidden, side); });
     also(L.dx);
     also(L.dw);
   }
@@ -519,14 +503,16 @@ template <Form FA, Form FB>
 int launch_grad(GradArgs a, const Tiling& t, float* partial, uint32_t* queue, hipStream_t st) {
   a.cut = t.cut;
   a.partial = partial;
-  a.tiles_m = uint32_t(t.tiles_m);
-  a.tiles_n = uint32_t(t.tiles_n);
+  a.tiles_m = uint32_t(tiles_on(a.to[0].rows, t.side));
+  a.tiles_n = uint32_t(tiles_on(a.to[0].cols, t.side));
   a.queue = t.cut.items > tile_slots(t.side) ? queue : nullptr;
   const dim3 grid(resident_groups(t.cut.items, t.side));
   if (t.side == 256)
     hipLaunchKernelGGL((gated_grad_kernel<FA, FB, 256, 2, 4>), grid, dim3(512), 0, st, a);
-  else
+  else if (t.side == 128)
     hipLaunchKernelGGL((gated_grad_kernel<FA, FB, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((gated_grad_kernel<FA, FB, 64, 2, 2>), grid, dim3(256), 0, st, a);
   TIDE_LAUNCHED();
   if (t.cut.splits == 1) return 0;
   const unsigned rest = t.cut.tiles - t.cut.full;
@@ -617,28 +603,36 @@ int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
     a.depth = L.depth;
     a.cut = L.fwd.cut;
     a.partial = partial;
-    a.tiles_m = uint32_t(L.fwd.tiles_m);
-    a.tiles_n = uint32_t(L.fwd.tiles_n);
+    a.tiles_m = uint32_t(tiles_on(c.tokens, L.fwd.side));
+    a.tiles_n = uint32_t(tiles_on(c.ffn, pair_columns(L.fwd.side)));
     a.queue = a.cut.items > tile_slots(L.fwd.side) ? queues : nullptr;
     a.f = f;
     const dim3 grid(resident_groups(a.cut.items, L.fwd.side));
-    const unsigned rest = a.cut.tiles - a.cut.full;
     if (L.fwd.side == 256) {
       if (c.grad)
-        hipLaunchKernelGGL((gated_kernel<true, 256, 2, 4>), grid, dim3(512), 0, st, a);
+        hipLaunchKernelGGL((gated_kernel<true, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
       else
-        hipLaunchKernelGGL((gated_kernel<false, 256, 2, 4>), grid, dim3(512), 0, st, a);
-      TIDE_LAUNCHED();
-      if (a.cut.splits > 1) hipLaunchKernelGGL(join_gated_kernel<256>, dim3(rest * 16), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((gated_kernel<false, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
+    } else if (L.fwd.side == 128) {
+      if (c.grad)
+        hipLaunchKernelGGL((gated_kernel<true, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((gated_kernel<false, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
     } else {
       if (c.grad)
-        hipLaunchKernelGGL((gated_kernel<true, 128, 2, 2>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((gated_kernel<true, 64, 128, 2, 2>), grid, dim3(256), 0, st, a);
       else
-        hipLaunchKernelGGL((gated_kernel<false, 128, 2, 2>), grid, dim3(256), 0, st, a);
-      TIDE_LAUNCHED();
-      if (a.cut.splits > 1) hipLaunchKernelGGL(join_gated_kernel<128>, dim3(rest * 4), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((gated_kernel<false, 64, 128, 2, 2>), grid, dim3(256), 0, st, a);
     }
     TIDE_LAUNCHED();
+    if (a.cut.splits > 1) {
+      const unsigned rest = a.cut.tiles - a.cut.full;
+      if (L.fwd.side == 256)
+        hipLaunchKernelGGL(join_gated_kernel<256>, dim3(rest * 16), dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL(join_gated_kernel<128>, dim3(rest * 4), dim3(256), 0, st, a);
+      TIDE_LAUNCHED();
+    }
   }
   if (!c.grad) return 0;
 

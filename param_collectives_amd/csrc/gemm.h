@@ -26,7 +26,8 @@
 //     group 16 different places (r / 4 mod 4 does not: measured, bank conflicts
 //     in 21% of a kernel's cycles);
 //   kCols, kStack, kPacked tile [32 k][rows]: chunk c of row k is kept at
-//     c ^ 2 f(k), f(k) made of bits 0, 1 and 3 of k; a fragment is read by the
+//     c ^ 2 f(k), f(k) made of bits 0, 1 and 3 of k (of 64 columns, whose rows
+//     are half a turn of the banks, of bits 1 and 3); a fragment is read by the
 //     transposing LDS read, whose 32 lanes touch 8 rows k of 32 bytes each.
 // The products take the n side first, so a lane holds 4 consecutive n of one m.
 #pragma once
@@ -91,8 +92,8 @@ __device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, v
 // on their way and, with LGKM, until its LDS accesses are done.
 template <int N, bool LGKM>
 __device__ __forceinline__ void wait_loads() {
-  static_assert(N < 16, "the counter's low bits");
-  __builtin_amdgcn_s_waitcnt((LGKM ? 0x0070 : 0x0F70) | N);
+  static_assert(N < 64, "the counter's bits");
+  __builtin_amdgcn_s_waitcnt((LGKM ? 0x0070 : 0x0F70) | (N & 15) | (N >> 4) << 14);
 }
 
 // A barrier that waits for nothing but the other waves: what must have arrived
@@ -205,6 +206,9 @@ struct Side {
   // (kPair: a fragment's rows 4 b .. 4 b + 3 are the tile's 8 b .. 8 b + 3, or the
   // four after them, so that a lane holds 8 neighbouring columns of C; the swizzle
   // goes with the fragment's rows.)
+  static __device__ __forceinline__ int swizzle_of_k(int k) {
+    return ROWS == 64 ? (k & 2) | ((k >> 1) & 4) : col_swizzle(k);
+  }
   static __device__ __forceinline__ int swizzle(int r) { return row_swizzle(kPair ? r >> 1 : r); }
   static __device__ __forceinline__ int part_k(int lin) {
     return kAlong ? ((lin & 3) ^ swizzle(lin >> 2)) * 8 : lin / (kPacked ? ROWS / 16 : kRowChunks);
@@ -232,7 +236,7 @@ struct Side {
       step = o.ld * (kBK * 2);
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
-        const int lin = i * THREADS + tid, k = part_k(lin), c = (lin % kRowChunks) ^ col_swizzle(k);
+        const int lin = i * THREADS + tid, k = part_k(lin), c = (lin % kRowChunks) ^ swizzle_of_k(k);
         off[i] = uint32_t(k) * uint32_t(o.ld * 2) + (c * 8 <= last ? uint32_t(c * 16) : 0u);
       }
     } else {
@@ -246,7 +250,7 @@ struct Side {
         const bool in = u * 16 <= last;
         off[i] = uint32_t(k) * uint32_t(o.ld) + (in ? uint32_t(u * 16) : 0u);
         scale_off[i] = uint32_t(k) * uint32_t(o.scale_ld) + (in ? uint32_t(u >> 1) : 0u);
-        put[i] = uint32_t((k * kRowChunks + ((2 * u) ^ col_swizzle(k))) * 16);
+        put[i] = uint32_t((k * kRowChunks + ((2 * u) ^ swizzle_of_k(k))) * 16);
       }
     }
   }
@@ -324,7 +328,7 @@ struct Side {
       // a transposing read gives lane l of 16 the values of column l in the
       // four rows k of which lanes 4j .. 4j+3 point at 4 columns each
       const int k = 8 * (lane >> 4) + ((lane & 15) >> 2), col = r0 + 4 * (lane & 3);
-      const uint32_t first = uint32_t((k * kRowChunks + ((col >> 3) ^ col_swizzle(k))) * 16 + (col & 4) * 2);
+      const uint32_t first = uint32_t((k * kRowChunks + ((col >> 3) ^ swizzle_of_k(k))) * 16 + (col & 4) * 2);
 #pragma unroll
       for (int i = 0; i < kSpots; ++i) at[i] = spot(first, i);
     }
@@ -770,14 +774,14 @@ struct Gemm {
     }
   }
 
-  // The same, where f may change the values; with `mirror` also t(row, values of 8
+  // The same, where f may change the values; with `mirror` also t(row, q, values of 8
   // rows of a column) of the changed values: rows `row` + 0..7 or, in the odd lanes,
-  // 8..15, of column mirror_column() (+ 32 in the second call).
+  // 8..15, of column mirror_column() + 32 q.
   __device__ __forceinline__ int mirror_column() const { return wn * (BN / WN) + (lane >> 1); }
   template <typename P, typename F, typename T, typename H>
   __device__ __forceinline__ void each_mirrored(char* lds, bool mirror, P before, F f, T t, H halfway) {
     constexpr int kCols = BN / WN, kMask = kCols / 4 - 1, kRows = 64 / kRowGroups;
-    static_assert(kCols == 64 && WM * WN * 16 * kCols * 4 <= kStage, "epilogue rows");
+    static_assert(kCols % 32 == 0 && WM * WN * 16 * kCols * 4 <= kStage, "epilogue rows");
     float* rows = reinterpret_cast<float*>(lds) + wave_index() * 16 * kCols;
     const int w = lane & 15, c = lane % kRowGroups;
     before(0);
@@ -804,7 +808,7 @@ struct Gemm {
       if (mirror) {
         const int r0 = (lane & 1) * 8;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kCols / 32; ++q) {
           const int n = (lane >> 1) + 32 * q;
           f32x4v lo, hi;
 #pragma unroll
@@ -875,6 +879,147 @@ struct Gemm {
     else
       each<false>(
           lds, [&](int r, int c, f32x4v lo, f32x4v hi) { put_some(t, m0 + r, n0 + c, lo, hi); }, halfway);
+  }
+};
+
+// The same for small tiles of few products, whose time is that of their loads on
+// their way: a stage is U steps, so up to 3 U of them are, and a barrier comes once
+// in U steps.  The steps are filled up to a multiple of 4 U with empty ones, which
+// go first; a short last step goes last, filled up with zeros.  (A 64 x 64 tile's
+// step takes about 0.1 us, where a 128 x 128 tile's, four times the products, takes
+// 0.45 us with three steps on their way.)
+template <Form FA, Form FB, int BM, int BN, int WM, int WN, bool F16, int U>
+struct DeepGemm : Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true> {
+  using Base = Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true>;
+  using typename Base::SA;
+  using typename Base::SB;
+  using Base::kFM;
+  using Base::kFN;
+  using Base::sa;
+  using Base::sb;
+  using Base::acc;
+  using Base::tid;
+  using Base::s;
+  using Base::first;
+  using Base::whole;
+  using Base::rounds;
+  using Base::left;
+  static constexpr int kStage = U * Base::kStage;
+  static constexpr int kLoads = U * (SA::kLoads + SB::kLoads);  // of a stage
+
+  __device__ __forceinline__ void fetch_step(char* stage, int u, int64_t step) {
+    typename SA::Held na;
+    typename SB::Held nb;
+    char *la = stage + u * SA::kBytes, *lb = stage + U * SA::kBytes + u * SB::kBytes;
+    if (step >= first && step < whole) {
+      sa.template fetch<false>(la, na, step, 0, tid);
+      sb.template fetch<false>(lb, nb, step, 0, tid);
+    } else {
+      const bool tail = step == whole;
+      sa.template fetch<true>(la, na, tail ? whole : first, tail ? left : 0, tid);
+      sb.template fetch<true>(lb, nb, tail ? whole : first, tail ? left : 0, tid);
+    }
+  }
+  __device__ __forceinline__ void fetch_stage(char* stage, int64_t step) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch_step(stage, u, step + u);
+  }
+  // Load n of a whole stage's.
+  __device__ __forceinline__ void fetch_part(char* stage, int64_t step, int n) {
+    constexpr int kEach = SA::kParts + SB::kParts;
+    const int u = n / kEach, i = n % kEach;
+    if (i < SA::kParts)
+      sa.fetch_part(stage + u * SA::kBytes, step + u, i);
+    else
+      sb.fetch_part(stage + U * SA::kBytes + u * SB::kBytes, step + u, i - SA::kParts);
+  }
+
+  __device__ __forceinline__ void open(const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k_first,
+                                       int64_t k_end, char* l0, char* l1, char* l2) {
+    sa.init(a, m0, tid);
+    sb.init(b, n0, tid);
+    first = k_first / kBK;
+    whole = k_end > k_first ? k_end / kBK : first;
+    left = k_end > k_first ? int(k_end - whole * kBK) : 0;
+    const int64_t steps = whole - first + (left > 0 ? 1 : 0);
+    rounds = (steps + 4 * U - 1) / (4 * U);
+    s = first + steps - rounds * 4 * U;
+    if (rounds == 0) return;
+    fetch_stage(l0, s);
+    fetch_stage(l1, s + U);
+    fetch_stage(l2, s + 2 * U);
+  }
+
+  __device__ __forceinline__ void loop(char* l0, char* l1, char* l2, char* l3) {
+    bf16x8 fa[kFM], fb[kFN];
+    auto read = [&](const char* stage, int u) {
+#pragma unroll
+      for (int i = 0; i < kFM; ++i) fa[i] = SA::fragment(stage + u * SA::kBytes, Base::at_a, i);
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) fb[j] = SB::fragment(stage + U * SA::kBytes + u * SB::kBytes, Base::at_b, j);
+    };
+    // Multiplies the stage in `now`, whose first step's fragments have been read, and
+    // reads those of the stage in `next`; LOAD: starts the loads of the stage 3 on.
+    auto stage = [&](const char* now, const char* next, char* to3, bool load, bool more) {
+      const bool plain = s + 3 * U >= first && s + 4 * U <= whole;
+      if (load && !plain) fetch_stage(to3, s + 3 * U);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        bf16x8 a[kFM], b[kFN];
+#pragma unroll
+        for (int i = 0; i < kFM; ++i) a[i] = fa[i];
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) b[j] = fb[j];
+        if (u + 1 < U)
+          read(now, u + 1);
+        else if (more)
+          read(next, 0);
+        if (load && plain) {
+#pragma unroll
+          for (int n = u * kLoads / U; n < (u + 1) * kLoads / U; ++n) fetch_part(to3, s + 3 * U, n);
+        }
+#pragma unroll
+        for (int i = 0; i < kFM; ++i)
+#pragma unroll
+          for (int j = 0; j < kFN; ++j) acc[i][j] = Base::product(b[j], a[i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      s += U;
+    };
+#pragma unroll
+    for (int i = 0; i < kFM; ++i)
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    if (rounds > 0) {
+      wait_loads<2 * kLoads, true>();
+      bare_barrier();
+      read(l0, 0);
+      for (int64_t r = 1; r < rounds; ++r) {
+        wait_loads<kLoads, false>();
+        bare_barrier();
+        stage(l0, l1, l3, true, true);
+        wait_loads<kLoads, false>();
+        bare_barrier();
+        stage(l1, l2, l0, true, true);
+        wait_loads<kLoads, false>();
+        bare_barrier();
+        stage(l2, l3, l1, true, true);
+        wait_loads<kLoads, false>();
+        bare_barrier();
+        stage(l3, l0, l2, true, true);
+      }
+      wait_loads<kLoads, false>();
+      bare_barrier();
+      stage(l0, l1, l3, true, true);
+      wait_loads<kLoads, false>();
+      bare_barrier();
+      stage(l1, l2, nullptr, false, true);
+      wait_loads<0, false>();
+      bare_barrier();
+      stage(l2, l3, nullptr, false, true);
+      stage(l3, nullptr, nullptr, false, false);
+    }
+    lds_barrier();
   }
 };
 

@@ -21,6 +21,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "gemm.h"
 #include "training.h"
@@ -60,6 +61,10 @@ __host__ __device__ __forceinline__ int64_t padded(int64_t n) { return (n + kBK 
 struct Pointers {
   void* p[kMost];
 };
+
+template <Form FA, Form FB, int SIDE, int WM, int WN>
+using Products = std::conditional_t<SIDE == 64, DeepGemm<FA, FB, SIDE, SIDE, WM, WN, true, 4>,
+                                    Gemm<FA, FB, Code::kE4m3, SIDE, SIDE, WM, WN, true, true>>;
 
 // ------------------------------------------------------------ the norm
 
@@ -199,8 +204,8 @@ __device__ __forceinline__ void symmetric_tile(const SymmetricArgs& a, uint32_t 
 }
 
 template <Form F, int SIDE, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64, 2) void symmetric_kernel(SymmetricArgs a) {
-  using G = Gemm<F, F, Code::kE4m3, SIDE, SIDE, WM, WN, true, true>;
+__global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_kernel(SymmetricArgs a) {
+  using G = Products<F, F, SIDE, WM, WN>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
@@ -237,14 +242,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void symmetric_kernel(SymmetricArgs
     const int64_t first = z * a.matrix + m1 * a.ld + n1;
     uint16_t* const mirrored = a.out + z * a.matrix + n1 * a.ld + m1;
     // G's values of the rows that come next
-    u32x4 old[2][2];
+    constexpr int kRows = 64 / G::kRowGroups, kCalls = 16 / kRows;  // rows of a call, calls of 16 rows
+    u32x4 old[2][kCalls];
     auto before = [&](int i) {
       if (a.g == nullptr || s1 >= 0) return;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int r = g.wm * (SIDE / WM) + i * 16 + q * 8;
+      for (int q = 0; q < kCalls; ++q) {
+        const int r = g.wm * (SIDE / WM) + i * 16 + q * kRows;
         if (r < rows && left > 0) old[i & 1][q] = *reinterpret_cast<const u32x4*>(a.g + first + ahead);
-        ahead += 8 * ld;
+        ahead += kRows * ld;
       }
     };
     // rows of the mirrored tile are this one's columns
@@ -257,7 +263,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void symmetric_kernel(SymmetricArgs
           if (s1 >= 0) return put_slot<SIDE>(a.partial, s1, r + row, g.column(), lo, hi);
           const f32x8v v = a.value(m1 + r + row, n1 + g.column(), lo, hi, a.g ? old[i & 1][q] : u32x4{0, 0, 0, 0});
           if (r < rows && left > 0) *reinterpret_cast<u32x4*>(a.out + first + at) = eight_f16(v);
-          at += 8 * ld;
+          at += kRows * ld;
           lo = __builtin_shufflevector(v, v, 0, 1, 2, 3);
           hi = __builtin_shufflevector(v, v, 4, 5, 6, 7);
         },
@@ -388,8 +394,8 @@ __device__ __forceinline__ void update_tile(const UpdateArgs& a, uint32_t t, int
 }
 
 template <Form FB, int SIDE, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64, 2) void update_kernel(UpdateArgs a) {
-  using G = Gemm<Form::kRows, FB, Code::kE4m3, SIDE, SIDE, WM, WN, true, true>;
+__global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void update_kernel(UpdateArgs a) {
+  using G = Products<Form::kRows, FB, SIDE, WM, WN>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
@@ -429,17 +435,18 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void update_kernel(UpdateArgs a) {
     const int64_t first = z * a.matrix + m1 * a.ld + n1;
     uint16_t* out = static_cast<uint16_t*>(a.out.p[z]) + m1 * a.out_ld + n1;
     // X's values of the rows that come next
-    u32x4 x[2][2], y[2][2];
+    constexpr int kRows = 64 / G::kRowGroups, kCalls = 16 / kRows;  // rows of a call, calls of 16 rows
+    u32x4 x[2][kCalls], y[2][kCalls];
     auto before = [&](int i) {
       if (a.hi == nullptr || s1 >= 0) return;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int r = g.wm * (SIDE / WM) + i * 16 + q * 8;
+      for (int q = 0; q < kCalls; ++q) {
+        const int r = g.wm * (SIDE / WM) + i * 16 + q * kRows;
         if (r - rows < row_pad && left > -col_pad) {
           x[i & 1][q] = *reinterpret_cast<const u32x4*>(a.hi + first + ahead);
           y[i & 1][q] = *reinterpret_cast<const u32x4*>(a.lo + first + ahead);
         }
-        ahead += 8 * ld;
+        ahead += kRows * ld;
       }
     };
     g.each_rows(
@@ -447,8 +454,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void update_kernel(UpdateArgs a) {
         [&](int r, int i, int q, f32x4v lo, f32x4v hi) {
           if (s1 >= 0) return put_slot<SIDE>(a.partial, s1, r + row, g.column(), lo, hi);
           const uint32_t here = at, out_here = out_at;
-          at += 8 * ld;
-          out_at += 8 * out_ld;
+          at += kRows * ld;
+          out_at += kRows * out_ld;
           if (r - rows >= row_pad || left <= -col_pad) return;
           a.put(a.value(lo, hi, x[i & 1][q], y[i & 1][q]), r < rows ? left : 0, a.next + first + here,
                 a.lo + first + here, out + out_here);
@@ -485,30 +492,6 @@ __global__ __launch_bounds__(256) void join_update_kernel(UpdateArgs a) {
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-struct Tiling {
-  int64_t side = 256, tiles = 0;  // of all matrices
-  Cut cut{};
-};
-// The side and the cut that are estimated to end first, of tiles(side) tiles.
-template <typename F>
-Tiling tiling(int64_t depth, F tiles) {
-  const int64_t steps = (depth + kBK - 1) / kBK;
-  Tiling best;
-  double least = 0;
-  for (int64_t side : {256, 128}) {
-    Tiling t;
-    t.side = side;
-    t.tiles = tiles(side);
-    t.cut = cut_tiles(t.tiles, steps, side);
-    const double cost = cut_cost(t.cut, steps, side);
-    if (side == 256 || cost < least) {
-      best = t;
-      least = cost;
-    }
-  }
-  return best;
-}
-
 // Where one call's workspace keeps what, of `piece` matrices at a time.
 struct Layout {
   bool tall = false;
@@ -522,6 +505,7 @@ struct Layout {
 struct Tilings {
   Tiling gram, square, update;
 };
+int64_t steps_of(int64_t depth) { return padded(depth) / kBK; }
 Tilings tilings_of(const OrthogonalCall& c, const Layout& L, int64_t count) {
   const int64_t large = c.rows > c.cols ? c.rows : c.cols;
   auto triangle = [&](int64_t side) {
@@ -529,9 +513,9 @@ Tilings tilings_of(const OrthogonalCall& c, const Layout& L, int64_t count) {
     return count * t * (t + 1) / 2;
   };
   Tilings t;
-  t.gram = tiling(large, triangle);
-  t.square = tiling(L.small, triangle);
-  t.update = tiling(L.small, [&](int64_t side) { return count * ((c.rows + side - 1) / side) * ((c.cols + side - 1) / side); });
+  t.gram = tiling_of(steps_of(large), triangle);
+  t.square = tiling_of(steps_of(L.small), triangle);
+  t.update = tiling_of(steps_of(L.small), [&](int64_t side) { return count * ((c.rows + side - 1) / side) * ((c.cols + side - 1) / side); });
   return t;
 }
 
@@ -589,14 +573,16 @@ Layout layout_of(const OrthogonalCall& c) {
 template <Form F>
 int launch_symmetric(SymmetricArgs a, const Tiling& t, int64_t count, uint32_t* queue, hipStream_t st) {
   a.cut = t.cut;
-  a.tiles = uint32_t(t.tiles / count);
+  a.tiles = uint32_t(t.cut.tiles / count);
   a.side_tiles = uint32_t((a.size + t.side - 1) / t.side);
   a.queue = t.cut.items > tile_slots(t.side) ? queue : nullptr;
   const dim3 grid(resident_groups(t.cut.items, t.side));
   if (t.side == 256)
     hipLaunchKernelGGL((symmetric_kernel<F, 256, 2, 4>), grid, dim3(512), 0, st, a);
-  else
+  else if (t.side == 128)
     hipLaunchKernelGGL((symmetric_kernel<F, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((symmetric_kernel<F, 64, 2, 2>), grid, dim3(256), 0, st, a);
   TIDE_LAUNCHED();
   if (t.cut.splits == 1) return 0;
   const unsigned rest = t.cut.tiles - t.cut.full;
@@ -616,8 +602,10 @@ int launch_update(UpdateArgs a, const Tiling& t, uint32_t* queue, hipStream_t st
   const dim3 grid(resident_groups(t.cut.items, t.side));
   if (t.side == 256)
     hipLaunchKernelGGL((update_kernel<FB, 256, 2, 4>), grid, dim3(512), 0, st, a);
-  else
+  else if (t.side == 128)
     hipLaunchKernelGGL((update_kernel<FB, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((update_kernel<FB, 64, 2, 2>), grid, dim3(256), 0, st, a);
   TIDE_LAUNCHED();
   if (t.cut.splits == 1) return 0;
   const unsigned rest = t.cut.tiles - t.cut.full;

@@ -54,7 +54,9 @@ struct Cut {
 #define TIDE_BOTH
 #endif
 
-TIDE_BOTH inline int64_t tile_slots(int64_t side) { return side == 256 ? 256 : 512; }
+// Workgroups of tiles of a side that the 256 CUs hold at once, by their LDS: two a
+// CU of 128, one of 256 or, with as many loads on their way, of 64.
+TIDE_BOTH inline int64_t tile_slots(int64_t side) { return side == 128 ? 512 : 256; }
 
 // The rest is split so that its pieces fill a round, or not at all, whichever is
 // estimated to end first: a round takes its steps (0.72 us each for a 256 x 256
@@ -98,6 +100,37 @@ inline double cut_cost(const Cut& c, int64_t steps, int64_t side) {
   const int64_t slots = tile_slots(side), rounds = (c.full + slots - 1) / slots, more = (c.items - c.full + slots - 1) / slots;
   return double(rounds) * (double(steps) * step + tile) + double(more) * (double(c.per) * step + tile) +
          (c.splits > 1 ? 5.0 + 0.4e-6 * double(partial_bytes(c, side)) : 0.0);
+}
+
+// A product's tiles: the side (a small tile's is that of its rows) and the cut that
+// are estimated to end first.  tiles(side) counts them.  Tiles of 64 are not split: a
+// step of them takes 0.1 us, a tile about 3 more.
+struct Tiling {
+  int64_t side = 256;
+  Cut cut{};
+};
+template <typename F>
+inline Tiling tiling_of(int64_t steps, F tiles) {
+  Tiling best;
+  double least = 0;
+  for (int64_t side : {256, 128, 64}) {
+    Tiling t;
+    t.side = side;
+    const int64_t n = tiles(side);
+    double cost;
+    if (side == 64) {
+      t.cut = Cut{uint32_t(n), uint32_t(n), 1, uint32_t(steps), uint32_t(n)};
+      cost = double((n + 255) / 256) * (double(steps) * 0.1 + 3.0);
+    } else {
+      t.cut = cut_tiles(n, steps, side);
+      cost = cut_cost(t.cut, steps, side);
+    }
+    if (side == 256 || cost < least) {
+      best = t;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 // How a weight gradient is laid out, and its workspace: dy_bytes of aligned

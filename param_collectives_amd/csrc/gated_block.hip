@@ -175,7 +175,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM == 64 ? 1 : 2) void gated_kernel(Ga
     m0 = int64_t(tm) * BM;
     n0 = int64_t(tn) * (BN / 2);
     slot = p.slot;
-    g.open(a.x, a.w, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
+    g.open(a.x, a.w, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2, lds3);
   };
   const int32_t gelu = a.f.gelu;
   open(item);
@@ -370,6 +370,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void gated_grad_ke
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
+  __shared__ __align__(16) char own[own_rows<G, SIDE>()];
   __shared__ uint32_t turn;
   Queue q;
   uint32_t item = blockIdx.x;
@@ -388,7 +389,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void gated_grad_ke
     slot = p.slot;
     Operand left = a.a;
     left.base = static_cast<const char*>(left.base) + second * a.shift;
-    g.open(left, a.b, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
+    g.open(left, a.b, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2, lds3);
   };
   open(item);
   while (item != kNoItem) {
@@ -396,7 +397,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void gated_grad_ke
     const uint32_t k = a.queue ? q.ask() : 0;
     const Target t = slot >= 0 ? slot_target<SIDE>(a.partial, slot, a.to[0].rows - m0) : second ? a.to[1] : a.to[0];
     const int64_t m1 = slot >= 0 ? 0 : m0, n1 = slot >= 0 ? 0 : n0;
-    g.write_rows(t, m1, n1, lds3, [&] {
+    g.write_rows(t, m1, n1, SIDE == 64 ? own : lds3, [&] {
       item = a.queue ? next_item(q, k, &turn) : kNoItem;
       if (item != kNoItem) open(item);
     });
@@ -473,13 +474,15 @@ Layout layout_of(const GatedCall& c) {
     L.queued |= t.cut.items > tile_slots(t.side);
   };
   if (L.gates && !L.few) {
-    L.fwd = tiling_of(L.depth / kBK,
+    L.fwd = tiling_of(L.depth / kBK, 0,  // k along the rows of both
                       [&](int64_t side) { return tiles_on(c.tokens, side) * tiles_on(c.ffn, pair_columns(side)); });
     also(L.fwd);
   }
   if (c.grad) {
-    L.dx = tiling_of(2 * L.half / kBK, [&](int64_t side) { return tiles_on(c.tokens, side) * tiles_on(c.hidden, side); });
-    L.dw = tiling_of((c.tokens + kBK - 1) / kBK,
+    const int64_t w_ld = L.copy_w ? L.ld : c.gate_ld, x_ld = L.copy_x ? L.ld : c.x_ld;
+    const int64_t wide = 2 * L.half > x_ld ? 2 * L.half : x_ld;
+    L.dx = tiling_of(2 * L.half / kBK, L.half * w_ld * 2, [&](int64_t side) { return tiles_on(c.tokens, side) * tiles_on(c.hidden, side); });
+    L.dw = tiling_of((c.tokens + kBK - 1) / kBK, c.tokens * wide * 2,
                      [&](int64_t side) { return 2 * tiles_on(c.ffn, side) * tiles_on(c.hidden, side); });
     also(L.dx);
     also(L.dw);

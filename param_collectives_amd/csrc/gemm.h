@@ -88,6 +88,12 @@ __device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, v
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (TIDE_LDS void*)lds, 16, int(offset), 0, 0, 0);
 }
 
+// The same with an offset that all lanes share.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t shared, void* lds) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (TIDE_LDS void*)lds, 16, int(offset), int(shared), 0, 0);
+}
+
 // Waits until at most N of this wave's loads (to LDS or registers) are still
 // on their way and, with LGKM, until its LDS accesses are done.
 template <int N, bool LGKM>
@@ -298,6 +304,19 @@ struct Side {
   // Part i of a whole step's loads to LDS.
   __device__ __forceinline__ void fetch_part(char* lds, int64_t s, int i) {
     load_to_lds(at_step(s, i), off[i], lds + (i * THREADS + wave_index() * 64) * 16);
+  }
+
+  // The same for an operand of less than 4 GiB: what all lanes share goes into the
+  // instruction's own offset, and little is computed for a load.
+  __device__ __forceinline__ void fetch_near(char* lds, uint32_t s, int i) {
+    char* to = lds + (i * THREADS + wave_index() * 64) * 16;
+    if constexpr (kPair)
+      load_to_lds(i < kParts / 2 ? base : second, off[i], s * uint32_t(step), to);
+    else if constexpr (kStack) {
+      const bool in = int64_t(s) < split;
+      load_to_lds(in ? base : second, off[i], (in ? s : s - uint32_t(split)) * uint32_t(step), to);
+    } else
+      load_to_lds(base, off[i], s * uint32_t(step), to);
   }
 
   // kPacked: widen what fetch() loaded, halves [h0, h1) of each unit, and write
@@ -540,7 +559,7 @@ struct Gemm {
   // Starts the tile at (m0, n0), k in [k_first, k_end) (k_first a multiple of
   // 32), in the first three stages, which no wave uses any more.
   __device__ __forceinline__ void open(const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k_first,
-                                       int64_t k_end, char* l0, char* l1, char* l2) {
+                                       int64_t k_end, char* l0, char* l1, char* l2, char* = nullptr) {
     sa.init(a, m0, tid);
     sb.init(b, n0, tid);
     first = k_first / kBK;
@@ -883,11 +902,12 @@ struct Gemm {
 };
 
 // The same for small tiles of few products, whose time is that of their loads on
-// their way: a stage is U steps, so up to 3 U of them are, and a barrier comes once
-// in U steps.  The steps are filled up to a multiple of 4 U with empty ones, which
-// go first; a short last step goes last, filled up with zeros.  (A 64 x 64 tile's
-// step takes about 0.1 us, where a 128 x 128 tile's, four times the products, takes
-// 0.45 us with three steps on their way.)
+// their way: a stage is U steps, so up to 3 U of them are, a barrier comes once in U
+// steps, and a stage's fragments are read while the one before is multiplied.  The
+// steps are filled up to a multiple of U with empty ones; they and a short last step,
+// filled up with zeros, go first, so that the loop starts whole ones only.  The
+// stages' places are chosen so that the last one ends a turn of the four: open()
+// may fill any of them, and the epilogue needs LDS of its own.
 template <Form FA, Form FB, int BM, int BN, int WM, int WN, bool F16, int U>
 struct DeepGemm : Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true> {
   using Base = Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true>;
@@ -905,8 +925,13 @@ struct DeepGemm : Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true> {
   using Base::rounds;
   using Base::left;
   static constexpr int kStage = U * Base::kStage;
+  static constexpr int kRows = Base::kStage;                    // bytes of the epilogue's LDS
   static constexpr int kLoads = U * (SA::kLoads + SB::kLoads);  // of a stage
 
+  uint32_t skip;  // places of the first turn that no stage takes
+
+  // Step `step` of one of the first three stages.  Below `first`: the short last step,
+  // just below it, or an empty one; from `whole` on: empty.
   __device__ __forceinline__ void fetch_step(char* stage, int u, int64_t step) {
     typename SA::Held na;
     typename SB::Held nb;
@@ -915,76 +940,83 @@ struct DeepGemm : Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true> {
       sa.template fetch<false>(la, na, step, 0, tid);
       sb.template fetch<false>(lb, nb, step, 0, tid);
     } else {
-      const bool tail = step == whole;
+      const bool tail = left > 0 && step + 1 == first;
       sa.template fetch<true>(la, na, tail ? whole : first, tail ? left : 0, tid);
       sb.template fetch<true>(lb, nb, tail ? whole : first, tail ? left : 0, tid);
     }
   }
-  __device__ __forceinline__ void fetch_stage(char* stage, int64_t step) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) fetch_step(stage, u, step + u);
-  }
   // Load n of a whole stage's.
-  __device__ __forceinline__ void fetch_part(char* stage, int64_t step, int n) {
+  __device__ __forceinline__ void fetch_part(char* stage, uint32_t step, int n) {
     constexpr int kEach = SA::kParts + SB::kParts;
     const int u = n / kEach, i = n % kEach;
     if (i < SA::kParts)
-      sa.fetch_part(stage + u * SA::kBytes, step + u, i);
+      sa.fetch_near(stage + u * SA::kBytes, step + u, i);
     else
-      sb.fetch_part(stage + U * SA::kBytes + u * SB::kBytes, step + u, i - SA::kParts);
+      sb.fetch_near(stage + U * SA::kBytes + u * SB::kBytes, step + u, i - SA::kParts);
   }
 
   __device__ __forceinline__ void open(const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k_first,
-                                       int64_t k_end, char* l0, char* l1, char* l2) {
+                                       int64_t k_end, char* l0, char* l1, char* l2, char* l3) {
     sa.init(a, m0, tid);
     sb.init(b, n0, tid);
     first = k_first / kBK;
     whole = k_end > k_first ? k_end / kBK : first;
     left = k_end > k_first ? int(k_end - whole * kBK) : 0;
-    const int64_t steps = whole - first + (left > 0 ? 1 : 0);
-    rounds = (steps + 4 * U - 1) / (4 * U);
-    s = first + steps - rounds * 4 * U;
+    const int64_t steps = whole - first + (left > 0 ? 1 : 0), stages = (steps + U - 1) / U;
+    rounds = (stages + 3) / 4;
+    skip = uint32_t(-stages) & 3;
+    s = whole - stages * U;
     if (rounds == 0) return;
-    fetch_stage(l0, s);
-    fetch_stage(l1, s + U);
-    fetch_stage(l2, s + 2 * U);
+    // always three stages, so that the waits count the same loads
+#pragma unroll 1
+    for (uint32_t t = 0; t < 3; ++t) {
+      const uint32_t place = (skip + t) & 3;
+      char* const to = place == 0 ? l0 : place == 1 ? l1 : place == 2 ? l2 : l3;
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) fetch_step(to, u, s + int(t) * U + u);
+    }
   }
 
   __device__ __forceinline__ void loop(char* l0, char* l1, char* l2, char* l3) {
-    bf16x8 fa[kFM], fb[kFN];
-    auto read = [&](const char* stage, int u) {
+    struct Fragments {
+      bf16x8 a[U][kFM], b[U][kFN];
+    } even, odd;
+    auto read = [&](Fragments& f, const char* stage, int u) {
 #pragma unroll
-      for (int i = 0; i < kFM; ++i) fa[i] = SA::fragment(stage + u * SA::kBytes, Base::at_a, i);
+      for (int i = 0; i < kFM; ++i) f.a[u][i] = SA::fragment(stage + u * SA::kBytes, Base::at_a, i);
 #pragma unroll
-      for (int j = 0; j < kFN; ++j) fb[j] = SB::fragment(stage + U * SA::kBytes + u * SB::kBytes, Base::at_b, j);
+      for (int j = 0; j < kFN; ++j) f.b[u][j] = SB::fragment(stage + U * SA::kBytes + u * SB::kBytes, Base::at_b, j);
     };
-    // Multiplies the stage in `now`, whose first step's fragments have been read, and
-    // reads those of the stage in `next`; LOAD: starts the loads of the stage 3 on.
-    auto stage = [&](const char* now, const char* next, char* to3, bool load, bool more) {
-      const bool plain = s + 3 * U >= first && s + 4 * U <= whole;
-      if (load && !plain) fetch_stage(to3, s + 3 * U);
+    auto read_all = [&](Fragments& f, const char* stage) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) read(f, stage, u);
+    };
+    // Multiplies a stage and reads the next one; LOAD: starts the loads of the one
+    // three stages on.
+    auto stage = [&](const Fragments& now, Fragments& next, const char* from, char* to3, bool load, bool more) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        bf16x8 a[kFM], b[kFN];
+        if (more) read(next, from, u);
+        if (load) {
 #pragma unroll
-        for (int i = 0; i < kFM; ++i) a[i] = fa[i];
-#pragma unroll
-        for (int j = 0; j < kFN; ++j) b[j] = fb[j];
-        if (u + 1 < U)
-          read(now, u + 1);
-        else if (more)
-          read(next, 0);
-        if (load && plain) {
-#pragma unroll
-          for (int n = u * kLoads / U; n < (u + 1) * kLoads / U; ++n) fetch_part(to3, s + 3 * U, n);
+          for (int n = u * kLoads / U; n < (u + 1) * kLoads / U; ++n) fetch_part(to3, uint32_t(s) + 3 * U, n);
         }
 #pragma unroll
         for (int i = 0; i < kFM; ++i)
 #pragma unroll
-          for (int j = 0; j < kFN; ++j) acc[i][j] = Base::product(b[j], a[i], acc[i][j]);
+          for (int j = 0; j < kFN; ++j) acc[i][j] = Base::product(now.b[u][j], now.a[u][i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
       s += U;
+    };
+    // Before a stage: the next one has arrived for all waves, and what this wave read
+    // of this one (whose place the loads after it go to) has come back.
+    auto ready = [&](bool last) {
+      if (last)
+        wait_loads<0, true>();
+      else
+        wait_loads<kLoads, true>();
+      bare_barrier();
     };
 #pragma unroll
     for (int i = 0; i < kFM; ++i)
@@ -993,35 +1025,58 @@ struct DeepGemm : Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true> {
     if (rounds > 0) {
       wait_loads<2 * kLoads, true>();
       bare_barrier();
-      read(l0, 0);
+      if (skip == 0)
+        read_all(even, l0);
+      else if (skip == 1)
+        read_all(odd, l1);
+      else if (skip == 2)
+        read_all(even, l2);
+      else
+        read_all(odd, l3);
+      uint32_t over = skip;
       for (int64_t r = 1; r < rounds; ++r) {
-        wait_loads<kLoads, false>();
-        bare_barrier();
-        stage(l0, l1, l3, true, true);
-        wait_loads<kLoads, false>();
-        bare_barrier();
-        stage(l1, l2, l0, true, true);
-        wait_loads<kLoads, false>();
-        bare_barrier();
-        stage(l2, l3, l1, true, true);
-        wait_loads<kLoads, false>();
-        bare_barrier();
-        stage(l3, l0, l2, true, true);
+        if (over == 0) {
+          ready(false);
+          stage(even, odd, l1, l3, true, true);
+        }
+        if (over <= 1) {
+          ready(false);
+          stage(odd, even, l2, l0, true, true);
+        }
+        if (over <= 2) {
+          ready(false);
+          stage(even, odd, l3, l1, true, true);
+        }
+        ready(false);
+        stage(odd, even, l0, l2, true, true);
+        over = 0;
       }
-      wait_loads<kLoads, false>();
-      bare_barrier();
-      stage(l0, l1, l3, true, true);
-      wait_loads<kLoads, false>();
-      bare_barrier();
-      stage(l1, l2, nullptr, false, true);
-      wait_loads<0, false>();
-      bare_barrier();
-      stage(l2, l3, nullptr, false, true);
-      stage(l3, nullptr, nullptr, false, false);
+      if (over == 0) {
+        ready(false);
+        stage(even, odd, l1, l3, true, true);
+      }
+      if (over <= 1) {
+        ready(false);
+        stage(odd, even, l2, nullptr, false, true);
+      }
+      if (over <= 2) {
+        ready(true);
+        stage(even, odd, l3, nullptr, false, true);
+      }
+      stage(odd, even, nullptr, nullptr, false, false);
     }
     lds_barrier();
   }
 };
+
+// Bytes of LDS that an epilogue needs beside the stages.
+template <typename G, int SIDE>
+constexpr int own_rows() {
+  if constexpr (SIDE == 64)
+    return G::kRows;
+  else
+    return 16;
+}
 
 // The items of a launch (tiles, or pieces of them) are handed out by queues: one
 // word for each of the 8 XCDs, cleared before the launch, counts the items that

@@ -210,6 +210,8 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_ker
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
+  __shared__ __align__(16) char own[own_rows<G, SIDE>()];
+  char* const rows_lds = SIDE == 64 ? own : lds3;  // the epilogue's
   __shared__ uint32_t turn;
   Queue q;
   uint32_t item = blockIdx.x;
@@ -227,7 +229,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_ker
     slot = p.slot;
     Operand x = a.a;
     x.base = static_cast<const uint16_t*>(x.base) + z * a.a_matrix;
-    g.open(x, x, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
+    g.open(x, x, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2, lds3);
   };
   open(item);
   while (item != kNoItem) {
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_ker
     const int64_t m_rows = a.size - n1 - g.mirror_column(), m_left = a.size - m1 - (g.lane & 1) * 8;
     const int64_t m_pad = padded(a.size) - a.size;
     g.each_mirrored(
-        lds3, s1 < 0 && m1 != n1, before,
+        rows_lds, s1 < 0 && m1 != n1, before,
         [&](int r, int i, int q, f32x4v& lo, f32x4v& hi) {
           if (s1 >= 0) return put_slot<SIDE>(a.partial, s1, r + row, g.column(), lo, hi);
           const f32x8v v = a.value(m1 + r + row, n1 + g.column(), lo, hi, a.g ? old[i & 1][q] : u32x4{0, 0, 0, 0});
@@ -400,6 +402,8 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void update_kernel
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
   __shared__ __align__(16) char lds3[G::kStage];
+  __shared__ __align__(16) char own[own_rows<G, SIDE>()];
+  char* const rows_lds = SIDE == 64 ? own : lds3;  // the epilogue's
   __shared__ uint32_t turn;
   Queue q;
   uint32_t item = blockIdx.x;
@@ -418,7 +422,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void update_kernel
     Operand x = a.a, y = a.b;
     x.base = static_cast<const uint16_t*>(x.base) + z * a.a_matrix;
     y.base = static_cast<const uint16_t*>(y.base) + z * a.b_matrix;
-    g.open(x, y, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2);
+    g.open(x, y, m0, n0, p.k_first, p.k_end, lds0, lds1, lds2, lds3);
   };
   open(item);
   while (item != kNoItem) {
@@ -450,7 +454,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void update_kernel
       }
     };
     g.each_rows(
-        lds3, before,
+        rows_lds, before,
         [&](int r, int i, int q, f32x4v lo, f32x4v hi) {
           if (s1 >= 0) return put_slot<SIDE>(a.partial, s1, r + row, g.column(), lo, hi);
           const uint32_t here = at, out_here = out_at;
@@ -513,9 +517,9 @@ Tilings tilings_of(const OrthogonalCall& c, const Layout& L, int64_t count) {
     return count * t * (t + 1) / 2;
   };
   Tilings t;
-  t.gram = tiling_of(steps_of(large), triangle);
-  t.square = tiling_of(steps_of(L.small), triangle);
-  t.update = tiling_of(steps_of(L.small), [&](int64_t side) { return count * ((c.rows + side - 1) / side) * ((c.cols + side - 1) / side); });
+  t.gram = tiling_of(steps_of(large), L.matrix * 2, triangle);
+  t.square = tiling_of(steps_of(L.small), L.small_matrix * 2, triangle);
+  t.update = tiling_of(steps_of(L.small), L.matrix * 2, [&](int64_t side) { return count * ((c.rows + side - 1) / side) * ((c.cols + side - 1) / side); });
   return t;
 }
 

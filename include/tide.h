@@ -625,7 +625,7 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
  * than columns the same from X^T X, on the right.)  The norm is summed in fp64,
  * every product in fp32; the products' operands X, G and the polynomial are rounded
  * to fp16 times 2^12 (by at most 2^-11 of themselves, or by 2^-37), but in the first
- * three steps the term a X comes from X to 22 bits; the result is rounded once to
+ * three steps a times what X's rounding left is added; the result is rounded once to
  * bf16.  The order of every sum depends on the sizes and the count only.  Entries of
  * those operands must stay below 16: coefficients and steps with which they may
  * not are refused (TIDE_ERR_INVALID).
@@ -639,7 +639,7 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
  *           one that is listed twice, or as another's input, is refused.
  *           Both lists are read during the call only.
  *   workspace  as for the weight gradient above; matrices are taken so many at a
- *           time that it stays below about 1 GiB, one at least
+ *           time that it stays below about 384 MiB, one at least
  * Sizes: rows and cols up to 2^22, matrices and the square of the smaller side as
  * for the checkpoints; steps in [1, 64].
  * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.

@@ -12,10 +12,11 @@
 // normal numbers down to 2^-26, rounded by at most 2^-11.  bf16's roundings come
 // out as errors of 1 to 3% in the 2-norm where a few directions are strong: what
 // the first roundings of X leave in the weak directions is raised with them.  For
-// the same reason the first kExact steps take the term a X from X with the rest of
-// its rounding, a second fp16, and P without its diagonal: 0.1% instead of 0.4%
-// (a simulation in 64 bits with these roundings).  From then on the weak
-// directions are large enough, and a I stays in P.
+// the same reason the first kExact steps add a times the rest of X's rounding, a
+// second fp16: 0.1% instead of 0.4% (a simulation in 64 bits with these roundings).
+// From then on the weak directions are large enough.  A bf16 X has no rest at the
+// start: it is scaled by a power of two, and what the norm is more than that goes
+// into the first step's factors.
 //
 // The norm is summed in fp64, which no entry's square leaves.
 #include <hip/hip_runtime.h>
@@ -62,6 +63,10 @@ struct Pointers {
   void* p[kMost];
 };
 
+// Sixteens of rows that an epilogue loads ahead, a power of two less one: its
+// operations on one take 0.3 us, a load one or two.
+constexpr int kAhead = 3;
+
 template <Form FA, Form FB, int SIDE, int WM, int WN>
 using Products = std::conditional_t<SIDE == 64, DeepGemm<FA, FB, SIDE, SIDE, WM, WN, true, 4>,
                                     Gemm<FA, FB, Code::kE4m3, SIDE, SIDE, WM, WN, true, true>>;
@@ -72,7 +77,8 @@ struct StartArgs {
   Pointers x;
   int32_t f32;
   int64_t ld, rows, cols;
-  double* sums;  // [matrix][gridDim.x]
+  double* sums;    // [matrix][gridDim.x]
+  float* factors;  // [matrix]: X over its norm is this times what is kept
   uint32_t* queues;
   uint32_t queue_words;
   float eps;
@@ -113,11 +119,19 @@ __global__ __launch_bounds__(256) void square_sums_kernel(StartArgs a) {
   const void* x = a.x.p[blockIdx.y];
   const int64_t groups = (a.cols + 7) / 8, all = a.rows * groups;
   double s = 0;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / groups;
-    const f32x8v v = eight_values(a, x, r, (i - r * groups) * 8);
+  const int64_t step = int64_t(gridDim.x) * 256;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += 4 * step) {
+    f32x8v v[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += double(v[j]) * double(v[j]);
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = i + k * step, r = at / groups;
+      v[k] = f32x8v{};
+      if (at < all) v[k] = eight_values(a, x, r, (at - r * groups) * 8);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += double(v[k][j]) * double(v[k][j]);
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
@@ -126,8 +140,9 @@ __global__ __launch_bounds__(256) void square_sums_kernel(StartArgs a) {
   if (threadIdx.x == 0) a.sums[blockIdx.y * gridDim.x + blockIdx.x] = part[0] + part[1] + part[2] + part[3];
 }
 
-// X over its norm, times kUnit, in two fp16; zeros around it.  The
-// product is taken in fp64: the factor may lie outside fp32's range.
+// X over its norm, times kUnit, but for a factor in [1, 2), in fp16, and of an fp32 X
+// the rest in another; zeros around it.  The product is taken in fp64: its factor may
+// lie outside fp32's range.
 __global__ __launch_bounds__(256) void normalize_kernel(StartArgs a, int32_t blocks) {
   __shared__ double factor;
   if (threadIdx.x < 64) {
@@ -135,7 +150,13 @@ __global__ __launch_bounds__(256) void normalize_kernel(StartArgs a, int32_t blo
     for (int i = threadIdx.x; i < blocks; i += 64) s += a.sums[int64_t(blockIdx.y) * blocks + i];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    if (threadIdx.x == 0) factor = double(kUnit) / (sqrt(s) + double(a.eps));
+    if (threadIdx.x == 0) {
+      const double f = double(kUnit) / (sqrt(s) + double(a.eps));
+      // (a norm that is 0, infinite or NaN: all that is not 0 becomes NaN, or all)
+      const bool plain = f > 0 && f < __builtin_inf();
+      factor = plain ? ldexp(1.0, ilogb(f)) : f;
+      if (blockIdx.x == 0) a.factors[blockIdx.y] = plain ? float(f / ldexp(1.0, ilogb(f))) : 1.0f;
+    }
   }
   __syncthreads();
   const double f = factor;
@@ -151,7 +172,7 @@ __global__ __launch_bounds__(256) void normalize_kernel(StartArgs a, int32_t blo
     split_eight(v, &hi, &lo);
     const int64_t at = int64_t(blockIdx.y) * a.matrix + r * a.pitch + c;
     *reinterpret_cast<u32x4*>(a.hi + at) = hi;
-    *reinterpret_cast<u32x4*>(a.lo + at) = lo;
+    if (a.f32) *reinterpret_cast<u32x4*>(a.lo + at) = lo;
   }
 }
 
@@ -170,13 +191,15 @@ struct SymmetricArgs {
   uint16_t* out;      // size x size each (columns to padded(size)), rows `ld` apart, `matrix` elements from one to the next
   int64_t size, ld, matrix;
   float alpha, beta, diagonal;
+  const float* factors;  // of A, or null: 1
 
+  __device__ __forceinline__ float scale(int64_t z) const { return factors ? factors[z] * factors[z] * alpha : alpha; }
   // The values of 8 columns of row m from column n, whose G (if any) is `old`.
-  __device__ __forceinline__ f32x8v value(int64_t m, int64_t n, f32x4v lo, f32x4v hi, u32x4 old) const {
+  __device__ __forceinline__ f32x8v value(float scale, int64_t m, int64_t n, f32x4v lo, f32x4v hi, u32x4 old) const {
     f32x8v v = join_quads(lo, hi);
     const f32x8v o = f16_values(old);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = alpha * v[j] + (g ? beta * o[j] : 0.0f);
+    for (int j = 0; j < 8; ++j) v[j] = scale * v[j] + (g ? beta * o[j] : 0.0f);
     if (diagonal != 0.0f) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -236,6 +259,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_ker
     g.loop(lds0, lds1, lds2, lds3);
     const uint32_t k = a.queue ? q.ask() : 0;
     const int64_t m1 = m0, n1 = n0, s1 = slot;
+    const float scale = a.scale(z);
     g.renew_lane();
     const uint32_t row = g.lane / G::kRowGroups, ld = uint32_t(a.ld);
     // the rows come in order, and the places go on with them
@@ -245,15 +269,17 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_ker
     uint16_t* const mirrored = a.out + z * a.matrix + n1 * a.ld + m1;
     // G's values of the rows that come next
     constexpr int kRows = 64 / G::kRowGroups, kCalls = 16 / kRows;  // rows of a call, calls of 16 rows
-    u32x4 old[2][kCalls];
+    u32x4 old[kAhead + 1][kCalls];
     auto before = [&](int i) {
       if (a.g == nullptr || s1 >= 0) return;
 #pragma unroll
-      for (int q = 0; q < kCalls; ++q) {
-        const int r = g.wm * (SIDE / WM) + i * 16 + q * kRows;
-        if (r < rows && left > 0) old[i & 1][q] = *reinterpret_cast<const u32x4*>(a.g + first + ahead);
-        ahead += kRows * ld;
-      }
+      for (int b = i == 0 ? 0 : i + kAhead - 1; b < i + kAhead && b < G::kFM; ++b)
+#pragma unroll
+        for (int q = 0; q < kCalls; ++q) {
+          const int r = g.wm * (SIDE / WM) + b * 16 + q * kRows;
+          if (r < rows && left > 0) old[b & kAhead][q] = *reinterpret_cast<const u32x4*>(a.g + first + ahead);
+          ahead += kRows * ld;
+        }
     };
     // rows of the mirrored tile are this one's columns
     const uint32_t m_at = uint32_t(g.mirror_column()) * ld + uint32_t(g.lane & 1) * 8;
@@ -263,7 +289,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_ker
         rows_lds, s1 < 0 && m1 != n1, before,
         [&](int r, int i, int q, f32x4v& lo, f32x4v& hi) {
           if (s1 >= 0) return put_slot<SIDE>(a.partial, s1, r + row, g.column(), lo, hi);
-          const f32x8v v = a.value(m1 + r + row, n1 + g.column(), lo, hi, a.g ? old[i & 1][q] : u32x4{0, 0, 0, 0});
+          const f32x8v v = a.value(scale, m1 + r + row, n1 + g.column(), lo, hi, a.g ? old[i & kAhead][q] : u32x4{0, 0, 0, 0});
           if (r < rows && left > 0) *reinterpret_cast<u32x4*>(a.out + first + at) = eight_f16(v);
           at += kRows * ld;
           lo = __builtin_shufflevector(v, v, 0, 1, 2, 3);
@@ -306,7 +332,7 @@ __global__ __launch_bounds__(256) void join_symmetric_kernel(SymmetricArgs a) {
     f32x4v lo, hi;
     join_eight<SIDE>(a.partial, a.cut, r, r0 + row, c0 + col, &lo, &hi);
     const int64_t at = z * a.matrix + m1 * a.ld + n1;
-    v = a.value(m1, n1, lo, hi, a.g ? *reinterpret_cast<const u32x4*>(a.g + at) : u32x4{0, 0, 0, 0});
+    v = a.value(a.scale(z), m1, n1, lo, hi, a.g ? *reinterpret_cast<const u32x4*>(a.g + at) : u32x4{0, 0, 0, 0});
     *reinterpret_cast<u32x4*>(a.out + at) = eight_f16(v);
   }
   if (tm == tn) return;
@@ -333,25 +359,24 @@ struct UpdateArgs {
   uint32_t tiles_m, tiles_n;
   uint32_t* queue;
   int64_t rows, cols, ld, matrix;
-  const uint16_t* hi;  // X, where its term is added here (with lo), or null
+  int32_t rest;  // what lo holds of X is added
   uint16_t* lo;
+  const float* factors;  // of X, or null: 1
   float coefficient;
   uint16_t* next;  // X's next, or null: the last step's result goes to out
   int32_t keep;    // the rest of its rounding goes to lo
   Pointers out;
   int64_t out_ld;
 
-  // The next X times kUnit, of 8 columns, whose own X (if it is added here) is in
-  // two parts.
-  __device__ __forceinline__ f32x8v value(f32x4v l, f32x4v h, u32x4 x, u32x4 y) const {
+  // The next X times kUnit, of 8 columns, the rest of whose own X is y (or zeros);
+  // f: factors' of the matrix.
+  __device__ __forceinline__ float factor(int64_t z) const { return factors ? factors[z] : 1.0f; }
+  __device__ __forceinline__ f32x8v value(float f, f32x4v l, f32x4v h, u32x4 y) const {
+    const float scale = f * (1.0f / kUnit), more = f * coefficient * (1.0f / kRest);
     f32x8v v = join_quads(l, h);
+    const f32x8v b = f16_values(y);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= 1.0f / kUnit;
-    if (hi) {
-      const f32x8v a = f16_values(x), b = f16_values(y);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = coefficient * (a[j] + b[j] * (1.0f / kRest)) + v[j];
-    }
+    for (int j = 0; j < 8; ++j) v[j] = scale * v[j] + (rest ? more * b[j] : 0.0f);
     return v;
   }
   // Its 8 columns, of which `left` exist (0 of a row that fills up), to places in
@@ -438,20 +463,20 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void update_kernel
     const int64_t row_pad = padded(a.rows) - a.rows, col_pad = padded(a.cols) - a.cols;
     const int64_t first = z * a.matrix + m1 * a.ld + n1;
     uint16_t* out = static_cast<uint16_t*>(a.out.p[z]) + m1 * a.out_ld + n1;
-    // X's values of the rows that come next
+    const float factor = a.factor(z);
+    // what is left of X in the rows that come next
     constexpr int kRows = 64 / G::kRowGroups, kCalls = 16 / kRows;  // rows of a call, calls of 16 rows
-    u32x4 x[2][kCalls], y[2][kCalls];
+    u32x4 y[kAhead + 1][kCalls];
     auto before = [&](int i) {
-      if (a.hi == nullptr || s1 >= 0) return;
+      if (!a.rest || s1 >= 0) return;
 #pragma unroll
-      for (int q = 0; q < kCalls; ++q) {
-        const int r = g.wm * (SIDE / WM) + i * 16 + q * kRows;
-        if (r - rows < row_pad && left > -col_pad) {
-          x[i & 1][q] = *reinterpret_cast<const u32x4*>(a.hi + first + ahead);
-          y[i & 1][q] = *reinterpret_cast<const u32x4*>(a.lo + first + ahead);
+      for (int b = i == 0 ? 0 : i + kAhead - 1; b < i + kAhead && b < G::kFM; ++b)
+#pragma unroll
+        for (int q = 0; q < kCalls; ++q) {
+          const int r = g.wm * (SIDE / WM) + b * 16 + q * kRows;
+          if (r < rows && left > 0) y[b & kAhead][q] = *reinterpret_cast<const u32x4*>(a.lo + first + ahead);
+          ahead += kRows * ld;
         }
-        ahead += kRows * ld;
-      }
     };
     g.each_rows(
         rows_lds, before,
@@ -461,7 +486,7 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void update_kernel
           at += kRows * ld;
           out_at += kRows * out_ld;
           if (r - rows >= row_pad || left <= -col_pad) return;
-          a.put(a.value(lo, hi, x[i & 1][q], y[i & 1][q]), r < rows ? left : 0, a.next + first + here,
+          a.put(a.value(factor, lo, hi, a.rest ? y[i & kAhead][q] : u32x4{0, 0, 0, 0}), r < rows ? left : 0, a.next + first + here,
                 a.lo + first + here, out + out_here);
         },
         [&] {
@@ -484,12 +509,9 @@ __global__ __launch_bounds__(256) void join_update_kernel(UpdateArgs a) {
   f32x4v lo = {}, hi = {};
   if (m < a.rows) join_eight<SIDE>(a.partial, a.cut, r, row, col, &lo, &hi);
   const int64_t at = z * a.matrix + m * a.ld + n;
-  u32x4 x = u32x4{0, 0, 0, 0}, y = x;
-  if (a.hi) {
-    x = *reinterpret_cast<const u32x4*>(a.hi + at);
-    y = *reinterpret_cast<const u32x4*>(a.lo + at);
-  }
-  a.put(a.value(lo, hi, x, y), m < a.rows ? a.cols - n : 0, a.next + at, a.lo + at, static_cast<uint16_t*>(a.out.p[z]) + m * a.out_ld + n);
+  u32x4 y = u32x4{0, 0, 0, 0};
+  if (a.rest && m < a.rows && n < a.cols) y = *reinterpret_cast<const u32x4*>(a.lo + at);
+  a.put(a.value(a.factor(z), lo, hi, y), m < a.rows ? a.cols - n : 0, a.next + at, a.lo + at, static_cast<uint16_t*>(a.out.p[z]) + m * a.out_ld + n);
 }
 
 // ------------------------------------------------------------ launches
@@ -503,7 +525,7 @@ struct Layout {
   int64_t sum_blocks = 0;
   int64_t partial_bytes = 0;
   // byte offsets
-  int64_t sums = 0, queues = 0, x0 = 0, x1 = 0, lo = 0, g = 0, p = 0, partial = 0, bytes = 0;
+  int64_t sums = 0, factors = 0, queues = 0, x0 = 0, x1 = 0, lo = 0, g = 0, p = 0, partial = 0, bytes = 0;
 };
 
 struct Tilings {
@@ -532,7 +554,9 @@ Layout layout_of(const OrthogonalCall& c) {
   L.matrix = padded(c.rows) * L.pitch;
   L.small_matrix = L.small * L.small_pitch;
   const int64_t each = 3 * L.matrix * 2 + 2 * L.small_matrix * 2;
-  L.piece = (int64_t(1) << 30) / each;
+  // (128 of 2048 x 768, all at a time that 1 GiB holds 4.47 ms, 384 MiB 4.31, 256 MiB
+  // 4.73: smaller pieces stay in the caches, but leave CUs without a tile)
+  L.piece = (int64_t(3) << 27) / each;
   L.piece = L.piece < 1 ? 1 : L.piece > kMost ? kMost : L.piece;
   if (L.piece > c.count) L.piece = c.count;
   // pieces of one size, the last one's rest apart
@@ -557,6 +581,7 @@ Layout layout_of(const OrthogonalCall& c) {
     return here;
   };
   L.sums = take(L.piece * L.sum_blocks * 8);
+  L.factors = take(L.piece * 4);
   L.queues = take(3 * c.steps * kQueueWords * kQueuePitch * 4);
   L.x0 = take(L.piece * L.matrix * 2);
   L.x1 = take(L.piece * L.matrix * 2);
@@ -639,6 +664,7 @@ int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t c
   s.rows = c.rows;
   s.cols = c.cols;
   s.sums = reinterpret_cast<double*>(ws + L.sums);
+  s.factors = reinterpret_cast<float*>(ws + L.factors);
   s.queues = queues;
   s.queue_words = uint32_t(3 * c.steps * kQueueWords * kQueuePitch);
   s.eps = c.eps;
@@ -653,7 +679,8 @@ int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t c
   TIDE_LAUNCHED();
   const Tilings t = tilings_of(c, L, count);
   for (int32_t k = 0; k < c.steps; ++k) {
-    const bool exact = k < kExact, last = k + 1 == c.steps;
+    const bool last = k + 1 == c.steps;
+    const float* factors = k == 0 ? s.factors : nullptr;
     uint32_t* q = queues + 3 * k * kQueueWords * kQueuePitch;
     SymmetricArgs g{};
     g.a = Operand{now, nullptr, L.pitch, 0, L.small};
@@ -665,17 +692,19 @@ int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t c
     g.ld = L.small_pitch;
     g.matrix = L.small_matrix;
     g.alpha = 1.0f / kUnit;
+    g.factors = factors;
     int rc = L.tall ? launch_symmetric<Form::kCols>(g, t.gram, count, q, st)
                     : launch_symmetric<Form::kRows>(g, t.gram, count, q, st);
     if (rc != 0) return rc;
     g.a = Operand{gram, nullptr, L.small_pitch, 0, L.small};
     g.a_matrix = L.small_matrix;
     g.depth = padded(L.small);
+    g.factors = nullptr;
     g.g = gram;
     g.out = poly;
     g.alpha = c.c / kUnit;
     g.beta = c.b;
-    g.diagonal = exact ? 0.0f : c.a * kUnit;
+    g.diagonal = c.a * kUnit;
     rc = launch_symmetric<Form::kRows>(g, t.square, count, q + kQueueWords * kQueuePitch, st);
     if (rc != 0) return rc;
     UpdateArgs u{};
@@ -685,7 +714,8 @@ int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t c
     u.cols = c.cols;
     u.ld = L.pitch;
     u.matrix = L.matrix;
-    u.hi = exact ? now : nullptr;
+    u.rest = k == 0 ? c.x_f32 : k < kExact;
+    u.factors = factors;
     u.lo = lo;
     u.coefficient = c.a;
     u.next = last ? nullptr : next;

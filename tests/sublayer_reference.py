@@ -182,15 +182,16 @@ def newton_schulz(x, steps, a, b, c, eps):
     return x
 
 
-def orthogonalize(x, steps, a, b, c, eps, exact=3):
+def orthogonalize(x, steps, a, b, c, eps, exact=3, f32=True):
     """(value, tolerance of the error's Frobenius norm after the rounding to bf16) of
     a float64 matrix.
 
     A bound that takes every rounding at its worst and in the worst direction is of
     no use here: a step multiplies by up to 3.5 what lies in the weak directions.
     The tolerance is the error of the definition with the kernels' roundings put in
-    where they are (X, G and the polynomial to fp16 times 2^12, a X from 22 bits in
-    the first `exact` steps), 1.5 times, since the kernels' own fp32 sums let some
+    where they are (X, G and the polynomial to fp16 times 2^12; in the first `exact`
+    steps a times the rest of X's rounding, to 11 bits, is added; a bf16 matrix has
+    none in the first), 1.5 times, since the kernels' own fp32 sums let some
     values round the other way: as many roundings of the same sizes in other
     directions, not more or larger ones (the sums' own errors are 2^-13 of them).
     To it comes 1.5 times the root mean square of the result's rounding."""
@@ -199,12 +200,8 @@ def orthogonalize(x, steps, a, b, c, eps, exact=3):
     y = x.T if tall else x
     y = y / (np.sqrt((y**2).sum()) + eps)
     for k in range(steps):
-        h = _f16(y)
+        h = _f16(y) if k > 0 or f32 else y
         g = _f16(h @ h.T)
-        q = b * g + c * (g @ g)
-        if k < exact:
-            y = a * (h + _f16((y - h) * 2048) / 2048) + _f16(q) @ h
-        else:
-            y = _f16(q + a * np.eye(len(g))) @ h
+        y = _f16(b * g + c * (g @ g) + a * np.eye(len(g))) @ h + (a * _f16((y - h) * 2048) / 2048 if k < exact else 0)
     err = np.linalg.norm((y.T if tall else y) - value)
     return value, 1.5 * (err + HALF["bf16"] / np.sqrt(3) * np.linalg.norm(value)) + 2.0**-20 * np.linalg.norm(value)

@@ -25,8 +25,8 @@ def tide():
     return tide
 
 
-def check(out, x, steps=5, abc=ABC, eps=EPS):
-    value, tolerance = ref.orthogonalize(x, steps, *abc, eps)
+def check(out, x, steps=5, abc=ABC, eps=EPS, dtype="f32"):
+    value, tolerance = ref.orthogonalize(x, steps, *abc, eps, f32=dtype == "f32")
     got = out.double().cpu().numpy()
     assert got.shape == value.shape
     assert np.linalg.norm(got - value) <= tolerance, (np.linalg.norm(got - value), tolerance, np.linalg.norm(value))
@@ -48,7 +48,7 @@ SIZES = [(1, 1), (1, 7), (7, 1), (5, 9), (9, 5), (16, 16), (33, 70), (70, 33), (
 def test_sizes(tide, rows, cols, kind):
     dtype = "f32" if (rows + cols) % 2 else "bf16"
     x = held(matrix(np.random.default_rng(rows + cols), rows, cols, kind), dtype)
-    check(run(tide, [x], dtype)[0], x)
+    check(run(tide, [x], dtype)[0], x, dtype=dtype)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -60,7 +60,7 @@ def test_many(tide, count, rows, cols, dtype):
     xs = [held(matrix(rng, rows, cols, "strong" if i % 3 == 0 else "noise"), dtype) for i in range(count)]
     outs = run(tide, xs, dtype)
     for i in {0, 1, count // 2, count - 2, count - 1}:
-        check(outs[i], xs[i])
+        check(outs[i], xs[i], dtype=dtype)
     # a matrix's result does not depend on its place; of the sums' order, which the count may change, only roundings do
     again = run(tide, xs[::-1], dtype)[::-1]
     for a, b in zip(outs, again):
@@ -95,7 +95,7 @@ def test_large(tide, rows, cols):
 def test_steps_and_coefficients(tide, abc, steps):
     for rows, cols in ((60, 140), (140, 60)):
         x = held(matrix(np.random.default_rng(steps), rows, cols, "noise"), "bf16")
-        check(run(tide, [x], "bf16", steps=steps, coefficients=abc)[0], x, steps, abc)
+        check(run(tide, [x], "bf16", steps=steps, coefficients=abc)[0], x, steps, abc, dtype="bf16")
 
 
 @pytest.mark.parametrize("unit", [2.0**-100, 2.0**-130, 2.0**70, 2.0**110])

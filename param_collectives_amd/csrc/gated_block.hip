@@ -273,10 +273,10 @@ __global__ __launch_bounds__(256) void kept_gates_kernel(const uint16_t* gates, 
 // tokens' states, which every workgroup reads, from the caches.  Rows may start
 // anywhere: nothing is copied first.
 template <int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void few_gated_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* gate,
+__global__ __launch_bounds__(WAVES * 64, 4) void few_gated_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* gate,
                                                                int64_t gate_ld, const uint16_t* up, int64_t up_ld,
                                                                int64_t depth, Finish f) {
-  constexpr int kDeep = 8;  // steps whose loads go out together
+  constexpr int kDeep = 4;  // steps whose loads go out together
   __shared__ f32x4v part[2][WAVES][64];
   const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
   const int64_t n0 = int64_t(blockIdx.x) * 16;
@@ -291,19 +291,50 @@ __global__ __launch_bounds__(WAVES * 64) void few_gated_kernel(const uint16_t* x
   int64_t s = wave * per;
   const int64_t end = s + per < whole ? s + per : whole;
   f32x4v ag = f32x4v{0.f, 0.f, 0.f, 0.f}, au = ag;
-  for (; s + kDeep <= end; s += kDeep) {
-    bf16x8 bg[kDeep], bu[kDeep], bx[kDeep];
+  struct Steps {
+    bf16x8 g[kDeep], u[kDeep], x[kDeep];
+  } even, odd;
+  auto fetch = [&](Steps& to, int64_t at) {
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
-      bg[i] = load(wg + (s + i) * 32);
-      bu[i] = load(wu + (s + i) * 32);
-      bx[i] = load(xt + (s + i) * 32);
+      to.g[i] = load(wg + (at + i) * 32);
+      to.u[i] = load(wu + (at + i) * 32);
+      to.x[i] = load(xt + (at + i) * 32);
     }
+    __builtin_amdgcn_sched_barrier(0);  // all of them on their way before the first product
+  };
+  auto multiply = [&](const Steps& w) {
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
-      ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bg[i], bx[i], ag, 0, 0, 0);
-      au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bu[i], bx[i], au, 0, 0, 0);
+      ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.g[i], w.x[i], ag, 0, 0, 0);
+      au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.u[i], w.x[i], au, 0, 0, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int64_t blocks = end > s ? (end - s) / kDeep : 0;
+  if (blocks > 0) {
+    int64_t b = blockIdx.x % blocks;
+    auto next = [&] {
+      const int64_t at = s + b * kDeep;
+      b = b + 1 == blocks ? 0 : b + 1;
+      return at;
+    };
+    fetch(even, next());
+    int64_t n = 1;
+    for (; n + 2 <= blocks; n += 2) {
+      fetch(odd, next());
+      multiply(even);
+      fetch(even, next());
+      multiply(odd);
+    }
+    if (n < blocks) {
+      fetch(odd, next());
+      multiply(even);
+      multiply(odd);
+    } else {
+      multiply(even);
+    }
+    s += blocks * kDeep;
   }
   for (; s < end; ++s) {
     const bf16x8 bg = load(wg + s * 32), bu = load(wu + s * 32), bx = load(xt + s * 32);
@@ -596,7 +627,7 @@ int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
       hipLaunchKernelGGL(few_gated_kernel<4>, dim3(grid), dim3(256), 0, st, xp, c.x_ld, gate, c.gate_ld, up_w, c.up_ld,
                          c.hidden, f);
     else
-      hipLaunchKernelGGL(few_gated_kernel<16>, dim3(grid), dim3(1024), 0, st, xp, c.x_ld, gate, c.gate_ld, up_w, c.up_ld,
+      hipLaunchKernelGGL(few_gated_kernel<8>, dim3(grid), dim3(512), 0, st, xp, c.x_ld, gate, c.gate_ld, up_w, c.up_ld,
                          c.hidden, f);
     TIDE_LAUNCHED();
   } else {

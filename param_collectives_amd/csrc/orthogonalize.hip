@@ -35,7 +35,7 @@ constexpr int kExact = 3;               // steps whose a X keeps the rest of X's
 constexpr float kUnit = 4096.0f;        // entries are kept times this
 constexpr float kRest = 2048.0f;        // and the rest of a rounding times this as well
 constexpr int64_t kMost = 64;           // matrices of a piece, whose addresses go with the launch
-constexpr int64_t kSumBlocks = 256;     // workgroups that share a matrix's norm, at most
+constexpr int64_t kSumBlocks = 1024;    // workgroups that share a matrix's norm, at most
 
 typedef float f32x8v __attribute__((ext_vector_type(8)));
 
@@ -522,7 +522,7 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 struct Layout {
   bool tall = false;
   int64_t piece = 0, small = 0, pitch = 0, small_pitch = 0, matrix = 0, small_matrix = 0;
-  int64_t sum_blocks = 0;
+  int64_t sum_blocks = 0, copy_blocks = 0;  // workgroups of a matrix
   int64_t partial_bytes = 0;
   // byte offsets
   int64_t sums = 0, factors = 0, queues = 0, x0 = 0, x1 = 0, lo = 0, g = 0, p = 0, partial = 0, bytes = 0;
@@ -565,7 +565,9 @@ Layout layout_of(const OrthogonalCall& c) {
   const int64_t groups = (padded(c.rows) * (L.pitch / 8) + 255) / 256;
   L.sum_blocks = 2048 / L.piece;
   if (L.sum_blocks > kSumBlocks) L.sum_blocks = kSumBlocks;
-  if (L.sum_blocks > groups) L.sum_blocks = groups;
+  if (L.sum_blocks > (groups + 3) / 4) L.sum_blocks = (groups + 3) / 4;  // of four groups a thread
+  L.copy_blocks = 8192 / L.piece;
+  if (L.copy_blocks > groups) L.copy_blocks = groups;
   const int64_t last = c.count - (pieces - 1) * L.piece;
   for (int64_t n : {L.piece, last}) {
     const Tilings t = tilings_of(c, L, n);
@@ -674,7 +676,7 @@ int run_piece(const OrthogonalCall& c, const Layout& L, int64_t first, int64_t c
   s.matrix = L.matrix;
   hipLaunchKernelGGL(square_sums_kernel, dim3(unsigned(L.sum_blocks), unsigned(count)), dim3(256), 0, st, s);
   TIDE_LAUNCHED();
-  hipLaunchKernelGGL(normalize_kernel, dim3(unsigned(L.sum_blocks), unsigned(count)), dim3(256), 0, st, s,
+  hipLaunchKernelGGL(normalize_kernel, dim3(unsigned(L.copy_blocks), unsigned(count)), dim3(256), 0, st, s,
                      int32_t(L.sum_blocks));
   TIDE_LAUNCHED();
   const Tilings t = tilings_of(c, L, count);

@@ -794,14 +794,20 @@ def vocab_loss_grad(hidden, weight, targets, grad_loss, loss, lse, dhidden, dwei
 # ------------------------------------------------------------ layer norm
 
 
-def _affine(named, cols):
-    """(addresses, TIDE_DTYPE_*) of vectors of `cols` values that may be None,
-    all of one dtype."""
-    given = [t for _, t in named if t is not None]
-    dtype = given[0].dtype if given and isinstance(given[0], torch.Tensor) else torch.float32
-    if dtype not in _FLOATS:
-        raise TypeError(f"{' and '.join(what for what, _ in named)}: expected torch.bfloat16 or torch.float32, got {dtype}")
-    return [None if t is None else _vector(t, dtype, cols, what) for what, t in named], _FLOATS[dtype]
+def _affine_dtype(*vectors):
+    """The dtype of the first of the vectors that are given (fp32 if none is), and
+    its TIDE_DTYPE_*."""
+    for t in vectors:
+        if t is not None:
+            dtype = getattr(t, "dtype", None)
+            if dtype not in _FLOATS:
+                raise TypeError(f"weight and bias: expected torch.bfloat16 or torch.float32, got {dtype}")
+            return dtype, _FLOATS[dtype]
+    return torch.float32, DTYPE_F32
+
+
+def _optional(t, dtype, n, what):
+    return None if t is None else _vector(t, dtype, n, what)
 
 
 def _same_shape(rows, cols, what, got):
@@ -811,11 +817,12 @@ def _same_shape(rows, cols, what, got):
 
 def _layer_norm_args(x, weight, bias, out, mean, rstd, eps):
     p, rows, cols, stride = _matrix(x, _FLOATS, "x")
-    y, *shape, y_stride = _matrix(out, _FLOATS, "out")
-    _same_shape(rows, cols, "out", tuple(shape))
-    (w, b), affine = _affine((("weight", weight), ("bias", bias)), cols)
-    stats = [None if t is None else _vector(t, torch.float32, rows, what) for what, t in (("mean", mean), ("rstd", rstd))]
-    return p, _FLOATS[x.dtype], stride, rows, cols, w, b, affine, eps, y, _FLOATS[out.dtype], y_stride, *stats
+    y, y_rows, y_cols, y_stride = _matrix(out, _FLOATS, "out")
+    _same_shape(rows, cols, "out", (y_rows, y_cols))
+    at, affine = _affine_dtype(weight, bias)
+    return (p, _FLOATS[x.dtype], stride, rows, cols, _optional(weight, at, cols, "weight"),
+            _optional(bias, at, cols, "bias"), affine, eps, y, _FLOATS[out.dtype], y_stride,
+            _optional(mean, torch.float32, rows, "mean"), _optional(rstd, torch.float32, rows, "rstd"))
 
 
 def layer_norm_call(x, weight, bias, out, mean=None, rstd=None, eps=1e-5):
@@ -839,6 +846,7 @@ def layer_norm_grad_workspace(x, dout):
     return _layer_norm_grad_bytes(_FLOATS[x.dtype], _FLOATS[dout.dtype], rows, cols)
 
 
+@functools.lru_cache(maxsize=256)
 def _layer_norm_grad_bytes(x_dtype, dout_dtype, rows, cols):
     need = ctypes.c_int64()
     _check(lib.tide_layer_norm_grad_workspace(x_dtype, dout_dtype, rows, cols, ctypes.byref(need)))
@@ -848,15 +856,17 @@ def _layer_norm_grad_bytes(x_dtype, dout_dtype, rows, cols):
 def _layer_norm_grad_args(dout, x, weight, mean, rstd, dx, dweight, dbias, accumulate):
     """(arguments up to the workspace's, bytes of workspace)."""
     p, rows, cols, stride = _matrix(x, _FLOATS, "x")
-    y, *y_shape, y_stride = _matrix(dout, _FLOATS, "dout")
-    _same_shape(rows, cols, "dout", tuple(y_shape))
-    d, *d_shape, d_stride = _matrix(dx, (x.dtype,), "dx")
-    _same_shape(rows, cols, "dx", tuple(d_shape))
-    (w, dw, db), affine = _affine((("weight", weight), ("dweight", dweight), ("dbias", dbias)), cols)
-    m, r = _vector(mean, torch.float32, rows, "mean"), _vector(rstd, torch.float32, rows, "rstd")
+    y, y_rows, y_cols, y_stride = _matrix(dout, _FLOATS, "dout")
+    _same_shape(rows, cols, "dout", (y_rows, y_cols))
+    d, d_rows, d_cols, d_stride = _matrix(dx, (x.dtype,), "dx")
+    _same_shape(rows, cols, "dx", (d_rows, d_cols))
+    at, affine = _affine_dtype(weight, dweight, dbias)
+    dw, db = _optional(dweight, at, cols, "dweight"), _optional(dbias, at, cols, "dbias")
     xt, yt = _FLOATS[x.dtype], _FLOATS[dout.dtype]
     need = 0 if dw is None and db is None else _layer_norm_grad_bytes(xt, yt, rows, cols)
-    return (y, yt, y_stride, p, xt, stride, rows, cols, w, affine, m, r, d, d_stride, dw, db, int(bool(accumulate))), need
+    return (y, yt, y_stride, p, xt, stride, rows, cols, _optional(weight, at, cols, "weight"), affine,
+            _vector(mean, torch.float32, rows, "mean"), _vector(rstd, torch.float32, rows, "rstd"), d, d_stride, dw, db,
+            int(bool(accumulate))), need
 
 
 def layer_norm_grad_call(dout, x, weight, mean, rstd, dx, dweight=None, dbias=None, accumulate=False, workspace=None):

@@ -585,9 +585,10 @@ tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t d
  *   x, dx, w_gate, w_up, out, dout, gates  rows their strides apart, 2-byte
  *           aligned.  What lies between two rows is left alone.  No output may
  *           overlap an input.  Where rows of x or of the weights do not all start
- *           and end on 16 bytes, the weights' strides differ, or, for the
- *           gradients, ffn_size is no multiple of 32, the workspace holds a copy of
- *           them (the forward pass of up to 16 tokens needs none).
+ *           and end on 16 bytes, hidden_size is no multiple of 32 (not where the
+ *           product is small), the weights' strides differ, or, for the gradients,
+ *           ffn_size is no multiple of 32, the workspace holds a copy of them (the
+ *           forward pass of up to 16 tokens needs none).
  *   dw_gate, dw_up  ffn_size x hidden_size of dw_dtype, without gaps
  *   workspace  as for the weight gradient above; with gradients it also holds dg
  *           and du.  The _workspace call takes the same gates (NULL or not).

@@ -150,11 +150,12 @@ struct GatedArgs {
 // A lane's columns of both products lie side by side in its accumulators (Form::kPair):
 // the epilogue takes no LDS, its stores are 16 bytes a lane, 64 a row, from one
 // shared address and the lane's offset, and dh's rows are asked for before the
-// first is used.  GRAD: dg and du instead of h.
-template <bool GRAD, int BM, int BN, int WM, int WN>
+// first is used.  GRAD: dg and du instead of h.  WHOLE: k is whole steps (tiles of 64
+// take any).
+template <bool GRAD, bool WHOLE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, BM == 64 ? 1 : 2) void gated_kernel(GatedArgs a) {
   using G = std::conditional_t<BM == 64, DeepGemm<Form::kRows, Form::kPair, BM, BN, WM, WN, false, 2>,
-                               Gemm<Form::kRows, Form::kPair, Code::kE4m3, BM, BN, WM, WN, false, true>>;
+                               Gemm<Form::kRows, Form::kPair, Code::kE4m3, BM, BN, WM, WN, false, WHOLE>>;
   __shared__ __align__(16) char lds0[G::kStage];
   __shared__ __align__(16) char lds1[G::kStage];
   __shared__ __align__(16) char lds2[G::kStage];
@@ -484,11 +485,17 @@ Layout layout_of(const GatedCall& c) {
   L.few = c.tokens <= kFew;
   L.half = up(c.ffn, 32);
   L.ld = up(c.hidden, 64);
-  L.depth = up(c.hidden, kBK);
-  // Tiles read rows that start and end on 16 bytes, of whole steps of k (copies are
-  // filled up with zeros); dx reads the weights one behind the other.
+  if (L.gates && !L.few)
+    L.fwd = tiling_of((c.hidden + kBK - 1) / kBK, 0,  // k along the rows of both
+                      [&](int64_t side) { return tiles_on(c.tokens, side) * tiles_on(c.ffn, pair_columns(side)); }, 0.2);
+  // Tiles read rows that start and end on 16 bytes, those of 256 whole steps of k too:
+  // a short last one spills their registers (8192 tokens, 4104 x 14336 2190 us, with
+  // the copies, which are filled up with zeros, 1620), the smaller tiles' not (700,
+  // 1016 x 2000 15 us, with the copies 28).  dx reads the weights one behind the
+  // other.
   const bool tiles = c.grad || !L.few;
-  const bool steps = !(L.gates && !L.few) || c.hidden % kBK == 0;
+  const bool steps = !(L.gates && !L.few) || L.fwd.side < 256 || c.hidden % kBK == 0;
+  L.depth = steps ? c.hidden : up(c.hidden, kBK);
   const bool w_aligned = steps && rows_aligned(c.w_gate, c.gate_ld, c.hidden) && rows_aligned(c.w_up, c.up_ld, c.hidden) &&
                          c.gate_ld == c.up_ld;
   L.copy_x = tiles && !(steps && rows_aligned(c.x, c.x_ld, c.hidden));
@@ -504,11 +511,7 @@ Layout layout_of(const GatedCall& c) {
     partial = n > partial ? n : partial;
     L.queued |= t.cut.items > tile_slots(t.side);
   };
-  if (L.gates && !L.few) {
-    L.fwd = tiling_of(L.depth / kBK, 0,  // k along the rows of both
-                      [&](int64_t side) { return tiles_on(c.tokens, side) * tiles_on(c.ffn, pair_columns(side)); });
-    also(L.fwd);
-  }
+  if (L.gates && !L.few) also(L.fwd);
   if (c.grad) {
     const int64_t w_ld = L.copy_w ? L.ld : c.gate_ld, x_ld = L.copy_x ? L.ld : c.x_ld;
     const int64_t wide = 2 * L.half > x_ld ? 2 * L.half : x_ld;
@@ -642,22 +645,22 @@ int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
     a.queue = a.cut.items > tile_slots(L.fwd.side) ? queues : nullptr;
     a.f = f;
     const dim3 grid(resident_groups(a.cut.items, L.fwd.side));
-    if (L.fwd.side == 256) {
-      if (c.grad)
-        hipLaunchKernelGGL((gated_kernel<true, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
-      else
-        hipLaunchKernelGGL((gated_kernel<false, 256, 256, 2, 4>), grid, dim3(512), 0, st, a);
-    } else if (L.fwd.side == 128) {
-      if (c.grad)
-        hipLaunchKernelGGL((gated_kernel<true, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
-      else
-        hipLaunchKernelGGL((gated_kernel<false, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
-    } else {
-      if (c.grad)
-        hipLaunchKernelGGL((gated_kernel<true, 64, 128, 2, 2>), grid, dim3(256), 0, st, a);
-      else
-        hipLaunchKernelGGL((gated_kernel<false, 64, 128, 2, 2>), grid, dim3(256), 0, st, a);
-    }
+#define TIDE_GATED(WHOLE, BM, BN, WN)                                                                \
+  do {                                                                                               \
+    if (c.grad)                                                                                      \
+      hipLaunchKernelGGL((gated_kernel<true, WHOLE, BM, BN, 2, WN>), grid, dim3(128 * WN), 0, st, a); \
+    else                                                                                             \
+      hipLaunchKernelGGL((gated_kernel<false, WHOLE, BM, BN, 2, WN>), grid, dim3(128 * WN), 0, st, a); \
+  } while (0)
+    if (L.fwd.side == 256)
+      TIDE_GATED(true, 256, 256, 4);
+    else if (L.fwd.side == 128 && L.depth % kBK == 0)
+      TIDE_GATED(true, 128, 128, 2);
+    else if (L.fwd.side == 128)
+      TIDE_GATED(false, 128, 128, 2);
+    else
+      TIDE_GATED(true, 64, 128, 2);
+#undef TIDE_GATED
     TIDE_LAUNCHED();
     if (a.cut.splits > 1) {
       const unsigned rest = a.cut.tiles - a.cut.full;

@@ -104,13 +104,14 @@ inline double cut_cost(const Cut& c, int64_t steps, int64_t side) {
 
 // A product's tiles: the side (a small tile's is that of its rows) and the cut that
 // are estimated to end first.  tiles(side) counts them.  Tiles of 64 are not split (a
-// step of them takes 0.1 us, a tile about 3 more) and read operands below 4 GiB.
+// step of them takes `small_step` us, a tile about 4 more) and read operands below 4
+// GiB.
 struct Tiling {
   int64_t side = 256;
   Cut cut{};
 };
 template <typename F>
-inline Tiling tiling_of(int64_t steps, int64_t operand_bytes, F tiles) {
+inline Tiling tiling_of(int64_t steps, int64_t operand_bytes, F tiles, double small_step = 0.15) {
   Tiling best;
   double least = 0;
   for (int64_t side : {256, 128, 64}) {
@@ -121,7 +122,7 @@ inline Tiling tiling_of(int64_t steps, int64_t operand_bytes, F tiles) {
     if (side == 64) {
       if (operand_bytes >= int64_t(1) << 31) break;
       t.cut = Cut{uint32_t(n), uint32_t(n), 1, uint32_t(steps), uint32_t(n)};
-      cost = double((n + 255) / 256) * (double(steps) * 0.1 + 3.0);
+      cost = double((n + 255) / 256) * (double(steps) * small_step + 4.0);
     } else {
       t.cut = cut_tiles(n, steps, side);
       cost = cut_cost(t.cut, steps, side);

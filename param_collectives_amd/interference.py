@@ -25,7 +25,9 @@ a small-M GEMM (256 x 8192 x 8192, bf16) and a large GEMM (8192^3, bf16), both
 torch.matmul (the vendor GEMM library).  On request (--victims), the library's
 own kernels of the backward pass that a reduce-scatter overlaps: a down
 projection's weight gradient from its 8-bit checkpoint (8192 tokens, 4096 x
-14336) and the vocabulary loss with its gradients (2048 tokens, 32000 x 4096).
+14336), the vocabulary loss with its gradients (2048 tokens, 32000 x 4096), layer
+norm's gradients (8192 tokens, 4096) and the gated block's (4096 tokens, 14336 x
+4096); and of the optimizer's step, an orthogonalized update (4096 x 4096).
 Reported per pair: the victim's p50
 latency alone and beside the aggressor (only launches that ran entirely
 inside the aggressor's run count), the slowdown, the aggressor's own time
@@ -58,9 +60,13 @@ ROOT = os.path.dirname(HERE)
 
 ELEMENTWISE_ELEMS = 64 * 2**20  # 256 MiB of fp32 in, 256 MiB out
 GEMMS = {"gemm_256x8192x8192": (256, 8192, 8192), "gemm_8192x8192x8192": (8192, 8192, 8192)}
-# tokens, out features, in features; tokens, hidden size, vocabulary
+# tokens, out features, in features; tokens, hidden size, vocabulary; tokens, hidden size; tokens, hidden size, ffn size;
+# rows, columns
 WEIGHT_GRADS = {"weight_grad_8192x4096x14336": (8192, 4096, 14336)}
 VOCAB_LOSSES = {"vocab_loss_grad_2048x4096x32000": (2048, 4096, 32000)}
+NORM_GRADS = {"layer_norm_grad_8192x4096": (8192, 4096)}
+GATED_GRADS = {"gated_block_grad_4096x4096x14336": (4096, 4096, 14336)}
+UPDATES = {"orthogonalize_4096x4096": (4096, 4096)}
 
 
 def _median(v):
@@ -153,6 +159,28 @@ class Study:
             dh, dw = torch.empty_like(h), torch.empty_like(w)
             torch.cuda.synchronize()
             return tide.vocab_loss_grad_call(h, w, t, g, loss, None, dh, dw)
+        if name in NORM_GRADS:
+            tokens, size = NORM_GRADS[name]
+            x, dy = (torch.randn(tokens, size, device="cuda").to(torch.bfloat16) for _ in range(2))
+            w, dw, db = (torch.ones(size, device="cuda") for _ in range(3))
+            mean, rstd = torch.empty(tokens, device="cuda"), torch.empty(tokens, device="cuda")
+            dx = torch.empty_like(x)
+            tide.layer_norm(x, w, None, dx, mean, rstd)
+            torch.cuda.synchronize()
+            return tide.layer_norm_grad_call(dy, x, w, mean, rstd, dx, dw, db)
+        if name in GATED_GRADS:
+            tokens, size, ffn = GATED_GRADS[name]
+            x = torch.randn(tokens, size, device="cuda").to(torch.bfloat16)
+            wg, wu = ((torch.randn(ffn, size, device="cuda") * size**-0.5).to(torch.bfloat16) for _ in range(2))
+            dout = torch.randn(tokens, ffn, device="cuda").to(torch.bfloat16)
+            dx, dwg, dwu = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+            torch.cuda.synchronize()
+            return tide.gated_block_grad_call(dout, x, wg, wu, dx, dwg, dwu)
+        if name in UPDATES:
+            update = torch.randn(*UPDATES[name], device="cuda").to(torch.bfloat16)
+            out = torch.empty_like(update)
+            torch.cuda.synchronize()
+            return tide.orthogonalize_call([update], [out])
         m, k, n = GEMMS[name]
         a = torch.randn(m, k, device="cuda").to(torch.bfloat16)
         b = torch.randn(k, n, device="cuda").to(torch.bfloat16)
@@ -429,7 +457,7 @@ def main(argv=None):
     ap.add_argument("--out", required=True, help="folder for the JSON result")
     ap.add_argument("--profiles", default=None, help="also write the text summary here")
     ap.add_argument("--victims", default="elementwise," + ",".join(GEMMS),
-                    help="also: " + ", ".join([*WEIGHT_GRADS, *VOCAB_LOSSES]))
+                    help="also: " + ", ".join([*WEIGHT_GRADS, *VOCAB_LOSSES, *NORM_GRADS, *GATED_GRADS, *UPDATES]))
     ap.add_argument("--per-call", action="store_true", help="one aggressor call inside a victim sequence")
     args = ap.parse_args(argv)
     if ROOT not in sys.path:

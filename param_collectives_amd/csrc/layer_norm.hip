@@ -5,9 +5,9 @@
 //   dx = rstd (g - sum g / n - xh sum (g xh) / n)
 //   dw = sum over rows of dy xh,  db = sum over rows of dy.
 //
-// Bound by HBM.  A row stays in the registers of the threads that share it (a
-// wave, or a workgroup of 256 or 512), so that every value is read once: the mean,
-// the squares around it and the result come from there.  A thread takes 16 bytes
+// Bound by HBM.  A row stays in the registers of the threads that share it (16
+// lanes, a wave, or a workgroup of 256 to 1024), so that every value is read once:
+// the mean, the squares around it and the result come from there.  A thread takes 16 bytes
 // of the wider type at a time, neighbouring threads neighbouring ones, and holds
 // the same columns of each row that its workgroup walks: weight and bias are read
 // once, and the sums of dw and db go on in registers, fp32, until the workgroup's
@@ -18,6 +18,10 @@
 // A row's values are summed in fp64 and the mean is kept in two fp32: a mean far
 // above the deviations costs the rounding of x alone.  The other sums of a row are
 // fp32 in a thread (at most 32 values) and fp64 over the threads.
+//
+// Measured: 8191 rows of 5120, fp32 to bf16, 47 us (5.3 TB/s); gradients of 16384
+// rows of 8192 in bf16 160 us (5.0 TB/s), of 262144 rows of 128 45 us (4.5 TB/s, two
+// launches; the forward pass 28 us); a few rows 3 us of kernel in a call of 4.5.
 //
 // Rows too long for the registers are read two or three times, by loops.
 #include <hip/hip_runtime.h>
@@ -140,6 +144,7 @@ __device__ __forceinline__ Columns columns_of(int cols, int j, int t) {
   return Columns{uint32_t(over > 0 ? cols - U : c), over <= 0 ? 0 : over < U ? over : U};
 }
 
+// Column c's weight or bias.
 __device__ __forceinline__ float affine(const void* p, int32_t f32, int64_t c, float none) {
   if (p == nullptr) return none;
   return f32 ? static_cast<const float*>(p)[c] : low_bf16(static_cast<const uint16_t*>(p)[c]);
@@ -167,8 +172,9 @@ __device__ __forceinline__ void affine_values(const void* p, int32_t f32, uint32
   }
 }
 
-// The sum over a wave, in every lane: within 16 lanes, then lane 15 of a row of
-// lanes to the next one and lane 31 to the upper half.
+// The sum over 16 neighbouring lanes or a wave, in every one of them: within 16
+// lanes, then lane 15 of a row of lanes to the next one and lane 31 to the upper
+// half.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float moved(float v) {
   return __uint_as_float(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, ROWS, 0xF, true));
@@ -188,12 +194,13 @@ __device__ __forceinline__ double last_lane(double v) {
   return __builtin_bit_cast(double, uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(b >> 32), 63))) << 32 |
                                         uint32_t(__builtin_amdgcn_readlane(uint32_t(b), 63)));
 }
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
+template <int LANES, typename T>
+__device__ __forceinline__ T lanes_sum(T v) {
   v += moved<0xB1, 0xF>(v);   // lane ^ 1
   v += moved<0x4E, 0xF>(v);   // lane ^ 2
   v += moved<0x141, 0xF>(v);  // the other four of eight
   v += moved<0x140, 0xF>(v);  // the other eight of sixteen
+  if constexpr (LANES == 16) return v;
   v += moved<0x142, 0xA>(v);
   v += moved<0x143, 0xC>(v);
   return last_lane(v);
@@ -204,14 +211,14 @@ __device__ __forceinline__ T wave_sum(T v) {
 // only, not for the rows on their way.
 template <int SHARE>
 struct RowSum {
-  static constexpr int kWaves = SHARE / 64;
+  static constexpr int kWaves = SHARE < 64 ? 1 : SHARE / 64;
   double (*words)[2][kWaves];
   int turn = 0;
 
   template <int N, typename T>
   __device__ __forceinline__ void operator()(T* v) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+    for (int k = 0; k < N; ++k) v[k] = lanes_sum<SHARE < 64 ? SHARE : 64>(v[k]);
     if constexpr (kWaves > 1) {
       T(*w)[kWaves] = reinterpret_cast<T(*)[kWaves]>(words[turn]);
       if ((threadIdx.x & 63) == 0) {
@@ -251,11 +258,18 @@ __device__ __forceinline__ float rstd_of(float square, float rest, float eps) {
   return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
 }
 
-// The same for all lanes of a wave.
+// The same for all lanes of a wave but where they share several rows.
 template <int SHARE>
 __device__ __forceinline__ int64_t first_row() {
-  static_assert(SHARE == 64 || SHARE == kBlock<SHARE>, "rows of a workgroup");
+  static_assert(SHARE == 16 || SHARE == 64 || SHARE == kBlock<SHARE>, "rows of a workgroup");
+  if constexpr (SHARE == 16) return int64_t(blockIdx.x) * (kBlock<SHARE> / SHARE) + threadIdx.x / SHARE;
   return SHARE == 64 ? int64_t(blockIdx.x) * (kBlock<SHARE> / SHARE) + wave_index() : int64_t(blockIdx.x);
+}
+
+template <int SHARE>
+__device__ __forceinline__ char* row_at(const void* p, int64_t bytes) {
+  const char* row = static_cast<const char*>(p) + bytes;
+  return const_cast<char*>(SHARE < 64 ? row : uniform(row));
 }
 
 // One row after another through SETS sets of registers: use(k, row) is called
@@ -282,7 +296,7 @@ constexpr int sets_of(int words, int most) { return 3 * words > most ? 2 : 3; }
 template <bool XF32, bool YF32, int SHARE, int J>
 __global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_kernel(NormArgs a) {
   constexpr int U = XF32 || YF32 ? 4 : 8, kRows = kBlock<SHARE> / SHARE;
-  __shared__ double words[2][2][SHARE / 64];
+  __shared__ double words[2][2][RowSum<SHARE>::kWaves];
   RowSum<SHARE> sum{words};
   const int t = threadIdx.x % SHARE;
   const double per_value = 1.0 / double(a.cols);
@@ -299,7 +313,7 @@ __global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_kernel(NormArgs a) {
   walk<kSet>(
       first_row<SHARE>(), int64_t(gridDim.x) * kRows, a.rows,
       [&](int set, int64_t row) {
-        const char* p = uniform(static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>);
+        const char* p = row_at<SHARE>(a.x, row * a.x_ld * kSize<XF32>);
 #pragma unroll
         for (int j = 0; j < J; ++j)
           if (at[j].again < U) x[set][j].load(p, at[j].first);
@@ -335,7 +349,7 @@ __global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_kernel(NormArgs a) {
         for (int j = 0; j < J; ++j) x[set][j].renewed();
         m.rstd = rstd_of(square[0] / float(a.cols), m.rest, a.eps);
         const float back = -m.rest * m.rstd;
-        char* out = const_cast<char*>(uniform(static_cast<const char*>(a.out) + row * a.out_ld * kSize<YF32>));
+        char* out = row_at<SHARE>(a.out, row * a.out_ld * kSize<YF32>);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if (at[j].again == U) continue;
@@ -357,7 +371,7 @@ __global__ __launch_bounds__(kBlock<SHARE>) void layer_norm_kernel(NormArgs a) {
 template <bool XF32, bool YF32, int SHARE, int J>
 __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormArgs a) {
   constexpr int U = XF32 || YF32 ? 4 : 8, kRows = kBlock<SHARE> / SHARE;
-  __shared__ double words[2][2][SHARE / 64];
+  __shared__ double words[2][2][RowSum<SHARE>::kWaves];
   RowSum<SHARE> sum{words};
   const int t = threadIdx.x % SHARE;
   const float per_value = 1.0f / float(a.cols);
@@ -377,8 +391,8 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
   walk<kSet>(
       first_row<SHARE>(), int64_t(gridDim.x) * kRows, a.rows,
       [&](int set, int64_t row) {
-        const char* px = uniform(static_cast<const char*>(a.x) + row * a.x_ld * kSize<XF32>);
-        const char* py = uniform(static_cast<const char*>(a.dy) + row * a.dy_ld * kSize<YF32>);
+        const char* px = row_at<SHARE>(a.x, row * a.x_ld * kSize<XF32>);
+        const char* py = row_at<SHARE>(a.dy, row * a.dy_ld * kSize<YF32>);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if (at[j].again == U) continue;
@@ -427,7 +441,7 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
         }
         s = both[0] * per_value;
         sx = -both[1] * per_value;
-        char* out = const_cast<char*>(uniform(static_cast<const char*>(a.out) + row * a.out_ld * kSize<XF32>));
+        char* out = row_at<SHARE>(a.out, row * a.out_ld * kSize<XF32>);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if (at[j].again == U) continue;
@@ -446,10 +460,20 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
   if (a.partial == nullptr) return;
   float* p = a.partial + int64_t(blockIdx.x) * 2 * a.cols;
   if constexpr (kRows > 1) {
-    // the waves' sums, one after the other
+    // the sums of a wave's rows, then those of the waves, one after the other
+    if constexpr (SHARE < 64) {
+#pragma unroll
+      for (int k = 0; k < J * U; ++k)
+#pragma unroll
+        for (int lanes = SHARE; lanes < 64; lanes *= 2) {
+          dw[k] += __shfl_xor(dw[k], lanes);
+          db[k] += __shfl_xor(db[k], lanes);
+        }
+    }
     __shared__ float all[2 * SHARE * U * J];
-    for (int turn = 0; turn < kRows; ++turn) {
-      if (int(threadIdx.x) / SHARE == turn) {
+    constexpr int kWaves = kBlock<SHARE> / 64;
+    for (int turn = 0; turn < kWaves; ++turn) {
+      if (int(threadIdx.x) / 64 == turn && int(threadIdx.x) % 64 < SHARE) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -465,7 +489,7 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
       }
       __syncthreads();
     }
-    if (int(threadIdx.x) / SHARE != kRows - 1) return;
+    if (int(threadIdx.x) / 64 != kWaves - 1 || int(threadIdx.x) % 64 >= SHARE) return;
   }
 #pragma unroll
   for (int j = 0; j < J; ++j)
@@ -480,7 +504,7 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
 
 // The sums of dw and db over the workgroups: kSlices threads a column, each
 // adding its share of the workgroups in order, then one the shares.
-constexpr int kSlices = 16, kJoinCols = 64;
+constexpr int kSlices = 16, kJoinCols = 64, kAtOnce = 16;  // loads on their way
 __global__ __launch_bounds__(kSlices* kJoinCols) void join_affine_kernel(const float* partial, int64_t groups,
                                                                          int64_t cols, void* dw, void* db,
                                                                          int32_t f32, int32_t accumulate) {
@@ -490,10 +514,21 @@ __global__ __launch_bounds__(kSlices* kJoinCols) void join_affine_kernel(const f
   float a = 0.0f, b = 0.0f;
   if (c < cols) {
     const int64_t per = (groups + kSlices - 1) / kSlices, g0 = slice * per, g1 = g0 + per < groups ? g0 + per : groups;
-#pragma unroll 4
-    for (int64_t g = g0; g < g1; ++g) {
-      a += partial[g * 2 * cols + c];
-      b += partial[(g * 2 + 1) * cols + c];
+    const float* p = partial + g0 * 2 * cols + c;
+    int64_t left = g1 - g0;
+    for (; left > 0; left -= kAtOnce, p += kAtOnce * 2 * cols) {
+      float v[kAtOnce], w[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t at = (i < left ? i : 0) * 2 * cols;
+        v[i] = p[at];
+        w[i] = p[at + cols];
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        a += i < left ? v[i] : 0.0f;
+        b += i < left ? w[i] : 0.0f;
+      }
     }
   }
   part[0][slice][k] = a;
@@ -651,19 +686,20 @@ struct Shape {
   int64_t groups;
 };
 
-// As few threads a row as hold it in 32 values each (16 of a wave's, and for the
-// gradients, which hold three more values for each), so that several rows are
-// worked on in a CU and few threads wait for each other.  A workgroup of the
-// gradients leaves two fp32 sums a column, so there are no more of them than a 16th
-// of the rows, but one a CU.
+// As few threads a row as hold it in 32 values each (16 of 16 lanes' and a wave's
+// and for the gradients, which hold three more values for each; 8 of 16 lanes' for
+// the gradients, 16 spill: 65536 rows of 200 126 us instead of 34), so that several
+// rows are worked on in a CU and few threads wait for each other: 262144 rows of 128
+// take 28 us by 16 lanes and 79 by a wave, their gradients 45 and 75.  A workgroup
+// of the gradients leaves two fp32 sums a column, so there is at most one for 64
+// rows (16 where all of it shares a row), but one a CU.
 Shape shape_of(const LayerNormCall& c, bool grad) {
   const int64_t u = c.x_f32 || c.y_f32 ? 4 : 8;
   Shape s{0, 0, 0};
-  if (c.cols >= u)
-  for (int share : {64, 256, 512, 1024}) {
-    const int64_t most = (share == 64 || grad ? 16 : 32) / u;
+  for (int share : {16, 64, 256, 512, 1024}) {
+    const int64_t most = (share == 16 && grad ? 8 : share <= 64 || grad ? 16 : 32) / u;
     if (!grad && share == 1024) break;
-    if (c.cols <= share * u * most) {
+    if (c.cols >= u && c.cols <= share * u * most) {
       s.share = share;
       s.j = int((c.cols + share * u - 1) / (share * u));
       break;
@@ -677,7 +713,8 @@ Shape shape_of(const LayerNormCall& c, bool grad) {
   const int64_t need = (c.rows + at_once - 1) / at_once;
   int64_t most = 1024 * 256 / block;
   if (grad) {
-    if (most > need / 16) most = need / 16;
+    const int64_t each = s.share == 16 ? 4 : 16;
+    if (most > need / each) most = need / each;
     if (most < 256) most = 256;
   }
   s.groups = need < most ? need : most;
@@ -707,7 +744,9 @@ int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad,
   constexpr int kMore = kPer == 2 ? 3 : 2, kFive = kPer == 2 ? 5 : 3;
 #define TIDE_NORM(KERNEL, SHARE, J) hipLaunchKernelGGL((KERNEL<XF32, YF32, SHARE, J>), grid, dim3(kBlock<SHARE>), 0, st, a)
   if (grad) {
-    if (s.share == 64 && s.j <= kPer)
+    if (s.share == 16)
+      TIDE_NORM(layer_norm_grad_kernel, 16, kPer);
+    else if (s.share == 64 && s.j <= kPer)
       TIDE_NORM(layer_norm_grad_kernel, 64, kPer);
     else if (s.share == 64)
       TIDE_NORM(layer_norm_grad_kernel, 64, 2 * kPer);
@@ -724,7 +763,11 @@ int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad,
     else
       TIDE_NORM(layer_norm_grad_kernel, 1024, 2 * kPer);
   } else {
-    if (s.share == 64 && s.j <= kPer)
+    if (s.share == 16 && s.j <= kPer)
+      TIDE_NORM(layer_norm_kernel, 16, kPer);
+    else if (s.share == 16)
+      TIDE_NORM(layer_norm_kernel, 16, 2 * kPer);
+    else if (s.share == 64 && s.j <= kPer)
       TIDE_NORM(layer_norm_kernel, 64, kPer);
     else if (s.share == 64)
       TIDE_NORM(layer_norm_kernel, 64, 2 * kPer);

@@ -151,7 +151,7 @@ struct GatedArgs {
 // the epilogue takes no LDS, its stores are 16 bytes a lane, 64 a row, from one
 // shared address and the lane's offset, and dh's rows are asked for before the
 // first is used.  GRAD: dg and du instead of h.  WHOLE: k is whole steps (tiles of 64
-// take any).
+// rows take any).
 template <bool GRAD, bool WHOLE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, BM == 64 ? 1 : 2) void gated_kernel(GatedArgs a) {
   using G = std::conditional_t<BM == 64, DeepGemm<Form::kRows, Form::kPair, BM, BN, WM, WN, false, 2>,
@@ -464,6 +464,7 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 int64_t tiles_on(int64_t n, int64_t side) { return (n + side - 1) / side; }
 // Columns of g and u in a tile.
+// Columns of h in a tile (of 64 rows: 32 in the narrow ones).
 int64_t pair_columns(int64_t side) { return side == 64 ? 64 : side / 2; }
 
 constexpr int64_t kFew = 16;       // tokens that few_gated_kernel takes
@@ -471,7 +472,7 @@ constexpr uint32_t kProducts = 3;  // g and u; dx; dWg and dWu
 
 // Where one call's workspace keeps what.
 struct Layout {
-  bool few = false, copy_x = false, copy_w = false, gates = false;  // gates: g and u are formed
+  bool few = false, narrow = false, copy_x = false, copy_w = false, gates = false;  // gates: g and u are formed
   int64_t ld = 0, half = 0, depth = 0;
   Tiling fwd, dx, dw;
   bool queued = false;
@@ -488,6 +489,14 @@ Layout layout_of(const GatedCall& c) {
   if (L.gates && !L.few)
     L.fwd = tiling_of((c.hidden + kBK - 1) / kBK, 0,  // k along the rows of both
                       [&](int64_t side) { return tiles_on(c.tokens, side) * tiles_on(c.ffn, pair_columns(side)); }, 0.2);
+  // Small tiles' steps take the time of their LDS accesses.  As long as all of them are
+  // on CUs of their own, tiles of half the columns, of two waves, take less (17 tokens,
+  // 2048 x 768 10.7 us instead of 13.6); with more tiles the wide ones, which read
+  // less (64 tokens, 4096 x 14336 53 us instead of 70).
+  if (const int64_t n = tiles_on(c.tokens, 64) * tiles_on(c.ffn, 32); L.fwd.side == 64 && n <= tile_slots(64)) {
+    L.narrow = true;
+    L.fwd.cut.items = L.fwd.cut.tiles = L.fwd.cut.full = uint32_t(n);
+  }
   // Tiles read rows that start and end on 16 bytes, those of 256 whole steps of k too:
   // a short last one spills their registers (8192 tokens, 4104 x 14336 2190 us, with
   // the copies, which are filled up with zeros, 1620), the smaller tiles' not (700,
@@ -641,7 +650,7 @@ int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
     a.cut = L.fwd.cut;
     a.partial = partial;
     a.tiles_m = uint32_t(tiles_on(c.tokens, L.fwd.side));
-    a.tiles_n = uint32_t(tiles_on(c.ffn, pair_columns(L.fwd.side)));
+    a.tiles_n = uint32_t(tiles_on(c.ffn, L.narrow ? 32 : pair_columns(L.fwd.side)));
     a.queue = a.cut.items > tile_slots(L.fwd.side) ? queues : nullptr;
     a.f = f;
     const dim3 grid(resident_groups(a.cut.items, L.fwd.side));
@@ -658,6 +667,8 @@ int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
       TIDE_GATED(true, 128, 128, 2);
     else if (L.fwd.side == 128)
       TIDE_GATED(false, 128, 128, 2);
+    else if (L.narrow)
+      TIDE_GATED(true, 64, 64, 1);
     else
       TIDE_GATED(true, 64, 128, 2);
 #undef TIDE_GATED

@@ -75,7 +75,7 @@ class Block:
 # more tiles than workgroups, of each product; large tiles
 SIZES = [(1, 8, 1), (1, 64, 32), (3, 40, 33), (16, 100, 70), (16, 2048, 768), (5, 33, 17), (7, 64, 8200), (2, 1000, 8193),
          (17, 64, 64), (64, 72, 130), (130, 257, 131), (200, 520, 1000), (33, 2048, 200), (600, 1000, 700), (2100, 40, 4100),
-         (2100, 2200, 96), (520, 8200, 40), (40, 8200, 300)]
+         (2100, 2200, 96), (520, 8200, 40), (40, 8200, 300), (20, 72, 9001), (130, 264, 4100)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])

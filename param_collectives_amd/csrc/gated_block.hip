@@ -463,8 +463,7 @@ __global__ __launch_bounds__(256) void clear_gradients_kernel(uint16_t* a, uint1
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 int64_t tiles_on(int64_t n, int64_t side) { return (n + side - 1) / side; }
-// Columns of g and u in a tile.
-// Columns of h in a tile (of 64 rows: 32 in the narrow ones).
+// Columns of g and u in a tile (32 in the narrow ones).
 int64_t pair_columns(int64_t side) { return side == 64 ? 64 : side / 2; }
 
 constexpr int64_t kFew = 16;       // tokens that few_gated_kernel takes

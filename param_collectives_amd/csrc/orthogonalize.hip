@@ -185,7 +185,7 @@ struct SymmetricArgs {
   int64_t depth;
   Cut cut;
   float* partial;
-  uint32_t tiles, side_tiles;  // of a matrix; on its side
+  uint32_t tiles;  // of a matrix
   uint32_t* queue;
   const uint16_t* g;  // or null
   uint16_t* out;      // size x size each (columns to padded(size)), rows `ld` apart, `matrix` elements from one to the next
@@ -311,6 +311,103 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_ker
           if (item != kNoItem) open(item);
         });
   }
+}
+
+// Few and small matrices, k along the rows: a workgroup has a tile of 32 x 32 and its
+// waves split k, each reading its steps of the rows straight into registers, eight of
+// them on their way.  Taken where every tile has a CU (512 x 2048 orthogonalized
+// takes 136 us, by tiles of 64 through LDS 143; 60 of 64 x 128 86 for 101; 16 of 256 x
+// 256, whose 576 tiles are too many, 107 either way).  What is left is the launches':
+// one that only waits for the last one's results takes 4 us of the 8 a launch.
+constexpr int kFewWaves = 8;
+__global__ __launch_bounds__(kFewWaves * 64) void few_symmetric_kernel(SymmetricArgs a) {
+  constexpr int kDeep = 4;  // steps whose loads go out together
+  __shared__ f32x4v part[kFewWaves][4][64];
+  __shared__ float values[32][33];
+  const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
+  int64_t z;
+  uint32_t tm, tn;
+  symmetric_tile(a, blockIdx.x, &z, &tm, &tn);
+  const int64_t m0 = int64_t(tm) * 32, n0 = int64_t(tn) * 32;
+  // rows past the end read the last one: their results are dropped
+  const uint16_t* rows = static_cast<const uint16_t*>(a.a.base) + z * a.a_matrix + 8 * g;
+  const uint16_t* from[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = (i < 2 ? m0 : n0) + 16 * (i & 1) + r;
+    from[i] = rows + (row < a.size ? row : a.size - 1) * a.a.ld;
+  }
+  const int64_t steps = a.depth / kBK, per = (steps + kFewWaves - 1) / kFewWaves, first = wave * per;
+  const int64_t end = first + per < steps ? first + per : steps;
+  f32x4v acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  struct Steps {
+    f16x8 x[kDeep][4];
+  } even, odd;
+  auto fetch = [&](Steps& to, int64_t s) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int64_t at = (s + u < end ? s + u : end - 1) * kBK;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to.x[u][i] = *(const TIDE_GLOBAL f16x8*)(from[i] + at);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all of them on their way before the first product
+  };
+  auto multiply = [&](const Steps& w, int64_t s) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      if (s + u >= end) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.x[u][2 + j], w.x[u][i], acc[i][j], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (first < end) {
+    fetch(even, first);
+    for (int64_t s = first; s < end; s += 2 * kDeep) {
+      if (s + kDeep < end) fetch(odd, s + kDeep);
+      multiply(even, s);
+      if (s + kDeep >= end) break;
+      if (s + 2 * kDeep < end) fetch(even, s + 2 * kDeep);
+      multiply(odd, s + kDeep);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[wave][i][lane] = acc[i >> 1][i & 1];
+  __syncthreads();
+  // a lane holds of row m0 + 16 i + r the columns n0 + 16 j + 4 g + 0..3; 128 threads take 8 columns each
+  if (threadIdx.x < 128) {
+    const int row = threadIdx.x / 4, col = threadIdx.x % 4 * 8, i = row / 16 * 2 + col / 16;
+    const int at = (row & 15) + (col & 15) / 4 * 16;
+    const int64_t m = m0 + row, n = n0 + col;
+    f32x8v v = {};
+    if (m < a.size) {
+      f32x4v lo = part[0][i][at], hi = part[0][i][at + 16];
+#pragma unroll
+      for (int k = 1; k < kFewWaves; ++k) {
+        lo = add4(lo, part[k][i][at]);
+        hi = add4(hi, part[k][i][at + 16]);
+      }
+      const int64_t to = z * a.matrix + m * a.ld + n;
+      v = a.value(a.scale(z), m, n, lo, hi, a.g ? *reinterpret_cast<const u32x4*>(a.g + to) : u32x4{0, 0, 0, 0});
+      *reinterpret_cast<u32x4*>(a.out + to) = eight_f16(v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) values[row][col + j] = v[j];
+  }
+  if (tm == tn) return;
+  __syncthreads();
+  if (threadIdx.x >= 128) return;
+  const int n = threadIdx.x / 4, m = threadIdx.x % 4 * 8;
+  if (n0 + n >= a.size) return;
+  f32x8v v;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = values[m + j][n];
+  *reinterpret_cast<u32x4*>(a.out + z * a.matrix + (n0 + n) * a.ld + m0 + m) = eight_f16(v);
 }
 
 // A part of a tile is 32 rows of 64 columns.
@@ -605,7 +702,13 @@ template <Form F>
 int launch_symmetric(SymmetricArgs a, const Tiling& t, int64_t count, uint32_t* queue, hipStream_t st) {
   a.cut = t.cut;
   a.tiles = uint32_t(t.cut.tiles / count);
-  a.side_tiles = uint32_t((a.size + t.side - 1) / t.side);
+  const int64_t on_side = (a.size + 31) / 32, few = count * on_side * (on_side + 1) / 2;
+  if (F == Form::kRows && t.side == 64 && few <= tile_slots(64)) {
+    a.cut.tiles = uint32_t(few);
+    a.tiles = uint32_t(few / count);
+    hipLaunchKernelGGL(few_symmetric_kernel, dim3(unsigned(few)), dim3(kFewWaves * 64), 0, st, a);
+    return int(hipGetLastError());
+  }
   a.queue = t.cut.items > tile_slots(t.side) ? queue : nullptr;
   const dim3 grid(resident_groups(t.cut.items, t.side));
   if (t.side == 256)

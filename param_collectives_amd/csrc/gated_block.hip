@@ -16,6 +16,12 @@
 // unrounded sums go in, and nothing but dg and du is written.  dx is one product
 // over 2 F values of k, the two weights stacked; dWg and dWu are one launch.
 //
+// Bound by the matrix cores and their power: 8192 tokens, 4096 x 14336 1.52 to 1.57
+// ms (1240 TFLOP/s; the cores busy 71% of its cycles), the gradients from x 4.4 ms
+// (1310 TFLOP/s), of 4096 tokens, 5120 x 13824 from kept gates 1.83 ms (1270).  Starting
+// the next tile's loads before a tile's whole epilogue gains nothing (-1.7% to +0.5%),
+// nor does leaving a tile's stores on their way behind them (-1.5% to 0).
+//
 // Up to 16 tokens, the weights' traffic is all that counts (few_gated_kernel).
 #include <hip/hip_runtime.h>
 
@@ -272,13 +278,18 @@ __global__ __launch_bounds__(256) void kept_gates_kernel(const uint16_t* gates, 
 // Up to 16 tokens: a workgroup has 16 columns, and its waves split k; each reads
 // its part of the 16 rows of both weights straight into registers, and the
 // tokens' states, which every workgroup reads, from the caches.  Rows may start
-// anywhere: nothing is copied first.
-template <int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 4) void few_gated_kernel(const uint16_t* x, int64_t x_ld, const uint16_t* gate,
-                                                               int64_t gate_ld, const uint16_t* up, int64_t up_ld,
-                                                               int64_t depth, Finish f) {
+// anywhere: nothing is copied first.  Bound by the bytes on their way: 1 token, 4096 x
+// 14336 43 us (5.4 TB/s), 16 tokens 51, 1 token, 8192 x 28672 156 us (6.0 TB/s).  (With
+// 4 waves 48, 53.5 and 155 us, with 16 50, 59 and 176; loads of 8 steps at once
+// spill, 110 us.)  Two sets of loads take turns, and each workgroup starts at a place
+// of its own in its rows, so that they do not ask the same channels at one time.
+constexpr int kFewWaves = 8;
+__global__ __launch_bounds__(kFewWaves * 64, 4) void few_gated_kernel(const uint16_t* x, int64_t x_ld,
+                                                                      const uint16_t* gate, int64_t gate_ld,
+                                                                      const uint16_t* up, int64_t up_ld, int64_t depth,
+                                                                      Finish f) {
   constexpr int kDeep = 4;  // steps whose loads go out together
-  __shared__ f32x4v part[2][WAVES][64];
+  __shared__ f32x4v part[2][kFewWaves][64];
   const int lane = threadIdx.x & 63, wave = wave_index(), r = lane & 15, g = lane >> 4;
   const int64_t n0 = int64_t(blockIdx.x) * 16;
   // rows past the end read the last one: their results are dropped
@@ -288,7 +299,7 @@ __global__ __launch_bounds__(WAVES * 64, 4) void few_gated_kernel(const uint16_t
   const uint16_t* xt = x + t * x_ld + 8 * g;
   typedef bf16x8 any_bf16x8 __attribute__((aligned(2)));
   auto load = [](const uint16_t* p) -> bf16x8 { return *(const TIDE_GLOBAL any_bf16x8*)p; };
-  const int64_t whole = depth / 32, per = (whole + WAVES - 1) / WAVES;
+  const int64_t whole = depth / 32, per = (whole + kFewWaves - 1) / kFewWaves;
   int64_t s = wave * per;
   const int64_t end = s + per < whole ? s + per : whole;
   f32x4v ag = f32x4v{0.f, 0.f, 0.f, 0.f}, au = ag;
@@ -342,7 +353,7 @@ __global__ __launch_bounds__(WAVES * 64, 4) void few_gated_kernel(const uint16_t
     ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bg, bx, ag, 0, 0, 0);
     au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bu, bx, au, 0, 0, 0);
   }
-  if (wave == WAVES - 1 && whole * 32 < depth) {
+  if (wave == kFewWaves - 1 && whole * 32 < depth) {
     const int64_t k = whole * 32, left = depth - k - 8 * g;
     auto some = [&](const uint16_t* p) {
       const u32x4 b = eight_of(p + k, left);
@@ -366,7 +377,7 @@ __global__ __launch_bounds__(WAVES * 64, 4) void few_gated_kernel(const uint16_t
   for (int i = 0; i < 4; ++i) {
     sum[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < WAVES; ++k) sum[i] = add4(sum[i], part[i >> 1][k][token + 16 * (2 * pair + (i & 1))]);
+    for (int k = 0; k < kFewWaves; ++k) sum[i] = add4(sum[i], part[i >> 1][k][token + 16 * (2 * pair + (i & 1))]);
   }
   finish(f, token, n0 + 8 * pair, sum[0], sum[1], sum[2], sum[3]);
 }
@@ -466,7 +477,7 @@ int64_t tiles_on(int64_t n, int64_t side) { return (n + side - 1) / side; }
 // Columns of g and u in a tile (32 in the narrow ones).
 int64_t pair_columns(int64_t side) { return side == 64 ? 64 : side / 2; }
 
-constexpr int64_t kFew = 16;       // tokens that few_gated_kernel takes
+constexpr int64_t kFew = 16;       // tokens that few_gated_kernel takes: one product's rows
 constexpr uint32_t kProducts = 3;  // g and u; dx; dWg and dWu
 
 // Where one call's workspace keeps what.
@@ -634,12 +645,8 @@ int launch_gated_block(const GatedCall& c, void* workspace, void* stream) {
     const unsigned grid = unsigned((c.grad ? L.half : c.ffn) + 15) / 16;
     const uint16_t *xp = static_cast<const uint16_t*>(c.x), *gate = static_cast<const uint16_t*>(c.w_gate),
                    *up_w = static_cast<const uint16_t*>(c.w_up);
-    if (grid >= 512)
-      hipLaunchKernelGGL(few_gated_kernel<4>, dim3(grid), dim3(256), 0, st, xp, c.x_ld, gate, c.gate_ld, up_w, c.up_ld,
-                         c.hidden, f);
-    else
-      hipLaunchKernelGGL(few_gated_kernel<8>, dim3(grid), dim3(512), 0, st, xp, c.x_ld, gate, c.gate_ld, up_w, c.up_ld,
-                         c.hidden, f);
+    hipLaunchKernelGGL(few_gated_kernel, dim3(grid), dim3(kFewWaves * 64), 0, st, xp, c.x_ld, gate, c.gate_ld, up_w,
+                       c.up_ld, c.hidden, f);
     TIDE_LAUNCHED();
   } else {
     GatedArgs a;

@@ -907,7 +907,10 @@ struct Gemm {
 // steps are filled up to a multiple of U with empty ones; they and a short last step,
 // filled up with zeros, go first, so that the loop starts whole ones only.  The
 // stages' places are chosen so that the last one ends a turn of the four: open()
-// may fill any of them, and the epilogue needs LDS of its own.
+// may fill any of them, and the epilogue needs LDS of its own.  (512 x 2048
+// orthogonalized by tiles of 64 took 187 us where they were 128, and a stage's
+// fragments read ahead 4% less; of 64 x 128 tiles three steps a stage instead of two,
+// 108 KB on their way, 2% more: what bounds a step is its LDS traffic.)
 template <Form FA, Form FB, int BM, int BN, int WM, int WN, bool F16, int U>
 struct DeepGemm : Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true> {
   using Base = Gemm<FA, FB, Code::kE4m3, BM, BN, WM, WN, F16, true>;

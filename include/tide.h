@@ -534,7 +534,7 @@ tide_status tide_vocab_loss_grad(const uint16_t* hidden, int64_t hidden_stride, 
  *   x, dx    rows x cols of x_dtype;  out, dout  rows x cols of out_dtype
  *            (dout_dtype); rows their strides apart, aligned to the element.
  *            What lies between two rows is left alone.  No output may overlap
- *            an input.
+ *            an input or another output.
  *   weight, bias, dweight, dbias  cols values of affine_dtype without gaps.
  *            weight NULL stands for 1, bias NULL for 0; dweight or dbias NULL:
  *            not wanted.
@@ -584,7 +584,7 @@ tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t d
  *
  *   x, dx, w_gate, w_up, out, dout, gates  rows their strides apart, 2-byte
  *           aligned.  What lies between two rows is left alone.  No output may
- *           overlap an input.  Where rows of x or of the weights do not all start
+ *           overlap an input or another output.  Where rows of x or of the weights do not all start
  *           and end on 16 bytes, hidden_size is no multiple of 32 (not where the
  *           product is small), the weights' strides differ, or, for the gradients,
  *           ffn_size is no multiple of 32, the workspace holds a copy of them (the

@@ -439,6 +439,7 @@ tide_status tide_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, in
     c.out = out;
     c.mean = mean;
     c.rstd = rstd;
+    if (mean != nullptr && mean == rstd) return invalid("mean and rstd are the same vector");
     return hip_status(tide::launch_layer_norm(c, nullptr, stream), "layer norm launch");
   });
 }
@@ -488,6 +489,7 @@ tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t d
     c.rstd = const_cast<float*>(rstd);
     c.dx = dx;
     c.dx_ld = dx_stride;
+    if (rows > 0 && dweight != nullptr && dweight == dbias) return invalid("dweight and dbias are the same vector");
     return hip_status(tide::launch_layer_norm(c, workspace, stream), "layer norm gradient launch");
   });
 }
@@ -558,6 +560,7 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
     c.dw_up = dw_up;
     c.dw_f32 = dw_dtype == TIDE_DTYPE_F32;
     c.accumulate = accumulate;
+    if (tokens > 0 && dw_gate == dw_up) return invalid("dw_gate and dw_up are the same matrix");
     return hip_status(tide::launch_gated_block(c, workspace, stream), "gated block gradient launch");
   });
 }

@@ -686,18 +686,23 @@ struct Shape {
   int64_t groups;
 };
 
-// As few threads a row as hold it in 32 values each (16 of 16 lanes' and a wave's
-// and for the gradients, which hold three more values for each; 8 of 16 lanes' for
-// the gradients, 16 spill: 65536 rows of 200 126 us instead of 34), so that several
-// rows are worked on in a CU and few threads wait for each other: 262144 rows of 128
-// take 28 us by 16 lanes and 79 by a wave, their gradients 45 and 75.  A workgroup
-// of the gradients leaves two fp32 sums a column, so there is at most one for 64
-// rows (16 where all of it shares a row), but one a CU.
+// As few threads a row as hold it in so many values each that several rows are worked
+// on in a CU and few threads wait for each other.  That many are 32, 16 of 16 lanes'
+// and a wave's, and for the gradients, which hold three more values for each, 16 of
+// bf16 and 12 where there is fp32: 16 spill (8192 fp32 rows of 4096 116 us instead of
+// 74; of 8192 124 instead of 79).  16 lanes have 8 of the gradients' (65536 rows of
+// 200 126 us with 16 and 34 by a wave).  By 16 lanes 262144 rows of 128 take 28 us, by
+// a wave 79, their gradients 45 and 75.  Above 12288 columns fp32 spills in the
+// registers of 1024 threads, but loops would take longer (4096 rows of 14336 300 and
+// 376 us).
+// A workgroup of the gradients leaves two fp32 sums a column, so there is at most one
+// for 64 rows, for 32 where a wave or all of it shares a row (one for 16: 16384 rows
+// of 2048 84 us instead of 74), but one a CU.
 Shape shape_of(const LayerNormCall& c, bool grad) {
   const int64_t u = c.x_f32 || c.y_f32 ? 4 : 8;
   Shape s{0, 0, 0};
   for (int share : {16, 64, 256, 512, 1024}) {
-    const int64_t most = (share == 16 && grad ? 8 : share <= 64 || grad ? 16 : 32) / u;
+    const int64_t most = (!grad ? share <= 64 ? 16 : 32 : share == 16 ? 8 : u == 4 && share < 1024 ? 12 : 16) / u;
     if (!grad && share == 1024) break;
     if (c.cols >= u && c.cols <= share * u * most) {
       s.share = share;
@@ -713,7 +718,7 @@ Shape shape_of(const LayerNormCall& c, bool grad) {
   const int64_t need = (c.rows + at_once - 1) / at_once;
   int64_t most = 1024 * 256 / block;
   if (grad) {
-    const int64_t each = s.share == 16 ? 4 : 16;
+    const int64_t each = s.share == 16 ? 4 : s.share == 64 ? 8 : 32;
     if (most > need / each) most = need / each;
     if (most < 256) most = 256;
   }
@@ -749,15 +754,17 @@ int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad,
     else if (s.share == 64 && s.j <= kPer)
       TIDE_NORM(layer_norm_grad_kernel, 64, kPer);
     else if (s.share == 64)
-      TIDE_NORM(layer_norm_grad_kernel, 64, 2 * kPer);
+      TIDE_NORM(layer_norm_grad_kernel, 64, kMore);
     else if (s.share == 256 && s.j <= kPer)
       TIDE_NORM(layer_norm_grad_kernel, 256, kPer);
     else if (s.share == 256)
-      TIDE_NORM(layer_norm_grad_kernel, 256, 2 * kPer);
-    else if (s.share == 512 && s.j <= kMore)
-      TIDE_NORM(layer_norm_grad_kernel, 512, kMore);
+      TIDE_NORM(layer_norm_grad_kernel, 256, kMore);
+    else if (s.share == 512 && s.j <= kPer)
+      TIDE_NORM(layer_norm_grad_kernel, 512, kPer);
     else if (s.share == 512)
-      TIDE_NORM(layer_norm_grad_kernel, 512, 2 * kPer);
+      TIDE_NORM(layer_norm_grad_kernel, 512, kMore);
+    else if (s.j <= kPer)
+      TIDE_NORM(layer_norm_grad_kernel, 1024, kPer);
     else if (s.j <= kMore)
       TIDE_NORM(layer_norm_grad_kernel, 1024, kMore);
     else

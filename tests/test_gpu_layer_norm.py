@@ -87,7 +87,7 @@ class Norm:
 # than workgroups
 SIZES = [(1, 1), (1, 8), (3, 7), (5, 64), (4, 512), (5, 513), (6, 1000), (7, 1024), (3, 1025), (9, 2048), (3, 4095),
          (2, 4096), (2, 4097), (2, 8192), (3, 8200), (2, 16384), (2, 16385), (3, 20011), (300, 96), (5000, 40), (2500, 1030),
-         (1100, 4100), (1, 16), (1000, 128), (777, 121), (333, 256), (4097, 200), (20000, 17)]
+         (1100, 4100), (1, 16), (1000, 128), (777, 121), (333, 256), (4097, 200), (20000, 17), (70, 790), (40, 6200), (530, 12300), (20, 14000)]
 TYPES = list(itertools.product(["bf16", "f32"], repeat=2))
 
 

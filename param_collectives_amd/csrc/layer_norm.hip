@@ -697,7 +697,10 @@ struct Shape {
 // 376 us).
 // A workgroup of the gradients leaves two fp32 sums a column, so there is at most one
 // for 64 rows, for 32 where a wave or all of it shares a row (one for 16: 16384 rows
-// of 2048 84 us instead of 74), but one a CU.
+// of 2048 84 us instead of 74), but one a CU; and no more than 512 of 256 threads (1024
+// of 16 lanes' a row: 65536 bf16 rows of 2048 149 us and not 167 with 1024 of them, 32768
+// of 8192 by 512 threads 282 and not 292 with 512, 262144 of 128 by 16 lanes 46 and 50
+// with 512).
 Shape shape_of(const LayerNormCall& c, bool grad) {
   const int64_t u = c.x_f32 || c.y_f32 ? 4 : 8;
   Shape s{0, 0, 0};
@@ -716,7 +719,7 @@ Shape shape_of(const LayerNormCall& c, bool grad) {
   }
   const int64_t block = s.share < 256 ? 256 : s.share, at_once = block / s.share;
   const int64_t need = (c.rows + at_once - 1) / at_once;
-  int64_t most = 1024 * 256 / block;
+  int64_t most = (grad && s.share > 16 ? 512 : 1024) * 256 / block;
   if (grad) {
     const int64_t each = s.share == 16 ? 4 : s.share == 64 ? 8 : 32;
     if (most > need / each) most = need / each;

@@ -19,8 +19,8 @@
 // above the deviations costs the rounding of x alone.  The other sums of a row are
 // fp32 in a thread (at most 32 values) and fp64 over the threads.
 //
-// Measured: 8191 rows of 5120, fp32 to bf16, 47 us (5.3 TB/s); gradients of 16384
-// rows of 8192 in bf16 160 us (5.0 TB/s), of 262144 rows of 128 45 us (4.5 TB/s, two
+// Measured: 8191 rows of 5120, fp32 to bf16, 42 us (6.0 TB/s); gradients of 16384
+// rows of 8192 in bf16 155 us (5.2 TB/s), of 262144 rows of 128 45 us (4.5 TB/s, two
 // launches; the forward pass 28 us); a few rows 3 us of kernel in a call of 4.5.
 //
 // Rows too long for the registers are read two or three times, by loops.
@@ -700,7 +700,9 @@ struct Shape {
 // of 2048 84 us instead of 74), but one a CU; and no more than 512 of 256 threads (1024
 // of 16 lanes' a row: 65536 bf16 rows of 2048 149 us and not 167 with 1024 of them, 32768
 // of 8192 by 512 threads 282 and not 292 with 512, 262144 of 128 by 16 lanes 46 and 50
-// with 512).
+// with 512).  The forward pass has 512 too, whose threads start seldom, where a thread
+// has enough values on its way (8191 fp32 rows of 5120 42 us, 47 with 1024, 55 with 256),
+// and 1024 where it has 8 at most (65536 bf16 rows of 2048 104 us, 143 with 512).
 Shape shape_of(const LayerNormCall& c, bool grad) {
   const int64_t u = c.x_f32 || c.y_f32 ? 4 : 8;
   Shape s{0, 0, 0};
@@ -719,7 +721,7 @@ Shape shape_of(const LayerNormCall& c, bool grad) {
   }
   const int64_t block = s.share < 256 ? 256 : s.share, at_once = block / s.share;
   const int64_t need = (c.rows + at_once - 1) / at_once;
-  int64_t most = (grad && s.share > 16 ? 512 : 1024) * 256 / block;
+  int64_t most = ((grad ? s.share > 16 : s.j * u > 8) ? 512 : 1024) * 256 / block;
   if (grad) {
     const int64_t each = s.share == 16 ? 4 : s.share == 64 ? 8 : 32;
     if (most > need / each) most = need / each;

@@ -384,7 +384,11 @@ __global__ __launch_bounds__(kBlock<SHARE>, 4) void layer_norm_grad_kernel(NormA
 #pragma unroll
     for (int i = 0; i < U; ++i) dw[j * U + i] = db[j * U + i] = 0.0f;
   }
-  constexpr int kSet = sets_of(J * (Raw<XF32, U>::kWords + Raw<YF32, U>::kWords), 24);
+  // (1024 threads' rows of more than 8192 columns with fp32 are not fetched ahead: 4096
+  // of 12288 114 us instead of 123, of 14336 138 instead of 300, which spills)
+  constexpr int kSet = SHARE == 1024 && U == 4 && J > 2
+                           ? 1
+                           : sets_of(J * (Raw<XF32, U>::kWords + Raw<YF32, U>::kWords), 24);
   Raw<XF32, U> x[kSet][J];
   Raw<YF32, U> y[kSet][J];
   float mean[kSet], rstd[kSet];
@@ -692,9 +696,8 @@ struct Shape {
 // bf16 and 12 where there is fp32: 16 spill (8192 fp32 rows of 4096 116 us instead of
 // 74; of 8192 124 instead of 79).  16 lanes have 8 of the gradients' (65536 rows of
 // 200 126 us with 16 and 34 by a wave).  By 16 lanes 262144 rows of 128 take 28 us, by
-// a wave 79, their gradients 45 and 75.  Above 12288 columns fp32 spills in the
-// registers of 1024 threads, but loops would take longer (4096 rows of 14336 300 and
-// 376 us).
+// a wave 79, their gradients 45 and 75.  1024 threads have 16 of either (4096
+// fp32 rows of 14336 138 us; by loops 376).
 // A workgroup of the gradients leaves two fp32 sums a column, so there is at most one
 // for 64 rows, for 32 where a wave or all of it shares a row (one for 16: 16384 rows
 // of 2048 84 us instead of 74), but one a CU; and no more than 512 of 256 threads (1024

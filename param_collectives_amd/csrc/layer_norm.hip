@@ -694,7 +694,7 @@ struct Shape {
 // on in a CU and few threads wait for each other.  That many are 32, 16 of 16 lanes'
 // and a wave's, and for the gradients, which hold three more values for each, 16 of
 // bf16 and 12 where there is fp32: 16 spill (8192 fp32 rows of 4096 116 us instead of
-// 74; of 8192 124 instead of 79).  16 lanes have 8 of the gradients' (65536 rows of
+// 74, 4096 of 8192 124 instead of 79).  16 lanes have 8 of the gradients' (65536 rows of
 // 200 126 us with 16 and 34 by a wave).  By 16 lanes 262144 rows of 128 take 28 us, by
 // a wave 79, their gradients 45 and 75.  1024 threads have 16 of either (4096
 // fp32 rows of 14336 138 us; by loops 376).

@@ -526,10 +526,11 @@ tide_status tide_vocab_loss_grad(const uint16_t* hidden, int64_t hidden_stride, 
  *   dx      = rstd * (g - sum g / n - xh * sum (g * xh) / n)
  *   dweight = sum over rows of dout * xh,  dbias = sum over rows of dout
  *                                     (+ old, accumulate = 1)
- * Everything is computed in fp32 and rounded once to the results' types; sums go
- * in an order that depends on the sizes and types only.  A row that holds a NaN
- * or an infinity comes out as NaN, the other rows are not touched by it (dweight
- * and dbias sum over all).
+ * Everything is computed in fp32 (a row's mean more exactly) and rounded once to
+ * the results' types; sums go in an order that depends on the sizes and types
+ * only.  A row that holds a NaN or an infinity comes out as NaN, the other rows are
+ * not touched by it (dweight and dbias sum over all).  Finite rows have to have a
+ * sum of (x - mean)^2, and gradients sums of |g| and |g * xh|, that fp32 holds.
  *
  *   x, dx    rows x cols of x_dtype;  out, dout  rows x cols of out_dtype
  *            (dout_dtype); rows their strides apart, aligned to the element.

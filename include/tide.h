@@ -535,7 +535,9 @@ tide_status tide_vocab_loss_grad(const uint16_t* hidden, int64_t hidden_stride, 
  *   x, dx    rows x cols of x_dtype;  out, dout  rows x cols of out_dtype
  *            (dout_dtype); rows their strides apart, aligned to the element.
  *            What lies between two rows is left alone.  No output may overlap
- *            an input or another output.
+ *            an input or another output: such a call is refused
+ *            (TIDE_ERR_INVALID; of two matrices with gaps between their rows and
+ *            different pitches in bytes only if they start together).
  *   weight, bias, dweight, dbias  cols values of affine_dtype without gaps.
  *            weight NULL stands for 1, bias NULL for 0; dweight or dbias NULL:
  *            not wanted.
@@ -585,7 +587,8 @@ tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t d
  *
  *   x, dx, w_gate, w_up, out, dout, gates  rows their strides apart, 2-byte
  *           aligned.  What lies between two rows is left alone.  No output may
- *           overlap an input or another output.  Where rows of x or of the weights do not all start
+ *           overlap an input or another output: refused as for layer norm.  Where
+ *           rows of x or of the weights do not all start
  *           and end on 16 bytes, hidden_size is no multiple of 32 (not where the
  *           product is small), the weights' strides differ, or, for the gradients,
  *           ffn_size is no multiple of 32, the workspace holds a copy of them (the
@@ -638,7 +641,8 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
  *           elements apart (all the same)
  *   out     count matrices of bf16, rows out_stride apart.  out[i] may be x[i]
  *           (bf16, the same strides), otherwise none may overlap another or an input;
- *           one that is listed twice, or as another's input, is refused.
+ *           one that is listed twice, or that overlaps another or another's input, is
+ *           refused as for layer norm.
  *           Both lists are read during the call only.
  *   workspace  as for the weight gradient above; matrices are taken so many at a
  *           time that it stays below about 384 MiB, one at least

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <string>
 #include <utility>
 #include <vector>
@@ -75,6 +76,51 @@ tide_status check_workspace(const void* workspace, int64_t given, int64_t need) 
   } while (0)
 
 uintptr_t size_of(int32_t dtype) { return dtype == TIDE_DTYPE_F32 ? 4 : 2; }
+
+// Rows of `bytes` each, `pitch` apart.
+struct Area {
+  const char* name;
+  uintptr_t at;
+  int64_t rows, bytes, pitch;
+
+  bool empty() const { return at == 0 || rows == 0 || bytes == 0; }
+  bool solid() const { return rows == 1 || pitch == bytes; }
+  uintptr_t end() const { return at + uintptr_t((rows - 1) * pitch + bytes); }
+};
+Area matrix_area(const char* name, const void* p, int64_t rows, int64_t cols, int64_t stride, uintptr_t size) {
+  return Area{name, reinterpret_cast<uintptr_t>(p), rows, cols * int64_t(size), stride * int64_t(size)};
+}
+Area vector_area(const char* name, const void* p, int64_t n, uintptr_t size) {
+  return matrix_area(name, p, 1, n, n, size);
+}
+
+// Whether two areas share a byte.  Of two with gaps between their rows and different
+// pitches only those that start together are known to.
+bool overlap(const Area& a, const Area& b) {
+  if (a.empty() || b.empty() || a.at >= b.end() || b.at >= a.end()) return false;
+  if (a.at == b.at) return true;
+  if (a.at > b.at) return overlap(b, a);
+  const int64_t off = int64_t(b.at - a.at);
+  if (b.solid()) {
+    // a's last row that starts before b ends, from the first that ends behind b's start
+    const int64_t first = off < a.bytes ? 0 : (off - a.bytes) / a.pitch + 1;
+    return first < a.rows && a.at + uintptr_t(first * a.pitch) < b.end();
+  }
+  if (a.solid()) return true;  // b's first row starts in it
+  if (a.pitch != b.pitch) return false;
+  // b's rows start `in` bytes after the start of a's from row `row` on
+  const int64_t row = off / a.pitch, in = off % a.pitch;
+  return in < a.bytes || (in + b.bytes > a.pitch && row + 1 < a.rows);
+}
+
+// No output (the first `outs` of the areas) may share memory with another area.
+tide_status check_apart(std::initializer_list<Area> areas, size_t outs) {
+  const Area* all = areas.begin();
+  for (size_t i = 0; i < outs; ++i)
+    for (size_t j = i + 1; j < areas.size(); ++j)
+      if (overlap(all[i], all[j])) return invalid(std::string(all[i].name) + " overlaps " + all[j].name);
+  return TIDE_OK;
+}
 
 // Checks shared by the pack and the unpack; *call is filled in.
 tide_status checkpoint_call(const char* name, const void* x, int32_t dtype, int64_t rows, int64_t cols,
@@ -251,20 +297,31 @@ tide_status check_coefficients(double a, double b, double c, int32_t steps) {
   return TIDE_OK;
 }
 
-// No output twice, and none that is another matrix's input.
-tide_status check_distinct(const void* const* x, uint16_t* const* out, int32_t count) {
+// No output twice, and none that shares memory with another output or another
+// matrix's input (its own has been read when it is written).
+tide_status check_distinct(const void* const* x, uintptr_t x_size, int64_t x_stride, uint16_t* const* out,
+                           int64_t out_stride, int32_t count, int64_t rows, int64_t cols) {
+  auto place = [](const char* list, int32_t i) { return std::string(list) + "[" + std::to_string(i) + "]"; };
+  auto area = [&](const void* p, int64_t stride, uintptr_t size) { return matrix_area("", p, rows, cols, stride, size); };
   std::vector<std::pair<uintptr_t, int32_t>> at(count);
   for (int32_t i = 0; i < count; ++i) at[i] = {reinterpret_cast<uintptr_t>(out[i]), i};
   std::sort(at.begin(), at.end());
   for (int32_t i = 1; i < count; ++i)
     if (at[i].first == at[i - 1].first)
-      return invalid("out[" + std::to_string(at[i - 1].second) + "] and out[" + std::to_string(at[i].second) +
-                     "] are the same matrix");
+      return invalid(place("out", at[i - 1].second) + " and " + place("out", at[i].second) + " are the same matrix");
   for (int32_t i = 0; i < count; ++i) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(x[i]);
-    const auto same = std::lower_bound(at.begin(), at.end(), std::make_pair(p, int32_t(0)));
-    if (same != at.end() && same->first == p && same->second != i)
-      return invalid("out[" + std::to_string(same->second) + "] is x[" + std::to_string(i) + "]");
+    const Area a = area(out[at[i].second], out_stride, 2);
+    for (int32_t j = i + 1; j < count && at[j].first < a.end(); ++j)
+      if (overlap(a, area(out[at[j].second], out_stride, 2)))
+        return invalid(place("out", at[i].second) + " overlaps " + place("out", at[j].second));
+  }
+  const uintptr_t span = area(out[0], out_stride, 2).end() - reinterpret_cast<uintptr_t>(out[0]);
+  for (int32_t i = 0; i < count; ++i) {
+    const Area a = area(x[i], x_stride, x_size);
+    auto near = std::lower_bound(at.begin(), at.end(), std::make_pair(a.at > span ? a.at - span : 0, int32_t(0)));
+    for (; near != at.end() && near->first < a.end(); ++near)
+      if (near->second != i && overlap(a, area(out[near->second], out_stride, 2)))
+        return invalid(place("out", near->second) + (near->first == a.at ? " is " : " overlaps ") + place("x", i));
   }
   return TIDE_OK;
 }
@@ -440,6 +497,11 @@ tide_status tide_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, in
     c.mean = mean;
     c.rstd = rstd;
     if (mean != nullptr && mean == rstd) return invalid("mean and rstd are the same vector");
+    const uintptr_t affine = size_of(affine_dtype);
+    TIDE_TRY(check_apart({matrix_area("out", out, rows, cols, out_stride, size_of(out_dtype)), vector_area("mean", mean, rows, 4),
+                          vector_area("rstd", rstd, rows, 4), matrix_area("x", x, rows, cols, x_stride, size_of(x_dtype)),
+                          vector_area("weight", weight, cols, affine), vector_area("bias", bias, cols, affine)},
+                         3));
     return hip_status(tide::launch_layer_norm(c, nullptr, stream), "layer norm launch");
   });
 }
@@ -490,6 +552,14 @@ tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t d
     c.dx = dx;
     c.dx_ld = dx_stride;
     if (rows > 0 && dweight != nullptr && dweight == dbias) return invalid("dweight and dbias are the same vector");
+    const uintptr_t affine = size_of(affine_dtype);
+    if (rows > 0)
+      TIDE_TRY(check_apart({matrix_area("dx", dx, rows, cols, dx_stride, size_of(x_dtype)), vector_area("dweight", dweight, cols, affine),
+                            vector_area("dbias", dbias, cols, affine),
+                            matrix_area("dout", dout, rows, cols, dout_stride, size_of(dout_dtype)),
+                            matrix_area("x", x, rows, cols, x_stride, size_of(x_dtype)), vector_area("weight", weight, cols, affine),
+                            vector_area("mean", mean, rows, 4), vector_area("rstd", rstd, rows, 4)},
+                           3));
     return hip_status(tide::launch_layer_norm(c, workspace, stream), "layer norm gradient launch");
   });
 }
@@ -523,6 +593,12 @@ tide_status tide_gated_block(const uint16_t* x, int64_t x_stride, const uint16_t
     if (tokens == 0) return TIDE_OK;
     TIDE_TRY(check_pointer("out", out, 2));
     TIDE_TRY(check_workspace(workspace, workspace_bytes, tide::gated_block_bytes(c)));
+    TIDE_TRY(check_apart({matrix_area("out", out, tokens, ffn_size, out_stride, 2),
+                          matrix_area("gates", gates, tokens, 2 * ffn_size, gates_stride, 2),
+                          matrix_area("x", x, tokens, hidden_size, x_stride, 2),
+                          matrix_area("w_gate", w_gate, ffn_size, hidden_size, gate_stride, 2),
+                          matrix_area("w_up", w_up, ffn_size, hidden_size, up_stride, 2)},
+                         2));
     c.out = out;
     c.out_ld = out_stride;
     return hip_status(tide::launch_gated_block(c, workspace, stream), "gated block launch");
@@ -561,6 +637,16 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
     c.dw_f32 = dw_dtype == TIDE_DTYPE_F32;
     c.accumulate = accumulate;
     if (tokens > 0 && dw_gate == dw_up) return invalid("dw_gate and dw_up are the same matrix");
+    if (tokens > 0)
+      TIDE_TRY(check_apart({matrix_area("dx", dx, tokens, hidden_size, dx_stride, 2),
+                            matrix_area("dw_gate", dw_gate, ffn_size, hidden_size, hidden_size, size_of(dw_dtype)),
+                            matrix_area("dw_up", dw_up, ffn_size, hidden_size, hidden_size, size_of(dw_dtype)),
+                            matrix_area("dout", dout, tokens, ffn_size, dout_stride, 2),
+                            matrix_area("x", x, tokens, hidden_size, x_stride, 2),
+                            matrix_area("w_gate", w_gate, ffn_size, hidden_size, gate_stride, 2),
+                            matrix_area("w_up", w_up, ffn_size, hidden_size, up_stride, 2),
+                            matrix_area("gates", gates, tokens, 2 * ffn_size, gates_stride, 2)},
+                           3));
     return hip_status(tide::launch_gated_block(c, workspace, stream), "gated block gradient launch");
   });
 }
@@ -596,7 +682,7 @@ tide_status tide_orthogonalize(const void* const* x, int32_t x_dtype, int64_t x_
       TIDE_TRY(check_pointer(("x" + n).c_str(), x[i], size_of(x_dtype)));
       TIDE_TRY(check_pointer(("out" + n).c_str(), out[i], 2));
     }
-    TIDE_TRY(check_distinct(x, out, count));
+    TIDE_TRY(check_distinct(x, size_of(x_dtype), x_stride, out, out_stride, count, rows, cols));
     tide::OrthogonalCall o{};
     o.x = x;
     o.x_f32 = x_dtype == TIDE_DTYPE_F32;

@@ -645,7 +645,8 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
  *           refused as for layer norm.
  *           Both lists are read during the call only.
  *   workspace  as for the weight gradient above; matrices are taken so many at a
- *           time that it stays below about 384 MiB, one at least
+ *           time that they take 384 MiB of it at most, one at least, and partial
+ *           sums of their products up to 192 MiB
  * Sizes: rows and cols up to 2^22, matrices and the square of the smaller side as
  * for the checkpoints; steps in [1, 64].
  * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.

@@ -596,8 +596,9 @@ tide_status tide_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t d
  *   dw_gate, dw_up  ffn_size x hidden_size of dw_dtype, without gaps
  *   workspace  as for the weight gradient above; with gradients it also holds dg
  *           and du.  The _workspace call takes the same gates (NULL or not).
- * Sizes: matrices as for the checkpoints, hidden_size and ffn_size at least 1,
- * ffn_size up to 2^21.  tokens = 0: the weights' gradients become 0, or stay.
+ * Sizes: matrices as for the checkpoints (for the gradients gates' too, which are
+ * dg and du's in the workspace), hidden_size and ffn_size at least 1, ffn_size up to
+ * 2^21.  tokens = 0: the weights' gradients become 0, or stay.
  * Errors: TIDE_ERR_INVALID, TIDE_ERR_RANGE, TIDE_ERR_ALIGN, TIDE_ERR_HIP.
  * ------------------------------------------------------------------------ */
 #define TIDE_ACT_SILU 0

@@ -217,7 +217,8 @@ tide_status layer_norm_call(const void* x, int32_t x_dtype, int64_t x_stride, co
 // filled in.
 tide_status gated_call(const uint16_t* x, int64_t x_stride, const uint16_t* w_gate, int64_t gate_stride,
                        const uint16_t* w_up, int64_t up_stride, int64_t tokens, int64_t hidden_size, int64_t ffn_size,
-                       int32_t activation, const uint16_t* gates, int64_t gates_stride, tide::GatedCall* call) {
+                       int32_t activation, const uint16_t* gates, int64_t gates_stride, bool grad,
+                       tide::GatedCall* call) {
   if (activation != TIDE_ACT_SILU && activation != TIDE_ACT_GELU)
     return invalid("activation must be TIDE_ACT_SILU or TIDE_ACT_GELU");
   TIDE_TRY(check_matrix("x", tokens, hidden_size, x_stride));
@@ -225,7 +226,8 @@ tide_status gated_call(const uint16_t* x, int64_t x_stride, const uint16_t* w_ga
   TIDE_TRY(check_matrix("w_up", ffn_size, hidden_size, up_stride));
   if (hidden_size < 1 || ffn_size < 1) return invalid("the hidden sizes must be at least 1");
   if (ffn_size > kMaxFeatures / 2) return tide::set_error(TIDE_ERR_RANGE, "an inner size above 2^21");
-  TIDE_TRY(check_matrix("gates", tokens, 2 * ffn_size, gates ? gates_stride : 2 * ffn_size));
+  // (the gradients' workspace holds dg and du, which are as large)
+  if (gates || grad) TIDE_TRY(check_matrix("gates", tokens, 2 * ffn_size, gates ? gates_stride : 2 * ffn_size));
   if (tokens > 0) {
     TIDE_TRY(check_pointer("x", x, 2));
     TIDE_TRY(check_pointer("w_gate", w_gate, 2));
@@ -245,6 +247,7 @@ tide_status gated_call(const uint16_t* x, int64_t x_stride, const uint16_t* w_ga
   call->gelu = activation == TIDE_ACT_GELU;
   call->gates = const_cast<uint16_t*>(gates);
   call->gates_ld = gates_stride;
+  call->grad = grad;
   return TIDE_OK;
 }
 
@@ -573,8 +576,8 @@ tide_status tide_gated_block_workspace(const uint16_t* x, int64_t x_stride, cons
     if (gradients != 0 && gradients != 1) return invalid("gradients must be 0 or 1");
     tide::GatedCall c;
     TIDE_TRY(gated_call(x, x_stride, w_gate, gate_stride, w_up, up_stride, tokens, hidden_size, ffn_size, TIDE_ACT_SILU,
-                        gates, 2 * ffn_size, &c));
-    c.grad = gradients == 1;
+                        gates, 2 * ffn_size, gradients == 1, &c));
+    if (gradients == 0) TIDE_TRY(check_matrix("out", tokens, ffn_size, ffn_size));
     *bytes = tide::gated_block_bytes(c);
     return TIDE_OK;
   });
@@ -588,7 +591,7 @@ tide_status tide_gated_block(const uint16_t* x, int64_t x_stride, const uint16_t
     tide::clear_error();
     tide::GatedCall c;
     TIDE_TRY(gated_call(x, x_stride, w_gate, gate_stride, w_up, up_stride, tokens, hidden_size, ffn_size, activation,
-                        gates, gates_stride, &c));
+                        gates, gates_stride, false, &c));
     TIDE_TRY(check_matrix("out", tokens, ffn_size, out_stride));
     if (tokens == 0) return TIDE_OK;
     TIDE_TRY(check_pointer("out", out, 2));
@@ -617,12 +620,11 @@ tide_status tide_gated_block_grad(const uint16_t* dout, int64_t dout_stride, con
     if (accumulate != 0 && accumulate != 1) return invalid("accumulate must be 0 or 1");
     tide::GatedCall c;
     TIDE_TRY(gated_call(x, x_stride, w_gate, gate_stride, w_up, up_stride, tokens, hidden_size, ffn_size, activation,
-                        gates, gates_stride, &c));
+                        gates, gates_stride, true, &c));
     TIDE_TRY(check_matrix("dout", tokens, ffn_size, dout_stride));
     TIDE_TRY(check_matrix("dx", tokens, hidden_size, dx_stride));
     TIDE_TRY(check_pointer("dw_gate", dw_gate, size_of(dw_dtype)));
     TIDE_TRY(check_pointer("dw_up", dw_up, size_of(dw_dtype)));
-    c.grad = true;
     if (tokens > 0) {
       TIDE_TRY(check_pointer("dout", dout, 2));
       TIDE_TRY(check_pointer("dx", dx, 2));

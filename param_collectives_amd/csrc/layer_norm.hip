@@ -763,7 +763,7 @@ int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad,
   const dim3 grid(static_cast<unsigned>(s.groups));
   if (s.share == 0) return launch_wide<XF32, YF32>(c, s, a, grad, st);
   constexpr int kPer = XF32 || YF32 ? 2 : 1;  // pieces of 8 values
-  constexpr int kMore = kPer == 2 ? 3 : 2, kFive = kPer == 2 ? 5 : 3;
+  constexpr int kMore = kPer == 2 ? 3 : 2;
 #define TIDE_NORM(KERNEL, SHARE, J) hipLaunchKernelGGL((KERNEL<XF32, YF32, SHARE, J>), grid, dim3(kBlock<SHARE>), 0, st, a)
   if (grad) {
     if (s.share == 16)
@@ -801,8 +801,6 @@ int launch(const LayerNormCall& c, const Shape& s, const NormArgs& a, bool grad,
       TIDE_NORM(layer_norm_kernel, 256, kPer);
     else if (s.j <= 2 * kPer)
       TIDE_NORM(layer_norm_kernel, 256, 2 * kPer);
-    else if (s.j <= kFive)
-      TIDE_NORM(layer_norm_kernel, 256, kFive);
     else if (s.j <= 3 * kPer)
       TIDE_NORM(layer_norm_kernel, 256, 3 * kPer);
     else

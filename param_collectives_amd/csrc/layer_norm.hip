@@ -22,11 +22,14 @@
 // most 12 additions for each), and over the threads (at most 22).  (In fp64 over the
 // threads the gradients spill: 16384 bf16 rows of 8192 204 us instead of 154.)
 //
-// Measured: 8191 rows of 5120, fp32 to bf16, 42 us (6.0 TB/s); gradients of 16384
-// rows of 8192 in bf16 155 us (5.2 TB/s), of 262144 rows of 128 45 us (4.5 TB/s, two
-// launches; the forward pass 28 us); a few rows 3 us of kernel in a call of 4.5.
+// Measured: 8191 rows of 5120, fp32 to bf16, 42 to 44 us (5.7 to 6.0 TB/s); gradients
+// of 16384 rows of 8192 in bf16 155 us (5.2 TB/s), of 262144 rows of 128 45 us (4.5
+// TB/s, two launches; the forward pass 28 us); a few rows 3 us of kernel in a call of
+// 4.5.
 //
-// Rows too long for the registers are read two or three times, by loops.
+// Rows too long for the registers are read three times, by loops, and take 3 to 6
+// times what their bytes do once: 4096 rows of 18432 in bf16 292 us, their gradients
+// 404, 512 of 65536 in fp32 143 and 320.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

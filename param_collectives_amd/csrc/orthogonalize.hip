@@ -19,9 +19,9 @@
 // into the first step's factors.
 //
 // Measured: one of 14336 x 4096 in fp32 4.3 ms (920 TFLOP/s), 128 of 2048 x 768 4.3 to
-// 5.0 ms (600 to 520): their products have 24 and 64 steps of k, and what a tile takes
+// 5.1 ms (600 to 510): their products have 24 and 64 steps of k, and what a tile takes
 // beside them (X's rest read, X and its rest written, G and P written twice) is as
-// much again.
+// much again; G and P of 32 at a time are 192 tiles, which leave 64 CUs idle.
 //
 // The norm is summed in fp64, which no entry's square leaves.
 #include <hip/hip_runtime.h>
@@ -322,7 +322,9 @@ __global__ __launch_bounds__(WM* WN * 64, SIDE == 64 ? 1 : 2) void symmetric_ker
 // waves split k, each reading its steps of the rows straight into registers, eight of
 // them on their way.  Taken where every tile has a CU (512 x 2048 orthogonalized
 // takes 136 us, by tiles of 64 through LDS 143; 60 of 64 x 128 86 for 101; 16 of 256 x
-// 256, whose 576 tiles are too many, 107 either way).  What is left is the launches':
+// 256, whose 576 tiles are too many, 107 either way).  The first product of tall
+// matrices, whose k runs down the columns, keeps the tiles of 64, which transpose as
+// they read: 2048 x 512 takes 141 us, 60 of 128 x 64 94.  What is left is the launches':
 // one that only waits for the last one's results takes 4 us of the 8 a launch.
 constexpr int kFewWaves = 8;
 __global__ __launch_bounds__(kFewWaves * 64) void few_symmetric_kernel(SymmetricArgs a) {
@@ -656,8 +658,10 @@ Layout layout_of(const OrthogonalCall& c) {
   L.matrix = padded(c.rows) * L.pitch;
   L.small_matrix = L.small * L.small_pitch;
   const int64_t each = 3 * L.matrix * 2 + 2 * L.small_matrix * 2;
-  // (128 of 2048 x 768, all at a time that 1 GiB holds 4.47 ms, 384 MiB 4.31, 256 MiB
-  // 4.73: smaller pieces stay in the caches, but leave CUs without a tile)
+  // (With 256, 384, 512 MiB and 1 GiB 128 of 2048 x 768 take 5.38, 4.96, 5.10 and 4.90
+  // ms, 64 of 2048 x 1408 7.54, 7.61, 7.00 and 7.11, 40 of 4096 x 1024 4.61, 4.68, 4.35
+  // and 4.16: how a piece's tiles fill whole rounds decides.  384 MiB is as fast for
+  // the first, and the memory is the caller's.)
   L.piece = (int64_t(3) << 27) / each;
   L.piece = L.piece < 1 ? 1 : L.piece > kMost ? kMost : L.piece;
   if (L.piece > c.count) L.piece = c.count;

@@ -104,9 +104,9 @@ inline double cut_cost(const Cut& c, int64_t steps, int64_t side) {
 
 // A product's tiles: the side (a small tile's is that of its rows) and the cut that
 // are estimated to end first.  tiles(side) counts them.  Tiles of 64 are not split (a
-// step of them takes `small_step` us, a tile about 4 more) and read operands below 4
-// GiB.  (509 tokens, 2048 x 768, gated block's gradients: 43 us with them, 46 without;
-// 512 x 2048 orthogonalized 147 and 187 us.)
+// step of them takes `small_step` us, a tile about 4 more: fitted to the two sizes
+// that follow) and read operands below 4 GiB.  (509 tokens, 2048 x 768, gated block's
+// gradients: 43 us with them, 46 without; 512 x 2048 orthogonalized 147 and 187 us.)
 struct Tiling {
   int64_t side = 256;
   Cut cut{};
